@@ -521,6 +521,73 @@ mx_status mx_grouped_gemm_swiglu_quantize(const mx_operand* a, const mx_operand*
                                           int n_groups, void* row_data, void* row_scale, void* col_data,
                                           void* col_scale, int64_t col_capacity, int* dev_status, void* stream);
 
+/*
+ * Operators around the products of a training step
+ * ------------------------------------------------
+ * What stands between the calls above in one step of training: the optimizer
+ * that updates the FP32 masters mx_quantize_f32 reads. Element types are named
+ * by mx_dtype. Pointers need the alignment of their element type unless a call
+ * says otherwise; 16-byte aligned pointers and pitches take the fast paths.
+ */
+typedef enum mx_dtype { MX_BF16 = 0, MX_F32 = 1 } mx_dtype;
+
+/*
+ * mx_adamw_step - one AdamW step over n tensors, in place ("DeepSeek-V3 16B
+ * FSDP2 MXFP8/HiF8 训练设计" §8.1, §10: FP32 masters, updated before the
+ * quantised copies are refreshed). Per element, in FP32:
+ *
+ *   g' = grad_scale * g
+ *   m  = beta1 * m + (1 - beta1) * g'
+ *   v  = beta2 * v + (1 - beta2) * g' * g'
+ *   p  = (1 - lr * weight_decay) * p
+ *        - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ *
+ *   tensors     host array of n descriptors (read before return). Every tensor
+ *               is numel consecutive elements; a tensor of numel 0 is skipped.
+ *   state_bits  32: exp_avg and exp_avg_sq are FP32 arrays of numel (the scale
+ *               pointers are unused).
+ *               8: both are byte arrays of numel with one FP32 scale per
+ *               MX_ADAMW_STATE_BLOCK consecutive elements, ceil(numel / 256)
+ *               each. exp_avg holds E4M3 codes, value = code * scale (scale =
+ *               amax / 448). exp_avg_sq holds codes c of value 0 (c = 0) or
+ *               2^(floor((c+1)/8) - 32) * (1 + ((c+1) mod 8)/8) (c >= 1; code
+ *               255 is 1), times the scale (= amax); it is rounded up or down
+ *               at random in proportion, by a hash of hyper->seed, the tensor's
+ *               index in this call and the element's index. All-zero bytes and
+ *               scales are the zero state. A block holding NaN or an infinity
+ *               gets a scale that is not finite.
+ *   hyper       host pointer: 0 <= beta < 1, eps >= 0, step >= 1 (the first
+ *               step is 1), lr finite. seed: a new one every step (the step
+ *               count, say); read with 8-bit states only.
+ *   grad_scale  device float that multiplies every gradient (an inverse loss
+ *               scale, a clipping factor), or NULL for 1. If it is NaN or
+ *               infinite the step changes nothing and dev_status gets
+ *               MX_ERR_DEVICE_CHECK.
+ * Parameters are FP32; gradients FP32 or BF16 per tensor. No two arrays may
+ * overlap. Same inputs give the same bits.
+ */
+#define MX_ADAMW_STATE_BLOCK 256
+typedef struct mx_adamw_tensor {
+  float* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;    /* 8-bit states only */
+  float* exp_avg_sq_scale; /* 8-bit states only */
+  int64_t numel;
+  double weight_decay;
+  int32_t grad_dtype; /* mx_dtype */
+  int32_t reserved;   /* 0 */
+} mx_adamw_tensor;
+typedef struct mx_adamw_hyper {
+  double lr, beta1, beta2, eps;
+  int64_t step;
+  uint32_t seed;
+  int32_t reserved; /* 0 */
+} mx_adamw_hyper;
+mx_status mx_adamw_step(const mx_adamw_tensor* tensors, int n, int state_bits, const mx_adamw_hyper* hyper,
+                        const float* grad_scale, int* dev_status, void* stream);
+
 /* Static description of a status code. */
 const char* mx_status_string(mx_status s);
 

@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -27,6 +28,8 @@ MX_FPROP, MX_DGRAD, MX_WGRAD = 0, 1, 2
 MX_MAX_MULTI = 8
 MX_MAX_GEMM_MULTI = 4
 MX_MAX_GROUPS = 512
+MX_BF16, MX_F32 = 0, 1
+MX_ADAMW_STATE_BLOCK = 256
 STATUS_NAMES = {0: "MX_OK", 1: "MX_ERR_INVALID_ARG", 2: "MX_ERR_UNSUPPORTED_SHAPE", 3: "MX_ERR_ALIGNMENT",
                 4: "MX_ERR_CUDA", 5: "MX_ERR_DEVICE_CHECK", 6: "MX_ERR_TIMEOUT", 7: "MX_ERR_NO_DEVICE"}
 
@@ -37,7 +40,7 @@ EXPORTED = ("mx_scale_bytes", "mx_grouped_padded_rows", "mx_quantize", "mx_quant
             "mx_gemm_fp8_blockwise", "mx_status_string", "mx_last_error", "mx_abi_version",
             "mx_selftest_wait_timeout", "mx_gemm_workspace_bytes", "mx_gemm_with_workspace", "mx_gemm_multi",
             "mx_gemm_static_workspace", "mx_current_amax", "mx_quantize_current", "mx_gemm_current",
-            "mx_grouped_gemm_current", "mx_gemm_current_multi", "mx_grouped_gemm_swiglu_quantize")
+            "mx_grouped_gemm_current", "mx_gemm_current_multi", "mx_grouped_gemm_swiglu_quantize", "mx_adamw_step")
 MX_STATIC_WORKSPACE_BYTES = 40 * 1024 * 1024
 
 
@@ -62,6 +65,19 @@ class MXQuantTensorC(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ldx", ctypes.c_int64),
                 ("row_data", ctypes.c_void_p), ("row_scale", ctypes.c_void_p), ("col_data", ctypes.c_void_p),
                 ("col_scale", ctypes.c_void_p)]
+
+
+class MXAdamWTensorC(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
+                ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("exp_avg_sq_scale", ctypes.c_void_p), ("numel", ctypes.c_int64), ("weight_decay", ctypes.c_double),
+                ("grad_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class MXAdamWHyperC(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("seed", ctypes.c_uint32),
+                ("reserved", ctypes.c_int32)]
 
 
 _lib = None
@@ -126,6 +142,8 @@ def lib() -> ctypes.CDLL:
     L.mx_quantize_fp8_blockwise.restype = i32
     L.mx_gemm_fp8_blockwise.argtypes = [vp, vp, i64, vp, vp, i64, i64, vp, i64, vp, vp]
     L.mx_gemm_fp8_blockwise.restype = i32
+    L.mx_adamw_step.argtypes = [vp, i32, i32, ctypes.POINTER(MXAdamWHyperC), vp, vp, vp]
+    L.mx_adamw_step.restype = i32
     L.mx_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp, vp]
     L.mx_selftest_wait_timeout.restype = i32
     L.mx_status_string.argtypes = [i32]
@@ -283,6 +301,11 @@ def mx_grouped_gemm_swiglu_quantize(a: MXOperandC, b: MXOperandC, group_offsets,
     _check(lib().mx_grouped_gemm_swiglu_quantize(_ref(a), _ref(b), group_offsets, n_groups, row_data, row_scale,
                                                  col_data, col_scale, col_capacity, dev_status, stream),
            "mx_grouped_gemm_swiglu_quantize")
+
+
+def mx_adamw_step(tensors, n, state_bits, hyper: MXAdamWHyperC, grad_scale, dev_status, stream) -> None:
+    """``tensors``: an array of n MXAdamWTensorC, or the bytes of one."""
+    _check(lib().mx_adamw_step(tensors, n, state_bits, _ref(hyper), grad_scale, dev_status, stream), "mx_adamw_step")
 
 
 # ---------------------------------------------------------------------------
@@ -647,3 +670,90 @@ def grouped_gemm_current(mode: int, a, b, group_offsets, out=None, status=None, 
     mx_grouped_gemm_current(mode, a.c_operand(), b.c_operand(), group_offsets.data_ptr(), E, out.data_ptr(),
                             out.stride(-2), _ptr(status), _stream(stream))
     return out
+
+
+# ---------------------------------------------------------------------------
+# Operators around the products of a training step
+# ---------------------------------------------------------------------------
+
+def _dtype(t) -> int:
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return MX_BF16
+    assert t.dtype == torch.float32, f"needs BF16 or FP32, got {t.dtype}"
+    return MX_F32
+
+
+@dataclass
+class AdamWState:
+    """AdamW's two moments of one tensor. bits 32: FP32 tensors like it. bits 8:
+    code tensors of its numel (exp_avg: E4M3 as float8_e4m3fn or uint8;
+    exp_avg_sq: uint8) with one FP32 scale per MX_ADAMW_STATE_BLOCK elements."""
+    bits: int
+    exp_avg: "object"
+    exp_avg_sq: "object"
+    exp_avg_scale: "object" = None
+    exp_avg_sq_scale: "object" = None
+
+
+def adamw_state(param, bits: int = 32) -> AdamWState:
+    """The zero state of a parameter, before its first step."""
+    torch = _torch()
+    assert bits in (32, 8)
+    if bits == 32:
+        return AdamWState(32, torch.zeros_like(param, dtype=torch.float32), torch.zeros_like(param, dtype=torch.float32))
+    n = param.numel()
+    blocks = (n + MX_ADAMW_STATE_BLOCK - 1) // MX_ADAMW_STATE_BLOCK
+    u8 = dict(dtype=torch.uint8, device=param.device)
+    f32 = dict(dtype=torch.float32, device=param.device)
+    return AdamWState(8, torch.zeros(n, **u8), torch.zeros(n, **u8), torch.zeros(blocks, **f32),
+                      torch.zeros(blocks, **f32))
+
+
+_ADAMW_TENSOR = "6Qqd2i"  # mx_adamw_tensor
+
+
+def adamw_step(params, grads, states, lr: float, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.0,
+               step: int = 1, grad_scale=None, seed: int = 0, status=None, stream=None) -> None:
+    """One AdamW step, in place, over all tensors in one launch (per 448).
+
+    params: contiguous FP32 CUDA tensors; grads: contiguous, FP32 or BF16, each
+    of its parameter's numel; states: one AdamWState each, all of the same bits.
+    weight_decay: one value, or one per tensor. step counts from 1. grad_scale:
+    a CUDA FP32 tensor of one element that multiplies every gradient; where it
+    is not finite the step changes nothing (status 5). seed: with 8-bit states,
+    the second moment's random rounding; a new one every step, the step count
+    for instance."""
+    torch = _torch()
+    n = len(params)
+    assert len(grads) == n and len(states) == n, "one gradient and one state per parameter"
+    if n == 0:
+        return
+    bits = states[0].bits
+    decay = weight_decay if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
+    assert len(decay) == n
+    f32, bf16 = torch.float32, torch.bfloat16
+    flat = []
+    for p, g, s, wd in zip(params, grads, states, decay):
+        k = p.numel()
+        m, v = s.exp_avg, s.exp_avg_sq
+        assert s.bits == bits, "all states of one call have the same bits"
+        assert p.dtype is f32 and p.is_cuda and p.is_contiguous(), "parameters: contiguous FP32 CUDA tensors"
+        assert (g.dtype is bf16 or g.dtype is f32) and g.is_cuda and g.is_contiguous() and g.numel() == k, \
+            "gradients: contiguous FP32 or BF16 CUDA tensors of the parameters' sizes"
+        assert m.numel() == k and v.numel() == k and m.is_contiguous() and v.is_contiguous()
+        if bits == 8:
+            a, b = s.exp_avg_scale, s.exp_avg_sq_scale
+            blocks = (k + MX_ADAMW_STATE_BLOCK - 1) // MX_ADAMW_STATE_BLOCK
+            assert m.element_size() == 1 and v.element_size() == 1
+            assert a.dtype is f32 and b.dtype is f32 and a.numel() >= blocks and b.numel() >= blocks
+            flat += (p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(), k, wd,
+                     g.dtype is f32, 0)
+        else:
+            assert m.dtype is f32 and v.dtype is f32
+            flat += (p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), 0, 0, k, wd, g.dtype is f32, 0)
+    if grad_scale is not None:
+        assert grad_scale.dtype is f32 and grad_scale.is_cuda and grad_scale.numel() == 1
+    hyper = MXAdamWHyperC(lr, betas[0], betas[1], eps, step, seed & 0xFFFFFFFF, 0)
+    mx_adamw_step(struct.pack(_ADAMW_TENSOR * n, *flat), n, bits, hyper, _ptr(grad_scale), _ptr(status),
+                  _stream(stream))

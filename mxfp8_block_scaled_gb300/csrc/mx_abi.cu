@@ -21,21 +21,6 @@ thread_local char g_err[512] = "";
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// The current device must be an sm_103 part (the kernels are built for sm_103a only).
-mx_status check_device() {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return cuda_status(e, "cudaGetDevice");
-  int major = 0, minor = 0;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
-  if (major != 10 || minor != 3) {
-    set_error("device %d is sm_%d%d; this library runs on sm_103 only", dev, major, minor);
-    return MX_ERR_NO_DEVICE;
-  }
-  return MX_OK;
-}
-
 mx_status check_operand(const mx_operand* o, const char* name) {
   if (!o) {
     set_error("%s: null operand", name);
@@ -116,6 +101,20 @@ mx_status zero_output(void* c, int64_t ldc, int64_t N, int64_t rows, cudaStream_
                      "cudaMemset2DAsync");
 }
 }  // namespace
+
+mx_status check_device() {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_status(e, "cudaGetDevice");
+  int major = 0, minor = 0;
+  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+  if (major != 10 || minor != 3) {
+    set_error("device %d is sm_%d%d; this library runs on sm_103 only", dev, major, minor);
+    return MX_ERR_NO_DEVICE;
+  }
+  return MX_OK;
+}
 
 void set_error(const char* fmt, ...) {
   va_list ap;

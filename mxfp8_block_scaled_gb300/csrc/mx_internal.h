@@ -17,6 +17,10 @@ void set_error(const char* fmt, ...);
 // MX_OK if e == cudaSuccess, else records the message and returns MX_ERR_CUDA.
 mx_status cuda_status(cudaError_t e, const char* what);
 
+// MX_OK if the current device is an sm_103 part (the kernels are built for
+// sm_103a only).
+mx_status check_device();
+
 // Bounded-wait limit (nanoseconds) for device-side mbarrier waits. Read once
 // from the MXFP8_WAIT_TIMEOUT_NS environment variable (default 2 s).
 uint64_t wait_timeout_ns();
@@ -143,5 +147,9 @@ mx_status static_workspace(void** ptr, size_t* bytes);
 // Up to MX_MAX_GEMM_MULTI independent dense GEMMs; one launch of the pair
 // kernel when they fill the GPU together, else one launch each.
 mx_status launch_gemm_multi(const GemmLaunch* Ls, int n, cudaStream_t s);
+
+// --- operators around the products -----------------------------------------
+mx_status launch_adamw(const mx_adamw_tensor* tensors, int n, int bits, const mx_adamw_hyper& hy,
+                       const float* grad_scale, int* dev_status, cudaStream_t s);
 
 }  // namespace mx

@@ -1,0 +1,370 @@
+// mx_optim.cu - the AdamW step over many tensors in one launch, on the FP32
+// masters that the weight refresh (mx_quantize_f32) reads, with both moments in
+// FP32 or in 8 bits ("DeepSeek-V3 16B FSDP2 MXFP8/HiF8 训练设计" §8.1: the
+// quantised weight copies are refreshed from the FP32 master after the
+// optimizer step).
+//
+//   g' = grad_scale * g                       decay = 1 - lr * weight_decay
+//   m  = beta1 * m + (1 - beta1) * g'         step  = lr / (1 - beta1^t)
+//   v  = beta2 * v + (1 - beta2) * g'^2       rs    = 1 / sqrt(1 - beta2^t)
+//   p  = decay * p - step * m / (rs * sqrt(v) + eps)
+//
+// All arithmetic is FP32. The moments' products and sums are rounded one by one
+// (no contraction), so the stored states are a fixed function of the inputs,
+// whatever path an element takes. The step's quotient and square root are the
+// hardware's approximations (relative error below 1e-6 of an update that is
+// itself a small fraction of p); they touch the parameter only, never a state.
+//
+// 8-bit states: 256 consecutive elements share one FP32 scale per moment.
+//   m: E4M3(m * 448/amax), round to nearest even; value = code * amax/448. A
+//      block whose largest |m| is below 2^-100 (where 448/amax leaves FP32) is
+//      stored as zeros.
+//   v: an unsigned code of 5 exponent and 3 mantissa bits of v / amax: code 255
+//      is 1, each step down one eighth of a binade, code 1 is 2^-31.75, and 0 is
+//      zero alone (a positive v never becomes zero, so the update stays
+//      bounded). v moves by about (1 - beta2) = 0.1% a step, far less than the
+//      6-12% between neighbouring codes, so rounding to nearest would hold it
+//      where it is; it is rounded up or down at random in proportion
+//      (stochastic rounding, unbiased), the random bits a hash of (seed, tensor,
+//      element) that makes every step reproducible.
+//   A block that holds a NaN or an infinity gets a NaN or infinite scale: the
+//   whole block reads back as not finite.
+//
+// Both kernels are bound by HBM: 26 or 28 bytes per parameter with 32-bit
+// states, 14.1 or 16.1 with 8-bit ones (BF16 or FP32 gradients).
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "mx_codec.cuh"
+#include "mx_internal.h"
+#include "mx_ptx.cuh"
+
+namespace mx {
+namespace {
+
+constexpr int kOptThreads = 256;
+constexpr int kStateBlock = MX_ADAMW_STATE_BLOCK;  // elements that share the scales of 8-bit states
+static_assert(kStateBlock == 256, "one warp, eight elements a lane");
+// Elements of one work unit of a CTA: two float4 per thread with 32-bit states,
+// one state block per warp with 8-bit ones.
+constexpr int kChunk = 2048;
+
+struct OptTensor {
+  float* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t n;
+  float decay;      // 1 - lr * weight_decay
+  uint32_t key;     // hash of (seed, tensor)
+  int32_t chunk0;   // first work unit of this tensor
+  uint16_t g_f32;   // gradient type: 1 FP32, 0 BF16
+  uint16_t vec;     // every pointer allows 16-byte (codes: 8-byte) accesses
+};
+static_assert(sizeof(OptTensor) == 72, "layout");
+
+struct OptHyper {
+  float b1, c1, b2, c2, rs, eps, step;  // c1 = 1 - b1, c2 = 1 - b2
+  const float* grad_scale;
+  int* dev_status;
+  int32_t n;
+  int32_t chunks;
+};
+
+// The descriptors travel in the kernel parameters (no device table to keep).
+// Three sizes, because a launch copies its whole parameter block.
+template <int kCap>
+struct OptArgs {
+  OptHyper h;
+  OptTensor t[kCap];
+};
+constexpr int kCapSmall = 4, kCapMid = 48, kCapLarge = 448;
+static_assert(sizeof(OptArgs<kCapLarge>) <= 32764, "kernel parameter space");
+
+__host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {  // MurmurHash3's 32-bit finaliser
+  x ^= x >> 16;
+  x *= 0x85EBCA6Bu;
+  x ^= x >> 13;
+  x *= 0xC2B2AE35u;
+  return x ^ (x >> 16);
+}
+
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ void adamw_update(float& p, float g, float& m, float& v, const OptHyper& h, float gs,
+                                             float decay) {
+  g = __fmul_rn(g, gs);
+  m = __fadd_rn(__fmul_rn(m, h.b1), __fmul_rn(g, h.c1));
+  v = __fadd_rn(__fmul_rn(v, h.b2), __fmul_rn(__fmul_rn(g, g), h.c2));
+  const float den = fmaf(sqrt_approx(v), h.rs, h.eps);
+  p = fmaf(p, decay, -h.step * __fdividef(m, den));
+}
+
+__device__ __forceinline__ float load_grad(const OptTensor& t, int64_t i) {
+  return t.g_f32 ? static_cast<const float*>(t.g)[i]
+                 : __bfloat162float(static_cast<const __nv_bfloat16*>(t.g)[i]);
+}
+
+// The tensor that owns work unit c; `from` is a tensor at or before it.
+template <int kCap>
+__device__ __forceinline__ int tensor_of(const OptArgs<kCap>& a, int32_t c, int from) {
+  int lo = from, hi = a.h.n - 1;
+  if (lo == hi || c < a.t[lo + 1].chunk0) return lo;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a.t[mid].chunk0 <= c) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Reads the gradients' scale; false (every thread alike) if the step is skipped.
+__device__ __forceinline__ bool grad_scale_of(const OptHyper& h, float& gs) {
+  gs = h.grad_scale ? *h.grad_scale : 1.0f;
+  if (fabsf(gs) <= 3.402823466e38f) return true;
+  if (blockIdx.x == 0 && threadIdx.x == 0 && h.dev_status)
+    atomicExch(h.dev_status, static_cast<int>(MX_ERR_DEVICE_CHECK));
+  return false;
+}
+
+// 32-bit states: a thread takes two float4 of its CTA's unit, 256 float4 apart.
+template <int kCap>
+__global__ void __launch_bounds__(kOptThreads) adamw32_kernel(const __grid_constant__ OptArgs<kCap> a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  float gs;
+  if (!grad_scale_of(a.h, gs)) return;
+  int ti = 0;
+  for (int32_t c = blockIdx.x; c < a.h.chunks; c += gridDim.x) {
+    ti = tensor_of(a, c, ti);
+    const OptTensor& t = a.t[ti];
+    const int64_t base = static_cast<int64_t>(c - t.chunk0) * kChunk;
+    float* m = static_cast<float*>(t.m);
+    float* v = static_cast<float*>(t.v);
+    if (t.vec && base + kChunk <= t.n) {
+      float4 p4[2], m4[2], v4[2], g4[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int64_t i = base + (u * kOptThreads + threadIdx.x) * 4;
+        p4[u] = *reinterpret_cast<const float4*>(t.p + i);
+        m4[u] = *reinterpret_cast<const float4*>(m + i);
+        v4[u] = *reinterpret_cast<const float4*>(v + i);
+        if (t.g_f32) {
+          g4[u] = *reinterpret_cast<const float4*>(static_cast<const float*>(t.g) + i);
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(t.g) + i);
+          g4[u] = make_float4(lo_f(w.x), hi_f(w.x), lo_f(w.y), hi_f(w.y));
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int64_t i = base + (u * kOptThreads + threadIdx.x) * 4;
+        adamw_update(p4[u].x, g4[u].x, m4[u].x, v4[u].x, a.h, gs, t.decay);
+        adamw_update(p4[u].y, g4[u].y, m4[u].y, v4[u].y, a.h, gs, t.decay);
+        adamw_update(p4[u].z, g4[u].z, m4[u].z, v4[u].z, a.h, gs, t.decay);
+        adamw_update(p4[u].w, g4[u].w, m4[u].w, v4[u].w, a.h, gs, t.decay);
+        *reinterpret_cast<float4*>(t.p + i) = p4[u];
+        *reinterpret_cast<float4*>(m + i) = m4[u];
+        *reinterpret_cast<float4*>(v + i) = v4[u];
+      }
+    } else {
+      const int64_t end = min64(base + kChunk, t.n);
+      for (int64_t i = base + threadIdx.x; i < end; i += kOptThreads) {
+        float pi = t.p[i], mi = m[i], vi = v[i];
+        adamw_update(pi, load_grad(t, i), mi, vi, a.h, gs, t.decay);
+        t.p[i] = pi;
+        m[i] = mi;
+        v[i] = vi;
+      }
+    }
+  }
+}
+
+// 8-bit states: a warp takes one state block of 256 elements, eight a lane
+// (eight neighbours where the pointers allow wide accesses, else every 32nd),
+// so a block's amax is one warp reduction and its codes are written once.
+__device__ __forceinline__ uint32_t encode_v(float v, float inv, uint32_t rand) {
+  const int32_t c = static_cast<int32_t>((__float_as_uint(__fmul_rn(v, inv)) + (rand & 0xFFFFFu)) >> 20) - 761;
+  return v > 0.0f ? static_cast<uint32_t>(min(max(c, 1), 255)) : 0u;
+}
+
+__device__ __forceinline__ float decode_v(uint32_t c, float scale) {
+  return __fmul_rn(c ? __uint_as_float((c + 761u) << 20) : 0.0f, scale);
+}
+
+__device__ __forceinline__ float decode_e4m3(uint32_t c) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(c), __NV_E4M3);
+  return __half2float(__half(h));
+}
+
+template <int kCap>
+__global__ void __launch_bounds__(kOptThreads) adamw8_kernel(const __grid_constant__ OptArgs<kCap> a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  float gs;
+  if (!grad_scale_of(a.h, gs)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int ti = 0;
+  for (int32_t c = blockIdx.x; c < a.h.chunks; c += gridDim.x) {
+    ti = tensor_of(a, c, ti);
+    const OptTensor& t = a.t[ti];
+    const int64_t blk = static_cast<int64_t>(c - t.chunk0) * (kChunk / kStateBlock) + warp;
+    const int64_t base = blk * kStateBlock;
+    if (base >= t.n) continue;
+    uint8_t* mc = static_cast<uint8_t*>(t.m);
+    uint8_t* vc = static_cast<uint8_t*>(t.v);
+    const bool vec = t.vec && base + kStateBlock <= t.n;
+    const int64_t i0 = base + (vec ? lane * 8 : lane);
+    const int stride = vec ? 1 : 32;
+    const float ms = t.m_scale[blk], vs = t.v_scale[blk];
+    float p[8], g[8], m[8], v[8];
+    if (vec) {
+      const float4 p0 = *reinterpret_cast<const float4*>(t.p + i0), p1 = *reinterpret_cast<const float4*>(t.p + i0 + 4);
+      const uint2 mw = *reinterpret_cast<const uint2*>(mc + i0), vw = *reinterpret_cast<const uint2*>(vc + i0);
+      if (t.g_f32) {
+        const float* gp = static_cast<const float*>(t.g) + i0;
+        const float4 g0 = *reinterpret_cast<const float4*>(gp), g1 = *reinterpret_cast<const float4*>(gp + 4);
+        g[0] = g0.x, g[1] = g0.y, g[2] = g0.z, g[3] = g0.w, g[4] = g1.x, g[5] = g1.y, g[6] = g1.z, g[7] = g1.w;
+      } else {
+        const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(t.g) + i0);
+        g[0] = lo_f(w.x), g[1] = hi_f(w.x), g[2] = lo_f(w.y), g[3] = hi_f(w.y);
+        g[4] = lo_f(w.z), g[5] = hi_f(w.z), g[6] = lo_f(w.w), g[7] = hi_f(w.w);
+      }
+      p[0] = p0.x, p[1] = p0.y, p[2] = p0.z, p[3] = p0.w, p[4] = p1.x, p[5] = p1.y, p[6] = p1.z, p[7] = p1.w;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        m[j] = __fmul_rn(decode_e4m3(((j < 4 ? mw.x : mw.y) >> (8 * (j & 3))) & 0xFFu), ms);
+        v[j] = decode_v(((j < 4 ? vw.x : vw.y) >> (8 * (j & 3))) & 0xFFu, vs);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int64_t i = i0 + j * 32;
+        const bool in = i < t.n;  // past the end: zeros, which leave the block's amax alone
+        p[j] = in ? t.p[i] : 0.0f;
+        g[j] = in ? load_grad(t, i) : 0.0f;
+        m[j] = in ? __fmul_rn(decode_e4m3(mc[i]), ms) : 0.0f;
+        v[j] = in ? decode_v(vc[i], vs) : 0.0f;
+      }
+    }
+    uint32_t m_bits = 0, v_bits = 0;  // the largest magnitudes as integers: NaN above infinity above finite
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      adamw_update(p[j], g[j], m[j], v[j], a.h, gs, t.decay);
+      m_bits = max(m_bits, __float_as_uint(m[j]) & 0x7FFFFFFFu);
+      v_bits = max(v_bits, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    }
+    const float m_amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, m_bits));
+    const float v_amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, v_bits));
+    const bool tiny = m_amax < 7.888609052210118e-31f;  // 2^-100
+    const float m_inv = tiny ? 0.0f : __fmul_rn(__frcp_rn(m_amax), 448.0f);
+    const float v_inv = __frcp_rn(v_amax);
+    uint32_t vq[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t i = i0 + static_cast<int64_t>(j) * stride;
+      vq[j] = encode_v(v[j], v_inv, mix32(static_cast<uint32_t>(i) + t.key + static_cast<uint32_t>(i >> 32) * 0x9E3779B9u));
+      m[j] = __fmul_rn(m[j], m_inv);
+    }
+    if (lane == 0) {
+      t.m_scale[blk] = tiny ? 0.0f : __fmul_rn(m_amax, 1.0f / 448.0f);
+      t.v_scale[blk] = v_amax;
+    }
+    if (vec) {
+      *reinterpret_cast<float4*>(t.p + i0) = make_float4(p[0], p[1], p[2], p[3]);
+      *reinterpret_cast<float4*>(t.p + i0 + 4) = make_float4(p[4], p[5], p[6], p[7]);
+      *reinterpret_cast<uint2*>(mc + i0) = make_uint2(cvt_pair(m[0], m[1]) | cvt_pair(m[2], m[3]) << 16,
+                                                      cvt_pair(m[4], m[5]) | cvt_pair(m[6], m[7]) << 16);
+      *reinterpret_cast<uint2*>(vc + i0) = make_uint2(vq[0] | vq[1] << 8 | vq[2] << 16 | vq[3] << 24,
+                                                      vq[4] | vq[5] << 8 | vq[6] << 16 | vq[7] << 24);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int64_t i = i0 + j * 32;
+        if (i < t.n) {
+          t.p[i] = p[j];
+          mc[i] = static_cast<uint8_t>(cvt_pair(m[j], 0.0f));
+          vc[i] = static_cast<uint8_t>(vq[j]);
+        }
+      }
+    }
+  }
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+template <int kCap>
+mx_status launch_adamw_cap(const mx_adamw_tensor* tensors, int first, int n, int bits, const mx_adamw_hyper& hy,
+                           const float* grad_scale, int* dev_status, cudaStream_t s) {
+  static thread_local OptArgs<kCap> a;
+  const double bc1 = 1.0 - std::pow(hy.beta1, static_cast<double>(hy.step));
+  const double bc2 = 1.0 - std::pow(hy.beta2, static_cast<double>(hy.step));
+  a.h.b1 = static_cast<float>(hy.beta1);
+  a.h.c1 = static_cast<float>(1.0 - hy.beta1);
+  a.h.b2 = static_cast<float>(hy.beta2);
+  a.h.c2 = static_cast<float>(1.0 - hy.beta2);
+  a.h.rs = static_cast<float>(1.0 / std::sqrt(bc2));
+  a.h.eps = static_cast<float>(hy.eps);
+  a.h.step = static_cast<float>(hy.lr / bc1);
+  a.h.grad_scale = grad_scale;
+  a.h.dev_status = dev_status;
+  int64_t chunks = 0;
+  int k = 0;
+  for (int i = first; i < first + n; ++i) {
+    const mx_adamw_tensor& x = tensors[i];
+    if (x.numel == 0) continue;
+    OptTensor& t = a.t[k++];
+    t.p = x.param;
+    t.g = x.grad;
+    t.m = x.exp_avg;
+    t.v = x.exp_avg_sq;
+    t.m_scale = x.exp_avg_scale;
+    t.v_scale = x.exp_avg_sq_scale;
+    t.n = x.numel;
+    t.decay = static_cast<float>(1.0 - hy.lr * x.weight_decay);
+    t.key = mix32(hy.seed + 0x9E3779B9u * static_cast<uint32_t>(i + 1));
+    t.chunk0 = static_cast<int32_t>(chunks);
+    t.g_f32 = x.grad_dtype == MX_F32;
+    const uintptr_t ma = bits == 8 ? 8 : 16;
+    t.vec = aligned(x.param, 16) && aligned(x.grad, 16) && aligned(x.exp_avg, ma) && aligned(x.exp_avg_sq, ma);
+    chunks += (x.numel + kChunk - 1) / kChunk;
+    if (chunks > 0x7FFFFFFF) {
+      set_error("mx_adamw_step: too many elements in one call");
+      return MX_ERR_UNSUPPORTED_SHAPE;
+    }
+  }
+  if (k == 0) return MX_OK;
+  a.h.n = k;
+  a.h.chunks = static_cast<int32_t>(chunks);
+  const int64_t grid = std::min<int64_t>(chunks, static_cast<int64_t>(sm_count()) * 8);
+  auto kern = bits == 8 ? adamw8_kernel<kCap> : adamw32_kernel<kCap>;
+  return cuda_status(launch_kernel(kern, static_cast<unsigned>(grid), kOptThreads, 0, s, 1, a), "mx_adamw_step launch");
+}
+
+}  // namespace
+
+mx_status launch_adamw(const mx_adamw_tensor* tensors, int n, int bits, const mx_adamw_hyper& hy,
+                       const float* grad_scale, int* dev_status, cudaStream_t s) {
+  for (int i = 0; i < n; i += kCapLarge) {
+    const int k = std::min(n - i, kCapLarge);
+    mx_status st;
+    if (k <= kCapSmall) st = launch_adamw_cap<kCapSmall>(tensors, i, k, bits, hy, grad_scale, dev_status, s);
+    else if (k <= kCapMid) st = launch_adamw_cap<kCapMid>(tensors, i, k, bits, hy, grad_scale, dev_status, s);
+    else st = launch_adamw_cap<kCapLarge>(tensors, i, k, bits, hy, grad_scale, dev_status, s);
+    if (st != MX_OK) return st;
+  }
+  return MX_OK;
+}
+
+}  // namespace mx

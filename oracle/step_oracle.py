@@ -1,0 +1,52 @@
+"""CPU oracle of the operators around the products of a training step: AdamW.
+
+Test infrastructure only, plain float64 numpy written from the definitions in
+include/mxfp8.h; it shares no code with the CUDA path.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+STATE_BLOCK = 256
+
+
+# ---------------------------------------------------------------------------
+# AdamW
+# ---------------------------------------------------------------------------
+
+def adamw(p, g, m, v, lr, beta1, beta2, eps, weight_decay, step, grad_scale=1.0):
+    """One step in float64: (p, m, v, update), update = what the moments took off p."""
+    g = g * grad_scale
+    m = beta1 * m + (1 - beta1) * g
+    v = beta2 * v + (1 - beta2) * g * g
+    with np.errstate(invalid="ignore", divide="ignore"):
+        update = lr * (m / (1 - beta1 ** step)) / (np.sqrt(v / (1 - beta2 ** step)) + eps)
+    return p - lr * weight_decay * p - update, m, v, update
+
+
+def e4m3_values() -> np.ndarray:
+    """The value of each of the 256 E4M3 codes."""
+    c = np.arange(256)
+    e, f = (c >> 3) & 15, c & 7
+    mag = np.where(e == 0, f / 8 * 2.0 ** -6, (1 + f / 8) * 2.0 ** (e - 7.0))
+    mag = np.where((c & 0x7F) == 0x7F, np.nan, mag)
+    return np.where(c & 0x80, -mag, mag)
+
+
+def second_moment_values() -> np.ndarray:
+    """The value of each of the 256 codes of the second moment, in units of the
+    block's scale: 0, then eighths of binades up to code 255 = 1."""
+    out = np.zeros(256)
+    for c in range(1, 256):
+        out[c] = 2.0 ** ((c + 1) // 8 - 32) * (1 + ((c + 1) % 8) / 8)
+    return out
+
+
+def block_scale(scale, n) -> np.ndarray:
+    """One scale for each of n elements."""
+    return np.repeat(np.asarray(scale, dtype=np.float64), STATE_BLOCK)[:n]
+
+
+def block_amax(x) -> np.ndarray:
+    x = np.abs(np.asarray(x, dtype=np.float64))
+    return np.array([x[i:i + STATE_BLOCK].max() for i in range(0, len(x), STATE_BLOCK)])

@@ -1,0 +1,61 @@
+"""Host-side refusals of the operators around the products (no GPU needed):
+every invalid argument is rejected before any device work."""
+import os
+
+import pytest
+
+import mxfp8_block_scaled_gb300 as mx
+
+INVALID, SHAPE, ALIGN = 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(mx.LIB_PATH):
+        from mxfp8_block_scaled_gb300 import build
+        build.build()
+    return mx.lib()
+
+
+def status_of(fn, *args):
+    try:
+        fn(*args)
+    except mx.MXError as e:
+        return e.status
+    return 0
+
+
+def adamw_tensor(**kw):
+    d = dict(param=0x1000, grad=0x2000, exp_avg=0x3000, exp_avg_sq=0x4000, exp_avg_scale=0x5000, exp_avg_sq_scale=0x6000,
+             numel=100, weight_decay=0.0, grad_dtype=mx.MX_F32, reserved=0)
+    d.update(kw)
+    return mx.MXAdamWTensorC(**d)
+
+
+def adamw(tensor=None, bits=32, n=1, **hyper):
+    h = dict(lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, step=1, seed=0, reserved=0)
+    h.update(hyper)
+    t = (mx.MXAdamWTensorC * 1)(tensor or adamw_tensor())
+    return status_of(mx.mx_adamw_step, t, n, bits, mx.MXAdamWHyperC(**h), None, None, None)
+
+
+def test_adamw_refusals(L):
+    assert adamw(n=0) == 0
+    assert adamw(n=-1) == INVALID
+    assert adamw(bits=16) == INVALID
+    for bad in (dict(lr=float("nan")), dict(beta1=1.0), dict(beta1=-0.1), dict(beta2=1.0), dict(beta2=float("nan")),
+                dict(eps=-1.0), dict(eps=float("inf")), dict(step=0), dict(reserved=1)):
+        assert adamw(**bad) == INVALID, bad
+    for bad in (dict(param=0), dict(grad=0), dict(exp_avg=0), dict(exp_avg_sq=0), dict(numel=-1), dict(grad_dtype=2),
+                dict(reserved=1), dict(weight_decay=float("inf"))):
+        assert adamw(adamw_tensor(**bad)) == INVALID, bad
+    assert adamw(adamw_tensor(exp_avg_scale=0), bits=8) == INVALID
+    for bad in (dict(param=0x1002), dict(grad=0x2002), dict(exp_avg=0x3001), dict(exp_avg_sq=0x4002)):
+        assert adamw(adamw_tensor(**bad)) == ALIGN, bad
+    assert adamw(adamw_tensor(grad=0x2001, grad_dtype=mx.MX_BF16)) == ALIGN
+    assert adamw(adamw_tensor(exp_avg_scale=0x5002), bits=8) == ALIGN
+    t = (mx.MXAdamWTensorC * 1)(adamw_tensor())
+    h = mx.MXAdamWHyperC(1e-3, 0.9, 0.999, 1e-8, 1, 0, 0)
+    assert status_of(mx.mx_adamw_step, None, 1, 32, h, None, None, None) == INVALID
+    assert status_of(mx.mx_adamw_step, t, 1, 32, None, None, None, None) == INVALID
+    assert status_of(mx.mx_adamw_step, t, 1, 32, h, 0x7002, None, None) == ALIGN
