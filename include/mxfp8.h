@@ -588,6 +588,44 @@ typedef struct mx_adamw_hyper {
 mx_status mx_adamw_step(const mx_adamw_tensor* tensors, int n, int state_bits, const mx_adamw_hyper* hyper,
                         const float* grad_scale, int* dev_status, void* stream);
 
+/*
+ * mx_layer_norm - normalises each row of x[rows, cols] (pitch ldx):
+ *   y = (x - mean) * rstd * weight + bias,  rstd = 1 / sqrt(var + eps),
+ *   var = sum((x - mean)^2) / cols
+ * in FP32, rounded once to y's type. center = 1: mean is the row's (layer
+ * norm); center = 0: mean = 0 (root-mean-square norm, var = sum(x^2) / cols).
+ *
+ *   dtype        mx_dtype of x and y (pitch ldy).
+ *   weight, bias cols entries of param_dtype; NULL stands for 1 and 0.
+ *   mean, rstd   FP32 [rows] for the backward pass, written; NULL where they
+ *                are not wanted (mean is not written with center = 0).
+ *   1 <= cols < 2^31; rows may be 0. Any alignment of the element types works;
+ *   rows that all start on 16-byte boundaries are read in 16-byte vectors. No
+ *   output may overlap an input.
+ */
+mx_status mx_layer_norm(const void* x, int64_t ldx, const void* weight, const void* bias, int param_dtype, int64_t rows,
+                        int64_t cols, float eps, int center, int dtype, void* y, int64_t ldy, float* mean, float* rstd,
+                        int* dev_status, void* stream);
+
+/*
+ * mx_layer_norm_backward - gradients of mx_layer_norm from dy, x and the saved
+ * row statistics. With h = (x - mean) * rstd and g = dy * weight:
+ *   dx = rstd * (g - sum(g)/cols - h * sum(g h)/cols)   (center = 0: no sum(g))
+ *   dweight = sum over rows of dy * h,  dbias = sum over rows of dy.
+ *
+ *   dtype      mx_dtype of dy, x and dx (pitches lddy, ldx, lddx).
+ *   dweight, dbias  FP32 [cols], written; NULL where not wanted. rows = 0
+ *              writes zeros.
+ *   workspace  scratch of at least mx_layer_norm_backward_workspace_bytes(rows,
+ *              cols), 16-byte aligned; may be NULL if dweight and dbias both are.
+ * Sums over rows are added in a fixed order: same inputs, same bits.
+ */
+size_t mx_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+mx_status mx_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* weight,
+                                 int param_dtype, const float* mean, const float* rstd, int64_t rows, int64_t cols,
+                                 int center, int dtype, void* dx, int64_t lddx, float* dweight, float* dbias,
+                                 void* workspace, size_t workspace_bytes, int* dev_status, void* stream);
+
 /* Static description of a status code. */
 const char* mx_status_string(mx_status s);
 

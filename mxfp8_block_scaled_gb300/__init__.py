@@ -40,7 +40,8 @@ EXPORTED = ("mx_scale_bytes", "mx_grouped_padded_rows", "mx_quantize", "mx_quant
             "mx_gemm_fp8_blockwise", "mx_status_string", "mx_last_error", "mx_abi_version",
             "mx_selftest_wait_timeout", "mx_gemm_workspace_bytes", "mx_gemm_with_workspace", "mx_gemm_multi",
             "mx_gemm_static_workspace", "mx_current_amax", "mx_quantize_current", "mx_gemm_current",
-            "mx_grouped_gemm_current", "mx_gemm_current_multi", "mx_grouped_gemm_swiglu_quantize", "mx_adamw_step")
+            "mx_grouped_gemm_current", "mx_gemm_current_multi", "mx_grouped_gemm_swiglu_quantize", "mx_adamw_step",
+            "mx_layer_norm", "mx_layer_norm_backward_workspace_bytes", "mx_layer_norm_backward")
 MX_STATIC_WORKSPACE_BYTES = 40 * 1024 * 1024
 
 
@@ -144,6 +145,13 @@ def lib() -> ctypes.CDLL:
     L.mx_gemm_fp8_blockwise.restype = i32
     L.mx_adamw_step.argtypes = [vp, i32, i32, ctypes.POINTER(MXAdamWHyperC), vp, vp, vp]
     L.mx_adamw_step.restype = i32
+    L.mx_layer_norm.argtypes = [vp, i64, vp, vp, i32, i64, i64, ctypes.c_float, i32, i32, vp, i64, vp, vp, vp, vp]
+    L.mx_layer_norm.restype = i32
+    L.mx_layer_norm_backward_workspace_bytes.argtypes = [i64, i64]
+    L.mx_layer_norm_backward_workspace_bytes.restype = ctypes.c_size_t
+    L.mx_layer_norm_backward.argtypes = [vp, i64, vp, i64, vp, i32, vp, vp, i64, i64, i32, i32, vp, i64, vp, vp, vp,
+                                         ctypes.c_size_t, vp, vp]
+    L.mx_layer_norm_backward.restype = i32
     L.mx_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp, vp]
     L.mx_selftest_wait_timeout.restype = i32
     L.mx_status_string.argtypes = [i32]
@@ -306,6 +314,23 @@ def mx_grouped_gemm_swiglu_quantize(a: MXOperandC, b: MXOperandC, group_offsets,
 def mx_adamw_step(tensors, n, state_bits, hyper: MXAdamWHyperC, grad_scale, dev_status, stream) -> None:
     """``tensors``: an array of n MXAdamWTensorC, or the bytes of one."""
     _check(lib().mx_adamw_step(tensors, n, state_bits, _ref(hyper), grad_scale, dev_status, stream), "mx_adamw_step")
+
+
+def mx_layer_norm(x, ldx, weight, bias, param_dtype, rows, cols, eps, center, dtype, y, ldy, mean, rstd, dev_status,
+                  stream) -> None:
+    _check(lib().mx_layer_norm(x, ldx, weight, bias, param_dtype, rows, cols, eps, center, dtype, y, ldy, mean, rstd,
+                               dev_status, stream), "mx_layer_norm")
+
+
+def mx_layer_norm_backward_workspace_bytes(rows, cols) -> int:
+    return int(lib().mx_layer_norm_backward_workspace_bytes(rows, cols))
+
+
+def mx_layer_norm_backward(dy, lddy, x, ldx, weight, param_dtype, mean, rstd, rows, cols, center, dtype, dx, lddx,
+                           dweight, dbias, workspace, workspace_bytes, dev_status, stream) -> None:
+    _check(lib().mx_layer_norm_backward(dy, lddy, x, ldx, weight, param_dtype, mean, rstd, rows, cols, center, dtype,
+                                        dx, lddx, dweight, dbias, workspace, workspace_bytes, dev_status, stream),
+           "mx_layer_norm_backward")
 
 
 # ---------------------------------------------------------------------------
@@ -757,3 +782,65 @@ def adamw_step(params, grads, states, lr: float, betas=(0.9, 0.999), eps: float 
     hyper = MXAdamWHyperC(lr, betas[0], betas[1], eps, step, seed & 0xFFFFFFFF, 0)
     mx_adamw_step(struct.pack(_ADAMW_TENSOR * n, *flat), n, bits, hyper, _ptr(grad_scale), _ptr(status),
                   _stream(stream))
+
+
+def _rows(t) -> int:
+    """Pitch of a 2-D matrix with contiguous rows."""
+    assert t.dim() == 2 and t.is_cuda and (t.stride(1) == 1 or t.shape[1] <= 1), "needs 2-D CUDA tensors with contiguous rows"
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _params(weight, bias, cols) -> int:
+    """The one dtype of a norm's weight and bias."""
+    dtype = MX_F32
+    for p in (weight, bias):
+        if p is not None:
+            assert p.is_cuda and p.is_contiguous() and p.numel() == cols, "weight and bias: contiguous, one entry per column"
+            dtype = _dtype(p)
+    assert weight is None or bias is None or weight.dtype == bias.dtype, "weight and bias have the same dtype"
+    return dtype
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, center: bool = True, out=None, stats: bool = True,
+               status=None, stream=None):
+    """Layer norm of each row of x (2-D, BF16 or FP32, any row pitch), or with
+    center=False the root-mean-square norm. Returns (y, mean, rstd): y in x's
+    dtype, the FP32 row statistics for layer_norm_backward (mean None with
+    center=False, both None with stats=False)."""
+    torch = _torch()
+    R, C = x.shape
+    dev = x.device
+    dtype, pd, ldx = _dtype(x), _params(weight, bias, C), _rows(x)
+    if out is None:
+        out = torch.empty((R, C), dtype=x.dtype, device=dev)
+    assert out.dtype == x.dtype and out.shape == x.shape
+    mean = torch.empty(R, dtype=torch.float32, device=dev) if stats and center else None
+    rstd = torch.empty(R, dtype=torch.float32, device=dev) if stats else None
+    mx_layer_norm(x.data_ptr(), ldx, _ptr(weight), _ptr(bias), pd, R, C, eps, int(center), dtype, out.data_ptr(),
+                  _rows(out), _ptr(mean), _ptr(rstd), _ptr(status), _stream(stream))
+    return out, mean, rstd
+
+
+def layer_norm_backward(dy, x, weight, mean, rstd, center: bool = True, param_grads: bool = True, status=None,
+                        stream=None):
+    """Gradients of layer_norm: (dx in x's dtype, dweight FP32, dbias FP32; the
+    two None with param_grads=False). mean and rstd are layer_norm's."""
+    torch = _torch()
+    R, C = x.shape
+    dev = x.device
+    assert dy.shape == x.shape and dy.dtype == x.dtype
+    assert rstd.dtype == torch.float32 and rstd.is_contiguous() and rstd.numel() == R
+    assert not center or (mean.dtype == torch.float32 and mean.is_contiguous() and mean.numel() == R)
+    pd = _params(weight, None, C)
+    dx = torch.empty((R, C), dtype=x.dtype, device=dev)
+    dw = db = ws = None
+    need = 0
+    if param_grads:
+        dw = torch.empty(C, dtype=torch.float32, device=dev)
+        db = torch.empty(C, dtype=torch.float32, device=dev)
+        need = mx_layer_norm_backward_workspace_bytes(R, C)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    mx_layer_norm_backward(dy.data_ptr(), _rows(dy), x.data_ptr(), _rows(x), _ptr(weight), pd,
+                           _ptr(mean) if center else None, rstd.data_ptr(), R, C, int(center), _dtype(x), dx.data_ptr(),
+                           C, _ptr(dw), _ptr(db), _ptr(ws), need, _ptr(status), _stream(stream))
+    return dx, dw, db

@@ -40,6 +40,53 @@ mx_status check_adamw_tensor(const mx_adamw_tensor& t, int i, int bits) {
   return MX_OK;
 }
 
+// Sizes, types and pitches that both directions of the norm share.
+mx_status check_norm(const char* fn, int64_t rows, int64_t cols, int dtype, int param_dtype, int center) {
+  if (rows < 0 || cols < 1 || !known_dtype(dtype) || !known_dtype(param_dtype) || (center != 0 && center != 1)) {
+    set_error("%s: needs rows >= 0, cols >= 1, a known dtype and param_dtype, center 0 or 1", fn);
+    return MX_ERR_INVALID_ARG;
+  }
+  if (cols > 0x7FFFFFFFLL) {
+    set_error("%s: cols must be < 2^31", fn);
+    return MX_ERR_UNSUPPORTED_SHAPE;
+  }
+  return MX_OK;
+}
+
+// A matrix argument: present, a pitch of at least cols, aligned to its type.
+mx_status check_matrix(const char* fn, const char* name, const void* p, int64_t ld, int64_t cols, int elem) {
+  if (!p || ld < cols) {
+    set_error("%s: %s is null or its pitch is less than its columns", fn, name);
+    return MX_ERR_INVALID_ARG;
+  }
+  if (!aligned(p, elem)) {
+    set_error("%s: %s is not aligned to its element type", fn, name);
+    return MX_ERR_ALIGNMENT;
+  }
+  return MX_OK;
+}
+
+mx_status check_aligned(const char* fn, const char* name, const void* p, int a) {
+  if (aligned(p, a)) return MX_OK;
+  set_error("%s: %s is not %d-byte aligned", fn, name, a);
+  return MX_ERR_ALIGNMENT;
+}
+
+// Scratch of at least `need` bytes, 16-byte aligned.
+mx_status check_workspace(const char* fn, const void* ws, size_t bytes, size_t need) {
+  if (!ws || bytes < need) {
+    set_error("%s: needs a workspace of %llu bytes", fn, static_cast<unsigned long long>(need));
+    return MX_ERR_INVALID_ARG;
+  }
+  return check_aligned(fn, "workspace", ws, 16);
+}
+
+#define MX_CHECK(call)                       \
+  do {                                       \
+    const mx_status check_st = (call);       \
+    if (check_st != MX_OK) return check_st;  \
+  } while (0)
+
 }  // namespace
 
 extern "C" {
@@ -72,6 +119,97 @@ mx_status mx_adamw_step(const mx_adamw_tensor* tensors, int n, int state_bits, c
   const mx_status st = check_device();
   if (st != MX_OK) return st;
   return launch_adamw(tensors, n, state_bits, h, grad_scale, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+mx_status mx_layer_norm(const void* x, int64_t ldx, const void* weight, const void* bias, int param_dtype, int64_t rows,
+                        int64_t cols, float eps, int center, int dtype, void* y, int64_t ldy, float* mean, float* rstd,
+                        int* dev_status, void* stream) {
+  const char* fn = "mx_layer_norm";
+  (void)dev_status;  // nothing that only the device can check
+  MX_CHECK(check_norm(fn, rows, cols, dtype, param_dtype, center));
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) {
+    set_error("mx_layer_norm: eps must be finite and not negative");
+    return MX_ERR_INVALID_ARG;
+  }
+  if (rows == 0) return MX_OK;
+  MX_CHECK(check_matrix(fn, "x", x, ldx, cols, elem_size(dtype)));
+  MX_CHECK(check_matrix(fn, "y", y, ldy, cols, elem_size(dtype)));
+  MX_CHECK(check_aligned(fn, "weight", weight, elem_size(param_dtype)));
+  MX_CHECK(check_aligned(fn, "bias", bias, elem_size(param_dtype)));
+  MX_CHECK(check_aligned(fn, "mean", mean, 4));
+  MX_CHECK(check_aligned(fn, "rstd", rstd, 4));
+  MX_CHECK(check_device());
+  NormLaunch L = {};
+  L.x = x;
+  L.ldx = ldx;
+  L.weight = weight;
+  L.bias = bias;
+  L.param_dtype = param_dtype;
+  L.rows = rows;
+  L.cols = cols;
+  L.dtype = dtype;
+  L.center = center;
+  L.eps = eps;
+  L.out = y;
+  L.ldo = ldy;
+  L.mean = mean;
+  L.rstd = rstd;
+  return launch_norm_forward(L, static_cast<cudaStream_t>(stream));
+}
+
+size_t mx_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
+  return rows <= 0 || cols <= 0 ? 0 : norm_backward_workspace(rows, cols);
+}
+
+mx_status mx_layer_norm_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* weight,
+                                 int param_dtype, const float* mean, const float* rstd, int64_t rows, int64_t cols,
+                                 int center, int dtype, void* dx, int64_t lddx, float* dweight, float* dbias,
+                                 void* workspace, size_t workspace_bytes, int* dev_status, void* stream) {
+  const char* fn = "mx_layer_norm_backward";
+  (void)dev_status;
+  MX_CHECK(check_norm(fn, rows, cols, dtype, param_dtype, center));
+  MX_CHECK(check_aligned(fn, "dweight", dweight, 4));
+  MX_CHECK(check_aligned(fn, "dbias", dbias, 4));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    if (!dweight && !dbias) return MX_OK;
+    MX_CHECK(check_device());
+    for (float* p : {dweight, dbias})
+      if (p) MX_CHECK(cuda_status(cudaMemsetAsync(p, 0, static_cast<size_t>(cols) * 4, s), "cudaMemsetAsync"));
+    return MX_OK;
+  }
+  const int elem = elem_size(dtype);
+  MX_CHECK(check_matrix(fn, "dy", dy, lddy, cols, elem));
+  MX_CHECK(check_matrix(fn, "x", x, ldx, cols, elem));
+  MX_CHECK(check_matrix(fn, "dx", dx, lddx, cols, elem));
+  if (!rstd || (center && !mean)) {
+    set_error("mx_layer_norm_backward: null rstd or mean");
+    return MX_ERR_INVALID_ARG;
+  }
+  MX_CHECK(check_aligned(fn, "weight", weight, elem_size(param_dtype)));
+  MX_CHECK(check_aligned(fn, "mean", mean, 4));
+  MX_CHECK(check_aligned(fn, "rstd", rstd, 4));
+  if (dweight || dbias) MX_CHECK(check_workspace(fn, workspace, workspace_bytes, norm_backward_workspace(rows, cols)));
+  MX_CHECK(check_device());
+  NormLaunch L = {};
+  L.x = x;
+  L.ldx = ldx;
+  L.dy = dy;
+  L.lddy = lddy;
+  L.weight = weight;
+  L.param_dtype = param_dtype;
+  L.rows = rows;
+  L.cols = cols;
+  L.dtype = dtype;
+  L.center = center;
+  L.out = dx;
+  L.ldo = lddx;
+  L.mean = const_cast<float*>(mean);
+  L.rstd = const_cast<float*>(rstd);
+  L.dweight = dweight;
+  L.dbias = dbias;
+  L.ws = workspace;
+  return launch_norm_backward(L, s);
 }
 
 }  // extern "C"

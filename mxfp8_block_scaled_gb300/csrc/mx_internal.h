@@ -152,4 +152,32 @@ mx_status launch_gemm_multi(const GemmLaunch* Ls, int n, cudaStream_t s);
 mx_status launch_adamw(const mx_adamw_tensor* tensors, int n, int bits, const mx_adamw_hyper& hy,
                        const float* grad_scale, int* dev_status, cudaStream_t s);
 
+struct NormLaunch {
+  const void* x;
+  int64_t ldx;
+  const void* dy;  // backward
+  int64_t lddy;
+  const void* weight;  // null: 1
+  const void* bias;    // null: 0
+  int param_dtype;
+  int64_t rows, cols;
+  int dtype;
+  int center;
+  float eps;
+  void* out;  // y or dx
+  int64_t ldo;
+  float* mean;
+  float* rstd;
+  float* dweight;  // backward, may be null
+  float* dbias;
+  void* ws;
+};
+mx_status launch_norm_forward(const NormLaunch& L, cudaStream_t s);
+mx_status launch_norm_backward(const NormLaunch& L, cudaStream_t s);
+size_t norm_backward_workspace(int64_t rows, int64_t cols);
+// Sums over p < parts of partial[p][c], added in a fixed order: columns [0, n0)
+// to out0, [n0, n0 + n1) to out1 (null: not wanted).
+mx_status launch_column_reduce(const float* partial, int parts, int64_t n0, int64_t n1, float* out0, float* out1,
+                               cudaStream_t s);
+
 }  // namespace mx

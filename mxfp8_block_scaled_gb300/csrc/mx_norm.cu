@@ -1,0 +1,622 @@
+// mx_norm.cu - layer norm and root-mean-square norm over the rows of a matrix,
+// forward and backward (the norm before a Linear; "DeepSeek-V3 16B FSDP2
+// MXFP8/HiF8 训练设计" §1 keeps norms out of the low-precision operators).
+//
+//   forward   mean = sum(x) / C (0 without centring), var = sum((x - mean)^2) / C
+//             rstd = 1 / sqrt(var + eps), y = (x - mean) * rstd * w + b
+//   backward  h = (x - mean) * rstd, g = dy * w
+//             dx = rstd * (g - sum(g) / C - h * sum(g * h) / C)  (no sum(g) without centring)
+//             dw = sum over rows of dy * h, db = sum over rows of dy
+//
+// Everything is computed in FP32 and rounded once to the output's type. The
+// variance is summed over centred values held in registers (a second sweep of
+// registers, not of memory), so a mean much larger than the spread costs no
+// digits.
+//
+// Both directions are bound by HBM (forward: x read, y written; backward: x and
+// dy read, dx written). A row is held in the registers of TPR threads, K
+// 16-byte vectors each, and the next row's loads are issued before the current
+// row's sums, so a group always has loads in flight. A group is a warp for
+// narrow rows (no barrier at all), a warp's multiple for wide ones (one barrier
+// per sum over shared memory, two buffers in turn). Rows wider than the
+// registers take a looping kernel.
+// The backward pass keeps dw and db of its columns in registers over all rows
+// of its CTA, adds its groups in shared memory and leaves one partial row per
+// CTA in the workspace; a second launch adds those in a fixed order (same
+// inputs, same bits; no atomics).
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "mx_internal.h"
+#include "mx_ptx.cuh"
+
+namespace mx {
+namespace {
+
+// CTAs of the backward pass, hence partial rows of dw and db: two for each of
+// GB300's 152 SMs at most (a constant, so the workspace's size needs no device).
+constexpr int kMaxPartials = 304;
+
+struct NormArgs {
+  const void* x;
+  const void* dy;      // backward
+  const void* weight;  // null: 1
+  const void* bias;    // null: 0
+  void* out;           // y, or dx
+  float* mean;         // written (forward, may be null), read (backward)
+  float* rstd;
+  float* partial;      // backward: [grid][2][cols], or null: no dw and db wanted
+  int64_t rows;
+  int64_t ldx, lddy, ldo;
+  int32_t cols;
+  int32_t param_f32;
+  int32_t center;
+  float eps;
+  float inv_cols;
+};
+
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Pack {
+  T e[V];
+};
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f(float& d, float x) { d = x; }
+__device__ __forceinline__ void from_f(__nv_bfloat16& d, float x) { d = __float2bfloat16_rn(x); }
+
+// V elements at p, of which nv exist (V or more: all); the rest read as zero.
+template <typename T, int V>
+__device__ __forceinline__ Pack<T, V> load_pack(const T* p, int nv) {
+  Pack<T, V> r;
+  if (nv >= V) {
+    r = *reinterpret_cast<const Pack<T, V>*>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (i < nv) r.e[i] = p[i];
+      else from_f(r.e[i], 0.0f);
+    }
+  }
+  return r;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_pack(T* p, const Pack<T, V>& r, int nv) {
+  if (nv >= V) {
+    *reinterpret_cast<Pack<T, V>*>(p) = r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < nv) p[i] = r.e[i];
+  }
+}
+
+// V parameters from column c as FP32 (dflt where there are none).
+template <int V>
+__device__ __forceinline__ void load_param(const void* p, bool f32, int c, int nv, float dflt, float* o) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = dflt;
+  } else if (f32) {
+    constexpr int W = V < 4 ? V : 4;
+#pragma unroll
+    for (int j = 0; j < V; j += W) {
+      const Pack<float, W> v = load_pack<float, W>(static_cast<const float*>(p) + c + j, nv - j);
+#pragma unroll
+      for (int i = 0; i < W; ++i) o[j + i] = v.e[i];
+    }
+  } else {
+    const Pack<__nv_bfloat16, V> v = load_pack<__nv_bfloat16, V>(static_cast<const __nv_bfloat16*>(p) + c, nv);
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = to_f(v.e[i]);
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// Sums of two values over the TPR threads of a group, to all of them. `slot`:
+// the group's float2 per warp, two buffers in turn (`flip`), so one barrier a
+// sum is enough: nobody writes a buffer again before all have read it, which
+// the barrier of the sum in between shows.
+template <int TPR>
+__device__ __forceinline__ void group_sum(float& a, float& b, float2* slot, int& flip, int group) {
+  a = warp_sum(a);
+  b = warp_sum(b);
+  if constexpr (TPR > 32) {
+    constexpr int W = TPR / 32;
+    float2* buf = slot + flip * W;
+    flip ^= 1;
+    const int w = (threadIdx.x % TPR) >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) buf[w] = make_float2(a, b);
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(TPR) : "memory");
+    const float2 v = lane < W ? buf[lane] : make_float2(0.0f, 0.0f);
+    a = warp_sum(v.x);
+    b = warp_sum(v.y);
+  }
+}
+
+template <typename T, int V, int TPR, int K, int BLOCK>
+__global__ void __launch_bounds__(BLOCK) norm_forward_kernel(const NormArgs a) {
+  constexpr int G = BLOCK / TPR;
+  __shared__ float2 s_sum[G * 2 * (TPR / 32)];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int group = threadIdx.x / TPR, r = threadIdx.x % TPR;
+  float2* slot = s_sum + group * 2 * (TPR / 32);
+  int flip = 0;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * G + group;
+  const T* x = static_cast<const T*>(a.x);
+  Pack<T, V> cur[K], nxt[K];
+  auto fetch = [&](Pack<T, V>* to, int64_t at) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * TPR + r) * V;
+      to[k] = load_pack<T, V>(x + at * a.ldx + c, a.cols - c);
+    }
+  };
+  if (row < a.rows) fetch(cur, row);
+  for (; row < a.rows; row += step) {
+    if (row + step < a.rows) fetch(nxt, row + step);
+    float mean = 0.0f, zero = 0.0f;
+    if (a.center) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) mean += to_f(cur[k].e[i]);  // absent elements are zero
+      group_sum<TPR>(mean, zero, slot, flip, group);
+      mean *= a.inv_cols;
+    }
+    float sq = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int nv = a.cols - (k * TPR + r) * V;
+      if (nv >= V) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float d = to_f(cur[k].e[i]) - mean;
+          sq = fmaf(d, d, sq);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float d = to_f(cur[k].e[i]) - mean;
+          if (i < nv) sq = fmaf(d, d, sq);
+        }
+      }
+    }
+    group_sum<TPR>(sq, zero, slot, flip, group);
+    const float rstd = __frsqrt_rn(fmaf(sq, a.inv_cols, a.eps));
+    T* out = static_cast<T*>(a.out) + row * a.ldo;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * TPR + r) * V, nv = a.cols - c;
+      if (nv <= 0) break;
+      float w[V], b[V];
+      load_param<V>(a.weight, a.param_f32, c, nv, 1.0f, w);
+      load_param<V>(a.bias, a.param_f32, c, nv, 0.0f, b);
+      Pack<T, V> o;
+#pragma unroll
+      for (int i = 0; i < V; ++i) from_f(o.e[i], fmaf((to_f(cur[k].e[i]) - mean) * rstd, w[i], b[i]));
+      store_pack<T, V>(out + c, o, nv);
+    }
+    if (r == 0) {
+      if (a.mean && a.center) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) cur[k] = nxt[k];
+  }
+}
+
+// Rows wider than the registers of a CTA: one CTA a row, the row read three
+// times (from L2 after the first).
+template <typename T, int V>
+__global__ void __launch_bounds__(1024) norm_forward_wide_kernel(const NormArgs a) {
+  __shared__ float2 s_sum[64];
+  pdl_launch_dependents();
+  pdl_wait();
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+    T* out = static_cast<T*>(a.out) + row * a.ldo;
+    float mean = 0.0f, sq = 0.0f, zero = 0.0f;
+    if (a.center) {
+      for (int c = threadIdx.x * V; c < a.cols; c += 1024 * V) {
+        const Pack<T, V> p = load_pack<T, V>(x + c, a.cols - c);
+#pragma unroll
+        for (int i = 0; i < V; ++i) mean += to_f(p.e[i]);
+      }
+      group_sum<1024>(mean, zero, s_sum, flip, 0);
+      mean *= a.inv_cols;
+    }
+    for (int c = threadIdx.x * V; c < a.cols; c += 1024 * V) {
+      const Pack<T, V> p = load_pack<T, V>(x + c, a.cols - c);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float d = to_f(p.e[i]) - mean;
+        if (i < a.cols - c) sq = fmaf(d, d, sq);
+      }
+    }
+    group_sum<1024>(sq, zero, s_sum, flip, 0);
+    const float rstd = __frsqrt_rn(fmaf(sq, a.inv_cols, a.eps));
+    for (int c = threadIdx.x * V; c < a.cols; c += 1024 * V) {
+      const int nv = a.cols - c;
+      const Pack<T, V> p = load_pack<T, V>(x + c, nv);
+      float w[V], b[V];
+      load_param<V>(a.weight, a.param_f32, c, nv, 1.0f, w);
+      load_param<V>(a.bias, a.param_f32, c, nv, 0.0f, b);
+      Pack<T, V> o;
+#pragma unroll
+      for (int i = 0; i < V; ++i) from_f(o.e[i], fmaf((to_f(p.e[i]) - mean) * rstd, w[i], b[i]));
+      store_pack<T, V>(out + c, o, nv);
+    }
+    if (threadIdx.x == 0) {
+      if (a.mean && a.center) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+  }
+}
+
+template <typename T, int V, int TPR, int K, int BLOCK>
+__global__ void __launch_bounds__(BLOCK, BLOCK == 1024 || K * V > 8 ? 1 : 2) norm_backward_kernel(const NormArgs a) {
+  constexpr int G = BLOCK / TPR;
+  __shared__ float2 s_sum[G * 2 * (TPR / 32)];
+  __shared__ float s_acc[G > 1 ? 2 * TPR * K * V : 1];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int group = threadIdx.x / TPR, r = threadIdx.x % TPR;
+  float2* slot = s_sum + group * 2 * (TPR / 32);
+  int flip = 0;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * G + group;
+  const T* x = static_cast<const T*>(a.x);
+  const T* dy = static_cast<const T*>(a.dy);
+  float dw[K * V], db[K * V];
+#pragma unroll
+  for (int i = 0; i < K * V; ++i) dw[i] = db[i] = 0.0f;
+  Pack<T, V> cx[K], cd[K], nx[K], nd[K];
+  float mean = 0.0f, rstd = 0.0f, n_mean = 0.0f, n_rstd = 0.0f;
+  auto fetch = [&](Pack<T, V>* tx, Pack<T, V>* td, float& m, float& s, int64_t at) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * TPR + r) * V;
+      tx[k] = load_pack<T, V>(x + at * a.ldx + c, a.cols - c);
+      td[k] = load_pack<T, V>(dy + at * a.lddy + c, a.cols - c);
+    }
+    m = a.center ? a.mean[at] : 0.0f;
+    s = a.rstd[at];
+  };
+  if (row < a.rows) fetch(cx, cd, mean, rstd, row);
+  for (; row < a.rows; row += step) {
+    if (row + step < a.rows) fetch(nx, nd, n_mean, n_rstd, row + step);
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * TPR + r) * V;
+      if (a.cols - c <= 0) break;
+      float w[V];
+      load_param<V>(a.weight, a.param_f32, c, a.cols - c, 1.0f, w);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {  // absent elements have dy = 0 and add nothing
+        const float d = to_f(cd[k].e[i]), h = (to_f(cx[k].e[i]) - mean) * rstd, g = d * w[i];
+        s1 += g;
+        s2 = fmaf(g, h, s2);
+        dw[k * V + i] = fmaf(d, h, dw[k * V + i]);
+        db[k * V + i] += d;
+      }
+    }
+    group_sum<TPR>(s1, s2, slot, flip, group);
+    s1 = a.center ? s1 * a.inv_cols : 0.0f;
+    s2 *= a.inv_cols;
+    T* out = static_cast<T*>(a.out) + row * a.ldo;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * TPR + r) * V, nv = a.cols - c;
+      if (nv <= 0) break;
+      float w[V];
+      load_param<V>(a.weight, a.param_f32, c, nv, 1.0f, w);
+      Pack<T, V> o;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float h = (to_f(cx[k].e[i]) - mean) * rstd;
+        from_f(o.e[i], rstd * (to_f(cd[k].e[i]) * w[i] - s1 - h * s2));
+      }
+      store_pack<T, V>(out + c, o, nv);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      cx[k] = nx[k];
+      cd[k] = nd[k];
+    }
+    mean = n_mean;
+    rstd = n_rstd;
+  }
+  if (!a.partial) return;
+  // The CTA's groups, added in order.
+  if constexpr (G > 1) {
+    for (int q = 0; q < G; ++q) {
+      if (group == q) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            float* s = s_acc + (k * V + i) * TPR + r;  // neighbouring threads, neighbouring banks
+            s[0] = dw[k * V + i] + (q ? s[0] : 0.0f);
+            s[TPR * K * V] = db[k * V + i] + (q ? s[TPR * K * V] : 0.0f);
+          }
+      }
+      __syncthreads();
+    }
+    if (group != 0) return;
+#pragma unroll
+    for (int i = 0; i < K * V; ++i) {
+      dw[i] = s_acc[i * TPR + r];
+      db[i] = s_acc[i * TPR + r + TPR * K * V];
+    }
+  }
+  float* p = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = (k * TPR + r) * V + i;
+      if (c < a.cols) {
+        p[c] = dw[k * V + i];
+        p[a.cols + c] = db[k * V + i];
+      }
+    }
+}
+
+// Wide rows: dx with one CTA a row (the row read twice) ...
+template <typename T, int V>
+__global__ void __launch_bounds__(1024) norm_backward_wide_kernel(const NormArgs a) {
+  __shared__ float2 s_sum[64];
+  pdl_launch_dependents();
+  pdl_wait();
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T* x = static_cast<const T*>(a.x) + row * a.ldx;
+    const T* dy = static_cast<const T*>(a.dy) + row * a.lddy;
+    T* out = static_cast<T*>(a.out) + row * a.ldo;
+    const float mean = a.center ? a.mean[row] : 0.0f, rstd = a.rstd[row];
+    float s1 = 0.0f, s2 = 0.0f;
+    for (int c = threadIdx.x * V; c < a.cols; c += 1024 * V) {
+      const int nv = a.cols - c;
+      const Pack<T, V> px = load_pack<T, V>(x + c, nv), pd = load_pack<T, V>(dy + c, nv);
+      float w[V];
+      load_param<V>(a.weight, a.param_f32, c, nv, 1.0f, w);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float g = to_f(pd.e[i]) * w[i];
+        s1 += g;
+        s2 = fmaf(g, (to_f(px.e[i]) - mean) * rstd, s2);
+      }
+    }
+    group_sum<1024>(s1, s2, s_sum, flip, 0);
+    s1 = a.center ? s1 * a.inv_cols : 0.0f;
+    s2 *= a.inv_cols;
+    for (int c = threadIdx.x * V; c < a.cols; c += 1024 * V) {
+      const int nv = a.cols - c;
+      const Pack<T, V> px = load_pack<T, V>(x + c, nv), pd = load_pack<T, V>(dy + c, nv);
+      float w[V];
+      load_param<V>(a.weight, a.param_f32, c, nv, 1.0f, w);
+      Pack<T, V> o;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        from_f(o.e[i], rstd * (to_f(pd.e[i]) * w[i] - s1 - (to_f(px.e[i]) - mean) * rstd * s2));
+      store_pack<T, V>(out + c, o, nv);
+    }
+  }
+}
+
+// ... and dw, db by columns: CTA (bx, by) adds rows by, by + gridDim.y, ... of
+// 256 * V columns.
+template <typename T, int V>
+__global__ void __launch_bounds__(256) norm_backward_columns_kernel(const NormArgs a) {
+  pdl_launch_dependents();
+  pdl_wait();
+  const int c = (blockIdx.x * 256 + threadIdx.x) * V, nv = a.cols - c;
+  if (nv <= 0) return;
+  float dw[V], db[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) dw[i] = db[i] = 0.0f;
+#pragma unroll 4
+  for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+    const Pack<T, V> px = load_pack<T, V>(static_cast<const T*>(a.x) + row * a.ldx + c, nv);
+    const Pack<T, V> pd = load_pack<T, V>(static_cast<const T*>(a.dy) + row * a.lddy + c, nv);
+    const float mean = a.center ? a.mean[row] : 0.0f, rstd = a.rstd[row];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      dw[i] = fmaf(to_f(pd.e[i]), (to_f(px.e[i]) - mean) * rstd, dw[i]);
+      db[i] += to_f(pd.e[i]);
+    }
+  }
+  float* p = a.partial + static_cast<int64_t>(blockIdx.y) * 2 * a.cols;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i < nv) {
+      p[c + i] = dw[i];
+      p[a.cols + c + i] = db[i];
+    }
+}
+
+mx_status norm_launched(cudaError_t e) { return cuda_status(e, "mx_layer_norm launch"); }
+
+template <typename T, int V, int TPR, int K, int BLOCK>
+mx_status forward_cfg(const NormArgs& a, int per_sm, cudaStream_t s) {
+  constexpr int G = BLOCK / TPR;
+  const int64_t grid = std::min<int64_t>((a.rows + G - 1) / G, static_cast<int64_t>(sm_count()) * per_sm);
+  return norm_launched(launch_kernel(norm_forward_kernel<T, V, TPR, K, BLOCK>, static_cast<unsigned>(grid), BLOCK, 0, s,
+                                     1, a));
+}
+
+// Threads per row and vectors per thread by the row's number of vectors (V
+// elements each).
+template <typename T, int V>
+mx_status forward_any(const NormArgs& a, cudaStream_t s) {
+  const int64_t n = (a.cols + V - 1) / V;
+  if (n <= 32) return forward_cfg<T, V, 32, 1, 256>(a, 8, s);
+  if (n <= 64) return forward_cfg<T, V, 32, 2, 256>(a, 8, s);
+  if (n <= 128) return forward_cfg<T, V, 32, 4, 256>(a, 8, s);
+  if (n <= 256) return forward_cfg<T, V, 32, 8, 256>(a, 4, s);
+  if (n <= 512) return forward_cfg<T, V, 128, 4, 256>(a, 4, s);
+  if (n <= 1024) return forward_cfg<T, V, 256, 4, 256>(a, 4, s);
+  if (n <= 2048) return forward_cfg<T, V, 512, 4, 512>(a, 2, s);
+  if (n <= 4096) return forward_cfg<T, V, 1024, 4, 1024>(a, 1, s);
+  const int64_t grid = std::min<int64_t>(a.rows, 2 * static_cast<int64_t>(sm_count()));
+  return norm_launched(launch_kernel(norm_forward_wide_kernel<T, V>, static_cast<unsigned>(grid), 1024, 0, s, 1, a));
+}
+
+template <typename T, int V, int TPR, int K, int BLOCK>
+mx_status backward_cfg(const NormArgs& a, int* parts, cudaStream_t s) {
+  constexpr int G = BLOCK / TPR;
+  const int64_t grid = std::min<int64_t>((a.rows + G - 1) / G,
+                                         std::min<int64_t>(kMaxPartials, static_cast<int64_t>(sm_count()) * (BLOCK == 1024 ? 1 : 2)));
+  *parts = static_cast<int>(grid);
+  return norm_launched(launch_kernel(norm_backward_kernel<T, V, TPR, K, BLOCK>, static_cast<unsigned>(grid), BLOCK, 0,
+                                     s, 1, a));
+}
+
+template <typename T, int V>
+mx_status backward_any(const NormArgs& a, int* parts, cudaStream_t s) {
+  const int64_t n = (a.cols + V - 1) / V;
+  if (n <= 32) return backward_cfg<T, V, 32, 1, 512>(a, parts, s);
+  if (n <= 64) return backward_cfg<T, V, 32, 2, 512>(a, parts, s);
+  if (n <= 128) return backward_cfg<T, V, 128, 1, 512>(a, parts, s);
+  if (n <= 256) return backward_cfg<T, V, 256, 1, 512>(a, parts, s);
+  if (n <= 512) return backward_cfg<T, V, 256, 2, 512>(a, parts, s);
+  if (n <= 1024) return backward_cfg<T, V, 512, 2, 512>(a, parts, s);
+  if (n <= 2048) return backward_cfg<T, V, 1024, 2, 1024>(a, parts, s);
+  if (a.partial) {
+    const int bx = static_cast<int>((n + 255) / 256);
+    const int by = static_cast<int>(std::min<int64_t>(a.rows, std::max(1, std::min(kMaxPartials, 4 * sm_count() / bx))));
+    *parts = by;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(bx, by);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1] = {};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = pdl_enabled() ? 1 : 0;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const mx_status st = norm_launched(cudaLaunchKernelEx(&cfg, norm_backward_columns_kernel<T, V>, a));
+    if (st != MX_OK) return st;
+  }
+  const int64_t grid = std::min<int64_t>(a.rows, 2 * static_cast<int64_t>(sm_count()));
+  return norm_launched(launch_kernel(norm_backward_wide_kernel<T, V>, static_cast<unsigned>(grid), 1024, 0, s, 1, a));
+}
+
+bool vec_ok(const void* p, int64_t ld, int elem) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * elem % 16 == 0;
+}
+
+NormArgs norm_args(const NormLaunch& L) {
+  NormArgs a;
+  a.x = L.x;
+  a.dy = L.dy;
+  a.weight = L.weight;
+  a.bias = L.bias;
+  a.out = L.out;
+  a.mean = L.mean;
+  a.rstd = L.rstd;
+  a.partial = nullptr;
+  a.rows = L.rows;
+  a.ldx = L.ldx;
+  a.lddy = L.lddy;
+  a.ldo = L.ldo;
+  a.cols = static_cast<int32_t>(L.cols);
+  a.param_f32 = L.param_dtype == MX_F32;
+  a.center = L.center;
+  a.eps = L.eps;
+  a.inv_cols = static_cast<float>(1.0 / static_cast<double>(L.cols));
+  return a;
+}
+
+// 16-byte vectors where every row of every matrix and the parameters start on
+// a 16-byte boundary, else element by element.
+bool wide_access(const NormLaunch& L) {
+  const int e = L.dtype == MX_F32 ? 4 : 2;
+  return vec_ok(L.x, L.ldx, e) && vec_ok(L.out, L.ldo, e) && (!L.dy || vec_ok(L.dy, L.lddy, e)) &&
+         vec_ok(L.weight, 0, 4) && vec_ok(L.bias, 0, 4);
+}
+
+}  // namespace
+
+mx_status launch_norm_forward(const NormLaunch& L, cudaStream_t s) {
+  const NormArgs a = norm_args(L);
+  const bool vec = wide_access(L);
+  if (L.dtype == MX_F32) return vec ? forward_any<float, 4>(a, s) : forward_any<float, 1>(a, s);
+  return vec ? forward_any<__nv_bfloat16, 8>(a, s) : forward_any<__nv_bfloat16, 1>(a, s);
+}
+
+mx_status launch_norm_backward(const NormLaunch& L, cudaStream_t s) {
+  NormArgs a = norm_args(L);
+  const bool vec = wide_access(L);
+  const bool want = L.dweight || L.dbias;
+  a.partial = want ? static_cast<float*>(L.ws) : nullptr;
+  int parts = 0;
+  mx_status st;
+  if (L.dtype == MX_F32) st = vec ? backward_any<float, 4>(a, &parts, s) : backward_any<float, 1>(a, &parts, s);
+  else st = vec ? backward_any<__nv_bfloat16, 8>(a, &parts, s) : backward_any<__nv_bfloat16, 1>(a, &parts, s);
+  if (st != MX_OK || !want) return st;
+  return launch_column_reduce(a.partial, parts, L.cols, L.cols, L.dweight, L.dbias, s);
+}
+
+size_t norm_backward_workspace(int64_t rows, int64_t cols) {
+  return static_cast<size_t>(std::min<int64_t>(rows, kMaxPartials)) * 2 * static_cast<size_t>(cols) * sizeof(float);
+}
+
+// ---------------------------------------------------------------------------
+// Sum of partial rows
+// ---------------------------------------------------------------------------
+
+namespace {
+
+// out[c] = sum over p of partial[p][c], c over the n0 + n1 columns of a partial
+// row (the first n0 go to out0, the others to out1; null: not wanted). A CTA
+// takes 32 columns; thread row y adds the partial rows y, y + 32, ... and the
+// 32 sums of a column are added in order: a fixed order whatever the grid.
+__global__ void __launch_bounds__(1024) column_reduce_kernel(const float* partial, int parts, int64_t n0, int64_t n1,
+                                                             float* out0, float* out1) {
+  __shared__ float s[32][33];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + tx, n = n0 + n1;
+  float v = 0.0f;
+  if (c < n) {
+#pragma unroll 4
+    for (int p = ty; p < parts; p += 32) v += partial[static_cast<int64_t>(p) * n + c];
+  }
+  s[ty][tx] = v;
+  __syncthreads();
+  // warp ty sums column ty of the tile across its lanes
+  v = warp_sum(s[tx][ty]);
+  const int64_t oc = static_cast<int64_t>(blockIdx.x) * 32 + ty;
+  if (tx == 0 && oc < n) {
+    float* out = oc < n0 ? out0 : out1;
+    if (out) out[oc < n0 ? oc : oc - n0] = v;
+  }
+}
+
+}  // namespace
+
+mx_status launch_column_reduce(const float* partial, int parts, int64_t n0, int64_t n1, float* out0, float* out1,
+                               cudaStream_t s) {
+  return cuda_status(launch_kernel(column_reduce_kernel, static_cast<unsigned>((n0 + n1 + 31) / 32), 1024, 0, s, 1,
+                                   partial, parts, n0, n1, out0, out1),
+                     "partial sums launch");
+}
+
+}  // namespace mx

@@ -1,4 +1,5 @@
-"""CPU oracle of the operators around the products of a training step: AdamW.
+"""CPU oracle of the operators around the products of a training step: AdamW,
+layer norm.
 
 Test infrastructure only, plain float64 numpy written from the definitions in
 include/mxfp8.h; it shares no code with the CUDA path.
@@ -50,3 +51,28 @@ def block_scale(scale, n) -> np.ndarray:
 def block_amax(x) -> np.ndarray:
     x = np.abs(np.asarray(x, dtype=np.float64))
     return np.array([x[i:i + STATE_BLOCK].max() for i in range(0, len(x), STATE_BLOCK)])
+
+
+# ---------------------------------------------------------------------------
+# Layer norm and root-mean-square norm
+# ---------------------------------------------------------------------------
+
+def norm_stats(x, eps, center=True):
+    mean = x.mean(1) if center else np.zeros(len(x))
+    return mean, 1.0 / np.sqrt(((x - mean[:, None]) ** 2).mean(1) + eps)
+
+
+def norm(x, w, b, eps, center=True):
+    """(y, mean, rstd)."""
+    mean, rstd = norm_stats(x, eps, center)
+    return (x - mean[:, None]) * rstd[:, None] * w + b, mean, rstd
+
+
+def norm_backward(dy, x, w, mean, rstd, center=True):
+    """(dx, dw, db) from the row statistics."""
+    h = (x - mean[:, None]) * rstd[:, None] if center else x * rstd[:, None]
+    g = dy * w
+    dx = g - h * (g * h).mean(1, keepdims=True)
+    if center:
+        dx = dx - g.mean(1, keepdims=True)
+    return dx * rstd[:, None], (dy * h).sum(0), dy.sum(0)

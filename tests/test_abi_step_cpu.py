@@ -59,3 +59,41 @@ def test_adamw_refusals(L):
     assert status_of(mx.mx_adamw_step, None, 1, 32, h, None, None, None) == INVALID
     assert status_of(mx.mx_adamw_step, t, 1, 32, None, None, None, None) == INVALID
     assert status_of(mx.mx_adamw_step, t, 1, 32, h, 0x7002, None, None) == ALIGN
+
+
+def norm(**kw):
+    d = dict(x=0x1000, ldx=64, weight=0x2000, bias=0x3000, param_dtype=mx.MX_F32, rows=4, cols=64, eps=1e-5, center=1,
+             dtype=mx.MX_BF16, y=0x4000, ldy=64, mean=0x5000, rstd=0x6000, dev_status=None, stream=None)
+    d.update(kw)
+    return status_of(mx.mx_layer_norm, *d.values())
+
+
+def norm_backward(**kw):
+    d = dict(dy=0x1000, lddy=64, x=0x2000, ldx=64, weight=0x3000, param_dtype=mx.MX_F32, mean=0x4000, rstd=0x5000, rows=4,
+             cols=64, center=1, dtype=mx.MX_BF16, dx=0x6000, lddx=64, dweight=0x7000, dbias=0x8000, workspace=0x9000,
+             workspace_bytes=1 << 20, dev_status=None, stream=None)
+    d.update(kw)
+    return status_of(mx.mx_layer_norm_backward, *d.values())
+
+
+def test_norm_refusals(L):
+    assert norm(rows=0) == 0
+    for bad in (dict(rows=-1), dict(cols=0), dict(dtype=2), dict(param_dtype=-1), dict(center=2), dict(eps=-1.0),
+                dict(eps=float("nan")), dict(x=0), dict(y=0), dict(ldx=63), dict(ldy=63)):
+        assert norm(**bad) == INVALID, bad
+    assert norm(cols=1 << 31, ldx=1 << 31, ldy=1 << 31) == SHAPE
+    for bad in (dict(x=0x1001), dict(y=0x4001), dict(weight=0x2002), dict(bias=0x3001), dict(mean=0x5002), dict(rstd=0x6001),
+                dict(x=0x1002, dtype=mx.MX_F32)):
+        assert norm(**bad) == ALIGN, bad
+
+
+def test_norm_backward_refusals(L):
+    assert norm_backward(rows=0, dweight=None, dbias=None) == 0
+    for bad in (dict(rows=-1), dict(cols=0), dict(dtype=2), dict(center=-1), dict(dy=0), dict(x=0), dict(dx=0), dict(mean=None),
+                dict(rstd=None), dict(lddy=63), dict(lddx=63), dict(workspace=None), dict(workspace_bytes=100)):
+        assert norm_backward(**bad) == INVALID, bad
+    for bad in (dict(dx=0x6001), dict(workspace=0x9008), dict(dweight=0x7002), dict(rstd=0x5001)):
+        assert norm_backward(**bad) == ALIGN, bad
+    assert mx.mx_layer_norm_backward_workspace_bytes(4, 64) == 4 * 2 * 64 * 4
+    assert mx.mx_layer_norm_backward_workspace_bytes(1 << 20, 64) == 304 * 2 * 64 * 4
+    assert mx.mx_layer_norm_backward_workspace_bytes(0, 64) == 0
