@@ -626,6 +626,56 @@ mx_status mx_layer_norm_backward(const void* dy, int64_t lddy, const void* x, in
                                  int center, int dtype, void* dx, int64_t lddx, float* dweight, float* dbias,
                                  void* workspace, size_t workspace_bytes, int* dev_status, void* stream);
 
+/*
+ * mx_gemm_epilogue - mx_gemm with bias, activation and residual applied to the
+ * FP32 accumulators:
+ *   z = A . B^T + bias,  C = act(z) + residual
+ * rounded to BF16 once (and z once, where it is kept).
+ *
+ *   epilogue   host pointer (read before the call returns):
+ *     bias        N entries of bias_dtype, added to every row; NULL: none.
+ *     residual    BF16 [M, N], pitch ld_residual; NULL: none. May be C itself
+ *                 (same pointer and pitch): C = act(z) + C.
+ *     preact      BF16 [M, N], pitch ld_preact: receives z for
+ *                 mx_epilogue_backward; NULL: not kept. Overlaps nothing.
+ *     act         mx_act. GELU is the tanh form, 0.5 z (1 + tanh(sqrt(2/pi)
+ *                 (z + 0.044715 z^3))); SILU is z / (1 + exp(-z)). RELU passes
+ *                 NaN on.
+ *   Everything else as mx_gemm (any mode; whole tiles, no split tail). K = 0
+ *   takes the product as zero.
+ */
+typedef enum mx_act { MX_ACT_NONE = 0, MX_ACT_RELU = 1, MX_ACT_GELU = 2, MX_ACT_SILU = 3 } mx_act;
+typedef struct mx_epilogue {
+  const void* bias;
+  const void* residual;
+  void* preact;
+  int64_t ld_residual;
+  int64_t ld_preact;
+  int32_t bias_dtype; /* mx_dtype */
+  int32_t act;        /* mx_act */
+} mx_epilogue;
+mx_status mx_gemm_epilogue(int mode, const mx_operand* a, const mx_operand* b, const mx_epilogue* epilogue, void* c,
+                           int64_t ldc, int* dev_status, void* stream);
+
+/*
+ * mx_epilogue_backward - the gradient of that epilogue:
+ *   dz = dy * act'(z)                (BF16; the dY that dgrad and wgrad quantise)
+ *   dbias[n] = sum over rows of dy * act'(z), in FP32 before dz's rounding
+ * (RELU's slope at 0 is 0; the residual's gradient is dy itself).
+ *
+ *   dy, preact, dz   BF16 [rows, cols] with pitches lddy, ld_preact, lddz.
+ *              preact is unused with MX_ACT_NONE; dz may be NULL (not wanted)
+ *              and may not overlap the inputs.
+ *   dbias      FP32 [cols], written; NULL: not wanted. rows = 0 writes zeros.
+ *   workspace  scratch of mx_epilogue_backward_workspace_bytes(rows, cols),
+ *              16-byte aligned; may be NULL if that is 0 or dbias is NULL.
+ * Sums are added in a fixed order: same inputs, same bits.
+ */
+size_t mx_epilogue_backward_workspace_bytes(int64_t rows, int64_t cols);
+mx_status mx_epilogue_backward(const void* dy, int64_t lddy, const void* preact, int64_t ld_preact, int64_t rows,
+                               int64_t cols, int act, void* dz, int64_t lddz, float* dbias, void* workspace,
+                               size_t workspace_bytes, int* dev_status, void* stream);
+
 /* Static description of a status code. */
 const char* mx_status_string(mx_status s);
 

@@ -30,6 +30,8 @@ MX_MAX_GEMM_MULTI = 4
 MX_MAX_GROUPS = 512
 MX_BF16, MX_F32 = 0, 1
 MX_ADAMW_STATE_BLOCK = 256
+MX_ACT_NONE, MX_ACT_RELU, MX_ACT_GELU, MX_ACT_SILU = 0, 1, 2, 3
+ACTIVATIONS = {"none": MX_ACT_NONE, "relu": MX_ACT_RELU, "gelu": MX_ACT_GELU, "silu": MX_ACT_SILU}
 STATUS_NAMES = {0: "MX_OK", 1: "MX_ERR_INVALID_ARG", 2: "MX_ERR_UNSUPPORTED_SHAPE", 3: "MX_ERR_ALIGNMENT",
                 4: "MX_ERR_CUDA", 5: "MX_ERR_DEVICE_CHECK", 6: "MX_ERR_TIMEOUT", 7: "MX_ERR_NO_DEVICE"}
 
@@ -41,7 +43,8 @@ EXPORTED = ("mx_scale_bytes", "mx_grouped_padded_rows", "mx_quantize", "mx_quant
             "mx_selftest_wait_timeout", "mx_gemm_workspace_bytes", "mx_gemm_with_workspace", "mx_gemm_multi",
             "mx_gemm_static_workspace", "mx_current_amax", "mx_quantize_current", "mx_gemm_current",
             "mx_grouped_gemm_current", "mx_gemm_current_multi", "mx_grouped_gemm_swiglu_quantize", "mx_adamw_step",
-            "mx_layer_norm", "mx_layer_norm_backward_workspace_bytes", "mx_layer_norm_backward")
+            "mx_layer_norm", "mx_layer_norm_backward_workspace_bytes", "mx_layer_norm_backward",
+            "mx_gemm_epilogue", "mx_epilogue_backward_workspace_bytes", "mx_epilogue_backward")
 MX_STATIC_WORKSPACE_BYTES = 40 * 1024 * 1024
 
 
@@ -66,6 +69,12 @@ class MXQuantTensorC(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("ldx", ctypes.c_int64),
                 ("row_data", ctypes.c_void_p), ("row_scale", ctypes.c_void_p), ("col_data", ctypes.c_void_p),
                 ("col_scale", ctypes.c_void_p)]
+
+
+class MXEpilogueC(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("preact", ctypes.c_void_p),
+                ("ld_residual", ctypes.c_int64), ("ld_preact", ctypes.c_int64), ("bias_dtype", ctypes.c_int32),
+                ("act", ctypes.c_int32)]
 
 
 class MXAdamWTensorC(ctypes.Structure):
@@ -152,6 +161,13 @@ def lib() -> ctypes.CDLL:
     L.mx_layer_norm_backward.argtypes = [vp, i64, vp, i64, vp, i32, vp, vp, i64, i64, i32, i32, vp, i64, vp, vp, vp,
                                          ctypes.c_size_t, vp, vp]
     L.mx_layer_norm_backward.restype = i32
+    L.mx_gemm_epilogue.argtypes = [i32, ctypes.POINTER(MXOperandC), ctypes.POINTER(MXOperandC),
+                                   ctypes.POINTER(MXEpilogueC), vp, i64, vp, vp]
+    L.mx_gemm_epilogue.restype = i32
+    L.mx_epilogue_backward_workspace_bytes.argtypes = [i64, i64]
+    L.mx_epilogue_backward_workspace_bytes.restype = ctypes.c_size_t
+    L.mx_epilogue_backward.argtypes = [vp, i64, vp, i64, i64, i64, i32, vp, i64, vp, vp, ctypes.c_size_t, vp, vp]
+    L.mx_epilogue_backward.restype = i32
     L.mx_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp, vp]
     L.mx_selftest_wait_timeout.restype = i32
     L.mx_status_string.argtypes = [i32]
@@ -331,6 +347,21 @@ def mx_layer_norm_backward(dy, lddy, x, ldx, weight, param_dtype, mean, rstd, ro
     _check(lib().mx_layer_norm_backward(dy, lddy, x, ldx, weight, param_dtype, mean, rstd, rows, cols, center, dtype,
                                         dx, lddx, dweight, dbias, workspace, workspace_bytes, dev_status, stream),
            "mx_layer_norm_backward")
+
+
+def mx_gemm_epilogue(mode, a: MXOperandC, b: MXOperandC, epilogue: MXEpilogueC, c, ldc, dev_status, stream) -> None:
+    _check(lib().mx_gemm_epilogue(mode, _ref(a), _ref(b), _ref(epilogue), c, ldc, dev_status, stream),
+           "mx_gemm_epilogue")
+
+
+def mx_epilogue_backward_workspace_bytes(rows, cols) -> int:
+    return int(lib().mx_epilogue_backward_workspace_bytes(rows, cols))
+
+
+def mx_epilogue_backward(dy, lddy, preact, ld_preact, rows, cols, act, dz, lddz, dbias, workspace, workspace_bytes,
+                         dev_status, stream) -> None:
+    _check(lib().mx_epilogue_backward(dy, lddy, preact, ld_preact, rows, cols, act, dz, lddz, dbias, workspace,
+                                      workspace_bytes, dev_status, stream), "mx_epilogue_backward")
 
 
 # ---------------------------------------------------------------------------
@@ -844,3 +875,51 @@ def layer_norm_backward(dy, x, weight, mean, rstd, center: bool = True, param_gr
                            _ptr(mean) if center else None, rstd.data_ptr(), R, C, int(center), _dtype(x), dx.data_ptr(),
                            C, _ptr(dw), _ptr(db), _ptr(ws), need, _ptr(status), _stream(stream))
     return dx, dw, db
+
+
+def gemm_epilogue(mode: int, a: MXTensor, b: MXTensor, bias=None, act: str = "none", residual=None,
+                  keep_preact: bool = False, out=None, preact=None, status=None, stream=None):
+    """out = act(A . B^T + bias) + residual in BF16, from the FP32 accumulators.
+    bias: [N] FP32 or BF16; residual: BF16 [M, N] (may be ``out``); act: one of
+    ACTIVATIONS. Returns (out, z): z the BF16 pre-activation for
+    epilogue_backward with keep_preact (or a ``preact`` tensor to fill), else None."""
+    torch = _torch()
+    M, N = a.rows, b.rows
+    dev = a.data.device
+    bf16 = torch.bfloat16
+    if out is None:
+        out = torch.empty((M, N), dtype=bf16, device=dev)
+    if preact is None and keep_preact:
+        preact = torch.empty((M, N), dtype=bf16, device=dev)
+    for t in (out, residual, preact):
+        assert t is None or (t.dtype == bf16 and t.shape == (M, N)), "out, residual and preact: BF16 [M, N]"
+    bd = MX_F32
+    if bias is not None:
+        assert bias.is_cuda and bias.is_contiguous() and bias.numel() == N, "bias: contiguous, one entry per column"
+        bd = _dtype(bias)
+    e = MXEpilogueC(_ptr(bias), _ptr(residual), _ptr(preact), 0 if residual is None else _rows(residual),
+                    0 if preact is None else _rows(preact), bd, ACTIVATIONS[act])
+    mx_gemm_epilogue(mode, a.c_operand(), b.c_operand(), e, out.data_ptr(), _rows(out), _ptr(status), _stream(stream))
+    return out, preact
+
+
+def epilogue_backward(dy, preact, act: str = "none", bias_grad: bool = True, dz=None, status=None, stream=None):
+    """Gradient of gemm_epilogue's epilogue: (dz BF16 [M, N], dbias FP32 [N] or
+    None). preact: gemm_epilogue's z (unused, may be None, with act "none")."""
+    torch = _torch()
+    assert dy.dtype == torch.bfloat16
+    M, N = dy.shape
+    a = ACTIVATIONS[act]
+    assert a == MX_ACT_NONE or (preact.dtype == torch.bfloat16 and preact.shape == dy.shape), "preact: BF16, of dy's shape"
+    if dz is None:
+        dz = torch.empty((M, N), dtype=torch.bfloat16, device=dy.device)
+    assert dz.dtype == torch.bfloat16 and dz.shape == dy.shape
+    dbias = ws = None
+    need = 0
+    if bias_grad:
+        dbias = torch.empty(N, dtype=torch.float32, device=dy.device)
+        need = mx_epilogue_backward_workspace_bytes(M, N)
+        ws = torch.empty(need, dtype=torch.uint8, device=dy.device) if need else None
+    mx_epilogue_backward(dy.data_ptr(), _rows(dy), _ptr(preact), 0 if preact is None else _rows(preact), M, N, a,
+                         dz.data_ptr(), _rows(dz), _ptr(dbias), _ptr(ws), need, _ptr(status), _stream(stream))
+    return dz, dbias

@@ -537,6 +537,47 @@ mx_status mx_gemm(int mode, const mx_operand* a, const mx_operand* b, void* c, i
   return dense_gemm_run(L, stream);
 }
 
+mx_status mx_gemm_epilogue(int mode, const mx_operand* a, const mx_operand* b, const mx_epilogue* epilogue, void* c,
+                           int64_t ldc, int* dev_status, void* stream) {
+  GemmLaunch L;
+  mx_status st = dense_gemm_setup("mx_gemm_epilogue", mode, a, b, c, ldc, dev_status, true, &L);
+  if (st != MX_OK) return st;
+  if (!epilogue) {
+    set_error("mx_gemm_epilogue: null epilogue");
+    return MX_ERR_INVALID_ARG;
+  }
+  const mx_epilogue& e = *epilogue;
+  if (e.act < MX_ACT_NONE || e.act > MX_ACT_SILU || (e.bias_dtype != MX_BF16 && e.bias_dtype != MX_F32)) {
+    set_error("mx_gemm_epilogue: unknown act %d or bias_dtype %d", e.act, e.bias_dtype);
+    return MX_ERR_INVALID_ARG;
+  }
+  if ((e.residual && e.ld_residual < L.N) || (e.preact && e.ld_preact < L.N)) {
+    set_error("mx_gemm_epilogue: ld_residual or ld_preact < N");
+    return MX_ERR_INVALID_ARG;
+  }
+  const uintptr_t odd = (reinterpret_cast<uintptr_t>(e.residual) | reinterpret_cast<uintptr_t>(e.preact)) & 1u;
+  const uintptr_t bias_odd = reinterpret_cast<uintptr_t>(e.bias) & (e.bias_dtype == MX_F32 ? 3u : 1u);
+  if (odd || bias_odd) {
+    set_error("mx_gemm_epilogue: bias, residual or preact is not aligned to its element type");
+    return MX_ERR_ALIGNMENT;
+  }
+  L.has_epi = true;
+  L.epi.bias = e.bias;
+  L.epi.residual = e.residual;
+  L.epi.preact = e.preact;
+  L.epi.ld_residual = e.ld_residual;
+  L.epi.ld_preact = e.ld_preact;
+  L.epi.bias_f32 = e.bias_dtype == MX_F32;
+  L.epi.bias_vec = aligned16(e.bias);
+  L.epi.act = e.act;
+  if (L.M == 0 || L.N == 0) return MX_OK;
+  st = check_device();
+  if (st != MX_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (L.K == 0) return launch_epilogue_only(L.epi, L.M, L.N, L.c, L.ldc, s);
+  return launch_gemm(L, s);
+}
+
 mx_status mx_gemm_workspace_bytes(int mode, const mx_operand* a, const mx_operand* b, size_t* bytes) {
   if (!bytes) {
     set_error("mx_gemm_workspace_bytes: bytes is null");

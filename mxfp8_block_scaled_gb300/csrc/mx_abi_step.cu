@@ -212,4 +212,50 @@ mx_status mx_layer_norm_backward(const void* dy, int64_t lddy, const void* x, in
   return launch_norm_backward(L, s);
 }
 
+size_t mx_epilogue_backward_workspace_bytes(int64_t rows, int64_t cols) {
+  return rows <= 0 || cols <= 0 ? 0 : epilogue_backward_workspace(rows, cols);
+}
+
+mx_status mx_epilogue_backward(const void* dy, int64_t lddy, const void* preact, int64_t ld_preact, int64_t rows,
+                               int64_t cols, int act, void* dz, int64_t lddz, float* dbias, void* workspace,
+                               size_t workspace_bytes, int* dev_status, void* stream) {
+  const char* fn = "mx_epilogue_backward";
+  (void)dev_status;
+  if (rows < 0 || cols < 0 || act < MX_ACT_NONE || act > MX_ACT_SILU) {
+    set_error("mx_epilogue_backward: negative size or unknown act %d", act);
+    return MX_ERR_INVALID_ARG;
+  }
+  if (rows > 0x7FFFFFFFLL || cols > 0x7FFFFFFFLL) {
+    set_error("mx_epilogue_backward: sizes must be < 2^31");
+    return MX_ERR_UNSUPPORTED_SHAPE;
+  }
+  MX_CHECK(check_aligned(fn, "dbias", dbias, 4));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (cols == 0 || (!dz && !dbias)) return MX_OK;
+  if (rows == 0) {
+    if (!dbias) return MX_OK;
+    MX_CHECK(check_device());
+    return cuda_status(cudaMemsetAsync(dbias, 0, static_cast<size_t>(cols) * 4, s), "cudaMemsetAsync");
+  }
+  MX_CHECK(check_matrix(fn, "dy", dy, lddy, cols, 2));
+  if (act != MX_ACT_NONE) MX_CHECK(check_matrix(fn, "preact", preact, ld_preact, cols, 2));
+  if (dz) MX_CHECK(check_matrix(fn, "dz", dz, lddz, cols, 2));
+  const size_t need = epilogue_backward_workspace(rows, cols);
+  if (dbias && need > 0) MX_CHECK(check_workspace(fn, workspace, workspace_bytes, need));
+  MX_CHECK(check_device());
+  EpilogueBackwardLaunch L = {};
+  L.dy = dy;
+  L.lddy = lddy;
+  L.z = preact;
+  L.ldz = ld_preact;
+  L.rows = rows;
+  L.cols = cols;
+  L.act = act;
+  L.dz = dz;
+  L.lddz = lddz;
+  L.dbias = dbias;
+  L.ws = workspace;
+  return launch_epilogue_backward(L, s);
+}
+
 }  // extern "C"

@@ -70,6 +70,7 @@
 #include <utility>
 #include <vector>
 
+#include "mx_act.cuh"
 #include "mx_codec.cuh"
 #include "mx_internal.h"
 #include "mx_ptx.cuh"
@@ -615,10 +616,24 @@ __device__ __forceinline__ void swiglu_quant_row_padding(const GParams& p, const
     *reinterpret_cast<uint32_t*>(q.row_scale + scale_offset(p.M + epi_thread, ti.n0 >> 5, (p.n_out + 127) / 128)) = 0u;
 }
 
+// Where a tile's BF16 output goes: element (m0, n0) of the tile, row pitch,
+// columns, and which stores its alignment allows (GParams' c_vec and c_tma).
+struct OutView {
+  __nv_bfloat16* cbase;
+  int64_t ldc;
+  int64_t n_out;
+  int32_t c_vec;
+  int32_t c_tma;
+};
+
+__device__ __forceinline__ OutView out_view(const GParams& p, const Tile& ti) {
+  return OutView{ti.cbase, p.ldc, p.n_out, p.c_vec, p.c_tma};
+}
+
 // Epilogue of one warp: its 32 rows (TMEM lane quarter) x my_chunks 32-column
 // chunks starting at col_off, already in registers r[] (FP32 bit patterns).
 template <int KIND, int kCols, int kBufs = 1>
-__device__ __forceinline__ void store_tile(const GParams& p, const Tile& ti, const uint32_t* r, int quarter,
+__device__ __forceinline__ void store_tile(const OutView& p, const Tile& ti, const uint32_t* r, int quarter,
                                            int lane, int my_chunks, int col_off, uint8_t* stg,
                                            const CUtensorMap* tmap_c) {
   const int row = quarter * 32 + lane;
@@ -650,7 +665,7 @@ __device__ __forceinline__ void store_tile(const GParams& p, const Tile& ti, con
         const int64_t tcol = col_off + ch * 32 + cc * 8;
         const int64_t ncol = p.n_out - (ti.n0 + tcol);
         if (trow < ti.valid_m && ncol > 0) {
-          __nv_bfloat16* dst = ti.cbase + static_cast<int64_t>(trow) * p.ldc + tcol;
+          __nv_bfloat16* dst = p.cbase + static_cast<int64_t>(trow) * p.ldc + tcol;
           if (ncol >= 8) {
             *reinterpret_cast<uint4*>(dst) = v;
           } else {
@@ -701,7 +716,7 @@ __device__ __forceinline__ void store_tile(const GParams& p, const Tile& ti, con
   } else if (row < ti.valid_m) {
     const int64_t col0 = ti.n0 + col_off;
     const int64_t ncols = min64(my_chunks * 32, p.n_out - col0);
-    __nv_bfloat16* dst = ti.cbase + static_cast<int64_t>(row) * p.ldc + col_off;
+    __nv_bfloat16* dst = p.cbase + static_cast<int64_t>(row) * p.ldc + col_off;
     if (ncols == my_chunks * 32 && p.c_vec) {
 #pragma unroll
       for (int j = 0; j < kCols; j += 8) {
@@ -721,14 +736,159 @@ __device__ __forceinline__ void store_tile(const GParams& p, const Tile& ti, con
   }
 }
 
+// ---------------------------------------------------------------------------
+// Bias, activation and residual (mx_gemm_epilogue): out = act(acc + bias) +
+// residual on the FP32 accumulators, rounded to BF16 once; the pre-activation
+// acc + bias is stored too where it is wanted.
+// ---------------------------------------------------------------------------
+
+struct EpiNone {};
+struct EpiArgs {
+  CUtensorMap z;   // pre-activation, as the output's map
+  GemmEpilogue e;
+  int32_t z_vec;   // as GParams' c_vec and c_tma, for the pre-activation
+  int32_t z_tma;
+  int32_t r_vec;   // 1: every residual row start is 16-byte aligned
+};
+template <bool kEpi>
+struct EpiParamT { using type = EpiNone; };
+template <>
+struct EpiParamT<true> { using type = EpiArgs; };
+
+// Asks L2 for this warp's part of the residual while the tile's MMAs run (lane
+// = row, one 128-byte line at a time).
+__device__ __forceinline__ void epi_prefetch(const GParams& p, const EpiArgs& ea, const Tile& ti, int quarter, int lane,
+                                             int cols, int col_off) {
+  const GemmEpilogue& e = ea.e;
+  const int row = quarter * 32 + lane;
+  if (!e.residual || row >= ti.valid_m) return;
+  const int64_t col0 = ti.n0 + col_off, end = min64(col0 + cols, p.N);
+  const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(e.residual) + (ti.m0 + row) * e.ld_residual;
+  for (int64_t c = col0; c < end; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + c));
+}
+
+template <int kAct, int kCols>
+__device__ __forceinline__ void epi_activate(uint32_t* r) {
+#pragma unroll
+  for (int j = 0; j < kCols; ++j) r[j] = __float_as_uint(act_value<kAct>(__uint_as_float(r[j])));
+}
+
+// r: kCols FP32 accumulators of row quarter * 32 + lane from column n0 +
+// col_off. The residual is read through the warp's staging box, four rows of
+// the 32 x 32 box per 8 lanes (whole 64-byte pieces of its rows), one box ahead
+// of the additions.
+template <int kCols, int kBufs>
+__device__ __forceinline__ void epi_tile(const GParams& p, const EpiArgs& ea, const Tile& ti, uint32_t* r, int quarter,
+                                         int lane, int my_chunks, int col_off, uint8_t* stg,
+                                         const CUtensorMap* tmap_c) {
+  const GemmEpilogue& e = ea.e;
+  const int64_t col0 = ti.n0 + col_off;
+  if (e.bias) {
+    // The same columns for every lane: broadcast loads.
+#pragma unroll
+    for (int j = 0; j < kCols; j += 4) {
+      const int64_t c = col0 + j;
+      float4 b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (e.bias_vec && c + 4 <= p.N) {
+        if (e.bias_f32) {
+          b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(e.bias) + c));
+        } else {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(e.bias) + c));
+          b = make_float4(lo_f(w.x), hi_f(w.x), lo_f(w.y), hi_f(w.y));
+        }
+      } else {
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[i] = c + i >= p.N ? 0.0f
+                 : e.bias_f32 ? __ldg(static_cast<const float*>(e.bias) + c + i)
+                              : __bfloat162float(static_cast<const __nv_bfloat16*>(e.bias)[c + i]);
+        b = make_float4(v[0], v[1], v[2], v[3]);
+      }
+      r[j + 0] = __float_as_uint(__uint_as_float(r[j + 0]) + b.x);
+      r[j + 1] = __float_as_uint(__uint_as_float(r[j + 1]) + b.y);
+      r[j + 2] = __float_as_uint(__uint_as_float(r[j + 2]) + b.z);
+      r[j + 3] = __float_as_uint(__uint_as_float(r[j + 3]) + b.w);
+    }
+  }
+  if (e.preact) {
+    const OutView z{static_cast<__nv_bfloat16*>(e.preact) + ti.m0 * e.ld_preact + ti.n0, e.ld_preact, p.N, ea.z_vec,
+                    ea.z_tma};
+    store_tile<GEMM_DENSE, kCols, kBufs>(z, ti, r, quarter, lane, my_chunks, col_off, stg, &ea.z);
+  }
+  if (e.act == MX_ACT_RELU) epi_activate<MX_ACT_RELU, kCols>(r);
+  else if (e.act == MX_ACT_GELU) epi_activate<MX_ACT_GELU, kCols>(r);
+  else if (e.act == MX_ACT_SILU) epi_activate<MX_ACT_SILU, kCols>(r);
+  if (e.residual) {
+    const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(e.residual) + ti.m0 * e.ld_residual + col0;
+    if (ea.r_vec) {
+      const int rr0 = lane >> 2, cc = lane & 3;  // row of each eight, 16-byte piece
+      uint4 v[4];
+      auto fetch = [&](int ch) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int trow = quarter * 32 + q * 8 + rr0;
+          const int64_t c = ch * 32 + cc * 8;
+          const int64_t left = p.N - (col0 + c);
+          const __nv_bfloat16* src = res + static_cast<int64_t>(trow) * e.ld_residual + c;
+          v[q] = make_uint4(0u, 0u, 0u, 0u);
+          if (trow < ti.valid_m && left >= 8) {
+            v[q] = *reinterpret_cast<const uint4*>(src);
+          } else if (trow < ti.valid_m && left > 0) {
+            uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i < left) w[i >> 1] |= static_cast<uint32_t>(__bfloat16_as_ushort(src[i])) << (16 * (i & 1));
+            v[q] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      };
+      fetch(0);
+      if (lane == 0) bulk_wait_read_all();  // the box may still feed the pre-activation's store
+      __syncwarp();
+#pragma unroll
+      for (int ch = 0; ch < kCols / 32; ++ch) {
+        if (ch >= my_chunks) break;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int rr = q * 8 + rr0;
+          st_shared_v4(stg + rr * 64 + ((cc ^ ((rr >> 1) & 3)) << 4), v[q]);
+        }
+        if (ch + 1 < my_chunks) fetch(ch + 1);
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint4 x = ld_shared_v4(stg + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4));
+          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int j = ch * 32 + q * 8 + 2 * i;
+            r[j] = __float_as_uint(__uint_as_float(r[j]) + lo_f(w[i]));
+            r[j + 1] = __float_as_uint(__uint_as_float(r[j + 1]) + hi_f(w[i]));
+          }
+        }
+        __syncwarp();
+      }
+    } else if (quarter * 32 + lane < ti.valid_m) {
+      const __nv_bfloat16* src = res + static_cast<int64_t>(quarter * 32 + lane) * e.ld_residual;
+#pragma unroll
+      for (int j = 0; j < kCols; ++j)
+        if (j < my_chunks * 32 && col0 + j < p.N) r[j] = __float_as_uint(__uint_as_float(r[j]) + __bfloat162float(src[j]));
+    }
+  }
+  store_tile<GEMM_DENSE, kCols, kBufs>(out_view(p, ti), ti, r, quarter, lane, my_chunks, col_off, stg, tmap_c);
+}
+
 // ===========================================================================
 // Single-CTA kernel (dense and grouped)
 // ===========================================================================
 
-template <int BN, int KIND>
+template <int BN, int KIND, bool kEpi>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
-                   const __grid_constant__ CUtensorMap tmap_c, const GParams p) {
+                   const __grid_constant__ CUtensorMap tmap_c, const GParams p,
+                   const __grid_constant__ typename EpiParamT<kEpi>::type epi) {
+  static_assert(!kEpi || KIND == GEMM_DENSE, "the bias / activation / residual epilogue is the dense GEMM's");
   using C = Cfg<BN>;
   constexpr int S = C::kStages;
   constexpr int ACC = C::kAcc;
@@ -977,6 +1137,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t acc_phase = 0;
     for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x) {
       const Tile ti = get_tile<BN, KIND>(p, g, t);
+      if constexpr (kEpi) epi_prefetch(p, epi, ti, quarter, lane, my_chunks * 32, col_off);
       if (!wait_or_abort(&acc_full[acc], acc_phase, p, s_abort)) break;
       tc_fence_after_sync();
       uint32_t r[kCols];
@@ -997,7 +1158,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc = 0;
         acc_phase ^= 1;
       }
-      store_tile<KIND, kCols>(p, ti, r, quarter, lane, my_chunks, col_off, stg, &tmap_c);
+      if constexpr (kEpi) epi_tile<kCols, 1>(p, epi, ti, r, quarter, lane, my_chunks, col_off, stg, &tmap_c);
+      else store_tile<KIND, kCols>(out_view(p, ti), ti, r, quarter, lane, my_chunks, col_off, stg, &tmap_c);
     }
     // Bulk stores must have completed before the CTA's shared memory goes away.
     if (lane == 0) bulk_wait_all();
@@ -1049,9 +1211,12 @@ __device__ __forceinline__ int problem_of(const PairArgs& args, int64_t t) {
 
 // kSwiGLU_: 0 none; 1 the SwiGLU epilogue writes its BF16 output; 2 it writes
 // the output's MX copies instead.
-template <int KIND, int kSwiGLU_, bool kMulti, int BN_, bool kTS>
+// kEpi: the bias / activation / residual epilogue (one dense problem, whole tiles).
+template <int KIND, int kSwiGLU_, bool kMulti, int BN_, bool kTS, bool kEpi>
 __global__ void __launch_bounds__(kPairThreads, 1)
-    mx_gemm_pair_kernel(const __grid_constant__ PairArgs args) {
+    mx_gemm_pair_kernel(const __grid_constant__ PairArgs args,
+                        const __grid_constant__ typename EpiParamT<kEpi>::type epi) {
+  static_assert(!kEpi || (KIND == GEMM_DENSE && !kSwiGLU_ && !kMulti && !kTS), "dense, block-scaled, one problem");
   constexpr bool kSwiGLU = kSwiGLU_ != 0;
   constexpr bool kSwiQ = kSwiGLU_ == 2;
   using C = PairCfgT<BN_, kTS, KIND != GEMM_DENSE>;
@@ -1428,6 +1593,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       if (ti.part == -2) continue;
       float ts = 1.0f;  // the tile's product of tensor scales (kTS), read while the MMAs run
       if constexpr (kTS) ts = __ldg(pp.ts_a) * __ldg(pp.ts_b + (KIND == GEMM_GROUPED_M ? ti.group : 0));
+      if constexpr (kEpi) epi_prefetch(pp, epi, ti, quarter, lane, kCols, col_off);
       if (!wait_or_abort<true>(&acc_full[acc], acc_phase, p, s_abort)) break;
       tc_fence_after_sync();
       uint32_t r[kCols];
@@ -1463,7 +1629,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll
         for (int i = 0; i < kCols; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * ts);
       }
-      if constexpr (KIND == GEMM_DENSE && BN == 256 && !kTS) {
+      if constexpr (KIND == GEMM_DENSE && BN == 256 && !kTS && !kEpi) {
         if (ti.part >= 0) {
           // Split-tail segment: the FP32 partial goes to the workspace.
           float4* dst = reinterpret_cast<float4*>(pp.ws) +
@@ -1488,10 +1654,12 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           swiglu_quant_epilogue(pp, args.q, g, ti, r, quarter, half, lane, stg);
           if (crank == 0 && t < nt) swiglu_quant_row_padding(pp, args.q, ti, (warp - 2) * 32 + lane);
         } else {
-          store_tile<KIND, 64, C::kEpiBufs>(pp, ti, r, quarter, lane, 2, 64 * half, stg, &args.prob[pi].c);
+          store_tile<KIND, 64, C::kEpiBufs>(out_view(pp, ti), ti, r, quarter, lane, 2, 64 * half, stg, &args.prob[pi].c);
         }
+      } else if constexpr (kEpi) {
+        epi_tile<kCols, C::kEpiBufs>(pp, epi, ti, r, quarter, lane, kCols / 32, col_off, stg, &args.prob[pi].c);
       } else {
-        store_tile<KIND, kCols, C::kEpiBufs>(pp, ti, r, quarter, lane, kCols / 32, col_off, stg, &args.prob[pi].c);
+        store_tile<KIND, kCols, C::kEpiBufs>(out_view(pp, ti), ti, r, quarter, lane, kCols / 32, col_off, stg, &args.prob[pi].c);
       }
     }
     if (lane == 0) bulk_wait_all();
@@ -1815,7 +1983,7 @@ __global__ void __launch_bounds__(BwCfg<BN_>::kThreads, 1)
         b_s = b_next;
       }
       if (!ok) break;
-      store_tile<GEMM_DENSE, kCols>(p, ti, reinterpret_cast<const uint32_t*>(acc), quarter, lane, kCols / 32,
+      store_tile<GEMM_DENSE, kCols>(out_view(p, ti), ti, reinterpret_cast<const uint32_t*>(acc), quarter, lane, kCols / 32,
                                     col_off, stg, &tmap_c);
     }
     if (lane == 0) bulk_wait_all();
@@ -1916,7 +2084,24 @@ void output_map(const GemmLaunch& L, GParams& p, CUtensorMap* mc, int kind) {
   }
 }
 
-template <int BN, int KIND>
+// The epilogue's launch argument: the pre-activation's map where it takes TMA
+// stores (the same conditions as the output's).
+template <bool kEpi>
+mx_status epi_args(const GemmLaunch& L, typename EpiParamT<kEpi>::type* a) {
+  if constexpr (kEpi) {
+    std::memset(a, 0, sizeof(*a));
+    a->e = L.epi;
+    a->r_vec = (reinterpret_cast<uintptr_t>(L.epi.residual) & 15u) == 0 && L.epi.ld_residual % 8 == 0;
+    if (L.epi.preact) {
+      a->z_vec = (reinterpret_cast<uintptr_t>(L.epi.preact) & 15u) == 0 && L.epi.ld_preact % 8 == 0;
+      if (a->z_vec && L.N % 8 == 0 && make_out_map(&a->z, L.epi.preact, 1, L.M, L.N, L.epi.ld_preact) == MX_OK)
+        a->z_tma = 1;
+    }
+  }
+  return MX_OK;
+}
+
+template <int BN, int KIND, bool kEpi = false>
 mx_status launch_cfg(const GemmLaunch& L, const GParams& p_in, int64_t tiles_upper, cudaStream_t s) {
   GParams p = p_in;
   CUtensorMap ma, mb, mc;
@@ -1926,11 +2111,14 @@ mx_status launch_cfg(const GemmLaunch& L, const GParams& p_in, int64_t tiles_upp
   if (st != MX_OK) return st;
   output_map(L, p, &mc, KIND);
   const size_t smem = Cfg<BN>::smem_bytes(KIND != GEMM_DENSE);
-  auto kern = mx_gemm_kernel<BN, KIND>;
+  typename EpiParamT<kEpi>::type epi;
+  st = epi_args<kEpi>(L, &epi);
+  if (st != MX_OK) return st;
+  auto kern = mx_gemm_kernel<BN, KIND, kEpi>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(smem)");
   const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(tiles_upper, sm_count()));
-  return cuda_status(launch_kernel(kern, static_cast<unsigned>(grid), kThreads, smem, s, 1, ma, mb, mc, p),
+  return cuda_status(launch_kernel(kern, static_cast<unsigned>(grid), kThreads, smem, s, 1, ma, mb, mc, p, epi),
                      "mx_gemm launch");
 }
 
@@ -2005,7 +2193,7 @@ PairArgs* pair_args_scratch() {
   return &args;
 }
 
-template <int KIND, int kSwiGLU = 0, int BN = 256, bool kTS = false>
+template <int KIND, int kSwiGLU = 0, int BN = 256, bool kTS = false, bool kEpi = false>
 mx_status launch_pair(const GemmLaunch& L, const GParams& p_in, cudaStream_t s) {
   GParams p = p_in;
   CUtensorMap ma, mb, msa, msb, mc;
@@ -2029,13 +2217,16 @@ mx_status launch_pair(const GemmLaunch& L, const GParams& p_in, cudaStream_t s) 
   }
   output_map(L, p, &mc, KIND);
   const size_t smem = PairCfgT<BN, kTS, KIND != GEMM_DENSE>::smem_bytes();
-  auto kern = mx_gemm_pair_kernel<KIND, kSwiGLU, false, BN, kTS>;
+  typename EpiParamT<kEpi>::type epi;
+  st = epi_args<kEpi>(L, &epi);
+  if (st != MX_OK) return st;
+  auto kern = mx_gemm_pair_kernel<KIND, kSwiGLU, false, BN, kTS, kEpi>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(pair smem)");
   int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(pair_tiles_upper(L, BN), sm_count() / 2));
   PairPlan pl;
   if constexpr (KIND == GEMM_DENSE && BN == 256 && !kTS) {
-    pl = plan_pair_dense(L, true);
+    pl = plan_pair_dense(L, !kEpi);
     if (pl.sk_w > 0 && !split_allowed(L, pl.ws_bytes)) pl = plan_pair_dense(L, false);
     if (pl.sk_w > 0) {
       p.ws = static_cast<float*>(L.ws);
@@ -2052,7 +2243,7 @@ mx_status launch_pair(const GemmLaunch& L, const GParams& p_in, cudaStream_t s) 
   args->q = QOut{static_cast<uint8_t*>(L.q_row_data), static_cast<uint8_t*>(L.q_row_scale),
                  static_cast<uint8_t*>(L.q_col_data), static_cast<uint8_t*>(L.q_col_scale)};
   args->n = 1;
-  st = cuda_status(launch_kernel(kern, static_cast<unsigned>(2 * clusters), kPairThreads, smem, s, 2, *args),
+  st = cuda_status(launch_kernel(kern, static_cast<unsigned>(2 * clusters), kPairThreads, smem, s, 2, *args, epi),
                    "mx_gemm launch (CTA pairs)");
   if (st == MX_OK && p.sk_w > 0)
     st = cuda_status(launch_kernel(mx_gemm_sk_reduce_kernel, static_cast<unsigned>(32 * pl.tail_tiles), 256, 0, s, 1, p),
@@ -2334,8 +2525,8 @@ mx_status launch_pair_multi(const GemmLaunch* Ls_in, int n, cudaStream_t s) {
   args->tile0[n] = tiles;
   args->n = n;
   const size_t smem = ts ? PairCfgT<BN, true, false>::smem_bytes() : PairCfgT<BN, false, false>::smem_bytes();
-  auto kern = ts ? mx_gemm_pair_kernel<GEMM_DENSE, 0, true, BN, true>
-                 : mx_gemm_pair_kernel<GEMM_DENSE, 0, true, BN, false>;
+  auto kern = ts ? mx_gemm_pair_kernel<GEMM_DENSE, 0, true, BN, true, false>
+                 : mx_gemm_pair_kernel<GEMM_DENSE, 0, true, BN, false, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(pair smem)");
   const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(tiles, sm_count() / 2));
@@ -2347,7 +2538,8 @@ mx_status launch_pair_multi(const GemmLaunch* Ls_in, int n, cudaStream_t s) {
     const int64_t rr = schedule_round_robin(Ls, n, clusters);
     args->sched = (greedy > 0 && greedy * 100 < rr * 97) ? 1 : 0;
   }
-  return cuda_status(launch_kernel(kern, static_cast<unsigned>(2 * clusters), kPairThreads, smem, s, 2, *args),
+  return cuda_status(launch_kernel(kern, static_cast<unsigned>(2 * clusters), kPairThreads, smem, s, 2, *args,
+                                   EpiNone{}),
                      "mx_gemm_multi launch (CTA pairs)");
 }
 
@@ -2374,7 +2566,8 @@ mx_status launch_gemm(const GemmLaunch& L, cudaStream_t s) {
   int bn;
   if (L.kind == GEMM_DENSE) {
     const int cfg = choose_dense_cfg(L);
-    if (cfg == CFG_PAIR) return launch_pair<GEMM_DENSE>(L, p, s);
+    if (cfg == CFG_PAIR)
+      return L.has_epi ? launch_pair<GEMM_DENSE, 0, 256, false, true>(L, p, s) : launch_pair<GEMM_DENSE>(L, p, s);
     bn = cfg == CFG_BN256 ? 256 : 128;
   } else {
     if (use_pairs(L))
@@ -2389,6 +2582,9 @@ mx_status launch_gemm(const GemmLaunch& L, cudaStream_t s) {
 
   switch (L.kind) {
     case GEMM_DENSE:
+      if (L.has_epi)
+        return bn == 256 ? launch_cfg<256, GEMM_DENSE, true>(L, p, tiles_upper, s)
+                         : launch_cfg<128, GEMM_DENSE, true>(L, p, tiles_upper, s);
       return bn == 256 ? launch_cfg<256, GEMM_DENSE>(L, p, tiles_upper, s)
                        : launch_cfg<128, GEMM_DENSE>(L, p, tiles_upper, s);
     case GEMM_GROUPED_M:

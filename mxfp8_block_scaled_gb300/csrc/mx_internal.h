@@ -99,6 +99,18 @@ mx_status launch_quantize_blockwise(const void* x, int64_t rows, int64_t cols, i
 // --- GEMM ------------------------------------------------------------------
 enum GemmKind { GEMM_DENSE = 0, GEMM_GROUPED_M = 1, GEMM_GROUPED_K = 2 };
 
+// The epilogue of mx_gemm_epilogue; null pointers: not there.
+struct GemmEpilogue {
+  const void* bias;      // N entries
+  const void* residual;  // BF16 [M, N]
+  void* preact;          // BF16 [M, N], written
+  int64_t ld_residual;
+  int64_t ld_preact;
+  int32_t bias_f32;
+  int32_t bias_vec;      // the bias allows 4-element loads
+  int32_t act;           // mx_act
+};
+
 struct GemmLaunch {
   GemmKind kind;
   const void* a_data;
@@ -137,6 +149,10 @@ struct GemmLaunch {
   void* q_col_data = nullptr;
   void* q_col_scale = nullptr;
   int64_t q_cap = 0;
+  // Dense, block-scaled only: C = act(A . B^T + bias) + residual (whole tiles,
+  // no split tail).
+  bool has_epi = false;
+  GemmEpilogue epi = {};
 };
 mx_status launch_gemm(const GemmLaunch& g, cudaStream_t s);
 // Bytes of workspace the dense GEMM L would use for its split tail (0: none).
@@ -151,6 +167,24 @@ mx_status launch_gemm_multi(const GemmLaunch* Ls, int n, cudaStream_t s);
 // --- operators around the products -----------------------------------------
 mx_status launch_adamw(const mx_adamw_tensor* tensors, int n, int bits, const mx_adamw_hyper& hy,
                        const float* grad_scale, int* dev_status, cudaStream_t s);
+
+// The epilogue alone, on a product that is zero (empty contraction).
+mx_status launch_epilogue_only(const GemmEpilogue& e, int64_t M, int64_t N, void* c, int64_t ldc, cudaStream_t s);
+
+struct EpilogueBackwardLaunch {
+  const void* dy;
+  int64_t lddy;
+  const void* z;  // unused with MX_ACT_NONE
+  int64_t ldz;
+  int64_t rows, cols;
+  int act;
+  void* dz;  // may be null
+  int64_t lddz;
+  float* dbias;  // may be null
+  void* ws;
+};
+mx_status launch_epilogue_backward(const EpilogueBackwardLaunch& L, cudaStream_t s);
+size_t epilogue_backward_workspace(int64_t rows, int64_t cols);
 
 struct NormLaunch {
   const void* x;

@@ -1,5 +1,5 @@
 """CPU oracle of the operators around the products of a training step: AdamW,
-layer norm.
+layer norm, the epilogue of a product.
 
 Test infrastructure only, plain float64 numpy written from the definitions in
 include/mxfp8.h; it shares no code with the CUDA path.
@@ -76,3 +76,42 @@ def norm_backward(dy, x, w, mean, rstd, center=True):
     if center:
         dx = dx - g.mean(1, keepdims=True)
     return dx * rstd[:, None], (dy * h).sum(0), dy.sum(0)
+
+
+# ---------------------------------------------------------------------------
+# Epilogue of a product: out = act(z) + residual, z = A . B^T + bias
+# ---------------------------------------------------------------------------
+
+def act(z, name):
+    with np.errstate(over="ignore"):
+        if name == "relu":
+            return np.where(z > 0, z, 0.0)
+        if name == "gelu":
+            return 0.5 * z * (1 + np.tanh(np.sqrt(2 / np.pi) * (z + 0.044715 * z ** 3)))
+        if name == "silu":
+            return z / (1 + np.exp(-z))
+    return z
+
+
+def act_slope(z, name):
+    with np.errstate(over="ignore"):
+        if name == "relu":
+            return (z > 0).astype(np.float64)
+        if name == "gelu":
+            a = np.sqrt(2 / np.pi)
+            t = np.tanh(a * (z + 0.044715 * z ** 3))
+            return 0.5 * (1 + t) + 0.5 * z * (1 - t * t) * a * (1 + 3 * 0.044715 * z * z)
+        if name == "silu":
+            q = 1 / (1 + np.exp(-z))
+            return q + z * q * (1 - q)
+    return np.ones_like(z)
+
+
+def epilogue(z, name, residual):
+    return act(z, name) + residual
+
+
+def epilogue_backward(dy, z, name):
+    """(dz, dbias)."""
+    dz = dy * act_slope(z, name)
+    return dz, dz.sum(0)

@@ -97,3 +97,48 @@ def test_norm_backward_refusals(L):
     assert mx.mx_layer_norm_backward_workspace_bytes(4, 64) == 4 * 2 * 64 * 4
     assert mx.mx_layer_norm_backward_workspace_bytes(1 << 20, 64) == 304 * 2 * 64 * 4
     assert mx.mx_layer_norm_backward_workspace_bytes(0, 64) == 0
+
+
+def operand(data=0x10000, scale=0x20000, rows=128, k=256, ld=0, orient=mx.MX_ROWWISE):
+    return mx.MXOperandC(data, scale, rows, k, ld, orient, 0)
+
+
+def epilogue(a=None, b=None, c=0x40000, ldc=128, mode=mx.MX_FPROP, **kw):
+    d = dict(bias=0x1000, residual=0x2000, preact=0x3000, ld_residual=128, ld_preact=128, bias_dtype=mx.MX_F32,
+             act=mx.MX_ACT_GELU)
+    d.update(kw)
+    return status_of(mx.mx_gemm_epilogue, mode, a or operand(), b or operand(), mx.MXEpilogueC(**d), c, ldc, None, None)
+
+
+def test_epilogue_refusals(L):
+    assert epilogue(a=operand(rows=0)) == 0
+    for bad in (dict(act=-1), dict(act=4), dict(bias_dtype=2), dict(ld_residual=127), dict(ld_preact=127), dict(c=0),
+                dict(ldc=127), dict(mode=mx.MX_DGRAD), dict(a=operand(k=128))):
+        assert epilogue(**bad) == INVALID, bad
+    assert status_of(mx.mx_gemm_epilogue, mx.MX_FPROP, operand(), operand(), None, 0x40000, 128, None, None) == INVALID
+    assert epilogue(a=operand(k=48), b=operand(k=48)) == SHAPE
+    for bad in (dict(bias=0x1002), dict(bias=0x1001, bias_dtype=mx.MX_BF16), dict(residual=0x2001), dict(preact=0x3001),
+                dict(c=0x40001), dict(a=operand(data=0x10008))):
+        assert epilogue(**bad) == ALIGN, bad
+
+
+def epilogue_backward(**kw):
+    d = dict(dy=0x1000, lddy=512, preact=0x2000, ld_preact=512, rows=64, cols=512, act=mx.MX_ACT_SILU, dz=0x3000, lddz=512,
+             dbias=0x4000, workspace=0x5000, workspace_bytes=1 << 24, dev_status=None, stream=None)
+    d.update(kw)
+    return status_of(mx.mx_epilogue_backward, *d.values())
+
+
+def test_epilogue_backward_refusals(L):
+    assert epilogue_backward(cols=0) == 0
+    assert epilogue_backward(dz=None, dbias=None) == 0
+    assert epilogue_backward(rows=0, dbias=None) == 0
+    for bad in (dict(rows=-1), dict(cols=-1), dict(act=4), dict(dy=0), dict(preact=None), dict(lddy=511), dict(ld_preact=511),
+                dict(lddz=511), dict(workspace=None), dict(workspace_bytes=16)):
+        assert epilogue_backward(**bad) == INVALID, bad
+    assert epilogue_backward(rows=1 << 31) == SHAPE
+    for bad in (dict(dy=0x1001), dict(preact=0x2001), dict(dz=0x3001), dict(dbias=0x4002), dict(workspace=0x5008)):
+        assert epilogue_backward(**bad) == ALIGN, bad
+    assert mx.mx_epilogue_backward_workspace_bytes(8, 512) == 0          # one CTA deep: straight into dbias
+    assert mx.mx_epilogue_backward_workspace_bytes(64, 512) == 8 * 512 * 4
+    assert mx.mx_epilogue_backward_workspace_bytes(0, 512) == 0

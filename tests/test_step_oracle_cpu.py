@@ -44,3 +44,14 @@ def test_adamw_closed_forms():
     p, m, v, u = so.adamw(np.array([1.0, 1.0]), np.array([3.0, -1e-3]), np.zeros(2), np.zeros(2), 0.1, 0.9, 0.999, 0.0, 0.5, 1)
     assert np.allclose(u, [0.1, -0.1]) and np.allclose(p, 1 - 0.05 - u)
     assert np.allclose(m, [0.3, -1e-4]) and np.allclose(v, [9e-3, 1e-9])
+
+
+@pytest.mark.parametrize("name", ["none", "relu", "gelu", "silu"])
+def test_epilogue_gradient_against_differences(name):
+    r = np.random.Generator(np.random.Philox(6))
+    z, dy, b = r.standard_normal((4, 5)) * 2, r.standard_normal((4, 5)), r.standard_normal(5)
+    z = z + np.sign(z) * 0.01     # away from relu's corner
+    dz, db = so.epilogue_backward(dy, z, name)
+    loss = lambda z_, b_: float((so.epilogue(z_ + b_ - b, name, 1.0) * dy).sum())  # noqa: E731
+    assert np.allclose(dz, differences(lambda t: loss(t, b), z), atol=1e-7)
+    assert np.allclose(db, differences(lambda t: loss(z, t), b), atol=1e-7)
