@@ -676,6 +676,55 @@ mx_status mx_epilogue_backward(const void* dy, int64_t lddy, const void* preact,
                                int64_t cols, int act, void* dz, int64_t lddz, float* dbias, void* workspace,
                                size_t workspace_bytes, int* dev_status, void* stream);
 
+/*
+ * mx_router_forward - the router of the routed experts: choice, gate weights,
+ * the grouped calls' offsets and the balance loss, from logits [tokens,
+ * n_experts] (pitch ld). With p the softmax of a token's logits over the experts:
+ *   indices [tokens, top_k]  the top_k largest logits, largest first, ties to
+ *                  the lowest expert; weights their p, divided by their sum
+ *                  with normalize = 1.
+ *   counts [n_experts]  how many tokens chose each expert; group_offsets
+ *                  [n_experts + 1] its exclusive prefix sums: the offsets of
+ *                  the grouped calls for rows sorted by expert.
+ *   load [sequences, n_experts]  coef * n_experts / (top_k * S') * hits / n^2,
+ *                  hits the sequence's choices of the expert, n its valid
+ *                  tokens, S' the sequences with n > 0 (0 for the others): the
+ *                  loss's slope by each p, read by the backward pass.
+ *   loss [1]       sum of load * (sum of p over the sequence's valid tokens):
+ *                  coef * mean over sequences of sum_e f_e P_e, f_e = n_experts
+ *                  * hits / (top_k * n), P_e the mean of p.
+ *
+ *   tokens_per_seq sequences are runs of this many tokens, the last one may be
+ *                  shorter (tokens or more: one sequence).
+ *   token_mask     byte per token, 0: the token is left out (padding): its
+ *                  logits are not read, indices -1, weights 0. NULL: none is.
+ *   A logit of -inf takes its expert out for the token (p = 0, never chosen); a
+ *   token all of whose logits are -inf is left out; slots without a choice hold
+ *   index -1, weight 0. A NaN logit is never chosen and makes the token's p NaN.
+ *   dtype of logits; n_experts <= MX_MAX_GROUPS, 1 <= top_k <= n_experts.
+ *   workspace      scratch of mx_router_workspace_bytes(...), 16-byte aligned.
+ *   tokens = 0 writes zero counts, offsets and loss. Sums are added in a fixed
+ *   order: same inputs, same bits.
+ */
+size_t mx_router_workspace_bytes(int64_t tokens, int64_t tokens_per_seq, int n_experts);
+mx_status mx_router_forward(const void* logits, int64_t ld, int dtype, const uint8_t* token_mask, int64_t tokens,
+                            int64_t tokens_per_seq, int n_experts, int top_k, int normalize, float coef,
+                            int32_t* indices, float* weights, int64_t* counts, int64_t* group_offsets, float* load,
+                            float* loss, void* workspace, size_t workspace_bytes, int* dev_status, void* stream);
+
+/*
+ * mx_router_backward - dlogits (logits' dtype, pitch lddx) from the gradients of
+ * the weights and of the loss; indices and load are mx_router_forward's. The
+ * choice and the hits are constants: dlogits = p * (g - sum_e p g), g = dloss *
+ * load + the weights' gradient at the chosen experts. Tokens left out get zeros.
+ *   dweights  FP32 [tokens, top_k], or NULL for none (indices may then be NULL).
+ *   dloss     device float, or NULL for 0.
+ */
+mx_status mx_router_backward(const void* logits, int64_t ld, int dtype, const uint8_t* token_mask, int64_t tokens,
+                             int64_t tokens_per_seq, int n_experts, int top_k, int normalize, const int32_t* indices,
+                             const float* load, const float* dweights, const float* dloss, void* dlogits, int64_t lddx,
+                             int* dev_status, void* stream);
+
 /* Static description of a status code. */
 const char* mx_status_string(mx_status s);
 

@@ -44,7 +44,8 @@ EXPORTED = ("mx_scale_bytes", "mx_grouped_padded_rows", "mx_quantize", "mx_quant
             "mx_gemm_static_workspace", "mx_current_amax", "mx_quantize_current", "mx_gemm_current",
             "mx_grouped_gemm_current", "mx_gemm_current_multi", "mx_grouped_gemm_swiglu_quantize", "mx_adamw_step",
             "mx_layer_norm", "mx_layer_norm_backward_workspace_bytes", "mx_layer_norm_backward",
-            "mx_gemm_epilogue", "mx_epilogue_backward_workspace_bytes", "mx_epilogue_backward")
+            "mx_gemm_epilogue", "mx_epilogue_backward_workspace_bytes", "mx_epilogue_backward",
+            "mx_router_workspace_bytes", "mx_router_forward", "mx_router_backward")
 MX_STATIC_WORKSPACE_BYTES = 40 * 1024 * 1024
 
 
@@ -168,6 +169,13 @@ def lib() -> ctypes.CDLL:
     L.mx_epilogue_backward_workspace_bytes.restype = ctypes.c_size_t
     L.mx_epilogue_backward.argtypes = [vp, i64, vp, i64, i64, i64, i32, vp, i64, vp, vp, ctypes.c_size_t, vp, vp]
     L.mx_epilogue_backward.restype = i32
+    L.mx_router_workspace_bytes.argtypes = [i64, i64, i32]
+    L.mx_router_workspace_bytes.restype = ctypes.c_size_t
+    L.mx_router_forward.argtypes = [vp, i64, i32, vp, i64, i64, i32, i32, i32, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp,
+                                    ctypes.c_size_t, vp, vp]
+    L.mx_router_forward.restype = i32
+    L.mx_router_backward.argtypes = [vp, i64, i32, vp, i64, i64, i32, i32, i32, vp, vp, vp, vp, vp, i64, vp, vp]
+    L.mx_router_backward.restype = i32
     L.mx_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp, vp]
     L.mx_selftest_wait_timeout.restype = i32
     L.mx_status_string.argtypes = [i32]
@@ -362,6 +370,25 @@ def mx_epilogue_backward(dy, lddy, preact, ld_preact, rows, cols, act, dz, lddz,
                          dev_status, stream) -> None:
     _check(lib().mx_epilogue_backward(dy, lddy, preact, ld_preact, rows, cols, act, dz, lddz, dbias, workspace,
                                       workspace_bytes, dev_status, stream), "mx_epilogue_backward")
+
+
+def mx_router_workspace_bytes(tokens, tokens_per_seq, n_experts) -> int:
+    return int(lib().mx_router_workspace_bytes(tokens, tokens_per_seq, n_experts))
+
+
+def mx_router_forward(logits, ld, dtype, token_mask, tokens, tokens_per_seq, n_experts, top_k, normalize, coef, indices,
+                      weights, counts, group_offsets, load, loss, workspace, workspace_bytes, dev_status,
+                      stream) -> None:
+    _check(lib().mx_router_forward(logits, ld, dtype, token_mask, tokens, tokens_per_seq, n_experts, top_k, normalize,
+                                   coef, indices, weights, counts, group_offsets, load, loss, workspace,
+                                   workspace_bytes, dev_status, stream), "mx_router_forward")
+
+
+def mx_router_backward(logits, ld, dtype, token_mask, tokens, tokens_per_seq, n_experts, top_k, normalize, indices, load,
+                       dweights, dloss, dlogits, lddx, dev_status, stream) -> None:
+    _check(lib().mx_router_backward(logits, ld, dtype, token_mask, tokens, tokens_per_seq, n_experts, top_k, normalize,
+                                    indices, load, dweights, dloss, dlogits, lddx, dev_status, stream),
+           "mx_router_backward")
 
 
 # ---------------------------------------------------------------------------
@@ -923,3 +950,70 @@ def epilogue_backward(dy, preact, act: str = "none", bias_grad: bool = True, dz=
     mx_epilogue_backward(dy.data_ptr(), _rows(dy), _ptr(preact), 0 if preact is None else _rows(preact), M, N, a,
                          dz.data_ptr(), _rows(dz), _ptr(dbias), _ptr(ws), need, _ptr(status), _stream(stream))
     return dz, dbias
+
+
+@dataclass
+class Routing:
+    """What router_forward returns."""
+    indices: "object"        # int32 [T, top_k], -1: no choice
+    weights: "object"        # FP32 [T, top_k]
+    counts: "object"         # int64 [E]
+    group_offsets: "object"  # int64 [E + 1], the grouped calls' offsets
+    load: "object"           # FP32 [sequences, E], for router_backward
+    loss: "object"           # FP32 [1]
+
+
+def router_forward(logits, top_k: int, tokens_per_seq: Optional[int] = None, token_mask=None, normalize: bool = False,
+                   coef: float = 1.0, status=None, stream=None) -> Routing:
+    """Routes logits [T, E] (FP32 or BF16, any row pitch): the top_k experts of
+    each token (ties to the lowest), their softmax weights (divided by their sum
+    with normalize), the per-expert counts and group offsets, and the balance
+    loss, averaged over sequences of tokens_per_seq tokens (default: one
+    sequence). token_mask: bool or uint8 [T], false: left out."""
+    torch = _torch()
+    T, E = logits.shape
+    dev = logits.device
+    seq = max(T, 1) if tokens_per_seq is None else tokens_per_seq
+    assert seq >= 1 and 1 <= top_k <= E
+    mask = _mask(token_mask, T)
+    seqs = (T + seq - 1) // seq
+    f32 = dict(dtype=torch.float32, device=dev)
+    i64 = torch.empty(2 * E + 1, dtype=torch.int64, device=dev)
+    r = Routing(torch.empty((T, top_k), dtype=torch.int32, device=dev), torch.empty((T, top_k), **f32), i64[:E], i64[E:],
+                torch.empty((seqs, E), **f32), torch.empty(1, **f32))
+    need = mx_router_workspace_bytes(T, seq, E)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    mx_router_forward(logits.data_ptr(), _rows(logits), _dtype(logits), mask, T, seq, E, top_k, int(normalize), coef,
+                      r.indices.data_ptr(), r.weights.data_ptr(), r.counts.data_ptr(), r.group_offsets.data_ptr(),
+                      r.load.data_ptr(), r.loss.data_ptr(), ws.data_ptr(), need, _ptr(status), _stream(stream))
+    return r
+
+
+def _mask(token_mask, tokens) -> Optional[int]:
+    if token_mask is None:
+        return None
+    torch = _torch()
+    assert token_mask.dtype in (torch.bool, torch.uint8) and token_mask.is_cuda and token_mask.is_contiguous()
+    assert token_mask.numel() == tokens, "token_mask: one entry per token"
+    return token_mask.data_ptr()
+
+
+def router_backward(logits, indices, load, dweights=None, dloss=None, tokens_per_seq: Optional[int] = None,
+                    token_mask=None, normalize: bool = False, status=None, stream=None):
+    """dlogits (logits' dtype) from dweights (FP32 [T, top_k] or None) and dloss
+    (FP32 [1] on the device, or None); indices, load, tokens_per_seq, token_mask
+    and normalize as in router_forward."""
+    torch = _torch()
+    T, E = logits.shape
+    top_k = indices.shape[1]
+    seq = max(T, 1) if tokens_per_seq is None else tokens_per_seq
+    f32 = torch.float32
+    assert indices.dtype == torch.int32 and indices.is_contiguous() and indices.shape[0] == T
+    assert load.dtype == f32 and load.is_contiguous() and load.shape == ((T + seq - 1) // seq, E)
+    assert dweights is None or (dweights.dtype == f32 and dweights.is_contiguous() and dweights.shape == indices.shape)
+    assert dloss is None or (dloss.dtype == f32 and dloss.is_cuda and dloss.numel() == 1)
+    dx = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    mx_router_backward(logits.data_ptr(), _rows(logits), _dtype(logits), _mask(token_mask, T), T, seq, E, top_k,
+                       int(normalize), indices.data_ptr(), load.data_ptr(), _ptr(dweights), _ptr(dloss), dx.data_ptr(),
+                       E, _ptr(status), _stream(stream))
+    return dx

@@ -21,7 +21,7 @@ OUT_DIR = os.path.join(PKG, "_lib")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_NAME = "libmxfp8_gb300.so"
 SOURCES = ("mx_abi.cu", "mx_abi_step.cu", "mx_quant.cu", "mx_gemm.cu", "mx_optim.cu",
-           "mx_norm.cu", "mx_epilogue.cu")
+           "mx_norm.cu", "mx_epilogue.cu", "mx_router.cu")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "-Xptxas", "-v"] + ARCH
 # MXFP8_DISPATCH_OVERRIDES=1 at build time: a measurement build whose GEMM

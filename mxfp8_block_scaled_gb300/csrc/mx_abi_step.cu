@@ -81,6 +81,29 @@ mx_status check_workspace(const char* fn, const void* ws, size_t bytes, size_t n
   return check_aligned(fn, "workspace", ws, 16);
 }
 
+// What both directions of the router share; MX_OK with tokens = 0 too.
+mx_status check_router(const char* fn, int dtype, int64_t tokens, int64_t tokens_per_seq, int experts, int top_k,
+                       int normalize) {
+  if (!known_dtype(dtype) || tokens < 0 || tokens_per_seq < 1 || experts < 1 || top_k < 1 || top_k > experts ||
+      (normalize != 0 && normalize != 1)) {
+    set_error("%s: needs a known dtype, tokens >= 0, tokens_per_seq >= 1, 1 <= top_k <= experts, normalize 0 or 1", fn);
+    return MX_ERR_INVALID_ARG;
+  }
+  if (experts > MX_MAX_GROUPS || tokens > 0x7FFFFFFFLL || (tokens > 0 && !router_fits(tokens, tokens_per_seq, experts))) {
+    set_error("%s: at most %d experts and 2^31 - 1 tokens", fn, MX_MAX_GROUPS);
+    return MX_ERR_UNSUPPORTED_SHAPE;
+  }
+  return MX_OK;
+}
+
+mx_status check_present(const char* fn, const char* name, const void* p, int a) {
+  if (!p) {
+    set_error("%s: %s is null", fn, name);
+    return MX_ERR_INVALID_ARG;
+  }
+  return check_aligned(fn, name, p, a);
+}
+
 #define MX_CHECK(call)                       \
   do {                                       \
     const mx_status check_st = (call);       \
@@ -256,6 +279,93 @@ mx_status mx_epilogue_backward(const void* dy, int64_t lddy, const void* preact,
   L.dbias = dbias;
   L.ws = workspace;
   return launch_epilogue_backward(L, s);
+}
+
+size_t mx_router_workspace_bytes(int64_t tokens, int64_t tokens_per_seq, int n_experts) {
+  if (tokens <= 0 || tokens_per_seq <= 0 || n_experts <= 0) return 0;
+  return router_workspace(tokens, tokens_per_seq, n_experts);
+}
+
+mx_status mx_router_forward(const void* logits, int64_t ld, int dtype, const uint8_t* token_mask, int64_t tokens,
+                            int64_t tokens_per_seq, int n_experts, int top_k, int normalize, float coef,
+                            int32_t* indices, float* weights, int64_t* counts, int64_t* group_offsets, float* load,
+                            float* loss, void* workspace, size_t workspace_bytes, int* dev_status, void* stream) {
+  const char* fn = "mx_router_forward";
+  (void)dev_status;
+  MX_CHECK(check_router(fn, dtype, tokens, tokens_per_seq, n_experts, top_k, normalize));
+  if (!std::isfinite(coef)) {
+    set_error("mx_router_forward: coef is not finite");
+    return MX_ERR_INVALID_ARG;
+  }
+  MX_CHECK(check_present(fn, "counts", counts, 8));
+  MX_CHECK(check_present(fn, "group_offsets", group_offsets, 8));
+  MX_CHECK(check_present(fn, "loss", loss, 4));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (tokens == 0) {
+    MX_CHECK(check_device());
+    MX_CHECK(cuda_status(cudaMemsetAsync(counts, 0, static_cast<size_t>(n_experts) * 8, s), "cudaMemsetAsync"));
+    MX_CHECK(cuda_status(cudaMemsetAsync(group_offsets, 0, static_cast<size_t>(n_experts + 1) * 8, s), "cudaMemsetAsync"));
+    return cuda_status(cudaMemsetAsync(loss, 0, 4, s), "cudaMemsetAsync");
+  }
+  MX_CHECK(check_matrix(fn, "logits", logits, ld, n_experts, elem_size(dtype)));
+  MX_CHECK(check_present(fn, "indices", indices, 4));
+  MX_CHECK(check_present(fn, "weights", weights, 4));
+  MX_CHECK(check_present(fn, "load", load, 4));
+  MX_CHECK(check_workspace(fn, workspace, workspace_bytes, router_workspace(tokens, tokens_per_seq, n_experts)));
+  MX_CHECK(check_device());
+  RouterLaunch L = {};
+  L.logits = logits;
+  L.ld = ld;
+  L.dtype = dtype;
+  L.mask = token_mask;
+  L.tokens = tokens;
+  L.tokens_per_seq = tokens_per_seq;
+  L.experts = n_experts;
+  L.top_k = top_k;
+  L.normalize = normalize;
+  L.coef = coef;
+  L.indices = indices;
+  L.weights = weights;
+  L.counts = counts;
+  L.offsets = group_offsets;
+  L.load = load;
+  L.loss = loss;
+  L.ws = workspace;
+  return launch_router_forward(L, s);
+}
+
+mx_status mx_router_backward(const void* logits, int64_t ld, int dtype, const uint8_t* token_mask, int64_t tokens,
+                             int64_t tokens_per_seq, int n_experts, int top_k, int normalize, const int32_t* indices,
+                             const float* load, const float* dweights, const float* dloss, void* dlogits, int64_t lddx,
+                             int* dev_status, void* stream) {
+  const char* fn = "mx_router_backward";
+  (void)dev_status;
+  MX_CHECK(check_router(fn, dtype, tokens, tokens_per_seq, n_experts, top_k, normalize));
+  if (tokens == 0) return MX_OK;
+  MX_CHECK(check_matrix(fn, "logits", logits, ld, n_experts, elem_size(dtype)));
+  MX_CHECK(check_matrix(fn, "dlogits", dlogits, lddx, n_experts, elem_size(dtype)));
+  MX_CHECK(check_present(fn, "load", load, 4));
+  if (dweights) MX_CHECK(check_present(fn, "indices", indices, 4));
+  MX_CHECK(check_aligned(fn, "dweights", dweights, 4));
+  MX_CHECK(check_aligned(fn, "dloss", dloss, 4));
+  MX_CHECK(check_device());
+  RouterLaunch L = {};
+  L.logits = logits;
+  L.ld = ld;
+  L.dtype = dtype;
+  L.mask = token_mask;
+  L.tokens = tokens;
+  L.tokens_per_seq = tokens_per_seq;
+  L.experts = n_experts;
+  L.top_k = top_k;
+  L.normalize = normalize;
+  L.indices = const_cast<int32_t*>(indices);
+  L.load = const_cast<float*>(load);
+  L.dweights = dweights;
+  L.dloss = dloss;
+  L.dlogits = dlogits;
+  L.lddx = lddx;
+  return launch_router_backward(L, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -186,6 +186,32 @@ struct EpilogueBackwardLaunch {
 mx_status launch_epilogue_backward(const EpilogueBackwardLaunch& L, cudaStream_t s);
 size_t epilogue_backward_workspace(int64_t rows, int64_t cols);
 
+struct RouterLaunch {
+  const void* logits;
+  int64_t ld;
+  int dtype;
+  const uint8_t* mask;  // may be null
+  int64_t tokens, tokens_per_seq;
+  int experts, top_k, normalize;
+  float coef;             // forward
+  int32_t* indices;       // written (forward), read (backward)
+  float* weights;         // forward outputs ...
+  int64_t* counts;
+  int64_t* offsets;
+  float* load;            // written (forward), read (backward)
+  float* loss;
+  void* ws;
+  const float* dweights;  // backward inputs (may be null) and output
+  const float* dloss;
+  void* dlogits;
+  int64_t lddx;
+};
+mx_status launch_router_forward(const RouterLaunch& L, cudaStream_t s);
+mx_status launch_router_backward(const RouterLaunch& L, cudaStream_t s);
+size_t router_workspace(int64_t tokens, int64_t tokens_per_seq, int experts);
+// Whether the launch's CTAs can be counted.
+bool router_fits(int64_t tokens, int64_t tokens_per_seq, int experts);
+
 struct NormLaunch {
   const void* x;
   int64_t ldx;

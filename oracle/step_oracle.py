@@ -1,5 +1,5 @@
 """CPU oracle of the operators around the products of a training step: AdamW,
-layer norm, the epilogue of a product.
+layer norm, the epilogue of a product, the router.
 
 Test infrastructure only, plain float64 numpy written from the definitions in
 include/mxfp8.h; it shares no code with the CUDA path.
@@ -115,3 +115,65 @@ def epilogue_backward(dy, z, name):
     """(dz, dbias)."""
     dz = dy * act_slope(z, name)
     return dz, dz.sum(0)
+
+
+# ---------------------------------------------------------------------------
+# Router: choice, weights, counts, balance loss
+# ---------------------------------------------------------------------------
+
+def router_probs(x, mask=None):
+    """(p, valid): softmax of each row; rows left out (masked, or no logit above
+    -inf) are zero."""
+    valid = ~(x == -np.inf).all(1)
+    if mask is not None:
+        valid &= mask
+    y = np.where(valid[:, None], x, 0.0)
+    with np.errstate(invalid="ignore"):
+        m = np.fmax.reduce(y, axis=1, keepdims=True)
+        e = np.exp(y - m)
+        p = e / e.sum(1, keepdims=True)
+    return np.where(valid[:, None], p, 0.0), valid
+
+
+def router(x, top_k, seq, mask=None, normalize=False, coef=1.0):
+    """dict of indices, weights, counts, offsets, load, loss (and p, valid)."""
+    T, E = x.shape
+    p, valid = router_probs(x, mask)
+    seqs = -(-T // seq)
+    idx = np.full((T, top_k), -1)
+    w = np.zeros((T, top_k))
+    hits = np.zeros((seqs, E), dtype=np.int64)
+    for t in range(T):
+        if not valid[t]:
+            continue
+        order = sorted((e for e in range(E) if x[t, e] > -np.inf), key=lambda e: (-x[t, e], e))[:top_k]
+        idx[t, :len(order)] = order
+        w[t, :len(order)] = p[t, order]
+        if normalize:
+            w[t] /= p[t, order].sum()
+        for e in order:
+            hits[t // seq, e] += 1
+    n = np.array([valid[s * seq:(s + 1) * seq].sum() for s in range(seqs)])
+    psum = np.array([p[s * seq:(s + 1) * seq].sum(0) for s in range(seqs)]).reshape(seqs, E)
+    live = max(1, int((n > 0).sum()))
+    load = coef * E / (top_k * live) * hits / np.maximum(n, 1)[:, None] ** 2.0
+    counts = hits.sum(0)
+    return dict(indices=idx, weights=w, counts=counts, offsets=np.concatenate([[0], np.cumsum(counts)]), load=load,
+                loss=(load * psum).sum(), p=p, valid=valid, psum=psum)
+
+
+def router_backward(x, idx, load, dweights, dloss, seq, mask=None, normalize=False):
+    p, valid = router_probs(x, mask)
+    T, E = x.shape
+    g = dloss * load[np.arange(T) // seq]
+    for t in range(T):
+        if dweights is None or not valid[t]:
+            continue
+        sel = idx[t][idx[t] >= 0]
+        dw = dweights[t][idx[t] >= 0]
+        if normalize:
+            z = p[t, sel].sum()
+            dw = (dw - (dw * p[t, sel] / z).sum()) / z
+        g[t, sel] += dw
+    dx = p * (g - (p * g).sum(1, keepdims=True))
+    return np.where(valid[:, None], dx, 0.0)

@@ -142,3 +142,40 @@ def test_epilogue_backward_refusals(L):
     assert mx.mx_epilogue_backward_workspace_bytes(8, 512) == 0          # one CTA deep: straight into dbias
     assert mx.mx_epilogue_backward_workspace_bytes(64, 512) == 8 * 512 * 4
     assert mx.mx_epilogue_backward_workspace_bytes(0, 512) == 0
+
+
+def router_forward(**kw):
+    d = dict(logits=0x1000, ld=64, dtype=mx.MX_F32, token_mask=None, tokens=100, tokens_per_seq=50, n_experts=64, top_k=6,
+             normalize=0, coef=1.0, indices=0x2000, weights=0x3000, counts=0x4000, group_offsets=0x5000, load=0x6000,
+             loss=0x7000, workspace=0x8000, workspace_bytes=1 << 24, dev_status=None, stream=None)
+    d.update(kw)
+    return status_of(mx.mx_router_forward, *d.values())
+
+
+def router_backward(**kw):
+    d = dict(logits=0x1000, ld=64, dtype=mx.MX_F32, token_mask=None, tokens=100, tokens_per_seq=50, n_experts=64, top_k=6,
+             normalize=0, indices=0x2000, load=0x3000, dweights=0x4000, dloss=0x5000, dlogits=0x6000, lddx=64,
+             dev_status=None, stream=None)
+    d.update(kw)
+    return status_of(mx.mx_router_backward, *d.values())
+
+
+def test_router_refusals(L):
+    assert router_backward(tokens=0) == 0
+    common = (dict(dtype=2), dict(tokens=-1), dict(tokens_per_seq=0), dict(n_experts=0), dict(top_k=0), dict(top_k=65),
+              dict(normalize=2), dict(logits=0), dict(ld=63), dict(load=None))
+    for bad in common + (dict(coef=float("nan")), dict(indices=None), dict(weights=None), dict(counts=None),
+                         dict(group_offsets=None), dict(loss=None), dict(workspace=None), dict(workspace_bytes=64)):
+        assert router_forward(**bad) == INVALID, bad
+    for bad in common + (dict(indices=None), dict(dlogits=0), dict(lddx=63)):
+        assert router_backward(**bad) == INVALID, bad
+    for bad in (dict(n_experts=513, ld=513), dict(tokens=1 << 31)):
+        assert router_forward(**bad) == SHAPE and router_backward(**bad, lddx=513) == SHAPE, bad
+    for bad in (dict(logits=0x1002), dict(counts=0x4004), dict(group_offsets=0x5004), dict(weights=0x3002), dict(loss=0x7001),
+                dict(workspace=0x8008), dict(load=0x6002), dict(indices=0x2001)):
+        assert router_forward(**bad) == ALIGN, bad
+    for bad in (dict(dlogits=0x6002), dict(dweights=0x4001), dict(dloss=0x5002), dict(load=0x3001), dict(indices=0x2002)):
+        assert router_backward(**bad) == ALIGN, bad
+    assert mx.mx_router_workspace_bytes(0, 1, 64) == 0
+    # 4 CTAs of 32 tokens (two sequences of 50): (4 + 2) rows of 64 x 8 bytes, and the counts of valid tokens
+    assert mx.mx_router_workspace_bytes(100, 50, 64) == 6 * 64 * 8 + 16 + 16

@@ -55,3 +55,34 @@ def test_epilogue_gradient_against_differences(name):
     loss = lambda z_, b_: float((so.epilogue(z_ + b_ - b, name, 1.0) * dy).sum())  # noqa: E731
     assert np.allclose(dz, differences(lambda t: loss(t, b), z), atol=1e-7)
     assert np.allclose(db, differences(lambda t: loss(z, t), b), atol=1e-7)
+
+
+@pytest.mark.parametrize("normalize", [False, True])
+def test_router_gradient_against_differences(normalize):
+    r = np.random.Generator(np.random.Philox(7))
+    x, dw = r.standard_normal((6, 5)) * 2, r.standard_normal((6, 2))
+    x[1, 3] = -np.inf
+    mask = np.array([1, 1, 0, 1, 1, 1], dtype=bool)
+    f = so.router(x, 2, 4, mask, normalize, 0.7)
+    dx = so.router_backward(x, f["indices"], f["load"], dw, 1.3, 4, mask, normalize)
+
+    def loss(t):     # the choice and the load are constants
+        g = so.router(t, 2, 4, mask, normalize, 0.7)
+        assert (g["indices"] == f["indices"]).all()
+        return float((g["weights"] * dw).sum() + 1.3 * (f["load"] * g["psum"]).sum())
+
+    num = differences(loss, np.where(np.isinf(x), -50.0, x))
+    assert np.allclose(dx, num, atol=1e-7)
+    assert (dx[2] == 0).all() and dx[1, 3] == 0
+
+
+def test_router_balance_closed_forms():
+    # every token spread evenly, choices even: loss = coef
+    x = np.zeros((4, 4))
+    x[np.arange(4), np.arange(4)] = 1e-9
+    f = so.router(x, 1, 4, coef=0.3)
+    assert np.isclose(f["loss"], 0.3) and (f["counts"] == 1).all() and (f["offsets"] == np.arange(5)).all()
+    # all tokens to one expert with certainty: loss = coef * E
+    x = np.zeros((4, 4))
+    x[:, 2] = 100.0
+    assert np.isclose(so.router(x, 1, 2, coef=0.3)["loss"], 1.2)
