@@ -148,7 +148,6 @@ mx_status mx_layer_norm(const void* x, int64_t ldx, const void* weight, const vo
                         int64_t cols, float eps, int center, int dtype, void* y, int64_t ldy, float* mean, float* rstd,
                         int* dev_status, void* stream) {
   const char* fn = "mx_layer_norm";
-  (void)dev_status;  // nothing that only the device can check
   MX_CHECK(check_norm(fn, rows, cols, dtype, param_dtype, center));
   if (!(eps >= 0.0f) || !std::isfinite(eps)) {
     set_error("mx_layer_norm: eps must be finite and not negative");
@@ -177,6 +176,7 @@ mx_status mx_layer_norm(const void* x, int64_t ldx, const void* weight, const vo
   L.ldo = ldy;
   L.mean = mean;
   L.rstd = rstd;
+  L.dev_status = dev_status;
   return launch_norm_forward(L, static_cast<cudaStream_t>(stream));
 }
 
@@ -189,7 +189,6 @@ mx_status mx_layer_norm_backward(const void* dy, int64_t lddy, const void* x, in
                                  int center, int dtype, void* dx, int64_t lddx, float* dweight, float* dbias,
                                  void* workspace, size_t workspace_bytes, int* dev_status, void* stream) {
   const char* fn = "mx_layer_norm_backward";
-  (void)dev_status;
   MX_CHECK(check_norm(fn, rows, cols, dtype, param_dtype, center));
   MX_CHECK(check_aligned(fn, "dweight", dweight, 4));
   MX_CHECK(check_aligned(fn, "dbias", dbias, 4));
@@ -232,6 +231,7 @@ mx_status mx_layer_norm_backward(const void* dy, int64_t lddy, const void* x, in
   L.dweight = dweight;
   L.dbias = dbias;
   L.ws = workspace;
+  L.dev_status = dev_status;
   return launch_norm_backward(L, s);
 }
 

@@ -231,6 +231,7 @@ struct NormLaunch {
   float* dweight;  // backward, may be null
   float* dbias;
   void* ws;
+  int* dev_status;
 };
 mx_status launch_norm_forward(const NormLaunch& L, cudaStream_t s);
 mx_status launch_norm_backward(const NormLaunch& L, cudaStream_t s);

@@ -57,6 +57,8 @@ struct NormArgs {
   int32_t center;
   float eps;
   float inv_cols;
+  int* dev_status;
+  uint64_t timeout_ns;
 };
 
 template <typename T, int V>
@@ -123,6 +125,15 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// Keeps a row packed between two sweeps: without it the compiler carries the
+// first sweep's FP32 values along, twice the registers.
+template <typename T, int V, int K>
+__device__ __forceinline__ void keep_packed(Pack<T, V>* p) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(p);
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(K * V * sizeof(T) / 4); ++i) asm volatile("" : "+r"(w[i]));
+}
+
 // Sums of two values over the TPR threads of a group, to all of them. `slot`:
 // the group's float2 per warp, two buffers in turn (`flip`), so one barrier a
 // sum is enough: nobody writes a buffer again before all have read it, which
@@ -176,6 +187,7 @@ __global__ void __launch_bounds__(BLOCK) norm_forward_kernel(const NormArgs a) {
       group_sum<TPR>(mean, zero, slot, flip, group);
       mean *= a.inv_cols;
     }
+    keep_packed<T, V, K>(cur);
     float sq = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -195,6 +207,7 @@ __global__ void __launch_bounds__(BLOCK) norm_forward_kernel(const NormArgs a) {
       }
     }
     group_sum<TPR>(sq, zero, slot, flip, group);
+    keep_packed<T, V, K>(cur);
     const float rstd = __frsqrt_rn(fmaf(sq, a.inv_cols, a.eps));
     T* out = static_cast<T*>(a.out) + row * a.ldo;
 #pragma unroll
@@ -316,6 +329,8 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 1024 || K * V > 8 ? 1 : 2) nor
       }
     }
     group_sum<TPR>(s1, s2, slot, flip, group);
+    keep_packed<T, V, K>(cx);
+    keep_packed<T, V, K>(cd);
     s1 = a.center ? s1 * a.inv_cols : 0.0f;
     s2 *= a.inv_cols;
     T* out = static_cast<T*>(a.out) + row * a.ldo;
@@ -450,6 +465,346 @@ __global__ void __launch_bounds__(256) norm_backward_columns_kernel(const NormAr
     }
 }
 
+// ---------------------------------------------------------------------------
+// Rows through shared memory (every row a whole number of 16-byte vectors on
+// 16-byte boundaries): bulk copies fill a ring of stages per group while the
+// group works on registers, so the bytes in flight cost no registers. A group
+// is W warps; its first thread issues the copies.
+// ---------------------------------------------------------------------------
+
+// Waits for a stage; a wait that runs out records MX_ERR_TIMEOUT and lets the
+// CTA run on without further waits (its rows are then wrong, the status says so).
+__device__ __forceinline__ void stage_wait(uint64_t* bar, uint32_t parity, const NormArgs& a, volatile int32_t* gave_up) {
+  if (mbar_try_wait(bar, parity) || *gave_up) return;
+  if (mbar_wait(bar, parity, a.timeout_ns)) return;
+  *gave_up = 1;
+  if (a.dev_status) atomicExch(a.dev_status, static_cast<int>(MX_ERR_TIMEOUT));
+}
+
+// The copies that a group's first thread has issued: one phase of full[s] each.
+// After a wait that ran out it issues no more, and leave() lets the ones in
+// flight land (again with a limit) before the CTA's shared memory goes away.
+struct StageLog {
+  uint32_t used = 0, next = 0;  // per stage: ever issued; parity of the next issue
+  __device__ __forceinline__ void note(int s) {
+    used |= 1u << s;
+    next ^= 1u << s;
+  }
+  __device__ __forceinline__ void leave(uint64_t* full, int stages, const NormArgs& a, volatile int32_t* gave_up) const {
+    if (!*gave_up) return;
+    for (int s = 0; s < stages; ++s)
+      if (used >> s & 1u) mbar_wait(&full[s], (next >> s & 1u) ^ 1u, a.timeout_ns);
+  }
+};
+
+// Sums of two values over the W warps of a group, to all of its threads; `slot`
+// and `flip` as in group_sum.
+template <int W>
+__device__ __forceinline__ void warps_sum(float& a, float& b, float2* slot, int& flip, int group) {
+  a = warp_sum(a);
+  b = warp_sum(b);
+  if constexpr (W > 1) {
+    float2* buf = slot + flip * W;
+    flip ^= 1;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) buf[(threadIdx.x >> 5) % W] = make_float2(a, b);
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * W) : "memory");
+    const float2 v = buf[lane % W];
+    a = v.x;
+    b = v.y;
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) {
+      a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+      b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+    }
+  } else {
+    __syncwarp();
+  }
+}
+
+// Forward, two rows at a time: they share each read of weight and bias (which
+// come from L1, whose bandwidth they would otherwise fill) and each barrier. A
+// thread holds up to kFwdVecs vectors of each row.
+constexpr int kFwdVecs = 4;
+constexpr int kFwdStages = 2;
+template <int W>
+constexpr int kFwdBlock = W <= 8 ? 256 : 32 * W;
+
+template <typename T, int W>
+__global__ void __launch_bounds__(kFwdBlock<W>, W <= 8 ? 3 : 1) norm_forward_ring_kernel(const NormArgs a) {
+  constexpr int V = 16 / sizeof(T), K = kFwdVecs, G = kFwdBlock<W> / (32 * W), S = kFwdStages;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[G][S];
+  __shared__ float2 s_sum[G][2 * W];
+  __shared__ int32_t gave_up;
+  pdl_launch_dependents();
+  const int group = threadIdx.x / (32 * W), r = threadIdx.x % (32 * W);
+  const uint32_t row_bytes = static_cast<uint32_t>(a.cols) * sizeof(T);
+  uint8_t* stages = ring + static_cast<size_t>(group) * S * 2 * row_bytes;
+  const T* x = static_cast<const T*>(a.x);
+  const int64_t pairs = (a.rows + 1) / 2, step = static_cast<int64_t>(gridDim.x) * G;
+  if (r == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(&full[group][s], 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 0) gave_up = 0;
+  __syncthreads();
+  pdl_wait();
+  StageLog log;
+  auto issue = [&](int s, int64_t pair) {
+    if (*const_cast<volatile int32_t*>(&gave_up)) return;
+    log.note(s);
+    const bool two = 2 * pair + 1 < a.rows;
+    uint8_t* to = stages + static_cast<size_t>(s) * 2 * row_bytes;
+    mbar_arrive_expect_tx(&full[group][s], two ? 2 * row_bytes : row_bytes);
+    bulk_load(to, x + 2 * pair * a.ldx, row_bytes, &full[group][s]);
+    if (two) bulk_load(to + row_bytes, x + (2 * pair + 1) * a.ldx, row_bytes, &full[group][s]);
+  };
+  int64_t pair = static_cast<int64_t>(blockIdx.x) * G + group;
+  if (r == 0)
+    for (int s = 0; s < S; ++s)
+      if (pair + s * step < pairs) issue(s, pair + s * step);
+  int s = 0, flip = 0;
+  uint32_t parity = 0;
+  const int n = a.cols / V;
+  for (; pair < pairs; pair += step) {
+    stage_wait(&full[group][s], parity, a, &gave_up);
+    const bool two = 2 * pair + 1 < a.rows;
+    const uint8_t* from = stages + static_cast<size_t>(s) * 2 * row_bytes;
+    Pack<T, V> p[2][K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int v = k * 32 * W + r;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        if (v < n && (q == 0 || two)) {
+          p[q][k] = *reinterpret_cast<const Pack<T, V>*>(from + q * row_bytes + v * 16);
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i) from_f(p[q][k].e[i], 0.0f);
+        }
+      }
+    }
+    float mean[2] = {0.0f, 0.0f}, sq[2] = {0.0f, 0.0f};
+    if (a.center) {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          mean[0] += to_f(p[0][k].e[i]);
+          mean[1] += to_f(p[1][k].e[i]);
+        }
+      warps_sum<W>(mean[0], mean[1], s_sum[group], flip, group);
+      mean[0] *= a.inv_cols;
+      mean[1] *= a.inv_cols;
+      keep_packed<T, V, K>(p[0]);
+      keep_packed<T, V, K>(p[1]);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+      if (k * 32 * W + r < n) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const float d0 = to_f(p[0][k].e[i]) - mean[0], d1 = to_f(p[1][k].e[i]) - mean[1];
+          sq[0] = fmaf(d0, d0, sq[0]);
+          sq[1] = fmaf(d1, d1, sq[1]);
+        }
+      }
+    warps_sum<W>(sq[0], sq[1], s_sum[group], flip, group);
+    keep_packed<T, V, K>(p[0]);
+    keep_packed<T, V, K>(p[1]);
+    // Every thread of the group has its vectors in registers: the stage is free.
+    if (r == 0 && pair + S * step < pairs) issue(s, pair + S * step);
+    if (++s == S) {
+      s = 0;
+      parity ^= 1;
+    }
+    const float rstd[2] = {__frsqrt_rn(fmaf(sq[0], a.inv_cols, a.eps)), __frsqrt_rn(fmaf(sq[1], a.inv_cols, a.eps))};
+    T* out = static_cast<T*>(a.out) + 2 * pair * a.ldo;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * 32 * W + r) * V;
+      if (c >= a.cols) break;
+      Pack<T, V> o[2];
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        float w[4], b[4];
+        asm volatile("" ::: "memory");  // four parameters at a time: hoisted, they would fill the registers
+        load_param<4>(a.weight, a.param_f32, c + j, 4, 1.0f, w);
+        load_param<4>(a.bias, a.param_f32, c + j, 4, 0.0f, b);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          from_f(o[0].e[j + i], fmaf((to_f(p[0][k].e[j + i]) - mean[0]) * rstd[0], w[i], b[i]));
+          from_f(o[1].e[j + i], fmaf((to_f(p[1][k].e[j + i]) - mean[1]) * rstd[1], w[i], b[i]));
+        }
+      }
+      *reinterpret_cast<Pack<T, V>*>(out + c) = o[0];
+      if (two) *reinterpret_cast<Pack<T, V>*>(out + a.ldo + c) = o[1];
+    }
+    if (r < (two ? 2 : 1)) {
+      if (a.mean && a.center) a.mean[2 * pair + r] = r ? mean[1] : mean[0];
+      if (a.rstd) a.rstd[2 * pair + r] = r ? rstd[1] : rstd[0];
+    }
+  }
+  if (r == 0) log.leave(full[group], S, a, &gave_up);
+}
+
+// Backward: a stage is a row of x and one of dy; S of them in flight. The stage
+// of the row before is refilled after a row's barrier, which every thread
+// reaches only once it has done with that row.
+template <int W>
+constexpr int kBwdBlock = W <= 16 ? 512 : 32 * W;
+
+template <typename T, int W, int K>
+__global__ void __launch_bounds__(kBwdBlock<W>, W <= 16 ? 2 : 1) norm_backward_ring_kernel(const NormArgs a, const int S) {
+  constexpr int V = 16 / sizeof(T), G = kBwdBlock<W> / (32 * W), kMaxS = 8;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[G][kMaxS];
+  __shared__ float2 s_sum[G][2 * W];
+  __shared__ int32_t gave_up;
+  pdl_launch_dependents();
+  const int group = threadIdx.x / (32 * W), r = threadIdx.x % (32 * W);
+  const uint32_t row_bytes = static_cast<uint32_t>(a.cols) * sizeof(T);
+  uint8_t* stages = ring + static_cast<size_t>(group) * S * 2 * row_bytes;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+  if (r == 0) {
+    for (int s = 0; s < S; ++s) mbar_init(&full[group][s], 1);
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 0) gave_up = 0;
+  __syncthreads();
+  pdl_wait();
+  StageLog log;
+  auto issue = [&](int s, int64_t row) {
+    if (*const_cast<volatile int32_t*>(&gave_up)) return;
+    log.note(s);
+    uint8_t* to = stages + static_cast<size_t>(s) * 2 * row_bytes;
+    mbar_arrive_expect_tx(&full[group][s], 2 * row_bytes);
+    bulk_load(to, static_cast<const T*>(a.x) + row * a.ldx, row_bytes, &full[group][s]);
+    bulk_load(to + row_bytes, static_cast<const T*>(a.dy) + row * a.lddy, row_bytes, &full[group][s]);
+  };
+  int64_t row = static_cast<int64_t>(blockIdx.x) * G + group;
+  if (r == 0)
+    for (int s = 0; s < S; ++s)
+      if (row + s * step < a.rows) issue(s, row + s * step);
+  float dw[K * V], db[K * V];
+#pragma unroll
+  for (int i = 0; i < K * V; ++i) dw[i] = db[i] = 0.0f;
+  float w1[K == 1 ? V : 1];  // one vector a thread: its weights stay in registers
+  if constexpr (K == 1) load_param<V>(a.weight, a.param_f32, r * V, a.cols - r * V, 1.0f, w1);
+  int s = 0, flip = 0;
+  uint32_t parity = 0;
+  float mean = 0.0f, rstd = 0.0f;
+  if (row < a.rows) {
+    mean = a.center ? a.mean[row] : 0.0f;
+    rstd = a.rstd[row];
+  }
+  for (bool first = true; row < a.rows; row += step, first = false) {
+    stage_wait(&full[group][s], parity, a, &gave_up);
+    float n_mean = 0.0f, n_rstd = 0.0f;
+    if (row + step < a.rows) {
+      n_mean = a.center ? a.mean[row + step] : 0.0f;
+      n_rstd = a.rstd[row + step];
+    }
+    const uint8_t* from = stages + static_cast<size_t>(s) * 2 * row_bytes;
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * 32 * W + r) * V;
+      if (c >= a.cols) break;
+      const Pack<T, V> px = *reinterpret_cast<const Pack<T, V>*>(from + c * sizeof(T));
+      const Pack<T, V> pd = *reinterpret_cast<const Pack<T, V>*>(from + row_bytes + c * sizeof(T));
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        float w[4];
+        if constexpr (K > 1) {
+          asm volatile("" ::: "memory");
+          load_param<4>(a.weight, a.param_f32, c + j, 4, 1.0f, w);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float d = to_f(pd.e[j + i]), h = (to_f(px.e[j + i]) - mean) * rstd, g = d * (K == 1 ? w1[j + i] : w[i]);
+          s1 += g;
+          s2 = fmaf(g, h, s2);
+          dw[k * V + j + i] = fmaf(d, h, dw[k * V + j + i]);
+          db[k * V + j + i] += d;
+        }
+      }
+    }
+    warps_sum<W>(s1, s2, s_sum[group], flip, group);
+    if (r == 0 && !first && row + (S - 1) * step < a.rows) issue(s == 0 ? S - 1 : s - 1, row + (S - 1) * step);
+    s1 = a.center ? s1 * a.inv_cols : 0.0f;
+    s2 *= a.inv_cols;
+    T* out = static_cast<T*>(a.out) + row * a.ldo;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int c = (k * 32 * W + r) * V;
+      if (c >= a.cols) break;
+      const Pack<T, V> px = *reinterpret_cast<const Pack<T, V>*>(from + c * sizeof(T));
+      const Pack<T, V> pd = *reinterpret_cast<const Pack<T, V>*>(from + row_bytes + c * sizeof(T));
+      Pack<T, V> o;
+#pragma unroll
+      for (int j = 0; j < V; j += 4) {
+        float w[4];
+        if constexpr (K > 1) {
+          asm volatile("" ::: "memory");
+          load_param<4>(a.weight, a.param_f32, c + j, 4, 1.0f, w);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float h = (to_f(px.e[j + i]) - mean) * rstd;
+          from_f(o.e[j + i], rstd * (to_f(pd.e[j + i]) * (K == 1 ? w1[j + i] : w[i]) - s1 - h * s2));
+        }
+      }
+      *reinterpret_cast<Pack<T, V>*>(out + c) = o;
+    }
+    mean = n_mean;
+    rstd = n_rstd;
+    if (++s == S) {
+      s = 0;
+      parity ^= 1;
+    }
+  }
+  if (r == 0) log.leave(full[group], S, a, &gave_up);
+  if (!a.partial) return;
+  float* p = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+  if constexpr (G > 1) {
+    // The CTA's groups, added in order, in the ring (no copy is in flight).
+    float* acc = reinterpret_cast<float*>(ring);
+    constexpr int N = 32 * W * K * V;
+    __syncthreads();
+    for (int q = 0; q < G; ++q) {
+      if (group == q) {
+#pragma unroll
+        for (int i = 0; i < K * V; ++i) {
+          float* t = acc + i * 32 * W + r;
+          if ((i / V * 32 * W + r) * V < a.cols) {
+            t[0] = dw[i] + (q ? t[0] : 0.0f);
+            t[N] = db[i] + (q ? t[N] : 0.0f);
+            if (q == G - 1) {
+              dw[i] = t[0];
+              db[i] = t[N];
+            }
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (group != G - 1) return;
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int c = (k * 32 * W + r) * V;
+    if (c >= a.cols) break;
+#pragma unroll
+    for (int j = 0; j < V; j += 4) {
+      *reinterpret_cast<float4*>(p + c + j) = make_float4(dw[k * V + j], dw[k * V + j + 1], dw[k * V + j + 2], dw[k * V + j + 3]);
+      *reinterpret_cast<float4*>(p + a.cols + c + j) =
+          make_float4(db[k * V + j], db[k * V + j + 1], db[k * V + j + 2], db[k * V + j + 3]);
+    }
+  }
+}
+
 mx_status norm_launched(cudaError_t e) { return cuda_status(e, "mx_layer_norm launch"); }
 
 template <typename T, int V, int TPR, int K, int BLOCK>
@@ -475,6 +830,45 @@ mx_status forward_any(const NormArgs& a, cudaStream_t s) {
   if (n <= 4096) return forward_cfg<T, V, 1024, 4, 1024>(a, 1, s);
   const int64_t grid = std::min<int64_t>(a.rows, 2 * static_cast<int64_t>(sm_count()));
   return norm_launched(launch_kernel(norm_forward_wide_kernel<T, V>, static_cast<unsigned>(grid), 1024, 0, s, 1, a));
+}
+
+template <typename T, int W>
+mx_status forward_ring(const NormArgs& a, cudaStream_t s) {
+  constexpr int G = kFwdBlock<W> / (32 * W);
+  const size_t smem = static_cast<size_t>(G) * kFwdStages * 2 * a.cols * sizeof(T);
+  auto kern = norm_forward_ring_kernel<T, W>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(norm smem)");
+  const int64_t grid = std::min<int64_t>(((a.rows + 1) / 2 + G - 1) / G, static_cast<int64_t>(sm_count()) * (W <= 8 ? 3 : 1));
+  return norm_launched(launch_kernel(kern, static_cast<unsigned>(grid), kFwdBlock<W>, smem, s, 1, a));
+}
+
+template <typename T>
+mx_status forward_rows(const NormArgs& a, cudaStream_t s) {
+  constexpr int V = 16 / sizeof(T);
+  const int64_t n = a.cols / V;
+  if (a.cols % V == 0 && n > 32) {
+    if (n <= 128) return forward_ring<T, 1>(a, s);
+    if (n <= 256) return forward_ring<T, 2>(a, s);
+    if (n <= 512) return forward_ring<T, 4>(a, s);
+    if (n <= 1024) return forward_ring<T, 8>(a, s);
+    if (n <= 2048) return forward_ring<T, 16>(a, s);
+  }
+  return forward_any<T, V>(a, s);
+}
+
+template <typename T, int W, int K>
+mx_status backward_ring(const NormArgs& a, int* parts, cudaStream_t s) {
+  constexpr int G = kBwdBlock<W> / (32 * W);
+  const size_t stage = static_cast<size_t>(G) * 2 * a.cols * sizeof(T);
+  const int S = static_cast<int>(std::min<size_t>(4, (W <= 16 ? 110592 : 204800) / stage));
+  auto kern = norm_backward_ring_kernel<T, W, K>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S * stage));
+  if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(norm smem)");
+  const int64_t grid = std::min<int64_t>((a.rows + G - 1) / G,
+                                         std::min<int64_t>(kMaxPartials, static_cast<int64_t>(sm_count()) * (W <= 16 ? 2 : 1)));
+  *parts = static_cast<int>(grid);
+  return norm_launched(launch_kernel(kern, static_cast<unsigned>(grid), kBwdBlock<W>, S * stage, s, 1, a, S));
 }
 
 template <typename T, int V, int TPR, int K, int BLOCK>
@@ -517,6 +911,20 @@ mx_status backward_any(const NormArgs& a, int* parts, cudaStream_t s) {
   return norm_launched(launch_kernel(norm_backward_wide_kernel<T, V>, static_cast<unsigned>(grid), 1024, 0, s, 1, a));
 }
 
+template <typename T>
+mx_status backward_rows(const NormArgs& a, int* parts, cudaStream_t s) {
+  constexpr int V = 16 / sizeof(T);
+  const int64_t n = a.cols / V;
+  if (a.cols % V == 0 && n > 64) {
+    if (n <= 128) return backward_ring<T, 4, 1>(a, parts, s);
+    if (n <= 256) return backward_ring<T, 8, 1>(a, parts, s);
+    if (n <= 512) return backward_ring<T, 16, 1>(a, parts, s);
+    if (n <= 1024) return backward_ring<T, 16, 2>(a, parts, s);
+    if (n <= 2048) return backward_ring<T, 32, 2>(a, parts, s);
+  }
+  return backward_any<T, V>(a, parts, s);
+}
+
 bool vec_ok(const void* p, int64_t ld, int elem) {
   return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld * elem % 16 == 0;
 }
@@ -540,6 +948,8 @@ NormArgs norm_args(const NormLaunch& L) {
   a.center = L.center;
   a.eps = L.eps;
   a.inv_cols = static_cast<float>(1.0 / static_cast<double>(L.cols));
+  a.dev_status = L.dev_status;
+  a.timeout_ns = wait_timeout_ns();
   return a;
 }
 
@@ -556,8 +966,8 @@ bool wide_access(const NormLaunch& L) {
 mx_status launch_norm_forward(const NormLaunch& L, cudaStream_t s) {
   const NormArgs a = norm_args(L);
   const bool vec = wide_access(L);
-  if (L.dtype == MX_F32) return vec ? forward_any<float, 4>(a, s) : forward_any<float, 1>(a, s);
-  return vec ? forward_any<__nv_bfloat16, 8>(a, s) : forward_any<__nv_bfloat16, 1>(a, s);
+  if (L.dtype == MX_F32) return vec ? forward_rows<float>(a, s) : forward_any<float, 1>(a, s);
+  return vec ? forward_rows<__nv_bfloat16>(a, s) : forward_any<__nv_bfloat16, 1>(a, s);
 }
 
 mx_status launch_norm_backward(const NormLaunch& L, cudaStream_t s) {
@@ -567,8 +977,8 @@ mx_status launch_norm_backward(const NormLaunch& L, cudaStream_t s) {
   a.partial = want ? static_cast<float*>(L.ws) : nullptr;
   int parts = 0;
   mx_status st;
-  if (L.dtype == MX_F32) st = vec ? backward_any<float, 4>(a, &parts, s) : backward_any<float, 1>(a, &parts, s);
-  else st = vec ? backward_any<__nv_bfloat16, 8>(a, &parts, s) : backward_any<__nv_bfloat16, 1>(a, &parts, s);
+  if (L.dtype == MX_F32) st = vec ? backward_rows<float>(a, &parts, s) : backward_any<float, 1>(a, &parts, s);
+  else st = vec ? backward_rows<__nv_bfloat16>(a, &parts, s) : backward_any<__nv_bfloat16, 1>(a, &parts, s);
   if (st != MX_OK || !want) return st;
   return launch_column_reduce(a.partial, parts, L.cols, L.cols, L.dweight, L.dbias, s);
 }
