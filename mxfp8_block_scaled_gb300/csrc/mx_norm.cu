@@ -497,30 +497,60 @@ struct StageLog {
   }
 };
 
-// Sums of two values over the W warps of a group, to all of its threads; `slot`
-// and `flip` as in group_sum.
-template <int W>
-__device__ __forceinline__ void warps_sum(float& a, float& b, float2* slot, int& flip, int group) {
-  a = warp_sum(a);
-  b = warp_sum(b);
-  if constexpr (W > 1) {
-    float2* buf = slot + flip * W;
-    flip ^= 1;
-    const int lane = threadIdx.x & 31;
-    if (lane == 0) buf[(threadIdx.x >> 5) % W] = make_float2(a, b);
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * W) : "memory");
-    const float2 v = buf[lane % W];
-    a = v.x;
-    b = v.y;
+// Sums of N values over the W warps of a group, each to all of its threads.
+// The first log2(N) shuffle steps halve the values a lane carries (one half of
+// them goes to the lanes on either side), so N sums cost N - 1 + log2(32 / N)
+// shuffles instead of 5 N. `slot`: N * W floats of the group, two buffers in
+// turn, as in group_sum.
+template <int N, int W>
+__device__ __forceinline__ void group_totals(float (&v)[N], float* slot, int& flip, int group) {
+  constexpr int L = 32 / N;  // lanes that end up with one value
+  const int lane = threadIdx.x & 31;
+  float t[N];
 #pragma unroll
-    for (int o = W / 2; o > 0; o >>= 1) {
-      a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-      b += __shfl_xor_sync(0xFFFFFFFFu, b, o);
+  for (int i = 0; i < N; ++i) t[i] = v[i];
+#pragma unroll
+  for (int n = N / 2, o = 16; n > 0; n /= 2, o /= 2) {
+    const bool upper = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float got = __shfl_xor_sync(0xFFFFFFFFu, upper ? t[i] : t[i + n], o);
+      t[i] = (upper ? t[i + n] : t[i]) + got;
     }
-  } else {
-    __syncwarp();
   }
+#pragma unroll
+  for (int o = L / 2; o > 0; o /= 2) t[0] += __shfl_xor_sync(0xFFFFFFFFu, t[0], o);
+  if constexpr (W > 1) {
+    float* buf = slot + flip * N * W + (lane / L) * W;  // W warps' sums of this lane's value
+    flip ^= 1;
+    if (lane % L == 0) buf[(threadIdx.x >> 5) % W] = t[0];
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * W) : "memory");
+    t[0] = 0.0f;
+#pragma unroll
+    for (int e = 0; e < W; e += L)
+      if (W >= L || lane % L < W) t[0] += buf[e + lane % L];
+#pragma unroll
+    for (int o = L / 2; o > 0; o /= 2) t[0] += __shfl_xor_sync(0xFFFFFFFFu, t[0], o);
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, t[0], i * L);
 }
+
+// Two neighbouring elements of a pack as FP32, for the packed FP32 instructions
+// (two results an issue slot: both ring kernels are near the issue rate).
+__device__ __forceinline__ float2 two_of(const Pack<float, 4>& p, int j) { return make_float2(p.e[2 * j], p.e[2 * j + 1]); }
+__device__ __forceinline__ float2 two_of(const Pack<__nv_bfloat16, 8>& p, int j) {
+  const uint32_t w = reinterpret_cast<const uint32_t*>(&p)[j];
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+__device__ __forceinline__ void set_two(Pack<float, 4>& p, int j, float2 v) {
+  p.e[2 * j] = v.x;
+  p.e[2 * j + 1] = v.y;
+}
+__device__ __forceinline__ void set_two(Pack<__nv_bfloat16, 8>& p, int j, float2 v) {
+  reinterpret_cast<__nv_bfloat162*>(&p)[j] = __float22bfloat162_rn(v);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // Forward, two rows at a time: they share each read of weight and bias (which
 // come from L1, whose bandwidth they would otherwise fill) and each barrier. A
@@ -535,7 +565,7 @@ __global__ void __launch_bounds__(kFwdBlock<W>, W <= 8 ? 3 : 1) norm_forward_rin
   constexpr int V = 16 / sizeof(T), K = kFwdVecs, G = kFwdBlock<W> / (32 * W), S = kFwdStages;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[G][S];
-  __shared__ float2 s_sum[G][2 * W];
+  __shared__ float s_sum[G][2 * 2 * W];
   __shared__ int32_t gave_up;
   pdl_launch_dependents();
   const int group = threadIdx.x / (32 * W), r = threadIdx.x % (32 * W);
@@ -587,30 +617,39 @@ __global__ void __launch_bounds__(kFwdBlock<W>, W <= 8 ? 3 : 1) norm_forward_rin
     }
     float mean[2] = {0.0f, 0.0f}, sq[2] = {0.0f, 0.0f};
     if (a.center) {
+      float2 t[2] = {both(0.0f), both(0.0f)};
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          mean[0] += to_f(p[0][k].e[i]);
-          mean[1] += to_f(p[1][k].e[i]);
-        }
-      warps_sum<W>(mean[0], mean[1], s_sum[group], flip, group);
+        for (int j = 0; j < V / 2; ++j)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) t[q] = __fadd2_rn(t[q], two_of(p[q][k], j));
+      mean[0] = t[0].x + t[0].y;
+      mean[1] = t[1].x + t[1].y;
+      group_totals<2, W>(mean, s_sum[group], flip, group);
       mean[0] *= a.inv_cols;
       mean[1] *= a.inv_cols;
       keep_packed<T, V, K>(p[0]);
       keep_packed<T, V, K>(p[1]);
     }
+    {
+      const float2 minus[2] = {both(-mean[0]), both(-mean[1])};
+      float2 t[2] = {both(0.0f), both(0.0f)};
 #pragma unroll
-    for (int k = 0; k < K; ++k)
-      if (k * 32 * W + r < n) {
+      for (int k = 0; k < K; ++k)
+        if (k * 32 * W + r < n) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float d0 = to_f(p[0][k].e[i]) - mean[0], d1 = to_f(p[1][k].e[i]) - mean[1];
-          sq[0] = fmaf(d0, d0, sq[0]);
-          sq[1] = fmaf(d1, d1, sq[1]);
+          for (int j = 0; j < V / 2; ++j)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const float2 d = __fadd2_rn(two_of(p[q][k], j), minus[q]);
+              t[q] = __ffma2_rn(d, d, t[q]);
+            }
         }
-      }
-    warps_sum<W>(sq[0], sq[1], s_sum[group], flip, group);
+      sq[0] = t[0].x + t[0].y;
+      sq[1] = t[1].x + t[1].y;
+    }
+    group_totals<2, W>(sq, s_sum[group], flip, group);
     keep_packed<T, V, K>(p[0]);
     keep_packed<T, V, K>(p[1]);
     // Every thread of the group has its vectors in registers: the stage is free.
@@ -633,10 +672,12 @@ __global__ void __launch_bounds__(kFwdBlock<W>, W <= 8 ? 3 : 1) norm_forward_rin
         load_param<4>(a.weight, a.param_f32, c + j, 4, 1.0f, w);
         load_param<4>(a.bias, a.param_f32, c + j, 4, 0.0f, b);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          from_f(o[0].e[j + i], fmaf((to_f(p[0][k].e[j + i]) - mean[0]) * rstd[0], w[i], b[i]));
-          from_f(o[1].e[j + i], fmaf((to_f(p[1][k].e[j + i]) - mean[1]) * rstd[1], w[i], b[i]));
-        }
+        for (int i = 0; i < 4; i += 2)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const float2 h = __fmul2_rn(__fadd2_rn(two_of(p[q][k], (j + i) / 2), both(-mean[q])), both(rstd[q]));
+            set_two(o[q], (j + i) / 2, __ffma2_rn(h, make_float2(w[i], w[i + 1]), make_float2(b[i], b[i + 1])));
+          }
       }
       *reinterpret_cast<Pack<T, V>*>(out + c) = o[0];
       if (two) *reinterpret_cast<Pack<T, V>*>(out + a.ldo + c) = o[1];
@@ -649,24 +690,27 @@ __global__ void __launch_bounds__(kFwdBlock<W>, W <= 8 ? 3 : 1) norm_forward_rin
   if (r == 0) log.leave(full[group], S, a, &gave_up);
 }
 
-// Backward: a stage is a row of x and one of dy; S of them in flight. The stage
-// of the row before is refilled after a row's barrier, which every thread
-// reaches only once it has done with that row.
+// Backward, R rows at a time: a stage is R neighbouring rows of x and of dy, S
+// stages in flight. The rows share the barrier, the reductions and the loop's
+// own instructions, which for one row are more than its arithmetic. The stage
+// before is refilled after a stage's barrier, which every thread reaches only
+// once it has done with that one.
 template <int W>
-constexpr int kBwdBlock = W <= 16 ? 512 : 32 * W;
+constexpr int kBwdBlock = W <= 8 ? 256 : 32 * W;
 
-template <typename T, int W, int K>
-__global__ void __launch_bounds__(kBwdBlock<W>, W <= 16 ? 2 : 1) norm_backward_ring_kernel(const NormArgs a, const int S) {
-  constexpr int V = 16 / sizeof(T), G = kBwdBlock<W> / (32 * W), kMaxS = 8;
+template <typename T, int W, int K, int R>
+__global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ring_kernel(const NormArgs a, const int S) {
+  constexpr int V = 16 / sizeof(T), P = V / 2, G = kBwdBlock<W> / (32 * W), kMaxS = 8;
+  constexpr bool kHold = K == 1;  // one vector a thread: weights, h and g stay in registers
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[G][kMaxS];
-  __shared__ float2 s_sum[G][2 * W];
+  __shared__ float s_sum[G][2 * 2 * R * W];
   __shared__ int32_t gave_up;
   pdl_launch_dependents();
   const int group = threadIdx.x / (32 * W), r = threadIdx.x % (32 * W);
   const uint32_t row_bytes = static_cast<uint32_t>(a.cols) * sizeof(T);
-  uint8_t* stages = ring + static_cast<size_t>(group) * S * 2 * row_bytes;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
+  uint8_t* stages = ring + static_cast<size_t>(group) * S * 2 * R * row_bytes;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * G * R;
   if (r == 0) {
     for (int s = 0; s < S; ++s) mbar_init(&full[group][s], 1);
     fence_mbar_init();
@@ -678,88 +722,127 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 16 ? 2 : 1) norm_backward_r
   auto issue = [&](int s, int64_t row) {
     if (*const_cast<volatile int32_t*>(&gave_up)) return;
     log.note(s);
-    uint8_t* to = stages + static_cast<size_t>(s) * 2 * row_bytes;
-    mbar_arrive_expect_tx(&full[group][s], 2 * row_bytes);
-    bulk_load(to, static_cast<const T*>(a.x) + row * a.ldx, row_bytes, &full[group][s]);
-    bulk_load(to + row_bytes, static_cast<const T*>(a.dy) + row * a.lddy, row_bytes, &full[group][s]);
+    const int n = static_cast<int>(min64(R, a.rows - row));
+    uint8_t* to = stages + static_cast<size_t>(s) * 2 * R * row_bytes;
+    mbar_arrive_expect_tx(&full[group][s], 2 * n * row_bytes);
+    for (int q = 0; q < n; ++q) {
+      bulk_load(to + q * row_bytes, static_cast<const T*>(a.x) + (row + q) * a.ldx, row_bytes, &full[group][s]);
+      bulk_load(to + (R + q) * row_bytes, static_cast<const T*>(a.dy) + (row + q) * a.lddy, row_bytes, &full[group][s]);
+    }
   };
-  int64_t row = static_cast<int64_t>(blockIdx.x) * G + group;
+  int64_t row = (static_cast<int64_t>(blockIdx.x) * G + group) * R;
   if (r == 0)
     for (int s = 0; s < S; ++s)
       if (row + s * step < a.rows) issue(s, row + s * step);
-  float dw[K * V], db[K * V];
+  float2 dw[K * P], db[K * P];
 #pragma unroll
-  for (int i = 0; i < K * V; ++i) dw[i] = db[i] = 0.0f;
-  float w1[K == 1 ? V : 1];  // one vector a thread: its weights stay in registers
-  if constexpr (K == 1) load_param<V>(a.weight, a.param_f32, r * V, a.cols - r * V, 1.0f, w1);
+  for (int i = 0; i < K * P; ++i) dw[i] = db[i] = both(0.0f);
+  float2 w1[kHold ? P : 1];
+  if constexpr (kHold) {
+    float w[V];
+    load_param<V>(a.weight, a.param_f32, r * V, a.cols - r * V, 1.0f, w);
+#pragma unroll
+    for (int j = 0; j < P; ++j) w1[j] = make_float2(w[2 * j], w[2 * j + 1]);
+  }
+  float mean[R], rstd[R];
+  auto statistics = [&](int64_t at) {
+#pragma unroll
+    for (int q = 0; q < R; ++q) {
+      const bool in = at + q < a.rows;
+      mean[q] = in && a.center ? a.mean[at + q] : 0.0f;
+      rstd[q] = in ? a.rstd[at + q] : 0.0f;
+    }
+  };
+  // Vector k of row q of the stage: h = (x - mean) rstd, g = dy w, d = dy.
+  auto values = [&](const uint8_t* from, int q, int c, int j, const Pack<T, V>& px, const Pack<T, V>& pd, float2 w,
+                    float2& h, float2& g, float2& d) {
+    d = two_of(pd, j);
+    g = __fmul2_rn(d, w);
+    h = __fmul2_rn(__fadd2_rn(two_of(px, j), both(-mean[q])), both(rstd[q]));
+  };
   int s = 0, flip = 0;
   uint32_t parity = 0;
-  float mean = 0.0f, rstd = 0.0f;
-  if (row < a.rows) {
-    mean = a.center ? a.mean[row] : 0.0f;
-    rstd = a.rstd[row];
-  }
   for (bool first = true; row < a.rows; row += step, first = false) {
+    statistics(row);
     stage_wait(&full[group][s], parity, a, &gave_up);
-    float n_mean = 0.0f, n_rstd = 0.0f;
-    if (row + step < a.rows) {
-      n_mean = a.center ? a.mean[row + step] : 0.0f;
-      n_rstd = a.rstd[row + step];
-    }
-    const uint8_t* from = stages + static_cast<size_t>(s) * 2 * row_bytes;
-    float s1 = 0.0f, s2 = 0.0f;
+    const int n = static_cast<int>(min64(R, a.rows - row));
+    const uint8_t* from = stages + static_cast<size_t>(s) * 2 * R * row_bytes;
+    float2 h[kHold ? R * P : 1], g[kHold ? R * P : 1];
+    float sum[2 * R];  // of g, then of g h
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * 32 * W + r) * V;
-      if (c >= a.cols) break;
-      const Pack<T, V> px = *reinterpret_cast<const Pack<T, V>*>(from + c * sizeof(T));
-      const Pack<T, V> pd = *reinterpret_cast<const Pack<T, V>*>(from + row_bytes + c * sizeof(T));
+    for (int q = 0; q < R; ++q) {
+      float2 t1 = both(0.0f), t2 = both(0.0f);
 #pragma unroll
-      for (int j = 0; j < V; j += 4) {
-        float w[4];
-        if constexpr (K > 1) {
-          asm volatile("" ::: "memory");
-          load_param<4>(a.weight, a.param_f32, c + j, 4, 1.0f, w);
+      for (int k = 0; k < K; ++k) {
+        const int c = (k * 32 * W + r) * V;
+        Pack<T, V> px, pd;
+        if (c < a.cols && q < n) {
+          px = *reinterpret_cast<const Pack<T, V>*>(from + q * row_bytes + c * sizeof(T));
+          pd = *reinterpret_cast<const Pack<T, V>*>(from + (R + q) * row_bytes + c * sizeof(T));
+        } else {  // no such row or column: dy = 0 adds nothing
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            from_f(px.e[i], 0.0f);
+            from_f(pd.e[i], 0.0f);
+          }
         }
+        float w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float d = to_f(pd.e[j + i]), h = (to_f(px.e[j + i]) - mean) * rstd, g = d * (K == 1 ? w1[j + i] : w[i]);
-          s1 += g;
-          s2 = fmaf(g, h, s2);
-          dw[k * V + j + i] = fmaf(d, h, dw[k * V + j + i]);
-          db[k * V + j + i] += d;
+        for (int j = 0; j < P; ++j) {
+          if (!kHold && j % 2 == 0) {
+            asm volatile("" ::: "memory");
+            load_param<4>(a.weight, a.param_f32, c + 2 * j, a.cols - c, 1.0f, w);
+          }
+          float2 hj, gj, d;
+          values(from, q, c, j, px, pd, kHold ? w1[kHold ? j : 0] : make_float2(w[2 * j & 3], w[(2 * j & 3) + 1]), hj, gj, d);
+          t1 = __fadd2_rn(t1, gj);
+          t2 = __ffma2_rn(gj, hj, t2);
+          dw[k * P + j] = __ffma2_rn(d, hj, dw[k * P + j]);
+          db[k * P + j] = __fadd2_rn(db[k * P + j], d);
+          if constexpr (kHold) {
+            h[q * P + j] = hj;
+            g[q * P + j] = gj;
+          }
         }
       }
+      sum[q] = t1.x + t1.y;
+      sum[R + q] = t2.x + t2.y;
     }
-    warps_sum<W>(s1, s2, s_sum[group], flip, group);
+    group_totals<2 * R, W>(sum, s_sum[group], flip, group);
     if (r == 0 && !first && row + (S - 1) * step < a.rows) issue(s == 0 ? S - 1 : s - 1, row + (S - 1) * step);
-    s1 = a.center ? s1 * a.inv_cols : 0.0f;
-    s2 *= a.inv_cols;
     T* out = static_cast<T*>(a.out) + row * a.ldo;
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * 32 * W + r) * V;
-      if (c >= a.cols) break;
-      const Pack<T, V> px = *reinterpret_cast<const Pack<T, V>*>(from + c * sizeof(T));
-      const Pack<T, V> pd = *reinterpret_cast<const Pack<T, V>*>(from + row_bytes + c * sizeof(T));
-      Pack<T, V> o;
+    for (int q = 0; q < R; ++q) {
+      if (q >= n) break;
+      // dx = rstd g - rstd sum(g)/C - rstd (sum(g h)/C) h
+      const float2 by_g = both(rstd[q]), add = both(a.center ? -rstd[q] * (sum[q] * a.inv_cols) : 0.0f),
+                   by_h = both(-rstd[q] * (sum[R + q] * a.inv_cols));
 #pragma unroll
-      for (int j = 0; j < V; j += 4) {
-        float w[4];
-        if constexpr (K > 1) {
-          asm volatile("" ::: "memory");
-          load_param<4>(a.weight, a.param_f32, c + j, 4, 1.0f, w);
-        }
+      for (int k = 0; k < K; ++k) {
+        const int c = (k * 32 * W + r) * V;
+        if (c >= a.cols) break;
+        Pack<T, V> o;
+        if constexpr (kHold) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float h = (to_f(px.e[j + i]) - mean) * rstd;
-          from_f(o.e[j + i], rstd * (to_f(pd.e[j + i]) * (K == 1 ? w1[j + i] : w[i]) - s1 - h * s2));
+          for (int j = 0; j < P; ++j) set_two(o, j, __ffma2_rn(by_h, h[q * P + j], __ffma2_rn(by_g, g[q * P + j], add)));
+        } else {
+          const Pack<T, V> px = *reinterpret_cast<const Pack<T, V>*>(from + q * row_bytes + c * sizeof(T));
+          const Pack<T, V> pd = *reinterpret_cast<const Pack<T, V>*>(from + (R + q) * row_bytes + c * sizeof(T));
+          float w[4];
+#pragma unroll
+          for (int j = 0; j < P; ++j) {
+            if (j % 2 == 0) {
+              asm volatile("" ::: "memory");
+              load_param<4>(a.weight, a.param_f32, c + 2 * j, 4, 1.0f, w);
+            }
+            float2 hj, gj, d;
+            values(from, q, c, j, px, pd, make_float2(w[2 * j & 3], w[(2 * j & 3) + 1]), hj, gj, d);
+            set_two(o, j, __ffma2_rn(by_h, hj, __ffma2_rn(by_g, gj, add)));
+          }
         }
+        *reinterpret_cast<Pack<T, V>*>(out + q * a.ldo + c) = o;
       }
-      *reinterpret_cast<Pack<T, V>*>(out + c) = o;
     }
-    mean = n_mean;
-    rstd = n_rstd;
     if (++s == S) {
       s = 0;
       parity ^= 1;
@@ -770,21 +853,21 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 16 ? 2 : 1) norm_backward_r
   float* p = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
   if constexpr (G > 1) {
     // The CTA's groups, added in order, in the ring (no copy is in flight).
-    float* acc = reinterpret_cast<float*>(ring);
-    constexpr int N = 32 * W * K * V;
+    float2* acc = reinterpret_cast<float2*>(ring);
+    constexpr int N = 32 * W * K * P;
     __syncthreads();
     for (int q = 0; q < G; ++q) {
       if (group == q) {
 #pragma unroll
-        for (int i = 0; i < K * V; ++i) {
-          float* t = acc + i * 32 * W + r;
-          if ((i / V * 32 * W + r) * V < a.cols) {
-            t[0] = dw[i] + (q ? t[0] : 0.0f);
-            t[N] = db[i] + (q ? t[N] : 0.0f);
-            if (q == G - 1) {
-              dw[i] = t[0];
-              db[i] = t[N];
+        for (int i = 0; i < K * P; ++i) {
+          if ((i / P * 32 * W + r) * V < a.cols) {
+            float2* t = acc + i * 32 * W + r;
+            if (q) {
+              dw[i] = __fadd2_rn(dw[i], t[0]);
+              db[i] = __fadd2_rn(db[i], t[N]);
             }
+            t[0] = dw[i];
+            t[N] = db[i];
           }
         }
       }
@@ -797,10 +880,10 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 16 ? 2 : 1) norm_backward_r
     const int c = (k * 32 * W + r) * V;
     if (c >= a.cols) break;
 #pragma unroll
-    for (int j = 0; j < V; j += 4) {
-      *reinterpret_cast<float4*>(p + c + j) = make_float4(dw[k * V + j], dw[k * V + j + 1], dw[k * V + j + 2], dw[k * V + j + 3]);
-      *reinterpret_cast<float4*>(p + a.cols + c + j) =
-          make_float4(db[k * V + j], db[k * V + j + 1], db[k * V + j + 2], db[k * V + j + 3]);
+    for (int j = 0; j < P; j += 2) {
+      const float2 w0 = dw[k * P + j], w1_ = dw[k * P + j + 1], b0 = db[k * P + j], b1 = db[k * P + j + 1];
+      *reinterpret_cast<float4*>(p + c + 2 * j) = make_float4(w0.x, w0.y, w1_.x, w1_.y);
+      *reinterpret_cast<float4*>(p + a.cols + c + 2 * j) = make_float4(b0.x, b0.y, b1.x, b1.y);
     }
   }
 }
@@ -857,16 +940,18 @@ mx_status forward_rows(const NormArgs& a, cudaStream_t s) {
   return forward_any<T, V>(a, s);
 }
 
-template <typename T, int W, int K>
+// R rows a stage, as many stages as the share of shared memory holds (two CTAs
+// an SM for groups of up to eight warps), four at most.
+template <typename T, int W, int K, int R>
 mx_status backward_ring(const NormArgs& a, int* parts, cudaStream_t s) {
-  constexpr int G = kBwdBlock<W> / (32 * W);
-  const size_t stage = static_cast<size_t>(G) * 2 * a.cols * sizeof(T);
-  const int S = static_cast<int>(std::min<size_t>(4, (W <= 16 ? 110592 : 204800) / stage));
-  auto kern = norm_backward_ring_kernel<T, W, K>;
+  constexpr int G = kBwdBlock<W> / (32 * W), per_sm = W <= 8 ? 2 : 1;
+  const size_t stage = static_cast<size_t>(G) * 2 * R * a.cols * sizeof(T);
+  const int S = static_cast<int>(std::min<size_t>(4, 212992 / per_sm / stage));
+  auto kern = norm_backward_ring_kernel<T, W, K, R>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S * stage));
   if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(norm smem)");
-  const int64_t grid = std::min<int64_t>((a.rows + G - 1) / G,
-                                         std::min<int64_t>(kMaxPartials, static_cast<int64_t>(sm_count()) * (W <= 16 ? 2 : 1)));
+  const int64_t grid = std::min<int64_t>((a.rows + G * R - 1) / (G * R),
+                                         std::min<int64_t>(kMaxPartials, static_cast<int64_t>(sm_count()) * per_sm));
   *parts = static_cast<int>(grid);
   return norm_launched(launch_kernel(kern, static_cast<unsigned>(grid), kBwdBlock<W>, S * stage, s, 1, a, S));
 }
@@ -916,11 +1001,11 @@ mx_status backward_rows(const NormArgs& a, int* parts, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   const int64_t n = a.cols / V;
   if (a.cols % V == 0 && n > 64) {
-    if (n <= 128) return backward_ring<T, 4, 1>(a, parts, s);
-    if (n <= 256) return backward_ring<T, 8, 1>(a, parts, s);
-    if (n <= 512) return backward_ring<T, 16, 1>(a, parts, s);
-    if (n <= 1024) return backward_ring<T, 16, 2>(a, parts, s);
-    if (n <= 2048) return backward_ring<T, 32, 2>(a, parts, s);
+    if (n <= 128) return backward_ring<T, 4, 1, 4>(a, parts, s);
+    if (n <= 256) return backward_ring<T, 8, 1, 4>(a, parts, s);
+    if (n <= 512) return backward_ring<T, 16, 1, 4>(a, parts, s);
+    if (n <= 1024) return backward_ring<T, 16, 2, 2>(a, parts, s);
+    if (n <= 2048) return backward_ring<T, 32, 2, 1>(a, parts, s);
   }
   return backward_any<T, V>(a, parts, s);
 }
