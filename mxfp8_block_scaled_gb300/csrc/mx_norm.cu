@@ -127,11 +127,13 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // Keeps a row packed between two sweeps: without it the compiler carries the
 // first sweep's FP32 values along, twice the registers.
-template <typename T, int V, int K>
-__device__ __forceinline__ void keep_packed(Pack<T, V>* p) {
-  uint32_t* w = reinterpret_cast<uint32_t*>(p);
+template <int K, typename P>
+__device__ __forceinline__ void keep_packed(P* p) {
+  if constexpr (sizeof(P) >= 4) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(p);
 #pragma unroll
-  for (int i = 0; i < static_cast<int>(K * V * sizeof(T) / 4); ++i) asm volatile("" : "+r"(w[i]));
+    for (int i = 0; i < static_cast<int>(K * sizeof(P) / 4); ++i) asm volatile("" : "+r"(w[i]));
+  }
 }
 
 // Sums of two values over the TPR threads of a group, to all of them. `slot`:
@@ -187,7 +189,7 @@ __global__ void __launch_bounds__(BLOCK) norm_forward_kernel(const NormArgs a) {
       group_sum<TPR>(mean, zero, slot, flip, group);
       mean *= a.inv_cols;
     }
-    keep_packed<T, V, K>(cur);
+    keep_packed<K>(cur);
     float sq = 0.0f;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -207,7 +209,7 @@ __global__ void __launch_bounds__(BLOCK) norm_forward_kernel(const NormArgs a) {
       }
     }
     group_sum<TPR>(sq, zero, slot, flip, group);
-    keep_packed<T, V, K>(cur);
+    keep_packed<K>(cur);
     const float rstd = __frsqrt_rn(fmaf(sq, a.inv_cols, a.eps));
     T* out = static_cast<T*>(a.out) + row * a.ldo;
 #pragma unroll
@@ -329,8 +331,8 @@ __global__ void __launch_bounds__(BLOCK, BLOCK == 1024 || K * V > 8 ? 1 : 2) nor
       }
     }
     group_sum<TPR>(s1, s2, slot, flip, group);
-    keep_packed<T, V, K>(cx);
-    keep_packed<T, V, K>(cd);
+    keep_packed<K>(cx);
+    keep_packed<K>(cd);
     s1 = a.center ? s1 * a.inv_cols : 0.0f;
     s2 *= a.inv_cols;
     T* out = static_cast<T*>(a.out) + row * a.ldo;
@@ -536,21 +538,29 @@ __device__ __forceinline__ void group_totals(float (&v)[N], float* slot, int& fl
   for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, t[0], i * L);
 }
 
-// Two neighbouring elements of a pack as FP32, for the packed FP32 instructions
-// (two results an issue slot: both ring kernels are near the issue rate).
-__device__ __forceinline__ float2 two_of(const Pack<float, 4>& p, int j) { return make_float2(p.e[2 * j], p.e[2 * j + 1]); }
-__device__ __forceinline__ float2 two_of(const Pack<__nv_bfloat16, 8>& p, int j) {
-  const uint32_t w = reinterpret_cast<const uint32_t*>(&p)[j];
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+// Sixteen bytes of a row as 32-bit words, and two neighbouring elements of them
+// as FP32 for the packed FP32 instructions (two results an issue slot: both
+// ring kernels are near the issue rate).
+struct alignas(16) Words {
+  uint32_t w[4];
+};
+template <typename T>
+__device__ __forceinline__ float2 two_of(const Words& p, int j) {
+  if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(p.w[2 * j]), __uint_as_float(p.w[2 * j + 1]));
+  return make_float2(__uint_as_float(p.w[j] << 16), __uint_as_float(p.w[j] & 0xFFFF0000u));
 }
-__device__ __forceinline__ void set_two(Pack<float, 4>& p, int j, float2 v) {
-  p.e[2 * j] = v.x;
-  p.e[2 * j + 1] = v.y;
-}
-__device__ __forceinline__ void set_two(Pack<__nv_bfloat16, 8>& p, int j, float2 v) {
-  reinterpret_cast<__nv_bfloat162*>(&p)[j] = __float22bfloat162_rn(v);
+template <typename T>
+__device__ __forceinline__ void set_two(Words& p, int j, float2 v) {
+  if constexpr (sizeof(T) == 4) {
+    p.w[2 * j] = __float_as_uint(v.x);
+    p.w[2 * j + 1] = __float_as_uint(v.y);
+  } else {
+    const __nv_bfloat162 h = __float22bfloat162_rn(v);
+    p.w[j] = *reinterpret_cast<const uint32_t*>(&h);
+  }
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ Words words_at(const void* p) { return *reinterpret_cast<const Words*>(p); }
 
 // Forward, two rows at a time: they share each read of weight and bias (which
 // come from L1, whose bandwidth they would otherwise fill) and each barrier. A
@@ -560,7 +570,10 @@ constexpr int kFwdStages = 2;
 template <int W>
 constexpr int kFwdBlock = W <= 8 ? 256 : 32 * W;
 
-template <typename T, int W>
+// kF32: weight and bias are both there, in FP32 (the usual case: read with no
+// further questions; asking per vector cost as many instructions as the row's
+// arithmetic).
+template <typename T, int W, bool kF32>
 __global__ void __launch_bounds__(kFwdBlock<W>, W <= 8 ? 3 : 1) norm_forward_ring_kernel(const NormArgs a) {
   constexpr int V = 16 / sizeof(T), K = kFwdVecs, G = kFwdBlock<W> / (32 * W), S = kFwdStages;
   extern __shared__ __align__(128) uint8_t ring[];
@@ -597,22 +610,20 @@ __global__ void __launch_bounds__(kFwdBlock<W>, W <= 8 ? 3 : 1) norm_forward_rin
   int s = 0, flip = 0;
   uint32_t parity = 0;
   const int n = a.cols / V;
+  const float4* const w4 = static_cast<const float4*>(a.weight) + r * (V / 4);
+  const float4* const b4 = static_cast<const float4*>(a.bias) + r * (V / 4);
   for (; pair < pairs; pair += step) {
     stage_wait(&full[group][s], parity, a, &gave_up);
     const bool two = 2 * pair + 1 < a.rows;
-    const uint8_t* from = stages + static_cast<size_t>(s) * 2 * row_bytes;
-    Pack<T, V> p[2][K];
+    const uint8_t* from = stages + static_cast<uint32_t>(s) * 2 * row_bytes + r * 16;
+    Words p[2][K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
       const int v = k * 32 * W + r;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        if (v < n && (q == 0 || two)) {
-          p[q][k] = *reinterpret_cast<const Pack<T, V>*>(from + q * row_bytes + v * 16);
-        } else {
-#pragma unroll
-          for (int i = 0; i < V; ++i) from_f(p[q][k].e[i], 0.0f);
-        }
+        p[q][k] = Words{{0u, 0u, 0u, 0u}};
+        if (v < n && (q == 0 || two)) p[q][k] = words_at(from + q * row_bytes + k * 32 * W * 16);
       }
     }
     float mean[2] = {0.0f, 0.0f}, sq[2] = {0.0f, 0.0f};
@@ -623,14 +634,14 @@ __global__ void __launch_bounds__(kFwdBlock<W>, W <= 8 ? 3 : 1) norm_forward_rin
 #pragma unroll
         for (int j = 0; j < V / 2; ++j)
 #pragma unroll
-          for (int q = 0; q < 2; ++q) t[q] = __fadd2_rn(t[q], two_of(p[q][k], j));
+          for (int q = 0; q < 2; ++q) t[q] = __fadd2_rn(t[q], two_of<T>(p[q][k], j));
       mean[0] = t[0].x + t[0].y;
       mean[1] = t[1].x + t[1].y;
       group_totals<2, W>(mean, s_sum[group], flip, group);
       mean[0] *= a.inv_cols;
       mean[1] *= a.inv_cols;
-      keep_packed<T, V, K>(p[0]);
-      keep_packed<T, V, K>(p[1]);
+      keep_packed<K>(p[0]);
+      keep_packed<K>(p[1]);
     }
     {
       const float2 minus[2] = {both(-mean[0]), both(-mean[1])};
@@ -642,7 +653,7 @@ __global__ void __launch_bounds__(kFwdBlock<W>, W <= 8 ? 3 : 1) norm_forward_rin
           for (int j = 0; j < V / 2; ++j)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const float2 d = __fadd2_rn(two_of(p[q][k], j), minus[q]);
+              const float2 d = __fadd2_rn(two_of<T>(p[q][k], j), minus[q]);
               t[q] = __ffma2_rn(d, d, t[q]);
             }
         }
@@ -650,8 +661,8 @@ __global__ void __launch_bounds__(kFwdBlock<W>, W <= 8 ? 3 : 1) norm_forward_rin
       sq[1] = t[1].x + t[1].y;
     }
     group_totals<2, W>(sq, s_sum[group], flip, group);
-    keep_packed<T, V, K>(p[0]);
-    keep_packed<T, V, K>(p[1]);
+    keep_packed<K>(p[0]);
+    keep_packed<K>(p[1]);
     // Every thread of the group has its vectors in registers: the stage is free.
     if (r == 0 && pair + S * step < pairs) issue(s, pair + S * step);
     if (++s == S) {
@@ -659,28 +670,34 @@ __global__ void __launch_bounds__(kFwdBlock<W>, W <= 8 ? 3 : 1) norm_forward_rin
       parity ^= 1;
     }
     const float rstd[2] = {__frsqrt_rn(fmaf(sq[0], a.inv_cols, a.eps)), __frsqrt_rn(fmaf(sq[1], a.inv_cols, a.eps))};
-    T* out = static_cast<T*>(a.out) + 2 * pair * a.ldo;
+    T* const out0 = static_cast<T*>(a.out) + 2 * pair * a.ldo + r * V;
+    T* const out1 = out0 + a.ldo;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int c = (k * 32 * W + r) * V;
-      if (c >= a.cols) break;
-      Pack<T, V> o[2];
+      if (k * 32 * W + r >= n) break;
+      Words o[2];
 #pragma unroll
       for (int j = 0; j < V; j += 4) {
-        float w[4], b[4];
+        float4 w, b;
         asm volatile("" ::: "memory");  // four parameters at a time: hoisted, they would fill the registers
-        load_param<4>(a.weight, a.param_f32, c + j, 4, 1.0f, w);
-        load_param<4>(a.bias, a.param_f32, c + j, 4, 0.0f, b);
+        if constexpr (kF32) {
+          w = w4[(k * 32 * W * V + j) / 4];
+          b = b4[(k * 32 * W * V + j) / 4];
+        } else {
+          const int c = (k * 32 * W + r) * V + j;
+          load_param<4>(a.weight, a.param_f32, c, 4, 1.0f, &w.x);
+          load_param<4>(a.bias, a.param_f32, c, 4, 0.0f, &b.x);
+        }
 #pragma unroll
-        for (int i = 0; i < 4; i += 2)
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const float2 h = __fmul2_rn(__fadd2_rn(two_of(p[q][k], (j + i) / 2), both(-mean[q])), both(rstd[q]));
-            set_two(o[q], (j + i) / 2, __ffma2_rn(h, make_float2(w[i], w[i + 1]), make_float2(b[i], b[i + 1])));
-          }
+        for (int q = 0; q < 2; ++q) {
+          const float2 lo = __fmul2_rn(__fadd2_rn(two_of<T>(p[q][k], j / 2), both(-mean[q])), both(rstd[q]));
+          const float2 hi = __fmul2_rn(__fadd2_rn(two_of<T>(p[q][k], j / 2 + 1), both(-mean[q])), both(rstd[q]));
+          set_two<T>(o[q], j / 2, __ffma2_rn(lo, make_float2(w.x, w.y), make_float2(b.x, b.y)));
+          set_two<T>(o[q], j / 2 + 1, __ffma2_rn(hi, make_float2(w.z, w.w), make_float2(b.z, b.w)));
+        }
       }
-      *reinterpret_cast<Pack<T, V>*>(out + c) = o[0];
-      if (two) *reinterpret_cast<Pack<T, V>*>(out + a.ldo + c) = o[1];
+      *reinterpret_cast<Words*>(out0 + k * 32 * W * V) = o[0];
+      if (two) *reinterpret_cast<Words*>(out1 + k * 32 * W * V) = o[1];
     }
     if (r < (two ? 2 : 1)) {
       if (a.mean && a.center) a.mean[2 * pair + r] = r ? mean[1] : mean[0];
@@ -754,11 +771,11 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ri
     }
   };
   // Vector k of row q of the stage: h = (x - mean) rstd, g = dy w, d = dy.
-  auto values = [&](const uint8_t* from, int q, int c, int j, const Pack<T, V>& px, const Pack<T, V>& pd, float2 w,
+  auto values = [&](const uint8_t* from, int q, int c, int j, const Words& px, const Words& pd, float2 w,
                     float2& h, float2& g, float2& d) {
-    d = two_of(pd, j);
+    d = two_of<T>(pd, j);
     g = __fmul2_rn(d, w);
-    h = __fmul2_rn(__fadd2_rn(two_of(px, j), both(-mean[q])), both(rstd[q]));
+    h = __fmul2_rn(__fadd2_rn(two_of<T>(px, j), both(-mean[q])), both(rstd[q]));
   };
   int s = 0, flip = 0;
   uint32_t parity = 0;
@@ -775,16 +792,10 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ri
 #pragma unroll
       for (int k = 0; k < K; ++k) {
         const int c = (k * 32 * W + r) * V;
-        Pack<T, V> px, pd;
+        Words px{{0u, 0u, 0u, 0u}}, pd{{0u, 0u, 0u, 0u}};  // no such row or column: dy = 0 adds nothing
         if (c < a.cols && q < n) {
-          px = *reinterpret_cast<const Pack<T, V>*>(from + q * row_bytes + c * sizeof(T));
-          pd = *reinterpret_cast<const Pack<T, V>*>(from + (R + q) * row_bytes + c * sizeof(T));
-        } else {  // no such row or column: dy = 0 adds nothing
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            from_f(px.e[i], 0.0f);
-            from_f(pd.e[i], 0.0f);
-          }
+          px = words_at(from + q * row_bytes + c * sizeof(T));
+          pd = words_at(from + (R + q) * row_bytes + c * sizeof(T));
         }
         float w[4];
 #pragma unroll
@@ -821,13 +832,13 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ri
       for (int k = 0; k < K; ++k) {
         const int c = (k * 32 * W + r) * V;
         if (c >= a.cols) break;
-        Pack<T, V> o;
+        Words o;
         if constexpr (kHold) {
 #pragma unroll
-          for (int j = 0; j < P; ++j) set_two(o, j, __ffma2_rn(by_h, h[q * P + j], __ffma2_rn(by_g, g[q * P + j], add)));
+          for (int j = 0; j < P; ++j) set_two<T>(o, j, __ffma2_rn(by_h, h[q * P + j], __ffma2_rn(by_g, g[q * P + j], add)));
         } else {
-          const Pack<T, V> px = *reinterpret_cast<const Pack<T, V>*>(from + q * row_bytes + c * sizeof(T));
-          const Pack<T, V> pd = *reinterpret_cast<const Pack<T, V>*>(from + (R + q) * row_bytes + c * sizeof(T));
+          const Words px = words_at(from + q * row_bytes + c * sizeof(T));
+          const Words pd = words_at(from + (R + q) * row_bytes + c * sizeof(T));
           float w[4];
 #pragma unroll
           for (int j = 0; j < P; ++j) {
@@ -837,10 +848,10 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ri
             }
             float2 hj, gj, d;
             values(from, q, c, j, px, pd, make_float2(w[2 * j & 3], w[(2 * j & 3) + 1]), hj, gj, d);
-            set_two(o, j, __ffma2_rn(by_h, hj, __ffma2_rn(by_g, gj, add)));
+            set_two<T>(o, j, __ffma2_rn(by_h, hj, __ffma2_rn(by_g, gj, add)));
           }
         }
-        *reinterpret_cast<Pack<T, V>*>(out + q * a.ldo + c) = o;
+        *reinterpret_cast<Words*>(out + q * a.ldo + c) = o;
       }
     }
     if (++s == S) {
@@ -919,7 +930,7 @@ template <typename T, int W>
 mx_status forward_ring(const NormArgs& a, cudaStream_t s) {
   constexpr int G = kFwdBlock<W> / (32 * W);
   const size_t smem = static_cast<size_t>(G) * kFwdStages * 2 * a.cols * sizeof(T);
-  auto kern = norm_forward_ring_kernel<T, W>;
+  auto kern = a.weight && a.bias && a.param_f32 ? norm_forward_ring_kernel<T, W, true> : norm_forward_ring_kernel<T, W, false>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(norm smem)");
   const int64_t grid = std::min<int64_t>(((a.rows + 1) / 2 + G - 1) / G, static_cast<int64_t>(sm_count()) * (W <= 8 ? 3 : 1));
