@@ -718,7 +718,9 @@ constexpr int kBwdBlock = W <= 8 ? 256 : 32 * W;
 template <typename T, int W, int K, int R>
 __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ring_kernel(const NormArgs a, const int S) {
   constexpr int V = 16 / sizeof(T), P = V / 2, G = kBwdBlock<W> / (32 * W), kMaxS = 8;
-  constexpr bool kHold = K == 1;  // one vector a thread: weights, h and g stay in registers
+  // What stays in a thread's registers besides dw and db: its weights, g of the
+  // R rows, and h too where there is room. The rest is read or computed again.
+  constexpr bool kHold = K <= 2 && W <= 16, kHoldH = K == 1 && G == 1;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[G][kMaxS];
   __shared__ float s_sum[G][2 * 2 * R * W];
@@ -754,13 +756,27 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ri
   float2 dw[K * P], db[K * P];
 #pragma unroll
   for (int i = 0; i < K * P; ++i) dw[i] = db[i] = both(0.0f);
-  float2 w1[kHold ? P : 1];
+  float2 w1[kHold ? K * P : 1];
   if constexpr (kHold) {
-    float w[V];
-    load_param<V>(a.weight, a.param_f32, r * V, a.cols - r * V, 1.0f, w);
 #pragma unroll
-    for (int j = 0; j < P; ++j) w1[j] = make_float2(w[2 * j], w[2 * j + 1]);
+    for (int k = 0; k < K; ++k) {
+      float w[V];
+      const int c = (k * 32 * W + r) * V;
+      load_param<V>(a.weight, a.param_f32, c, a.cols - c, 1.0f, w);
+#pragma unroll
+      for (int j = 0; j < P; ++j) w1[k * P + j] = make_float2(w[2 * j], w[2 * j + 1]);
+    }
   }
+  // Weights 2 j .. 2 j + 3 of vector c / V, of which the pair at j is wanted.
+  auto weight2 = [&](int k, int c, int j, float4& w) {
+    if constexpr (kHold) return w1[kHold ? k * P + j : 0];
+    if (j % 2 == 0) {
+      asm volatile("" ::: "memory");
+      if (a.weight && a.param_f32) w = *reinterpret_cast<const float4*>(static_cast<const float*>(a.weight) + c + 2 * j);
+      else load_param<4>(a.weight, a.param_f32, c + 2 * j, 4, 1.0f, &w.x);
+    }
+    return j % 2 == 0 ? make_float2(w.x, w.y) : make_float2(w.z, w.w);
+  };
   float mean[R], rstd[R];
   auto statistics = [&](int64_t at) {
 #pragma unroll
@@ -770,12 +786,8 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ri
       rstd[q] = in ? a.rstd[at + q] : 0.0f;
     }
   };
-  // Vector k of row q of the stage: h = (x - mean) rstd, g = dy w, d = dy.
-  auto values = [&](const uint8_t* from, int q, int c, int j, const Words& px, const Words& pd, float2 w,
-                    float2& h, float2& g, float2& d) {
-    d = two_of<T>(pd, j);
-    g = __fmul2_rn(d, w);
-    h = __fmul2_rn(__fadd2_rn(two_of<T>(px, j), both(-mean[q])), both(rstd[q]));
+  auto h_of = [&](const Words& px, int q, int j) {
+    return __fmul2_rn(__fadd2_rn(two_of<T>(px, j), both(-mean[q])), both(rstd[q]));
   };
   int s = 0, flip = 0;
   uint32_t parity = 0;
@@ -784,7 +796,7 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ri
     stage_wait(&full[group][s], parity, a, &gave_up);
     const int n = static_cast<int>(min64(R, a.rows - row));
     const uint8_t* from = stages + static_cast<size_t>(s) * 2 * R * row_bytes;
-    float2 h[kHold ? R * P : 1], g[kHold ? R * P : 1];
+    float2 g[kHold ? R * K * P : 1], h[kHoldH ? R * P : 1];  // h = (x - mean) rstd, g = dy w
     float sum[2 * R];  // of g, then of g h
 #pragma unroll
     for (int q = 0; q < R; ++q) {
@@ -797,22 +809,17 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ri
           px = words_at(from + q * row_bytes + c * sizeof(T));
           pd = words_at(from + (R + q) * row_bytes + c * sizeof(T));
         }
-        float w[4];
+        if (kHold || c < a.cols) {
+          float4 w;
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-          if (!kHold && j % 2 == 0) {
-            asm volatile("" ::: "memory");
-            load_param<4>(a.weight, a.param_f32, c + 2 * j, a.cols - c, 1.0f, w);
-          }
-          float2 hj, gj, d;
-          values(from, q, c, j, px, pd, kHold ? w1[kHold ? j : 0] : make_float2(w[2 * j & 3], w[(2 * j & 3) + 1]), hj, gj, d);
-          t1 = __fadd2_rn(t1, gj);
-          t2 = __ffma2_rn(gj, hj, t2);
-          dw[k * P + j] = __ffma2_rn(d, hj, dw[k * P + j]);
-          db[k * P + j] = __fadd2_rn(db[k * P + j], d);
-          if constexpr (kHold) {
-            h[q * P + j] = hj;
-            g[q * P + j] = gj;
+          for (int j = 0; j < P; ++j) {
+            const float2 d = two_of<T>(pd, j), gj = __fmul2_rn(d, weight2(k, c, j, w)), hj = h_of(px, q, j);
+            t1 = __fadd2_rn(t1, gj);
+            t2 = __ffma2_rn(gj, hj, t2);
+            dw[k * P + j] = __ffma2_rn(d, hj, dw[k * P + j]);
+            db[k * P + j] = __fadd2_rn(db[k * P + j], d);
+            if constexpr (kHold) g[(q * K + k) * P + j] = gj;
+            if constexpr (kHoldH) h[q * P + j] = hj;
           }
         }
       }
@@ -832,24 +839,18 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ri
       for (int k = 0; k < K; ++k) {
         const int c = (k * 32 * W + r) * V;
         if (c >= a.cols) break;
-        Words o;
-        if constexpr (kHold) {
+        Words o, px, pd;
+        if constexpr (!kHoldH) px = words_at(from + q * row_bytes + c * sizeof(T));
+        if constexpr (!kHold) pd = words_at(from + (R + q) * row_bytes + c * sizeof(T));
+        float4 w;
 #pragma unroll
-          for (int j = 0; j < P; ++j) set_two<T>(o, j, __ffma2_rn(by_h, h[q * P + j], __ffma2_rn(by_g, g[q * P + j], add)));
-        } else {
-          const Words px = words_at(from + q * row_bytes + c * sizeof(T));
-          const Words pd = words_at(from + (R + q) * row_bytes + c * sizeof(T));
-          float w[4];
-#pragma unroll
-          for (int j = 0; j < P; ++j) {
-            if (j % 2 == 0) {
-              asm volatile("" ::: "memory");
-              load_param<4>(a.weight, a.param_f32, c + 2 * j, 4, 1.0f, w);
-            }
-            float2 hj, gj, d;
-            values(from, q, c, j, px, pd, make_float2(w[2 * j & 3], w[(2 * j & 3) + 1]), hj, gj, d);
-            set_two<T>(o, j, __ffma2_rn(by_h, hj, __ffma2_rn(by_g, gj, add)));
-          }
+        for (int j = 0; j < P; ++j) {
+          float2 gj, hj;
+          if constexpr (kHold) gj = g[(q * K + k) * P + j];
+          else gj = __fmul2_rn(two_of<T>(pd, j), weight2(k, c, j, w));
+          if constexpr (kHoldH) hj = h[q * P + j];
+          else hj = h_of(px, q, j);
+          set_two<T>(o, j, __ffma2_rn(by_h, hj, __ffma2_rn(by_g, gj, add)));
         }
         *reinterpret_cast<Words*>(out + q * a.ldo + c) = o;
       }
@@ -958,6 +959,7 @@ mx_status backward_ring(const NormArgs& a, int* parts, cudaStream_t s) {
   constexpr int G = kBwdBlock<W> / (32 * W), per_sm = W <= 8 ? 2 : 1;
   const size_t stage = static_cast<size_t>(G) * 2 * R * a.cols * sizeof(T);
   const int S = static_cast<int>(std::min<size_t>(4, 212992 / per_sm / stage));
+  static_assert(2 * G * 2 * R * 32 * W * K * 16 <= 212992 / per_sm, "a stage is refilled while another one is worked on");
   auto kern = norm_backward_ring_kernel<T, W, K, R>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S * stage));
   if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(norm smem)");
@@ -1011,12 +1013,14 @@ template <typename T>
 mx_status backward_rows(const NormArgs& a, int* parts, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   const int64_t n = a.cols / V;
-  if (a.cols % V == 0 && n > 64) {
+  if (a.cols % V == 0 && n > 16) {
+    if (n <= 32) return backward_ring<T, 1, 1, 4>(a, parts, s);
+    if (n <= 64) return backward_ring<T, 2, 1, 4>(a, parts, s);
     if (n <= 128) return backward_ring<T, 4, 1, 4>(a, parts, s);
     if (n <= 256) return backward_ring<T, 8, 1, 4>(a, parts, s);
-    if (n <= 512) return backward_ring<T, 16, 1, 4>(a, parts, s);
+    if (n <= 512) return backward_ring<T, 8, 2, 2>(a, parts, s);
     if (n <= 1024) return backward_ring<T, 16, 2, 2>(a, parts, s);
-    if (n <= 2048) return backward_ring<T, 32, 2, 1>(a, parts, s);
+    if (n <= 2048) return backward_ring<T, 16, 4, 1>(a, parts, s);
   }
   return backward_any<T, V>(a, parts, s);
 }
@@ -1091,28 +1095,41 @@ namespace {
 
 // out[c] = sum over p of partial[p][c], c over the n0 + n1 columns of a partial
 // row (the first n0 go to out0, the others to out1; null: not wanted). A CTA
-// takes 32 columns; thread row y adds the partial rows y, y + 32, ... and the
-// 32 sums of a column are added in order: a fixed order whatever the grid.
-__global__ void __launch_bounds__(1024) column_reduce_kernel(const float* partial, int parts, int64_t n0, int64_t n1,
-                                                             float* out0, float* out1) {
-  __shared__ float s[32][33];
+// takes 8 * V columns; thread row y adds the partial rows y, y + 32, ... and a
+// column's 32 sums are then added pairwise: a fixed order whatever the grid.
+template <int V>
+__global__ void __launch_bounds__(256) column_reduce_kernel(const float* partial, int parts, int64_t n0, int64_t n1,
+                                                            float* out0, float* out1) {
+  __shared__ float s[32][8 * V + 1];
   pdl_launch_dependents();
+  const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
+  const int64_t n = n0 + n1, c = (static_cast<int64_t>(blockIdx.x) * 8 + tx) * V;
+  float v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = 0.0f;
   pdl_wait();
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + tx, n = n0 + n1;
-  float v = 0.0f;
   if (c < n) {
-#pragma unroll 4
-    for (int p = ty; p < parts; p += 32) v += partial[static_cast<int64_t>(p) * n + c];
+#pragma unroll 8
+    for (int p = ty; p < parts; p += 32) {
+      const Pack<float, V> q = *reinterpret_cast<const Pack<float, V>*>(partial + static_cast<int64_t>(p) * n + c);
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] += q.e[i];
+    }
   }
-  s[ty][tx] = v;
+#pragma unroll
+  for (int i = 0; i < V; ++i) s[ty][tx * V + i] = v[i];
   __syncthreads();
-  // warp ty sums column ty of the tile across its lanes
-  v = warp_sum(s[tx][ty]);
-  const int64_t oc = static_cast<int64_t>(blockIdx.x) * 32 + ty;
-  if (tx == 0 && oc < n) {
-    float* out = oc < n0 ? out0 : out1;
-    if (out) out[oc < n0 ? oc : oc - n0] = v;
+  // Warp w adds columns w, w + 8, ... of the tile, a lane for each thread row.
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    const int col = j * 8 + w;
+    const float t = warp_sum(s[lane][col]);
+    const int64_t oc = static_cast<int64_t>(blockIdx.x) * 8 * V + col;
+    if (lane == 0 && oc < n) {
+      float* out = oc < n0 ? out0 : out1;
+      if (out) out[oc < n0 ? oc : oc - n0] = t;
+    }
   }
 }
 
@@ -1120,8 +1137,12 @@ __global__ void __launch_bounds__(1024) column_reduce_kernel(const float* partia
 
 mx_status launch_column_reduce(const float* partial, int parts, int64_t n0, int64_t n1, float* out0, float* out1,
                                cudaStream_t s) {
-  return cuda_status(launch_kernel(column_reduce_kernel, static_cast<unsigned>((n0 + n1 + 31) / 32), 1024, 0, s, 1,
-                                   partial, parts, n0, n1, out0, out1),
+  const int64_t n = n0 + n1;
+  const bool vec = n % 4 == 0 && (reinterpret_cast<uintptr_t>(partial) & 15) == 0;
+  const int width = vec ? 32 : 8;
+  return cuda_status(launch_kernel(vec ? column_reduce_kernel<4> : column_reduce_kernel<1>,
+                                   static_cast<unsigned>((n + width - 1) / width), 256, 0, s, 1, partial, parts, n0, n1,
+                                   out0, out1),
                      "partial sums launch");
 }
 
