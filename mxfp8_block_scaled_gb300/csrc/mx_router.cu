@@ -18,12 +18,14 @@
 //
 // One read of the logits each way. A token's row lies in the registers of LPT
 // lanes, EPL neighbouring experts each, so a warp works on 32 / LPT tokens at
-// once and nothing but shuffles joins the lanes; top_k rounds of a group
-// maximum choose the experts. Each CTA takes a run of tokens of one sequence and
-// keeps its per-expert sums of p and counts in registers; they are added over
-// the CTA in shared memory and over CTAs by two short launches, everything in a
-// fixed order (same inputs, same bits; no atomics). Sums of p are FP32 over at
-// most a few hundred terms at each level.
+// once and nothing but shuffles joins the lanes. The work is bound by issued
+// instructions before it is by memory, so the choice is made on one 32-bit key
+// per logit that also holds the expert: the lanes sort their keys once and
+// top_k rounds of a group maximum take the heads. Each CTA takes a run of tokens
+// of one sequence; its sums of p stay in registers, are added over the CTA in
+// shared memory and over CTAs by two short launches, in a fixed order (same
+// inputs, same bits). Only whole numbers are added by atomics, in shared memory.
+// Sums of p are FP32 over at most a few hundred terms at each level.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -96,12 +98,6 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 template <int LPT>
-__device__ __forceinline__ float group_maxf(float v) {
-#pragma unroll
-  for (int o = LPT / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-  return v;
-}
-template <int LPT>
 __device__ __forceinline__ uint32_t group_max(uint32_t v) {
   if constexpr (LPT == 32) return __reduce_max_sync(kFull, v);
 #pragma unroll
@@ -134,29 +130,34 @@ __device__ __forceinline__ void load_row(const T* row, int first, int experts, b
   }
 }
 
-// Softmax of a token over its group, in place; false (0 everywhere) if no logit
-// is above -inf. A NaN logit makes the whole row NaN.
-template <int LPT, int EPL>
-__device__ __forceinline__ bool group_softmax(float* x) {
-  float m = -INFINITY;
-  bool any = false;
+// A logit as an unsigned number of the same order, above 0; 0 for what is not
+// to be chosen (-inf, NaN). -0 counts as +0.
+__device__ __forceinline__ uint32_t order_key(float x) {
+  const uint32_t b = __float_as_uint(x + 0.0f);
+  return x > -INFINITY ? b ^ (static_cast<int32_t>(b) < 0 ? 0xFFFFFFFFu : 0x80000000u) : 0u;
+}
+
+__device__ __forceinline__ void order_pair(uint32_t& a, uint32_t& b) {
+  const uint32_t hi = max(a, b);
+  b = min(a, b);
+  a = hi;
+}
+
+// Descending: halves sorted, then merged (the second half met in reverse, which
+// leaves two bitonic halves).
+template <int N>
+__device__ __forceinline__ void sort_keys(uint32_t* k) {
+  if constexpr (N > 1) {
+    sort_keys<N / 2>(k);
+    sort_keys<N / 2>(k + N / 2);
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    m = fmaxf(m, x[i]);
-    any |= !(x[i] == -INFINITY);
+    for (int i = 0; i < N / 2; ++i) order_pair(k[i], k[N - 1 - i]);
+#pragma unroll
+    for (int q = N / 4; q >= 1; q /= 2)
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if ((i & q) == 0) order_pair(k[i], k[i + q]);
   }
-  m = group_maxf<LPT>(m);
-  any = group_max<LPT>(any ? 1u : 0u) != 0;
-  float sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    x[i] = __expf(x[i] - m);
-    sum += x[i];
-  }
-  const float inv = __frcp_rn(group_sum<LPT>(sum));
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) x[i] = any ? x[i] * inv : 0.0f;
-  return any;
 }
 
 // The tokens of this CTA: [first, end) of sequence s.
@@ -174,105 +175,153 @@ __device__ __forceinline__ Run run_of(const RouterArgs& a) {
 
 template <typename T, int LPT, int EPL>
 __global__ void __launch_bounds__(kRouterThreads) router_forward_kernel(const RouterArgs a) {
-  constexpr int TPW = 32 / LPT;  // tokens of a warp at a time
-  __shared__ float s_p[kRouterWarps][LPT * EPL];
-  __shared__ int32_t s_n[kRouterWarps][LPT * EPL];
+  constexpr int TPW = 32 / LPT;   // tokens of a warp at a time
+  constexpr int E = LPT * EPL;    // experts that fit
+  // A packed key: the logit's key without its lowest bits, which hold E - 1 -
+  // expert, so that the larger key wins and ties go to the lowest expert. BF16
+  // logits lose nothing by it. FP32 ones do: where two keys that meet in the
+  // choice agree in all that is left of their logits, the token is done again
+  // with whole keys.
+  constexpr uint32_t kLow = E - 1;
+  static_assert((E & (E - 1)) == 0 && E <= 512, "bits for the expert");
+  constexpr bool kExact = sizeof(T) == 2;
+  __shared__ float s_p[kRouterWarps][E];
+  __shared__ int32_t s_n[E];
   __shared__ int32_t s_v[kRouterWarps];
   pdl_launch_dependents();
+  for (int e = threadIdx.x; e < E; e += kRouterThreads) s_n[e] = 0;
+  __syncthreads();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LPT, sub = lane / LPT;
   const int first = l * EPL;
   const Run run = run_of(a);
   float psum[EPL];
-  int32_t hits[EPL];
-  int32_t valid = 0;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    psum[i] = 0.0f;
-    hits[i] = 0;
-  }
+  for (int i = 0; i < EPL; ++i) psum[i] = 0.0f;
+  int32_t valid = 0;
   for (int64_t t0 = run.first + warp * TPW; t0 < run.end; t0 += kRouterWarps * TPW) {
     const int64_t t = t0 + sub;
     const bool in = t < run.end;
     const bool live = in && (!a.mask || a.mask[t] != 0);
+    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    int32_t* idx = a.indices + t * a.top_k;
     float x[EPL];
-    if (live) {
-      load_row<T, EPL>(static_cast<const T*>(a.logits) + t * a.ld, first, a.experts, a.vec, x);
-    } else {
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) x[i] = -INFINITY;
-    }
-    // Keys in the logits' order; 0: not to be chosen (-inf, NaN, past the last).
+    for (int i = 0; i < EPL; ++i) x[i] = -INFINITY;
+    if (live) load_row<T, EPL>(row, first, a.experts, a.vec, x);
     uint32_t key[EPL];
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const uint32_t b = __float_as_uint(x[i] + 0.0f);  // -0 becomes +0
-      key[i] = x[i] > -INFINITY ? b ^ (static_cast<int32_t>(b) < 0 ? 0xFFFFFFFFu : 0x80000000u) : 0u;
+      const uint32_t k = order_key(x[i]);
+      key[i] = k ? (k & ~kLow) | (kLow - static_cast<uint32_t>(first + i)) : 0u;
     }
-    const bool any = group_softmax<LPT, EPL>(x);
-    int32_t rank[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) rank[i] = -1;
-    float chosen = 0.0f;
-    int32_t found = 0;
+    sort_keys<EPL>(key);
+    uint32_t top = 0, last = 0;
+    int32_t found = 0, mine = -1;  // choices made; the one of round j % LPT == l (kept where top_k <= LPT)
+    bool close = false;
     for (int j = 0; j < a.top_k; ++j) {
-      uint32_t best = 0;
-      int at = 0;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (key[i] > best) {
-          best = key[i];
-          at = i;
-        }
-      const uint32_t top = group_max<LPT>(best);
-      const uint32_t who = group_min<LPT>(best == top ? static_cast<uint32_t>(first + at) : 0xFFFFFFFFu);
-      if (top != 0) {
+      const uint32_t best = group_max<LPT>(key[0]);
+      if (j == 0) top = best;
+      else if (!kExact) close |= best != 0 && ((best ^ last) & ~kLow) == 0;
+      last = best;
+      if (best != 0) {
         found = j + 1;
+        if (j % LPT == l) {
+          mine = static_cast<int32_t>(kLow - (best & kLow));
+          idx[j] = mine;
+        }
+        if (key[0] == best) {  // one lane: keys differ by their experts
 #pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          if (who == static_cast<uint32_t>(first + i)) {
-            key[i] = 0;
-            rank[i] = j;
-            chosen += x[i];
-            ++hits[i];
-          }
+          for (int i = 0; i + 1 < EPL; ++i) key[i] = key[i + 1];
+          key[EPL - 1] = 0;
+        }
       }
+    }
+    if constexpr (!kExact) {
+      // The first one not chosen may be as close to the last one chosen.
+      const uint32_t next = group_max<LPT>(key[0]);
+      close |= next != 0 && last != 0 && ((next ^ last) & ~kLow) == 0;
+      if (__any_sync(kFull, close)) {
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) key[i] = order_key(x[i]);
+        for (int j = 0; j < a.top_k; ++j) {
+          uint32_t best = 0;
+          int at = 0;
+#pragma unroll
+          for (int i = 0; i < EPL; ++i)
+            if (key[i] > best) {
+              best = key[i];
+              at = i;
+            }
+          const uint32_t most = group_max<LPT>(best);
+          const uint32_t who = group_min<LPT>(best == most ? static_cast<uint32_t>(first + at) : kFull);
+          if (most != 0) {
+            if (j % LPT == l) {
+              mine = static_cast<int32_t>(who);
+              idx[j] = mine;
+            }
+#pragma unroll
+            for (int i = 0; i < EPL; ++i)
+              if (who == static_cast<uint32_t>(first + i)) key[i] = 0;
+          }
+        }
+      }
+    }
+    // A row without a key is left out, unless a NaN is why.
+    bool any = top != 0;
+    if (__any_sync(kFull, live && !any)) {
+      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) nan |= x[i] != x[i];
+      any |= group_max<LPT>(nan ? 1u : 0u) != 0;
+    }
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) m = fmaxf(m, x[i]);
+#pragma unroll
+    for (int o = LPT / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      x[i] = __expf(x[i] - m);
+      sum += x[i];
+    }
+    const float inv = __frcp_rn(group_sum<LPT>(sum));
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) psum[i] += any ? x[i] * inv : 0.0f;
+    valid += any;
+    // The chosen weights: lane j % LPT takes choice j and computes its p from the logit.
+    float chosen = 0.0f, p = 0.0f;
+    for (int j = l; j < found; j += LPT) {
+      const int e = a.top_k <= LPT ? mine : idx[j];
+      p = __expf(to_f(row[e]) - m) * inv;
+      chosen += p;
+      atomicAdd(&s_n[e], 1);
     }
     const float scale = a.normalize ? group_sum<LPT>(chosen) : 1.0f;
     if (in) {
-      int32_t* idx = a.indices + t * a.top_k;
       float* w = a.weights + t * a.top_k;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (rank[i] >= 0) {
-          idx[rank[i]] = first + i;
-          w[rank[i]] = a.normalize ? __fdiv_rn(x[i], scale) : x[i];
+      for (int j = l; j < a.top_k; j += LPT) {
+        if (j >= found) {
+          idx[j] = -1;
+          w[j] = 0.0f;
+        } else {
+          if (a.top_k > LPT) p = __expf(to_f(row[idx[j]]) - m) * inv;
+          w[j] = a.normalize ? __fdiv_rn(p, scale) : p;
         }
-      for (int j = found + l; j < a.top_k; j += LPT) {
-        idx[j] = -1;
-        w[j] = 0.0f;
       }
     }
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) psum[i] += x[i];
-    valid += any;
   }
   // Over the warp's subgroups, then over the warps in order.
 #pragma unroll
   for (int o = LPT; o < 32; o <<= 1) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      psum[i] += __shfl_xor_sync(kFull, psum[i], o);
-      hits[i] += __shfl_xor_sync(kFull, hits[i], o);
-    }
+    for (int i = 0; i < EPL; ++i) psum[i] += __shfl_xor_sync(kFull, psum[i], o);
     valid += __shfl_xor_sync(kFull, valid, o);
   }
   if (sub == 0) {
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      s_p[warp][first + i] = psum[i];
-      s_n[warp][first + i] = hits[i];
-    }
+    for (int i = 0; i < EPL; ++i) s_p[warp][first + i] = psum[i];
   }
   if (lane == 0) s_v[warp] = valid;
   __syncthreads();
@@ -280,13 +329,10 @@ __global__ void __launch_bounds__(kRouterThreads) router_forward_kernel(const Ro
     float p = 0.0f;
     int32_t n = 0;
     if (e < a.experts) {
+      n = s_n[e];
       p = s_p[0][e];
-      n = s_n[0][e];
 #pragma unroll
-      for (int w = 1; w < kRouterWarps; ++w) {
-        p += s_p[w][e];
-        n += s_n[w][e];
-      }
+      for (int w = 1; w < kRouterWarps; ++w) p += s_p[w][e];
     }
     a.part_p[blockIdx.x * a.pitch + e] = p;
     a.part_n[blockIdx.x * a.pitch + e] = n;
@@ -415,91 +461,147 @@ __global__ void __launch_bounds__(512) router_finish_kernel(const RouterSums a) 
   }
 }
 
+// Sums of four values over a group, to all of its lanes: two halving steps, then
+// the rest of the tree on one value.
+template <int LPT>
+__device__ __forceinline__ void group_sum4(float (&v)[4]) {
+  constexpr int L = LPT / 4;  // lanes that end up with one value
+  const int l = threadIdx.x % LPT, base = (threadIdx.x & 31) - l;
+  const bool up = (l & LPT / 2) != 0, up2 = (l & LPT / 4) != 0;
+  float a = (up ? v[2] : v[0]) + __shfl_xor_sync(kFull, up ? v[0] : v[2], LPT / 2);
+  const float b = (up ? v[3] : v[1]) + __shfl_xor_sync(kFull, up ? v[1] : v[3], LPT / 2);
+  a = (up2 ? b : a) + __shfl_xor_sync(kFull, up2 ? a : b, LPT / 4);
+#pragma unroll
+  for (int o = L / 2; o > 0; o >>= 1) a += __shfl_xor_sync(kFull, a, o);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(kFull, a, base + i * L);
+}
+
+// With e = exp(x - m) and p = e / sum(e), one reduction over the group gives
+// sum(e), sum(e load), and over the chosen ones z = sum(e) and s = sum(e dw).
+// Not normalised: dot = sum(p load) + sum(p dw). Normalised (w = e / z): the
+// chosen ones' dp = (dw - s/z) / (z/sum), whose p-weighted sum is zero, so dot =
+// sum(p load); every dw is taken against the first one, so that equal ones (a
+// single choice too) cancel exactly. The chosen elements' results are computed
+// by the lanes that hold their dw and put over the row's in shared memory.
 template <typename T, int LPT, int EPL>
 __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const RouterArgs a) {
-  constexpr int TPW = 32 / LPT;
+  constexpr int TPW = 32 / LPT, E = LPT * EPL, W = 16 / sizeof(T);
+  __shared__ __align__(16) T s_row[kRouterWarps * TPW][E];
+  __shared__ float s_load[E];
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LPT, sub = lane / LPT;
   const int first = l * EPL;
   const Run run = run_of(a);
-  float load[EPL];
   const float dloss = a.dloss ? *a.dloss : 0.0f;
+  for (int e = threadIdx.x; e < E; e += kRouterThreads)
+    s_load[e] = e < a.experts ? dloss * a.load[run.s * a.experts + e] : 0.0f;
+  __syncthreads();
+  float load[EPL];
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) load[i] = first + i < a.experts ? dloss * a.load[run.s * a.experts + first + i] : 0.0f;
+  for (int i = 0; i < EPL; ++i) load[i] = s_load[first + i];
+  T* const mine = s_row[warp * TPW + sub];
   for (int64_t t0 = run.first + warp * TPW; t0 < run.end; t0 += kRouterWarps * TPW) {
-    const int64_t t = t0 + sub;
+    const int64_t t = t0 + sub, at = t * a.top_k;
     const bool in = t < run.end;
     const bool live = in && (!a.mask || a.mask[t] != 0);
-    float x[EPL], g[EPL];
-    if (live) {
-      load_row<T, EPL>(static_cast<const T*>(a.logits) + t * a.ld, first, a.experts, a.vec, x);
-    } else {
+    const bool picks = live && a.dweights;
+    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
+    float x[EPL];
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) x[i] = -INFINITY;
+    for (int i = 0; i < EPL; ++i) x[i] = -INFINITY;
+    if (live) load_row<T, EPL>(row, first, a.experts, a.vec, x);
+    // The lane's (first) choice: expert (-1: none) and dw.
+    const float d0 = picks && a.normalize ? a.dweights[at] : 0.0f;
+    int e0 = -1;
+    float d = 0.0f, x0 = 0.0f;
+    auto choice = [&](int j, int& e, float& dw, float& logit) {
+      e = a.indices[at + j];
+      dw = a.dweights[at + j] - d0;
+      if (static_cast<uint32_t>(e) >= static_cast<uint32_t>(a.experts)) e = -1;
+      logit = e >= 0 ? to_f(row[e]) : 0.0f;
+    };
+    if (picks && l < a.top_k) choice(l, e0, d, x0);
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) m = fmaxf(m, x[i]);
+#pragma unroll
+    for (int o = LPT / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // sum(e), sum(e load), z, s
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      x[i] = __expf(x[i] - m);
+      v[0] += x[i];
+      v[1] = fmaf(x[i], load[i], v[1]);
     }
-    const bool any = group_softmax<LPT, EPL>(x);
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) g[i] = load[i];
-    if (a.dweights) {
-      // The chosen weights' gradients at their experts. When normalised, w_j =
-      // p_j / z: dp_j = (dw_j - sum_i w_i dw_i) / z, with every dw taken against
-      // the first one so that equal ones (a single choice too) cancel exactly.
-      float dw[EPL];
-      uint32_t mine = 0;
-      const int64_t at = t * a.top_k;
-      const float d0 = live && a.normalize ? a.dweights[at] : 0.0f;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) dw[i] = 0.0f;
-      for (int j = 0; j < a.top_k; ++j) {
-        const int e = live ? a.indices[at + j] - first : -1;
-        const float d = live ? a.dweights[at + j] - d0 : 0.0f;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          if (e == i) {
-            dw[i] = d;
-            mine |= 1u << i;
-          }
-      }
-      if (a.normalize) {
-        float z = 0.0f, s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          if (mine >> i & 1u) {
-            z += x[i];
-            s = fmaf(x[i], dw[i], s);
-          }
-        const float inv = __frcp_rn(group_sum<LPT>(z));
-        s = group_sum<LPT>(s) * inv;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i)
-          if (mine >> i & 1u) g[i] = fmaf(dw[i] - s, inv, g[i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) g[i] += dw[i];
-      }
+    const float ex0 = e0 >= 0 ? __expf(x0 - m) : 0.0f;
+    if (e0 >= 0) {
+      v[2] = ex0;
+      v[3] = ex0 * d;
     }
-    float dot = 0.0f;
+    if (picks)
+      for (int j = l + LPT; j < a.top_k; j += LPT) {
+        int e;
+        float dw, logit;
+        choice(j, e, dw, logit);
+        if (e >= 0) {
+          const float ex = __expf(logit - m);
+          v[2] += ex;
+          v[3] = fmaf(ex, dw, v[3]);
+        }
+      }
+    group_sum4<LPT>(v);
+    // Left out: masked, or no logit above -inf (m is -inf with no NaN about; the sum is then NaN).
+    bool any = live && m > -INFINITY;
+    if (__any_sync(kFull, live && !any)) {
+      bool nan = false;
+      if (live) {
+        float y[EPL];
+        load_row<T, EPL>(row, first, a.experts, a.vec, y);
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) dot = fmaf(x[i], g[i], dot);
-    dot = group_sum<LPT>(dot);
+        for (int i = 0; i < EPL; ++i) nan |= y[i] != y[i];
+      }
+      any |= group_max<LPT>(nan ? 1u : 0u) != 0;
+    }
+    const float inv = __frcp_rn(v[0]), base = v[1] * inv, rz = __frcp_rn(v[2]), mean_d = v[3] * rz;
+    const float dot = a.normalize ? base : fmaf(v[3], inv, base);
+    // The row without its chosen ones' own gradients ...
+#pragma unroll
+    for (int j = 0; j < EPL; j += W) {
+      Vec16<T> o;
+#pragma unroll
+      for (int i = 0; i < W; ++i) from_f(o.e[i], any ? x[j + i] * inv * (load[j + i] - dot) : 0.0f);
+      *reinterpret_cast<Vec16<T>*>(mine + first + j) = o;
+    }
+    __syncwarp();
+    // ... and those: p * (load + dp - dot), dp = dw, or (dw - s/z) sum/z.
+    auto put = [&](int e, float ex, float dw) {
+      const float dp = a.normalize ? (dw - mean_d) * rz * v[0] : dw;
+      from_f(mine[e], ex * inv * (s_load[e] + dp - dot));
+    };
+    if (any && e0 >= 0) put(e0, ex0, d);
+    if (any && picks)
+      for (int j = l + LPT; j < a.top_k; j += LPT) {
+        int e;
+        float dw, logit;
+        choice(j, e, dw, logit);
+        if (e >= 0) put(e, __expf(logit - m), dw);
+      }
+    __syncwarp();
     if (in) {
       T* out = static_cast<T*>(a.dlogits) + t * a.lddx + first;
-      constexpr int W = 16 / sizeof(T);
       if (a.vec && first + EPL <= a.experts) {
 #pragma unroll
-        for (int j = 0; j < EPL; j += W) {
-          Vec16<T> v;
-#pragma unroll
-          for (int i = 0; i < W; ++i) from_f(v.e[i], any ? x[j + i] * (g[j + i] - dot) : 0.0f);
-          *reinterpret_cast<Vec16<T>*>(out + j) = v;
-        }
+        for (int j = 0; j < EPL; j += W)
+          *reinterpret_cast<Vec16<T>*>(out + j) = *reinterpret_cast<const Vec16<T>*>(mine + first + j);
       } else {
 #pragma unroll
         for (int i = 0; i < EPL; ++i)
-          if (first + i < a.experts) from_f(out[i], any ? x[i] * (g[i] - dot) : 0.0f);
+          if (first + i < a.experts) out[i] = mine[first + i];
       }
     }
+    __syncwarp();
   }
 }
 
