@@ -15,6 +15,7 @@ torch tensors, allocating outputs with torch.
 from __future__ import annotations
 
 import ctypes
+import itertools
 import os
 import struct
 from dataclasses import dataclass
@@ -395,9 +396,15 @@ def mx_router_backward(logits, ld, dtype, token_mask, tokens, tokens_per_seq, n_
 # torch-tensor wrappers
 # ---------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t) -> Optional[int]:
@@ -405,9 +412,12 @@ def _ptr(t) -> Optional[int]:
 
 
 def _stream(stream) -> Optional[int]:
-    torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # The current stream of the current device, without building a Stream object
+    # (3 us of a call's 10 on the host).
+    c = _torch()._C
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 @dataclass
@@ -812,40 +822,46 @@ def adamw_step(params, grads, states, lr: float, betas=(0.9, 0.999), eps: float 
     assert len(grads) == n and len(states) == n, "one gradient and one state per parameter"
     if n == 0:
         return
+    f32, bf16 = torch.float32, torch.bfloat16
     bits = states[0].bits
     decay = weight_decay if isinstance(weight_decay, (list, tuple)) else [weight_decay] * n
-    assert len(decay) == n
-    f32, bf16 = torch.float32, torch.bfloat16
-    flat = []
-    for p, g, s, wd in zip(params, grads, states, decay):
-        k = p.numel()
-        m, v = s.exp_avg, s.exp_avg_sq
-        assert s.bits == bits, "all states of one call have the same bits"
-        assert p.dtype is f32 and p.is_cuda and p.is_contiguous(), "parameters: contiguous FP32 CUDA tensors"
-        assert (g.dtype is bf16 or g.dtype is f32) and g.is_cuda and g.is_contiguous() and g.numel() == k, \
-            "gradients: contiguous FP32 or BF16 CUDA tensors of the parameters' sizes"
-        assert m.numel() == k and v.numel() == k and m.is_contiguous() and v.is_contiguous()
-        if bits == 8:
-            a, b = s.exp_avg_scale, s.exp_avg_sq_scale
-            blocks = (k + MX_ADAMW_STATE_BLOCK - 1) // MX_ADAMW_STATE_BLOCK
-            assert m.element_size() == 1 and v.element_size() == 1
-            assert a.dtype is f32 and b.dtype is f32 and a.numel() >= blocks and b.numel() >= blocks
-            flat += (p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), a.data_ptr(), b.data_ptr(), k, wd,
-                     g.dtype is f32, 0)
-        else:
-            assert m.dtype is f32 and v.dtype is f32
-            flat += (p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), 0, 0, k, wd, g.dtype is f32, 0)
+    # Attribute by attribute over all tensors rather than tensor by tensor: a
+    # step over many small tensors is bound by this function.
+    T = torch.Tensor
+    tensors = [*params, *grads, *[s.exp_avg for s in states], *[s.exp_avg_sq for s in states]]
+    size, ptr, dtype = (list(map(f, tensors)) for f in (T.numel, T.data_ptr, T.dtype.__get__))
+    kinds = set(dtype[n:2 * n])
+    assert len(decay) == n and all([s.bits == bits for s in states]), "all states of one call have the same bits"
+    assert set(dtype[:n]) == {f32}, "parameters: FP32"
+    assert kinds <= {f32, bf16}, "gradients: FP32 or BF16"
+    assert size == size[:n] * 4, "gradients and states: of the parameters' sizes"
+    if bits == 8:
+        scales = [*[s.exp_avg_scale for s in states], *[s.exp_avg_sq_scale for s in states]]
+        assert {t.itemsize for t in set(dtype[2 * n:])} == {1}, "8-bit states: one byte an element"
+        assert set(map(T.dtype.__get__, scales)) == {f32}, "scales: FP32"
+        assert all([k >= (m + MX_ADAMW_STATE_BLOCK - 1) // MX_ADAMW_STATE_BLOCK
+                    for k, m in zip(map(T.numel, scales), size[2 * n:])]), "scales: one per block"
+        tensors += scales
+        ptr += map(T.data_ptr, scales)
+    else:
+        assert set(dtype[2 * n:]) == {f32}, "32-bit states: FP32"
+        ptr += [0] * (2 * n)
+    assert all(map(T.is_contiguous, tensors)) and all(map(T.is_cuda.__get__, tensors)), "contiguous CUDA tensors"
     if grad_scale is not None:
         assert grad_scale.dtype is f32 and grad_scale.is_cuda and grad_scale.numel() == 1
+    g32 = [0] * n if kinds == {bf16} else [int(t is f32) for t in dtype[n:2 * n]]
+    rows = zip(*[ptr[k * n:(k + 1) * n] for k in range(6)], size, decay, g32, [0] * n)
     hyper = MXAdamWHyperC(lr, betas[0], betas[1], eps, step, seed & 0xFFFFFFFF, 0)
-    mx_adamw_step(struct.pack(_ADAMW_TENSOR * n, *flat), n, bits, hyper, _ptr(grad_scale), _ptr(status),
-                  _stream(stream))
+    mx_adamw_step(struct.pack(_ADAMW_TENSOR * n, *itertools.chain.from_iterable(rows)), n, bits, hyper, _ptr(grad_scale),
+                  _ptr(status), _stream(stream))
 
 
 def _rows(t) -> int:
     """Pitch of a 2-D matrix with contiguous rows."""
-    assert t.dim() == 2 and t.is_cuda and (t.stride(1) == 1 or t.shape[1] <= 1), "needs 2-D CUDA tensors with contiguous rows"
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    R, C = t.shape
+    p, q = t.stride()
+    assert t.is_cuda and (q == 1 or C <= 1), "needs 2-D CUDA tensors with contiguous rows"
+    return p if R > 1 else C
 
 
 def _params(weight, bias, cols) -> int:
@@ -868,14 +884,16 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, center: bool = True
     torch = _torch()
     R, C = x.shape
     dev = x.device
-    dtype, pd, ldx = _dtype(x), _params(weight, bias, C), _rows(x)
+    dtype, pd, ldx, ldy = _dtype(x), _params(weight, bias, C), _rows(x), C
     if out is None:
         out = torch.empty((R, C), dtype=x.dtype, device=dev)
-    assert out.dtype == x.dtype and out.shape == x.shape
+    else:
+        assert out.dtype == x.dtype and out.shape == x.shape
+        ldy = _rows(out)
     mean = torch.empty(R, dtype=torch.float32, device=dev) if stats and center else None
     rstd = torch.empty(R, dtype=torch.float32, device=dev) if stats else None
-    mx_layer_norm(x.data_ptr(), ldx, _ptr(weight), _ptr(bias), pd, R, C, eps, int(center), dtype, out.data_ptr(),
-                  _rows(out), _ptr(mean), _ptr(rstd), _ptr(status), _stream(stream))
+    mx_layer_norm(x.data_ptr(), ldx, _ptr(weight), _ptr(bias), pd, R, C, eps, int(center), dtype, out.data_ptr(), ldy,
+                  _ptr(mean), _ptr(rstd), _ptr(status), _stream(stream))
     return out, mean, rstd
 
 
@@ -914,19 +932,26 @@ def gemm_epilogue(mode: int, a: MXTensor, b: MXTensor, bias=None, act: str = "no
     M, N = a.rows, b.rows
     dev = a.data.device
     bf16 = torch.bfloat16
+
+    def pitch(t):
+        assert t.dtype == bf16 and t.shape == (M, N), "out, residual and preact: BF16 [M, N]"
+        return _rows(t)
+
+    ldc, ldr, ldz = N, 0 if residual is None else pitch(residual), N
     if out is None:
         out = torch.empty((M, N), dtype=bf16, device=dev)
-    if preact is None and keep_preact:
+    else:
+        ldc = pitch(out)
+    if preact is not None:
+        ldz = pitch(preact)
+    elif keep_preact:
         preact = torch.empty((M, N), dtype=bf16, device=dev)
-    for t in (out, residual, preact):
-        assert t is None or (t.dtype == bf16 and t.shape == (M, N)), "out, residual and preact: BF16 [M, N]"
     bd = MX_F32
     if bias is not None:
         assert bias.is_cuda and bias.is_contiguous() and bias.numel() == N, "bias: contiguous, one entry per column"
         bd = _dtype(bias)
-    e = MXEpilogueC(_ptr(bias), _ptr(residual), _ptr(preact), 0 if residual is None else _rows(residual),
-                    0 if preact is None else _rows(preact), bd, ACTIVATIONS[act])
-    mx_gemm_epilogue(mode, a.c_operand(), b.c_operand(), e, out.data_ptr(), _rows(out), _ptr(status), _stream(stream))
+    e = MXEpilogueC(_ptr(bias), _ptr(residual), _ptr(preact), ldr, ldz, bd, ACTIVATIONS[act])
+    mx_gemm_epilogue(mode, a.c_operand(), b.c_operand(), e, out.data_ptr(), ldc, _ptr(status), _stream(stream))
     return out, preact
 
 
@@ -938,9 +963,12 @@ def epilogue_backward(dy, preact, act: str = "none", bias_grad: bool = True, dz=
     M, N = dy.shape
     a = ACTIVATIONS[act]
     assert a == MX_ACT_NONE or (preact.dtype == torch.bfloat16 and preact.shape == dy.shape), "preact: BF16, of dy's shape"
+    lddz = N
     if dz is None:
         dz = torch.empty((M, N), dtype=torch.bfloat16, device=dy.device)
-    assert dz.dtype == torch.bfloat16 and dz.shape == dy.shape
+    else:
+        assert dz.dtype == torch.bfloat16 and dz.shape == dy.shape
+        lddz = _rows(dz)
     dbias = ws = None
     need = 0
     if bias_grad:
@@ -948,7 +976,7 @@ def epilogue_backward(dy, preact, act: str = "none", bias_grad: bool = True, dz=
         need = mx_epilogue_backward_workspace_bytes(M, N)
         ws = torch.empty(need, dtype=torch.uint8, device=dy.device) if need else None
     mx_epilogue_backward(dy.data_ptr(), _rows(dy), _ptr(preact), 0 if preact is None else _rows(preact), M, N, a,
-                         dz.data_ptr(), _rows(dz), _ptr(dbias), _ptr(ws), need, _ptr(status), _stream(stream))
+                         dz.data_ptr(), lddz, _ptr(dbias), _ptr(ws), need, _ptr(status), _stream(stream))
     return dz, dbias
 
 
@@ -976,17 +1004,19 @@ def router_forward(logits, top_k: int, tokens_per_seq: Optional[int] = None, tok
     seq = max(T, 1) if tokens_per_seq is None else tokens_per_seq
     assert seq >= 1 and 1 <= top_k <= E
     mask = _mask(token_mask, T)
-    seqs = (T + seq - 1) // seq
-    f32 = dict(dtype=torch.float32, device=dev)
-    i64 = torch.empty(2 * E + 1, dtype=torch.int64, device=dev)
-    r = Routing(torch.empty((T, top_k), dtype=torch.int32, device=dev), torch.empty((T, top_k), **f32), i64[:E], i64[E:],
-                torch.empty((seqs, E), **f32), torch.empty(1, **f32))
+    empty, f32, i64 = torch.empty, torch.float32, torch.int64
+    indices = empty((T, top_k), dtype=torch.int32, device=dev)
+    weights = empty((T, top_k), dtype=f32, device=dev)
+    counts = empty(E, dtype=i64, device=dev)
+    offsets = empty(E + 1, dtype=i64, device=dev)
+    load = empty(((T + seq - 1) // seq, E), dtype=f32, device=dev)
+    loss = empty(1, dtype=f32, device=dev)
     need = mx_router_workspace_bytes(T, seq, E)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws = empty(need, dtype=torch.uint8, device=dev)
     mx_router_forward(logits.data_ptr(), _rows(logits), _dtype(logits), mask, T, seq, E, top_k, int(normalize), coef,
-                      r.indices.data_ptr(), r.weights.data_ptr(), r.counts.data_ptr(), r.group_offsets.data_ptr(),
-                      r.load.data_ptr(), r.loss.data_ptr(), ws.data_ptr(), need, _ptr(status), _stream(stream))
-    return r
+                      indices.data_ptr(), weights.data_ptr(), counts.data_ptr(), offsets.data_ptr(), load.data_ptr(),
+                      loss.data_ptr(), ws.data_ptr(), need, _ptr(status), _stream(stream))
+    return Routing(indices, weights, counts, offsets, load, loss)
 
 
 def _mask(token_mask, tokens) -> Optional[int]:

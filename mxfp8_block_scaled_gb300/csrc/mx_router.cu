@@ -41,7 +41,7 @@ namespace {
 
 constexpr int kRouterWarps = 8;
 constexpr int kRouterThreads = 32 * kRouterWarps;
-constexpr int kTargetCtas = 1216;  // eight per SM of GB300; a constant, so the workspace's size needs no device
+constexpr int kTargetCtas = 608;   // four per SM of GB300; a constant, so the workspace's size needs no device
 constexpr int kMinChunk = 32;      // tokens of a CTA at least
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
@@ -130,11 +130,20 @@ __device__ __forceinline__ void load_row(const T* row, int first, int experts, b
   }
 }
 
-// A logit as an unsigned number of the same order, above 0; 0 for what is not
-// to be chosen (-inf, NaN). -0 counts as +0.
+// A logit as an unsigned number of the same order; -0 counts as +0. -inf (and a
+// NaN with its sign bit set) gives at most kNoKey, every number more; other
+// NaNs come out above +inf.
+constexpr uint32_t kNoKey = 0x007FFFFFu, kInfKey = 0xFF800000u;
 __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t b = __float_as_uint(x + 0.0f);
-  return x > -INFINITY ? b ^ (static_cast<int32_t>(b) < 0 ? 0xFFFFFFFFu : 0x80000000u) : 0u;
+  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+
+// exp(x) for x <= 0 with results below 2^-126 flushed to zero.
+__device__ __forceinline__ float exp_of(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.4426950408889634f));
+  return r;
 }
 
 __device__ __forceinline__ void order_pair(uint32_t& a, uint32_t& b) {
@@ -174,7 +183,7 @@ __device__ __forceinline__ Run run_of(const RouterArgs& a) {
 }
 
 template <typename T, int LPT, int EPL>
-__global__ void __launch_bounds__(kRouterThreads) router_forward_kernel(const RouterArgs a) {
+__global__ void __launch_bounds__(kRouterThreads, EPL == 8 ? 4 : 2) router_forward_kernel(const RouterArgs a) {
   constexpr int TPW = 32 / LPT;   // tokens of a warp at a time
   constexpr int E = LPT * EPL;    // experts that fit
   // A packed key: the logit's key without its lowest bits, which hold E - 1 -
@@ -199,102 +208,111 @@ __global__ void __launch_bounds__(kRouterThreads) router_forward_kernel(const Ro
 #pragma unroll
   for (int i = 0; i < EPL; ++i) psum[i] = 0.0f;
   int32_t valid = 0;
+  // The next token's row is on its way while this one is worked on.
+  float ahead[EPL];
+  bool live_ahead;
+  auto fetch = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) ahead[i] = -INFINITY;
+    live_ahead = t < run.end && (!a.mask || a.mask[t] != 0);
+    if (live_ahead) load_row<T, EPL>(static_cast<const T*>(a.logits) + t * a.ld, first, a.experts, a.vec, ahead);
+  };
+  fetch(run.first + warp * TPW + sub);
   for (int64_t t0 = run.first + warp * TPW; t0 < run.end; t0 += kRouterWarps * TPW) {
     const int64_t t = t0 + sub;
     const bool in = t < run.end;
-    const bool live = in && (!a.mask || a.mask[t] != 0);
     const T* row = static_cast<const T*>(a.logits) + t * a.ld;
     int32_t* idx = a.indices + t * a.top_k;
-    float x[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) x[i] = -INFINITY;
-    if (live) load_row<T, EPL>(row, first, a.experts, a.vec, x);
+    float x[EPL];  // a token left out is -inf throughout
     uint32_t key[EPL];
+    float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const uint32_t k = order_key(x[i]);
-      key[i] = k ? (k & ~kLow) | (kLow - static_cast<uint32_t>(first + i)) : 0u;
+      x[i] = ahead[i];
+      m = fmaxf(m, x[i]);
+      key[i] = (order_key(x[i]) & ~kLow) | (kLow - static_cast<uint32_t>(first + i));
     }
+    const bool live = live_ahead;
+    fetch(t + kRouterWarps * TPW);
+#pragma unroll
+    for (int o = LPT / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
     sort_keys<EPL>(key);
     uint32_t top = 0, last = 0;
     int32_t found = 0, mine = -1;  // choices made; the one of round j % LPT == l (kept where top_k <= LPT)
-    bool close = false;
+    bool again = false;
     for (int j = 0; j < a.top_k; ++j) {
       const uint32_t best = group_max<LPT>(key[0]);
       if (j == 0) top = best;
-      else if (!kExact) close |= best != 0 && ((best ^ last) & ~kLow) == 0;
+      else if (!kExact) again |= ((best ^ last) & ~kLow) == 0;
       last = best;
-      if (best != 0) {
+      if (best > kNoKey) {
         found = j + 1;
         if (j % LPT == l) {
           mine = static_cast<int32_t>(kLow - (best & kLow));
           idx[j] = mine;
         }
-        if (key[0] == best) {  // one lane: keys differ by their experts
+      }
+      if (key[0] == best) {  // one lane: keys differ by their experts
 #pragma unroll
-          for (int i = 0; i + 1 < EPL; ++i) key[i] = key[i + 1];
-          key[EPL - 1] = 0;
-        }
+        for (int i = 0; i + 1 < EPL; ++i) key[i] = key[i + 1];
+        key[EPL - 1] = 0;
       }
     }
-    if constexpr (!kExact) {
-      // The first one not chosen may be as close to the last one chosen.
-      const uint32_t next = group_max<LPT>(key[0]);
-      close |= next != 0 && last != 0 && ((next ^ last) & ~kLow) == 0;
-      if (__any_sync(kFull, close)) {
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) key[i] = order_key(x[i]);
-        for (int j = 0; j < a.top_k; ++j) {
-          uint32_t best = 0;
-          int at = 0;
-#pragma unroll
-          for (int i = 0; i < EPL; ++i)
-            if (key[i] > best) {
-              best = key[i];
-              at = i;
-            }
-          const uint32_t most = group_max<LPT>(best);
-          const uint32_t who = group_min<LPT>(best == most ? static_cast<uint32_t>(first + at) : kFull);
-          if (most != 0) {
-            if (j % LPT == l) {
-              mine = static_cast<int32_t>(who);
-              idx[j] = mine;
-            }
-#pragma unroll
-            for (int i = 0; i < EPL; ++i)
-              if (who == static_cast<uint32_t>(first + i)) key[i] = 0;
-          }
-        }
-      }
-    }
-    // A row without a key is left out, unless a NaN is why.
-    bool any = top != 0;
-    if (__any_sync(kFull, live && !any)) {
+    // The first one not chosen may be as close to the last one chosen.
+    if (!kExact) again |= ((group_max<LPT>(key[0]) ^ last) & ~kLow) == 0;
+    bool any = top > kNoKey;
+    // Once more with whole keys, if rounding or a NaN may have changed the
+    // choice (a row of -inf alone does not count).
+    again = (again && any) || top >= kInfKey;
+    if (__any_sync(kFull, again || (live && !any))) {
       bool nan = false;
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) nan |= x[i] != x[i];
+      for (int i = 0; i < EPL; ++i) {
+        nan |= x[i] != x[i];
+        key[i] = x[i] > -INFINITY ? order_key(x[i]) : 0u;
+      }
       any |= group_max<LPT>(nan ? 1u : 0u) != 0;
+      found = 0;
+      for (int j = 0; j < a.top_k; ++j) {
+        uint32_t best = 0;
+        int at = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (key[i] > best) {
+            best = key[i];
+            at = i;
+          }
+        const uint32_t most = group_max<LPT>(best);
+        const uint32_t who = group_min<LPT>(best == most ? static_cast<uint32_t>(first + at) : kFull);
+        if (most != 0) {
+          found = j + 1;
+          if (j % LPT == l) {
+            mine = static_cast<int32_t>(who);
+            idx[j] = mine;
+          }
+#pragma unroll
+          for (int i = 0; i < EPL; ++i)
+            if (who == static_cast<uint32_t>(first + i)) key[i] = 0;
+        }
+      }
     }
-    float m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) m = fmaxf(m, x[i]);
-#pragma unroll
-    for (int o = LPT / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    if (!any) m = 0.0f;  // the row's exponentials are then zero
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      x[i] = __expf(x[i] - m);
+      x[i] = exp_of(x[i] - m);
       sum += x[i];
     }
-    const float inv = __frcp_rn(group_sum<LPT>(sum));
+    sum = group_sum<LPT>(sum);
+    const float inv = any ? __frcp_rn(sum) : 0.0f;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) psum[i] += any ? x[i] * inv : 0.0f;
+    for (int i = 0; i < EPL; ++i) psum[i] = fmaf(x[i], inv, psum[i]);
     valid += any;
     // The chosen weights: lane j % LPT takes choice j and computes its p from the logit.
     float chosen = 0.0f, p = 0.0f;
     for (int j = l; j < found; j += LPT) {
       const int e = a.top_k <= LPT ? mine : idx[j];
-      p = __expf(to_f(row[e]) - m) * inv;
+      p = exp_of(to_f(row[e]) - m) * inv;
       chosen += p;
       atomicAdd(&s_n[e], 1);
     }
@@ -306,7 +324,7 @@ __global__ void __launch_bounds__(kRouterThreads) router_forward_kernel(const Ro
           idx[j] = -1;
           w[j] = 0.0f;
         } else {
-          if (a.top_k > LPT) p = __expf(to_f(row[idx[j]]) - m) * inv;
+          if (a.top_k > LPT) p = exp_of(to_f(row[idx[j]]) - m) * inv;
           w[j] = a.normalize ? __fdiv_rn(p, scale) : p;
         }
       }
@@ -406,59 +424,68 @@ __global__ void __launch_bounds__(1024) router_sequence_kernel(const RouterSums 
   }
 }
 
-// Loads of every sequence (all CTAs); counts, offsets and loss (CTA 0).
-__global__ void __launch_bounds__(512) router_finish_kernel(const RouterSums a) {
-  __shared__ int32_t s_live[16];
-  __shared__ float s_loss[16];
-  __shared__ int64_t s_scan[512];
+// Loads of every sequence (each CTA takes every gridDim-th one of G at a time);
+// counts, offsets and loss (CTA 0, over all of them). A thread has one expert.
+__global__ void __launch_bounds__(1024) router_finish_kernel(const RouterSums a, int width) {
+  __shared__ int32_t s_live[32];
+  __shared__ float s_loss[32];
+  __shared__ int64_t s_count[1024];
+  __shared__ int64_t s_warp[32];
   pdl_launch_dependents();
   pdl_wait();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // width: a power of two at least the number of experts
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, e = tid & (width - 1), g = tid / width, G = 1024 / width;
   int32_t live = 0;
-  for (int64_t s = tid; s < a.seqs; s += 512) live += a.seq_v[s] > 0;
+  for (int64_t s = tid; s < a.seqs; s += 1024) live += a.seq_v[s] > 0;
   live = __reduce_add_sync(kFull, live);
   if (lane == 0) s_live[warp] = live;
   __syncthreads();
-  live = 0;
-  for (int w = 0; w < 16; ++w) live += s_live[w];
+  live = __reduce_add_sync(kFull, s_live[lane]);
   const float factor = a.coef * (static_cast<float>(a.experts) / (static_cast<float>(a.top_k) * static_cast<float>(max(live, 1))));
-  const int64_t total = a.seqs * a.experts;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 512 + tid; i < total; i += static_cast<int64_t>(gridDim.x) * 512) {
-    const int64_t s = i / a.experts, e = i % a.experts;
-    const float n = static_cast<float>(max(a.seq_v[s], 1));
-    a.load[i] = factor * static_cast<float>(a.seq_n[s * a.pitch + e]) / (n * n);
-  }
-  if (blockIdx.x != 0) return;
   float loss = 0.0f;
   int64_t count = 0;
-  if (tid < a.experts) {
+  if (e < a.experts) {
+    const bool all = blockIdx.x == 0;  // CTA 0 also needs the other CTAs' sequences
 #pragma unroll 4
-    for (int64_t s = 0; s < a.seqs; ++s) {
+    for (int64_t s = all ? g : g + static_cast<int64_t>(blockIdx.x) * G; s < a.seqs; s += all ? G : static_cast<int64_t>(gridDim.x) * G) {
       const float n = static_cast<float>(max(a.seq_v[s], 1));
-      const int32_t hit = a.seq_n[s * a.pitch + tid];
-      count += hit;
-      loss += factor * static_cast<float>(hit) / (n * n) * a.seq_p[s * a.pitch + tid];
+      const int32_t hit = a.seq_n[s * a.pitch + e];
+      const float load = factor * static_cast<float>(hit) / (n * n);
+      if (!all || s / G % gridDim.x == 0) a.load[s * a.experts + e] = load;
+      if (all) {
+        count += hit;
+        loss = fmaf(load, a.seq_p[s * a.pitch + e], loss);
+      }
     }
-    a.counts[tid] = count;
   }
+  if (blockIdx.x != 0) return;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(kFull, loss, o);
   if (lane == 0) s_loss[warp] = loss;
-  s_scan[tid] = count;
+  s_count[tid] = count;
   __syncthreads();
-  for (int o = 1; o < 512; o <<= 1) {
-    const int64_t before = tid >= o ? s_scan[tid - o] : 0;
-    __syncthreads();
-    s_scan[tid] += before;
-    __syncthreads();
-  }
-  if (tid < a.experts) a.offsets[tid + 1] = s_scan[tid];
   if (tid == 0) {
-    a.offsets[0] = 0;
     loss = 0.0f;
-    for (int w = 0; w < 16; ++w) loss += s_loss[w];
+    for (int w = 0; w < 32; ++w) loss += s_loss[w];
     *a.loss = loss;
+    a.offsets[0] = 0;
   }
+  // Experts' totals and their running sums: over the lanes, then over the warps.
+  count = 0;
+  if (tid < a.experts) {
+    for (int q = 0; q < G; ++q) count += s_count[q * width + tid];
+    a.counts[tid] = count;
+  }
+  int64_t run = count;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int64_t before = __shfl_up_sync(kFull, run, o);
+    if (lane >= o) run += before;
+  }
+  if (lane == 31) s_warp[warp] = run;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) run += s_warp[w];
+  if (tid < a.experts) a.offsets[tid + 1] = run;
 }
 
 // Sums of four values over a group, to all of its lanes: two halving steps, then
@@ -531,11 +558,11 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const R
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // sum(e), sum(e load), z, s
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      x[i] = __expf(x[i] - m);
+      x[i] = exp_of(x[i] - m);
       v[0] += x[i];
       v[1] = fmaf(x[i], load[i], v[1]);
     }
-    const float ex0 = e0 >= 0 ? __expf(x0 - m) : 0.0f;
+    const float ex0 = e0 >= 0 ? exp_of(x0 - m) : 0.0f;
     if (e0 >= 0) {
       v[2] = ex0;
       v[3] = ex0 * d;
@@ -546,7 +573,7 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const R
         float dw, logit;
         choice(j, e, dw, logit);
         if (e >= 0) {
-          const float ex = __expf(logit - m);
+          const float ex = exp_of(logit - m);
           v[2] += ex;
           v[3] = fmaf(ex, dw, v[3]);
         }
@@ -586,7 +613,7 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const R
         int e;
         float dw, logit;
         choice(j, e, dw, logit);
-        if (e >= 0) put(e, __expf(logit - m), dw);
+        if (e >= 0) put(e, exp_of(logit - m), dw);
       }
     __syncwarp();
     if (in) {
@@ -695,8 +722,10 @@ mx_status launch_router_forward(const RouterLaunch& L, cudaStream_t s) {
   st = cuda_status(launch_kernel(router_sequence_kernel, static_cast<unsigned>(p.seqs), 1024, 0, s, 1, q),
                    "mx_router launch (sequences)");
   if (st != MX_OK) return st;
-  const int64_t grid = std::min<int64_t>(sm_count(), (p.seqs * L.experts + 2047) / 2048);
-  return cuda_status(launch_kernel(router_finish_kernel, static_cast<unsigned>(grid), 512, 0, s, 1, q),
+  int width = 32;
+  while (width < L.experts) width *= 2;
+  const int64_t grid = std::min<int64_t>(sm_count(), (p.seqs * width + 8191) / 8192);
+  return cuda_status(launch_kernel(router_finish_kernel, static_cast<unsigned>(grid), 1024, 0, s, 1, q, width),
                      "mx_router launch (loss)");
 }
 
