@@ -568,7 +568,6 @@ mx_status mx_gemm_epilogue(int mode, const mx_operand* a, const mx_operand* b, c
   L.epi.ld_residual = e.ld_residual;
   L.epi.ld_preact = e.ld_preact;
   L.epi.bias_f32 = e.bias_dtype == MX_F32;
-  L.epi.bias_vec = aligned16(e.bias);
   L.epi.act = e.act;
   if (L.M == 0 || L.N == 0) return MX_OK;
   st = check_device();

@@ -27,10 +27,36 @@ namespace {
 constexpr int kRowLanes = 8;      // a CTA is 32 column lanes x 8 row lanes
 constexpr int kTargetCtas = 1216; // eight per SM of GB300; a constant, so the workspace's size needs no device
 
+// V neighbouring BF16 elements (8 as one 16-byte access, or 1) as FP32 pairs.
 template <int V>
-struct alignas(2 * V) Half {
-  __nv_bfloat16 e[V];
+struct Piece;
+template <>
+struct Piece<8> {
+  uint4 w;
+  __device__ __forceinline__ float2 pair(int i) const {
+    const uint32_t v = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ void set(int i, float2 v) {
+    const __nv_bfloat162 h = __float22bfloat162_rn(v);
+    (i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w) = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  __device__ __forceinline__ void put(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = w; }
 };
+template <>
+struct Piece<1> {
+  __nv_bfloat16 e;
+  __device__ __forceinline__ float2 pair(int) const { return make_float2(__bfloat162float(e), 0.0f); }
+  __device__ __forceinline__ void set(int, float2 v) { e = __float2bfloat16_rn(v.x); }
+  __device__ __forceinline__ void put(__nv_bfloat16* p) const { *p = e; }
+};
+template <int V>
+__device__ __forceinline__ Piece<V> piece_at(const __nv_bfloat16* p) {
+  Piece<V> r;
+  if constexpr (V == 8) r.w = *reinterpret_cast<const uint4*>(p);
+  else r.e = *p;
+  return r;
+}
 
 struct EpiBackwardArgs {
   const __nv_bfloat16* dy;
@@ -49,42 +75,46 @@ __global__ void __launch_bounds__(32 * kRowLanes) epilogue_backward_kernel(const
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + tx) * V;
   const int nv = static_cast<int>(min64(V, a.cols - c));
-  float sum[V];
+  constexpr int P = (V + 1) / 2;
+  float2 sum[P];
 #pragma unroll
-  for (int i = 0; i < V; ++i) sum[i] = 0.0f;
+  for (int i = 0; i < P; ++i) sum[i] = act_pair(0.0f);
   if (nv == V) {
 #pragma unroll 4
     for (int64_t row = static_cast<int64_t>(blockIdx.y) * kRowLanes + ty; row < a.rows;
          row += static_cast<int64_t>(gridDim.y) * kRowLanes) {
-      const Half<V> d = *reinterpret_cast<const Half<V>*>(a.dy + row * a.lddy + c);
-      Half<V> z, o;
-      if (kAct != MX_ACT_NONE) z = *reinterpret_cast<const Half<V>*>(a.z + row * a.ldz + c);
+      const Piece<V> d = piece_at<V>(a.dy + row * a.lddy + c);
+      Piece<V> z = {}, o;
+      if (kAct != MX_ACT_NONE) z = piece_at<V>(a.z + row * a.ldz + c);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float g = kAct == MX_ACT_NONE ? __bfloat162float(d.e[i])
-                                            : __bfloat162float(d.e[i]) * act_slope<kAct>(__bfloat162float(z.e[i]));
-        sum[i] += g;
-        o.e[i] = __float2bfloat16_rn(g);
+      for (int i = 0; i < P; ++i) {
+        float2 g = d.pair(i);
+        if (kAct != MX_ACT_NONE) g = __fmul2_rn(g, act_slope<kAct>(z.pair(i)));
+        sum[i] = __fadd2_rn(sum[i], g);
+        o.set(i, g);
       }
-      if (a.dz) *reinterpret_cast<Half<V>*>(a.dz + row * a.lddz + c) = o;
+      if (a.dz) o.put(a.dz + row * a.lddz + c);
     }
-  } else if (nv > 0) {
+  } else if (nv > 0) {  // the last columns of a width that is no multiple of V
     for (int64_t row = static_cast<int64_t>(blockIdx.y) * kRowLanes + ty; row < a.rows;
          row += static_cast<int64_t>(gridDim.y) * kRowLanes) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         if (i < nv) {
-          float g = __bfloat162float(a.dy[row * a.lddy + c + i]);
-          if (kAct != MX_ACT_NONE) g *= act_slope<kAct>(__bfloat162float(a.z[row * a.ldz + c + i]));
-          sum[i] += g;
-          if (a.dz) a.dz[row * a.lddz + c + i] = __float2bfloat16_rn(g);
+          const Piece<1> d = piece_at<1>(a.dy + row * a.lddy + c + i);
+          float2 g = d.pair(0);
+          if (kAct != MX_ACT_NONE) g = __fmul2_rn(g, act_slope<kAct>(piece_at<1>(a.z + row * a.ldz + c + i).pair(0)));
+          (i & 1 ? sum[i / 2].y : sum[i / 2].x) += g.x;
+          Piece<1> o;
+          o.set(0, g);
+          if (a.dz) o.put(a.dz + row * a.lddz + c + i);
         }
       }
     }
   }
   if (!a.partial) return;
 #pragma unroll
-  for (int i = 0; i < V; ++i) s[ty][tx * V + i] = sum[i];
+  for (int i = 0; i < V; ++i) s[ty][tx * V + i] = i & 1 ? sum[i / 2].y : sum[i / 2].x;
   __syncthreads();
   for (int j = threadIdx.x; j < 32 * V; j += 32 * kRowLanes) {
     const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 * V + j;
@@ -109,7 +139,7 @@ __global__ void __launch_bounds__(256) epilogue_only_kernel(const GemmEpilogue e
       z = e.bias_f32 ? static_cast<const float*>(e.bias)[col]
                      : __bfloat162float(static_cast<const __nv_bfloat16*>(e.bias)[col]);
     if (e.preact) static_cast<__nv_bfloat16*>(e.preact)[row * e.ld_preact + col] = __float2bfloat16_rn(z);
-    z = act_value<kAct>(z);
+    z = act_value<kAct>(act_pair(z)).x;
     if (e.residual) z += __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[row * e.ld_residual + col]);
     c[row * ldc + col] = __float2bfloat16_rn(z);
   }

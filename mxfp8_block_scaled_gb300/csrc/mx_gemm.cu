@@ -89,6 +89,7 @@ constexpr int kMaxGroups = MX_MAX_GROUPS;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kEpiWarpBytes = 32 * 64;  // one 32-row x 32-column BF16 box per epilogue warp
 constexpr int kEpiBytes = 8 * kEpiWarpBytes;
+constexpr int kEpiBiasBytes = 8 * 128 * 4;  // 128 FP32 bias entries per epilogue warp
 
 // Epilogue write-out: 0 = TMA tensor stores from the staging box (asynchronous:
 // the warp stages the next box while the previous one drains; 2-8% faster on
@@ -138,13 +139,15 @@ struct Cfg {
 #ifndef MX_PAIR_EPI_BUFS
 #define MX_PAIR_EPI_BUFS 1
 #endif
-template <int BN_, bool kTS_, bool kGrouped_>
+// kEpi (bias / activation / residual epilogue): a stage less makes room for two
+// staging boxes per epilogue warp and its bias.
+template <int BN_, bool kTS_, bool kGrouped_, bool kEpi_ = false>
 struct PairCfgT {
   static constexpr int BN = BN_;
   static constexpr bool kTS = kTS_;
   static_assert(BN == 256, "pair tiles are 256 wide");
-  static constexpr int kStages = MX_PAIR_STAGES;
-  static constexpr int kEpiBufs = MX_PAIR_EPI_BUFS;  // staging boxes per epilogue warp
+  static constexpr int kStages = kEpi_ ? MX_PAIR_STAGES - 1 : MX_PAIR_STAGES;
+  static constexpr int kEpiBufs = kEpi_ ? 2 : MX_PAIR_EPI_BUFS;  // staging boxes per epilogue warp
   static constexpr int kABytes = kBM * kBK;
   static constexpr int kBBytes = (BN / 2) * kBK;
   static constexpr int kSfaBytes = kTS ? 0 : 512;
@@ -158,13 +161,16 @@ struct PairCfgT {
   static constexpr int kGroupBytes = 3 * (kMaxGroups + 1) * 4;
   __host__ __device__ static constexpr size_t smem_bytes() {
     return 1024 + static_cast<size_t>(kStages) * kStageTx + kEpiBufs * kEpiBytes + kBarBytes +
-           (kGrouped_ ? kGroupBytes : 0);
+           (kGrouped_ ? kGroupBytes : 0) + (kEpi_ ? kEpiBiasBytes : 0);
   }
 };
 // The configuration bookkeeping that does not depend on the tile width.
 using PairCfg = PairCfgT<256, false, false>;
 static_assert(PairCfgT<256, false, true>::smem_bytes() <= 232448, "shared memory");
 static_assert(PairCfgT<256, true, true>::smem_bytes() <= 232448, "shared memory");
+static_assert(PairCfgT<256, false, false, true>::smem_bytes() <= 232448, "shared memory");
+static_assert(Cfg<128>::smem_bytes(false) + kEpiBiasBytes <= 232448, "shared memory");
+static_assert(Cfg<256>::smem_bytes(false) + kEpiBiasBytes <= 232448, "shared memory");
 
 struct GParams {
   const uint8_t* a_scale;
@@ -746,8 +752,7 @@ struct EpiNone {};
 struct EpiArgs {
   CUtensorMap z;   // pre-activation, as the output's map
   GemmEpilogue e;
-  int32_t z_vec;   // as GParams' c_vec and c_tma, for the pre-activation
-  int32_t z_tma;
+  int32_t z_tma;   // as GParams' c_tma, for the pre-activation
   int32_t r_vec;   // 1: every residual row start is 16-byte aligned
 };
 template <bool kEpi>
@@ -755,128 +760,171 @@ struct EpiParamT { using type = EpiNone; };
 template <>
 struct EpiParamT<true> { using type = EpiArgs; };
 
-// Asks L2 for this warp's part of the residual while the tile's MMAs run (lane
-// = row, one 128-byte line at a time).
-__device__ __forceinline__ void epi_prefetch(const GParams& p, const EpiArgs& ea, const Tile& ti, int quarter, int lane,
-                                             int cols, int col_off) {
+// Before a tile's accumulator is ready: asks L2 for this warp's part of the
+// residual (lane = row, one 128-byte line at a time) and returns the bias of
+// four of its columns, for the warp's 512 bytes of shared memory.
+__device__ __forceinline__ float4 epi_prepare(const GParams& p, const EpiArgs& ea, const Tile& ti, int quarter, int lane,
+                                              int cols, int col_off) {
   const GemmEpilogue& e = ea.e;
   const int row = quarter * 32 + lane;
-  if (!e.residual || row >= ti.valid_m) return;
   const int64_t col0 = ti.n0 + col_off, end = min64(col0 + cols, p.N);
-  const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(e.residual) + (ti.m0 + row) * e.ld_residual;
-  for (int64_t c = col0; c < end; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + c));
+  if (e.residual && row < ti.valid_m) {
+    const __nv_bfloat16* r = static_cast<const __nv_bfloat16*>(e.residual) + (ti.m0 + row) * e.ld_residual;
+    for (int64_t c = col0; c < end; c += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + c));
+  }
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  const int64_t c = col0 + 4 * lane;
+  if (e.bias && c < end) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < end)
+        v[i] = e.bias_f32 ? __ldg(static_cast<const float*>(e.bias) + c + i)
+                          : __bfloat162float(static_cast<const __nv_bfloat16*>(e.bias)[c + i]);
+  }
+  return make_float4(v[0], v[1], v[2], v[3]);
 }
 
-template <int kAct, int kCols>
-__device__ __forceinline__ void epi_activate(uint32_t* r) {
+// One 32 x 32 box of a warp to its place: `r` the FP32 values of the lane's
+// row. Through the staging box and TMA where the output allows it (rows and
+// columns outside it are clipped), else with plain bounded stores. A box is
+// written again once its last store has been read out; `turns`: the warp's last
+// store was the other box's and may still be in flight.
+__device__ __forceinline__ void epi_wait_box(bool turns, int lane) {
+  if (lane == 0) {
+    if (turns) bulk_wait_read_one_pending(); else bulk_wait_read_all();
+  }
+  __syncwarp();
+}
+
+__device__ __forceinline__ void epi_store_box(const OutView& o, const CUtensorMap* map, const Tile& ti, const float2* r,
+                                              int quarter, int lane, int col, uint8_t* box, bool turns) {
+  if (o.c_tma) {
+    epi_wait_box(turns, lane);
 #pragma unroll
-  for (int j = 0; j < kCols; ++j) r[j] = __float_as_uint(act_value<kAct>(__uint_as_float(r[j])));
+    for (int q = 0; q < 4; ++q) {
+      uint4 w;
+      w.x = pack_bf16(r[4 * q + 0].x, r[4 * q + 0].y);
+      w.y = pack_bf16(r[4 * q + 1].x, r[4 * q + 1].y);
+      w.z = pack_bf16(r[4 * q + 2].x, r[4 * q + 2].y);
+      w.w = pack_bf16(r[4 * q + 3].x, r[4 * q + 3].y);
+      st_shared_v4(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4), w);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      tma_store_3d(map, box, static_cast<int32_t>(ti.n0 + col), static_cast<int32_t>(ti.m0 + quarter * 32), 0);
+      bulk_commit_group();
+    }
+    return;
+  }
+  const int row = quarter * 32 + lane;
+  if (row >= ti.valid_m) return;
+  const int64_t n = min64(32, o.n_out - (ti.n0 + col));
+  __nv_bfloat16* dst = o.cbase + static_cast<int64_t>(row) * o.ldc + col;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    if (2 * i < n) dst[2 * i] = __float2bfloat16_rn(r[i].x);
+    if (2 * i + 1 < n) dst[2 * i + 1] = __float2bfloat16_rn(r[i].y);
+  }
+}
+
+template <int kAct>
+__device__ __forceinline__ void epi_activate(float2* r) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = act_value<kAct>(r[i]);
+}
+
+// The residual's 32 x 32 box at column `col` of the tile: 16-byte pieces, eight
+// rows of four a load, so whole 64-byte pieces of its rows are read.
+__device__ __forceinline__ void epi_fetch_residual(const GParams& p, const EpiArgs& ea, const Tile& ti, int quarter,
+                                                   int lane, int col, uint4* v) {
+  const GemmEpilogue& e = ea.e;
+  const int64_t c = ti.n0 + col + (lane & 3) * 8, left = p.N - c;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int trow = quarter * 32 + q * 8 + (lane >> 2);
+    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(e.residual) + (ti.m0 + trow) * e.ld_residual + c;
+    v[q] = make_uint4(0u, 0u, 0u, 0u);
+    if (trow < ti.valid_m && left > 0) {
+      if (ea.r_vec && left >= 8) {
+        v[q] = *reinterpret_cast<const uint4*>(src);
+      } else {
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i < left) w[i >> 1] |= static_cast<uint32_t>(__bfloat16_as_ushort(src[i])) << (16 * (i & 1));
+        v[q] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
 }
 
 // r: kCols FP32 accumulators of row quarter * 32 + lane from column n0 +
-// col_off. The residual is read through the warp's staging box, four rows of
-// the 32 x 32 box per 8 lanes (whole 64-byte pieces of its rows), one box ahead
-// of the additions.
+// col_off, worked on 32 columns at a time: bias (broadcast reads of the warp's
+// shared memory), the pre-activation's box, activation, residual (through the
+// box that its sum leaves by), the output's box. With two boxes the
+// pre-activation and the output have one each.
 template <int kCols, int kBufs>
-__device__ __forceinline__ void epi_tile(const GParams& p, const EpiArgs& ea, const Tile& ti, uint32_t* r, int quarter,
-                                         int lane, int my_chunks, int col_off, uint8_t* stg,
+__device__ __forceinline__ void epi_tile(const GParams& p, const EpiArgs& ea, const Tile& ti, uint32_t* r, float4 bias,
+                                         int quarter, int lane, int my_chunks, int col_off, uint8_t* stg, float* s_bias,
                                          const CUtensorMap* tmap_c) {
   const GemmEpilogue& e = ea.e;
-  const int64_t col0 = ti.n0 + col_off;
+  const OutView out = out_view(p, ti);
+  const OutView zv{static_cast<__nv_bfloat16*>(e.preact) + ti.m0 * e.ld_preact + ti.n0, e.ld_preact, p.N, 0, ea.z_tma};
+  uint8_t* box_z = stg;
+  uint8_t* box_c = stg + (kBufs == 2 ? kEpiWarpBytes : 0);
   if (e.bias) {
-    // The same columns for every lane: broadcast loads.
+    __syncwarp();  // the last tile's reads
+    reinterpret_cast<float4*>(s_bias)[lane] = bias;
+    __syncwarp();
+  }
+  // Two boxes take turns: the pre-activation's and the output's, or, with
+  // neither pre-activation nor residual, the output's in both.
+  const bool swap = kBufs == 2 && !e.preact && !e.residual;
+  const bool turns = swap || (kBufs == 2 && e.preact && ea.z_tma && p.c_tma);
+  uint4 res[4];
+  if (e.residual) epi_fetch_residual(p, ea, ti, quarter, lane, col_off, res);
 #pragma unroll
-    for (int j = 0; j < kCols; j += 4) {
-      const int64_t c = col0 + j;
-      float4 b = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (e.bias_vec && c + 4 <= p.N) {
-        if (e.bias_f32) {
-          b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(e.bias) + c));
-        } else {
-          const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(e.bias) + c));
-          b = make_float4(lo_f(w.x), hi_f(w.x), lo_f(w.y), hi_f(w.y));
-        }
-      } else {
-        float v[4];
+  for (int ch = 0; ch < kCols / 32; ++ch) {
+    if (ch >= my_chunks) break;
+    const int col = col_off + ch * 32;
+    float2 v[16];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[i] = c + i >= p.N ? 0.0f
-                 : e.bias_f32 ? __ldg(static_cast<const float*>(e.bias) + c + i)
-                              : __bfloat162float(static_cast<const __nv_bfloat16*>(e.bias)[c + i]);
-        b = make_float4(v[0], v[1], v[2], v[3]);
+    for (int i = 0; i < 16; ++i)
+      v[i] = make_float2(__uint_as_float(r[ch * 32 + 2 * i]), __uint_as_float(r[ch * 32 + 2 * i + 1]));
+    if (e.bias) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 b = reinterpret_cast<const float4*>(s_bias)[ch * 8 + i];
+        v[2 * i] = __fadd2_rn(v[2 * i], make_float2(b.x, b.y));
+        v[2 * i + 1] = __fadd2_rn(v[2 * i + 1], make_float2(b.z, b.w));
       }
-      r[j + 0] = __float_as_uint(__uint_as_float(r[j + 0]) + b.x);
-      r[j + 1] = __float_as_uint(__uint_as_float(r[j + 1]) + b.y);
-      r[j + 2] = __float_as_uint(__uint_as_float(r[j + 2]) + b.z);
-      r[j + 3] = __float_as_uint(__uint_as_float(r[j + 3]) + b.w);
     }
-  }
-  if (e.preact) {
-    const OutView z{static_cast<__nv_bfloat16*>(e.preact) + ti.m0 * e.ld_preact + ti.n0, e.ld_preact, p.N, ea.z_vec,
-                    ea.z_tma};
-    store_tile<GEMM_DENSE, kCols, kBufs>(z, ti, r, quarter, lane, my_chunks, col_off, stg, &ea.z);
-  }
-  if (e.act == MX_ACT_RELU) epi_activate<MX_ACT_RELU, kCols>(r);
-  else if (e.act == MX_ACT_GELU) epi_activate<MX_ACT_GELU, kCols>(r);
-  else if (e.act == MX_ACT_SILU) epi_activate<MX_ACT_SILU, kCols>(r);
-  if (e.residual) {
-    const __nv_bfloat16* res = static_cast<const __nv_bfloat16*>(e.residual) + ti.m0 * e.ld_residual + col0;
-    if (ea.r_vec) {
-      const int rr0 = lane >> 2, cc = lane & 3;  // row of each eight, 16-byte piece
-      uint4 v[4];
-      auto fetch = [&](int ch) {
+    if (e.preact) epi_store_box(zv, &ea.z, ti, v, quarter, lane, col, box_z, turns);
+    if (e.act == MX_ACT_GELU) epi_activate<MX_ACT_GELU>(v);
+    else if (e.act == MX_ACT_SILU) epi_activate<MX_ACT_SILU>(v);
+    else if (e.act == MX_ACT_RELU) epi_activate<MX_ACT_RELU>(v);
+    if (e.residual) {
+      epi_wait_box(turns, lane);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int trow = quarter * 32 + q * 8 + rr0;
-          const int64_t c = ch * 32 + cc * 8;
-          const int64_t left = p.N - (col0 + c);
-          const __nv_bfloat16* src = res + static_cast<int64_t>(trow) * e.ld_residual + c;
-          v[q] = make_uint4(0u, 0u, 0u, 0u);
-          if (trow < ti.valid_m && left >= 8) {
-            v[q] = *reinterpret_cast<const uint4*>(src);
-          } else if (trow < ti.valid_m && left > 0) {
-            uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (i < left) w[i >> 1] |= static_cast<uint32_t>(__bfloat16_as_ushort(src[i])) << (16 * (i & 1));
-            v[q] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-      };
-      fetch(0);
-      if (lane == 0) bulk_wait_read_all();  // the box may still feed the pre-activation's store
+      for (int q = 0; q < 4; ++q) {
+        const int rr = q * 8 + (lane >> 2);
+        st_shared_v4(box_c + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4), res[q]);
+      }
+      if (ch + 1 < my_chunks) epi_fetch_residual(p, ea, ti, quarter, lane, col + 32, res);
       __syncwarp();
 #pragma unroll
-      for (int ch = 0; ch < kCols / 32; ++ch) {
-        if (ch >= my_chunks) break;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int rr = q * 8 + rr0;
-          st_shared_v4(stg + rr * 64 + ((cc ^ ((rr >> 1) & 3)) << 4), v[q]);
-        }
-        if (ch + 1 < my_chunks) fetch(ch + 1);
-        __syncwarp();
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint4 x = ld_shared_v4(stg + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4));
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int j = ch * 32 + q * 8 + 2 * i;
-            r[j] = __float_as_uint(__uint_as_float(r[j]) + lo_f(w[i]));
-            r[j + 1] = __float_as_uint(__uint_as_float(r[j + 1]) + hi_f(w[i]));
-          }
-        }
-        __syncwarp();
+      for (int q = 0; q < 4; ++q) {
+        const uint4 x = ld_shared_v4(box_c + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4));
+        v[4 * q + 0] = __fadd2_rn(v[4 * q + 0], make_float2(lo_f(x.x), hi_f(x.x)));
+        v[4 * q + 1] = __fadd2_rn(v[4 * q + 1], make_float2(lo_f(x.y), hi_f(x.y)));
+        v[4 * q + 2] = __fadd2_rn(v[4 * q + 2], make_float2(lo_f(x.z), hi_f(x.z)));
+        v[4 * q + 3] = __fadd2_rn(v[4 * q + 3], make_float2(lo_f(x.w), hi_f(x.w)));
       }
-    } else if (quarter * 32 + lane < ti.valid_m) {
-      const __nv_bfloat16* src = res + static_cast<int64_t>(quarter * 32 + lane) * e.ld_residual;
-#pragma unroll
-      for (int j = 0; j < kCols; ++j)
-        if (j < my_chunks * 32 && col0 + j < p.N) r[j] = __float_as_uint(__uint_as_float(r[j]) + __bfloat162float(src[j]));
+      __syncwarp();
     }
+    epi_store_box(out, tmap_c, ti, v, quarter, lane, col, swap && (ch & 1) ? box_z : box_c, turns);
   }
-  store_tile<GEMM_DENSE, kCols, kBufs>(out_view(p, ti), ti, r, quarter, lane, my_chunks, col_off, stg, tmap_c);
 }
 
 // ===========================================================================
@@ -1133,11 +1181,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int my_chunks = half == 0 ? kHalf0 : kChunks - kHalf0;
     const int col_off = half * kHalf0 * 32;
     uint8_t* stg = sEpi + (warp - 2) * kEpiWarpBytes;
+    [[maybe_unused]] float* s_bias = reinterpret_cast<float*>(smem + C::smem_bytes(false) - 1024) + (warp - 2) * 128;
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x) {
       const Tile ti = get_tile<BN, KIND>(p, g, t);
-      if constexpr (kEpi) epi_prefetch(p, epi, ti, quarter, lane, my_chunks * 32, col_off);
+      [[maybe_unused]] float4 bias;
+      if constexpr (kEpi) bias = epi_prepare(p, epi, ti, quarter, lane, my_chunks * 32, col_off);
       if (!wait_or_abort(&acc_full[acc], acc_phase, p, s_abort)) break;
       tc_fence_after_sync();
       uint32_t r[kCols];
@@ -1158,7 +1208,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc = 0;
         acc_phase ^= 1;
       }
-      if constexpr (kEpi) epi_tile<kCols, 1>(p, epi, ti, r, quarter, lane, my_chunks, col_off, stg, &tmap_c);
+      if constexpr (kEpi)
+        epi_tile<kCols, 1>(p, epi, ti, r, bias, quarter, lane, my_chunks, col_off, stg, s_bias, &tmap_c);
       else store_tile<KIND, kCols>(out_view(p, ti), ti, r, quarter, lane, my_chunks, col_off, stg, &tmap_c);
     }
     // Bulk stores must have completed before the CTA's shared memory goes away.
@@ -1219,7 +1270,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   static_assert(!kEpi || (KIND == GEMM_DENSE && !kSwiGLU_ && !kMulti && !kTS), "dense, block-scaled, one problem");
   constexpr bool kSwiGLU = kSwiGLU_ != 0;
   constexpr bool kSwiQ = kSwiGLU_ == 2;
-  using C = PairCfgT<BN_, kTS, KIND != GEMM_DENSE>;
+  using C = PairCfgT<BN_, kTS, KIND != GEMM_DENSE, kEpi>;
   static_assert(!kMulti || (KIND == GEMM_DENSE && !kSwiGLU), "several problems per launch: dense GEMMs only");
   // Problem 0 holds the fields every problem shares (status word, wait bound)
   // and, unless kMulti, the whole GEMM.
@@ -1584,6 +1635,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     constexpr int kCols = BN / 2;
     const int col_off = half * kCols;
     uint8_t* stg = sEpi + (warp - 2) * C::kEpiBufs * kEpiWarpBytes;
+    [[maybe_unused]] float* s_bias = reinterpret_cast<float*>(smem + C::smem_bytes() - 1024 - (kEpi ? kEpiBiasBytes : 0)) + (warp - 2) * 128;
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int64_t it = 0, t; (t = next_tile(it)) >= 0; ++it) {
@@ -1593,7 +1645,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       if (ti.part == -2) continue;
       float ts = 1.0f;  // the tile's product of tensor scales (kTS), read while the MMAs run
       if constexpr (kTS) ts = __ldg(pp.ts_a) * __ldg(pp.ts_b + (KIND == GEMM_GROUPED_M ? ti.group : 0));
-      if constexpr (kEpi) epi_prefetch(pp, epi, ti, quarter, lane, kCols, col_off);
+      [[maybe_unused]] float4 bias;
+      if constexpr (kEpi) bias = epi_prepare(pp, epi, ti, quarter, lane, kCols, col_off);
       if (!wait_or_abort<true>(&acc_full[acc], acc_phase, p, s_abort)) break;
       tc_fence_after_sync();
       uint32_t r[kCols];
@@ -1657,7 +1710,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           store_tile<KIND, 64, C::kEpiBufs>(out_view(pp, ti), ti, r, quarter, lane, 2, 64 * half, stg, &args.prob[pi].c);
         }
       } else if constexpr (kEpi) {
-        epi_tile<kCols, C::kEpiBufs>(pp, epi, ti, r, quarter, lane, kCols / 32, col_off, stg, &args.prob[pi].c);
+        epi_tile<kCols, C::kEpiBufs>(pp, epi, ti, r, bias, quarter, lane, kCols / 32, col_off, stg, s_bias,
+                                     &args.prob[pi].c);
       } else {
         store_tile<KIND, kCols, C::kEpiBufs>(out_view(pp, ti), ti, r, quarter, lane, kCols / 32, col_off, stg, &args.prob[pi].c);
       }
@@ -2093,8 +2147,8 @@ mx_status epi_args(const GemmLaunch& L, typename EpiParamT<kEpi>::type* a) {
     a->e = L.epi;
     a->r_vec = (reinterpret_cast<uintptr_t>(L.epi.residual) & 15u) == 0 && L.epi.ld_residual % 8 == 0;
     if (L.epi.preact) {
-      a->z_vec = (reinterpret_cast<uintptr_t>(L.epi.preact) & 15u) == 0 && L.epi.ld_preact % 8 == 0;
-      if (a->z_vec && L.N % 8 == 0 && make_out_map(&a->z, L.epi.preact, 1, L.M, L.N, L.epi.ld_preact) == MX_OK)
+      const bool vec = (reinterpret_cast<uintptr_t>(L.epi.preact) & 15u) == 0 && L.epi.ld_preact % 8 == 0;
+      if (vec && L.N % 8 == 0 && make_out_map(&a->z, L.epi.preact, 1, L.M, L.N, L.epi.ld_preact) == MX_OK)
         a->z_tma = 1;
     }
   }
@@ -2110,7 +2164,7 @@ mx_status launch_cfg(const GemmLaunch& L, const GParams& p_in, int64_t tiles_upp
   st = make_map(&mb, L.b_data, L.b_rows_total, L.K, L.b_ld, BN);
   if (st != MX_OK) return st;
   output_map(L, p, &mc, KIND);
-  const size_t smem = Cfg<BN>::smem_bytes(KIND != GEMM_DENSE);
+  const size_t smem = Cfg<BN>::smem_bytes(KIND != GEMM_DENSE) + (kEpi ? kEpiBiasBytes : 0);
   typename EpiParamT<kEpi>::type epi;
   st = epi_args<kEpi>(L, &epi);
   if (st != MX_OK) return st;
@@ -2216,7 +2270,7 @@ mx_status launch_pair(const GemmLaunch& L, const GParams& p_in, cudaStream_t s) 
     if (st != MX_OK) return st;
   }
   output_map(L, p, &mc, KIND);
-  const size_t smem = PairCfgT<BN, kTS, KIND != GEMM_DENSE>::smem_bytes();
+  const size_t smem = PairCfgT<BN, kTS, KIND != GEMM_DENSE, kEpi>::smem_bytes();
   typename EpiParamT<kEpi>::type epi;
   st = epi_args<kEpi>(L, &epi);
   if (st != MX_OK) return st;

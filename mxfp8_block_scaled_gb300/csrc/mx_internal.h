@@ -107,7 +107,6 @@ struct GemmEpilogue {
   int64_t ld_residual;
   int64_t ld_preact;
   int32_t bias_f32;
-  int32_t bias_vec;      // the bias allows 4-element loads
   int32_t act;           // mx_act
 };
 
