@@ -5,11 +5,13 @@
 //
 // and the epilogue alone for products over an empty contraction.
 //
-// Bound by HBM: dy and z read, dz written. A thread takes V neighbouring columns
-// (16 bytes) and walks down the rows, so the bias's gradient stays in its
-// registers and each column's terms are added in one order: the CTA's eight
-// row lanes in shared memory, then one partial row per CTA in the workspace,
-// added by a second launch (same inputs, same bits; no atomics).
+// Bound by HBM: dy and z read, dz written. A thread takes eight columns (16
+// neighbouring bytes, or every 32nd column where the pitches do not allow that)
+// and walks down the rows, so the bias's gradient stays in its registers and
+// each column's terms are added in one order: the CTA's eight row lanes in
+// shared memory, then one partial row per CTA in the workspace, added by a
+// second launch (same inputs, same bits; no atomics). The next row's loads are
+// issued before a row's arithmetic, six CTAs an SM.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -24,38 +26,51 @@
 namespace mx {
 namespace {
 
-constexpr int kRowLanes = 8;      // a CTA is 32 column lanes x 8 row lanes
-constexpr int kTargetCtas = 1216; // eight per SM of GB300; a constant, so the workspace's size needs no device
+constexpr int kRowLanes = 8;      // a CTA is 32 column lanes x 8 row lanes,
+constexpr int kWidth = 256;       // eight columns a lane
+static_assert(kWidth == 32 * kRowLanes, "a thread adds one column of the CTA");
+constexpr int kTargetCtas = 912;  // six per SM of GB300; a constant, so the workspace's size needs no device
 
-// V neighbouring BF16 elements (8 as one 16-byte access, or 1) as FP32 pairs.
-template <int V>
-struct Piece;
-template <>
-struct Piece<8> {
-  uint4 w;
+// A thread's eight BF16 elements of a row, two a word.
+struct Piece {
+  uint32_t w[4];
   __device__ __forceinline__ float2 pair(int i) const {
-    const uint32_t v = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
-    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+    return make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
   }
   __device__ __forceinline__ void set(int i, float2 v) {
     const __nv_bfloat162 h = __float22bfloat162_rn(v);
-    (i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w) = *reinterpret_cast<const uint32_t*>(&h);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  __device__ __forceinline__ void put(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = w; }
 };
-template <>
-struct Piece<1> {
-  __nv_bfloat16 e;
-  __device__ __forceinline__ float2 pair(int) const { return make_float2(__bfloat162float(e), 0.0f); }
-  __device__ __forceinline__ void set(int, float2 v) { e = __float2bfloat16_rn(v.x); }
-  __device__ __forceinline__ void put(__nv_bfloat16* p) const { *p = e; }
-};
-template <int V>
-__device__ __forceinline__ Piece<V> piece_at(const __nv_bfloat16* p) {
-  Piece<V> r;
-  if constexpr (V == 8) r.w = *reinterpret_cast<const uint4*>(p);
-  else r.e = *p;
+
+// The piece at p: 16 bytes, or elements p[0], p[32], ... Those that do not
+// exist (`left` columns from p on do) read as zero.
+template <bool kVec>
+__device__ __forceinline__ Piece load_piece(const __nv_bfloat16* p, int left) {
+  Piece r = {};
+  if constexpr (kVec) {
+    if (left > 0) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p);
+      r.w[0] = v.x, r.w[1] = v.y, r.w[2] = v.z, r.w[3] = v.w;
+    }
+  } else {
+    uint32_t e[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e[i] = 32 * i < left ? __bfloat16_as_ushort(p[32 * i]) : 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = e[2 * i] | e[2 * i + 1] << 16;
+  }
   return r;
+}
+template <bool kVec>
+__device__ __forceinline__ void store_piece(__nv_bfloat16* p, const Piece& r, int left) {
+  if constexpr (kVec) {
+    if (left > 0) *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (32 * i < left) p[32 * i] = __ushort_as_bfloat16(static_cast<unsigned short>(r.w[i / 2] >> (16 * (i & 1))));
+  }
 }
 
 struct EpiBackwardArgs {
@@ -67,62 +82,57 @@ struct EpiBackwardArgs {
   int64_t cols;
 };
 
-template <int kAct, int V>
-__global__ void __launch_bounds__(32 * kRowLanes) epilogue_backward_kernel(const EpiBackwardArgs a) {
-  __shared__ float s[kRowLanes][32 * V + 1];
+// kVec: every row is a whole number of aligned 16-byte pieces.
+template <int kAct, bool kVec>
+__global__ void __launch_bounds__(32 * kRowLanes, kVec ? 6 : 4) epilogue_backward_kernel(const EpiBackwardArgs a) {
+  __shared__ float s[kRowLanes][kWidth + 1];
   pdl_launch_dependents();
   pdl_wait();
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int64_t c = (static_cast<int64_t>(blockIdx.x) * 32 + tx) * V;
-  const int nv = static_cast<int>(min64(V, a.cols - c));
-  constexpr int P = (V + 1) / 2;
-  float2 sum[P];
+  const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kWidth;
+  const int64_t c = c0 + (kVec ? tx * 8 : tx);
+  const int left = static_cast<int>(min64(kWidth, a.cols - c));
+  float2 sum[4];
 #pragma unroll
-  for (int i = 0; i < P; ++i) sum[i] = act_pair(0.0f);
-  if (nv == V) {
-#pragma unroll 4
-    for (int64_t row = static_cast<int64_t>(blockIdx.y) * kRowLanes + ty; row < a.rows;
-         row += static_cast<int64_t>(gridDim.y) * kRowLanes) {
-      const Piece<V> d = piece_at<V>(a.dy + row * a.lddy + c);
-      Piece<V> z = {}, o;
-      if (kAct != MX_ACT_NONE) z = piece_at<V>(a.z + row * a.ldz + c);
-#pragma unroll
-      for (int i = 0; i < P; ++i) {
-        float2 g = d.pair(i);
-        if (kAct != MX_ACT_NONE) g = __fmul2_rn(g, act_slope<kAct>(z.pair(i)));
-        sum[i] = __fadd2_rn(sum[i], g);
-        o.set(i, g);
-      }
-      if (a.dz) o.put(a.dz + row * a.lddz + c);
+  for (int i = 0; i < 4; ++i) sum[i] = act_pair(0.0f);
+  const int64_t step = static_cast<int64_t>(gridDim.y) * kRowLanes;
+  int64_t row = static_cast<int64_t>(blockIdx.y) * kRowLanes + ty;
+  const __nv_bfloat16* dy = a.dy + row * a.lddy + c;
+  const __nv_bfloat16* zp = a.z + row * a.ldz + c;
+  Piece d = {}, z = {};
+  if (row < a.rows) {
+    d = load_piece<kVec>(dy, left);
+    if (kAct != MX_ACT_NONE) z = load_piece<kVec>(zp, left);
+  }
+#pragma unroll 1
+  for (; row < a.rows; row += step) {
+    Piece dn = {}, zn = {}, o;
+    dy += step * a.lddy;
+    zp += step * a.ldz;
+    if (row + step < a.rows) {
+      dn = load_piece<kVec>(dy, left);
+      if (kAct != MX_ACT_NONE) zn = load_piece<kVec>(zp, left);
     }
-  } else if (nv > 0) {  // the last columns of a width that is no multiple of V
-    for (int64_t row = static_cast<int64_t>(blockIdx.y) * kRowLanes + ty; row < a.rows;
-         row += static_cast<int64_t>(gridDim.y) * kRowLanes) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (i < nv) {
-          const Piece<1> d = piece_at<1>(a.dy + row * a.lddy + c + i);
-          float2 g = d.pair(0);
-          if (kAct != MX_ACT_NONE) g = __fmul2_rn(g, act_slope<kAct>(piece_at<1>(a.z + row * a.ldz + c + i).pair(0)));
-          (i & 1 ? sum[i / 2].y : sum[i / 2].x) += g.x;
-          Piece<1> o;
-          o.set(0, g);
-          if (a.dz) o.put(a.dz + row * a.lddz + c + i);
-        }
-      }
+    for (int i = 0; i < 4; ++i) {
+      float2 g = d.pair(i);
+      if (kAct != MX_ACT_NONE) g = __fmul2_rn(g, act_slope<kAct>(z.pair(i)));
+      sum[i] = __fadd2_rn(sum[i], g);
+      o.set(i, g);
     }
+    if (a.dz) store_piece<kVec>(a.dz + row * a.lddz + c, o, left);
+    d = dn;
+    z = zn;
   }
   if (!a.partial) return;
 #pragma unroll
-  for (int i = 0; i < V; ++i) s[ty][tx * V + i] = i & 1 ? sum[i / 2].y : sum[i / 2].x;
+  for (int i = 0; i < 8; ++i) s[ty][kVec ? tx * 8 + i : i * 32 + tx] = i & 1 ? sum[i / 2].y : sum[i / 2].x;
   __syncthreads();
-  for (int j = threadIdx.x; j < 32 * V; j += 32 * kRowLanes) {
-    const int64_t col = static_cast<int64_t>(blockIdx.x) * 32 * V + j;
-    if (col >= a.cols) break;
-    float v = s[0][j];
+  if (c0 + threadIdx.x < a.cols) {
+    float v = s[0][threadIdx.x];
 #pragma unroll
-    for (int y = 1; y < kRowLanes; ++y) v += s[y][j];
-    a.partial[static_cast<int64_t>(blockIdx.y) * a.cols + col] = v;
+    for (int y = 1; y < kRowLanes; ++y) v += s[y][threadIdx.x];
+    a.partial[static_cast<int64_t>(blockIdx.y) * a.cols + c0 + threadIdx.x] = v;
   }
 }
 
@@ -145,18 +155,16 @@ __global__ void __launch_bounds__(256) epilogue_only_kernel(const GemmEpilogue e
   }
 }
 
-// Columns of one CTA: 32 lanes of 16-byte vectors. The partial rows are counted
-// for that width whatever the alignment of a call's pointers turns out to be.
 int partial_rows(int64_t rows, int64_t cols) {
-  const int64_t blocks = (cols + 255) / 256;
+  const int64_t blocks = (cols + kWidth - 1) / kWidth;
   const int64_t want = std::max<int64_t>(1, kTargetCtas / blocks);
   return static_cast<int>(std::min(want, (rows + kRowLanes - 1) / kRowLanes));
 }
 
-template <int kAct, int V>
-mx_status launch_backward(const EpiBackwardArgs& a, int parts, cudaStream_t s) {
+template <int kAct>
+mx_status backward_act(const EpiBackwardArgs& a, int parts, bool vec, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.cols + 32 * V - 1) / (32 * V)), static_cast<unsigned>(parts));
+  cfg.gridDim = dim3(static_cast<unsigned>((a.cols + kWidth - 1) / kWidth), static_cast<unsigned>(parts));
   cfg.blockDim = dim3(32 * kRowLanes);
   cfg.stream = s;
   cudaLaunchAttribute attr[1] = {};
@@ -164,12 +172,7 @@ mx_status launch_backward(const EpiBackwardArgs& a, int parts, cudaStream_t s) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
-  return cuda_status(cudaLaunchKernelEx(&cfg, epilogue_backward_kernel<kAct, V>, a), "mx_epilogue_backward launch");
-}
-
-template <int kAct>
-mx_status backward_act(const EpiBackwardArgs& a, int parts, bool vec, cudaStream_t s) {
-  return vec ? launch_backward<kAct, 8>(a, parts, s) : launch_backward<kAct, 1>(a, parts, s);
+  return cuda_status(cudaLaunchKernelEx(&cfg, vec ? epilogue_backward_kernel<kAct, true> : epilogue_backward_kernel<kAct, false>, a), "mx_epilogue_backward launch");
 }
 
 bool vec_ok(const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && ld % 8 == 0; }
@@ -193,7 +196,7 @@ mx_status launch_epilogue_backward(const EpilogueBackwardLaunch& L, cudaStream_t
   a.cols = L.cols;
   const int parts = partial_rows(L.rows, L.cols);
   a.partial = !L.dbias ? nullptr : parts > 1 ? static_cast<float*>(L.ws) : L.dbias;
-  const bool vec = vec_ok(L.dy, L.lddy) && (L.act == MX_ACT_NONE || vec_ok(L.z, L.ldz)) && (!L.dz || vec_ok(L.dz, L.lddz));
+  const bool vec = L.cols % 8 == 0 && vec_ok(L.dy, L.lddy) && (L.act == MX_ACT_NONE || vec_ok(L.z, L.ldz)) && (!L.dz || vec_ok(L.dz, L.lddz));
   mx_status st = MX_OK;
   switch (L.act) {
     case MX_ACT_RELU: st = backward_act<MX_ACT_RELU>(a, parts, vec, s); break;

@@ -786,7 +786,7 @@ __device__ __forceinline__ float4 epi_prepare(const GParams& p, const EpiArgs& e
 
 // One 32 x 32 box of a warp to its place: `r` the FP32 values of the lane's
 // row. Through the staging box and TMA where the output allows it (rows and
-// columns outside it are clipped), else with plain bounded stores. A box is
+// columns outside it are clipped), else with bounded element stores. A box is
 // written again once its last store has been read out; `turns`: the warp's last
 // store was the other box's and may still be in flight.
 __device__ __forceinline__ void epi_wait_box(bool turns, int lane) {
@@ -794,6 +794,14 @@ __device__ __forceinline__ void epi_wait_box(bool turns, int lane) {
     if (turns) bulk_wait_read_one_pending(); else bulk_wait_read_all();
   }
   __syncwarp();
+}
+
+// The box's rows from shared memory, a lane per column: neighbouring lanes write
+// neighbouring elements (a lane per row would touch 32 rows a store).
+__device__ __noinline__ void epi_store_elements(__nv_bfloat16* dst, int64_t ldc, int rows, int lane, const uint8_t* box) {
+#pragma unroll 8
+  for (int k = 0; k < rows; ++k, dst += ldc)
+    *dst = *reinterpret_cast<const __nv_bfloat16*>(box + k * 64 + (((lane >> 3) ^ ((k >> 1) & 3)) << 4) + (lane & 7) * 2);
 }
 
 __device__ __forceinline__ void epi_store_box(const OutView& o, const CUtensorMap* map, const Tile& ti, const float2* r,
@@ -817,15 +825,17 @@ __device__ __forceinline__ void epi_store_box(const OutView& o, const CUtensorMa
     }
     return;
   }
-  const int row = quarter * 32 + lane;
-  if (row >= ti.valid_m) return;
-  const int64_t n = min64(32, o.n_out - (ti.n0 + col));
-  __nv_bfloat16* dst = o.cbase + static_cast<int64_t>(row) * o.ldc + col;
+  epi_wait_box(false, lane);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    if (2 * i < n) dst[2 * i] = __float2bfloat16_rn(r[i].x);
-    if (2 * i + 1 < n) dst[2 * i + 1] = __float2bfloat16_rn(r[i].y);
-  }
+  for (int q = 0; q < 4; ++q)
+    st_shared_v4(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4),
+                 make_uint4(pack_bf16(r[4 * q].x, r[4 * q].y), pack_bf16(r[4 * q + 1].x, r[4 * q + 1].y),
+                            pack_bf16(r[4 * q + 2].x, r[4 * q + 2].y), pack_bf16(r[4 * q + 3].x, r[4 * q + 3].y)));
+  __syncwarp();
+  if (ti.n0 + col + lane < o.n_out)
+    epi_store_elements(o.cbase + static_cast<int64_t>(quarter * 32) * o.ldc + col + lane, o.ldc,
+                       min(32, ti.valid_m - quarter * 32), lane, box);
+  __syncwarp();
 }
 
 template <int kAct>
@@ -834,8 +844,9 @@ __device__ __forceinline__ void epi_activate(float2* r) {
   for (int i = 0; i < 16; ++i) r[i] = act_value<kAct>(r[i]);
 }
 
-// The residual's 32 x 32 box at column `col` of the tile: 16-byte pieces, eight
-// rows of four a load, so whole 64-byte pieces of its rows are read.
+// The residual's 32 x 32 box at column `col` of the tile, where its rows start
+// on 16-byte boundaries: pieces of 16 bytes, eight rows of four a load, so whole
+// 64-byte pieces of its rows are read.
 __device__ __forceinline__ void epi_fetch_residual(const GParams& p, const EpiArgs& ea, const Tile& ti, int quarter,
                                                    int lane, int col, uint4* v) {
   const GemmEpilogue& e = ea.e;
@@ -843,10 +854,10 @@ __device__ __forceinline__ void epi_fetch_residual(const GParams& p, const EpiAr
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int trow = quarter * 32 + q * 8 + (lane >> 2);
-    const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(e.residual) + (ti.m0 + trow) * e.ld_residual + c;
     v[q] = make_uint4(0u, 0u, 0u, 0u);
     if (trow < ti.valid_m && left > 0) {
-      if (ea.r_vec && left >= 8) {
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(e.residual) + (ti.m0 + trow) * e.ld_residual + c;
+      if (left >= 8) {
         v[q] = *reinterpret_cast<const uint4*>(src);
       } else {
         uint32_t w[4] = {0u, 0u, 0u, 0u};
@@ -856,6 +867,30 @@ __device__ __forceinline__ void epi_fetch_residual(const GParams& p, const EpiAr
         v[q] = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
+  }
+}
+
+// The same box straight into shared memory, row by row with a lane per column.
+// Not inlined, like the element stores above: inlined, they would cost the TMA
+// path registers.
+__device__ __noinline__ void epi_copy_residual(const GParams& p, const EpiArgs& ea, const Tile& ti, int quarter,
+                                                  int lane, int col, uint8_t* box) {
+  const GemmEpilogue& e = ea.e;
+  const int rows = min(32, ti.valid_m - quarter * 32);
+  const bool in = ti.n0 + col + lane < p.N;
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(e.residual) +
+                             (ti.m0 + quarter * 32) * e.ld_residual + ti.n0 + col + lane;
+#pragma unroll 1
+  for (int k0 = 0; k0 < 32; k0 += 16) {  // sixteen rows in flight
+    __nv_bfloat16 v[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      v[k] = in && k0 + k < rows ? *src : __float2bfloat16_rn(0.0f);
+      src += e.ld_residual;
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      *reinterpret_cast<__nv_bfloat16*>(box + (k0 + k) * 64 + (((lane >> 3) ^ ((k >> 1) & 3)) << 4) + (lane & 7) * 2) = v[k];
   }
 }
 
@@ -883,7 +918,7 @@ __device__ __forceinline__ void epi_tile(const GParams& p, const EpiArgs& ea, co
   const bool swap = kBufs == 2 && !e.preact && !e.residual;
   const bool turns = swap || (kBufs == 2 && e.preact && ea.z_tma && p.c_tma);
   uint4 res[4];
-  if (e.residual) epi_fetch_residual(p, ea, ti, quarter, lane, col_off, res);
+  if (e.residual && ea.r_vec) epi_fetch_residual(p, ea, ti, quarter, lane, col_off, res);
 #pragma unroll
   for (int ch = 0; ch < kCols / 32; ++ch) {
     if (ch >= my_chunks) break;
@@ -906,12 +941,16 @@ __device__ __forceinline__ void epi_tile(const GParams& p, const EpiArgs& ea, co
     else if (e.act == MX_ACT_RELU) epi_activate<MX_ACT_RELU>(v);
     if (e.residual) {
       epi_wait_box(turns, lane);
+      if (ea.r_vec) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int rr = q * 8 + (lane >> 2);
-        st_shared_v4(box_c + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4), res[q]);
+        for (int q = 0; q < 4; ++q) {
+          const int rr = q * 8 + (lane >> 2);
+          st_shared_v4(box_c + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4), res[q]);
+        }
+        if (ch + 1 < my_chunks) epi_fetch_residual(p, ea, ti, quarter, lane, col + 32, res);
+      } else {
+        epi_copy_residual(p, ea, ti, quarter, lane, col, box_c);
       }
-      if (ch + 1 < my_chunks) epi_fetch_residual(p, ea, ti, quarter, lane, col + 32, res);
       __syncwarp();
 #pragma unroll
       for (int q = 0; q < 4; ++q) {

@@ -468,10 +468,19 @@ __global__ void __launch_bounds__(256) norm_backward_columns_kernel(const NormAr
 }
 
 // ---------------------------------------------------------------------------
-// Rows through shared memory (every row a whole number of 16-byte vectors on
-// 16-byte boundaries): bulk copies fill a ring of stages per group while the
-// group works on registers, so the bytes in flight cost no registers. A group
-// is W warps; its first thread issues the copies.
+// Rows through shared memory: bulk copies fill a ring of stages per group while
+// the group works on registers, so the bytes in flight cost no registers. A
+// group is W warps; its first thread issues the copies.
+//
+// kElem = false: every row is a whole number of 16-byte vectors on 16-byte
+// boundaries; a thread has vectors of V neighbouring elements, 32 W apart.
+// kElem = true: any alignment. A bulk copy moves whole aligned 16-byte units, so
+// a row's copy begins up to 15 bytes before the row and ends up to 15 after it,
+// which inside the matrix are bytes of the rows next to it (or of the gap between
+// them); where they would lie outside, before the first row or after the last
+// one, the group reads the row itself, element by element. A thread has every
+// 32 W-th element: neighbouring lanes, neighbouring elements, whatever the row's
+// start in shared memory.
 // ---------------------------------------------------------------------------
 
 // Waits for a stage; a wait that runs out records MX_ERR_TIMEOUT and lets the
@@ -562,6 +571,117 @@ __device__ __forceinline__ void set_two(Words& p, int j, float2 v) {
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 __device__ __forceinline__ Words words_at(const void* p) { return *reinterpret_cast<const Words*>(p); }
 
+// A thread's place in a row: element i of its vector k.
+template <typename T, int W, bool kElem>
+__device__ __forceinline__ int column_of(int r, int k, int i) {
+  constexpr int V = 16 / sizeof(T);
+  return kElem ? (k * V + i) * 32 * W + r : (k * 32 * W + r) * V + i;
+}
+
+// Vector k of the row that begins at `row` in shared memory; what lies past the
+// last column reads as zero.
+template <typename T, int W, bool kElem>
+__device__ __forceinline__ Words load_words(const uint8_t* row, int r, int k, int cols) {
+  Words v{{0u, 0u, 0u, 0u}};
+  if constexpr (!kElem) {
+    if (column_of<T, W, false>(r, k, 0) < cols) v = words_at(row + (k * 32 * W + r) * 16);
+  } else {
+    constexpr int V = 16 / sizeof(T);
+    uint32_t e[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = column_of<T, W, true>(r, k, i);
+      if constexpr (sizeof(T) == 4) e[i] = c < cols ? *reinterpret_cast<const uint32_t*>(row + 4 * c) : 0u;
+      else e[i] = c < cols ? *reinterpret_cast<const uint16_t*>(row + 2 * c) : 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (sizeof(T) == 4) v.w[j] = e[j];
+      else v.w[j] = e[2 * j] | e[2 * j + 1] << 16;
+    }
+  }
+  return v;
+}
+
+template <typename T, int W, bool kElem>
+__device__ __forceinline__ void store_words(T* row, const Words& v, int r, int k, int cols) {
+  if constexpr (!kElem) {
+    if (column_of<T, W, false>(r, k, 0) < cols) *reinterpret_cast<Words*>(row + column_of<T, W, false>(r, k, 0)) = v;
+  } else {
+    constexpr int V = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = column_of<T, W, true>(r, k, i);
+      if (c < cols) {
+        if constexpr (sizeof(T) == 4) row[c] = __uint_as_float(v.w[i]);
+        else row[c] = __ushort_as_bfloat16(static_cast<unsigned short>(v.w[i / 2] >> (16 * (i & 1))));
+      }
+    }
+  }
+}
+
+// Parameters of elements j .. j + 3 of vector k (zero past the last column).
+// kF32: they are there, in FP32.
+template <typename T, int W, bool kElem, bool kF32>
+__device__ __forceinline__ float4 param4(const void* p, bool f32, float dflt, int r, int k, int j, int cols) {
+  float v[4];
+  if constexpr (!kElem) {
+    const int c = column_of<T, W, false>(r, k, j);
+    if constexpr (kF32) return c < cols ? *reinterpret_cast<const float4*>(static_cast<const float*>(p) + c)
+                                        : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    load_param<4>(p, f32, c, cols - c, dflt, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = column_of<T, W, true>(r, k, j + i);
+      if constexpr (kF32) v[i] = c < cols ? static_cast<const float*>(p)[c] : 0.0f;
+      else load_param<1>(p, f32, c, cols - c, dflt, &v[i]);
+    }
+  }
+  return make_float4(v[0], v[1], v[2], v[3]);
+}
+
+// The rows of one matrix as stages hold them.
+template <typename T, bool kElem>
+struct RowSource {
+  const T* base;
+  int64_t ld, rows;
+  uint32_t bytes;  // of a row
+  __device__ __forceinline__ const T* at(int64_t row) const { return base + row * ld; }
+  __device__ __forceinline__ uint32_t lead(int64_t row) const {  // bytes before the row in its slot
+    return kElem ? static_cast<uint32_t>(reinterpret_cast<uintptr_t>(at(row)) & 15) : 0u;
+  }
+  static __device__ __forceinline__ uint32_t slot(uint32_t bytes) { return kElem ? ((bytes + 15) & ~15u) + 16 : bytes; }
+  // Whether the copy of the row would leave the matrix.
+  __device__ __forceinline__ bool edge(int64_t row) const {
+    if constexpr (!kElem) return false;
+    const uint32_t l = lead(row);
+    return (row == 0 && l != 0) || (row == rows - 1 && ((l + bytes) & 15) != 0);
+  }
+  __device__ __forceinline__ uint32_t copy_bytes(int64_t row) const {
+    return !kElem ? bytes : edge(row) ? 0u : (lead(row) + bytes + 15) & ~15u;
+  }
+  __device__ __forceinline__ void copy(uint8_t* to, int64_t row, uint64_t* bar) const {
+    const uint32_t n = copy_bytes(row);
+    if (n) bulk_load(to, reinterpret_cast<const uint8_t*>(at(row)) - lead(row), n, bar);
+  }
+  // The whole group, for an edge row.
+  __device__ __forceinline__ void read(uint8_t* to, int64_t row, int r, int threads) const {
+    T* const s = reinterpret_cast<T*>(to + lead(row));
+    const T* const g = at(row);
+    for (uint32_t c = r; c < bytes / sizeof(T); c += threads) s[c] = g[c];
+  }
+};
+
+// After read(): its elements are there for the group, and for the copies that
+// will overwrite them.
+template <int W>
+__device__ __forceinline__ void group_filled(int group) {
+  fence_proxy_async_smem();
+  if constexpr (W > 1) asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(32 * W) : "memory");
+  else __syncwarp();
+}
+
 // Forward, two rows at a time: they share each read of weight and bias (which
 // come from L1, whose bandwidth they would otherwise fill) and each barrier. A
 // thread holds up to kFwdVecs vectors of each row.
@@ -569,12 +689,15 @@ constexpr int kFwdVecs = 4;
 constexpr int kFwdStages = 2;
 template <int W>
 constexpr int kFwdBlock = W <= 8 ? 256 : 32 * W;
+// CTAs an SM: by the registers of a thread (BF16 elements one by one take more).
+template <typename T, int W, bool kElem>
+constexpr int kFwdPerSm = W > 8 ? 1 : kElem && sizeof(T) == 2 ? 2 : 3;
 
 // kF32: weight and bias are both there, in FP32 (the usual case: read with no
 // further questions; asking per vector cost as many instructions as the row's
 // arithmetic).
-template <typename T, int W, bool kF32>
-__global__ void __launch_bounds__(kFwdBlock<W>, W <= 8 ? 3 : 1) norm_forward_ring_kernel(const NormArgs a) {
+template <typename T, int W, bool kElem, bool kF32>
+__global__ void __launch_bounds__(kFwdBlock<W>, kFwdPerSm<T, W, kElem>) norm_forward_ring_kernel(const NormArgs a) {
   constexpr int V = 16 / sizeof(T), K = kFwdVecs, G = kFwdBlock<W> / (32 * W), S = kFwdStages;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[G][S];
@@ -582,9 +705,9 @@ __global__ void __launch_bounds__(kFwdBlock<W>, W <= 8 ? 3 : 1) norm_forward_rin
   __shared__ int32_t gave_up;
   pdl_launch_dependents();
   const int group = threadIdx.x / (32 * W), r = threadIdx.x % (32 * W);
-  const uint32_t row_bytes = static_cast<uint32_t>(a.cols) * sizeof(T);
-  uint8_t* stages = ring + static_cast<size_t>(group) * S * 2 * row_bytes;
-  const T* x = static_cast<const T*>(a.x);
+  const RowSource<T, kElem> x{static_cast<const T*>(a.x), a.ldx, a.rows, static_cast<uint32_t>(a.cols) * static_cast<uint32_t>(sizeof(T))};
+  const uint32_t slot = x.slot(x.bytes);
+  uint8_t* const stages = ring + static_cast<size_t>(group) * S * 2 * slot;
   const int64_t pairs = (a.rows + 1) / 2, step = static_cast<int64_t>(gridDim.x) * G;
   if (r == 0) {
     for (int s = 0; s < S; ++s) mbar_init(&full[group][s], 1);
@@ -598,10 +721,10 @@ __global__ void __launch_bounds__(kFwdBlock<W>, W <= 8 ? 3 : 1) norm_forward_rin
     if (*const_cast<volatile int32_t*>(&gave_up)) return;
     log.note(s);
     const bool two = 2 * pair + 1 < a.rows;
-    uint8_t* to = stages + static_cast<size_t>(s) * 2 * row_bytes;
-    mbar_arrive_expect_tx(&full[group][s], two ? 2 * row_bytes : row_bytes);
-    bulk_load(to, x + 2 * pair * a.ldx, row_bytes, &full[group][s]);
-    if (two) bulk_load(to + row_bytes, x + (2 * pair + 1) * a.ldx, row_bytes, &full[group][s]);
+    uint8_t* to = stages + static_cast<uint32_t>(s) * 2 * slot;
+    mbar_arrive_expect_tx(&full[group][s], x.copy_bytes(2 * pair) + (two ? x.copy_bytes(2 * pair + 1) : 0u));
+    x.copy(to, 2 * pair, &full[group][s]);
+    if (two) x.copy(to + slot, 2 * pair + 1, &full[group][s]);
   };
   int64_t pair = static_cast<int64_t>(blockIdx.x) * G + group;
   if (r == 0)
@@ -609,22 +732,22 @@ __global__ void __launch_bounds__(kFwdBlock<W>, W <= 8 ? 3 : 1) norm_forward_rin
       if (pair + s * step < pairs) issue(s, pair + s * step);
   int s = 0, flip = 0;
   uint32_t parity = 0;
-  const int n = a.cols / V;
-  const float4* const w4 = static_cast<const float4*>(a.weight) + r * (V / 4);
-  const float4* const b4 = static_cast<const float4*>(a.bias) + r * (V / 4);
   for (; pair < pairs; pair += step) {
     stage_wait(&full[group][s], parity, a, &gave_up);
     const bool two = 2 * pair + 1 < a.rows;
-    const uint8_t* from = stages + static_cast<uint32_t>(s) * 2 * row_bytes + r * 16;
+    uint8_t* const from = stages + static_cast<uint32_t>(s) * 2 * slot;
+    if (kElem && (x.edge(2 * pair) || (two && x.edge(2 * pair + 1)))) {
+      if (x.edge(2 * pair)) x.read(from, 2 * pair, r, 32 * W);
+      if (two && x.edge(2 * pair + 1)) x.read(from + slot, 2 * pair + 1, r, 32 * W);
+      group_filled<W>(group);
+    }
+    const uint8_t* const row0 = from + x.lead(2 * pair);
+    const uint8_t* const row1 = from + slot + x.lead(2 * pair + 1);
     Words p[2][K];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int v = k * 32 * W + r;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        p[q][k] = Words{{0u, 0u, 0u, 0u}};
-        if (v < n && (q == 0 || two)) p[q][k] = words_at(from + q * row_bytes + k * 32 * W * 16);
-      }
+      p[0][k] = load_words<T, W, kElem>(row0, r, k, a.cols);
+      p[1][k] = load_words<T, W, kElem>(row1, r, k, two ? a.cols : 0);
     }
     float mean[2] = {0.0f, 0.0f}, sq[2] = {0.0f, 0.0f};
     if (a.center) {
@@ -648,12 +771,16 @@ __global__ void __launch_bounds__(kFwdBlock<W>, W <= 8 ? 3 : 1) norm_forward_rin
       float2 t[2] = {both(0.0f), both(0.0f)};
 #pragma unroll
       for (int k = 0; k < K; ++k)
-        if (k * 32 * W + r < n) {
+        if (kElem || column_of<T, W, kElem>(r, k, 0) < a.cols) {
 #pragma unroll
           for (int j = 0; j < V / 2; ++j)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              const float2 d = __fadd2_rn(two_of<T>(p[q][k], j), minus[q]);
+              float2 d = __fadd2_rn(two_of<T>(p[q][k], j), minus[q]);
+              if constexpr (kElem) {  // absent elements are no part of the variance
+                if (column_of<T, W, kElem>(r, k, 2 * j) >= a.cols) d.x = 0.0f;
+                if (column_of<T, W, kElem>(r, k, 2 * j + 1) >= a.cols) d.y = 0.0f;
+              }
               t[q] = __ffma2_rn(d, d, t[q]);
             }
         }
@@ -670,24 +797,16 @@ __global__ void __launch_bounds__(kFwdBlock<W>, W <= 8 ? 3 : 1) norm_forward_rin
       parity ^= 1;
     }
     const float rstd[2] = {__frsqrt_rn(fmaf(sq[0], a.inv_cols, a.eps)), __frsqrt_rn(fmaf(sq[1], a.inv_cols, a.eps))};
-    T* const out0 = static_cast<T*>(a.out) + 2 * pair * a.ldo + r * V;
-    T* const out1 = out0 + a.ldo;
+    T* const out = static_cast<T*>(a.out) + 2 * pair * a.ldo;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      if (k * 32 * W + r >= n) break;
+      if (column_of<T, W, kElem>(r, k, 0) >= a.cols) break;
       Words o[2];
 #pragma unroll
       for (int j = 0; j < V; j += 4) {
-        float4 w, b;
         asm volatile("" ::: "memory");  // four parameters at a time: hoisted, they would fill the registers
-        if constexpr (kF32) {
-          w = w4[(k * 32 * W * V + j) / 4];
-          b = b4[(k * 32 * W * V + j) / 4];
-        } else {
-          const int c = (k * 32 * W + r) * V + j;
-          load_param<4>(a.weight, a.param_f32, c, 4, 1.0f, &w.x);
-          load_param<4>(a.bias, a.param_f32, c, 4, 0.0f, &b.x);
-        }
+        const float4 w = param4<T, W, kElem, kF32>(a.weight, a.param_f32, 1.0f, r, k, j, a.cols);
+        const float4 b = param4<T, W, kElem, kF32>(a.bias, a.param_f32, 0.0f, r, k, j, a.cols);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const float2 lo = __fmul2_rn(__fadd2_rn(two_of<T>(p[q][k], j / 2), both(-mean[q])), both(rstd[q]));
@@ -696,8 +815,8 @@ __global__ void __launch_bounds__(kFwdBlock<W>, W <= 8 ? 3 : 1) norm_forward_rin
           set_two<T>(o[q], j / 2 + 1, __ffma2_rn(hi, make_float2(w.z, w.w), make_float2(b.z, b.w)));
         }
       }
-      *reinterpret_cast<Words*>(out0 + k * 32 * W * V) = o[0];
-      if (two) *reinterpret_cast<Words*>(out1 + k * 32 * W * V) = o[1];
+      store_words<T, W, kElem>(out, o[0], r, k, a.cols);
+      if (two) store_words<T, W, kElem>(out + a.ldo, o[1], r, k, a.cols);
     }
     if (r < (two ? 2 : 1)) {
       if (a.mean && a.center) a.mean[2 * pair + r] = r ? mean[1] : mean[0];
@@ -715,7 +834,7 @@ __global__ void __launch_bounds__(kFwdBlock<W>, W <= 8 ? 3 : 1) norm_forward_rin
 template <int W>
 constexpr int kBwdBlock = W <= 8 ? 256 : 32 * W;
 
-template <typename T, int W, int K, int R>
+template <typename T, int W, int K, int R, bool kElem>
 __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ring_kernel(const NormArgs a, const int S) {
   constexpr int V = 16 / sizeof(T), P = V / 2, G = kBwdBlock<W> / (32 * W), kMaxS = 8;
   // What stays in a thread's registers besides dw and db: its weights, g of the
@@ -727,8 +846,11 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ri
   __shared__ int32_t gave_up;
   pdl_launch_dependents();
   const int group = threadIdx.x / (32 * W), r = threadIdx.x % (32 * W);
-  const uint32_t row_bytes = static_cast<uint32_t>(a.cols) * sizeof(T);
-  uint8_t* stages = ring + static_cast<size_t>(group) * S * 2 * R * row_bytes;
+  const uint32_t row_bytes = static_cast<uint32_t>(a.cols) * static_cast<uint32_t>(sizeof(T));
+  const RowSource<T, kElem> x{static_cast<const T*>(a.x), a.ldx, a.rows, row_bytes};
+  const RowSource<T, kElem> dy{static_cast<const T*>(a.dy), a.lddy, a.rows, row_bytes};
+  const uint32_t slot = x.slot(row_bytes);
+  uint8_t* const stages = ring + static_cast<size_t>(group) * S * 2 * R * slot;
   const int64_t step = static_cast<int64_t>(gridDim.x) * G * R;
   if (r == 0) {
     for (int s = 0; s < S; ++s) mbar_init(&full[group][s], 1);
@@ -742,11 +864,13 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ri
     if (*const_cast<volatile int32_t*>(&gave_up)) return;
     log.note(s);
     const int n = static_cast<int>(min64(R, a.rows - row));
-    uint8_t* to = stages + static_cast<size_t>(s) * 2 * R * row_bytes;
-    mbar_arrive_expect_tx(&full[group][s], 2 * n * row_bytes);
+    uint8_t* to = stages + static_cast<uint32_t>(s) * 2 * R * slot;
+    uint32_t bytes = 0;
+    for (int q = 0; q < n; ++q) bytes += x.copy_bytes(row + q) + dy.copy_bytes(row + q);
+    mbar_arrive_expect_tx(&full[group][s], bytes);
     for (int q = 0; q < n; ++q) {
-      bulk_load(to + q * row_bytes, static_cast<const T*>(a.x) + (row + q) * a.ldx, row_bytes, &full[group][s]);
-      bulk_load(to + (R + q) * row_bytes, static_cast<const T*>(a.dy) + (row + q) * a.lddy, row_bytes, &full[group][s]);
+      x.copy(to + q * slot, row + q, &full[group][s]);
+      dy.copy(to + (R + q) * slot, row + q, &full[group][s]);
     }
   };
   int64_t row = (static_cast<int64_t>(blockIdx.x) * G + group) * R;
@@ -759,21 +883,21 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ri
   float2 w1[kHold ? K * P : 1];
   if constexpr (kHold) {
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      float w[V];
-      const int c = (k * 32 * W + r) * V;
-      load_param<V>(a.weight, a.param_f32, c, a.cols - c, 1.0f, w);
+    for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int j = 0; j < P; ++j) w1[k * P + j] = make_float2(w[2 * j], w[2 * j + 1]);
-    }
+      for (int j = 0; j < P; j += 2) {
+        const float4 w = param4<T, W, kElem, false>(a.weight, a.param_f32, 1.0f, r, k, 2 * j, a.cols);
+        w1[k * P + j] = make_float2(w.x, w.y);
+        w1[k * P + j + 1] = make_float2(w.z, w.w);
+      }
   }
-  // Weights 2 j .. 2 j + 3 of vector c / V, of which the pair at j is wanted.
-  auto weight2 = [&](int k, int c, int j, float4& w) {
+  // The weights of pair j of vector k (read by fours where they are not held).
+  auto weight2 = [&](int k, int j, float4& w) {
     if constexpr (kHold) return w1[kHold ? k * P + j : 0];
     if (j % 2 == 0) {
       asm volatile("" ::: "memory");
-      if (a.weight && a.param_f32) w = *reinterpret_cast<const float4*>(static_cast<const float*>(a.weight) + c + 2 * j);
-      else load_param<4>(a.weight, a.param_f32, c + 2 * j, 4, 1.0f, &w.x);
+      w = a.weight && a.param_f32 ? param4<T, W, kElem, true>(a.weight, true, 1.0f, r, k, 2 * j, a.cols)
+                                  : param4<T, W, kElem, false>(a.weight, a.param_f32, 1.0f, r, k, 2 * j, a.cols);
     }
     return j % 2 == 0 ? make_float2(w.x, w.y) : make_float2(w.z, w.w);
   };
@@ -795,7 +919,21 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ri
     statistics(row);
     stage_wait(&full[group][s], parity, a, &gave_up);
     const int n = static_cast<int>(min64(R, a.rows - row));
-    const uint8_t* from = stages + static_cast<size_t>(s) * 2 * R * row_bytes;
+    uint8_t* const from = stages + static_cast<uint32_t>(s) * 2 * R * slot;
+    if constexpr (kElem) {
+      bool filled = false;
+      for (int q = 0; q < n; ++q) {
+        if (x.edge(row + q)) x.read(from + q * slot, row + q, r, 32 * W), filled = true;
+        if (dy.edge(row + q)) dy.read(from + (R + q) * slot, row + q, r, 32 * W), filled = true;
+      }
+      if (filled) group_filled<W>(group);
+    }
+    auto x_words = [&](int q, int k) {
+      return load_words<T, W, kElem>(from + q * slot + x.lead(row + q), r, k, q < n ? a.cols : 0);
+    };
+    auto dy_words = [&](int q, int k) {
+      return load_words<T, W, kElem>(from + (R + q) * slot + dy.lead(row + q), r, k, q < n ? a.cols : 0);
+    };
     float2 g[kHold ? R * K * P : 1], h[kHoldH ? R * P : 1];  // h = (x - mean) rstd, g = dy w
     float sum[2 * R];  // of g, then of g h
 #pragma unroll
@@ -803,17 +941,12 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ri
       float2 t1 = both(0.0f), t2 = both(0.0f);
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int c = (k * 32 * W + r) * V;
-        Words px{{0u, 0u, 0u, 0u}}, pd{{0u, 0u, 0u, 0u}};  // no such row or column: dy = 0 adds nothing
-        if (c < a.cols && q < n) {
-          px = words_at(from + q * row_bytes + c * sizeof(T));
-          pd = words_at(from + (R + q) * row_bytes + c * sizeof(T));
-        }
-        if (kHold || c < a.cols) {
+        const Words px = x_words(q, k), pd = dy_words(q, k);  // no such row or column: dy = 0 adds nothing
+        if (kHold || column_of<T, W, kElem>(r, k, 0) < a.cols) {
           float4 w;
 #pragma unroll
           for (int j = 0; j < P; ++j) {
-            const float2 d = two_of<T>(pd, j), gj = __fmul2_rn(d, weight2(k, c, j, w)), hj = h_of(px, q, j);
+            const float2 d = two_of<T>(pd, j), gj = __fmul2_rn(d, weight2(k, j, w)), hj = h_of(px, q, j);
             t1 = __fadd2_rn(t1, gj);
             t2 = __ffma2_rn(gj, hj, t2);
             dw[k * P + j] = __ffma2_rn(d, hj, dw[k * P + j]);
@@ -837,22 +970,21 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ri
                    by_h = both(-rstd[q] * (sum[R + q] * a.inv_cols));
 #pragma unroll
       for (int k = 0; k < K; ++k) {
-        const int c = (k * 32 * W + r) * V;
-        if (c >= a.cols) break;
+        if (column_of<T, W, kElem>(r, k, 0) >= a.cols) break;
         Words o, px, pd;
-        if constexpr (!kHoldH) px = words_at(from + q * row_bytes + c * sizeof(T));
-        if constexpr (!kHold) pd = words_at(from + (R + q) * row_bytes + c * sizeof(T));
+        if constexpr (!kHoldH) px = x_words(q, k);
+        if constexpr (!kHold) pd = dy_words(q, k);
         float4 w;
 #pragma unroll
         for (int j = 0; j < P; ++j) {
           float2 gj, hj;
           if constexpr (kHold) gj = g[(q * K + k) * P + j];
-          else gj = __fmul2_rn(two_of<T>(pd, j), weight2(k, c, j, w));
+          else gj = __fmul2_rn(two_of<T>(pd, j), weight2(k, j, w));
           if constexpr (kHoldH) hj = h[q * P + j];
           else hj = h_of(px, q, j);
           set_two<T>(o, j, __ffma2_rn(by_h, hj, __ffma2_rn(by_g, gj, add)));
         }
-        *reinterpret_cast<Words*>(out + q * a.ldo + c) = o;
+        store_words<T, W, kElem>(out + q * a.ldo, o, r, k, a.cols);
       }
     }
     if (++s == S) {
@@ -872,15 +1004,13 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ri
       if (group == q) {
 #pragma unroll
         for (int i = 0; i < K * P; ++i) {
-          if ((i / P * 32 * W + r) * V < a.cols) {
-            float2* t = acc + i * 32 * W + r;
-            if (q) {
-              dw[i] = __fadd2_rn(dw[i], t[0]);
-              db[i] = __fadd2_rn(db[i], t[N]);
-            }
-            t[0] = dw[i];
-            t[N] = db[i];
+          float2* t = acc + i * 32 * W + r;
+          if (q) {
+            dw[i] = __fadd2_rn(dw[i], t[0]);
+            db[i] = __fadd2_rn(db[i], t[N]);
           }
+          t[0] = dw[i];
+          t[N] = db[i];
         }
       }
       __syncthreads();
@@ -889,13 +1019,25 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ri
   }
 #pragma unroll
   for (int k = 0; k < K; ++k) {
-    const int c = (k * 32 * W + r) * V;
-    if (c >= a.cols) break;
+    if constexpr (kElem) {
 #pragma unroll
-    for (int j = 0; j < P; j += 2) {
-      const float2 w0 = dw[k * P + j], w1_ = dw[k * P + j + 1], b0 = db[k * P + j], b1 = db[k * P + j + 1];
-      *reinterpret_cast<float4*>(p + c + 2 * j) = make_float4(w0.x, w0.y, w1_.x, w1_.y);
-      *reinterpret_cast<float4*>(p + a.cols + c + 2 * j) = make_float4(b0.x, b0.y, b1.x, b1.y);
+      for (int i = 0; i < V; ++i) {
+        const int c = column_of<T, W, true>(r, k, i);
+        const float2 w = dw[k * P + i / 2], b = db[k * P + i / 2];
+        if (c < a.cols) {
+          p[c] = i & 1 ? w.y : w.x;
+          p[a.cols + c] = i & 1 ? b.y : b.x;
+        }
+      }
+    } else {
+      const int c = column_of<T, W, false>(r, k, 0);
+      if (c >= a.cols) break;
+#pragma unroll
+      for (int j = 0; j < P; j += 2) {
+        const float2 w0 = dw[k * P + j], w1_ = dw[k * P + j + 1], b0 = db[k * P + j], b1 = db[k * P + j + 1];
+        *reinterpret_cast<float4*>(p + c + 2 * j) = make_float4(w0.x, w0.y, w1_.x, w1_.y);
+        *reinterpret_cast<float4*>(p + a.cols + c + 2 * j) = make_float4(b0.x, b0.y, b1.x, b1.y);
+      }
     }
   }
 }
@@ -910,57 +1052,62 @@ mx_status forward_cfg(const NormArgs& a, int per_sm, cudaStream_t s) {
                                      1, a));
 }
 
-// Threads per row and vectors per thread by the row's number of vectors (V
-// elements each).
+// Threads per row and vectors (V elements) per thread by the row's number of
+// vectors, for rows too narrow or too wide for the ring.
 template <typename T, int V>
 mx_status forward_any(const NormArgs& a, cudaStream_t s) {
   const int64_t n = (a.cols + V - 1) / V;
   if (n <= 32) return forward_cfg<T, V, 32, 1, 256>(a, 8, s);
   if (n <= 64) return forward_cfg<T, V, 32, 2, 256>(a, 8, s);
-  if (n <= 128) return forward_cfg<T, V, 32, 4, 256>(a, 8, s);
-  if (n <= 256) return forward_cfg<T, V, 32, 8, 256>(a, 4, s);
-  if (n <= 512) return forward_cfg<T, V, 128, 4, 256>(a, 4, s);
-  if (n <= 1024) return forward_cfg<T, V, 256, 4, 256>(a, 4, s);
-  if (n <= 2048) return forward_cfg<T, V, 512, 4, 512>(a, 2, s);
-  if (n <= 4096) return forward_cfg<T, V, 1024, 4, 1024>(a, 1, s);
+  if constexpr (V == 1)
+    if (n <= 256) return forward_cfg<T, V, 32, 8, 256>(a, 6, s);
   const int64_t grid = std::min<int64_t>(a.rows, 2 * static_cast<int64_t>(sm_count()));
   return norm_launched(launch_kernel(norm_forward_wide_kernel<T, V>, static_cast<unsigned>(grid), 1024, 0, s, 1, a));
 }
 
-template <typename T, int W>
+// Bytes of a row's slot in a stage.
+template <typename T>
+size_t slot_bytes(const NormArgs& a, bool elem) {
+  const size_t row = static_cast<size_t>(a.cols) * sizeof(T);
+  return elem ? (row + 15) / 16 * 16 + 16 : row;
+}
+
+template <typename T, int W, bool kElem>
 mx_status forward_ring(const NormArgs& a, cudaStream_t s) {
   constexpr int G = kFwdBlock<W> / (32 * W);
-  const size_t smem = static_cast<size_t>(G) * kFwdStages * 2 * a.cols * sizeof(T);
-  auto kern = a.weight && a.bias && a.param_f32 ? norm_forward_ring_kernel<T, W, true> : norm_forward_ring_kernel<T, W, false>;
+  const size_t smem = static_cast<size_t>(G) * kFwdStages * 2 * slot_bytes<T>(a, kElem);
+  auto kern = a.weight && a.bias && a.param_f32 ? norm_forward_ring_kernel<T, W, kElem, true>
+                                                : norm_forward_ring_kernel<T, W, kElem, false>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(norm smem)");
-  const int64_t grid = std::min<int64_t>(((a.rows + 1) / 2 + G - 1) / G, static_cast<int64_t>(sm_count()) * (W <= 8 ? 3 : 1));
+  const int64_t grid = std::min<int64_t>(((a.rows + 1) / 2 + G - 1) / G, static_cast<int64_t>(sm_count()) * kFwdPerSm<T, W, kElem>);
   return norm_launched(launch_kernel(kern, static_cast<unsigned>(grid), kFwdBlock<W>, smem, s, 1, a));
 }
 
-template <typename T>
+// Warps per row by its number of 16-byte vectors (begun ones counted).
+template <typename T, bool kElem>
 mx_status forward_rows(const NormArgs& a, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
-  const int64_t n = a.cols / V;
-  if (a.cols % V == 0 && n > 32) {
-    if (n <= 128) return forward_ring<T, 1>(a, s);
-    if (n <= 256) return forward_ring<T, 2>(a, s);
-    if (n <= 512) return forward_ring<T, 4>(a, s);
-    if (n <= 1024) return forward_ring<T, 8>(a, s);
-    if (n <= 2048) return forward_ring<T, 16>(a, s);
+  const int64_t n = (a.cols + V - 1) / V;
+  if (n > 32) {
+    if (n <= 128) return forward_ring<T, 1, kElem>(a, s);
+    if (n <= 256) return forward_ring<T, 2, kElem>(a, s);
+    if (n <= 512) return forward_ring<T, 4, kElem>(a, s);
+    if (n <= 1024) return forward_ring<T, 8, kElem>(a, s);
+    if (n <= 2048) return forward_ring<T, 16, kElem>(a, s);
   }
-  return forward_any<T, V>(a, s);
+  return forward_any<T, kElem ? 1 : V>(a, s);
 }
 
 // R rows a stage, as many stages as the share of shared memory holds (two CTAs
 // an SM for groups of up to eight warps), four at most.
-template <typename T, int W, int K, int R>
+template <typename T, int W, int K, int R, bool kElem>
 mx_status backward_ring(const NormArgs& a, int* parts, cudaStream_t s) {
   constexpr int G = kBwdBlock<W> / (32 * W), per_sm = W <= 8 ? 2 : 1;
-  const size_t stage = static_cast<size_t>(G) * 2 * R * a.cols * sizeof(T);
+  const size_t stage = static_cast<size_t>(G) * 2 * R * slot_bytes<T>(a, kElem);
   const int S = static_cast<int>(std::min<size_t>(4, 212992 / per_sm / stage));
-  static_assert(2 * G * 2 * R * 32 * W * K * 16 <= 212992 / per_sm, "a stage is refilled while another one is worked on");
-  auto kern = norm_backward_ring_kernel<T, W, K, R>;
+  static_assert(2 * G * 2 * R * (32 * W * K * 16 + 16) <= 212992 / per_sm, "a stage is refilled while another one is worked on");
+  auto kern = norm_backward_ring_kernel<T, W, K, R, kElem>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S * stage));
   if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(norm smem)");
   const int64_t grid = std::min<int64_t>((a.rows + G * R - 1) / (G * R),
@@ -983,12 +1130,8 @@ template <typename T, int V>
 mx_status backward_any(const NormArgs& a, int* parts, cudaStream_t s) {
   const int64_t n = (a.cols + V - 1) / V;
   if (n <= 32) return backward_cfg<T, V, 32, 1, 512>(a, parts, s);
-  if (n <= 64) return backward_cfg<T, V, 32, 2, 512>(a, parts, s);
-  if (n <= 128) return backward_cfg<T, V, 128, 1, 512>(a, parts, s);
-  if (n <= 256) return backward_cfg<T, V, 256, 1, 512>(a, parts, s);
-  if (n <= 512) return backward_cfg<T, V, 256, 2, 512>(a, parts, s);
-  if (n <= 1024) return backward_cfg<T, V, 512, 2, 512>(a, parts, s);
-  if (n <= 2048) return backward_cfg<T, V, 1024, 2, 1024>(a, parts, s);
+  if constexpr (V == 1)
+    if (n <= 128) return backward_cfg<T, V, 32, 4, 512>(a, parts, s);
   if (a.partial) {
     const int bx = static_cast<int>((n + 255) / 256);
     const int by = static_cast<int>(std::min<int64_t>(a.rows, std::max(1, std::min(kMaxPartials, 4 * sm_count() / bx))));
@@ -1009,20 +1152,20 @@ mx_status backward_any(const NormArgs& a, int* parts, cudaStream_t s) {
   return norm_launched(launch_kernel(norm_backward_wide_kernel<T, V>, static_cast<unsigned>(grid), 1024, 0, s, 1, a));
 }
 
-template <typename T>
+template <typename T, bool kElem>
 mx_status backward_rows(const NormArgs& a, int* parts, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
-  const int64_t n = a.cols / V;
-  if (a.cols % V == 0 && n > 16) {
-    if (n <= 32) return backward_ring<T, 1, 1, 4>(a, parts, s);
-    if (n <= 64) return backward_ring<T, 2, 1, 4>(a, parts, s);
-    if (n <= 128) return backward_ring<T, 4, 1, 4>(a, parts, s);
-    if (n <= 256) return backward_ring<T, 8, 1, 4>(a, parts, s);
-    if (n <= 512) return backward_ring<T, 8, 2, 2>(a, parts, s);
-    if (n <= 1024) return backward_ring<T, 16, 2, 2>(a, parts, s);
-    if (n <= 2048) return backward_ring<T, 16, 4, 1>(a, parts, s);
+  const int64_t n = (a.cols + V - 1) / V;
+  if (n > 16) {
+    if (n <= 32) return backward_ring<T, 1, 1, 4, kElem>(a, parts, s);
+    if (n <= 64) return backward_ring<T, 2, 1, 4, kElem>(a, parts, s);
+    if (n <= 128) return backward_ring<T, 4, 1, 4, kElem>(a, parts, s);
+    if (n <= 256) return backward_ring<T, 8, 1, 4, kElem>(a, parts, s);
+    if (n <= 512) return backward_ring<T, 8, 2, 2, kElem>(a, parts, s);
+    if (n <= 1024) return backward_ring<T, 16, 2, 2, kElem>(a, parts, s);
+    if (n <= 2048) return backward_ring<T, 16, 4, 1, kElem>(a, parts, s);
   }
-  return backward_any<T, V>(a, parts, s);
+  return backward_any<T, kElem ? 1 : V>(a, parts, s);
 }
 
 bool vec_ok(const void* p, int64_t ld, int elem) {
@@ -1053,11 +1196,11 @@ NormArgs norm_args(const NormLaunch& L) {
   return a;
 }
 
-// 16-byte vectors where every row of every matrix and the parameters start on
-// a 16-byte boundary, else element by element.
+// 16-byte vectors where every row of every matrix is a whole number of them and
+// starts, like the parameters, on a 16-byte boundary, else element by element.
 bool wide_access(const NormLaunch& L) {
   const int e = L.dtype == MX_F32 ? 4 : 2;
-  return vec_ok(L.x, L.ldx, e) && vec_ok(L.out, L.ldo, e) && (!L.dy || vec_ok(L.dy, L.lddy, e)) &&
+  return L.cols * e % 16 == 0 && vec_ok(L.x, L.ldx, e) && vec_ok(L.out, L.ldo, e) && (!L.dy || vec_ok(L.dy, L.lddy, e)) &&
          vec_ok(L.weight, 0, 4) && vec_ok(L.bias, 0, 4);
 }
 
@@ -1066,8 +1209,8 @@ bool wide_access(const NormLaunch& L) {
 mx_status launch_norm_forward(const NormLaunch& L, cudaStream_t s) {
   const NormArgs a = norm_args(L);
   const bool vec = wide_access(L);
-  if (L.dtype == MX_F32) return vec ? forward_rows<float>(a, s) : forward_any<float, 1>(a, s);
-  return vec ? forward_rows<__nv_bfloat16>(a, s) : forward_any<__nv_bfloat16, 1>(a, s);
+  if (L.dtype == MX_F32) return vec ? forward_rows<float, false>(a, s) : forward_rows<float, true>(a, s);
+  return vec ? forward_rows<__nv_bfloat16, false>(a, s) : forward_rows<__nv_bfloat16, true>(a, s);
 }
 
 mx_status launch_norm_backward(const NormLaunch& L, cudaStream_t s) {
@@ -1077,8 +1220,8 @@ mx_status launch_norm_backward(const NormLaunch& L, cudaStream_t s) {
   a.partial = want ? static_cast<float*>(L.ws) : nullptr;
   int parts = 0;
   mx_status st;
-  if (L.dtype == MX_F32) st = vec ? backward_rows<float>(a, &parts, s) : backward_any<float, 1>(a, &parts, s);
-  else st = vec ? backward_rows<__nv_bfloat16>(a, &parts, s) : backward_any<__nv_bfloat16, 1>(a, &parts, s);
+  if (L.dtype == MX_F32) st = vec ? backward_rows<float, false>(a, &parts, s) : backward_rows<float, true>(a, &parts, s);
+  else st = vec ? backward_rows<__nv_bfloat16, false>(a, &parts, s) : backward_rows<__nv_bfloat16, true>(a, &parts, s);
   if (st != MX_OK || !want) return st;
   return launch_column_reduce(a.partial, parts, L.cols, L.cols, L.dweight, L.dbias, s);
 }
