@@ -748,6 +748,10 @@ __device__ __forceinline__ void store_tile(const OutView& p, const Tile& ti, con
 // acc + bias is stored too where it is wanted.
 // ---------------------------------------------------------------------------
 
+// kEpi of the kernels: 0 none; 1 every box leaves by TMA and the residual's rows
+// allow 16-byte loads; 2 any alignment. Kinds of their own because the element
+// paths of the second would cost the first one registers, which it has none to
+// spare of.
 struct EpiNone {};
 struct EpiArgs {
   CUtensorMap z;   // pre-activation, as the output's map
@@ -755,10 +759,10 @@ struct EpiArgs {
   int32_t z_tma;   // as GParams' c_tma, for the pre-activation
   int32_t r_vec;   // 1: every residual row start is 16-byte aligned
 };
-template <bool kEpi>
-struct EpiParamT { using type = EpiNone; };
+template <int kEpi>
+struct EpiParamT { using type = EpiArgs; };
 template <>
-struct EpiParamT<true> { using type = EpiArgs; };
+struct EpiParamT<0> { using type = EpiNone; };
 
 // Before a tile's accumulator is ready: asks L2 for this warp's part of the
 // residual (lane = row, one 128-byte line at a time) and returns the bias of
@@ -798,15 +802,16 @@ __device__ __forceinline__ void epi_wait_box(bool turns, int lane) {
 
 // The box's rows from shared memory, a lane per column: neighbouring lanes write
 // neighbouring elements (a lane per row would touch 32 rows a store).
-__device__ __noinline__ void epi_store_elements(__nv_bfloat16* dst, int64_t ldc, int rows, int lane, const uint8_t* box) {
+__device__ __forceinline__ void epi_store_elements(__nv_bfloat16* dst, int64_t ldc, int rows, int lane, const uint8_t* box) {
 #pragma unroll 8
   for (int k = 0; k < rows; ++k, dst += ldc)
     *dst = *reinterpret_cast<const __nv_bfloat16*>(box + k * 64 + (((lane >> 3) ^ ((k >> 1) & 3)) << 4) + (lane & 7) * 2);
 }
 
+template <int kEpi>
 __device__ __forceinline__ void epi_store_box(const OutView& o, const CUtensorMap* map, const Tile& ti, const float2* r,
                                               int quarter, int lane, int col, uint8_t* box, bool turns) {
-  if (o.c_tma) {
+  if (kEpi == 1 || o.c_tma) {
     epi_wait_box(turns, lane);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -871,9 +876,7 @@ __device__ __forceinline__ void epi_fetch_residual(const GParams& p, const EpiAr
 }
 
 // The same box straight into shared memory, row by row with a lane per column.
-// Not inlined, like the element stores above: inlined, they would cost the TMA
-// path registers.
-__device__ __noinline__ void epi_copy_residual(const GParams& p, const EpiArgs& ea, const Tile& ti, int quarter,
+__device__ __forceinline__ void epi_copy_residual(const GParams& p, const EpiArgs& ea, const Tile& ti, int quarter,
                                                   int lane, int col, uint8_t* box) {
   const GemmEpilogue& e = ea.e;
   const int rows = min(32, ti.valid_m - quarter * 32);
@@ -899,7 +902,7 @@ __device__ __noinline__ void epi_copy_residual(const GParams& p, const EpiArgs& 
 // shared memory), the pre-activation's box, activation, residual (through the
 // box that its sum leaves by), the output's box. With two boxes the
 // pre-activation and the output have one each.
-template <int kCols, int kBufs>
+template <int kEpi, int kCols, int kBufs>
 __device__ __forceinline__ void epi_tile(const GParams& p, const EpiArgs& ea, const Tile& ti, uint32_t* r, float4 bias,
                                          int quarter, int lane, int my_chunks, int col_off, uint8_t* stg, float* s_bias,
                                          const CUtensorMap* tmap_c) {
@@ -916,9 +919,9 @@ __device__ __forceinline__ void epi_tile(const GParams& p, const EpiArgs& ea, co
   // Two boxes take turns: the pre-activation's and the output's, or, with
   // neither pre-activation nor residual, the output's in both.
   const bool swap = kBufs == 2 && !e.preact && !e.residual;
-  const bool turns = swap || (kBufs == 2 && e.preact && ea.z_tma && p.c_tma);
+  const bool turns = swap || (kBufs == 2 && e.preact && (kEpi == 1 || (ea.z_tma && p.c_tma)));
   uint4 res[4];
-  if (e.residual && ea.r_vec) epi_fetch_residual(p, ea, ti, quarter, lane, col_off, res);
+  if (e.residual && (kEpi == 1 || ea.r_vec)) epi_fetch_residual(p, ea, ti, quarter, lane, col_off, res);
 #pragma unroll
   for (int ch = 0; ch < kCols / 32; ++ch) {
     if (ch >= my_chunks) break;
@@ -935,13 +938,13 @@ __device__ __forceinline__ void epi_tile(const GParams& p, const EpiArgs& ea, co
         v[2 * i + 1] = __fadd2_rn(v[2 * i + 1], make_float2(b.z, b.w));
       }
     }
-    if (e.preact) epi_store_box(zv, &ea.z, ti, v, quarter, lane, col, box_z, turns);
+    if (e.preact) epi_store_box<kEpi>(zv, &ea.z, ti, v, quarter, lane, col, box_z, turns);
     if (e.act == MX_ACT_GELU) epi_activate<MX_ACT_GELU>(v);
     else if (e.act == MX_ACT_SILU) epi_activate<MX_ACT_SILU>(v);
     else if (e.act == MX_ACT_RELU) epi_activate<MX_ACT_RELU>(v);
     if (e.residual) {
       epi_wait_box(turns, lane);
-      if (ea.r_vec) {
+      if (kEpi == 1 || ea.r_vec) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int rr = q * 8 + (lane >> 2);
@@ -962,7 +965,7 @@ __device__ __forceinline__ void epi_tile(const GParams& p, const EpiArgs& ea, co
       }
       __syncwarp();
     }
-    epi_store_box(out, tmap_c, ti, v, quarter, lane, col, swap && (ch & 1) ? box_z : box_c, turns);
+    epi_store_box<kEpi>(out, tmap_c, ti, v, quarter, lane, col, swap && (ch & 1) ? box_z : box_c, turns);
   }
 }
 
@@ -970,7 +973,7 @@ __device__ __forceinline__ void epi_tile(const GParams& p, const EpiArgs& ea, co
 // Single-CTA kernel (dense and grouped)
 // ===========================================================================
 
-template <int BN, int KIND, bool kEpi>
+template <int BN, int KIND, int kEpi>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gemm_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
                    const __grid_constant__ CUtensorMap tmap_c, const GParams p,
@@ -1248,7 +1251,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc_phase ^= 1;
       }
       if constexpr (kEpi)
-        epi_tile<kCols, 1>(p, epi, ti, r, bias, quarter, lane, my_chunks, col_off, stg, s_bias, &tmap_c);
+        epi_tile<kEpi, kCols, 1>(p, epi, ti, r, bias, quarter, lane, my_chunks, col_off, stg, s_bias, &tmap_c);
       else store_tile<KIND, kCols>(out_view(p, ti), ti, r, quarter, lane, my_chunks, col_off, stg, &tmap_c);
     }
     // Bulk stores must have completed before the CTA's shared memory goes away.
@@ -1301,15 +1304,15 @@ __device__ __forceinline__ int problem_of(const PairArgs& args, int64_t t) {
 
 // kSwiGLU_: 0 none; 1 the SwiGLU epilogue writes its BF16 output; 2 it writes
 // the output's MX copies instead.
-// kEpi: the bias / activation / residual epilogue (one dense problem, whole tiles).
-template <int KIND, int kSwiGLU_, bool kMulti, int BN_, bool kTS, bool kEpi>
+// kEpi != 0: the bias / activation / residual epilogue (one dense problem, whole tiles).
+template <int KIND, int kSwiGLU_, bool kMulti, int BN_, bool kTS, int kEpi>
 __global__ void __launch_bounds__(kPairThreads, 1)
     mx_gemm_pair_kernel(const __grid_constant__ PairArgs args,
                         const __grid_constant__ typename EpiParamT<kEpi>::type epi) {
   static_assert(!kEpi || (KIND == GEMM_DENSE && !kSwiGLU_ && !kMulti && !kTS), "dense, block-scaled, one problem");
   constexpr bool kSwiGLU = kSwiGLU_ != 0;
   constexpr bool kSwiQ = kSwiGLU_ == 2;
-  using C = PairCfgT<BN_, kTS, KIND != GEMM_DENSE, kEpi>;
+  using C = PairCfgT<BN_, kTS, KIND != GEMM_DENSE, kEpi != 0>;
   static_assert(!kMulti || (KIND == GEMM_DENSE && !kSwiGLU), "several problems per launch: dense GEMMs only");
   // Problem 0 holds the fields every problem shares (status word, wait bound)
   // and, unless kMulti, the whole GEMM.
@@ -1749,7 +1752,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           store_tile<KIND, 64, C::kEpiBufs>(out_view(pp, ti), ti, r, quarter, lane, 2, 64 * half, stg, &args.prob[pi].c);
         }
       } else if constexpr (kEpi) {
-        epi_tile<kCols, C::kEpiBufs>(pp, epi, ti, r, bias, quarter, lane, kCols / 32, col_off, stg, s_bias,
+        epi_tile<kEpi, kCols, C::kEpiBufs>(pp, epi, ti, r, bias, quarter, lane, kCols / 32, col_off, stg, s_bias,
                                      &args.prob[pi].c);
       } else {
         store_tile<KIND, kCols, C::kEpiBufs>(out_view(pp, ti), ti, r, quarter, lane, kCols / 32, col_off, stg, &args.prob[pi].c);
@@ -2177,10 +2180,20 @@ void output_map(const GemmLaunch& L, GParams& p, CUtensorMap* mc, int kind) {
   }
 }
 
+// Which epilogue kernel a GEMM takes (EpiNone).
+int epi_kind(const GemmLaunch& L) {
+  if (!L.has_epi) return 0;
+  const auto aligned = [](const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; };
+  return L.N % 8 == 0 && aligned(L.c, L.ldc) && (!L.epi.preact || aligned(L.epi.preact, L.epi.ld_preact)) &&
+                 (!L.epi.residual || aligned(L.epi.residual, L.epi.ld_residual))
+             ? 1
+             : 2;
+}
+
 // The epilogue's launch argument: the pre-activation's map where it takes TMA
 // stores (the same conditions as the output's).
-template <bool kEpi>
-mx_status epi_args(const GemmLaunch& L, typename EpiParamT<kEpi>::type* a) {
+template <int kEpi>
+mx_status epi_args(const GemmLaunch& L, bool c_tma, typename EpiParamT<kEpi>::type* a) {
   if constexpr (kEpi) {
     std::memset(a, 0, sizeof(*a));
     a->e = L.epi;
@@ -2189,12 +2202,14 @@ mx_status epi_args(const GemmLaunch& L, typename EpiParamT<kEpi>::type* a) {
       const bool vec = (reinterpret_cast<uintptr_t>(L.epi.preact) & 15u) == 0 && L.epi.ld_preact % 8 == 0;
       if (vec && L.N % 8 == 0 && make_out_map(&a->z, L.epi.preact, 1, L.M, L.N, L.epi.ld_preact) == MX_OK)
         a->z_tma = 1;
+      if (kEpi == 1 && !a->z_tma) return MX_ERR_CUDA;  // the encoder's message stands
     }
+    if (kEpi == 1 && !c_tma) return MX_ERR_CUDA;
   }
   return MX_OK;
 }
 
-template <int BN, int KIND, bool kEpi = false>
+template <int BN, int KIND, int kEpi = 0>
 mx_status launch_cfg(const GemmLaunch& L, const GParams& p_in, int64_t tiles_upper, cudaStream_t s) {
   GParams p = p_in;
   CUtensorMap ma, mb, mc;
@@ -2205,7 +2220,7 @@ mx_status launch_cfg(const GemmLaunch& L, const GParams& p_in, int64_t tiles_upp
   output_map(L, p, &mc, KIND);
   const size_t smem = Cfg<BN>::smem_bytes(KIND != GEMM_DENSE) + (kEpi ? kEpiBiasBytes : 0);
   typename EpiParamT<kEpi>::type epi;
-  st = epi_args<kEpi>(L, &epi);
+  st = epi_args<kEpi>(L, p.c_tma != 0, &epi);
   if (st != MX_OK) return st;
   auto kern = mx_gemm_kernel<BN, KIND, kEpi>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -2286,7 +2301,7 @@ PairArgs* pair_args_scratch() {
   return &args;
 }
 
-template <int KIND, int kSwiGLU = 0, int BN = 256, bool kTS = false, bool kEpi = false>
+template <int KIND, int kSwiGLU = 0, int BN = 256, bool kTS = false, int kEpi = 0>
 mx_status launch_pair(const GemmLaunch& L, const GParams& p_in, cudaStream_t s) {
   GParams p = p_in;
   CUtensorMap ma, mb, msa, msb, mc;
@@ -2309,9 +2324,9 @@ mx_status launch_pair(const GemmLaunch& L, const GParams& p_in, cudaStream_t s) 
     if (st != MX_OK) return st;
   }
   output_map(L, p, &mc, KIND);
-  const size_t smem = PairCfgT<BN, kTS, KIND != GEMM_DENSE, kEpi>::smem_bytes();
+  const size_t smem = PairCfgT<BN, kTS, KIND != GEMM_DENSE, kEpi != 0>::smem_bytes();
   typename EpiParamT<kEpi>::type epi;
-  st = epi_args<kEpi>(L, &epi);
+  st = epi_args<kEpi>(L, p.c_tma != 0, &epi);
   if (st != MX_OK) return st;
   auto kern = mx_gemm_pair_kernel<KIND, kSwiGLU, false, BN, kTS, kEpi>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -2319,7 +2334,7 @@ mx_status launch_pair(const GemmLaunch& L, const GParams& p_in, cudaStream_t s) 
   int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(pair_tiles_upper(L, BN), sm_count() / 2));
   PairPlan pl;
   if constexpr (KIND == GEMM_DENSE && BN == 256 && !kTS) {
-    pl = plan_pair_dense(L, !kEpi);
+    pl = plan_pair_dense(L, kEpi == 0);
     if (pl.sk_w > 0 && !split_allowed(L, pl.ws_bytes)) pl = plan_pair_dense(L, false);
     if (pl.sk_w > 0) {
       p.ws = static_cast<float*>(L.ws);
@@ -2618,8 +2633,8 @@ mx_status launch_pair_multi(const GemmLaunch* Ls_in, int n, cudaStream_t s) {
   args->tile0[n] = tiles;
   args->n = n;
   const size_t smem = ts ? PairCfgT<BN, true, false>::smem_bytes() : PairCfgT<BN, false, false>::smem_bytes();
-  auto kern = ts ? mx_gemm_pair_kernel<GEMM_DENSE, 0, true, BN, true, false>
-                 : mx_gemm_pair_kernel<GEMM_DENSE, 0, true, BN, false, false>;
+  auto kern = ts ? mx_gemm_pair_kernel<GEMM_DENSE, 0, true, BN, true, 0>
+                 : mx_gemm_pair_kernel<GEMM_DENSE, 0, true, BN, false, 0>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(pair smem)");
   const int64_t clusters = std::max<int64_t>(1, std::min<int64_t>(tiles, sm_count() / 2));
@@ -2657,10 +2672,13 @@ mx_status launch_gemm(const GemmLaunch& L, cudaStream_t s) {
   }
   if (L.swiglu) return L.q_row_data ? launch_pair<GEMM_GROUPED_M, 2>(L, p, s) : launch_pair<GEMM_GROUPED_M, 1>(L, p, s);
   int bn;
+  const int epi = epi_kind(L);
   if (L.kind == GEMM_DENSE) {
     const int cfg = choose_dense_cfg(L);
     if (cfg == CFG_PAIR)
-      return L.has_epi ? launch_pair<GEMM_DENSE, 0, 256, false, true>(L, p, s) : launch_pair<GEMM_DENSE>(L, p, s);
+      return epi == 0 ? launch_pair<GEMM_DENSE>(L, p, s)
+             : epi == 1 ? launch_pair<GEMM_DENSE, 0, 256, false, 1>(L, p, s)
+                        : launch_pair<GEMM_DENSE, 0, 256, false, 2>(L, p, s);
     bn = cfg == CFG_BN256 ? 256 : 128;
   } else {
     if (use_pairs(L))
@@ -2675,9 +2693,12 @@ mx_status launch_gemm(const GemmLaunch& L, cudaStream_t s) {
 
   switch (L.kind) {
     case GEMM_DENSE:
-      if (L.has_epi)
-        return bn == 256 ? launch_cfg<256, GEMM_DENSE, true>(L, p, tiles_upper, s)
-                         : launch_cfg<128, GEMM_DENSE, true>(L, p, tiles_upper, s);
+      if (epi == 1)
+        return bn == 256 ? launch_cfg<256, GEMM_DENSE, 1>(L, p, tiles_upper, s)
+                         : launch_cfg<128, GEMM_DENSE, 1>(L, p, tiles_upper, s);
+      if (epi == 2)
+        return bn == 256 ? launch_cfg<256, GEMM_DENSE, 2>(L, p, tiles_upper, s)
+                         : launch_cfg<128, GEMM_DENSE, 2>(L, p, tiles_upper, s);
       return bn == 256 ? launch_cfg<256, GEMM_DENSE>(L, p, tiles_upper, s)
                        : launch_cfg<128, GEMM_DENSE>(L, p, tiles_upper, s);
     case GEMM_GROUPED_M:
