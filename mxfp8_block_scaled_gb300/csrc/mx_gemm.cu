@@ -139,15 +139,16 @@ struct Cfg {
 #ifndef MX_PAIR_EPI_BUFS
 #define MX_PAIR_EPI_BUFS 1
 #endif
-// kEpi (bias / activation / residual epilogue): a stage less makes room for two
-// staging boxes per epilogue warp and its bias.
+// kEpi (bias / activation / residual epilogue) adds room for the bias. (A stage
+// less and two staging boxes per epilogue warp measured 2% slower: 148 against
+// 145 us at 8192 x 10944 x 2048 with GELU and pre-activation.)
 template <int BN_, bool kTS_, bool kGrouped_, bool kEpi_ = false>
 struct PairCfgT {
   static constexpr int BN = BN_;
   static constexpr bool kTS = kTS_;
   static_assert(BN == 256, "pair tiles are 256 wide");
-  static constexpr int kStages = kEpi_ ? MX_PAIR_STAGES - 1 : MX_PAIR_STAGES;
-  static constexpr int kEpiBufs = kEpi_ ? 2 : MX_PAIR_EPI_BUFS;  // staging boxes per epilogue warp
+  static constexpr int kStages = MX_PAIR_STAGES;
+  static constexpr int kEpiBufs = MX_PAIR_EPI_BUFS;  // staging boxes per epilogue warp
   static constexpr int kABytes = kBM * kBK;
   static constexpr int kBBytes = (BN / 2) * kBK;
   static constexpr int kSfaBytes = kTS ? 0 : 512;
@@ -791,12 +792,9 @@ __device__ __forceinline__ float4 epi_prepare(const GParams& p, const EpiArgs& e
 // One 32 x 32 box of a warp to its place: `r` the FP32 values of the lane's
 // row. Through the staging box and TMA where the output allows it (rows and
 // columns outside it are clipped), else with bounded element stores. A box is
-// written again once its last store has been read out; `turns`: the warp's last
-// store was the other box's and may still be in flight.
-__device__ __forceinline__ void epi_wait_box(bool turns, int lane) {
-  if (lane == 0) {
-    if (turns) bulk_wait_read_one_pending(); else bulk_wait_read_all();
-  }
+// written again once its last store has been read out.
+__device__ __forceinline__ void epi_wait_box(int lane) {
+  if (lane == 0) bulk_wait_read_all();
   __syncwarp();
 }
 
@@ -810,9 +808,9 @@ __device__ __forceinline__ void epi_store_elements(__nv_bfloat16* dst, int64_t l
 
 template <int kEpi>
 __device__ __forceinline__ void epi_store_box(const OutView& o, const CUtensorMap* map, const Tile& ti, const float2* r,
-                                              int quarter, int lane, int col, uint8_t* box, bool turns) {
+                                              int quarter, int lane, int col, uint8_t* box) {
   if (kEpi == 1 || o.c_tma) {
-    epi_wait_box(turns, lane);
+    epi_wait_box(lane);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       uint4 w;
@@ -830,7 +828,7 @@ __device__ __forceinline__ void epi_store_box(const OutView& o, const CUtensorMa
     }
     return;
   }
-  epi_wait_box(false, lane);
+  epi_wait_box(lane);
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     st_shared_v4(box + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4),
@@ -900,26 +898,19 @@ __device__ __forceinline__ void epi_copy_residual(const GParams& p, const EpiArg
 // r: kCols FP32 accumulators of row quarter * 32 + lane from column n0 +
 // col_off, worked on 32 columns at a time: bias (broadcast reads of the warp's
 // shared memory), the pre-activation's box, activation, residual (through the
-// box that its sum leaves by), the output's box. With two boxes the
-// pre-activation and the output have one each.
-template <int kEpi, int kCols, int kBufs>
+// box that its sum leaves by), the output's box.
+template <int kEpi, int kCols>
 __device__ __forceinline__ void epi_tile(const GParams& p, const EpiArgs& ea, const Tile& ti, uint32_t* r, float4 bias,
                                          int quarter, int lane, int my_chunks, int col_off, uint8_t* stg, float* s_bias,
                                          const CUtensorMap* tmap_c) {
   const GemmEpilogue& e = ea.e;
   const OutView out = out_view(p, ti);
   const OutView zv{static_cast<__nv_bfloat16*>(e.preact) + ti.m0 * e.ld_preact + ti.n0, e.ld_preact, p.N, 0, ea.z_tma};
-  uint8_t* box_z = stg;
-  uint8_t* box_c = stg + (kBufs == 2 ? kEpiWarpBytes : 0);
   if (e.bias) {
     __syncwarp();  // the last tile's reads
     reinterpret_cast<float4*>(s_bias)[lane] = bias;
     __syncwarp();
   }
-  // Two boxes take turns: the pre-activation's and the output's, or, with
-  // neither pre-activation nor residual, the output's in both.
-  const bool swap = kBufs == 2 && !e.preact && !e.residual;
-  const bool turns = swap || (kBufs == 2 && e.preact && (kEpi == 1 || (ea.z_tma && p.c_tma)));
   uint4 res[4];
   if (e.residual && (kEpi == 1 || ea.r_vec)) epi_fetch_residual(p, ea, ti, quarter, lane, col_off, res);
 #pragma unroll
@@ -938,26 +929,26 @@ __device__ __forceinline__ void epi_tile(const GParams& p, const EpiArgs& ea, co
         v[2 * i + 1] = __fadd2_rn(v[2 * i + 1], make_float2(b.z, b.w));
       }
     }
-    if (e.preact) epi_store_box<kEpi>(zv, &ea.z, ti, v, quarter, lane, col, box_z, turns);
+    if (e.preact) epi_store_box<kEpi>(zv, &ea.z, ti, v, quarter, lane, col, stg);
     if (e.act == MX_ACT_GELU) epi_activate<MX_ACT_GELU>(v);
     else if (e.act == MX_ACT_SILU) epi_activate<MX_ACT_SILU>(v);
     else if (e.act == MX_ACT_RELU) epi_activate<MX_ACT_RELU>(v);
     if (e.residual) {
-      epi_wait_box(turns, lane);
+      epi_wait_box(lane);
       if (kEpi == 1 || ea.r_vec) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int rr = q * 8 + (lane >> 2);
-          st_shared_v4(box_c + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4), res[q]);
+          st_shared_v4(stg + rr * 64 + (((lane & 3) ^ ((rr >> 1) & 3)) << 4), res[q]);
         }
         if (ch + 1 < my_chunks) epi_fetch_residual(p, ea, ti, quarter, lane, col + 32, res);
       } else {
-        epi_copy_residual(p, ea, ti, quarter, lane, col, box_c);
+        epi_copy_residual(p, ea, ti, quarter, lane, col, stg);
       }
       __syncwarp();
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const uint4 x = ld_shared_v4(box_c + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4));
+        const uint4 x = ld_shared_v4(stg + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4));
         v[4 * q + 0] = __fadd2_rn(v[4 * q + 0], make_float2(lo_f(x.x), hi_f(x.x)));
         v[4 * q + 1] = __fadd2_rn(v[4 * q + 1], make_float2(lo_f(x.y), hi_f(x.y)));
         v[4 * q + 2] = __fadd2_rn(v[4 * q + 2], make_float2(lo_f(x.z), hi_f(x.z)));
@@ -965,7 +956,7 @@ __device__ __forceinline__ void epi_tile(const GParams& p, const EpiArgs& ea, co
       }
       __syncwarp();
     }
-    epi_store_box<kEpi>(out, tmap_c, ti, v, quarter, lane, col, swap && (ch & 1) ? box_z : box_c, turns);
+    epi_store_box<kEpi>(out, tmap_c, ti, v, quarter, lane, col, stg);
   }
 }
 
@@ -1251,7 +1242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc_phase ^= 1;
       }
       if constexpr (kEpi)
-        epi_tile<kEpi, kCols, 1>(p, epi, ti, r, bias, quarter, lane, my_chunks, col_off, stg, s_bias, &tmap_c);
+        epi_tile<kEpi, kCols>(p, epi, ti, r, bias, quarter, lane, my_chunks, col_off, stg, s_bias, &tmap_c);
       else store_tile<KIND, kCols>(out_view(p, ti), ti, r, quarter, lane, my_chunks, col_off, stg, &tmap_c);
     }
     // Bulk stores must have completed before the CTA's shared memory goes away.
@@ -1752,7 +1743,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
           store_tile<KIND, 64, C::kEpiBufs>(out_view(pp, ti), ti, r, quarter, lane, 2, 64 * half, stg, &args.prob[pi].c);
         }
       } else if constexpr (kEpi) {
-        epi_tile<kEpi, kCols, C::kEpiBufs>(pp, epi, ti, r, bias, quarter, lane, kCols / 32, col_off, stg, s_bias,
+        epi_tile<kEpi, kCols>(pp, epi, ti, r, bias, quarter, lane, kCols / 32, col_off, stg, s_bias,
                                      &args.prob[pi].c);
       } else {
         store_tile<KIND, kCols, C::kEpiBufs>(out_view(pp, ti), ti, r, quarter, lane, kCols / 32, col_off, stg, &args.prob[pi].c);

@@ -31,7 +31,9 @@
 //   whole block reads back as not finite.
 //
 // Both kernels are bound by HBM: 26 or 28 bytes per parameter with 32-bit
-// states, 14.1 or 16.1 with 8-bit ones (BF16 or FP32 gradients).
+// states, 14.1 or 16.1 with 8-bit ones (BF16 or FP32 gradients). The 8-bit one
+// comes close to the issue rate as well, hence its packed conversions and its
+// special-function forms without scaling code.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -97,19 +99,24 @@ __host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {  // MurmurHash3
   return x ^ (x >> 16);
 }
 
-__device__ __forceinline__ float sqrt_approx(float x) {
-  float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
+// The new moments, and the parameter from them. kTinyEps = false: a v below
+// 2^-126, whose root (below 2^-63) is then taken as zero, is lost beside eps
+// anyway (eps >= 2^25 * 2^-63 * rs), and the reciprocal needs no scaling.
+template <bool kTinyEps>
 __device__ __forceinline__ void adamw_update(float& p, float g, float& m, float& v, const OptHyper& h, float gs,
                                              float decay) {
   g = __fmul_rn(g, gs);
   m = __fadd_rn(__fmul_rn(m, h.b1), __fmul_rn(g, h.c1));
   v = __fadd_rn(__fmul_rn(v, h.b2), __fmul_rn(__fmul_rn(g, g), h.c2));
-  const float den = fmaf(sqrt_approx(v), h.rs, h.eps);
-  p = fmaf(p, decay, -h.step * __fdividef(m, den));
+  float root, inv;
+  if constexpr (kTinyEps) {
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(root) : "f"(v));
+    p = fmaf(p, decay, -h.step * __fdividef(m, fmaf(root, h.rs, h.eps)));
+  } else {
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(root) : "f"(v));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(fmaf(root, h.rs, h.eps)));
+    p = fmaf(-h.step, m * inv, p * decay);
+  }
 }
 
 __device__ __forceinline__ float load_grad(const OptTensor& t, int64_t i) {
@@ -139,7 +146,7 @@ __device__ __forceinline__ bool grad_scale_of(const OptHyper& h, float& gs) {
 }
 
 // 32-bit states: a thread takes two float4 of its CTA's unit, 256 float4 apart.
-template <int kCap>
+template <int kCap, bool kTinyEps>
 __global__ void __launch_bounds__(kOptThreads) adamw32_kernel(const __grid_constant__ OptArgs<kCap> a) {
   pdl_launch_dependents();
   pdl_wait();
@@ -170,10 +177,10 @@ __global__ void __launch_bounds__(kOptThreads) adamw32_kernel(const __grid_const
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int64_t i = base + (u * kOptThreads + threadIdx.x) * 4;
-        adamw_update(p4[u].x, g4[u].x, m4[u].x, v4[u].x, a.h, gs, t.decay);
-        adamw_update(p4[u].y, g4[u].y, m4[u].y, v4[u].y, a.h, gs, t.decay);
-        adamw_update(p4[u].z, g4[u].z, m4[u].z, v4[u].z, a.h, gs, t.decay);
-        adamw_update(p4[u].w, g4[u].w, m4[u].w, v4[u].w, a.h, gs, t.decay);
+        adamw_update<kTinyEps>(p4[u].x, g4[u].x, m4[u].x, v4[u].x, a.h, gs, t.decay);
+        adamw_update<kTinyEps>(p4[u].y, g4[u].y, m4[u].y, v4[u].y, a.h, gs, t.decay);
+        adamw_update<kTinyEps>(p4[u].z, g4[u].z, m4[u].z, v4[u].z, a.h, gs, t.decay);
+        adamw_update<kTinyEps>(p4[u].w, g4[u].w, m4[u].w, v4[u].w, a.h, gs, t.decay);
         *reinterpret_cast<float4*>(t.p + i) = p4[u];
         *reinterpret_cast<float4*>(m + i) = m4[u];
         *reinterpret_cast<float4*>(v + i) = v4[u];
@@ -182,7 +189,7 @@ __global__ void __launch_bounds__(kOptThreads) adamw32_kernel(const __grid_const
       const int64_t end = min64(base + kChunk, t.n);
       for (int64_t i = base + threadIdx.x; i < end; i += kOptThreads) {
         float pi = t.p[i], mi = m[i], vi = v[i];
-        adamw_update(pi, load_grad(t, i), mi, vi, a.h, gs, t.decay);
+        adamw_update<kTinyEps>(pi, load_grad(t, i), mi, vi, a.h, gs, t.decay);
         t.p[i] = pi;
         m[i] = mi;
         v[i] = vi;
@@ -194,21 +201,40 @@ __global__ void __launch_bounds__(kOptThreads) adamw32_kernel(const __grid_const
 // 8-bit states: a warp takes one state block of 256 elements, eight a lane
 // (eight neighbours where the pointers allow wide accesses, else every 32nd),
 // so a block's amax is one warp reduction and its codes are written once.
-__device__ __forceinline__ uint32_t encode_v(float v, float inv, uint32_t rand) {
-  const int32_t c = static_cast<int32_t>((__float_as_uint(__fmul_rn(v, inv)) + (rand & 0xFFFFFu)) >> 20) - 761;
-  return v > 0.0f ? static_cast<uint32_t>(min(max(c, 1), 255)) : 0u;
+
+// Code of a second moment, to be saturated at 255: v / amax's FP32 bits down to
+// three bits of mantissa, the random bits deciding which way; at least 1 for a
+// positive v, 0 for 0 (whatever 0 * inv is).
+__device__ __forceinline__ int32_t code_v(float v, float inv, uint32_t rand) {
+  const int32_t c = static_cast<int32_t>(__float_as_uint(__fmul_rn(v, inv)) + (rand & 0xFFFFFu) - (761u << 20)) >> 20;
+  return max(c, 1) * static_cast<int32_t>(min(__float_as_uint(v), 1u));
+}
+
+// Four codes as bytes, each saturated to 0 .. 255.
+__device__ __forceinline__ uint32_t pack_codes(int32_t a, int32_t b, int32_t c, int32_t d) {
+  uint32_t hi, r;
+  asm("cvt.pack.sat.u8.s32.b32 %0, %1, %2, 0;" : "=r"(hi) : "r"(d), "r"(c));
+  asm("cvt.pack.sat.u8.s32.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(b), "r"(a), "r"(hi));
+  return r;
 }
 
 __device__ __forceinline__ float decode_v(uint32_t c, float scale) {
-  return __fmul_rn(c ? __uint_as_float((c + 761u) << 20) : 0.0f, scale);
+  return __fmul_rn(c ? __uint_as_float((c << 20) + (761u << 20)) : 0.0f, scale);
 }
 
-__device__ __forceinline__ float decode_e4m3(uint32_t c) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(c), __NV_E4M3);
-  return __half2float(__half(h));
+// Two E4M3 codes (the low 16 bits).
+__device__ __forceinline__ float2 decode_e4m3(uint32_t c) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c), __NV_E4M3);
+  return __half22float2(__half2(h));
 }
 
-template <int kCap>
+__device__ __forceinline__ float max_magnitude(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+
+template <int kCap, bool kTinyEps>
 __global__ void __launch_bounds__(kOptThreads) adamw8_kernel(const __grid_constant__ OptArgs<kCap> a) {
   pdl_launch_dependents();
   pdl_wait();
@@ -226,7 +252,6 @@ __global__ void __launch_bounds__(kOptThreads) adamw8_kernel(const __grid_consta
     uint8_t* vc = static_cast<uint8_t*>(t.v);
     const bool vec = t.vec && base + kStateBlock <= t.n;
     const int64_t i0 = base + (vec ? lane * 8 : lane);
-    const int stride = vec ? 1 : 32;
     const float ms = t.m_scale[blk], vs = t.v_scale[blk];
     float p[8], g[8], m[8], v[8];
     if (vec) {
@@ -243,10 +268,13 @@ __global__ void __launch_bounds__(kOptThreads) adamw8_kernel(const __grid_consta
       }
       p[0] = p0.x, p[1] = p0.y, p[2] = p0.z, p[3] = p0.w, p[4] = p1.x, p[5] = p1.y, p[6] = p1.z, p[7] = p1.w;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        m[j] = __fmul_rn(decode_e4m3(((j < 4 ? mw.x : mw.y) >> (8 * (j & 3))) & 0xFFu), ms);
-        v[j] = decode_v(((j < 4 ? vw.x : vw.y) >> (8 * (j & 3))) & 0xFFu, vs);
+      for (int j = 0; j < 8; j += 2) {
+        const float2 d = decode_e4m3((j < 4 ? mw.x : mw.y) >> (8 * (j & 2)));
+        m[j] = __fmul_rn(d.x, ms);
+        m[j + 1] = __fmul_rn(d.y, ms);
       }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = decode_v(((j < 4 ? vw.x : vw.y) >> (8 * (j & 3))) & 0xFFu, vs);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -254,27 +282,29 @@ __global__ void __launch_bounds__(kOptThreads) adamw8_kernel(const __grid_consta
         const bool in = i < t.n;  // past the end: zeros, which leave the block's amax alone
         p[j] = in ? t.p[i] : 0.0f;
         g[j] = in ? load_grad(t, i) : 0.0f;
-        m[j] = in ? __fmul_rn(decode_e4m3(mc[i]), ms) : 0.0f;
+        m[j] = in ? __fmul_rn(decode_e4m3(mc[i]).x, ms) : 0.0f;
         v[j] = in ? decode_v(vc[i], vs) : 0.0f;
       }
     }
-    uint32_t m_bits = 0, v_bits = 0;  // the largest magnitudes as integers: NaN above infinity above finite
+    // The largest magnitudes, compared as integers (NaN above infinity above finite).
+    float m_most = 0.0f;
+    uint32_t v_bits = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      adamw_update(p[j], g[j], m[j], v[j], a.h, gs, t.decay);
-      m_bits = max(m_bits, __float_as_uint(m[j]) & 0x7FFFFFFFu);
-      v_bits = max(v_bits, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+      adamw_update<kTinyEps>(p[j], g[j], m[j], v[j], a.h, gs, t.decay);
+      m_most = max_magnitude(m_most, m[j]);
+      v_bits = max(v_bits, __float_as_uint(v[j]));
     }
-    const float m_amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, m_bits));
-    const float v_amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, v_bits));
+    const float m_amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(m_most) & 0x7FFFFFFFu));
+    const float v_amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, v_bits & 0x7FFFFFFFu));
     const bool tiny = m_amax < 7.888609052210118e-31f;  // 2^-100
     const float m_inv = tiny ? 0.0f : __fmul_rn(__frcp_rn(m_amax), 448.0f);
     const float v_inv = __frcp_rn(v_amax);
-    uint32_t vq[8];
+    const uint32_t key = static_cast<uint32_t>(i0) + t.key + static_cast<uint32_t>(i0 >> 32) * 0x9E3779B9u;
+    int32_t vq[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int64_t i = i0 + static_cast<int64_t>(j) * stride;
-      vq[j] = encode_v(v[j], v_inv, mix32(static_cast<uint32_t>(i) + t.key + static_cast<uint32_t>(i >> 32) * 0x9E3779B9u));
+      vq[j] = code_v(v[j], v_inv, mix32(key + static_cast<uint32_t>(vec ? j : j * 32)));
       m[j] = __fmul_rn(m[j], m_inv);
     }
     if (lane == 0) {
@@ -286,8 +316,8 @@ __global__ void __launch_bounds__(kOptThreads) adamw8_kernel(const __grid_consta
       *reinterpret_cast<float4*>(t.p + i0 + 4) = make_float4(p[4], p[5], p[6], p[7]);
       *reinterpret_cast<uint2*>(mc + i0) = make_uint2(cvt_pair(m[0], m[1]) | cvt_pair(m[2], m[3]) << 16,
                                                       cvt_pair(m[4], m[5]) | cvt_pair(m[6], m[7]) << 16);
-      *reinterpret_cast<uint2*>(vc + i0) = make_uint2(vq[0] | vq[1] << 8 | vq[2] << 16 | vq[3] << 24,
-                                                      vq[4] | vq[5] << 8 | vq[6] << 16 | vq[7] << 24);
+      *reinterpret_cast<uint2*>(vc + i0) =
+          make_uint2(pack_codes(vq[0], vq[1], vq[2], vq[3]), pack_codes(vq[4], vq[5], vq[6], vq[7]));
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -295,7 +325,7 @@ __global__ void __launch_bounds__(kOptThreads) adamw8_kernel(const __grid_consta
         if (i < t.n) {
           t.p[i] = p[j];
           mc[i] = static_cast<uint8_t>(cvt_pair(m[j], 0.0f));
-          vc[i] = static_cast<uint8_t>(vq[j]);
+          vc[i] = static_cast<uint8_t>(min(max(vq[j], 0), 255));
         }
       }
     }
@@ -347,8 +377,11 @@ mx_status launch_adamw_cap(const mx_adamw_tensor* tensors, int first, int n, int
   if (k == 0) return MX_OK;
   a.h.n = k;
   a.h.chunks = static_cast<int32_t>(chunks);
-  const int64_t grid = std::min<int64_t>(chunks, static_cast<int64_t>(sm_count()) * 8);
-  auto kern = bits == 8 ? adamw8_kernel<kCap> : adamw32_kernel<kCap>;
+  // More CTAs than fit at once: the last round is then short.
+  const int64_t grid = std::min<int64_t>(chunks, static_cast<int64_t>(sm_count()) * 16);
+  const bool tiny_eps = a.h.eps < a.h.rs * 3.637978807091713e-12f;  // 2^-38
+  auto kern = bits == 8 ? (tiny_eps ? adamw8_kernel<kCap, true> : adamw8_kernel<kCap, false>)
+                        : (tiny_eps ? adamw32_kernel<kCap, true> : adamw32_kernel<kCap, false>);
   return cuda_status(launch_kernel(kern, static_cast<unsigned>(grid), kOptThreads, 0, s, 1, a), "mx_adamw_step launch");
 }
 

@@ -327,3 +327,20 @@ def test_minimises_a_quadratic_with_either_states():
             mx.adamw_step([p], [p - target], [s], lr=0.05, step=t, seed=t)
         ends.append(float((p - target).norm() / target.norm()))
     assert ends[0] < 0.02 and ends[1] < 0.02, ends
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_no_eps_and_tiny_gradients(bits):
+    """eps = 0: the first step moves by lr however small the gradient, down to
+    squares below FP32's smallest normal number."""
+    g = torch.tensor([1e-3, -1e-10, 1e-17, -3e-19, 1.0], device="cuda")
+    p = torch.zeros(5, device="cuda")
+    s = mx.adamw_state(p, 32)
+    mx.adamw_step([p], [g], [s], lr=0.5, eps=0.0, step=1)
+    # v = 0.001 g^2 keeps 23 bits down to 2^-126, then loses them: 1e-17 -> 1e-37, 3e-19 -> 9e-41 (16 bits left)
+    assert torch.allclose(p, -0.5 * g.sign(), rtol=1e-4, atol=0), p
+    if bits == 8:
+        big = torch.full((512,), 1e-2, device="cuda")
+        q, t = torch.zeros(512, device="cuda"), mx.adamw_state(big, 8)
+        mx.adamw_step([q], [big], [t], lr=0.5, eps=0.0, step=1)
+        assert torch.allclose(q, torch.full_like(q, -0.5), rtol=1e-5)
