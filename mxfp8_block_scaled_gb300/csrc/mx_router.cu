@@ -208,21 +208,29 @@ __global__ void __launch_bounds__(kRouterThreads, EPL == 8 ? 4 : 2) router_forwa
 #pragma unroll
   for (int i = 0; i < EPL; ++i) psum[i] = 0.0f;
   int32_t valid = 0;
-  // The next token's row is on its way while this one is worked on.
+  // The next token's row is on its way while this one is worked on. Places move
+  // on by fixed steps: row, choices and weights of token t0 + sub.
+  constexpr int kStep = kRouterWarps * TPW;
+  const int64_t t0 = run.first + warp * TPW + sub;
+  const int tokens = static_cast<int>(run.end - run.first);
+  const T* row = static_cast<const T*>(a.logits) + t0 * a.ld;
+  const uint8_t* live_at = a.mask ? a.mask + t0 : nullptr;
+  int32_t* idx = a.indices + t0 * a.top_k;
+  float* w = a.weights + t0 * a.top_k;
+  const int64_t row_step = kStep * a.ld;
+  const int choice_step = kStep * a.top_k;
+  const bool few = a.top_k <= LPT;  // a lane has one choice at most
   float ahead[EPL];
   bool live_ahead;
-  auto fetch = [&](int64_t t) {
+  auto fetch = [&](bool there, const T* from) {
 #pragma unroll
     for (int i = 0; i < EPL; ++i) ahead[i] = -INFINITY;
-    live_ahead = t < run.end && (!a.mask || a.mask[t] != 0);
-    if (live_ahead) load_row<T, EPL>(static_cast<const T*>(a.logits) + t * a.ld, first, a.experts, a.vec, ahead);
+    live_ahead = there && (!a.mask || *live_at != 0);
+    if (live_ahead) load_row<T, EPL>(from, first, a.experts, a.vec, ahead);
   };
-  fetch(run.first + warp * TPW + sub);
-  for (int64_t t0 = run.first + warp * TPW; t0 < run.end; t0 += kRouterWarps * TPW) {
-    const int64_t t = t0 + sub;
-    const bool in = t < run.end;
-    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-    int32_t* idx = a.indices + t * a.top_k;
+  fetch(warp * TPW + sub < tokens, row);
+  for (int q = warp * TPW; q < tokens; q += kStep, row += row_step, idx += choice_step, w += choice_step) {
+    const bool in = q + sub < tokens;
     float x[EPL];  // a token left out is -inf throughout
     uint32_t key[EPL];
     float m = -INFINITY;
@@ -233,24 +241,24 @@ __global__ void __launch_bounds__(kRouterThreads, EPL == 8 ? 4 : 2) router_forwa
       key[i] = (order_key(x[i]) & ~kLow) | (kLow - static_cast<uint32_t>(first + i));
     }
     const bool live = live_ahead;
-    fetch(t + kRouterWarps * TPW);
+    if (a.mask) live_at += kStep;
+    fetch(q + sub + kStep < tokens, row + row_step);
 #pragma unroll
     for (int o = LPT / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
     sort_keys<EPL>(key);
-    uint32_t top = 0, last = 0;
-    int32_t found = 0, mine = -1;  // choices made; the one of round j % LPT == l (kept where top_k <= LPT)
-    bool again = false;
+    // Lane j % LPT holds choice j (the last such one; where there are more, each
+    // is written as it is made).
+    uint32_t last = 0, mine = 0, apart = kFull;
+    uint32_t top = 0;
     for (int j = 0; j < a.top_k; ++j) {
       const uint32_t best = group_max<LPT>(key[0]);
-      if (j == 0) top = best;
-      else if (!kExact) again |= ((best ^ last) & ~kLow) == 0;
+      if (!kExact) apart = min(apart, best ^ last);
       last = best;
-      if (best > kNoKey) {
-        found = j + 1;
-        if (j % LPT == l) {
-          mine = static_cast<int32_t>(kLow - (best & kLow));
-          idx[j] = mine;
-        }
+      if (j == 0) top = best;
+      if (few) {
+        if (j == l) mine = best;
+      } else if (j % LPT == l && in) {
+        idx[j] = best > kNoKey ? static_cast<int32_t>(kLow - (best & kLow)) : -1;
       }
       if (key[0] == best) {  // one lane: keys differ by their experts
 #pragma unroll
@@ -259,11 +267,12 @@ __global__ void __launch_bounds__(kRouterThreads, EPL == 8 ? 4 : 2) router_forwa
       }
     }
     // The first one not chosen may be as close to the last one chosen.
-    if (!kExact) again |= ((group_max<LPT>(key[0]) ^ last) & ~kLow) == 0;
+    if (!kExact) apart = min(apart, group_max<LPT>(key[0]) ^ last);
     bool any = top > kNoKey;
+    int e0 = mine > kNoKey ? static_cast<int>(kLow - (mine & kLow)) : -1;
     // Once more with whole keys, if rounding or a NaN may have changed the
     // choice (a row of -inf alone does not count).
-    again = (again && any) || top >= kInfKey;
+    const bool again = (!kExact && any && apart <= kLow) || top >= kInfKey;
     if (__any_sync(kFull, again || (live && !any))) {
       bool nan = false;
 #pragma unroll
@@ -272,7 +281,6 @@ __global__ void __launch_bounds__(kRouterThreads, EPL == 8 ? 4 : 2) router_forwa
         key[i] = x[i] > -INFINITY ? order_key(x[i]) : 0u;
       }
       any |= group_max<LPT>(nan ? 1u : 0u) != 0;
-      found = 0;
       for (int j = 0; j < a.top_k; ++j) {
         uint32_t best = 0;
         int at = 0;
@@ -284,16 +292,13 @@ __global__ void __launch_bounds__(kRouterThreads, EPL == 8 ? 4 : 2) router_forwa
           }
         const uint32_t most = group_max<LPT>(best);
         const uint32_t who = group_min<LPT>(best == most ? static_cast<uint32_t>(first + at) : kFull);
-        if (most != 0) {
-          found = j + 1;
-          if (j % LPT == l) {
-            mine = static_cast<int32_t>(who);
-            idx[j] = mine;
-          }
-#pragma unroll
-          for (int i = 0; i < EPL; ++i)
-            if (who == static_cast<uint32_t>(first + i)) key[i] = 0;
+        if (j % LPT == l) {
+          e0 = most != 0 ? static_cast<int>(who) : -1;
+          if (!few && in) idx[j] = e0;
         }
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (most != 0 && who == static_cast<uint32_t>(first + i)) key[i] = 0;
       }
     }
     if (!any) m = 0.0f;  // the row's exponentials are then zero
@@ -308,26 +313,36 @@ __global__ void __launch_bounds__(kRouterThreads, EPL == 8 ? 4 : 2) router_forwa
 #pragma unroll
     for (int i = 0; i < EPL; ++i) psum[i] = fmaf(x[i], inv, psum[i]);
     valid += any;
-    // The chosen weights: lane j % LPT takes choice j and computes its p from the logit.
-    float chosen = 0.0f, p = 0.0f;
-    for (int j = l; j < found; j += LPT) {
-      const int e = a.top_k <= LPT ? mine : idx[j];
-      p = exp_of(to_f(row[e]) - m) * inv;
-      chosen += p;
-      atomicAdd(&s_n[e], 1);
-    }
-    const float scale = a.normalize ? group_sum<LPT>(chosen) : 1.0f;
-    if (in) {
-      float* w = a.weights + t * a.top_k;
+    // The chosen weights, p computed again from the logit.
+    if (few) {
+      float p = 0.0f;
+      if (e0 >= 0) {
+        p = exp_of(to_f(row[e0]) - m) * inv;
+        atomicAdd(&s_n[e0], 1);
+      }
+      if (a.normalize) {
+        const float all = group_sum<LPT>(p);
+        if (e0 >= 0) p *= __frcp_rn(all);
+      }
+      if (in && l < a.top_k) {
+        idx[l] = e0;
+        w[l] = p;
+      }
+    } else {
+      float all = 0.0f;
       for (int j = l; j < a.top_k; j += LPT) {
-        if (j >= found) {
-          idx[j] = -1;
-          w[j] = 0.0f;
-        } else {
-          if (a.top_k > LPT) p = exp_of(to_f(row[idx[j]]) - m) * inv;
-          w[j] = a.normalize ? __fdiv_rn(p, scale) : p;
+        const int e = in ? idx[j] : -1;
+        if (e >= 0) {
+          all += exp_of(to_f(row[e]) - m) * inv;
+          atomicAdd(&s_n[e], 1);
         }
       }
+      const float scale = a.normalize ? __frcp_rn(group_sum<LPT>(all)) : 1.0f;
+      if (in)
+        for (int j = l; j < a.top_k; j += LPT) {
+          const int e = idx[j];
+          w[j] = e >= 0 ? exp_of(to_f(row[e]) - m) * inv * scale : 0.0f;
+        }
     }
   }
   // Over the warp's subgroups, then over the warps in order.
