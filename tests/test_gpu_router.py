@@ -304,3 +304,22 @@ def test_offsets_drive_the_grouped_product():
     e = r.indices.flatten()[order].long()
     ref = torch.einsum("rh,rnh->rn", rows.float(), w[e].float())
     assert (out.float() - ref).norm() / ref.norm() < 0.06        # two E4M3 operands: 2**-4 each at most
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,E,K,seq", [(32, 40, 3, 1), (33, 40, 3, 1), (2000, 64, 6, 3), (500, 300, 8, 7), (4100, 512, 2, 2),
+                                       (700, 5, 2, 20)])
+def test_many_sequences(T, E, K, seq, dtype):
+    """Around and above the number of sequences that one launch adds; the last
+    sequence is shorter, and some have no valid token."""
+    x = make(T, E, T + 3 * E, dtype)
+    g = workloads.philox(T + 1)
+    mask = (g.random(T) < 0.7) & (g.random((T + seq - 1) // seq) < 0.8).repeat(seq)[:T]
+    tm = torch.from_numpy(mask).cuda()
+    dw = torch.from_numpy(g.standard_normal((T, K)).astype(np.float32)).cuda()
+    dloss = torch.tensor([-0.6], device="cuda")
+    for m, t in ((None, None), (mask, tm)):
+        r = mx.router_forward(x, K, tokens_per_seq=seq, token_mask=t, coef=0.2)
+        f = check_forward(r, x, K, seq, m, False, 0.2)
+        dx = mx.router_backward(x, r.indices, r.load, dw, dloss, tokens_per_seq=seq, token_mask=t)
+        check_backward(dx, x, f, f["indices"], r.load, dw, np.float32(-0.6).astype(float), seq, m, False)
