@@ -42,20 +42,26 @@ namespace {
 constexpr int kRouterWarps = 8;
 constexpr int kRouterThreads = 32 * kRouterWarps;
 constexpr int kTargetCtas = 608;   // four per SM of GB300; a constant, so the workspace's size needs no device
-constexpr int kMinChunk = 32;      // tokens of a CTA at least
+constexpr int kMinChunk = 32;      // tokens of a CTA at least, and what a chunk is a multiple of
+// The backward pass leaves no partial rows, so its cut is its own: five CTAs per
+// SM, chunks of whole rounds of a CTA's warps (65536 tokens of 256 experts in
+// chunks of 128, 512 CTAs, took 11% longer: some SMs had four of them, some three).
+constexpr int kBackwardCtas = 760;
 constexpr uint32_t kFull = 0xFFFFFFFFu;
 
-// How the tokens are cut: `chunk` tokens a CTA, `per_seq` CTAs a sequence.
+// How the tokens are cut: `chunk` tokens a CTA (a multiple of step, about `target`
+// CTAs in all), `per_seq` CTAs a sequence.
 struct RouterPlan {
   int64_t seqs, per_seq, chunk, pitch;  // pitch: experts of a partial row (a multiple of 4)
   int64_t ctas() const { return seqs * per_seq; }
 };
 
-RouterPlan router_plan(int64_t tokens, int64_t per_seq_tokens, int64_t experts) {
+RouterPlan router_plan(int64_t tokens, int64_t per_seq_tokens, int64_t experts, int64_t target = kTargetCtas,
+                       int64_t step = kMinChunk) {
   RouterPlan p;
   p.seqs = (tokens + per_seq_tokens - 1) / per_seq_tokens;
-  const int64_t want = (tokens + kTargetCtas - 1) / kTargetCtas;
-  p.chunk = std::max<int64_t>(kMinChunk, (want + kMinChunk - 1) / kMinChunk * kMinChunk);
+  const int64_t want = (tokens + target - 1) / target;
+  p.chunk = std::max<int64_t>(kMinChunk, (want + step - 1) / step * step);
   p.per_seq = (std::min(per_seq_tokens, tokens) + p.chunk - 1) / p.chunk;
   p.pitch = (experts + 3) / 4 * 4;
   return p;
@@ -553,6 +559,26 @@ __device__ __forceinline__ void group_sum4(float (&v)[4]) {
   for (int i = 0; i < 4; ++i) v[i] = __shfl_sync(kFull, a, base + i * L);
 }
 
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// The maximum over a group; NaNs are passed over.
+template <int LPT>
+__device__ __forceinline__ float group_max_f(float v) {
+  if constexpr (LPT == 32) {
+    float r;
+    asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+  }
+#pragma unroll
+  for (int o = LPT / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+
+__device__ __forceinline__ void set_pair(float* d, float2 v) { *reinterpret_cast<float2*>(d) = v; }
+__device__ __forceinline__ void set_pair(__nv_bfloat16* d, float2 v) {
+  *reinterpret_cast<__nv_bfloat162*>(d) = __floats2bfloat162_rn(v.x, v.y);
+}
+
 // With e = exp(x - m) and p = e / sum(e), one reduction over the group gives
 // sum(e), sum(e load), and over the chosen ones z = sum(e) and s = sum(e dw).
 // Not normalised: dot = sum(p load) + sum(p dw). Normalised (w = e / z): the
@@ -561,10 +587,10 @@ __device__ __forceinline__ void group_sum4(float (&v)[4]) {
 // single choice too) cancel exactly. The chosen elements' results are computed
 // by the lanes that hold their dw and put over the row's in shared memory.
 template <typename T, int LPT, int EPL>
-__global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const RouterArgs a) {
-  constexpr int TPW = 32 / LPT, E = LPT * EPL, W = 16 / sizeof(T);
-  __shared__ __align__(16) T s_row[kRouterWarps * TPW][E];
-  __shared__ float s_load[E];
+__global__ void __launch_bounds__(kRouterThreads, EPL == 8 ? 5 : 2) router_backward_kernel(const RouterArgs a) {
+  constexpr int TPW = 32 / LPT, E = LPT * EPL, W = 16 / sizeof(T), P = EPL / 2, kStep = kRouterWarps * TPW;
+  __shared__ __align__(16) T s_row[kStep][E];
+  __shared__ __align__(16) float s_load[E];
   pdl_launch_dependents();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, l = lane % LPT, sub = lane / LPT;
@@ -574,49 +600,60 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const R
   for (int e = threadIdx.x; e < E; e += kRouterThreads)
     s_load[e] = e < a.experts ? dloss * a.load[run.s * a.experts + e] : 0.0f;
   __syncthreads();
-  float load[EPL];
+  float2 load[P];
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) load[i] = s_load[first + i];
+  for (int i = 0; i < P; ++i) load[i] = reinterpret_cast<const float2*>(s_load + first)[i];
   T* const mine = s_row[warp * TPW + sub];
-  for (int64_t t0 = run.first + warp * TPW; t0 < run.end; t0 += kRouterWarps * TPW) {
-    const int64_t t = t0 + sub, at = t * a.top_k;
-    const bool in = t < run.end;
+  const int64_t t0 = run.first + sub;
+  const int tokens = static_cast<int>(run.end - run.first);
+  for (int q = warp * TPW; q < tokens; q += kStep) {
+    const bool in = q + sub < tokens;
+    const int64_t t = t0 + q, at = t * a.top_k;
+    const T* const row = static_cast<const T*>(a.logits) + t * a.ld;
     const bool live = in && (!a.mask || a.mask[t] != 0);
     const bool picks = live && a.dweights;
-    const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-    float x[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) x[i] = -INFINITY;
-    if (live) load_row<T, EPL>(row, first, a.experts, a.vec, x);
     // The lane's (first) choice: expert (-1: none) and dw.
-    const float d0 = picks && a.normalize ? a.dweights[at] : 0.0f;
     int e0 = -1;
-    float d = 0.0f, x0 = 0.0f;
+    float d = 0.0f;
+    if (picks && l < a.top_k) {
+      e0 = a.indices[at + l];
+      d = a.dweights[at + l];
+    }
+    float y[EPL];
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) y[i] = -INFINITY;
+    if (live) load_row<T, EPL>(row, first, a.experts, a.vec, y);
+    if (static_cast<uint32_t>(e0) >= static_cast<uint32_t>(a.experts)) e0 = -1;
+    const float x0 = e0 >= 0 ? to_f(row[e0]) : 0.0f;
+    const float d0 = a.normalize ? __shfl_sync(kFull, d, lane - l) : 0.0f;
+    d -= d0;
+    // Choices past the lanes' first ones.
     auto choice = [&](int j, int& e, float& dw, float& logit) {
       e = a.indices[at + j];
       dw = a.dweights[at + j] - d0;
       if (static_cast<uint32_t>(e) >= static_cast<uint32_t>(a.experts)) e = -1;
       logit = e >= 0 ? to_f(row[e]) : 0.0f;
     };
-    if (picks && l < a.top_k) choice(l, e0, d, x0);
-    float m = -INFINITY;
+    float m = y[0];
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) m = fmaxf(m, x[i]);
+    for (int i = 1; i < EPL; ++i) m = fmaxf(m, y[i]);
+    m = group_max_f<LPT>(m);
+    // A row of -inf alone (one left out, too): its exponentials are zero.
+    const bool none = !(m > -INFINITY);
+    if (none) m = 0.0f;
+    float2 x[P], se = both(0.0f), sl = both(0.0f);
 #pragma unroll
-    for (int o = LPT / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // sum(e), sum(e load), z, s
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) {
-      x[i] = exp_of(x[i] - m);
-      v[0] += x[i];
-      v[1] = fmaf(x[i], load[i], v[1]);
+    for (int i = 0; i < P; ++i) {
+      const float2 u = __fadd2_rn(make_float2(y[2 * i], y[2 * i + 1]), both(-m));
+      x[i] = make_float2(exp_of(u.x), exp_of(u.y));
+      se = __fadd2_rn(se, x[i]);
+      sl = __ffma2_rn(x[i], load[i], sl);
     }
+    float v[4] = {se.x + se.y, sl.x + sl.y, 0.0f, 0.0f};  // sum(e), sum(e load), z, s
     const float ex0 = e0 >= 0 ? exp_of(x0 - m) : 0.0f;
-    if (e0 >= 0) {
-      v[2] = ex0;
-      v[3] = ex0 * d;
-    }
-    if (picks)
+    v[2] = ex0;
+    v[3] = e0 >= 0 ? ex0 * d : 0.0f;
+    if (a.top_k > LPT && picks)
       for (int j = l + LPT; j < a.top_k; j += LPT) {
         int e;
         float dw, logit;
@@ -628,36 +665,29 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const R
         }
       }
     group_sum4<LPT>(v);
-    // Left out: masked, or no logit above -inf (m is -inf with no NaN about; the sum is then NaN).
-    bool any = live && m > -INFINITY;
-    if (__any_sync(kFull, live && !any)) {
-      bool nan = false;
-      if (live) {
-        float y[EPL];
-        load_row<T, EPL>(row, first, a.experts, a.vec, y);
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) nan |= y[i] != y[i];
-      }
-      any |= group_max<LPT>(nan ? 1u : 0u) != 0;
-    }
-    const float inv = __frcp_rn(v[0]), base = v[1] * inv, rz = __frcp_rn(v[2]), mean_d = v[3] * rz;
+    // Left out: masked, or no logit above -inf and no NaN (the sum would be one).
+    const bool any = live && !(none && v[0] == 0.0f);
+    const float inv = any ? __frcp_rn(v[0]) : 0.0f, base = v[1] * inv;
     const float dot = a.normalize ? base : fmaf(v[3], inv, base);
-    // The row without its chosen ones' own gradients ...
+    // The row without its chosen ones' own gradients, p (load - dot) ...
+    const float2 inv2 = both(inv), off = both(-dot * inv);
 #pragma unroll
     for (int j = 0; j < EPL; j += W) {
       Vec16<T> o;
 #pragma unroll
-      for (int i = 0; i < W; ++i) from_f(o.e[i], any ? x[j + i] * inv * (load[j + i] - dot) : 0.0f);
+      for (int i = 0; i < W; i += 2)
+        set_pair(&o.e[i], __fmul2_rn(x[(j + i) / 2], __ffma2_rn(load[(j + i) / 2], inv2, off)));
       *reinterpret_cast<Vec16<T>*>(mine + first + j) = o;
     }
     __syncwarp();
     // ... and those: p * (load + dp - dot), dp = dw, or (dw - s/z) sum/z.
+    const float rz = __frcp_rn(v[2]), mean_d = v[3] * rz;
     auto put = [&](int e, float ex, float dw) {
       const float dp = a.normalize ? (dw - mean_d) * rz * v[0] : dw;
       from_f(mine[e], ex * inv * (s_load[e] + dp - dot));
     };
     if (any && e0 >= 0) put(e0, ex0, d);
-    if (any && picks)
+    if (a.top_k > LPT && any && picks)
       for (int j = l + LPT; j < a.top_k; j += LPT) {
         int e;
         float dw, logit;
@@ -666,7 +696,7 @@ __global__ void __launch_bounds__(kRouterThreads) router_backward_kernel(const R
       }
     __syncwarp();
     if (in) {
-      T* out = static_cast<T*>(a.dlogits) + t * a.lddx + first;
+      T* const out = static_cast<T*>(a.dlogits) + t * a.lddx + first;
       if (a.vec && first + EPL <= a.experts) {
 #pragma unroll
         for (int j = 0; j < EPL; j += W)
@@ -784,7 +814,7 @@ mx_status launch_router_forward(const RouterLaunch& L, cudaStream_t s) {
 }
 
 mx_status launch_router_backward(const RouterLaunch& L, cudaStream_t s) {
-  const RouterPlan p = router_plan(L.tokens, L.tokens_per_seq, L.experts);
+  const RouterPlan p = router_plan(L.tokens, L.tokens_per_seq, L.experts, kBackwardCtas, kRouterWarps);
   const RouterArgs a = router_args(L, p);
   return L.dtype == MX_F32 ? run_any<float>(a, p.ctas(), true, s) : run_any<__nv_bfloat16>(a, p.ctas(), true, s);
 }
