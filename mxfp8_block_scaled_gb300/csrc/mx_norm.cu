@@ -41,6 +41,12 @@ namespace {
 // GB300's 152 SMs at most (a constant, so the workspace's size needs no device).
 constexpr int kMaxPartials = 304;
 
+// Narrow rows (see below): threads of a CTA, CTAs per SM of the forward pass, and
+// the sets of rows in hand, one where a lane's eight elements come one by one.
+constexpr int kNarrowThreads = 256, kNarrowFwdPerSm = 3;
+template <int K>
+constexpr int kNarrowSets = K < 8 ? 2 : 1;
+
 struct NormArgs {
   const void* x;
   const void* dy;      // backward
@@ -157,82 +163,6 @@ __device__ __forceinline__ void group_sum(float& a, float& b, float2* slot, int&
   }
 }
 
-template <typename T, int V, int TPR, int K, int BLOCK>
-__global__ void __launch_bounds__(BLOCK) norm_forward_kernel(const NormArgs a) {
-  constexpr int G = BLOCK / TPR;
-  __shared__ float2 s_sum[G * 2 * (TPR / 32)];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int group = threadIdx.x / TPR, r = threadIdx.x % TPR;
-  float2* slot = s_sum + group * 2 * (TPR / 32);
-  int flip = 0;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * G + group;
-  const T* x = static_cast<const T*>(a.x);
-  Pack<T, V> cur[K], nxt[K];
-  auto fetch = [&](Pack<T, V>* to, int64_t at) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * TPR + r) * V;
-      to[k] = load_pack<T, V>(x + at * a.ldx + c, a.cols - c);
-    }
-  };
-  if (row < a.rows) fetch(cur, row);
-  for (; row < a.rows; row += step) {
-    if (row + step < a.rows) fetch(nxt, row + step);
-    float mean = 0.0f, zero = 0.0f;
-    if (a.center) {
-#pragma unroll
-      for (int k = 0; k < K; ++k)
-#pragma unroll
-        for (int i = 0; i < V; ++i) mean += to_f(cur[k].e[i]);  // absent elements are zero
-      group_sum<TPR>(mean, zero, slot, flip, group);
-      mean *= a.inv_cols;
-    }
-    keep_packed<K>(cur);
-    float sq = 0.0f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int nv = a.cols - (k * TPR + r) * V;
-      if (nv >= V) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float d = to_f(cur[k].e[i]) - mean;
-          sq = fmaf(d, d, sq);
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float d = to_f(cur[k].e[i]) - mean;
-          if (i < nv) sq = fmaf(d, d, sq);
-        }
-      }
-    }
-    group_sum<TPR>(sq, zero, slot, flip, group);
-    keep_packed<K>(cur);
-    const float rstd = __frsqrt_rn(fmaf(sq, a.inv_cols, a.eps));
-    T* out = static_cast<T*>(a.out) + row * a.ldo;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * TPR + r) * V, nv = a.cols - c;
-      if (nv <= 0) break;
-      float w[V], b[V];
-      load_param<V>(a.weight, a.param_f32, c, nv, 1.0f, w);
-      load_param<V>(a.bias, a.param_f32, c, nv, 0.0f, b);
-      Pack<T, V> o;
-#pragma unroll
-      for (int i = 0; i < V; ++i) from_f(o.e[i], fmaf((to_f(cur[k].e[i]) - mean) * rstd, w[i], b[i]));
-      store_pack<T, V>(out + c, o, nv);
-    }
-    if (r == 0) {
-      if (a.mean && a.center) a.mean[row] = mean;
-      if (a.rstd) a.rstd[row] = rstd;
-    }
-#pragma unroll
-    for (int k = 0; k < K; ++k) cur[k] = nxt[k];
-  }
-}
-
 // Rows wider than the registers of a CTA: one CTA a row, the row read three
 // times (from L2 after the first).
 template <typename T, int V>
@@ -280,118 +210,6 @@ __global__ void __launch_bounds__(1024) norm_forward_wide_kernel(const NormArgs 
       if (a.rstd) a.rstd[row] = rstd;
     }
   }
-}
-
-template <typename T, int V, int TPR, int K, int BLOCK>
-__global__ void __launch_bounds__(BLOCK, BLOCK == 1024 || K * V > 8 ? 1 : 2) norm_backward_kernel(const NormArgs a) {
-  constexpr int G = BLOCK / TPR;
-  __shared__ float2 s_sum[G * 2 * (TPR / 32)];
-  __shared__ float s_acc[G > 1 ? 2 * TPR * K * V : 1];
-  pdl_launch_dependents();
-  pdl_wait();
-  const int group = threadIdx.x / TPR, r = threadIdx.x % TPR;
-  float2* slot = s_sum + group * 2 * (TPR / 32);
-  int flip = 0;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * G;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * G + group;
-  const T* x = static_cast<const T*>(a.x);
-  const T* dy = static_cast<const T*>(a.dy);
-  float dw[K * V], db[K * V];
-#pragma unroll
-  for (int i = 0; i < K * V; ++i) dw[i] = db[i] = 0.0f;
-  Pack<T, V> cx[K], cd[K], nx[K], nd[K];
-  float mean = 0.0f, rstd = 0.0f, n_mean = 0.0f, n_rstd = 0.0f;
-  auto fetch = [&](Pack<T, V>* tx, Pack<T, V>* td, float& m, float& s, int64_t at) {
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * TPR + r) * V;
-      tx[k] = load_pack<T, V>(x + at * a.ldx + c, a.cols - c);
-      td[k] = load_pack<T, V>(dy + at * a.lddy + c, a.cols - c);
-    }
-    m = a.center ? a.mean[at] : 0.0f;
-    s = a.rstd[at];
-  };
-  if (row < a.rows) fetch(cx, cd, mean, rstd, row);
-  for (; row < a.rows; row += step) {
-    if (row + step < a.rows) fetch(nx, nd, n_mean, n_rstd, row + step);
-    float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * TPR + r) * V;
-      if (a.cols - c <= 0) break;
-      float w[V];
-      load_param<V>(a.weight, a.param_f32, c, a.cols - c, 1.0f, w);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {  // absent elements have dy = 0 and add nothing
-        const float d = to_f(cd[k].e[i]), h = (to_f(cx[k].e[i]) - mean) * rstd, g = d * w[i];
-        s1 += g;
-        s2 = fmaf(g, h, s2);
-        dw[k * V + i] = fmaf(d, h, dw[k * V + i]);
-        db[k * V + i] += d;
-      }
-    }
-    group_sum<TPR>(s1, s2, slot, flip, group);
-    keep_packed<K>(cx);
-    keep_packed<K>(cd);
-    s1 = a.center ? s1 * a.inv_cols : 0.0f;
-    s2 *= a.inv_cols;
-    T* out = static_cast<T*>(a.out) + row * a.ldo;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int c = (k * TPR + r) * V, nv = a.cols - c;
-      if (nv <= 0) break;
-      float w[V];
-      load_param<V>(a.weight, a.param_f32, c, nv, 1.0f, w);
-      Pack<T, V> o;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float h = (to_f(cx[k].e[i]) - mean) * rstd;
-        from_f(o.e[i], rstd * (to_f(cd[k].e[i]) * w[i] - s1 - h * s2));
-      }
-      store_pack<T, V>(out + c, o, nv);
-    }
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      cx[k] = nx[k];
-      cd[k] = nd[k];
-    }
-    mean = n_mean;
-    rstd = n_rstd;
-  }
-  if (!a.partial) return;
-  // The CTA's groups, added in order.
-  if constexpr (G > 1) {
-    for (int q = 0; q < G; ++q) {
-      if (group == q) {
-#pragma unroll
-        for (int k = 0; k < K; ++k)
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            float* s = s_acc + (k * V + i) * TPR + r;  // neighbouring threads, neighbouring banks
-            s[0] = dw[k * V + i] + (q ? s[0] : 0.0f);
-            s[TPR * K * V] = db[k * V + i] + (q ? s[TPR * K * V] : 0.0f);
-          }
-      }
-      __syncthreads();
-    }
-    if (group != 0) return;
-#pragma unroll
-    for (int i = 0; i < K * V; ++i) {
-      dw[i] = s_acc[i * TPR + r];
-      db[i] = s_acc[i * TPR + r + TPR * K * V];
-    }
-  }
-  float* p = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
-#pragma unroll
-  for (int k = 0; k < K; ++k)
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = (k * TPR + r) * V + i;
-      if (c < a.cols) {
-        p[c] = dw[k * V + i];
-        p[a.cols + c] = db[k * V + i];
-      }
-    }
 }
 
 // Wide rows: dx with one CTA a row (the row read twice) ...
@@ -465,6 +283,266 @@ __global__ void __launch_bounds__(256) norm_backward_columns_kernel(const NormAr
       p[c + i] = dw[i];
       p[a.cols + c + i] = db[i];
     }
+}
+
+// Sixteen bytes of a row as 32-bit words, and two neighbouring elements of them
+// as FP32 for the packed FP32 instructions (two results an issue slot: these
+// kernels are near the issue rate).
+struct alignas(16) Words {
+  uint32_t w[4];
+};
+template <typename T>
+__device__ __forceinline__ float2 two_of(const Words& p, int j) {
+  if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(p.w[2 * j]), __uint_as_float(p.w[2 * j + 1]));
+  return make_float2(__uint_as_float(p.w[j] << 16), __uint_as_float(p.w[j] & 0xFFFF0000u));
+}
+template <typename T>
+__device__ __forceinline__ void set_two(Words& p, int j, float2 v) {
+  if constexpr (sizeof(T) == 4) {
+    p.w[2 * j] = __float_as_uint(v.x);
+    p.w[2 * j + 1] = __float_as_uint(v.y);
+  } else {
+    const __nv_bfloat162 h = __float22bfloat162_rn(v);
+    p.w[j] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ Words words_at(const void* p) { return *reinterpret_cast<const Words*>(p); }
+
+// ---------------------------------------------------------------------------
+// Narrow rows, at most 32 vectors: TPR lanes a row, 32 / TPR rows a warp at once,
+// U such sets of rows in hand and the next U on their way. A lane's columns are
+// the same in every row, so it keeps their weights, and in the backward pass
+// their gradients, in registers. V > 1: 16-byte vectors, one a lane (K = 1).
+// V = 1: any alignment, lane r has columns r, r + TPR, ... A lane's elements are
+// taken by twos. What bounds these is issued instructions until a row has some
+// sixteen vectors, hence as few lanes per row as hold it: with a whole warp a row,
+// 65536 rows of 64 BF16 columns took 23 us forward and 46 backward, now 5.9 and
+// 14; of 128 columns 24 and 47, now 10.5 and 16.7; 10^6 rows of 128 FP32 columns
+// 161 and 242 us, 6.4 TB/s both.
+// ---------------------------------------------------------------------------
+
+template <int TPR>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = TPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  return v;
+}
+
+// Elements of a row as a lane holds them: packed while they wait, FP32 in twos.
+template <typename T, int V, int TPR, int K>
+struct Lane {
+  static constexpr int E = V * K, P = (E + 1) / 2;
+  static_assert(V == 1 || K == 1, "vectors: one a lane");
+  int r, cols;
+  __device__ __forceinline__ int column(int i) const { return V > 1 ? r * V + i : i * TPR + r; }
+  __device__ __forceinline__ bool has(int i) const { return column(i) < cols; }  // V > 1: all of them or none
+  __device__ __forceinline__ void load(Pack<T, V> (&to)[K], const T* row, bool there) const {
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      if (there && has(k)) {
+        to[k] = *reinterpret_cast<const Pack<T, V>*>(row + column(V > 1 ? 0 : k));
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) from_f(to[k].e[i], 0.0f);
+      }
+    }
+  }
+  __device__ __forceinline__ float2 pair(const Pack<T, V> (&p)[K], int i) const {
+    if constexpr (V > 1) return make_float2(to_f(p[0].e[2 * i]), to_f(p[0].e[2 * i + 1]));
+    else if constexpr (K == 1) return make_float2(to_f(p[0].e[0]), 0.0f);
+    else return make_float2(to_f(p[2 * i].e[0]), to_f(p[2 * i + 1].e[0]));
+  }
+  __device__ __forceinline__ void store(T* row, const float2 (&v)[P]) const {
+    if constexpr (V > 1) {
+      if (!has(0)) return;
+      Words o;
+#pragma unroll
+      for (int i = 0; i < P; ++i) set_two<T>(o, i, v[i]);
+      *reinterpret_cast<Words*>(row + column(0)) = o;
+    } else {
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+        if (has(k)) from_f(row[column(k)], k & 1 ? v[k / 2].y : v[k / 2].x);
+    }
+  }
+  // Parameters of the lane's columns: dflt where there are none, zero past the last column.
+  __device__ __forceinline__ void param(const void* p, bool f32, float dflt, float2 (&o)[P]) const {
+    float f[2 * P];
+#pragma unroll
+    for (int i = 0; i < 2 * P; ++i) {
+      f[i] = 0.0f;
+      if (i < E && has(V > 1 ? 0 : i)) {
+        const int c = column(i);
+        f[i] = !p ? dflt : f32 ? static_cast<const float*>(p)[c] : to_f(static_cast<const __nv_bfloat16*>(p)[c]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < P; ++i) o[i] = make_float2(f[2 * i], f[2 * i + 1]);
+  }
+};
+
+template <typename T, int V, int TPR, int K>
+__global__ void __launch_bounds__(kNarrowThreads, kNarrowFwdPerSm) norm_forward_narrow_kernel(const NormArgs a) {
+  using L = Lane<T, V, TPR, K>;
+  constexpr int U = kNarrowSets<K>, P = L::P, kRows = U * 32 / TPR;
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / TPR;
+  const L me = {lane % TPR, a.cols};
+  float2 w[P], b[P];
+  me.param(a.weight, a.param_f32, 1.0f, w);
+  me.param(a.bias, a.param_f32, 0.0f, b);
+  const T* const x = static_cast<const T*>(a.x);
+  T* const out = static_cast<T*>(a.out);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kNarrowThreads / 32) * kRows;
+  int64_t base = (static_cast<int64_t>(blockIdx.x) * (kNarrowThreads / 32) + warp) * kRows;
+  Pack<T, V> nxt[U][K];
+  auto fetch = [&](int64_t at) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = at + u * (32 / TPR) + sub;
+      me.load(nxt[u], x + row * a.ldx, row < a.rows);
+    }
+  };
+  fetch(base);
+  for (; base < a.rows; base += step) {
+    Pack<T, V> cur[U][K];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < K; ++k) cur[u][k] = nxt[u][k];
+    fetch(base + step);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float mean = 0.0f;
+      if (a.center) {
+        float2 t = both(0.0f);
+#pragma unroll
+        for (int i = 0; i < P; ++i) t = __fadd2_rn(t, me.pair(cur[u], i));
+        mean = lanes_sum<TPR>(t.x + t.y) * a.inv_cols;
+      }
+      float2 d[P], q = both(0.0f);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        d[i] = __fadd2_rn(me.pair(cur[u], i), both(-mean));
+        if (V == 1 && !me.has(2 * i)) d[i].x = 0.0f;
+        if (V == 1 && (2 * i + 1 >= K || !me.has(2 * i + 1))) d[i].y = 0.0f;
+        q = __ffma2_rn(d[i], d[i], q);
+      }
+      const float sq = lanes_sum<TPR>(V > 1 && !me.has(0) ? 0.0f : q.x + q.y);
+      const float rstd = __frsqrt_rn(fmaf(sq, a.inv_cols, a.eps));
+      const int64_t row = base + u * (32 / TPR) + sub;
+      if (row < a.rows) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) d[i] = __ffma2_rn(__fmul2_rn(d[i], both(rstd)), w[i], b[i]);
+        me.store(out + row * a.ldo, d);
+        if (me.r == 0) {
+          if (a.mean && a.center) a.mean[row] = mean;
+          if (a.rstd) a.rstd[row] = rstd;
+        }
+      }
+    }
+  }
+}
+
+template <typename T, int V, int TPR, int K>
+__global__ void __launch_bounds__(kNarrowThreads, 2) norm_backward_narrow_kernel(const NormArgs a) {
+  using L = Lane<T, V, TPR, K>;
+  constexpr int U = kNarrowSets<K>, P = L::P, kRows = U * 32 / TPR, kWarps = kNarrowThreads / 32;
+  __shared__ float s_acc[2][kWarps][TPR * L::E];
+  pdl_launch_dependents();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane / TPR;
+  const L me = {lane % TPR, a.cols};
+  float2 w[P], dw[P], db[P];
+  me.param(a.weight, a.param_f32, 1.0f, w);
+#pragma unroll
+  for (int i = 0; i < P; ++i) dw[i] = db[i] = both(0.0f);
+  const T* const x = static_cast<const T*>(a.x);
+  const T* const dy = static_cast<const T*>(a.dy);
+  T* const out = static_cast<T*>(a.out);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * kRows;
+  int64_t base = (static_cast<int64_t>(blockIdx.x) * kWarps + warp) * kRows;
+  Pack<T, V> nx[U][K], nd[U][K];
+  float n_mean[U], n_rstd[U];
+  auto fetch = [&](int64_t at) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t row = at + u * (32 / TPR) + sub;
+      const bool in = row < a.rows;
+      me.load(nx[u], x + row * a.ldx, in);
+      me.load(nd[u], dy + row * a.lddy, in);
+      n_mean[u] = in && a.center ? a.mean[row] : 0.0f;
+      n_rstd[u] = in ? a.rstd[row] : 0.0f;
+    }
+  };
+  fetch(base);
+  for (; base < a.rows; base += step) {
+    Pack<T, V> cx[U][K], cd[U][K];
+    float mean[U], rstd[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        cx[u][k] = nx[u][k];
+        cd[u][k] = nd[u][k];
+      }
+      mean[u] = n_mean[u];
+      rstd[u] = n_rstd[u];
+    }
+    fetch(base + step);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float2 h[P], g[P], t1 = both(0.0f), t2 = both(0.0f);
+#pragma unroll
+      for (int i = 0; i < P; ++i) {  // absent elements have dy = 0 and w = 0
+        const float2 d = me.pair(cd[u], i);
+        h[i] = __fmul2_rn(__fadd2_rn(me.pair(cx[u], i), both(-mean[u])), both(rstd[u]));
+        if (V == 1 && !me.has(2 * i)) h[i].x = 0.0f;
+        if (V == 1 && (2 * i + 1 >= K || !me.has(2 * i + 1))) h[i].y = 0.0f;
+        if (V > 1 && !me.has(0)) h[i] = both(0.0f);
+        g[i] = __fmul2_rn(d, w[i]);
+        t1 = __fadd2_rn(t1, g[i]);
+        t2 = __ffma2_rn(g[i], h[i], t2);
+        dw[i] = __ffma2_rn(d, h[i], dw[i]);
+        db[i] = __fadd2_rn(db[i], d);
+      }
+      const float s1 = a.center ? lanes_sum<TPR>(t1.x + t1.y) * a.inv_cols : 0.0f;
+      const float s2 = lanes_sum<TPR>(t2.x + t2.y) * a.inv_cols;
+      const int64_t row = base + u * (32 / TPR) + sub;
+      if (row < a.rows) {
+#pragma unroll
+        for (int i = 0; i < P; ++i)
+          g[i] = __fmul2_rn(__ffma2_rn(h[i], both(-s2), __fadd2_rn(g[i], both(-s1))), both(rstd[u]));
+        me.store(out + row * a.ldo, g);
+      }
+    }
+  }
+  if (!a.partial) return;
+  // Over the warp's rows, then over the warps in order.
+#pragma unroll
+  for (int i = 0; i < L::E; ++i) {
+    float vw = i & 1 ? dw[i / 2].y : dw[i / 2].x, vb = i & 1 ? db[i / 2].y : db[i / 2].x;
+#pragma unroll
+    for (int o = TPR; o < 32; o <<= 1) {
+      vw += __shfl_xor_sync(0xFFFFFFFFu, vw, o);
+      vb += __shfl_xor_sync(0xFFFFFFFFu, vb, o);
+    }
+    if (sub == 0) {
+      s_acc[0][warp][me.column(i)] = vw;
+      s_acc[1][warp][me.column(i)] = vb;
+    }
+  }
+  __syncthreads();
+  float* p = a.partial + static_cast<int64_t>(blockIdx.x) * 2 * a.cols;
+  for (int i = threadIdx.x; i < 2 * a.cols; i += kNarrowThreads) {
+    const int which = i >= a.cols, c = i - which * a.cols;
+    float v = s_acc[which][0][c];
+#pragma unroll
+    for (int q = 1; q < kWarps; ++q) v += s_acc[which][q][c];
+    p[i] = v;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -546,30 +624,6 @@ __device__ __forceinline__ void group_totals(float (&v)[N], float* slot, int& fl
 #pragma unroll
   for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, t[0], i * L);
 }
-
-// Sixteen bytes of a row as 32-bit words, and two neighbouring elements of them
-// as FP32 for the packed FP32 instructions (two results an issue slot: both
-// ring kernels are near the issue rate).
-struct alignas(16) Words {
-  uint32_t w[4];
-};
-template <typename T>
-__device__ __forceinline__ float2 two_of(const Words& p, int j) {
-  if constexpr (sizeof(T) == 4) return make_float2(__uint_as_float(p.w[2 * j]), __uint_as_float(p.w[2 * j + 1]));
-  return make_float2(__uint_as_float(p.w[j] << 16), __uint_as_float(p.w[j] & 0xFFFF0000u));
-}
-template <typename T>
-__device__ __forceinline__ void set_two(Words& p, int j, float2 v) {
-  if constexpr (sizeof(T) == 4) {
-    p.w[2 * j] = __float_as_uint(v.x);
-    p.w[2 * j + 1] = __float_as_uint(v.y);
-  } else {
-    const __nv_bfloat162 h = __float22bfloat162_rn(v);
-    p.w[j] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-}
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-__device__ __forceinline__ Words words_at(const void* p) { return *reinterpret_cast<const Words*>(p); }
 
 // A thread's place in a row: element i of its vector k.
 template <typename T, int W, bool kElem>
@@ -1044,23 +1098,16 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ri
 
 mx_status norm_launched(cudaError_t e) { return cuda_status(e, "mx_layer_norm launch"); }
 
-template <typename T, int V, int TPR, int K, int BLOCK>
-mx_status forward_cfg(const NormArgs& a, int per_sm, cudaStream_t s) {
-  constexpr int G = BLOCK / TPR;
-  const int64_t grid = std::min<int64_t>((a.rows + G - 1) / G, static_cast<int64_t>(sm_count()) * per_sm);
-  return norm_launched(launch_kernel(norm_forward_kernel<T, V, TPR, K, BLOCK>, static_cast<unsigned>(grid), BLOCK, 0, s,
-                                     1, a));
+template <typename T, int V, int TPR, int K>
+mx_status forward_narrow(const NormArgs& a, cudaStream_t s) {
+  constexpr int kCtaRows = kNarrowThreads / TPR * kNarrowSets<K>;
+  const int64_t grid = std::min<int64_t>((a.rows + kCtaRows - 1) / kCtaRows, kNarrowFwdPerSm * static_cast<int64_t>(sm_count()));
+  return norm_launched(launch_kernel(norm_forward_narrow_kernel<T, V, TPR, K>, static_cast<unsigned>(grid), kNarrowThreads,
+                                     0, s, 1, a));
 }
 
-// Threads per row and vectors (V elements) per thread by the row's number of
-// vectors, for rows too narrow or too wide for the ring.
 template <typename T, int V>
-mx_status forward_any(const NormArgs& a, cudaStream_t s) {
-  const int64_t n = (a.cols + V - 1) / V;
-  if (n <= 32) return forward_cfg<T, V, 32, 1, 256>(a, 8, s);
-  if (n <= 64) return forward_cfg<T, V, 32, 2, 256>(a, 8, s);
-  if constexpr (V == 1)
-    if (n <= 256) return forward_cfg<T, V, 32, 8, 256>(a, 6, s);
+mx_status forward_wide(const NormArgs& a, cudaStream_t s) {
   const int64_t grid = std::min<int64_t>(a.rows, 2 * static_cast<int64_t>(sm_count()));
   return norm_launched(launch_kernel(norm_forward_wide_kernel<T, V>, static_cast<unsigned>(grid), 1024, 0, s, 1, a));
 }
@@ -1089,14 +1136,27 @@ template <typename T, bool kElem>
 mx_status forward_rows(const NormArgs& a, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   const int64_t n = (a.cols + V - 1) / V;
-  if (n > 32) {
-    if (n <= 128) return forward_ring<T, 1, kElem>(a, s);
-    if (n <= 256) return forward_ring<T, 2, kElem>(a, s);
-    if (n <= 512) return forward_ring<T, 4, kElem>(a, s);
-    if (n <= 1024) return forward_ring<T, 8, kElem>(a, s);
-    if (n <= 2048) return forward_ring<T, 16, kElem>(a, s);
+  if (n <= 32) {
+    if constexpr (kElem) {
+      if (a.cols <= 8) return forward_narrow<T, 1, 8, 1>(a, s);
+      if (a.cols <= 16) return forward_narrow<T, 1, 8, 2>(a, s);
+      if (a.cols <= 32) return forward_narrow<T, 1, 8, 4>(a, s);
+      if (a.cols <= 64) return forward_narrow<T, 1, 8, 8>(a, s);
+      if (a.cols <= 128) return forward_narrow<T, 1, 16, 8>(a, s);
+      return forward_narrow<T, 1, 32, 8>(a, s);
+    } else {
+      if (n <= 4) return forward_narrow<T, V, 4, 1>(a, s);
+      if (n <= 8) return forward_narrow<T, V, 8, 1>(a, s);
+      if (n <= 16) return forward_narrow<T, V, 16, 1>(a, s);
+      return forward_narrow<T, V, 32, 1>(a, s);
+    }
   }
-  return forward_any<T, kElem ? 1 : V>(a, s);
+  if (n <= 128) return forward_ring<T, 1, kElem>(a, s);
+  if (n <= 256) return forward_ring<T, 2, kElem>(a, s);
+  if (n <= 512) return forward_ring<T, 4, kElem>(a, s);
+  if (n <= 1024) return forward_ring<T, 8, kElem>(a, s);
+  if (n <= 2048) return forward_ring<T, 16, kElem>(a, s);
+  return forward_wide<T, kElem ? 1 : V>(a, s);
 }
 
 // R rows a stage, as many stages as the share of shared memory holds (two CTAs
@@ -1116,22 +1176,19 @@ mx_status backward_ring(const NormArgs& a, int* parts, cudaStream_t s) {
   return norm_launched(launch_kernel(kern, static_cast<unsigned>(grid), kBwdBlock<W>, S * stage, s, 1, a, S));
 }
 
-template <typename T, int V, int TPR, int K, int BLOCK>
-mx_status backward_cfg(const NormArgs& a, int* parts, cudaStream_t s) {
-  constexpr int G = BLOCK / TPR;
-  const int64_t grid = std::min<int64_t>((a.rows + G - 1) / G,
-                                         std::min<int64_t>(kMaxPartials, static_cast<int64_t>(sm_count()) * (BLOCK == 1024 ? 1 : 2)));
+template <typename T, int V, int TPR, int K>
+mx_status backward_narrow(const NormArgs& a, int* parts, cudaStream_t s) {
+  constexpr int kCtaRows = kNarrowThreads / TPR * kNarrowSets<K>;
+  const int64_t grid = std::min<int64_t>((a.rows + kCtaRows - 1) / kCtaRows,
+                                         std::min<int64_t>(kMaxPartials, 2 * static_cast<int64_t>(sm_count())));
   *parts = static_cast<int>(grid);
-  return norm_launched(launch_kernel(norm_backward_kernel<T, V, TPR, K, BLOCK>, static_cast<unsigned>(grid), BLOCK, 0,
-                                     s, 1, a));
+  return norm_launched(launch_kernel(norm_backward_narrow_kernel<T, V, TPR, K>, static_cast<unsigned>(grid),
+                                     kNarrowThreads, 0, s, 1, a));
 }
 
 template <typename T, int V>
-mx_status backward_any(const NormArgs& a, int* parts, cudaStream_t s) {
+mx_status backward_wide(const NormArgs& a, int* parts, cudaStream_t s) {
   const int64_t n = (a.cols + V - 1) / V;
-  if (n <= 32) return backward_cfg<T, V, 32, 1, 512>(a, parts, s);
-  if constexpr (V == 1)
-    if (n <= 128) return backward_cfg<T, V, 32, 4, 512>(a, parts, s);
   if (a.partial) {
     const int bx = static_cast<int>((n + 255) / 256);
     const int by = static_cast<int>(std::min<int64_t>(a.rows, std::max(1, std::min(kMaxPartials, 4 * sm_count() / bx))));
@@ -1156,16 +1213,30 @@ template <typename T, bool kElem>
 mx_status backward_rows(const NormArgs& a, int* parts, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
   const int64_t n = (a.cols + V - 1) / V;
-  if (n > 16) {
-    if (n <= 32) return backward_ring<T, 1, 1, 4, kElem>(a, parts, s);
-    if (n <= 64) return backward_ring<T, 2, 1, 4, kElem>(a, parts, s);
-    if (n <= 128) return backward_ring<T, 4, 1, 4, kElem>(a, parts, s);
-    if (n <= 256) return backward_ring<T, 8, 1, 4, kElem>(a, parts, s);
-    if (n <= 512) return backward_ring<T, 8, 2, 2, kElem>(a, parts, s);
-    if (n <= 1024) return backward_ring<T, 16, 2, 2, kElem>(a, parts, s);
-    if (n <= 2048) return backward_ring<T, 16, 4, 1, kElem>(a, parts, s);
+  constexpr int kNarrow = kElem || V == 4 ? 32 : 16;
+  if (n <= kNarrow) {
+    if constexpr (kElem) {
+      if (a.cols <= 8) return backward_narrow<T, 1, 8, 1>(a, parts, s);
+      if (a.cols <= 16) return backward_narrow<T, 1, 8, 2>(a, parts, s);
+      if (a.cols <= 32) return backward_narrow<T, 1, 8, 4>(a, parts, s);
+      if (a.cols <= 64) return backward_narrow<T, 1, 8, 8>(a, parts, s);
+      if (a.cols <= 128) return backward_narrow<T, 1, 16, 8>(a, parts, s);
+      return backward_narrow<T, 1, 32, 8>(a, parts, s);
+    } else {
+      if (n <= 4) return backward_narrow<T, V, 4, 1>(a, parts, s);
+      if (n <= 8) return backward_narrow<T, V, 8, 1>(a, parts, s);
+      if (n <= 16) return backward_narrow<T, V, 16, 1>(a, parts, s);
+      if constexpr (V == 4) return backward_narrow<T, V, 32, 1>(a, parts, s);
+    }
   }
-  return backward_any<T, kElem ? 1 : V>(a, parts, s);
+  if (n <= 32) return backward_ring<T, 1, 1, 4, kElem>(a, parts, s);
+  if (n <= 64) return backward_ring<T, 2, 1, 4, kElem>(a, parts, s);
+  if (n <= 128) return backward_ring<T, 4, 1, 4, kElem>(a, parts, s);
+  if (n <= 256) return backward_ring<T, 8, 1, 4, kElem>(a, parts, s);
+  if (n <= 512) return backward_ring<T, 8, 2, 2, kElem>(a, parts, s);
+  if (n <= 1024) return backward_ring<T, 16, 2, 2, kElem>(a, parts, s);
+  if (n <= 2048) return backward_ring<T, 16, 4, 1, kElem>(a, parts, s);
+  return backward_wide<T, kElem ? 1 : V>(a, parts, s);
 }
 
 bool vec_ok(const void* p, int64_t ld, int elem) {

@@ -235,3 +235,35 @@ def test_another_stream_and_a_captured_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(ref, cap))
+
+
+# Narrow rows: around every number of lanes a row takes, in vectors (of 8 or 4) and in elements.
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("cols", [2, 4, 7, 9, 16, 17, 24, 32, 33, 40, 63, 64, 65, 72, 96, 127, 128, 130, 136, 192, 250, 255])
+def test_narrow_rows(cols, dtype):
+    rows = 777
+    for pad, offset, center, pd in ((0, 0, True, torch.float32), (8, 0, False, torch.bfloat16), (1, 3, True, torch.bfloat16)):
+        x, dy = matrix(rows, cols, cols, dtype, pad, offset, mean=0.5), matrix(rows, cols, cols + 1, dtype, pad, offset)
+        w, b = vector(cols, 1, pd, 1.0), vector(cols, 2, pd)
+        out = matrix(rows, cols, 4, dtype, pad, offset)
+        y, mean, rstd = mx.layer_norm(x, w, b, center=center, out=out)
+        check_forward(x, w, b, 1e-5, center, y, mean, rstd)
+        if pad:
+            whole = out.as_strided((rows, cols + pad), (cols + pad, 1))[:-1, cols:]
+            assert torch.isnan(whole).all()      # the gaps are not written
+        got = mx.layer_norm_backward(dy, x, w, mean, rstd, center=center)
+        check_backward(dy, x, w, mean, rstd, center, *got)
+        for p, q in zip(got, mx.layer_norm_backward(dy, x, w, mean, rstd, center=center)):
+            assert torch.equal(p, q)
+        dx, dw, db = mx.layer_norm_backward(dy, x, None, mean, rstd, center=center, param_grads=False)
+        check_backward(dy, x, None, mean, rstd, center, dx, None, None)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("cols,rows", [(1, 1), (64, 1), (128, 33), (13, 60001), (128, 40000)])
+def test_narrow_rows_few_and_many(cols, rows, dtype):
+    x, dy = matrix(rows, cols, 3, dtype, mean=-0.2), matrix(rows, cols, 4, dtype)
+    w, b = vector(cols, 1, torch.float32, 1.0), vector(cols, 2, torch.float32)
+    y, mean, rstd = mx.layer_norm(x, w, b)
+    check_forward(x, w, b, 1e-5, True, y, mean, rstd)
+    check_backward(dy, x, w, mean, rstd, True, *mx.layer_norm_backward(dy, x, w, mean, rstd))
