@@ -685,7 +685,8 @@ mx_status mx_epilogue_backward(const void* dy, int64_t lddy, const void* preact,
  *                  with normalize = 1.
  *   counts [n_experts]  how many tokens chose each expert; group_offsets
  *                  [n_experts + 1] its exclusive prefix sums: the offsets of
- *                  the grouped calls for rows sorted by expert.
+ *                  the grouped calls for rows sorted by expert (as many rows as
+ *                  the last one says: tokens * top_k where no slot is empty).
  *   load [sequences, n_experts]  coef * n_experts / (top_k * S') * hits / n^2,
  *                  hits the sequence's choices of the expert, n its valid
  *                  tokens, S' the sequences with n > 0 (0 for the others): the

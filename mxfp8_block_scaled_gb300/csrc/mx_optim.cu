@@ -32,8 +32,11 @@
 //
 // Both kernels are bound by HBM: 26 or 28 bytes per parameter with 32-bit
 // states, 14.1 or 16.1 with 8-bit ones (BF16 or FP32 gradients). The 8-bit one
-// comes close to the issue rate as well, hence its packed conversions and its
-// special-function forms without scaling code.
+// comes close to the issue rate as well (70% of the issue slots), hence its packed
+// conversions and its special-function forms without scaling code. 45 million
+// parameters, FP32 gradients, 32-bit states: 185 us, 6.8 TB/s; 369 million, BF16
+// gradients, 8-bit states: 817 us, 6.4 TB/s. Where a pointer does not allow the
+// wide accesses an element is read at a time: 229 and 1920 us on the same tensors.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -82,16 +85,19 @@ struct OptHyper {
 };
 
 // The descriptors travel in the kernel parameters (no device table to keep).
-// Three sizes, because a launch copies its whole parameter block.
+// Two sizes, because a launch copies its whole parameter block: a step of one to
+// forty small tensors takes 1 us more of the host with the large one (12.2 against
+// 11.1 us for one tensor, 3.6 against 3.3 us on the device for forty); a smaller
+// one still, of four tensors, gained nothing.
 template <int kCap>
 struct OptArgs {
   OptHyper h;
   OptTensor t[kCap];
 };
-constexpr int kCapSmall = 4, kCapMid = 48, kCapLarge = 448;
-static_assert(sizeof(OptArgs<kCapLarge>) <= 32764, "kernel parameter space");
+constexpr int kCapFew = 48, kCapMany = 448;
+static_assert(sizeof(OptArgs<kCapMany>) <= 32764, "kernel parameter space");
 
-__host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {  // MurmurHash3's 32-bit finaliser
+__host__ __device__ __forceinline__ uint32_t mix32(uint32_t x) {  // a one-to-one mixer of 32-bit words
   x ^= x >> 16;
   x *= 0x85EBCA6Bu;
   x ^= x >> 13;
@@ -379,6 +385,8 @@ mx_status launch_adamw_cap(const mx_adamw_tensor* tensors, int first, int n, int
   a.h.chunks = static_cast<int32_t>(chunks);
   // More CTAs than fit at once: the last round is then short.
   const int64_t grid = std::min<int64_t>(chunks, static_cast<int64_t>(sm_count()) * 16);
+  // The scaling code costs the 8-bit kernel 5% (860 against 817 us for 369 million
+  // parameters) and the 32-bit one nothing; it is there for eps next to nothing only.
   const bool tiny_eps = a.h.eps < a.h.rs * 3.637978807091713e-12f;  // 2^-38
   auto kern = bits == 8 ? (tiny_eps ? adamw8_kernel<kCap, true> : adamw8_kernel<kCap, false>)
                         : (tiny_eps ? adamw32_kernel<kCap, true> : adamw32_kernel<kCap, false>);
@@ -389,12 +397,10 @@ mx_status launch_adamw_cap(const mx_adamw_tensor* tensors, int first, int n, int
 
 mx_status launch_adamw(const mx_adamw_tensor* tensors, int n, int bits, const mx_adamw_hyper& hy,
                        const float* grad_scale, int* dev_status, cudaStream_t s) {
-  for (int i = 0; i < n; i += kCapLarge) {
-    const int k = std::min(n - i, kCapLarge);
-    mx_status st;
-    if (k <= kCapSmall) st = launch_adamw_cap<kCapSmall>(tensors, i, k, bits, hy, grad_scale, dev_status, s);
-    else if (k <= kCapMid) st = launch_adamw_cap<kCapMid>(tensors, i, k, bits, hy, grad_scale, dev_status, s);
-    else st = launch_adamw_cap<kCapLarge>(tensors, i, k, bits, hy, grad_scale, dev_status, s);
+  for (int i = 0; i < n; i += kCapMany) {
+    const int k = std::min(n - i, kCapMany);
+    const mx_status st = k <= kCapFew ? launch_adamw_cap<kCapFew>(tensors, i, k, bits, hy, grad_scale, dev_status, s)
+                                      : launch_adamw_cap<kCapMany>(tensors, i, k, bits, hy, grad_scale, dev_status, s);
     if (st != MX_OK) return st;
   }
   return MX_OK;
