@@ -21,7 +21,7 @@
 //                stages in shared memory, the row held in the group's registers
 //   above        one CTA a row, the row read again from L2 for each sweep
 // BF16, measured: forward 16384 x 7168 80 us (5.9 TB/s, 88% of the copy rate),
-// 16384 x 2048 31 (65%), 65536 x 128 10.5 (49%); backward 16384 x 7168 120 (88%),
+// 16384 x 2048 27 (74%), 65536 x 128 10.5 (49%); backward 16384 x 7168 120 (88%),
 // 16384 x 2048 40 (76%, 4 of it the sum of partial rows), 65536 x 128 16.7 (46%).
 // FP32: 16384 x 4096 83 and 119 (97% and more). The looping kernels: 2048 x 32768
 // 116 and 227 (35% and 27%).
@@ -743,21 +743,21 @@ __device__ __forceinline__ void group_filled(int group) {
 
 // Forward, two rows at a time: they share each read of weight and bias (which
 // come from L1, whose bandwidth they would otherwise fill) and each barrier. A
-// thread holds up to kFwdVecs vectors of each row.
-constexpr int kFwdVecs = 4;
+// thread holds up to K vectors of each row.
 constexpr int kFwdStages = 2;
 template <int W>
 constexpr int kFwdBlock = W <= 8 ? 256 : 32 * W;
 // CTAs an SM: by the registers of a thread (BF16 elements one by one take more).
-template <typename T, int W, bool kElem>
-constexpr int kFwdPerSm = W > 8 ? 1 : kElem && sizeof(T) == 2 ? 2 : 3;
+// Five with K = 2 spilled and took 24% longer at 16384 x 2048 BF16.
+template <typename T, int W, int K, bool kElem>
+constexpr int kFwdPerSm = W > 8 ? 1 : kElem && sizeof(T) == 2 ? (K == 2 ? 3 : 2) : K == 2 ? 4 : 3;
 
 // kF32: weight and bias are both there, in FP32 (the usual case: read with no
 // further questions; asking per vector cost as many instructions as the row's
 // arithmetic).
-template <typename T, int W, bool kElem, bool kF32>
-__global__ void __launch_bounds__(kFwdBlock<W>, kFwdPerSm<T, W, kElem>) norm_forward_ring_kernel(const NormArgs a) {
-  constexpr int V = 16 / sizeof(T), K = kFwdVecs, G = kFwdBlock<W> / (32 * W), S = kFwdStages;
+template <typename T, int W, int K, bool kElem, bool kF32>
+__global__ void __launch_bounds__(kFwdBlock<W>, kFwdPerSm<T, W, K, kElem>) norm_forward_ring_kernel(const NormArgs a) {
+  constexpr int V = 16 / sizeof(T), G = kFwdBlock<W> / (32 * W), S = kFwdStages;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ uint64_t full[G][S];
   __shared__ float s_sum[G][2 * 2 * W];
@@ -1124,21 +1124,24 @@ size_t slot_bytes(const NormArgs& a, bool elem) {
   return elem ? (row + 15) / 16 * 16 + 16 : row;
 }
 
-template <typename T, int W, bool kElem>
+template <typename T, int W, int K, bool kElem>
 mx_status forward_ring(const NormArgs& a, cudaStream_t s) {
   constexpr int G = kFwdBlock<W> / (32 * W);
   const size_t smem = static_cast<size_t>(G) * kFwdStages * 2 * slot_bytes<T>(a, kElem);
-  auto kern = a.weight && a.bias && a.param_f32 ? norm_forward_ring_kernel<T, W, kElem, true>
-                                                : norm_forward_ring_kernel<T, W, kElem, false>;
+  auto kern = a.weight && a.bias && a.param_f32 ? norm_forward_ring_kernel<T, W, K, kElem, true>
+                                                : norm_forward_ring_kernel<T, W, K, kElem, false>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(norm smem)");
-  const int64_t grid = std::min<int64_t>(((a.rows + 1) / 2 + G - 1) / G, static_cast<int64_t>(sm_count()) * kFwdPerSm<T, W, kElem>);
+  const int64_t grid = std::min<int64_t>(((a.rows + 1) / 2 + G - 1) / G, static_cast<int64_t>(sm_count()) * kFwdPerSm<T, W, K, kElem>);
   return norm_launched(launch_kernel(kern, static_cast<unsigned>(grid), kFwdBlock<W>, smem, s, 1, a));
 }
 
-// Lanes or warps per row by its number of 16-byte vectors (begun ones counted). A
-// group of twice the warps costs 8192 x 8192 BF16 17% and 8192 x 4096 FP32 4%, and
-// gains 3% at 16384 x 2048 BF16.
+// Lanes or warps per row by its number of 16-byte vectors (begun ones counted).
+// BF16 rows of up to 512 take at most two vectors a thread, so that four CTAs fit
+// an SM: 16384 x 2048 27.2 us against 30.8 with four vectors and half the warps,
+// 16384 x 4096 46.3 against 53.0. FP32 rows, half the elements and no conversions,
+// gain nothing: 16384 x 2048 48.6 against 45.0. Nor do rows of more vectors (with 16
+// warps 5120 columns took 14% longer, 8192 9% less).
 template <typename T, bool kElem>
 mx_status forward_rows(const NormArgs& a, cudaStream_t s) {
   constexpr int V = 16 / sizeof(T);
@@ -1158,11 +1161,18 @@ mx_status forward_rows(const NormArgs& a, cudaStream_t s) {
       return forward_narrow<T, V, 32, 1>(a, s);
     }
   }
-  if (n <= 128) return forward_ring<T, 1, kElem>(a, s);
-  if (n <= 256) return forward_ring<T, 2, kElem>(a, s);
-  if (n <= 512) return forward_ring<T, 4, kElem>(a, s);
-  if (n <= 1024) return forward_ring<T, 8, kElem>(a, s);
-  if (n <= 2048) return forward_ring<T, 16, kElem>(a, s);
+  if constexpr (V == 8) {
+    if (n <= 64) return forward_ring<T, 1, 2, kElem>(a, s);
+    if (n <= 128) return forward_ring<T, 2, 2, kElem>(a, s);
+    if (n <= 256) return forward_ring<T, 4, 2, kElem>(a, s);
+    if (n <= 512) return forward_ring<T, 8, 2, kElem>(a, s);
+  } else {
+    if (n <= 128) return forward_ring<T, 1, 4, kElem>(a, s);
+    if (n <= 256) return forward_ring<T, 2, 4, kElem>(a, s);
+    if (n <= 512) return forward_ring<T, 4, 4, kElem>(a, s);
+  }
+  if (n <= 1024) return forward_ring<T, 8, 4, kElem>(a, s);
+  if (n <= 2048) return forward_ring<T, 16, 4, kElem>(a, s);
   return forward_wide<T, kElem ? 1 : V>(a, s);
 }
 
