@@ -1152,8 +1152,9 @@ mx_status forward_rows(const NormArgs& a, cudaStream_t s) {
       if (a.cols <= 16) return forward_narrow<T, 1, 8, 2>(a, s);
       if (a.cols <= 32) return forward_narrow<T, 1, 8, 4>(a, s);
       if (a.cols <= 64) return forward_narrow<T, 1, 8, 8>(a, s);
-      if (a.cols <= 128) return forward_narrow<T, 1, 16, 8>(a, s);
-      return forward_narrow<T, 1, 32, 8>(a, s);
+      if constexpr (V == 8)
+        if (a.cols > 128) return forward_narrow<T, 1, 32, 8>(a, s);
+      return forward_narrow<T, 1, 16, 8>(a, s);
     } else {
       if (n <= 4) return forward_narrow<T, V, 4, 1>(a, s);
       if (n <= 8) return forward_narrow<T, V, 8, 1>(a, s);
@@ -1239,8 +1240,9 @@ mx_status backward_rows(const NormArgs& a, int* parts, cudaStream_t s) {
       if (a.cols <= 16) return backward_narrow<T, 1, 8, 2>(a, parts, s);
       if (a.cols <= 32) return backward_narrow<T, 1, 8, 4>(a, parts, s);
       if (a.cols <= 64) return backward_narrow<T, 1, 8, 8>(a, parts, s);
-      if (a.cols <= 128) return backward_narrow<T, 1, 16, 8>(a, parts, s);
-      return backward_narrow<T, 1, 32, 8>(a, parts, s);
+      if constexpr (V == 8)
+        if (a.cols > 128) return backward_narrow<T, 1, 32, 8>(a, parts, s);
+      return backward_narrow<T, 1, 16, 8>(a, parts, s);
     } else {
       if (n <= 4) return backward_narrow<T, V, 4, 1>(a, parts, s);
       if (n <= 8) return backward_narrow<T, V, 8, 1>(a, parts, s);
@@ -1251,8 +1253,11 @@ mx_status backward_rows(const NormArgs& a, int* parts, cudaStream_t s) {
   if (n <= 32) return backward_ring<T, 1, 1, 4, kElem>(a, parts, s);
   if (n <= 64) return backward_ring<T, 2, 1, 4, kElem>(a, parts, s);
   if (n <= 128) return backward_ring<T, 4, 1, 4, kElem>(a, parts, s);
-  if (n <= 256) return backward_ring<T, 8, 1, 4, kElem>(a, parts, s);
-  if (n <= 512) return backward_ring<T, 8, 2, 2, kElem>(a, parts, s);
+  // Half the rows a stage for BF16 elements one by one: the others' number spills
+  // (16384 x 2047 63 us against 87, 16384 x 4001 111 against 116).
+  constexpr int kLess = kElem && V == 8 ? 2 : 1;
+  if (n <= 256) return backward_ring<T, 8, 1, 4 / kLess, kElem>(a, parts, s);
+  if (n <= 512) return backward_ring<T, 8, 2, 2 / kLess, kElem>(a, parts, s);
   if (n <= 1024) return backward_ring<T, 16, 2, 2, kElem>(a, parts, s);
   if (n <= 2048) return backward_ring<T, 16, 4, 1, kElem>(a, parts, s);
   return backward_wide<T, kElem ? 1 : V>(a, parts, s);
@@ -1289,7 +1294,7 @@ NormArgs norm_args(const NormLaunch& L) {
 // 16-byte vectors where every row of every matrix is a whole number of them and
 // starts, like the parameters, on a 16-byte boundary, else element by element. On
 // aligned BF16 matrices the latter take 119 instead of 80 us for 16384 x 7168
-// forward, 86 instead of 40 for 16384 x 2048 backward; FP32 ones 0-36% longer.
+// forward, 63 instead of 40 for 16384 x 2048 backward; FP32 ones 0-36% longer.
 bool wide_access(const NormLaunch& L) {
   const int e = L.dtype == MX_F32 ? 4 : 2;
   return L.cols * e % 16 == 0 && vec_ok(L.x, L.ldx, e) && vec_ok(L.out, L.ldo, e) && (!L.dy || vec_ok(L.dy, L.lddy, e)) &&
