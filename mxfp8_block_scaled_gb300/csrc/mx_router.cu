@@ -23,7 +23,7 @@
 // per logit that also holds the expert: the lanes sort their keys once and
 // top_k rounds of a group maximum take the heads. Each CTA takes a run of tokens
 // of one sequence; its sums of p stay in registers, are added over the CTA in
-// shared memory and over CTAs by two short launches, in a fixed order (same
+// shared memory and over CTAs by one or two short launches, in a fixed order (same
 // inputs, same bits). Only whole numbers are added by atomics, in shared memory.
 // Sums of p are FP32 over at most a few hundred terms at each level.
 
