@@ -9,7 +9,9 @@ The raw entry points keep the C names (``mx_quantize``, ``mx_gemm``,
 ``mx_grouped_gemm``, ``mx_scale_bytes``, ``mx_grouped_padded_rows``,
 ``mx_status_string``, ``mx_last_error``, ``mx_abi_version``) and take integer
 device pointers. ``quantize`` / ``gemm`` / ``grouped_gemm`` wrap them for
-torch tensors, allocating outputs with torch.
+torch tensors, allocating outputs with torch. A wrapper launches on the current
+stream, or on the ``stream`` it is given; its outputs and scratch belong to that
+stream, as if it had been called under ``torch.cuda.stream(stream)``.
 """
 
 from __future__ import annotations
@@ -420,6 +422,18 @@ def _stream(stream) -> Optional[int]:
     return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
+def _under(stream, wrapper, arguments):
+    """Calls a wrapper again under the stream it was given, so that what it
+    allocates (outputs, and scratch that is dropped on return while the kernels
+    still use it) is that stream's memory: the allocator then hands it on in that
+    stream's order only. Memory of the current stream would go to the current
+    stream's next allocation at once, or come from work there that is not done
+    with it."""
+    cuda = _torch().cuda
+    with cuda.stream(stream if isinstance(stream, cuda.Stream) else cuda.ExternalStream(stream.cuda_stream)):
+        return wrapper(**{**arguments, "stream": None})
+
+
 @dataclass
 class MXTensor:
     """One quantised copy ([rows, k] E4M3 codes + swizzled E8M0 scales)."""
@@ -450,6 +464,8 @@ def quantize(x, axis: int = MX_BOTH, group_offsets=None, col_capacity: Optional[
     (row_copy, col_copy), each an MXTensor or None. With ``group_offsets``
     (int64 CUDA tensor [E+1]) the column copy is per-group padded with width
     ``col_capacity``."""
+    if stream is not None:
+        return _under(stream, quantize, locals())
     torch = _torch()
     assert x.dim() == 2 and x.dtype in (torch.bfloat16, torch.float32) and x.is_cuda and x.stride(1) == 1
     assert x.dtype == torch.bfloat16 or group_offsets is None
@@ -487,6 +503,8 @@ def quantize_multi(xs, axis: int = MX_BOTH, status=None, stream=None):
     """MX-quantise up to MX_MAX_MULTI 2-D BF16 CUDA tensors of any shapes in
     one launch. Returns a list of (row_copy, col_copy), one per input, each
     exactly what ``quantize`` gives for that input alone."""
+    if stream is not None:
+        return _under(stream, quantize_multi, locals())
     torch = _torch()
     outs, descs = [], []
     for x in xs:
@@ -513,6 +531,8 @@ def quantize_multi(xs, axis: int = MX_BOTH, status=None, stream=None):
 def gemm(mode: int, a: MXTensor, b: MXTensor, out=None, status=None, stream=None, workspace=None):
     """C[M, N] = A . B^T in BF16 (FP32 accumulation). With `workspace` (a CUDA
     uint8 tensor, see gemm_workspace) the GEMM may split its last round."""
+    if stream is not None:
+        return _under(stream, gemm, locals())
     torch = _torch()
     if out is None:
         out = torch.empty((a.rows, b.rows), dtype=torch.bfloat16, device=a.data.device)
@@ -536,6 +556,8 @@ def gemm_workspace(mode: int, a: MXTensor, b: MXTensor):
 def gemm_multi(problems, status=None, stream=None):
     """Several independent GEMMs (mode, a, b[, out]) in one launch; returns the
     outputs (BF16 [a.rows, b.rows], allocated where not given)."""
+    if stream is not None:
+        return _under(stream, gemm_multi, locals())
     torch = _torch()
     outs, descs = [], []
     for pr in problems:
@@ -567,6 +589,8 @@ def quantize_stacked(w, axis: int, status=None, stream=None):
     """Quantise stacked expert weights w[E, N, K] (BF16, or the FP32 master) in
     one batched launch. Returns (row_stack [E][N][K], col_stack [E][K][N]);
     entries None if not asked."""
+    if stream is not None:
+        return _under(stream, quantize_stacked, locals())
     torch = _torch()
     E, N, K = w.shape
     dev = w.device
@@ -590,6 +614,8 @@ def grouped_gemm(mode: int, a, b, group_offsets, out=None, status=None, stream=N
     """Grouped GEMM. fprop/dgrad: a MXTensor [M_total, K] (rows grouped by
     expert), b MXStacked [E][N][K] -> out [M_total, N]. wgrad: a, b grouped
     column copies (MXTensor [N, cap], [Kout, cap]) -> out [E, N, Kout]."""
+    if stream is not None:
+        return _under(stream, grouped_gemm, locals())
     torch = _torch()
     E = group_offsets.numel() - 1
     if out is None:
@@ -607,6 +633,8 @@ def grouped_gemm_swiglu(a, b, group_offsets, out=None, status=None, stream=None)
     """Grouped gate_up fprop with SwiGLU in the epilogue: a MXTensor [M_total, K]
     (rows grouped by expert), b MXStacked [E][2F][K] (gate rows first) ->
     out [M_total, F] = silu(gate) * up in BF16."""
+    if stream is not None:
+        return _under(stream, grouped_gemm_swiglu, locals())
     torch = _torch()
     E = group_offsets.numel() - 1
     if out is None:
@@ -621,6 +649,8 @@ def grouped_gemm_swiglu_quantize(a, b, group_offsets, col_capacity: int, out=Non
     output: returns (row_copy, col_copy) as quantize(output, MX_BOTH,
     group_offsets, col_capacity) would ([M_total, F] and the per-expert padded
     [F, col_capacity]). ``out``: an existing (row_copy, col_copy) pair to fill."""
+    if stream is not None:
+        return _under(stream, grouped_gemm_swiglu_quantize, locals())
     torch = _torch()
     E = group_offsets.numel() - 1
     R, F = a.rows, b.rows // 2
@@ -652,6 +682,8 @@ class FP8Blockwise:
 
 def quantize_fp8_blockwise(x, block: int, status=None, stream=None) -> FP8Blockwise:
     """DeepSeek-V3 blockwise FP8 quantisation of a 2-D BF16 CUDA tensor."""
+    if stream is not None:
+        return _under(stream, quantize_fp8_blockwise, locals())
     torch = _torch()
     assert x.dim() == 2 and x.dtype == torch.bfloat16 and x.is_cuda and x.stride(1) == 1
     R, C = x.shape
@@ -665,6 +697,8 @@ def quantize_fp8_blockwise(x, block: int, status=None, stream=None) -> FP8Blockw
 
 def gemm_fp8_blockwise(a: FP8Blockwise, b: FP8Blockwise, out=None, status=None, stream=None):
     """C[M, N] = A . B^T for an activation (block 1) and a weight (block 128)."""
+    if stream is not None:
+        return _under(stream, gemm_fp8_blockwise, locals())
     torch = _torch()
     assert a.block == 1 and b.block == 128 and a.k == b.k
     if out is None:
@@ -683,6 +717,8 @@ CURRENT_FORMAT_MAX = 448.0
 
 def current_amax(x, status=None, stream=None):
     """amax of a 2-D BF16 tensor ([1] FP32) or of each matrix of a 3-D stack ([E])."""
+    if stream is not None:
+        return _under(stream, current_amax, locals())
     torch = _torch()
     xs = x if x.dim() == 3 else x.unsqueeze(0)
     assert xs.dtype == torch.bfloat16 and xs.is_cuda and xs.stride(2) == 1
@@ -698,6 +734,8 @@ def quantize_current(x, axis: int = MX_BOTH, amax=None, format_max: float = CURR
     scale per matrix). amax: FP32 [batch] (computed here when None). Returns
     (row_copy, col_copy); each copy's `scale` is the FP32 scale tensor [batch]
     (the same tensor for both copies)."""
+    if stream is not None:
+        return _under(stream, quantize_current, locals())
     torch = _torch()
     stacked = x.dim() == 3
     xs = x if stacked else x.unsqueeze(0)
@@ -729,6 +767,8 @@ def quantize_current(x, axis: int = MX_BOTH, amax=None, format_max: float = CURR
 
 def gemm_current(mode: int, a, b, out=None, status=None, stream=None):
     """C[M, N] = (A . B^T) * s_a * s_b in BF16 for current-scaled operands."""
+    if stream is not None:
+        return _under(stream, gemm_current, locals())
     torch = _torch()
     if out is None:
         out = torch.empty((a.rows, b.rows), dtype=torch.bfloat16, device=a.data.device)
@@ -740,6 +780,8 @@ def gemm_current_multi(problems, status=None, stream=None):
     """Several independent current-scaled GEMMs (mode, a, b[, out]) in one
     launch; returns the outputs (BF16 [a.rows, b.rows], allocated where not
     given)."""
+    if stream is not None:
+        return _under(stream, gemm_current_multi, locals())
     torch = _torch()
     outs, descs = [], []
     for pr in problems:
@@ -755,6 +797,8 @@ def gemm_current_multi(problems, status=None, stream=None):
 def grouped_gemm_current(mode: int, a, b, group_offsets, out=None, status=None, stream=None):
     """Grouped GEMM on current-scaled operands (layouts as grouped_gemm; the
     stacked weights carry one scale per expert)."""
+    if stream is not None:
+        return _under(stream, grouped_gemm_current, locals())
     torch = _torch()
     E = group_offsets.numel() - 1
     if out is None:
@@ -881,6 +925,8 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, center: bool = True
     center=False the root-mean-square norm. Returns (y, mean, rstd): y in x's
     dtype, the FP32 row statistics for layer_norm_backward (mean None with
     center=False, both None with stats=False)."""
+    if stream is not None:
+        return _under(stream, layer_norm, locals())
     torch = _torch()
     R, C = x.shape
     dev = x.device
@@ -901,6 +947,8 @@ def layer_norm_backward(dy, x, weight, mean, rstd, center: bool = True, param_gr
                         stream=None):
     """Gradients of layer_norm: (dx in x's dtype, dweight FP32, dbias FP32; the
     two None with param_grads=False). mean and rstd are layer_norm's."""
+    if stream is not None:
+        return _under(stream, layer_norm_backward, locals())
     torch = _torch()
     R, C = x.shape
     dev = x.device
@@ -928,6 +976,8 @@ def gemm_epilogue(mode: int, a: MXTensor, b: MXTensor, bias=None, act: str = "no
     bias: [N] FP32 or BF16; residual: BF16 [M, N] (may be ``out``); act: one of
     ACTIVATIONS. Returns (out, z): z the BF16 pre-activation for
     epilogue_backward with keep_preact (or a ``preact`` tensor to fill), else None."""
+    if stream is not None:
+        return _under(stream, gemm_epilogue, locals())
     torch = _torch()
     M, N = a.rows, b.rows
     dev = a.data.device
@@ -958,6 +1008,8 @@ def gemm_epilogue(mode: int, a: MXTensor, b: MXTensor, bias=None, act: str = "no
 def epilogue_backward(dy, preact, act: str = "none", bias_grad: bool = True, dz=None, status=None, stream=None):
     """Gradient of gemm_epilogue's epilogue: (dz BF16 [M, N], dbias FP32 [N] or
     None). preact: gemm_epilogue's z (unused, may be None, with act "none")."""
+    if stream is not None:
+        return _under(stream, epilogue_backward, locals())
     torch = _torch()
     assert dy.dtype == torch.bfloat16
     M, N = dy.shape
@@ -998,6 +1050,8 @@ def router_forward(logits, top_k: int, tokens_per_seq: Optional[int] = None, tok
     with normalize), the per-expert counts and group offsets, and the balance
     loss, averaged over sequences of tokens_per_seq tokens (default: one
     sequence). token_mask: bool or uint8 [T], false: left out."""
+    if stream is not None:
+        return _under(stream, router_forward, locals())
     torch = _torch()
     T, E = logits.shape
     dev = logits.device
@@ -1033,6 +1087,8 @@ def router_backward(logits, indices, load, dweights=None, dloss=None, tokens_per
     """dlogits (logits' dtype) from dweights (FP32 [T, top_k] or None) and dloss
     (FP32 [1] on the device, or None); indices, load, tokens_per_seq, token_mask
     and normalize as in router_forward."""
+    if stream is not None:
+        return _under(stream, router_backward, locals())
     torch = _torch()
     T, E = logits.shape
     top_k = indices.shape[1]
