@@ -45,7 +45,15 @@ __device__ __forceinline__ float2 act_value(float2 z) {
   return z;
 }
 
-// d act / dz: q + z u' q (1 - q)
+// d act / dz: q + z u' q (1 - q). z u' overflows where q has long been 0 or 1 and
+// the product is zero (GELU from |z| = 1.2e13 on; an infinite z), so it is held
+// within kSlopeMax: both functions have q (1 - q) = 0 in FP32 well below it (from
+// |u| = 88.8 on: |z u'| = 235 for GELU, 89 for SiLU). A NaN comes through by q.
+constexpr float kSlopeMax = 1.0e4f;
+__device__ __forceinline__ float2 slope_bounded(float2 v) {
+  return make_float2(fminf(fmaxf(v.x, -kSlopeMax), kSlopeMax), fminf(fmaxf(v.y, -kSlopeMax), kSlopeMax));
+}
+
 template <int kAct>
 __device__ __forceinline__ float2 act_slope(float2 z) {
   if constexpr (kAct == MX_ACT_RELU) return make_float2(z.x <= 0.0f ? 0.0f : 1.0f, z.y <= 0.0f ? 0.0f : 1.0f);
@@ -60,7 +68,7 @@ __device__ __forceinline__ float2 act_slope(float2 z) {
       zu = z;
     }
     const float2 rest = __fmul2_rn(q, __ffma2_rn(q, act_pair(-1.0f), act_pair(1.0f)));
-    return __ffma2_rn(zu, rest, q);
+    return __ffma2_rn(slope_bounded(zu), rest, q);
   }
   return make_float2(1.0f, 1.0f);
 }
