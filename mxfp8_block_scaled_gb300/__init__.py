@@ -851,7 +851,7 @@ _ADAMW_TENSOR = "6Qqd2i"  # mx_adamw_tensor
 
 
 def adamw_step(params, grads, states, lr: float, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.0,
-               step: int = 1, grad_scale=None, seed: int = 0, status=None, stream=None) -> None:
+               step: int = 1, grad_scale=None, seed: Optional[int] = None, status=None, stream=None) -> None:
     """One AdamW step, in place, over all tensors in one launch (per 448).
 
     params: contiguous FP32 CUDA tensors; grads: contiguous, FP32 or BF16, each
@@ -859,8 +859,9 @@ def adamw_step(params, grads, states, lr: float, betas=(0.9, 0.999), eps: float 
     weight_decay: one value, or one per tensor. step counts from 1. grad_scale:
     a CUDA FP32 tensor of one element that multiplies every gradient; where it
     is not finite the step changes nothing (status 5). seed: with 8-bit states,
-    the second moment's random rounding; a new one every step, the step count
-    for instance."""
+    the second moment's random rounding; a new one every step (the same one would
+    round an element the same way every time, and its moment would stand still).
+    Default: the step count."""
     torch = _torch()
     n = len(params)
     assert len(grads) == n and len(states) == n, "one gradient and one state per parameter"
@@ -895,7 +896,7 @@ def adamw_step(params, grads, states, lr: float, betas=(0.9, 0.999), eps: float 
         assert grad_scale.dtype is f32 and grad_scale.is_cuda and grad_scale.numel() == 1
     g32 = [0] * n if kinds == {bf16} else [int(t is f32) for t in dtype[n:2 * n]]
     rows = zip(*[ptr[k * n:(k + 1) * n] for k in range(6)], size, decay, g32, [0] * n)
-    hyper = MXAdamWHyperC(lr, betas[0], betas[1], eps, step, seed & 0xFFFFFFFF, 0)
+    hyper = MXAdamWHyperC(lr, betas[0], betas[1], eps, step, (step if seed is None else seed) & 0xFFFFFFFF, 0)
     mx_adamw_step(struct.pack(_ADAMW_TENSOR * n, *itertools.chain.from_iterable(rows)), n, bits, hyper, _ptr(grad_scale),
                   _ptr(status), _stream(stream))
 
