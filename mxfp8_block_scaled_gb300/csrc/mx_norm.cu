@@ -169,9 +169,14 @@ __device__ __forceinline__ void group_sum(float& a, float& b, float2* slot, int&
 }
 
 // Rows wider than the registers of a CTA: one CTA a row, the row read three
-// times (from L2 after the first).
+// times (from L2 after the first). The loops count the columns that are left (nv):
+// there are up to 2^31 - 1, and the place a step past the last one does not fit an
+// int. All but eight BF16 at a time fit two CTAs an SM and are held to that (the
+// compiler gives it up for a few registers: 63 us against 90 for 2048 x 16384 FP32).
+template <int V>
+constexpr int kWidePerSm = V == 8 ? 1 : 2;
 template <typename T, int V>
-__global__ void __launch_bounds__(1024) norm_forward_wide_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(1024, kWidePerSm<V>) norm_forward_wide_kernel(const NormArgs a) {
   __shared__ float2 s_sum[64];
   pdl_launch_dependents();
   pdl_wait();
@@ -181,26 +186,28 @@ __global__ void __launch_bounds__(1024) norm_forward_wide_kernel(const NormArgs 
     T* out = static_cast<T*>(a.out) + row * a.ldo;
     float mean = 0.0f, sq = 0.0f, zero = 0.0f;
     if (a.center) {
-      for (int c = threadIdx.x * V; c < a.cols; c += 1024 * V) {
-        const Pack<T, V> p = load_pack<T, V>(x + c, a.cols - c);
+      for (int nv = a.cols - threadIdx.x * V; nv > 0; nv -= 1024 * V) {
+        const int c = a.cols - nv;
+        const Pack<T, V> p = load_pack<T, V>(x + c, nv);
 #pragma unroll
         for (int i = 0; i < V; ++i) mean += to_f(p.e[i]);
       }
       group_sum<1024>(mean, zero, s_sum, flip, 0);
       mean *= a.inv_cols;
     }
-    for (int c = threadIdx.x * V; c < a.cols; c += 1024 * V) {
-      const Pack<T, V> p = load_pack<T, V>(x + c, a.cols - c);
+    for (int nv = a.cols - threadIdx.x * V; nv > 0; nv -= 1024 * V) {
+      const int c = a.cols - nv;
+      const Pack<T, V> p = load_pack<T, V>(x + c, nv);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float d = to_f(p.e[i]) - mean;
-        if (i < a.cols - c) sq = fmaf(d, d, sq);
+        if (i < nv) sq = fmaf(d, d, sq);
       }
     }
     group_sum<1024>(sq, zero, s_sum, flip, 0);
     const float rstd = __frsqrt_rn(fmaf(sq, a.inv_cols, a.eps));
-    for (int c = threadIdx.x * V; c < a.cols; c += 1024 * V) {
-      const int nv = a.cols - c;
+    for (int nv = a.cols - threadIdx.x * V; nv > 0; nv -= 1024 * V) {
+      const int c = a.cols - nv;
       const Pack<T, V> p = load_pack<T, V>(x + c, nv);
       float w[V], b[V];
       load_param<V>(a.weight, a.param_f32, c, nv, 1.0f, w);
@@ -219,7 +226,7 @@ __global__ void __launch_bounds__(1024) norm_forward_wide_kernel(const NormArgs 
 
 // Wide rows: dx with one CTA a row (the row read twice) ...
 template <typename T, int V>
-__global__ void __launch_bounds__(1024) norm_backward_wide_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(1024, kWidePerSm<V>) norm_backward_wide_kernel(const NormArgs a) {
   __shared__ float2 s_sum[64];
   pdl_launch_dependents();
   pdl_wait();
@@ -230,8 +237,8 @@ __global__ void __launch_bounds__(1024) norm_backward_wide_kernel(const NormArgs
     T* out = static_cast<T*>(a.out) + row * a.ldo;
     const float mean = a.center ? a.mean[row] : 0.0f, rstd = a.rstd[row];
     float s1 = 0.0f, s2 = 0.0f;
-    for (int c = threadIdx.x * V; c < a.cols; c += 1024 * V) {
-      const int nv = a.cols - c;
+    for (int nv = a.cols - threadIdx.x * V; nv > 0; nv -= 1024 * V) {
+      const int c = a.cols - nv;
       const Pack<T, V> px = load_pack<T, V>(x + c, nv), pd = load_pack<T, V>(dy + c, nv);
       float w[V];
       load_param<V>(a.weight, a.param_f32, c, nv, 1.0f, w);
@@ -245,8 +252,8 @@ __global__ void __launch_bounds__(1024) norm_backward_wide_kernel(const NormArgs
     group_sum<1024>(s1, s2, s_sum, flip, 0);
     s1 = a.center ? s1 * a.inv_cols : 0.0f;
     s2 *= a.inv_cols;
-    for (int c = threadIdx.x * V; c < a.cols; c += 1024 * V) {
-      const int nv = a.cols - c;
+    for (int nv = a.cols - threadIdx.x * V; nv > 0; nv -= 1024 * V) {
+      const int c = a.cols - nv;
       const Pack<T, V> px = load_pack<T, V>(x + c, nv), pd = load_pack<T, V>(dy + c, nv);
       float w[V];
       load_param<V>(a.weight, a.param_f32, c, nv, 1.0f, w);
@@ -265,8 +272,9 @@ template <typename T, int V>
 __global__ void __launch_bounds__(256) norm_backward_columns_kernel(const NormArgs a) {
   pdl_launch_dependents();
   pdl_wait();
-  const int c = (blockIdx.x * 256 + threadIdx.x) * V, nv = a.cols - c;
-  if (nv <= 0) return;
+  const uint32_t cols = a.cols, c = (blockIdx.x * 256 + threadIdx.x) * V;
+  if (c >= cols) return;
+  const int nv = cols - c;
   float dw[V], db[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) dw[i] = db[i] = 0.0f;
@@ -281,12 +289,13 @@ __global__ void __launch_bounds__(256) norm_backward_columns_kernel(const NormAr
       db[i] += to_f(pd.e[i]);
     }
   }
-  float* p = a.partial + static_cast<int64_t>(blockIdx.y) * 2 * a.cols;
+  float* const to_dw = a.partial + static_cast<int64_t>(blockIdx.y) * 2 * a.cols + c;
+  float* const to_db = to_dw + a.cols;
 #pragma unroll
   for (int i = 0; i < V; ++i)
     if (i < nv) {
-      p[c + i] = dw[i];
-      p[a.cols + c + i] = db[i];
+      to_dw[i] = dw[i];
+      to_db[i] = db[i];
     }
 }
 
