@@ -1126,11 +1126,22 @@ mx_status forward_wide(const NormArgs& a, cudaStream_t s) {
   return norm_launched(launch_kernel(norm_forward_wide_kernel<T, V>, static_cast<unsigned>(grid), 1024, 0, s, 1, a));
 }
 
-// Bytes of a row's slot in a stage.
+// Bytes of a row's slot in a stage, and of the widest row's that W warps of K
+// vectors a thread take.
 template <typename T>
 size_t slot_bytes(const NormArgs& a, bool elem) {
   const size_t row = static_cast<size_t>(a.cols) * sizeof(T);
   return elem ? (row + 15) / 16 * 16 + 16 : row;
+}
+constexpr size_t widest_slot(int W, int K, bool elem) { return static_cast<size_t>(W) * K * 512 + (elem ? 16 : 0); }
+
+// Allows a kernel `smem` bytes of dynamic shared memory: the most that any of its
+// launches takes, the same number every time, so that host threads cannot lower it
+// between each other's calls of this and launches.
+template <typename Kernel>
+mx_status allow_smem(Kernel kern, size_t smem) {
+  return cuda_status(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)),
+                     "cudaFuncSetAttribute(norm smem)");
 }
 
 template <typename T, int W, int K, bool kElem>
@@ -1139,8 +1150,8 @@ mx_status forward_ring(const NormArgs& a, cudaStream_t s) {
   const size_t smem = static_cast<size_t>(G) * kFwdStages * 2 * slot_bytes<T>(a, kElem);
   auto kern = a.weight && a.bias && a.param_f32 ? norm_forward_ring_kernel<T, W, K, kElem, true>
                                                 : norm_forward_ring_kernel<T, W, K, kElem, false>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(norm smem)");
+  const mx_status st = allow_smem(kern, G * kFwdStages * 2 * widest_slot(W, K, kElem));
+  if (st != MX_OK) return st;
   const int64_t grid = std::min<int64_t>(((a.rows + 1) / 2 + G - 1) / G, static_cast<int64_t>(sm_count()) * kFwdPerSm<T, W, K, kElem>);
   return norm_launched(launch_kernel(kern, static_cast<unsigned>(grid), kFwdBlock<W>, smem, s, 1, a));
 }
@@ -1192,11 +1203,12 @@ template <typename T, int W, int K, int R, bool kElem>
 mx_status backward_ring(const NormArgs& a, int* parts, cudaStream_t s) {
   constexpr int G = kBwdBlock<W> / (32 * W), per_sm = W <= 8 ? 2 : 1;
   const size_t stage = static_cast<size_t>(G) * 2 * R * slot_bytes<T>(a, kElem);
-  const int S = static_cast<int>(std::min<size_t>(4, 212992 / per_sm / stage));
-  static_assert(2 * G * 2 * R * (32 * W * K * 16 + 16) <= 212992 / per_sm, "a stage is refilled while another one is worked on");
+  constexpr size_t kSmem = 212992 / per_sm;
+  const int S = static_cast<int>(std::min<size_t>(4, kSmem / stage));
+  static_assert(2 * G * 2 * R * widest_slot(W, K, true) <= kSmem, "a stage is refilled while another one is worked on");
   auto kern = norm_backward_ring_kernel<T, W, K, R, kElem>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(S * stage));
-  if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(norm smem)");
+  const mx_status st = allow_smem(kern, kSmem);
+  if (st != MX_OK) return st;
   const int64_t grid = std::min<int64_t>((a.rows + G * R - 1) / (G * R),
                                          std::min<int64_t>(kMaxPartials, static_cast<int64_t>(sm_count()) * per_sm));
   *parts = static_cast<int>(grid);
