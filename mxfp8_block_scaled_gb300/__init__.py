@@ -954,8 +954,9 @@ def layer_norm_backward(dy, x, weight, mean, rstd, center: bool = True, param_gr
     R, C = x.shape
     dev = x.device
     assert dy.shape == x.shape and dy.dtype == x.dtype
-    assert rstd.dtype == torch.float32 and rstd.is_contiguous() and rstd.numel() == R
-    assert not center or (mean.dtype == torch.float32 and mean.is_contiguous() and mean.numel() == R)
+    for t in (rstd, mean) if center else (rstd,):
+        assert t.is_cuda and t.dtype == torch.float32 and t.is_contiguous() and t.numel() == R, \
+            "mean and rstd: contiguous FP32 CUDA tensors, one entry per row"
     pd = _params(weight, None, C)
     dx = torch.empty((R, C), dtype=x.dtype, device=dev)
     dw = db = ws = None
@@ -1095,6 +1096,7 @@ def router_backward(logits, indices, load, dweights=None, dloss=None, tokens_per
     top_k = indices.shape[1]
     seq = max(T, 1) if tokens_per_seq is None else tokens_per_seq
     f32 = torch.float32
+    assert indices.is_cuda and load.is_cuda and (dweights is None or dweights.is_cuda), "CUDA tensors"
     assert indices.dtype == torch.int32 and indices.is_contiguous() and indices.shape[0] == T
     assert load.dtype == f32 and load.is_contiguous() and load.shape == ((T + seq - 1) // seq, E)
     assert dweights is None or (dweights.dtype == f32 and dweights.is_contiguous() and dweights.shape == indices.shape)
