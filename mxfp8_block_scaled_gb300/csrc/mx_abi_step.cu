@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -79,6 +80,12 @@ mx_status check_workspace(const char* fn, const void* ws, size_t bytes, size_t n
     return MX_ERR_INVALID_ARG;
   }
   return check_aligned(fn, "workspace", ws, 16);
+}
+
+// Tokens of a sequence, as the router's sizes are computed from them: `tokens` or
+// more are one sequence (their sums could pass 64 bits).
+int64_t sequence_tokens(int64_t tokens_per_seq, int64_t tokens) {
+  return std::min(tokens_per_seq, std::max<int64_t>(tokens, 1));
 }
 
 // What both directions of the router share; MX_OK with tokens = 0 too.
@@ -283,7 +290,7 @@ mx_status mx_epilogue_backward(const void* dy, int64_t lddy, const void* preact,
 
 size_t mx_router_workspace_bytes(int64_t tokens, int64_t tokens_per_seq, int n_experts) {
   if (tokens <= 0 || tokens_per_seq <= 0 || n_experts <= 0) return 0;
-  return router_workspace(tokens, tokens_per_seq, n_experts);
+  return router_workspace(tokens, sequence_tokens(tokens_per_seq, tokens), n_experts);
 }
 
 mx_status mx_router_forward(const void* logits, int64_t ld, int dtype, const uint8_t* token_mask, int64_t tokens,
@@ -292,6 +299,7 @@ mx_status mx_router_forward(const void* logits, int64_t ld, int dtype, const uin
                             float* loss, void* workspace, size_t workspace_bytes, int* dev_status, void* stream) {
   const char* fn = "mx_router_forward";
   (void)dev_status;
+  tokens_per_seq = sequence_tokens(tokens_per_seq, tokens);
   MX_CHECK(check_router(fn, dtype, tokens, tokens_per_seq, n_experts, top_k, normalize));
   if (!std::isfinite(coef)) {
     set_error("mx_router_forward: coef is not finite");
@@ -340,6 +348,7 @@ mx_status mx_router_backward(const void* logits, int64_t ld, int dtype, const ui
                              int* dev_status, void* stream) {
   const char* fn = "mx_router_backward";
   (void)dev_status;
+  tokens_per_seq = sequence_tokens(tokens_per_seq, tokens);
   MX_CHECK(check_router(fn, dtype, tokens, tokens_per_seq, n_experts, top_k, normalize));
   if (tokens == 0) return MX_OK;
   MX_CHECK(check_matrix(fn, "logits", logits, ld, n_experts, elem_size(dtype)));
