@@ -305,7 +305,12 @@ __global__ void __launch_bounds__(kOptThreads) adamw8_kernel(const __grid_consta
     const float v_amax = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, v_bits & 0x7FFFFFFFu));
     const bool tiny = m_amax < 7.888609052210118e-31f;  // 2^-100
     const float m_inv = tiny ? 0.0f : __fmul_rn(__frcp_rn(m_amax), 448.0f);
-    const float v_inv = __frcp_rn(v_amax);
+    float v_inv = __frcp_rn(v_amax);
+    if (v_amax < 1.1754943508222875e-38f) {  // below 2^-126 the reciprocal can leave FP32: 2^64 times both
+      v_inv = __frcp_rn(v_amax * 18446744073709551616.0f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] *= 18446744073709551616.0f;
+    }
     const uint32_t key = static_cast<uint32_t>(i0) + t.key + static_cast<uint32_t>(i0 >> 32) * 0x9E3779B9u;
     int32_t vq[8];
 #pragma unroll
