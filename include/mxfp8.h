@@ -599,6 +599,8 @@ mx_status mx_adamw_step(const mx_adamw_tensor* tensors, int n, int state_bits, c
  *   weight, bias cols entries of param_dtype; NULL stands for 1 and 0.
  *   mean, rstd   FP32 [rows] for the backward pass, written; NULL where they
  *                are not wanted (mean is not written with center = 0).
+ *   dev_status   MX_ERR_TIMEOUT where a wait inside the kernel ran out; the rows
+ *                it was for are NaN (backward: dweight and dbias too).
  *   1 <= cols < 2^31; rows may be 0. Any alignment of the element types works;
  *   rows that all start on 16-byte boundaries are read in 16-byte vectors. No
  *   output may overlap an input.
@@ -748,6 +750,20 @@ int mx_abi_version(void);
  * lets its own copies and MMAs land, frees its tensor memory and returns.)
  */
 mx_status mx_selftest_wait_timeout(uint64_t timeout_ns, int* dev_status, void* stream);
+
+/*
+ * mx_selftest_norm_timeout - the same for the norms, whose rows come through
+ * bulk copies: one root-mean-square norm of x[rows, cols] (BF16, packed rows;
+ * out and rstd written), or with dy its backward pass (rstd read; out, dweight
+ * and dbias written, workspace as mx_layer_norm_backward's), in which every
+ * stage waits for bytes that nothing sends. The rows come out as NaN, as they
+ * do wherever a wait of the norms runs out, and the sums over them (the first or
+ * the last row may be right, where it is read without a copy); dev_status (may
+ * be NULL) gets MX_ERR_TIMEOUT. 1 ms <= timeout_ns <= 10 s; 257 <= cols <= 16384.
+ */
+mx_status mx_selftest_norm_timeout(uint64_t timeout_ns, const void* dy, const void* x, int64_t rows, int64_t cols,
+                                   void* out, float* rstd, float* dweight, float* dbias, void* workspace,
+                                   size_t workspace_bytes, int* dev_status, void* stream);
 
 #ifdef __cplusplus
 }

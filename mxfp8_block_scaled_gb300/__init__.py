@@ -48,7 +48,7 @@ EXPORTED = ("mx_scale_bytes", "mx_grouped_padded_rows", "mx_quantize", "mx_quant
             "mx_grouped_gemm_current", "mx_gemm_current_multi", "mx_grouped_gemm_swiglu_quantize", "mx_adamw_step",
             "mx_layer_norm", "mx_layer_norm_backward_workspace_bytes", "mx_layer_norm_backward",
             "mx_gemm_epilogue", "mx_epilogue_backward_workspace_bytes", "mx_epilogue_backward",
-            "mx_router_workspace_bytes", "mx_router_forward", "mx_router_backward")
+            "mx_router_workspace_bytes", "mx_router_forward", "mx_router_backward", "mx_selftest_norm_timeout")
 MX_STATIC_WORKSPACE_BYTES = 40 * 1024 * 1024
 
 
@@ -181,6 +181,8 @@ def lib() -> ctypes.CDLL:
     L.mx_router_backward.restype = i32
     L.mx_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp, vp]
     L.mx_selftest_wait_timeout.restype = i32
+    L.mx_selftest_norm_timeout.argtypes = [ctypes.c_uint64, vp, vp, i64, i64, vp, vp, vp, vp, vp, ctypes.c_size_t, vp, vp]
+    L.mx_selftest_norm_timeout.restype = i32
     L.mx_status_string.argtypes = [i32]
     L.mx_status_string.restype = ctypes.c_char_p
     L.mx_last_error.argtypes = []
@@ -258,6 +260,12 @@ def mx_gemm_fp8_blockwise(a_data, a_scale, M, b_data, b_scale, N, K, c, ldc, dev
 
 def mx_selftest_wait_timeout(timeout_ns, dev_status, stream) -> None:
     _check(lib().mx_selftest_wait_timeout(timeout_ns, dev_status, stream), "mx_selftest_wait_timeout")
+
+
+def mx_selftest_norm_timeout(timeout_ns, dy, x, rows, cols, out, rstd, dweight, dbias, workspace, workspace_bytes, dev_status,
+                             stream) -> None:
+    _check(lib().mx_selftest_norm_timeout(timeout_ns, dy, x, rows, cols, out, rstd, dweight, dbias, workspace,
+                                          workspace_bytes, dev_status, stream), "mx_selftest_norm_timeout")
 
 
 def _ref(op):

@@ -242,6 +242,47 @@ mx_status mx_layer_norm_backward(const void* dy, int64_t lddy, const void* x, in
   return launch_norm_backward(L, s);
 }
 
+mx_status mx_selftest_norm_timeout(uint64_t timeout_ns, const void* dy, const void* x, int64_t rows, int64_t cols,
+                                   void* out, float* rstd, float* dweight, float* dbias, void* workspace,
+                                   size_t workspace_bytes, int* dev_status, void* stream) {
+  const char* fn = "mx_selftest_norm_timeout";
+  if (timeout_ns < 1000000ull || timeout_ns > 10000000000ull || rows < 1 || cols < 257 || cols > 16384) {
+    set_error("mx_selftest_norm_timeout: needs 1 ms <= timeout_ns <= 10 s, rows >= 1, 257 <= cols <= 16384");
+    return MX_ERR_INVALID_ARG;
+  }
+  if (dy) MX_CHECK(check_matrix(fn, "dy", dy, cols, cols, 2));
+  MX_CHECK(check_matrix(fn, "x", x, cols, cols, 2));
+  MX_CHECK(check_matrix(fn, "out", out, cols, cols, 2));
+  MX_CHECK(check_present(fn, "rstd", rstd, 4));
+  if (dy) {
+    MX_CHECK(check_present(fn, "dweight", dweight, 4));
+    MX_CHECK(check_present(fn, "dbias", dbias, 4));
+    MX_CHECK(check_workspace(fn, workspace, workspace_bytes, norm_backward_workspace(rows, cols)));
+  }
+  MX_CHECK(check_device());
+  NormLaunch L = {};
+  L.x = x;
+  L.ldx = cols;
+  L.dy = dy;
+  L.lddy = cols;
+  L.param_dtype = MX_F32;
+  L.rows = rows;
+  L.cols = cols;
+  L.dtype = MX_BF16;
+  L.eps = 1e-5f;
+  L.out = out;
+  L.ldo = cols;
+  L.rstd = rstd;
+  L.dweight = dweight;
+  L.dbias = dbias;
+  L.ws = workspace;
+  L.dev_status = dev_status;
+  L.timeout_ns = timeout_ns;
+  L.withheld = 16;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return dy ? launch_norm_backward(L, s) : launch_norm_forward(L, s);
+}
+
 size_t mx_epilogue_backward_workspace_bytes(int64_t rows, int64_t cols) {
   return rows <= 0 || cols <= 0 ? 0 : epilogue_backward_workspace(rows, cols);
 }

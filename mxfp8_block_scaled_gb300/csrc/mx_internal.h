@@ -231,6 +231,10 @@ struct NormLaunch {
   float* dbias;
   void* ws;
   int* dev_status;
+  // The self test of the stages' waits: their limit (0: the library's), and the
+  // bytes that each waits for in vain.
+  uint64_t timeout_ns;
+  uint32_t withheld;
 };
 mx_status launch_norm_forward(const NormLaunch& L, cudaStream_t s);
 mx_status launch_norm_backward(const NormLaunch& L, cudaStream_t s);
