@@ -870,6 +870,7 @@ __global__ void __launch_bounds__(kFwdBlock<W>, kFwdPerSm<T, W, K, kElem>) norm_
     keep_packed<K>(p[0]);
     keep_packed<K>(p[1]);
     // Every thread of the group has its vectors in registers: the stage is free.
+    if constexpr (W == 1) __syncwarp();  // group_totals has a barrier for W > 1 only; shuffles order no memory
     if (r == 0 && pair + S * step < pairs) issue(s, pair + S * step);
     if (++s == S) {
       s = 0;
@@ -1039,6 +1040,7 @@ __global__ void __launch_bounds__(kBwdBlock<W>, W <= 8 ? 2 : 1) norm_backward_ri
       sum[R + q] = t2.x + t2.y;
     }
     group_totals<2 * R, W>(sum, s_sum[group], flip, group);
+    if constexpr (W == 1) __syncwarp();  // its barrier is for W > 1 only; shuffles order no memory
     if (r == 0 && !first && row + (S - 1) * step < a.rows) issue(s == 0 ? S - 1 : s - 1, row + (S - 1) * step);
     T* out = static_cast<T*>(a.out) + row * a.ldo;
 #pragma unroll
