@@ -48,7 +48,9 @@
 // Both also carry the epilogue of mx_gemm_epilogue (kEpi): bias, activation and
 // residual on the FP32 accumulators, the pre-activation stored beside the
 // output. M = 8192, N = 10944, K = 2048 with bias and GELU: 131 us (2.81
-// PFLOP/s), as the product alone (129); the pre-activation's 179 MB make it 148.
+// PFLOP/s), as the product alone (129); the pre-activation's 179 MB make it 142
+// to 148. Those are short runs at 2070 MHz; call after call the power cap holds
+// the SM clock at 1.6 to 1.7 GHz, and they take 146, 138 and 156 to 160 us.
 //
 // Every mbarrier wait is bounded in wall time; on expiry the CTA records
 // MX_ERR_TIMEOUT in dev_status, drains its own copies and MMAs, frees its
@@ -756,8 +758,10 @@ __device__ __forceinline__ void store_tile(const OutView& p, const Tile& ti, con
 
 // kEpi of the kernels: 0 none; 1 every box leaves by TMA and the residual's rows
 // allow 16-byte loads; 2 any alignment. Kinds of their own because the element
-// paths of the second would cost the first one registers, which it has none to
-// spare of: on aligned matrices kind 2 takes 176 us instead of 148 at 8192 x
+// paths of the second cost registers, and both spill at the 168 a thread has (bytes
+// stored and loaded: kind 1 64/128 with CTA pairs, 84/484 in the 256-wide
+// single-CTA kernel, kind 2 252/708 and 244/920; the plain products none): on
+// aligned matrices kind 2 takes 176 us instead of 148 at 8192 x
 // 10944 x 2048 with the pre-activation, 79 instead of 67 at 8192 x 4096 x 512
 // with SiLU, residual and pre-activation (131 both with neither of them).
 //

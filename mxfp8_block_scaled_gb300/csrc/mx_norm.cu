@@ -14,8 +14,8 @@
 // digits.
 //
 // Both directions are bound by HBM (forward: x read, y written; backward: x and
-// dy read, dx written), narrow rows by issued instructions. By a row's number of
-// 16-byte vectors:
+// dy read, dx written); narrow rows by neither that nor the issue rate alone (below).
+// By a row's number of 16-byte vectors:
 //   up to 32     several rows a warp, straight into registers (no barrier at all)
 //   up to 2048   a group of warps a row, fed by bulk copies through a ring of
 //                stages in shared memory, the row held in the group's registers
@@ -24,7 +24,7 @@
 // 16384 x 2048 27 (74%), 65536 x 128 10.5 (49%); backward 16384 x 7168 120 (88%),
 // 16384 x 2048 40 (76%, 4 of it the sum of partial rows), 65536 x 128 16.7 (46%).
 // FP32: 16384 x 4096 83 and 119 (97% and more). The looping kernels: 2048 x 32768
-// 116 and 227 (35% and 27%).
+// 116 and 226 (35% and 27%).
 // The backward pass keeps dw and db of its columns in registers over all rows
 // of its CTA, adds its groups in shared memory and leaves one partial row per
 // CTA in the workspace; a second launch adds those in a fixed order (same
@@ -330,9 +330,11 @@ __device__ __forceinline__ Words words_at(const void* p) { return *reinterpret_c
 // the same in every row, so it keeps their weights, and in the backward pass
 // their gradients, in registers. V > 1: 16-byte vectors, one a lane (K = 1).
 // V = 1: any alignment, lane r has columns r, r + TPR, ... A lane's elements are
-// taken by twos. What bounds these is issued instructions until a row has some
-// sixteen vectors, hence as few lanes per row as hold it: with a whole warp a row,
-// 65536 rows of 64 BF16 columns took 23 us forward and 46 backward, now 5.9 and
+// taken by twos. Per row the instructions are many until it has some sixteen vectors,
+// hence as few lanes per row as hold it. What is left is latency: 10^6 rows of 128
+// BF16 columns have 59% of the issue slots and 48% of DRAM's rate taken forward, 56%
+// of both backward, with the 35% and 24% of the warps that 79 and 127 registers leave
+// (the rows on their way hold half of them). With a whole warp a row, 65536 rows of 64 BF16 columns took 23 us forward and 46 backward, now 5.9 and
 // 14; of 128 columns 24 and 47, now 10.5 and 16.7; 10^6 rows of 128 FP32 columns
 // 161 and 242 us, 6.4 TB/s both.
 // ---------------------------------------------------------------------------

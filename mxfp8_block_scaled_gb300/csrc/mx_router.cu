@@ -190,6 +190,10 @@ __device__ __forceinline__ Run run_of(const RouterArgs& a) {
 
 // 65536 tokens, 64 FP32 experts, six choices: 16.5 us, 68% of the issue slots, a
 // third of the instructions in the six rounds of the choice; 20.5 us with the sums.
+// Some of the others move spilled registers: four CTAs an SM leave 64 a thread, and
+// x, ahead, key and psum are alive together. Bytes stored and loaded per thread, for
+// 4, 8, 16 and 32 lanes a token: FP32 52/76, 56/80, 56/80, 12/12; BF16 52/76, 32/44,
+// 32/44, 12/12.
 template <typename T, int LPT, int EPL>
 __global__ void __launch_bounds__(kRouterThreads, EPL == 8 ? 4 : 2) router_forward_kernel(const RouterArgs a) {
   constexpr int TPW = 32 / LPT;   // tokens of a warp at a time
