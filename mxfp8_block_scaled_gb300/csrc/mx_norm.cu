@@ -582,7 +582,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 2) norm_backward_narrow_kernel
 // CTA run on without further waits and copies. A thread whose stage has not come
 // fills all of it with NaN (every bit one): what it then reads is that, or the real
 // rows if they land after all, so what comes out is NaN or right, also where the
-// stage passes for complete a round later, its parity being the next one's. (The
+// stage passes for complete a turn of the ring later, by its parity. (The
 // fill's code costs BF16 rows off the 16-byte boundaries 3-4% forward, 16384 x 2047
 // 41.9 us against 40.4, the others nothing; a flag that each stage reads, 5-6%.)
 __device__ __forceinline__ void stage_wait(uint64_t* bar, uint32_t parity, const NormArgs& a, volatile int32_t* gave_up,

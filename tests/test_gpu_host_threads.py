@@ -9,7 +9,7 @@ import mxfp8_block_scaled_gb300 as mx
 import workloads
 
 pytestmark = pytest.mark.gpu
-ROUNDS = 15000
+CALLS = 15000
 
 
 def forward(cols):
@@ -42,7 +42,7 @@ def test_norms_of_two_widths(make, widths):
     failed = []
     def run(call, stream):
         try:
-            for _ in range(ROUNDS):
+            for _ in range(CALLS):
                 call(stream.cuda_stream)
         except mx.MXError as e:
             failed.append(str(e))
