@@ -728,6 +728,105 @@ mx_status mx_router_backward(const void* logits, int64_t ld, int dtype, const ui
                              const float* load, const float* dweights, const float* dloss, void* dlogits, int64_t lddx,
                              int* dev_status, void* stream);
 
+/*
+ * The gated feed-forward block
+ * ----------------------------
+ * What stands around the products of a block whose feed-forward part is gated:
+ * the residual's addition and the norm in front (mx_add_norm_quantize), both
+ * projections with the activation and the product of the two (mx_gemm_gated, or
+ * mx_grouped_gemm and mx_gated_quantize for routed experts), and the way back. The
+ * quantising calls form their blocks from FP32 values (scale rule, layouts and
+ * padding of mx_quantize), which are rounded once, to E4M3.
+ *
+ * mx_add_norm_quantize - adds the residual to x, takes the root-mean-square norm of
+ * the sum and writes it as MX copies. Per row, in FP32:
+ *   v = x + residual,  rstd = 1 / sqrt(sum(v^2) / cols + eps),  y = v * rstd * weight
+ *
+ *   x            BF16 [rows, cols], pitch ldx: the output of the product before.
+ *   residual     [rows, cols] of stream_dtype, pitch ld_residual; NULL: v = x.
+ *   weight       cols entries of param_dtype; NULL stands for 1.
+ *   axis         the copies of y: MX_ROWWISE, MX_COLWISE, MX_BOTH, or 0 for none
+ *                (then y must be wanted). Buffers as mx_quantize's dense ones. The
+ *                column copy needs rows % 32 == 0.
+ *   sum          v rounded to stream_dtype, pitch ld_sum: the residual stream
+ *                behind the addition. NULL: not wanted. May be the residual itself
+ *                (same pointer and pitch), or x with a BF16 stream.
+ *   y            BF16 [rows, cols], pitch ldy (a router's input); NULL: not wanted.
+ *   rstd         FP32 [rows] for the backward pass; NULL: not wanted.
+ *   cols a multiple of 32, at most MX_ADD_NORM_MAX_COLS. Matrices 16-byte aligned,
+ *   pitches multiples of 16 bytes. No output but sum may overlap an input. rows may
+ *   be 0. dev_status: MX_ERR_TIMEOUT where a wait inside the kernel ran out; the
+ *   rows it was for are NaN.
+ *
+ * mx_add_norm_backward - from the gradients of y (dy) and of sum (dsum), the gradient
+ * of v, which is x's and the residual's. With h = sum * rstd and g = dy * weight:
+ *   dx = dsum + rstd * (g - h * sum(g h) / cols)
+ *   dweight = sum over rows of dy * h
+ *
+ *   dy           BF16, pitch lddy; sum, dsum, dx of stream_dtype with their
+ *                pitches. dsum NULL: zeros. dx may be dsum itself (same pointer and
+ *                pitch) and overlaps nothing else.
+ *   axis         MX copies of dx (before its rounding to stream_dtype): the dY of the
+ *                product that wrote x. 0: none. dx may be NULL where there are some.
+ *   dweight      FP32 [cols], written; NULL: not wanted. rows = 0 writes zeros.
+ *   workspace    scratch of mx_add_norm_backward_workspace_bytes(rows, cols), 16-byte
+ *                aligned; may be NULL if dweight is.
+ *   Sums are added in a fixed order: same inputs on the same GPU, same bits.
+ */
+#define MX_ADD_NORM_MAX_COLS 16384
+mx_status mx_add_norm_quantize(const void* x, int64_t ldx, const void* residual, int64_t ld_residual, int stream_dtype,
+                               const void* weight, int param_dtype, int64_t rows, int64_t cols, float eps, int axis,
+                               void* sum, int64_t ld_sum, void* y, int64_t ldy, float* rstd, void* row_data,
+                               void* row_scale, void* col_data, void* col_scale, int* dev_status, void* stream);
+size_t mx_add_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+mx_status mx_add_norm_backward(const void* dy, int64_t lddy, const void* sum, int64_t ld_sum, const void* dsum,
+                               int64_t ld_dsum, int stream_dtype, const void* weight, int param_dtype,
+                               const float* rstd, int64_t rows, int64_t cols, int axis, void* dx, int64_t lddx,
+                               float* dweight, void* row_data, void* row_scale, void* col_data, void* col_scale,
+                               void* workspace, size_t workspace_bytes, int* dev_status, void* stream);
+
+/*
+ * mx_gemm_gated - both projections of a gated feed-forward block in one launch:
+ *   C = act(A . gate^T) * (A . up^T)
+ * on the FP32 accumulators, rounded to BF16 once.
+ *
+ *   a            row copy [M, K] of the tokens.
+ *   gate, up     row copies [F, K] of the two weights (each of its own scale buffer:
+ *                the two matrices of one mx_quantize_batched or mx_quantize_f32 call
+ *                with batch 2, for a weight kept as [2F, K], gate first).
+ *   act          mx_act (SiLU: SwiGLU, GELU: GEGLU, ReLU: ReGLU, none: bilinear).
+ *   c            BF16 [M, F], pitch ldc.
+ *   preact       BF16 [M, 2F], pitch ld_preact: receives [A . gate^T | A . up^T] for
+ *                mx_gated_backward_quantize; NULL: not kept.
+ *   Alignment, K = 0 and errors as mx_gemm. No output overlaps another or an input.
+ */
+mx_status mx_gemm_gated(const mx_operand* a, const mx_operand* gate, const mx_operand* up, int act, void* c, int64_t ldc,
+                        void* preact, int64_t ld_preact, int* dev_status, void* stream);
+
+/*
+ * mx_gated_quantize - h = act(gate) * up from gate_up = [gate | up], BF16 [rows, 2F],
+ * pitch ld, as MX copies of h [rows, F] (what the down projection reads).
+ *
+ * mx_gated_backward_quantize - from dh, BF16 [rows, F] (the down projection's dgrad),
+ * and gate_up, the MX copies of [dgate | dup], [rows, 2F] (the dY of the two
+ * projections, whose weight is kept as [2F, K], gate first):
+ *   dgate = dh * up * act'(gate),  dup = dh * act(gate)
+ *
+ *   axis         MX_ROWWISE, MX_COLWISE or MX_BOTH; row_data .. col_capacity, groups
+ *                and their errors as mx_quantize's of the [rows, F] (backward: [rows,
+ *                2F]) matrix. Dense column copies need rows % 32 == 0.
+ *   F a multiple of 32. gate_up and dh 16-byte aligned, pitches multiples of 8.
+ *   dev_status: also MX_ERR_TIMEOUT where a wait inside the kernel ran out; the values
+ *   it was for are NaN.
+ */
+mx_status mx_gated_quantize(const void* gate_up, int64_t ld, int64_t rows, int64_t f, int act, int axis, void* row_data,
+                            void* row_scale, void* col_data, void* col_scale, const int64_t* group_offsets, int n_groups,
+                            int64_t col_capacity, int* dev_status, void* stream);
+mx_status mx_gated_backward_quantize(const void* dh, int64_t lddh, const void* gate_up, int64_t ld, int64_t rows,
+                                     int64_t f, int act, int axis, void* row_data, void* row_scale, void* col_data,
+                                     void* col_scale, const int64_t* group_offsets, int n_groups, int64_t col_capacity,
+                                     int* dev_status, void* stream);
+
 /* Static description of a status code. */
 const char* mx_status_string(mx_status s);
 

@@ -33,6 +33,7 @@ MX_MAX_GEMM_MULTI = 4
 MX_MAX_GROUPS = 512
 MX_BF16, MX_F32 = 0, 1
 MX_ADAMW_STATE_BLOCK = 256
+MX_ADD_NORM_MAX_COLS = 16384
 MX_ACT_NONE, MX_ACT_RELU, MX_ACT_GELU, MX_ACT_SILU = 0, 1, 2, 3
 ACTIVATIONS = {"none": MX_ACT_NONE, "relu": MX_ACT_RELU, "gelu": MX_ACT_GELU, "silu": MX_ACT_SILU}
 STATUS_NAMES = {0: "MX_OK", 1: "MX_ERR_INVALID_ARG", 2: "MX_ERR_UNSUPPORTED_SHAPE", 3: "MX_ERR_ALIGNMENT",
@@ -48,7 +49,9 @@ EXPORTED = ("mx_scale_bytes", "mx_grouped_padded_rows", "mx_quantize", "mx_quant
             "mx_grouped_gemm_current", "mx_gemm_current_multi", "mx_grouped_gemm_swiglu_quantize", "mx_adamw_step",
             "mx_layer_norm", "mx_layer_norm_backward_workspace_bytes", "mx_layer_norm_backward",
             "mx_gemm_epilogue", "mx_epilogue_backward_workspace_bytes", "mx_epilogue_backward",
-            "mx_router_workspace_bytes", "mx_router_forward", "mx_router_backward", "mx_selftest_norm_timeout")
+            "mx_router_workspace_bytes", "mx_router_forward", "mx_router_backward", "mx_selftest_norm_timeout",
+            "mx_add_norm_quantize", "mx_add_norm_backward_workspace_bytes", "mx_add_norm_backward", "mx_gemm_gated",
+            "mx_gated_quantize", "mx_gated_backward_quantize")
 MX_STATIC_WORKSPACE_BYTES = 40 * 1024 * 1024
 
 
@@ -179,6 +182,21 @@ def lib() -> ctypes.CDLL:
     L.mx_router_forward.restype = i32
     L.mx_router_backward.argtypes = [vp, i64, i32, vp, i64, i64, i32, i32, i32, vp, vp, vp, vp, vp, i64, vp, vp]
     L.mx_router_backward.restype = i32
+    L.mx_add_norm_quantize.argtypes = [vp, i64, vp, i64, i32, vp, i32, i64, i64, ctypes.c_float, i32, vp, i64, vp, i64, vp,
+                                       vp, vp, vp, vp, vp, vp]
+    L.mx_add_norm_quantize.restype = i32
+    L.mx_add_norm_backward_workspace_bytes.argtypes = [i64, i64]
+    L.mx_add_norm_backward_workspace_bytes.restype = ctypes.c_size_t
+    L.mx_add_norm_backward.argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, i32, vp, i64, i64, i32, vp, i64, vp, vp, vp, vp,
+                                       vp, vp, ctypes.c_size_t, vp, vp]
+    L.mx_add_norm_backward.restype = i32
+    L.mx_gemm_gated.argtypes = [ctypes.POINTER(MXOperandC), ctypes.POINTER(MXOperandC), ctypes.POINTER(MXOperandC), i32,
+                                vp, i64, vp, i64, vp, vp]
+    L.mx_gemm_gated.restype = i32
+    L.mx_gated_quantize.argtypes = [vp, i64, i64, i64, i32, i32, vp, vp, vp, vp, vp, i32, i64, vp, vp]
+    L.mx_gated_quantize.restype = i32
+    L.mx_gated_backward_quantize.argtypes = [vp, i64, vp, i64, i64, i64, i32, i32, vp, vp, vp, vp, vp, i32, i64, vp, vp]
+    L.mx_gated_backward_quantize.restype = i32
     L.mx_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp, vp]
     L.mx_selftest_wait_timeout.restype = i32
     L.mx_selftest_norm_timeout.argtypes = [ctypes.c_uint64, vp, vp, i64, i64, vp, vp, vp, vp, vp, ctypes.c_size_t, vp, vp]
@@ -400,6 +418,44 @@ def mx_router_backward(logits, ld, dtype, token_mask, tokens, tokens_per_seq, n_
     _check(lib().mx_router_backward(logits, ld, dtype, token_mask, tokens, tokens_per_seq, n_experts, top_k, normalize,
                                     indices, load, dweights, dloss, dlogits, lddx, dev_status, stream),
            "mx_router_backward")
+
+
+def mx_add_norm_quantize(x, ldx, residual, ld_residual, stream_dtype, weight, param_dtype, rows, cols, eps, axis, sum,
+                         ld_sum, y, ldy, rstd, row_data, row_scale, col_data, col_scale, dev_status, stream) -> None:
+    _check(lib().mx_add_norm_quantize(x, ldx, residual, ld_residual, stream_dtype, weight, param_dtype, rows, cols, eps,
+                                      axis, sum, ld_sum, y, ldy, rstd, row_data, row_scale, col_data, col_scale,
+                                      dev_status, stream), "mx_add_norm_quantize")
+
+
+def mx_add_norm_backward_workspace_bytes(rows, cols) -> int:
+    return int(lib().mx_add_norm_backward_workspace_bytes(rows, cols))
+
+
+def mx_add_norm_backward(dy, lddy, sum, ld_sum, dsum, ld_dsum, stream_dtype, weight, param_dtype, rstd, rows, cols, axis,
+                         dx, lddx, dweight, row_data, row_scale, col_data, col_scale, workspace, workspace_bytes,
+                         dev_status, stream) -> None:
+    _check(lib().mx_add_norm_backward(dy, lddy, sum, ld_sum, dsum, ld_dsum, stream_dtype, weight, param_dtype, rstd, rows,
+                                      cols, axis, dx, lddx, dweight, row_data, row_scale, col_data, col_scale, workspace,
+                                      workspace_bytes, dev_status, stream), "mx_add_norm_backward")
+
+
+def mx_gemm_gated(a: MXOperandC, gate: MXOperandC, up: MXOperandC, act, c, ldc, preact, ld_preact, dev_status,
+                  stream) -> None:
+    _check(lib().mx_gemm_gated(_ref(a), _ref(gate), _ref(up), act, c, ldc, preact, ld_preact, dev_status, stream),
+           "mx_gemm_gated")
+
+
+def mx_gated_quantize(gate_up, ld, rows, f, act, axis, row_data, row_scale, col_data, col_scale, group_offsets, n_groups,
+                      col_capacity, dev_status, stream) -> None:
+    _check(lib().mx_gated_quantize(gate_up, ld, rows, f, act, axis, row_data, row_scale, col_data, col_scale,
+                                   group_offsets, n_groups, col_capacity, dev_status, stream), "mx_gated_quantize")
+
+
+def mx_gated_backward_quantize(dh, lddh, gate_up, ld, rows, f, act, axis, row_data, row_scale, col_data, col_scale,
+                               group_offsets, n_groups, col_capacity, dev_status, stream) -> None:
+    _check(lib().mx_gated_backward_quantize(dh, lddh, gate_up, ld, rows, f, act, axis, row_data, row_scale, col_data,
+                                            col_scale, group_offsets, n_groups, col_capacity, dev_status, stream),
+           "mx_gated_backward_quantize")
 
 
 # ---------------------------------------------------------------------------
@@ -1114,3 +1170,23 @@ def router_backward(logits, indices, load, dweights=None, dloss=None, tokens_per
                        int(normalize), indices.data_ptr(), load.data_ptr(), _ptr(dweights), _ptr(dloss), dx.data_ptr(),
                        E, _ptr(status), _stream(stream))
     return dx
+
+
+# ---------------------------------------------------------------------------
+# The gated feed-forward block's wrappers: a module of their own, loaded when one
+# of them is first asked for
+# ---------------------------------------------------------------------------
+
+_GATED_BLOCK = ("AddNorm", "AddNormGrads", "add_norm_quantize", "add_norm_backward", "gemm_gated", "gated_quantize",
+                "gated_backward_quantize")
+
+
+def __getattr__(name):
+    if name in _GATED_BLOCK:
+        from . import gated_block
+        return getattr(gated_block, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted([*globals(), *_GATED_BLOCK])

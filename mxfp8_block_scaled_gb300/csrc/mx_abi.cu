@@ -577,6 +577,51 @@ mx_status mx_gemm_epilogue(int mode, const mx_operand* a, const mx_operand* b, c
   return launch_gemm(L, s);
 }
 
+mx_status mx_gemm_gated(const mx_operand* a, const mx_operand* gate, const mx_operand* up, int act, void* c, int64_t ldc,
+                        void* preact, int64_t ld_preact, int* dev_status, void* stream) {
+  GemmLaunch L;
+  mx_status st = dense_gemm_setup("mx_gemm_gated", MX_FPROP, a, gate, c, ldc, dev_status, true, &L);
+  if (st != MX_OK) return st;
+  st = check_operand(up, "up");
+  if (st != MX_OK) return st;
+  if (up->orient != MX_ROWWISE || up->rows != gate->rows || up->k != gate->k) {
+    set_error("mx_gemm_gated: gate and up must both be row copies of the same size");
+    return MX_ERR_INVALID_ARG;
+  }
+  if (act < MX_ACT_NONE || act > MX_ACT_SILU) {
+    set_error("mx_gemm_gated: unknown act %d", act);
+    return MX_ERR_INVALID_ARG;
+  }
+  if (gate->rows > 0x3FFFFFFFLL) {
+    set_error("mx_gemm_gated: F must be < 2^30");
+    return MX_ERR_UNSUPPORTED_SHAPE;
+  }
+  if (preact && ld_preact < 2 * L.N) {
+    set_error("mx_gemm_gated: ld_preact < 2F");
+    return MX_ERR_INVALID_ARG;
+  }
+  if ((reinterpret_cast<uintptr_t>(preact) & 1u) != 0) {
+    set_error("mx_gemm_gated: preact must be 2-byte aligned (BF16)");
+    return MX_ERR_ALIGNMENT;
+  }
+  if (L.M == 0 || L.N == 0) return MX_OK;
+  st = check_device();
+  if (st != MX_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (L.K == 0) {  // act(0) * 0
+    st = zero_output(c, ldc, L.N, L.M, s);
+    return st == MX_OK && preact ? zero_output(preact, ld_preact, 2 * L.N, L.M, s) : st;
+  }
+  L.up_data = up->data;
+  L.up_scale = up->scale;
+  L.up_ld = up->ld ? up->ld : up->k;
+  L.N *= 2;  // both projections' columns
+  L.epi.preact = preact;
+  L.epi.ld_preact = ld_preact;
+  L.epi.act = act;
+  return launch_gemm(L, s);
+}
+
 mx_status mx_gemm_workspace_bytes(int mode, const mx_operand* a, const mx_operand* b, size_t* bytes) {
   if (!bytes) {
     set_error("mx_gemm_workspace_bytes: bytes is null");

@@ -111,11 +111,112 @@ mx_status check_present(const char* fn, const char* name, const void* p, int a) 
   return check_aligned(fn, name, p, a);
 }
 
+// The copies that `axis` asks for of a [rows, cols] matrix: present and aligned,
+// sizes whole blocks (mx_quantize's rules).
+mx_status check_copies(const char* fn, int axis, int64_t rows, int64_t cols, const void* row_data, const void* row_scale,
+                       const void* col_data, const void* col_scale, bool grouped) {
+  const bool row = (axis & MX_ROWWISE) != 0, col = (axis & MX_COLWISE) != 0;
+  if (cols % 32 != 0 || (col && !grouped && rows % 32 != 0)) {
+    set_error("%s: the columns (and the rows for a dense column copy) must be a multiple of 32", fn);
+    return MX_ERR_UNSUPPORTED_SHAPE;
+  }
+  if (rows == 0 || cols == 0) return MX_OK;
+  if ((row && (!row_data || !row_scale)) || (col && (!col_data || !col_scale))) {
+    set_error("%s: a requested copy is null", fn);
+    return MX_ERR_INVALID_ARG;
+  }
+  for (const void* p : {row_data, row_scale, col_data, col_scale}) {
+    if (!aligned(p, 16)) {
+      set_error("%s: the copies must be 16-byte aligned", fn);
+      return MX_ERR_ALIGNMENT;
+    }
+  }
+  return MX_OK;
+}
+
+// A matrix that is read or written in 16-byte pieces.
+mx_status check_wide_matrix(const char* fn, const char* name, const void* p, int64_t ld, int64_t cols, int elem) {
+  if (!p || ld < cols) {
+    set_error("%s: %s is null or its pitch is less than its columns", fn, name);
+    return MX_ERR_INVALID_ARG;
+  }
+  if (!aligned(p, 16) || ld % (16 / elem) != 0) {
+    set_error("%s: %s and its rows must be 16-byte aligned", fn, name);
+    return MX_ERR_ALIGNMENT;
+  }
+  return MX_OK;
+}
+
+// What both directions of the norm with the residual's addition share.
+mx_status check_add_norm(const char* fn, int64_t rows, int64_t cols, int stream_dtype, int param_dtype, int axis) {
+  if (rows < 0 || cols < 1 || !known_dtype(stream_dtype) || !known_dtype(param_dtype) || axis < 0 || axis > MX_BOTH) {
+    set_error("%s: needs rows >= 0, cols >= 1, a known stream_dtype and param_dtype, axis 0 or an mx_axis", fn);
+    return MX_ERR_INVALID_ARG;
+  }
+  if (cols > MX_ADD_NORM_MAX_COLS || rows > 0x7FFFFFFFLL) {
+    set_error("%s: at most %d columns and 2^31 - 1 rows", fn, MX_ADD_NORM_MAX_COLS);
+    return MX_ERR_UNSUPPORTED_SHAPE;
+  }
+  return MX_OK;
+}
+
 #define MX_CHECK(call)                       \
   do {                                       \
     const mx_status check_st = (call);       \
     if (check_st != MX_OK) return check_st;  \
   } while (0)
+
+// Both directions of the gate.
+mx_status gated(const char* fn, bool backward, const void* dh, int64_t lddh, const void* gate_up, int64_t ld, int64_t rows,
+                int64_t f, int act, int axis, void* row_data, void* row_scale, void* col_data, void* col_scale,
+                const int64_t* group_offsets, int n_groups, int64_t col_capacity, int* dev_status, void* stream) {
+  if (rows < 0 || f < 0 || act < MX_ACT_NONE || act > MX_ACT_SILU || axis < MX_ROWWISE || axis > MX_BOTH) {
+    set_error("%s: negative size, unknown act %d or axis %d", fn, act, axis);
+    return MX_ERR_INVALID_ARG;
+  }
+  if (rows > 0x7FFFFFFFLL || f > 0x3FFFFFFFLL) {
+    set_error("%s: rows must be < 2^31, F < 2^30", fn);
+    return MX_ERR_UNSUPPORTED_SHAPE;
+  }
+  const bool grouped = group_offsets != nullptr, col = (axis & MX_COLWISE) != 0;
+  MX_CHECK(check_copies(fn, axis, rows, f, row_data, row_scale, col_data, col_scale, grouped));
+  if (grouped) {
+    if (n_groups < 1 || (col && (col_capacity < 0 || col_capacity % 128 != 0))) {
+      set_error("%s: needs n_groups >= 1 and col_capacity a multiple of 128", fn);
+      return MX_ERR_INVALID_ARG;
+    }
+    if (n_groups > MX_MAX_GROUPS || col_capacity > 0x7FFFFFFFLL) {
+      set_error("%s: at most %d groups, col_capacity < 2^31", fn, MX_MAX_GROUPS);
+      return MX_ERR_UNSUPPORTED_SHAPE;
+    }
+    MX_CHECK(check_aligned(fn, "group_offsets", group_offsets, 8));
+  }
+  if (rows == 0 || f == 0) return MX_OK;
+  if (backward) MX_CHECK(check_wide_matrix(fn, "dh", dh, lddh, f, 2));
+  MX_CHECK(check_wide_matrix(fn, "gate_up", gate_up, ld, 2 * f, 2));
+  MX_CHECK(check_device());
+  GatedLaunch L = {};
+  L.dh = backward ? dh : nullptr;
+  L.lddh = lddh;
+  L.gate_up = gate_up;
+  L.ld = ld;
+  L.rows = rows;
+  L.f = f;
+  L.act = act;
+  if (axis & MX_ROWWISE) {
+    L.row_data = row_data;
+    L.row_scale = row_scale;
+  }
+  if (col) {
+    L.col_data = col_data;
+    L.col_scale = col_scale;
+  }
+  L.offsets = group_offsets;
+  L.n_groups = n_groups;
+  L.col_pitch = grouped ? col_capacity : rows;
+  L.dev_status = dev_status;
+  return launch_gated(L, static_cast<cudaStream_t>(stream));
+}
 
 }  // namespace
 
@@ -416,6 +517,131 @@ mx_status mx_router_backward(const void* logits, int64_t ld, int dtype, const ui
   L.dlogits = dlogits;
   L.lddx = lddx;
   return launch_router_backward(L, static_cast<cudaStream_t>(stream));
+}
+
+mx_status mx_add_norm_quantize(const void* x, int64_t ldx, const void* residual, int64_t ld_residual, int stream_dtype,
+                               const void* weight, int param_dtype, int64_t rows, int64_t cols, float eps, int axis,
+                               void* sum, int64_t ld_sum, void* y, int64_t ldy, float* rstd, void* row_data,
+                               void* row_scale, void* col_data, void* col_scale, int* dev_status, void* stream) {
+  const char* fn = "mx_add_norm_quantize";
+  MX_CHECK(check_add_norm(fn, rows, cols, stream_dtype, param_dtype, axis));
+  if (!(eps >= 0.0f) || !std::isfinite(eps)) {
+    set_error("mx_add_norm_quantize: eps must be finite and not negative");
+    return MX_ERR_INVALID_ARG;
+  }
+  if (axis == 0 && !y && rows > 0) {
+    set_error("mx_add_norm_quantize: axis 0 without y: nothing of the norm's output is wanted");
+    return MX_ERR_INVALID_ARG;
+  }
+  MX_CHECK(check_copies(fn, axis, rows, cols, row_data, row_scale, col_data, col_scale, false));
+  if (rows == 0) return MX_OK;
+  const int elem = elem_size(stream_dtype);
+  MX_CHECK(check_wide_matrix(fn, "x", x, ldx, cols, 2));
+  if (residual) MX_CHECK(check_wide_matrix(fn, "residual", residual, ld_residual, cols, elem));
+  if (sum) MX_CHECK(check_wide_matrix(fn, "sum", sum, ld_sum, cols, elem));
+  if (y) MX_CHECK(check_wide_matrix(fn, "y", y, ldy, cols, 2));
+  MX_CHECK(check_aligned(fn, "weight", weight, elem_size(param_dtype)));
+  MX_CHECK(check_aligned(fn, "rstd", rstd, 4));
+  MX_CHECK(check_device());
+  AddNormLaunch L = {};
+  L.stream_f32 = stream_dtype == MX_F32;
+  L.first = x;
+  L.ld_first = ldx;
+  L.second = residual;
+  L.ld_second = ld_residual;
+  L.weight = weight;
+  L.param_dtype = param_dtype;
+  L.rows = rows;
+  L.cols = cols;
+  L.eps = eps;
+  L.out = sum;
+  L.ld_out = ld_sum;
+  L.y = y;
+  L.ldy = ldy;
+  L.rstd = rstd;
+  if (axis & MX_ROWWISE) {
+    L.row_data = row_data;
+    L.row_scale = row_scale;
+  }
+  if (axis & MX_COLWISE) {
+    L.col_data = col_data;
+    L.col_scale = col_scale;
+  }
+  L.dev_status = dev_status;
+  return launch_add_norm(L, static_cast<cudaStream_t>(stream));
+}
+
+size_t mx_add_norm_backward_workspace_bytes(int64_t rows, int64_t cols) {
+  return rows <= 0 || cols <= 0 ? 0 : add_norm_backward_workspace(rows, cols);
+}
+
+mx_status mx_add_norm_backward(const void* dy, int64_t lddy, const void* sum, int64_t ld_sum, const void* dsum,
+                               int64_t ld_dsum, int stream_dtype, const void* weight, int param_dtype,
+                               const float* rstd, int64_t rows, int64_t cols, int axis, void* dx, int64_t lddx,
+                               float* dweight, void* row_data, void* row_scale, void* col_data, void* col_scale,
+                               void* workspace, size_t workspace_bytes, int* dev_status, void* stream) {
+  const char* fn = "mx_add_norm_backward";
+  MX_CHECK(check_add_norm(fn, rows, cols, stream_dtype, param_dtype, axis));
+  MX_CHECK(check_copies(fn, axis, rows, cols, row_data, row_scale, col_data, col_scale, false));
+  MX_CHECK(check_aligned(fn, "dweight", dweight, 4));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    if (!dweight) return MX_OK;
+    MX_CHECK(check_device());
+    return cuda_status(cudaMemsetAsync(dweight, 0, static_cast<size_t>(cols) * 4, s), "cudaMemsetAsync");
+  }
+  const int elem = elem_size(stream_dtype);
+  MX_CHECK(check_wide_matrix(fn, "dy", dy, lddy, cols, 2));
+  MX_CHECK(check_wide_matrix(fn, "sum", sum, ld_sum, cols, elem));
+  if (dsum) MX_CHECK(check_wide_matrix(fn, "dsum", dsum, ld_dsum, cols, elem));
+  if (dx || axis == 0) MX_CHECK(check_wide_matrix(fn, "dx", dx, lddx, cols, elem));
+  MX_CHECK(check_present(fn, "rstd", rstd, 4));
+  MX_CHECK(check_aligned(fn, "weight", weight, elem_size(param_dtype)));
+  if (dweight) MX_CHECK(check_workspace(fn, workspace, workspace_bytes, add_norm_backward_workspace(rows, cols)));
+  MX_CHECK(check_device());
+  AddNormLaunch L = {};
+  L.backward = true;
+  L.stream_f32 = stream_dtype == MX_F32;
+  L.first = dy;
+  L.ld_first = lddy;
+  L.second = sum;
+  L.ld_second = ld_sum;
+  L.third = dsum;
+  L.ld_third = ld_dsum;
+  L.weight = weight;
+  L.param_dtype = param_dtype;
+  L.rows = rows;
+  L.cols = cols;
+  L.out = dx;
+  L.ld_out = lddx;
+  L.rstd = const_cast<float*>(rstd);
+  if (axis & MX_ROWWISE) {
+    L.row_data = row_data;
+    L.row_scale = row_scale;
+  }
+  if (axis & MX_COLWISE) {
+    L.col_data = col_data;
+    L.col_scale = col_scale;
+  }
+  L.dweight = dweight;
+  L.ws = workspace;
+  L.dev_status = dev_status;
+  return launch_add_norm(L, s);
+}
+
+mx_status mx_gated_quantize(const void* gate_up, int64_t ld, int64_t rows, int64_t f, int act, int axis, void* row_data,
+                            void* row_scale, void* col_data, void* col_scale, const int64_t* group_offsets, int n_groups,
+                            int64_t col_capacity, int* dev_status, void* stream) {
+  return gated("mx_gated_quantize", false, nullptr, 0, gate_up, ld, rows, f, act, axis, row_data, row_scale, col_data,
+               col_scale, group_offsets, n_groups, col_capacity, dev_status, stream);
+}
+
+mx_status mx_gated_backward_quantize(const void* dh, int64_t lddh, const void* gate_up, int64_t ld, int64_t rows,
+                                     int64_t f, int act, int axis, void* row_data, void* row_scale, void* col_data,
+                                     void* col_scale, const int64_t* group_offsets, int n_groups, int64_t col_capacity,
+                                     int* dev_status, void* stream) {
+  return gated("mx_gated_backward_quantize", true, dh, lddh, gate_up, ld, rows, f, act, axis, row_data, row_scale,
+               col_data, col_scale, group_offsets, n_groups, col_capacity, dev_status, stream);
 }
 
 }  // extern "C"

@@ -73,4 +73,26 @@ __device__ __forceinline__ float2 act_slope(float2 z) {
   return make_float2(1.0f, 1.0f);
 }
 
+// act and d act / dz from one logistic function.
+template <int kAct>
+__device__ __forceinline__ void act_both(float2 z, float2& value, float2& slope) {
+  if constexpr (kAct == MX_ACT_GELU || kAct == MX_ACT_SILU) {
+    float2 q, zu;
+    if constexpr (kAct == MX_ACT_GELU) {
+      const float2 zz = __fmul2_rn(z, z);
+      q = logistic_of_minus(__fmul2_rn(z, __ffma2_rn(zz, act_pair(-kGeluU3 * kLog2e), act_pair(-kGeluU1 * kLog2e))));
+      zu = __fmul2_rn(z, __ffma2_rn(zz, act_pair(3.0f * kGeluU3), act_pair(kGeluU1)));
+    } else {
+      q = logistic_of_minus(__fmul2_rn(z, act_pair(-kLog2e)));
+      zu = z;
+    }
+    const float2 rest = __fmul2_rn(q, __ffma2_rn(q, act_pair(-1.0f), act_pair(1.0f)));
+    slope = __ffma2_rn(slope_bounded(zu), rest, q);
+    value = __fmul2_rn(z, q);
+  } else {
+    slope = act_slope<kAct>(z);
+    value = act_value<kAct>(z);
+  }
+}
+
 }  // namespace mx

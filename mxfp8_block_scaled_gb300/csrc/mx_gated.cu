@@ -1,0 +1,278 @@
+// mx_gated.cu - between the two products of a gated feed-forward block, on
+// gate_up = [gate | up] in BF16, [rows, 2F]:
+//
+//   forward:   h = act(gate) up                            -> MX copies of h
+//   backward:  dgate = dh up act'(gate), dup = dh act(gate) -> MX copies of [dgate | dup]
+//
+// dense, or with the column copy in the experts' segments (padded with zero codes
+// to a multiple of 128 rows, as mx_quantize's). The values go from FP32 registers
+// into the blocks and are never written in BF16: 6.06 bytes per value of F forward,
+// 10.13 backward, which HBM bounds; through a BF16 tensor it would be 10.06 and
+// 18.13.
+//
+// A CTA takes tiles of 128 rows x 128 columns of F, its eight warps 32 x 64 each
+// (mx_block.cuh), on their own: a warp's next unit is on its way into shared memory
+// (TMA, its own mbarrier) while it works on the present one, and no warp waits for
+// another. The activation is computed once for both copies and both gradients.
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "mx_act.cuh"
+#include "mx_block.cuh"
+#include "mx_internal.h"
+#include "mx_ptx.cuh"
+
+namespace mx {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kTile = 128;  // rows and columns of a CTA's tile
+
+struct GatedArgs {
+  CUtensorMap dh, gate, up;
+  CopyOut q;
+  int64_t rows, f;
+  int64_t tiles_c;         // tiles along F
+  int64_t tiles_r;         // tiles along the rows (dense)
+  const int64_t* offsets;
+  int32_t n_groups;
+  int64_t capacity;
+  int* dev_status;
+  uint64_t timeout_ns;
+};
+
+// A warp's unit of a tile.
+struct Unit {
+  int64_t row0, c0, kpos;
+  int32_t rows;  // that exist, <= 0: none
+};
+
+__device__ __forceinline__ Unit unit_of(const GatedArgs& p, int64_t t, int warp, const int32_t* off, const int32_t* tile) {
+  Unit u;
+  const int64_t rt = t / p.tiles_c;
+  const int32_t r = (warp & 3) * kUnitRows;
+  u.c0 = (t - rt * p.tiles_c) * kTile + (warp >> 2) * kUnitCols;
+  u.kpos = rt * kTile + r;
+  if (off) {
+    int lo = 0, hi = p.n_groups - 1;  // the last group that starts at or before this tile (not empty)
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (tile[mid] <= rt) lo = mid; else hi = mid - 1;
+    }
+    const int32_t in = static_cast<int32_t>(rt - tile[lo]) * kTile + r;  // row within the group
+    u.row0 = static_cast<int64_t>(off[lo]) + in;
+    u.rows = min(kUnitRows, off[lo + 1] - off[lo] - in);
+  } else {
+    u.row0 = u.kpos;
+    u.rows = static_cast<int32_t>(min64(kUnitRows, p.rows - u.row0));
+  }
+  return u;
+}
+
+// Offsets of the groups, and their first tiles, into shared memory; returns how
+// many tiles they have, or -1 (status recorded) if they or the capacity are wrong.
+__device__ int32_t setup_groups(const GatedArgs& p, bool col, int32_t* off, int32_t* tile, int32_t* flag) {
+  const int tid = threadIdx.x, E = p.n_groups;
+  if (tid == 0) *flag = 0;
+  __syncthreads();
+  for (int e = tid; e <= E; e += blockDim.x) {
+    const int64_t o = p.offsets[e];
+    off[e] = static_cast<int32_t>(o);
+    if (o < 0 || o > p.rows || (e == 0 && o != 0) || (e == E && o != p.rows) || (e > 0 && o < p.offsets[e - 1])) *flag = 1;
+  }
+  __syncthreads();
+  if (*flag == 0 && tid < 32) {
+    // Exclusive prefix of the groups' tiles, 32 groups a step.
+    int32_t before = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + tid;
+      int32_t n = e < E ? (off[e + 1] - off[e] + kTile - 1) / kTile : 0;
+      const int32_t mine = n;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int32_t t = __shfl_up_sync(0xFFFFFFFFu, n, d);
+        if (tid >= d) n += t;
+      }
+      if (e < E) tile[e] = before + n - mine;
+      before += __shfl_sync(0xFFFFFFFFu, n, 31);
+    }
+    if (tid == 0) {
+      tile[E] = before;
+      if (col && static_cast<int64_t>(before) * kTile > p.capacity) *flag = 1;
+    }
+  }
+  __syncthreads();
+  if (*flag) {
+    if (tid == 0 && blockIdx.x == 0 && p.dev_status) atomicExch(p.dev_status, static_cast<int>(MX_ERR_DEVICE_CHECK));
+    return -1;
+  }
+  return tile[E];
+}
+
+template <int kAct, bool kBackward, bool kRow, bool kCol>
+__global__ void __launch_bounds__(32 * kWarps) gated_kernel(const __grid_constant__ GatedArgs p) {
+  constexpr uint32_t kStage = kBackward ? 3 * 4096 : 2 * 4096;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ uint64_t s_bar[kWarps];
+  __shared__ int32_t s_off[MX_MAX_GROUPS + 1], s_tile[MX_MAX_GROUPS + 1], s_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
+  uint8_t* stage = smem + warp * kStage;
+  uint64_t* bar = &s_bar[warp];
+  if (lane == 0) {
+    mbar_init(bar, 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  pdl_launch_dependents();
+  pdl_wait();
+
+  int64_t tiles_r = p.tiles_r;
+  const int32_t* off = nullptr;
+  if (p.offsets) {
+    tiles_r = setup_groups(p, kCol, s_off, s_tile, &s_flag);
+    if (tiles_r < 0) return;
+    off = s_off;
+  }
+  const int64_t tiles = tiles_r * p.tiles_c, width = kBackward ? 2 * p.f : p.f;
+  {
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x, n = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    if (kRow) zero_scale_padding(p.q.row_scale, p.rows, width >> 5, p.q.row_ka, id, n);
+    if (kCol) zero_scale_padding(p.q.col_scale, width, (off ? tiles_r * kTile : p.rows) >> 5, p.q.col_ka, id, n);
+  }
+
+  // The warp's next unit from tile t on that has something to do, or false.
+  auto find = [&](int64_t& t, Unit& u) {
+    for (; t < tiles; t += gridDim.x) {
+      u = unit_of(p, t, warp, off, s_tile);
+      if (u.c0 < p.f && (u.rows > 0 || (kCol && off))) return true;
+    }
+    return false;
+  };
+  auto load = [&](const Unit& u) {
+    mbar_arrive_expect_tx(bar, kStage);
+    const int32_t x = static_cast<int32_t>(u.c0), y = static_cast<int32_t>(u.row0);
+    tma_load_2d(stage, &p.gate, bar, x, y);
+    tma_load_2d(stage + 4096, &p.up, bar, x, y);
+    if (kBackward) tma_load_2d(stage + 8192, &p.dh, bar, x, y);
+  };
+
+  int64_t t = blockIdx.x;
+  Unit u;
+  bool have = find(t, u), ok = true;
+  if (have && lane == 0) load(u);
+  __syncwarp();
+  for (uint32_t phase = 0; have; phase ^= 1) {
+    if (ok) {
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait(bar, phase, p.timeout_ns));
+      if (!ok) {
+        // Nothing more is loaded; what is left comes out as NaN.
+        if (lane == 0) {
+          if (p.dev_status) atomicExch(p.dev_status, static_cast<int>(MX_ERR_TIMEOUT));
+          mbar_wait(bar, phase, p.timeout_ns);
+        }
+        __syncwarp();
+      }
+    }
+    float2 a[4][8];                   // h, or dgate
+    [[maybe_unused]] float2 b[4][8];  // dup
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 4 * g + i;
+      float2 gate[8], up[8];
+      unit_row_bf16(stage, r, q, gate);
+      unit_row_bf16(stage + 4096, r, q, up);
+      if constexpr (kBackward) {
+        float2 dh[8];
+        unit_row_bf16(stage + 8192, r, q, dh);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float2 value, slope;
+          act_both<kAct>(gate[j], value, slope);
+          a[i][j] = __fmul2_rn(__fmul2_rn(dh[j], up[j]), slope);
+          b[i][j] = __fmul2_rn(dh[j], value);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[i][j] = __fmul2_rn(act_value<kAct>(gate[j]), up[j]);
+      }
+    }
+    __syncwarp();
+    // The next unit's loads into the same stage.
+    const Unit now = u;
+    t += gridDim.x;
+    have = find(t, u);
+    if (have && ok && lane == 0) load(u);
+    __syncwarp();
+    if (!ok || now.rows < kUnitRows) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool there = 4 * g + i < now.rows;
+        const float fill = !ok && there ? __int_as_float(0x7FFFFFFF) : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (!there || !ok) a[i][j] = make_float2(fill, fill);
+          if constexpr (kBackward)
+            if (!there || !ok) b[i][j] = make_float2(fill, fill);
+        }
+      }
+    }
+    store_unit<kRow, kCol>(a, p.q, lane, now.row0, now.rows, now.c0, p.f, now.kpos);
+    if constexpr (kBackward) store_unit<kRow, kCol>(b, p.q, lane, now.row0, now.rows, now.c0 + p.f, 2 * p.f, now.kpos);
+  }
+}
+
+template <int kAct, bool kBackward>
+auto kernel_of(bool row, bool col) -> void (*)(const GatedArgs) {
+  if (row && col) return gated_kernel<kAct, kBackward, true, true>;
+  if (row) return gated_kernel<kAct, kBackward, true, false>;
+  return gated_kernel<kAct, kBackward, false, true>;
+}
+
+template <bool kBackward>
+auto kernel_of(int act, bool row, bool col) -> void (*)(const GatedArgs) {
+  switch (act) {
+    case MX_ACT_RELU: return kernel_of<MX_ACT_RELU, kBackward>(row, col);
+    case MX_ACT_GELU: return kernel_of<MX_ACT_GELU, kBackward>(row, col);
+    case MX_ACT_SILU: return kernel_of<MX_ACT_SILU, kBackward>(row, col);
+    default: return kernel_of<MX_ACT_NONE, kBackward>(row, col);
+  }
+}
+
+}  // namespace
+
+mx_status launch_gated(const GatedLaunch& L, cudaStream_t s) {
+  GatedArgs a = {};
+  const bool back = L.dh != nullptr, row = L.row_data != nullptr, col = L.col_data != nullptr;
+  const int64_t width = back ? 2 * L.f : L.f;
+  mx_status st = make_unit_map(&a.gate, false, L.gate_up, L.f, L.rows, L.ld);
+  if (st == MX_OK) st = make_unit_map(&a.up, false, static_cast<const uint16_t*>(L.gate_up) + L.f, L.f, L.rows, L.ld);
+  if (st == MX_OK && back) st = make_unit_map(&a.dh, false, L.dh, L.f, L.rows, L.lddh);
+  if (st != MX_OK) return st;
+  a.q = CopyOut{static_cast<uint8_t*>(L.row_data), static_cast<uint8_t*>(L.row_scale), static_cast<uint8_t*>(L.col_data),
+                static_cast<uint8_t*>(L.col_scale), width, (width + 127) / 128, L.col_pitch, (L.col_pitch + 127) / 128};
+  a.rows = L.rows;
+  a.f = L.f;
+  a.tiles_c = (L.f + kTile - 1) / kTile;
+  a.tiles_r = (L.rows + kTile - 1) / kTile;
+  a.offsets = L.offsets;
+  a.n_groups = L.n_groups;
+  a.capacity = L.col_pitch;
+  a.dev_status = L.dev_status;
+  a.timeout_ns = wait_timeout_ns();
+  const auto kern = back ? kernel_of<true>(L.act, row, col) : kernel_of<false>(L.act, row, col);
+  const size_t smem = 1024 + kWarps * (back ? 3 : 2) * 4096;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(gated)");
+  const int64_t upper = (a.tiles_r + (L.offsets ? L.n_groups : 0)) * a.tiles_c;
+  const unsigned grid = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(upper, (back ? 1 : 2) * sm_count())));
+  return cuda_status(launch_kernel(kern, grid, 32 * kWarps, smem, s, 1, a),
+                     back ? "mx_gated_backward_quantize launch" : "mx_gated_quantize launch");
+}
+
+}  // namespace mx

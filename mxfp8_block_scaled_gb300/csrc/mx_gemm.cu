@@ -273,7 +273,10 @@ __device__ __forceinline__ int64_t num_tiles(const GParams& p, const GroupInfo& 
   return static_cast<int64_t>(p.n_groups) * mt * nt;
 }
 
-template <int BN, int KIND>
+// kGated (mx_gemm_gated): tile column nb holds the output's columns [128 nb, 128 nb +
+// 128): their gate columns in the accumulator's first half, their up columns in
+// the second.
+template <int BN, int KIND, bool kGated = false>
 __device__ __forceinline__ Tile get_tile(const GParams& p, const GroupInfo& g, int64_t t) {
   Tile ti;
   ti.part = -1;
@@ -283,7 +286,7 @@ __device__ __forceinline__ Tile get_tile(const GParams& p, const GroupInfo& g, i
     const int64_t mb = p.n_fast ? t / nt : t % mt;
     const int64_t nb = p.n_fast ? t % nt : t / mt;
     ti.m0 = mb * kBM;
-    ti.n0 = nb * BN;
+    ti.n0 = nb * (kGated ? BN / 2 : BN);
     ti.a_row = ti.m0;
     ti.b_row = ti.n0;
     ti.k_atom0 = 0;
@@ -415,10 +418,16 @@ __device__ __forceinline__ Tile get_pair_tile(const GParams& p, const GroupInfo&
     ti.group = e;
   }
   ti.m0 = (2 * mp + crank) * kBM;
-  ti.n0 = nb * BN;
   ti.a_row = ti.m0;
-  ti.n_mma = pair_n_mma<BN>(p.N, ti.n0);
-  ti.b_row = ti.n0 + crank * (ti.n_mma / 2);
+  if (kSwiGLU) {
+    // Dense: gate and up are operands of their own, the even CTA's and the odd one's.
+    ti.n0 = nb * (BN / 2);
+    ti.b_row = ti.n0;
+  } else {
+    ti.n0 = nb * BN;
+    ti.n_mma = pair_n_mma<BN>(p.N, ti.n0);
+    ti.b_row = ti.n0 + crank * (ti.n_mma / 2);
+  }
   ti.valid_m = static_cast<int32_t>(min64(kBM, p.M - ti.m0));
   ti.sfb = p.b_scale;
   ti.cbase = p.c + static_cast<int64_t>(ti.group) * p.c_group_stride + ti.m0 * p.ldc + ti.n0;
@@ -778,10 +787,27 @@ struct EpiArgs {
   int32_t z_tma;   // as GParams' c_tma, for the pre-activation
   int32_t r_vec;   // 1: every residual row start is 16-byte aligned
 };
+// kEpi 3 and 4 (mx_gemm_gated; alignments as 1 and 2): out = act(gate) up on the
+// FP32 accumulators of the two products, each of them stored too where it is kept.
+struct GatedArgs {
+  CUtensorMap up, sf_up;   // the second operand and its scales
+  CUtensorMap zg, zu;      // kept projections, as the output's map
+  const uint8_t* up_scale;
+  __nv_bfloat16* preact;   // [M, 2F], gate first; null: not kept
+  int64_t ld_preact;
+  int32_t z_tma;
+  int32_t act;
+};
+__host__ __device__ constexpr bool gated_epi(int kEpi) { return kEpi >= 3; }
+__host__ __device__ constexpr bool bias_epi(int kEpi) { return kEpi == 1 || kEpi == 2; }
 template <int kEpi>
 struct EpiParamT { using type = EpiArgs; };
 template <>
 struct EpiParamT<0> { using type = EpiNone; };
+template <>
+struct EpiParamT<3> { using type = GatedArgs; };
+template <>
+struct EpiParamT<4> { using type = GatedArgs; };
 
 // Before a tile's accumulator is ready: asks L2 for this warp's part of the
 // residual (lane = row, one 128-byte line at a time) and returns the bias of
@@ -827,7 +853,7 @@ __device__ __forceinline__ void epi_store_elements(__nv_bfloat16* dst, int64_t l
 template <int kEpi>
 __device__ __forceinline__ void epi_store_box(const OutView& o, const CUtensorMap* map, const Tile& ti, const float2* r,
                                               int quarter, int lane, int col, uint8_t* box) {
-  if (kEpi == 1 || o.c_tma) {
+  if (kEpi == 1 || kEpi == 3 || o.c_tma) {
     epi_wait_box(lane);
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
@@ -978,6 +1004,37 @@ __device__ __forceinline__ void epi_tile(const GParams& p, const EpiArgs& ea, co
   }
 }
 
+// r: 64 gate accumulators of row quarter * 32 + lane (output columns from n0 +
+// col_off), then the 64 up ones of the same columns.
+template <int kEpi>
+__device__ __forceinline__ void gated_tile(const GParams& p, const GatedArgs& ga, const Tile& ti, const uint32_t* r,
+                                           int quarter, int lane, int col_off, uint8_t* stg, const CUtensorMap* tmap_c) {
+  const OutView out = out_view(p, ti);
+  __nv_bfloat16* z = ga.preact + ti.m0 * ga.ld_preact + ti.n0;
+  const OutView gv{z, ga.ld_preact, p.n_out, 0, ga.z_tma}, uv{z + p.n_out, ga.ld_preact, p.n_out, 0, ga.z_tma};
+#pragma unroll
+  for (int ch = 0; ch < 2; ++ch) {
+    const int col = col_off + ch * 32;
+    if (ti.n0 + col >= p.n_out) break;  // nothing of the output here
+    float2 gt[16], up[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      gt[i] = make_float2(__uint_as_float(r[ch * 32 + 2 * i]), __uint_as_float(r[ch * 32 + 2 * i + 1]));
+      up[i] = make_float2(__uint_as_float(r[64 + ch * 32 + 2 * i]), __uint_as_float(r[64 + ch * 32 + 2 * i + 1]));
+    }
+    if (ga.preact) {
+      epi_store_box<kEpi>(gv, &ga.zg, ti, gt, quarter, lane, col, stg);
+      epi_store_box<kEpi>(uv, &ga.zu, ti, up, quarter, lane, col, stg);
+    }
+    if (ga.act == MX_ACT_SILU) epi_activate<MX_ACT_SILU>(gt);
+    else if (ga.act == MX_ACT_GELU) epi_activate<MX_ACT_GELU>(gt);
+    else if (ga.act == MX_ACT_RELU) epi_activate<MX_ACT_RELU>(gt);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) gt[i] = __fmul2_rn(gt[i], up[i]);
+    epi_store_box<kEpi>(out, tmap_c, ti, gt, quarter, lane, col, stg);
+  }
+}
+
 // ===========================================================================
 // Single-CTA kernel (dense and grouped)
 // ===========================================================================
@@ -988,6 +1045,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap tmap_c, const GParams p,
                    const __grid_constant__ typename EpiParamT<kEpi>::type epi) {
   static_assert(!kEpi || KIND == GEMM_DENSE, "the bias / activation / residual epilogue is the dense GEMM's");
+  constexpr bool kGated = gated_epi(kEpi);
+  static_assert(!kGated || BN == 256, "128 gate and 128 up columns: whole scale atoms");
   using C = Cfg<BN>;
   constexpr int S = C::kStages;
   constexpr int ACC = C::kAcc;
@@ -1070,7 +1129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The whole warp only where it gathers scale words; otherwise lane 0 alone
     // (a per-stage warp shuffle slows the stage issue).
     for (int64_t t = blockIdx.x; t < ntiles && ok && (kGatherSfa || lane == 0); t += gridDim.x) {
-      const Tile ti = get_tile<BN, KIND>(p, g, t);
+      const Tile ti = get_tile<BN, KIND, kGated>(p, g, t);
       const int64_t sfb_row_atom0 = ti.n0 / 128;
       for (int kb = 0; kb < ti.nkb; ++kb) {
         const int64_t katom = ti.k_atom0 + kb;
@@ -1102,15 +1161,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t bytes = C::kABytes + C::kBBytes + (kGatherSfa ? 0 : 512);
 #pragma unroll
           for (int j = 0; j < C::kSfbAtoms; ++j)
-            if (sfb_row_atom0 + j < p.b_ra) bytes += 512;
+            if (kGated || sfb_row_atom0 + j < p.b_ra) bytes += 512;
           mbar_arrive_expect_tx(&full_bar[stage], bytes);
           const int32_t kx = static_cast<int32_t>(katom * kBK);
           tma_load_2d(sA + stage * C::kABytes, &tmap_a, &full_bar[stage], kx, static_cast<int32_t>(ti.a_row));
           tma_load_2d(sB + stage * C::kBBytes, &tmap_b, &full_bar[stage], kx, static_cast<int32_t>(ti.b_row));
+          if constexpr (kGated)  // the maps' boxes are 128 rows
+            tma_load_2d(sB + stage * C::kBBytes + 128 * kBK, &epi.up, &full_bar[stage], kx, static_cast<int32_t>(ti.b_row));
           if constexpr (!kGatherSfa)
             bulk_load(sSfa + stage * 512, p.a_scale + (((ti.m0 >> 7) * p.ka + katom) << 9), 512, &full_bar[stage]);
+          if constexpr (kGated) {
+            bulk_load(sSfb + stage * C::kSfbBytes, p.b_scale + ((sfb_row_atom0 * p.ka + katom) << 9), 512, &full_bar[stage]);
+            bulk_load(sSfb + stage * C::kSfbBytes + 512, epi.up_scale + ((sfb_row_atom0 * p.ka + katom) << 9), 512,
+                      &full_bar[stage]);
+          }
 #pragma unroll
-          for (int j = 0; j < C::kSfbAtoms; ++j)
+          for (int j = 0; j < (kGated ? 0 : C::kSfbAtoms); ++j)
             if (sfb_row_atom0 + j < p.b_ra)
               bulk_load(sSfb + stage * C::kSfbBytes + j * 512, ti.sfb + (((sfb_row_atom0 + j) * p.ka + katom) << 9),
                         512, &full_bar[stage]);
@@ -1144,7 +1210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t acc_phase = 0;
       bool ok = true;
       for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
-        const Tile ti = get_tile<BN, KIND>(p, g, t);
+        const Tile ti = get_tile<BN, KIND, kGated>(p, g, t);
         if (!wait_or_abort(&acc_empty[acc], acc_phase ^ 1, p, s_abort)) break;
         tc_fence_after_sync();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * BN);
@@ -1196,7 +1262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int64_t t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
-        const Tile ti = get_tile<BN, KIND>(p, g, t);
+        const Tile ti = get_tile<BN, KIND, kGated>(p, g, t);
         for (int kb = 0; kb < ti.nkb; ++kb) {
           if (!wait_or_abort(&full_bar[stage], phase, p, s_abort)) {
             ok = false;
@@ -1236,18 +1302,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int64_t t = blockIdx.x; t < ntiles; t += gridDim.x) {
-      const Tile ti = get_tile<BN, KIND>(p, g, t);
+      const Tile ti = get_tile<BN, KIND, kGated>(p, g, t);
       [[maybe_unused]] float4 bias;
-      if constexpr (kEpi) bias = epi_prepare(p, epi, ti, quarter, lane, my_chunks * 32, col_off);
+      if constexpr (bias_epi(kEpi)) bias = epi_prepare(p, epi, ti, quarter, lane, my_chunks * 32, col_off);
       if (!wait_or_abort(&acc_full[acc], acc_phase, p, s_abort)) break;
       tc_fence_after_sync();
       uint32_t r[kCols];
       if (ti.nkb > 0) {
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) +
                                static_cast<uint32_t>(acc * BN + col_off);
+        if constexpr (kGated) {
+          // 64 gate columns, then the up columns 128 further on.
+          const uint32_t half_addr = taddr - static_cast<uint32_t>(64 * half);
+          tmem_ld_32x32b_x32(half_addr, r);
+          tmem_ld_32x32b_x32(half_addr + 32, r + 32);
+          tmem_ld_32x32b_x32(half_addr + 128, r + 64);
+          tmem_ld_32x32b_x32(half_addr + 160, r + 96);
+        } else {
 #pragma unroll
-        for (int ch = 0; ch < kHalf0; ++ch)
-          if (ch < my_chunks) tmem_ld_32x32b_x32(taddr + ch * 32, r + ch * 32);
+          for (int ch = 0; ch < kHalf0; ++ch)
+            if (ch < my_chunks) tmem_ld_32x32b_x32(taddr + ch * 32, r + ch * 32);
+        }
         tmem_ld_wait();
       } else {
 #pragma unroll
@@ -1259,7 +1334,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         acc = 0;
         acc_phase ^= 1;
       }
-      if constexpr (kEpi)
+      if constexpr (kGated)
+        gated_tile<kEpi>(p, epi, ti, r, quarter, lane, 64 * half, stg, &tmap_c);
+      else if constexpr (bias_epi(kEpi))
         epi_tile<kEpi, kCols>(p, epi, ti, r, bias, quarter, lane, my_chunks, col_off, stg, s_bias, &tmap_c);
       else store_tile<KIND, kCols>(out_view(p, ti), ti, r, quarter, lane, my_chunks, col_off, stg, &tmap_c);
     }
@@ -1320,8 +1397,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                         const __grid_constant__ typename EpiParamT<kEpi>::type epi) {
   static_assert(!kEpi || (KIND == GEMM_DENSE && !kSwiGLU_ && !kMulti && !kTS), "dense, block-scaled, one problem");
   constexpr bool kSwiGLU = kSwiGLU_ != 0;
+  constexpr bool kGated = gated_epi(kEpi);
+  constexpr bool kTwoHalves = kSwiGLU || kGated;  // the accumulator holds 128 gate and 128 up columns
   constexpr bool kSwiQ = kSwiGLU_ == 2;
-  using C = PairCfgT<BN_, kTS, KIND != GEMM_DENSE, kEpi != 0>;
+  using C = PairCfgT<BN_, kTS, KIND != GEMM_DENSE, bias_epi(kEpi)>;
   static_assert(!kMulti || (KIND == GEMM_DENSE && !kSwiGLU), "several problems per launch: dense GEMMs only");
   // Problem 0 holds the fields every problem shares (status word, wait bound)
   // and, unless kMulti, the whole GEMM.
@@ -1456,7 +1535,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     for (int64_t it = 0, t; lane == 0 && ok && (t = next_tile(it)) >= 0; ++it) {
       const int pi = problem_of<kMulti>(args, t);
         const GParams& pp = args.prob[pi].p;
-        const Tile ti = get_pair_tile<KIND, kSwiGLU, BN>(pp, g, kMulti ? t - args.tile0[pi] : t, crank);
+        const Tile ti = get_pair_tile<KIND, kTwoHalves, BN>(pp, g, kMulti ? t - args.tile0[pi] : t, crank);
       // Rows-ragged: B's scale atoms are those of the tile's expert. SwiGLU:
       // the second atom holds the up rows, N/256 atoms after the gate rows.
       const int64_t sfb_atom_row = (KIND == GEMM_GROUPED_M ? ti.group * pp.b_ra : 0) + (ti.n0 >> 7);
@@ -1475,12 +1554,18 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mbar_arrive_expect_tx(&full_bar[stage], 2 * (C::kStageTx - (kGatherSfa ? C::kSfaBytes : 0)));
           const int32_t kx = static_cast<int32_t>(katom * kBK);
           tma_load_2d_pair(sA + stage * C::kABytes, &args.prob[pi].a, lfull, kx, static_cast<int32_t>(ti.a_row));
-          tma_load_2d_pair(sB + stage * C::kBBytes, &args.prob[pi].b, lfull, kx, static_cast<int32_t>(ti.b_row));
+          const CUtensorMap* map_b = &args.prob[pi].b;
+          if constexpr (kGated) map_b = leader ? map_b : &epi.up;
+          tma_load_2d_pair(sB + stage * C::kBBytes, map_b, lfull, kx, static_cast<int32_t>(ti.b_row));
           // Scale atoms through [atoms][128 words] views (rows past the end read as zero).
           if constexpr (!kTS && !kGatherSfa)
             tma_load_2d_pair(sSfa + stage * C::kSfaBytes, &args.prob[pi].sfa, lfull, 0,
                              static_cast<int32_t>((ti.m0 >> 7) * pp.ka + katom));
-          if constexpr (!kTS) {
+          if constexpr (kGated) {
+            const int32_t atom = static_cast<int32_t>((ti.n0 >> 7) * pp.ka + katom);
+            tma_load_2d_pair(sSfb + stage * C::kSfbBytes, &args.prob[pi].sfb, lfull, 0, atom);
+            tma_load_2d_pair(sSfb + stage * C::kSfbBytes + 512, &epi.sf_up, lfull, 0, atom);
+          } else if constexpr (!kTS) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
               tma_load_2d_pair(sSfb + stage * C::kSfbBytes + j * 512, &args.prob[pi].sfb, lfull, 0,
@@ -1519,7 +1604,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       for (int64_t it = 0, t; ok && (t = next_tile(it)) >= 0; ++it) {
         const int pi = problem_of<kMulti>(args, t);
         const GParams& pp = args.prob[pi].p;
-        const Tile ti = get_pair_tile<KIND, kSwiGLU, BN>(pp, g, kMulti ? t - args.tile0[pi] : t, crank);
+        const Tile ti = get_pair_tile<KIND, kTwoHalves, BN>(pp, g, kMulti ? t - args.tile0[pi] : t, crank);
         if (ti.part == -2) continue;  // an empty split-tail segment
         if (!wait_or_abort<true>(&acc_empty[acc], acc_phase ^ 1, p, s_abort)) break;
         tc_fence_after_sync();
@@ -1588,7 +1673,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       for (int64_t it = 0, t; ok && (t = next_tile(it)) >= 0; ++it) {
         const int pi = problem_of<kMulti>(args, t);
         const GParams& pp = args.prob[pi].p;
-        const Tile ti = get_pair_tile<KIND, kSwiGLU, BN>(pp, g, kMulti ? t - args.tile0[pi] : t, crank);
+        const Tile ti = get_pair_tile<KIND, kTwoHalves, BN>(pp, g, kMulti ? t - args.tile0[pi] : t, crank);
         for (int kb = 0; kb < ti.nkb; ++kb) {
           if (!wait_or_abort(&gfull[stage], phase, p, s_abort)) {
             ok = false;
@@ -1610,7 +1695,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       for (int64_t it = 0, t; ok && (t = next_tile(it)) >= 0; ++it) {
         const int pi = problem_of<kMulti>(args, t);
         const GParams& pp = args.prob[pi].p;
-        const Tile ti = get_pair_tile<KIND, kSwiGLU, BN>(pp, g, kMulti ? t - args.tile0[pi] : t, crank);
+        const Tile ti = get_pair_tile<KIND, kTwoHalves, BN>(pp, g, kMulti ? t - args.tile0[pi] : t, crank);
         for (int kb = 0; kb < ti.nkb; ++kb) {
           if (!wait_or_abort<true>(&full_bar[stage], phase, p, s_abort)) {
             ok = false;
@@ -1647,7 +1732,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       for (int64_t it = 0, t; ok && (t = next_tile(it)) >= 0; ++it) {
         const int pi = problem_of<kMulti>(args, t);
         const GParams& pp = args.prob[pi].p;
-        const Tile ti = get_pair_tile<KIND, kSwiGLU, BN>(pp, g, kMulti ? t - args.tile0[pi] : t, crank);
+        const Tile ti = get_pair_tile<KIND, kTwoHalves, BN>(pp, g, kMulti ? t - args.tile0[pi] : t, crank);
         for (int kb = 0; kb < ti.nkb; ++kb) {
           uint32_t good = 1;
           if (lane == 0) good = wait_or_abort<true>(&empty_bar[stage], phase ^ 1, p, s_abort) ? 1u : 0u;
@@ -1686,23 +1771,23 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     constexpr int kCols = BN / 2;
     const int col_off = half * kCols;
     uint8_t* stg = sEpi + (warp - 2) * C::kEpiBufs * kEpiWarpBytes;
-    [[maybe_unused]] float* s_bias = reinterpret_cast<float*>(smem + C::smem_bytes() - 1024 - (kEpi ? kEpiBiasBytes : 0)) + (warp - 2) * 128;
+    [[maybe_unused]] float* s_bias = reinterpret_cast<float*>(smem + C::smem_bytes() - 1024 - (bias_epi(kEpi) ? kEpiBiasBytes : 0)) + (warp - 2) * 128;
     int acc = 0;
     uint32_t acc_phase = 0;
     for (int64_t it = 0, t; (t = next_tile(it)) >= 0; ++it) {
       const int pi = problem_of<kMulti>(args, t);
       const GParams& pp = args.prob[pi].p;
-      const Tile ti = get_pair_tile<KIND, kSwiGLU, BN>(pp, g, kMulti ? t - args.tile0[pi] : t, crank);
+      const Tile ti = get_pair_tile<KIND, kTwoHalves, BN>(pp, g, kMulti ? t - args.tile0[pi] : t, crank);
       if (ti.part == -2) continue;
       float ts = 1.0f;  // the tile's product of tensor scales (kTS), read while the MMAs run
       if constexpr (kTS) ts = __ldg(pp.ts_a) * __ldg(pp.ts_b + (KIND == GEMM_GROUPED_M ? ti.group : 0));
       [[maybe_unused]] float4 bias;
-      if constexpr (kEpi) bias = epi_prepare(pp, epi, ti, quarter, lane, kCols, col_off);
+      if constexpr (bias_epi(kEpi)) bias = epi_prepare(pp, epi, ti, quarter, lane, kCols, col_off);
       if (!wait_or_abort<true>(&acc_full[acc], acc_phase, p, s_abort)) break;
       tc_fence_after_sync();
       uint32_t r[kCols];
       if (ti.nkb > 0) {
-        if (kSwiGLU) {
+        if (kTwoHalves) {
           // Features [64 half, 64 half + 64): gate columns then the up columns
           // 128 further on.
           const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(64 * half);
@@ -1760,6 +1845,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         } else {
           store_tile<KIND, 64, C::kEpiBufs>(out_view(pp, ti), ti, r, quarter, lane, 2, 64 * half, stg, &args.prob[pi].c);
         }
+      } else if constexpr (kGated) {
+        gated_tile<kEpi>(pp, epi, ti, r, quarter, lane, 64 * half, stg, &args.prob[pi].c);
       } else if constexpr (kEpi) {
         epi_tile<kEpi, kCols>(pp, epi, ti, r, bias, quarter, lane, kCols / 32, col_off, stg, s_bias,
                                      &args.prob[pi].c);
@@ -2179,7 +2266,7 @@ mx_status make_out_map(CUtensorMap* map, void* c, int64_t groups, int64_t rows, 
 void output_map(const GemmLaunch& L, GParams& p, CUtensorMap* mc, int kind) {
   std::memset(mc, 0, sizeof(*mc));
   p.c_tma = 0;
-  const int64_t n_out = L.swiglu ? L.N / 2 : L.N;
+  const int64_t n_out = L.swiglu || L.up_data ? L.N / 2 : L.N;
   // TMA stores clip a row at 16-byte granularity: with a row width that is not
   // a multiple of 8 elements they would also write the first elements of the
   // pitch gap, so such outputs take the plain bounded stores.
@@ -2191,8 +2278,10 @@ void output_map(const GemmLaunch& L, GParams& p, CUtensorMap* mc, int kind) {
 
 // Which epilogue kernel a GEMM takes (EpiNone).
 int epi_kind(const GemmLaunch& L) {
-  if (!L.has_epi) return 0;
   const auto aligned = [](const void* p, int64_t ld) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld % 8 == 0; };
+  if (L.up_data)
+    return L.N % 16 == 0 && aligned(L.c, L.ldc) && (!L.epi.preact || aligned(L.epi.preact, L.epi.ld_preact)) ? 3 : 4;
+  if (!L.has_epi) return 0;
   return L.N % 8 == 0 && aligned(L.c, L.ldc) && (!L.epi.preact || aligned(L.epi.preact, L.epi.ld_preact)) &&
                  (!L.epi.residual || aligned(L.epi.residual, L.epi.ld_residual))
              ? 1
@@ -2203,7 +2292,24 @@ int epi_kind(const GemmLaunch& L) {
 // stores (the same conditions as the output's).
 template <int kEpi>
 mx_status epi_args(const GemmLaunch& L, bool c_tma, typename EpiParamT<kEpi>::type* a) {
-  if constexpr (kEpi) {
+  if constexpr (gated_epi(kEpi)) {
+    std::memset(a, 0, sizeof(*a));
+    const int64_t f = L.N / 2;
+    mx_status st = make_map(&a->up, L.up_data, f, L.K, L.up_ld, kBM);
+    if (st == MX_OK) st = make_scale_map(&a->sf_up, L.up_scale, f, L.K);
+    if (st != MX_OK) return st;
+    a->up_scale = static_cast<const uint8_t*>(L.up_scale);
+    a->preact = static_cast<__nv_bfloat16*>(L.epi.preact);
+    a->ld_preact = L.epi.ld_preact;
+    a->act = L.epi.act;
+    if (kEpi == 3 && a->preact) {
+      st = make_out_map(&a->zg, a->preact, 1, L.M, f, a->ld_preact);
+      if (st == MX_OK) st = make_out_map(&a->zu, a->preact + f, 1, L.M, f, a->ld_preact);
+      if (st != MX_OK) return st;
+      a->z_tma = 1;
+    }
+    if (kEpi == 3 && !c_tma) return MX_ERR_CUDA;  // the encoder's message stands
+  } else if constexpr (kEpi) {
     std::memset(a, 0, sizeof(*a));
     a->e = L.epi;
     a->r_vec = (reinterpret_cast<uintptr_t>(L.epi.residual) & 15u) == 0 && L.epi.ld_residual % 8 == 0;
@@ -2224,10 +2330,10 @@ mx_status launch_cfg(const GemmLaunch& L, const GParams& p_in, int64_t tiles_upp
   CUtensorMap ma, mb, mc;
   mx_status st = make_map(&ma, L.a_data, L.M, L.K, L.a_ld, kBM);
   if (st != MX_OK) return st;
-  st = make_map(&mb, L.b_data, L.b_rows_total, L.K, L.b_ld, BN);
+  st = make_map(&mb, L.b_data, L.b_rows_total, L.K, L.b_ld, gated_epi(kEpi) ? BN / 2 : BN);
   if (st != MX_OK) return st;
   output_map(L, p, &mc, KIND);
-  const size_t smem = Cfg<BN>::smem_bytes(KIND != GEMM_DENSE) + (kEpi ? kEpiBiasBytes : 0);
+  const size_t smem = Cfg<BN>::smem_bytes(KIND != GEMM_DENSE) + (bias_epi(kEpi) ? kEpiBiasBytes : 0);
   typename EpiParamT<kEpi>::type epi;
   st = epi_args<kEpi>(L, p.c_tma != 0, &epi);
   if (st != MX_OK) return st;
@@ -2328,12 +2434,14 @@ mx_status launch_pair(const GemmLaunch& L, const GParams& p_in, cudaStream_t s) 
     st = make_scale_map(&msa, L.a_scale, L.M, L.K);
     if (st != MX_OK) return st;
     // Stacked experts: one [E x row atoms x K atoms] view of all experts' scales.
-    const int64_t sfb_rows = (KIND == GEMM_GROUPED_M) ? L.n_groups * ((L.N + 127) / 128 * 128) : L.N;
+    const int64_t sfb_rows = gated_epi(kEpi)            ? L.N / 2
+                             : (KIND == GEMM_GROUPED_M) ? L.n_groups * ((L.N + 127) / 128 * 128)
+                                                        : L.N;
     st = make_scale_map(&msb, L.b_scale, sfb_rows, L.K);
     if (st != MX_OK) return st;
   }
   output_map(L, p, &mc, KIND);
-  const size_t smem = PairCfgT<BN, kTS, KIND != GEMM_DENSE, kEpi != 0>::smem_bytes();
+  const size_t smem = PairCfgT<BN, kTS, KIND != GEMM_DENSE, bias_epi(kEpi)>::smem_bytes();
   typename EpiParamT<kEpi>::type epi;
   st = epi_args<kEpi>(L, p.c_tma != 0, &epi);
   if (st != MX_OK) return st;
@@ -2521,7 +2629,7 @@ GParams make_gparams(const GemmLaunch& L) {
   p.b_scale = static_cast<const uint8_t*>(L.b_scale);
   p.M = L.M;
   p.N = L.N;
-  p.n_out = L.swiglu ? L.N / 2 : L.N;
+  p.n_out = L.swiglu || L.up_data ? L.N / 2 : L.N;
   p.K = L.K;
   p.ka = (L.K + 127) / 128;
   p.a_ra = (L.M + 127) / 128;
@@ -2682,6 +2790,12 @@ mx_status launch_gemm(const GemmLaunch& L, cudaStream_t s) {
   if (L.swiglu) return L.q_row_data ? launch_pair<GEMM_GROUPED_M, 2>(L, p, s) : launch_pair<GEMM_GROUPED_M, 1>(L, p, s);
   int bn;
   const int epi = epi_kind(L);
+  if (gated_epi(epi)) {
+    const int64_t tiles = (L.M + kBM - 1) / kBM * ((L.N + 255) / 256);
+    if (dense_cfg_time_us(L, CFG_PAIR) <= dense_cfg_time_us(L, CFG_BN256))
+      return epi == 3 ? launch_pair<GEMM_DENSE, 0, 256, false, 3>(L, p, s) : launch_pair<GEMM_DENSE, 0, 256, false, 4>(L, p, s);
+    return epi == 3 ? launch_cfg<256, GEMM_DENSE, 3>(L, p, tiles, s) : launch_cfg<256, GEMM_DENSE, 4>(L, p, tiles, s);
+  }
   if (L.kind == GEMM_DENSE) {
     const int cfg = choose_dense_cfg(L);
     if (cfg == CFG_PAIR)

@@ -2,6 +2,7 @@
 // (host side only; no device code here).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <cstdint>
 #include <cstring>
@@ -152,6 +153,12 @@ struct GemmLaunch {
   // no split tail).
   bool has_epi = false;
   GemmEpilogue epi = {};
+  // Dense, block-scaled only (mx_gemm_gated): b is the gate's operand, this one the
+  // up projection's; N counts both (2F), C = act(A . B^T) * (A . up^T) has F
+  // columns; epi.preact (with ld_preact) and epi.act are read.
+  const void* up_data = nullptr;
+  const void* up_scale = nullptr;
+  int64_t up_ld = 0;
 };
 mx_status launch_gemm(const GemmLaunch& g, cudaStream_t s);
 // Bytes of workspace the dense GEMM L would use for its split tail (0: none).
@@ -239,6 +246,57 @@ struct NormLaunch {
 mx_status launch_norm_forward(const NormLaunch& L, cudaStream_t s);
 mx_status launch_norm_backward(const NormLaunch& L, cudaStream_t s);
 size_t norm_backward_workspace(int64_t rows, int64_t cols);
+// Tensor map over a [rows, cols] matrix (pitch ld elements) in boxes of 32 rows of
+// 128 bytes, 128-byte swizzle: BF16 boxes of 64 columns, FP32 ones of 32.
+mx_status make_unit_map(CUtensorMap* map, bool f32, const void* base, int64_t cols, int64_t rows, int64_t ld);
+
+struct AddNormLaunch {
+  bool backward;
+  bool stream_f32;      // residual and sum (backward: sum, dsum and dx) are FP32
+  const void* first;    // x; backward: dy (BF16)
+  int64_t ld_first;
+  const void* second;   // residual (may be null); backward: sum
+  int64_t ld_second;
+  const void* third;    // backward: dsum (may be null)
+  int64_t ld_third;
+  const void* weight;   // may be null
+  int param_dtype;
+  int64_t rows, cols;
+  float eps;
+  void* out;            // sum (may be null); backward: dx
+  int64_t ld_out;
+  void* y;              // forward, may be null
+  int64_t ldy;
+  float* rstd;          // written (may be null); backward: read
+  void* row_data;       // null: no row copy
+  void* row_scale;
+  void* col_data;       // null: no column copy
+  void* col_scale;
+  float* dweight;       // backward, may be null
+  void* ws;
+  int* dev_status;
+};
+mx_status launch_add_norm(const AddNormLaunch& L, cudaStream_t s);
+size_t add_norm_backward_workspace(int64_t rows, int64_t cols);
+
+struct GatedLaunch {
+  const void* dh;       // backward (BF16 [rows, F]); null: forward
+  int64_t lddh;
+  const void* gate_up;  // BF16 [rows, 2F]
+  int64_t ld;
+  int64_t rows, f;
+  int act;
+  void* row_data;       // null: no row copy
+  void* row_scale;
+  void* col_data;       // null: no column copy
+  void* col_scale;
+  const int64_t* offsets;  // null: dense
+  int n_groups;
+  int64_t col_pitch;    // rows (dense) or the capacity
+  int* dev_status;
+};
+mx_status launch_gated(const GatedLaunch& L, cudaStream_t s);
+
 // Sums over p < parts of partial[p][c], added in a fixed order: columns [0, n0)
 // to out0, [n0, n0 + n1) to out1 (null: not wanted).
 mx_status launch_column_reduce(const float* partial, int parts, int64_t n0, int64_t n1, float* out0, float* out1,

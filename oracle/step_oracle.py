@@ -177,3 +177,60 @@ def router_backward(x, idx, load, dweights, dloss, seq, mask=None, normalize=Fal
         g[t, sel] += dw
     dx = p * (g - (p * g).sum(1, keepdims=True))
     return np.where(valid[:, None], dx, 0.0)
+
+
+# ---------------------------------------------------------------------------
+# Gated feed-forward block: the norm with the residual's addition, the gate
+# ---------------------------------------------------------------------------
+
+def add_norm(x, residual, w, eps):
+    """(sum, rstd, y)."""
+    v = x + residual
+    rstd = 1.0 / np.sqrt((v * v).mean(1) + eps)
+    return v, rstd, v * rstd[:, None] * w
+
+
+def add_norm_backward(dy, v, w, rstd, dsum):
+    """(dx, dw) from the sum and its statistic."""
+    h = v * rstd[:, None]
+    g = dy * w
+    return dsum + rstd[:, None] * (g - h * (g * h).mean(1, keepdims=True)), (dy * h).sum(0)
+
+
+def gated(gate, up, name):
+    return act(gate, name) * up
+
+
+def gated_backward(dh, gate, up, name):
+    """(dgate, dup)."""
+    return dh * up * act_slope(gate, name), dh * act(gate, name)
+
+
+def segments(x, offsets):
+    """Rows of x with each group's padded with zeros to a multiple of 128."""
+    parts = [np.pad(x[a:b], ((0, -(b - a) % 128), (0, 0))) for a, b in zip(offsets, offsets[1:])]
+    return np.concatenate(parts) if parts else x[:0]
+
+
+def copy_error(codes, scales, ref, tol):
+    """How far an MX copy (codes [R, K], logical scales [R, K/32]) of values within
+    tol of ref goes beyond what its rounding allows, at most (<= 0: nowhere).
+
+    A block's exponent has to be the one of an amax within tol of ref's; a value may
+    be off by half an E4M3 step (2^-4 of it, or 2^-10 of the scale below the normal
+    range) and saturates at 448 times the scale."""
+    R, K = ref.shape
+    val = e4m3_values()[codes].reshape(R, K // 32, 32)
+    r, t = np.abs(ref).reshape(val.shape), np.broadcast_to(tol, ref.shape).reshape(val.shape)
+    sign_ref = ref.reshape(val.shape)
+    X = scales.astype(np.int64) - 127
+
+    def exponent(a):
+        with np.errstate(divide="ignore"):
+            return np.where(a > 0, np.clip(np.frexp(a)[1] - 1 - 8, -127, 127), -127)
+
+    low, high = exponent(np.maximum(r - t, 0).max(2)), exponent((r + t).max(2))
+    worst = np.where((X < low) | (X > high), np.inf, -np.inf).max(initial=-np.inf)
+    s = np.exp2(X.astype(np.float64))[..., None]
+    room = t + np.maximum((r + t) * 2.0 ** -4, s * 2.0 ** -10)
+    return max(worst, (np.abs(val * s - np.clip(sign_ref, -448 * s, 448 * s)) - room).max(initial=-np.inf))
