@@ -60,50 +60,86 @@ struct AddNormArgs {
   uint64_t timeout_ns;
 };
 
-__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+// Eight bytes into a CTA's shared memory of the cluster, in one access.
+__device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
+  asm volatile("st.relaxed.cluster.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t n;
   asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(n));
   return n;
 }
 
-// The rows' sums over all columns: each warp's are in lane order (lane = row).
+// The rows' sums over all columns: each warp's are in lane order (lane = row). Each
+// CTA sends its own to all CTAs of the cluster, a row's sum and the panel's number
+// (counted from 1) in one 8-byte store, and a warp that needs a panel's sums reads
+// its CTA's words until they carry that number. So nothing waits for the stores of
+// outputs, as a release at cluster scope would (a barrier of the cluster per panel
+// held every warp until its stores had been performed, a fifth of the time). Words
+// of even and of odd panels are apart: a CTA sends a panel's sums when all its warps
+// have read those of the panel before, and overwrites words two panels later, when
+// it has received the sums of the panel in between from every CTA.
 struct RowSums {
-  float (*part)[32];              // [warps][32]
-  float (*all)[kMaxCluster][32];  // [2][CTA][32]
+  float (*part)[32];            // [warps][32]
+  volatile uint64_t (*all)[32]; // [2 * CTAs][32]
 };
 
-__device__ __forceinline__ void sums_send(const RowSums& s, float mine, int warp, int lane, int warps, uint32_t crank,
-                                          uint32_t csize, int parity) {
+// Both in dynamic shared memory, behind the stages.
+constexpr size_t sums_bytes(int csize, int warps) { return static_cast<size_t>(csize) * 2 * 32 * 8 + static_cast<size_t>(warps) * 32 * 4; }
+
+__device__ __forceinline__ RowSums sums_at(uint8_t* at, uint32_t csize) {
+  return RowSums{reinterpret_cast<float(*)[32]>(at + csize * 2 * 32 * 8), reinterpret_cast<volatile uint64_t(*)[32]>(at)};
+}
+
+// `dead`: a wait of this warp has run out. Once one of the CTA's has, the CTA sends
+// nothing more (its panels come out as NaN, and the others' waits run out too):
+// returns true then.
+__device__ __forceinline__ bool sums_send(const RowSums& s, float mine, bool dead, int warp, int lane, int warps, uint32_t crank,
+                                          uint32_t csize, int k) {
   s.part[warp][lane] = mine;
-  __syncthreads();
+  if (__syncthreads_or(dead)) return true;
   if (warp == 0) {
     float t = 0.0f;
     for (int w = 0; w < warps; ++w) t += s.part[w][lane];
-    const uint32_t at = smem_u32(&s.all[parity][crank][lane]);
-    for (uint32_t r = 0; r < csize; ++r) st_cluster_f32(mapa_shared(at, r), t);
+    const uint64_t word = (static_cast<uint64_t>(static_cast<uint32_t>(k) + 1u) << 32) | __float_as_uint(t);
+    const uint32_t at = smem_u32(const_cast<uint64_t*>(&s.all[(k & 1) * csize + crank][lane]));
+    for (uint32_t r = 0; r < csize; ++r) st_cluster_u64(mapa_shared(at, r), word);
   }
-  cluster_arrive();
+  return false;
 }
 
-// After sums_send; the barrier also orders the next use of `part` and of this parity.
-__device__ __forceinline__ float sums_receive(const RowSums& s, int lane, uint32_t csize, int parity) {
-  cluster_wait();
+// After sums_send of panel k; NaN, and dead, where the wait runs out.
+__device__ __forceinline__ float sums_receive(const RowSums& s, bool& dead, int lane, uint32_t csize, int k,
+                                              const AddNormArgs& p) {
+  if (dead) return __int_as_float(0x7FFFFFFF);
+  const uint32_t number = static_cast<uint32_t>(k) + 1u;
   float t = 0.0f;
-  for (uint32_t r = 0; r < csize; ++r) t += s.all[parity][r][lane];
-  return t;
+  bool there = true;
+  for (uint32_t r = 0; r < csize; ++r) {
+    volatile uint64_t* at = &s.all[(k & 1) * csize + r][lane];
+    uint64_t word = *at;
+    if (static_cast<uint32_t>(word >> 32) != number) {
+      const uint64_t t0 = global_timer_ns();
+      do {
+#pragma unroll 1
+        for (int i = 0; i < 64 && static_cast<uint32_t>(word >> 32) != number; ++i) word = *at;
+        there = static_cast<uint32_t>(word >> 32) == number;
+      } while (!there && global_timer_ns() - t0 <= p.timeout_ns);
+      if (!there) break;
+    }
+    t += __uint_as_float(static_cast<uint32_t>(word));
+  }
+  if (!there && p.dev_status) atomicExch(p.dev_status, static_cast<int>(MX_ERR_TIMEOUT));
+  dead = !__all_sync(0xFFFFFFFFu, there);
+  return dead ? __int_as_float(0x7FFFFFFF) : t;
 }
 
-__device__ __forceinline__ void lane_weights(const AddNormArgs& p, int64_t c, float2 (&w)[8]) {
+__device__ __forceinline__ void lane_weights(const AddNormArgs& p, int64_t c, float2 (&w)[4]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = make_float2(c < p.cols ? 1.0f : 0.0f, c < p.cols ? 1.0f : 0.0f);
+  for (int j = 0; j < 4; ++j) w[j] = make_float2(c < p.cols ? 1.0f : 0.0f, c < p.cols ? 1.0f : 0.0f);
   if (!p.weight || c >= p.cols) return;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
+  for (int j = 0; j < 4; ++j) {
     if (p.weight_f32) {
       const float* f = static_cast<const float*>(p.weight) + c + 2 * j;
       w[j] = make_float2(f[0], f[1]);
@@ -118,7 +154,7 @@ __device__ __forceinline__ void lane_weights(const AddNormArgs& p, int64_t c, fl
 template <bool kF32>
 __device__ __forceinline__ void load_box(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int64_t c0, int64_t row0) {
   tma_load_2d(dst, map, bar, static_cast<int32_t>(c0), static_cast<int32_t>(row0));
-  if constexpr (kF32) tma_load_2d(dst + 4096, map, bar, static_cast<int32_t>(c0 + 32), static_cast<int32_t>(row0));
+  if constexpr (kF32) tma_load_2d(dst + kF32Box, map, bar, static_cast<int32_t>(c0 + 32), static_cast<int32_t>(row0));
 }
 
 // Waits for a stage; false (and a status) once the limit has passed.
@@ -128,38 +164,37 @@ __device__ __forceinline__ bool stage_wait(uint64_t* bar, uint32_t parity, const
   return false;
 }
 
-__device__ __forceinline__ void fill_nan(float2 (&v)[8]) {
+__device__ __forceinline__ void fill_nan(float2 (&v)[4]) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = make_float2(__int_as_float(0x7FFFFFFF), __int_as_float(0x7FFFFFFF));
+  for (int j = 0; j < 4; ++j) v[j] = make_float2(__int_as_float(0x7FFFFFFF), __int_as_float(0x7FFFFFFF));
 }
 
 // kF32: the residual stream (residual and sum; backward: sum, dsum and dx) is FP32.
 template <bool kF32, bool kRow, bool kCol, int kThreads>
 __global__ void __launch_bounds__(kThreads, 512 / kThreads) add_norm_kernel(const __grid_constant__ AddNormArgs p) {
-  constexpr uint32_t kStage = 4096 + (kF32 ? 8192 : 4096);
+  constexpr uint32_t kStage = 4096 + unit_box_bytes(kF32);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t s_bar[kMaxWarps];
-  __shared__ float s_part[kMaxWarps][32];
-  __shared__ float s_all[2][kMaxCluster][32];
-  const RowSums sums{s_part, s_all};
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 7, g = lane >> 3;
   const uint32_t crank = cluster_ctarank(), csize = cluster_size();
   const int64_t cluster = blockIdx.x / csize, clusters = gridDim.x / csize;
   const int64_t panels = (p.rows + 31) >> 5;
   const int64_t c0 = (static_cast<int64_t>(crank) * p.warps + warp) * kUnitCols;
-  const int64_t c = c0 + 16 * q;
+  const int64_t c = c0 + 8 * q;
   const bool active = c0 < p.cols;
   uint8_t* stage = smem + warp * kStage;
   uint64_t* bar = &s_bar[warp];
-  const uint32_t bytes = p.has_second ? kStage : 4096;
+  const RowSums sums = sums_at(smem + p.warps * kStage, csize);
+  const uint32_t bytes = 4096 + (p.has_second ? (kF32 ? 8192 : 4096) : 0);
 
   if (lane == 0) {
     mbar_init(bar, 1);
     fence_mbar_init();
   }
   __syncwarp();
+  for (uint32_t i = warp; i < 2 * csize; i += p.warps) sums.all[i][lane] = 0;
   pdl_launch_dependents();
   cluster_sync();  // every CTA of the cluster runs before one writes to it
   pdl_wait();
@@ -170,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) add_norm_kernel(cons
     if (p.has_second) load_box<kF32>(stage + 4096, &p.b, bar, c0, panel * 32);
   };
   if (active && lane == 0 && cluster < panels) load(cluster);
-  float2 w[8];
+  float2 w[4];
   lane_weights(p, c, w);
   {
     const int64_t id = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x, n = static_cast<int64_t>(gridDim.x) * blockDim.x;
@@ -178,12 +213,12 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) add_norm_kernel(cons
     if (kCol) zero_scale_padding(p.q.col_scale, p.cols, p.rows >> 5, p.q.col_ka, id, n);
   }
 
-  bool ok = true;
+  bool ok = true, dead = false;
   int k = 0, failed = 0;
   for (int64_t panel = cluster; panel < panels; panel += clusters, ++k) {
     const int64_t row0 = panel * 32;
     const int rows = static_cast<int>(min64(32, p.rows - row0));
-    float2 v[4][8];
+    float2 v[8][4];
     if (active) {
       if (ok) {
         ok = __all_sync(0xFFFFFFFFu, stage_wait(bar, k & 1, p));
@@ -191,14 +226,14 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) add_norm_kernel(cons
       }
       if (ok) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) unit_row_bf16(stage, 4 * g + i, q, v[i]);
+        for (int i = 0; i < 8; ++i) unit_row_bf16(stage, 8 * g + i, q, v[i]);
         if (p.has_second) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float2 r[8];
-            unit_row<kF32>(stage + 4096, 4 * g + i, q, r);
+          for (int i = 0; i < 8; ++i) {
+            float2 r[4];
+            unit_row<kF32>(stage + 4096, 8 * g + i, q, r);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = __fadd2_rn(v[i][j], r[j]);
+            for (int j = 0; j < 4; ++j) v[i][j] = __fadd2_rn(v[i][j], r[j]);
           }
         }
         __syncwarp();
@@ -206,40 +241,40 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) add_norm_kernel(cons
         __syncwarp();
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) fill_nan(v[i]);
+        for (int i = 0; i < 8; ++i) fill_nan(v[i]);
       }
     }
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (active) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 8; ++i) {
         float2 t = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t = __ffma2_rn(v[i][j], v[i][j], t);
+        for (int j = 0; j < 4; ++j) t = __ffma2_rn(v[i][j], v[i][j], t);
         s[i] = t.x + t.y;
       }
     }
-    sums_send(sums, fold_rows(s, lane), warp, lane, p.warps, crank, csize, k & 1);
+    dead = sums_send(sums, fold_rows(s, lane), dead, warp, lane, p.warps, crank, csize, k);
     if (active && p.out && c < p.cols) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (4 * g + i < rows) store_row<kF32>(p.out, (row0 + 4 * g + i) * p.ld_out + c, v[i]);
+      for (int i = 0; i < 8; ++i)
+        if (8 * g + i < rows) store_row<kF32>(p.out, (row0 + 8 * g + i) * p.ld_out + c, v[i]);
     }
-    const float total = sums_receive(sums, lane, csize, k & 1);
+    const float total = sums_receive(sums, dead, lane, csize, k, p);
     const float rstd = 1.0f / sqrtf(total / static_cast<float>(p.cols) + p.eps);
     if (crank == 0 && warp == 0 && p.rstd && lane < rows) p.rstd[row0 + lane] = rstd;
     if (!active) continue;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float r = __shfl_sync(0xFFFFFFFFu, rstd, 4 * g + i);
+    for (int i = 0; i < 8; ++i) {
+      const float r = __shfl_sync(0xFFFFFFFFu, rstd, 8 * g + i);
       const float2 r2 = make_float2(r, r);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = __fmul2_rn(__fmul2_rn(v[i][j], r2), w[j]);
+      for (int j = 0; j < 4; ++j) v[i][j] = __fmul2_rn(__fmul2_rn(v[i][j], r2), w[j]);
     }
     if (p.y && c < p.cols) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (4 * g + i < rows) store_row<false>(p.y, (row0 + 4 * g + i) * p.ldy + c, v[i]);
+      for (int i = 0; i < 8; ++i)
+        if (8 * g + i < rows) store_row<false>(p.y, (row0 + 8 * g + i) * p.ldy + c, v[i]);
     }
     store_unit<kRow, kCol>(v, p.q, lane, row0, rows, c0, p.cols, row0);
   }
@@ -251,91 +286,90 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) add_norm_kernel(cons
 
 template <bool kF32, bool kRow, bool kCol, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1) add_norm_backward_kernel(const __grid_constant__ AddNormArgs p) {
-  constexpr uint32_t kStream = kF32 ? 8192 : 4096;
-  const uint32_t stage_bytes = 4096 + (p.has_second == 1 ? 2 : 1) * kStream;
+  constexpr uint32_t kStream = unit_box_bytes(kF32);
+  const uint32_t streams = p.has_second == 1 ? 2 : 1, stage_bytes = 4096 + streams * kStream;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ uint64_t s_bar[kMaxWarps];
-  __shared__ float s_part[kMaxWarps][32];
-  __shared__ float s_all[2][kMaxCluster][32];
-  const RowSums sums{s_part, s_all};
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 7, g = lane >> 3;
   const uint32_t crank = cluster_ctarank(), csize = cluster_size();
   const int64_t cluster = blockIdx.x / csize, clusters = gridDim.x / csize;
   const int64_t panels = (p.rows + 31) >> 5;
   const int64_t c0 = (static_cast<int64_t>(crank) * p.warps + warp) * kUnitCols;
-  const int64_t c = c0 + 16 * q;
+  const int64_t c = c0 + 8 * q;
   const bool active = c0 < p.cols;
   uint8_t* stage = smem + warp * stage_bytes;
   uint64_t* bar = &s_bar[warp];
+  const RowSums sums = sums_at(smem + p.warps * stage_bytes, csize);
 
   if (lane == 0) {
     mbar_init(bar, 1);
     fence_mbar_init();
   }
   __syncwarp();
+  for (uint32_t i = warp; i < 2 * csize; i += p.warps) sums.all[i][lane] = 0;
   pdl_launch_dependents();
   cluster_sync();  // every CTA of the cluster runs before one writes to it
   pdl_wait();
 
   auto load = [&](int64_t panel) {
-    mbar_arrive_expect_tx(bar, stage_bytes);
+    mbar_arrive_expect_tx(bar, 4096 + streams * (kF32 ? 8192 : 4096));
     load_box<false>(stage, &p.a, bar, c0, panel * 32);
     load_box<kF32>(stage + 4096, &p.b, bar, c0, panel * 32);
     if (p.has_second == 1) load_box<kF32>(stage + 4096 + kStream, &p.c, bar, c0, panel * 32);
   };
   if (active && lane == 0 && cluster < panels) load(cluster);
-  float2 w[8], dw[8];
+  float2 w[4], dw[4];
   lane_weights(p, c, w);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) dw[j] = make_float2(0.0f, 0.0f);
+  for (int j = 0; j < 4; ++j) dw[j] = make_float2(0.0f, 0.0f);
   {
     const int64_t id = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x, n = static_cast<int64_t>(gridDim.x) * blockDim.x;
     if (kRow) zero_scale_padding(p.q.row_scale, p.rows, p.cols >> 5, p.q.row_ka, id, n);
     if (kCol) zero_scale_padding(p.q.col_scale, p.cols, p.rows >> 5, p.q.col_ka, id, n);
   }
 
-  bool ok = true;
+  bool ok = true, dead = false;
   int k = 0, failed = 0;
   for (int64_t panel = cluster; panel < panels; panel += clusters, ++k) {
     const int64_t row0 = panel * 32;
     const int rows = static_cast<int>(min64(32, p.rows - row0));
     const float rstd = lane < rows ? p.rstd_in[row0 + lane] : 0.0f;
-    float2 v[4][8], h[4][8];  // dsum + rstd g; h
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float2 v[8][4], h[8][4];  // dsum + rstd g; h
+    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (active) {
       if (ok) {
         ok = __all_sync(0xFFFFFFFFu, stage_wait(bar, k & 1, p));
         failed = k;
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float r = __shfl_sync(0xFFFFFFFFu, rstd, 4 * g + i);
+      for (int i = 0; i < 8; ++i) {
+        const float r = __shfl_sync(0xFFFFFFFFu, rstd, 8 * g + i);
         const float2 r2 = make_float2(r, r);
-        float2 dy[8], t = make_float2(0.0f, 0.0f);
+        float2 dy[4], t = make_float2(0.0f, 0.0f);
         if (ok) {
-          unit_row_bf16(stage, 4 * g + i, q, dy);
-          unit_row<kF32>(stage + 4096, 4 * g + i, q, h[i]);
+          unit_row_bf16(stage, 8 * g + i, q, dy);
+          unit_row<kF32>(stage + 4096, 8 * g + i, q, h[i]);
           if (p.has_second == 1) {
-            unit_row<kF32>(stage + 4096 + kStream, 4 * g + i, q, v[i]);
-          } else if (p.has_second == 2 && 4 * g + i < rows && c < p.cols) {
-            load_row<kF32>(p.direct, (row0 + 4 * g + i) * p.ld_direct + c, v[i]);
+            unit_row<kF32>(stage + 4096 + kStream, 8 * g + i, q, v[i]);
+          } else if (p.has_second == 2 && 8 * g + i < rows && c < p.cols) {
+            load_row<kF32>(p.direct, (row0 + 8 * g + i) * p.ld_direct + c, v[i]);
           } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = make_float2(0.0f, 0.0f);
+            for (int j = 0; j < 4; ++j) v[i][j] = make_float2(0.0f, 0.0f);
           }
         } else {
           fill_nan(dy);
           fill_nan(h[i]);
           fill_nan(v[i]);
         }
-        if (4 * g + i >= rows) {  // zeros from the load; rstd 0
+        if (8 * g + i >= rows) {  // zeros from the load; rstd 0
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dy[j] = h[i][j] = v[i][j] = make_float2(0.0f, 0.0f);
+          for (int j = 0; j < 4; ++j) dy[j] = h[i][j] = v[i][j] = make_float2(0.0f, 0.0f);
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           h[i][j] = __fmul2_rn(h[i][j], r2);
           dw[j] = __ffma2_rn(dy[j], h[i][j], dw[j]);
           dy[j] = __fmul2_rn(dy[j], w[j]);
@@ -348,31 +382,30 @@ __global__ void __launch_bounds__(kThreads, 1) add_norm_backward_kernel(const __
       if (ok && lane == 0 && panel + clusters < panels) load(panel + clusters);
       __syncwarp();
     }
-    sums_send(sums, fold_rows(s, lane), warp, lane, p.warps, crank, csize, k & 1);
-    const float total = sums_receive(sums, lane, csize, k & 1);
+    dead = sums_send(sums, fold_rows(s, lane), dead, warp, lane, p.warps, crank, csize, k);
+    const float total = sums_receive(sums, dead, lane, csize, k, p);
     const float mean = -rstd * (total / static_cast<float>(p.cols));
     if (!active) continue;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float m = __shfl_sync(0xFFFFFFFFu, mean, 4 * g + i);
+    for (int i = 0; i < 8; ++i) {
+      const float m = __shfl_sync(0xFFFFFFFFu, mean, 8 * g + i);
       const float2 m2 = make_float2(m, m);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = __ffma2_rn(h[i][j], m2, v[i][j]);
-      if (p.out && c < p.cols && 4 * g + i < rows) store_row<kF32>(p.out, (row0 + 4 * g + i) * p.ld_out + c, v[i]);
+      for (int j = 0; j < 4; ++j) v[i][j] = __ffma2_rn(h[i][j], m2, v[i][j]);
+      if (p.out && c < p.cols && 8 * g + i < rows) store_row<kF32>(p.out, (row0 + 8 * g + i) * p.ld_out + c, v[i]);
     }
     if constexpr (kRow || kCol) store_unit<kRow, kCol>(v, p.q, lane, row0, rows, c0, p.cols, row0);
   }
   if (active && p.partial) {
-    // The lanes' column sums as the column amaxes: lane 4 g + q ends with columns
-    // 16 q + 2 g and + 1.
+    // The four lanes of a column add up: lane 8 g + q ends with columns 8 q + 2 g and + 1.
 #pragma unroll
-    for (int half = 4; half >= 1; half >>= 1) {
+    for (int half = 2; half >= 1; half >>= 1) {
       const bool up = (g & half) != 0;
 #pragma unroll
       for (int j = 0; j < half; ++j) {
         const float2 send = up ? dw[j] : dw[j + half], keep = up ? dw[j + half] : dw[j];
-        dw[j] = make_float2(keep.x + __shfl_xor_sync(0xFFFFFFFFu, send.x, 4 * half),
-                            keep.y + __shfl_xor_sync(0xFFFFFFFFu, send.y, 4 * half));
+        dw[j] = make_float2(keep.x + __shfl_xor_sync(0xFFFFFFFFu, send.x, 8 * half),
+                            keep.y + __shfl_xor_sync(0xFFFFFFFFu, send.y, 8 * half));
       }
     }
     if (c < p.cols) *reinterpret_cast<float2*>(p.partial + cluster * p.cols + c + 2 * g) = dw[0];
@@ -501,7 +534,7 @@ mx_status launch_add_norm(const AddNormLaunch& L, cudaStream_t s) {
     a.has_second = L.second != nullptr;
     if (L.second) st = make_unit_map(&a.b, f32, L.second, L.cols, L.rows, L.ld_second);
     if (st != MX_OK) return st;
-    const size_t smem = 1024 + static_cast<size_t>(sp.warps) * (4096 + (f32 ? 8192 : 4096));
+    const size_t smem = 1024 + static_cast<size_t>(sp.warps) * (4096 + unit_box_bytes(f32)) + sums_bytes(sp.csize, sp.warps);
     const Kernel kern = sp.warps > 8 ? (f32 ? kernel_of<512, false, true>(row, col) : kernel_of<512, false, false>(row, col))
                                      : (f32 ? kernel_of<256, false, true>(row, col) : kernel_of<256, false, false>(row, col));
     return launch(kern, a, sp, smem, s, &clusters);
@@ -511,14 +544,15 @@ mx_status launch_add_norm(const AddNormLaunch& L, cudaStream_t s) {
   if (st == MX_OK && L.third) st = make_unit_map(&a.c, f32, L.third, L.cols, L.rows, L.ld_third);
   if (st != MX_OK) return st;
   a.partial = L.dweight ? static_cast<float*>(L.ws) : nullptr;
-  // With an FP32 stream a whole stage is 20 KB a warp; where a CTA's warps do not
-  // find room for that (above 10240 columns), dsum does not come through it.
-  if (a.has_second && f32 && sp.warps > 10) {
+  // With an FP32 stream a whole stage is 22 KB a warp; where a CTA's warps do not
+  // find room for that (above 9216 columns), dsum does not come through it.
+  if (a.has_second && f32 && sp.warps > 9) {
     a.has_second = 2;
     a.direct = L.third;
     a.ld_direct = L.ld_third;
   }
-  const size_t smem = 1024 + static_cast<size_t>(sp.warps) * (4096 + (a.has_second == 1 ? 2 : 1) * (f32 ? 8192 : 4096));
+  const size_t smem = 1024 + static_cast<size_t>(sp.warps) * (4096 + (a.has_second == 1 ? 2 : 1) * unit_box_bytes(f32)) +
+                      sums_bytes(sp.csize, sp.warps);
   const Kernel kern = sp.warps > 8 ? (f32 ? kernel_of<512, true, true>(row, col) : kernel_of<512, true, false>(row, col))
                                    : (f32 ? kernel_of<256, true, true>(row, col) : kernel_of<256, true, false>(row, col));
   st = launch(kern, a, sp, smem, s, &clusters);

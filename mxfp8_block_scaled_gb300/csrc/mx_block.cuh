@@ -3,16 +3,17 @@
 // quantise what they compute. Blocks are formed from the FP32 values: amax, scale
 // and elements, with one rounding, to E4M3.
 //
-// Lane 4 g + q holds rows 4 g .. 4 g + 3 and columns 16 q .. 16 q + 15, so that
-// - a row's block is two neighbouring lanes' (one shuffle for the amax, of two rows
-//   a register), and a lane's codes of a row are one 16-byte store (a quarter of
-//   the warp's 64 bytes of that row);
-// - a column's block is eight lanes' (columns split among them step by step: 7
-//   shuffles for 64 columns, 4 more to hand the scales back), and its 32 codes
-//   leave as eight 4-byte pieces of one 32-byte sector.
-// An amax is kept as the high half of its FP32 pattern (the exponent decides the
-// scale), two to a register. About 240 instructions for a lane's 64 values with
-// both copies, a tenth of the issue slots that HBM leaves at 8 bytes a value.
+// Lane 8 g + q holds rows 8 g .. 8 g + 7 and columns 8 q .. 8 q + 7, so that
+// - eight lanes read a whole 128-byte row of a shared-memory box, without bank
+//   conflicts whatever the row;
+// - a row's block is four lanes' and a column's four too, 8 rows x 8 columns of a
+//   lane: in each direction the four lanes fold their amaxes (two to a register)
+//   until each has two blocks' whole ones (3 shuffles), and hand the two scales
+//   round (3 more);
+// - a lane's codes of a row are an 8-byte store, eight lanes 64 bytes of the row;
+//   its codes of a column are one too, four lanes a 32-byte sector.
+// An amax is kept as the high half of its FP32 pattern: the exponent decides the
+// scale.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -50,148 +51,159 @@ __device__ __forceinline__ uint32_t high_halves(float lo, float hi) {
   return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }
 
-// 2^-X of scale code number i of four packed ones (255 as 0: its codes are replaced).
-__device__ __forceinline__ float unit_inv(uint32_t minus, int i) {
-  return __uint_as_float(__byte_perm(minus, 0u, i == 0 ? 0x0444 : i == 1 ? 0x1444 : i == 2 ? 0x2444 : 0x3444) >> 1);
+// The E8M0 codes (two 16-bit fields) of two amaxes' high halves: floor(log2) - 8 +
+// 127, at least 0; 247 for Inf and NaN, which the caller replaces.
+__device__ __forceinline__ uint32_t unit_codes(uint32_t amax2) {
+  return __vmaxu2((amax2 >> 7) & 0x00FF00FFu, 0x00080008u) - 0x00080008u;
 }
 
-// 254 - code in each byte, 254 for the code 255.
-__device__ __forceinline__ uint32_t minus_codes(uint32_t codes) {
-  const uint32_t nan = __vcmpeq4(codes, 0xFFFFFFFFu);
-  return 0xFEFEFEFEu - (codes & ~nan);
+// Folds the amaxes of a lane's eight rows (or columns), two to a register, over the
+// four lanes that share their blocks (lane bits `a` and `b` of it): the lane ends
+// with pair 2 b + a whole.
+__device__ __forceinline__ uint32_t unit_fold(const uint32_t (&p)[4], bool a, bool b, int xa, int xb) {
+  uint32_t s0 = __vmaxu2(b ? p[2] : p[0], __shfl_xor_sync(0xFFFFFFFFu, b ? p[0] : p[2], xb));
+  uint32_t s1 = __vmaxu2(b ? p[3] : p[1], __shfl_xor_sync(0xFFFFFFFFu, b ? p[1] : p[3], xb));
+  return __vmaxu2(a ? s1 : s0, __shfl_xor_sync(0xFFFFFFFFu, a ? s0 : s1, xa));
 }
 
-__device__ __forceinline__ uint32_t nan_code(float v) { return 0x7Fu | ((__float_as_uint(v) >> 24) & 0x80u); }
+// The other way: each lane's pair to all four, in order.
+__device__ __forceinline__ void unit_gather(uint32_t mine, bool a, bool b, int xa, int xb, uint32_t (&out)[4]) {
+  const uint32_t t = __shfl_xor_sync(0xFFFFFFFFu, mine, xa);
+  const uint32_t e0 = a ? t : mine, e1 = a ? mine : t;
+  const uint32_t f0 = __shfl_xor_sync(0xFFFFFFFFu, e0, xb), f1 = __shfl_xor_sync(0xFFFFFFFFu, e1, xb);
+  out[0] = b ? f0 : e0;
+  out[1] = b ? f1 : e1;
+  out[2] = b ? e0 : f0;
+  out[3] = b ? e1 : f1;
+}
 
-// One unit to its copies. v[i][j]: row 4 g + i, columns 16 q + 2 j and + 1.
+// Two fields of 16 bits, each all ones where the amax there is Inf or NaN.
+__device__ __forceinline__ uint32_t unit_bad(uint32_t amax2) {
+  return ((amax2 & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((amax2 & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+}
+
+// One unit to its copies. v[i][j]: row 8 g + i, columns 8 q + 2 j and + 1.
 //   row0, c0  the unit's first row and column in the matrix; c_end the matrix's
 //             columns (a multiple of 32; values past it are not read)
 //   rows      how many of its rows exist: others have no row copy. The column
 //             copy takes all 32 (the caller has zeroed what does not exist).
 //   kpos      position of its first row along the column copy's contraction.
+// A block with Inf or NaN takes scale 0xFF and codes 0x7F with the sign that the
+// element's conversion has.
 template <bool kRow, bool kCol>
-__device__ __forceinline__ void store_unit(const float2 (&v)[4][8], const CopyOut& o, int lane, int64_t row0, int rows,
+__device__ __forceinline__ void store_unit(const float2 (&v)[8][4], const CopyOut& o, int lane, int64_t row0, int rows,
                                            int64_t c0, int64_t c_end, int64_t kpos) {
-  const int q = lane & 3, g = lane >> 2;
-  const int64_t c = c0 + 16 * q;
-  const bool in = c < c_end;  // blocks are whole: so are a lane's 16 columns
+  const int q = lane & 7, g = lane >> 3;
+  const int64_t c = c0 + 8 * q;
+  const bool in = c < c_end;  // blocks are whole: so are a lane's columns
   if constexpr (kRow) {
-    float m[4];
+    uint32_t p[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      m[i] = amax3(v[i][0].x, v[i][0].y, v[i][1].x);
-      m[i] = amax3(m[i], v[i][1].y, v[i][2].x);
+    for (int i = 0; i < 8; i += 2) {
+      float m[2];
 #pragma unroll
-      for (int j = 2; j < 7; ++j) m[i] = amax3(m[i], v[i][j].y, v[i][j + 1].x);
-      m[i] = amax3(m[i], v[i][7].y, 0.0f);
+      for (int k = 0; k < 2; ++k) {
+        const float2(&r)[4] = v[i + k];
+        m[k] = amax3(amax3(r[0].x, r[0].y, r[1].x), amax3(r[1].y, r[2].x, r[2].y), amax3(r[3].x, r[3].y, 0.0f));
+      }
+      p[i >> 1] = high_halves(m[0], m[1]);
     }
-    uint32_t p0 = high_halves(m[0], m[1]), p1 = high_halves(m[2], m[3]);
-    p0 = __vmaxu2(p0, __shfl_xor_sync(0xFFFFFFFFu, p0, 1));
-    p1 = __vmaxu2(p1, __shfl_xor_sync(0xFFFFFFFFu, p1, 1));
-    const uint32_t codes = scale_code(p0 & 0xFFFFu) | (scale_code(p0 >> 16) << 8) | (scale_code(p1 & 0xFFFFu) << 16) |
-                           (scale_code(p1 >> 16) << 24);
-    const uint32_t minus = minus_codes(codes);
-    const uint32_t nans = __vcmpeq4(codes, 0xFFFFFFFFu);
-    const bool any_nan = __any_sync(0xFFFFFFFFu, nans != 0u);
-    uint8_t* dst = o.row_data + (row0 + 4 * g) * o.row_pitch + c;
+    const bool a = (q & 1) != 0, b = (q & 2) != 0;
+    const uint32_t amax = unit_fold(p, a, b, 1, 2);  // rows 8 g + 2 (q % 4) and + 1, this block
+    uint32_t codes = unit_codes(amax);
+    uint32_t inv[4];  // 2^-X of the eight rows, as BF16
+    unit_gather((0x00FE00FEu - codes) << 7, a, b, 1, 2, inv);
+    uint32_t bad = unit_bad(amax), bads[4] = {0u, 0u, 0u, 0u};
+    const bool any_bad = __any_sync(0xFFFFFFFFu, bad != 0u);
+    if (any_bad) {
+      codes |= bad & 0x00FF00FFu;
+      unit_gather(bad, a, b, 1, 2, bads);
+    }
+    uint8_t* dst = o.row_data + (row0 + 8 * g) * o.row_pitch + c;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float inv = unit_inv(minus, i);
-      const float2 s = make_float2(inv, inv);
-      uint32_t w[4];
+    for (int i = 0; i < 8; ++i) {
+      const float f = (i & 1) ? hi_f(inv[i >> 1]) : lo_f(inv[i >> 1]);
+      const float2 s = make_float2(f, f);
+      uint32_t w[2];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 a = __fmul2_rn(v[i][2 * j], s), b = __fmul2_rn(v[i][2 * j + 1], s);
-        w[j] = cvt_pair(a.x, a.y) | (cvt_pair(b.x, b.y) << 16);
+      for (int j = 0; j < 2; ++j) {
+        const float2 x = __fmul2_rn(v[i][2 * j], s), y = __fmul2_rn(v[i][2 * j + 1], s);
+        w[j] = cvt_pair(x.x, x.y) | (cvt_pair(y.x, y.y) << 16);
       }
-      if (any_nan && ((nans >> (8 * i)) & 1u)) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = nan_code(v[i][2 * j].x) | (nan_code(v[i][2 * j].y) << 8) | (nan_code(v[i][2 * j + 1].x) << 16) |
-                 (nan_code(v[i][2 * j + 1].y) << 24);
+      if (any_bad) {
+        const uint32_t fill = ((i & 1) ? bads[i >> 1] >> 16 : bads[i >> 1] & 0xFFFFu) ? 0x7F7F7F7Fu : 0u;
+        w[0] |= fill;
+        w[1] |= fill;
       }
-      if (in && 4 * g + i < rows) *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (in && 8 * g + i < rows) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
       dst += o.row_pitch;
     }
-    // Lane l writes both blocks' scales of row l.
-    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, codes, 2);
-    const uint32_t lo = ((q & 2) ? other : codes) >> (8 * q), hi = ((q & 2) ? codes : other) >> (8 * q);
-    if (lane < rows) {
-      const int64_t kb = c0 >> 5, r = row0 + lane;
+    // The lanes of the first block write row 8 g + 2 (q % 4), both blocks' scales,
+    // those of the second the row behind it.
+    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, codes, 4);
+    const bool second = (q & 4) != 0;
+    const uint32_t lo = second ? other >> 16 : codes, hi = second ? codes >> 16 : other;
+    const int r = 8 * g + 2 * (q & 3) + (second ? 1 : 0);
+    if (r < rows) {
+      const int64_t kb = c0 >> 5;
       if (c0 + 32 < c_end && (kb & 1) == 0) {
-        *reinterpret_cast<uint16_t*>(o.row_scale + scale_offset(r, kb, o.row_ka)) =
+        *reinterpret_cast<uint16_t*>(o.row_scale + scale_offset(row0 + r, kb, o.row_ka)) =
             static_cast<uint16_t>((lo & 0xFFu) | ((hi & 0xFFu) << 8));
       } else {
-        o.row_scale[scale_offset(r, kb, o.row_ka)] = static_cast<uint8_t>(lo);
-        if (c0 + 32 < c_end) o.row_scale[scale_offset(r, kb + 1, o.row_ka)] = static_cast<uint8_t>(hi);
+        o.row_scale[scale_offset(row0 + r, kb, o.row_ka)] = static_cast<uint8_t>(lo);
+        if (c0 + 32 < c_end) o.row_scale[scale_offset(row0 + r, kb + 1, o.row_ka)] = static_cast<uint8_t>(hi);
       }
     }
   }
   if constexpr (kCol) {
-    uint32_t p[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float x = amax3(amax3(v[0][j].x, v[1][j].x, v[2][j].x), v[3][j].x, 0.0f);
-      const float y = amax3(amax3(v[0][j].y, v[1][j].y, v[2][j].y), v[3][j].y, 0.0f);
-      p[j] = high_halves(x, y);
-    }
-    // Lane 4 g + q ends with pair g: columns 16 q + 2 g and + 1.
-    const bool b2 = (g & 4) != 0, b1 = (g & 2) != 0, b0 = (g & 1) != 0;
+    uint32_t p[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t t = __shfl_xor_sync(0xFFFFFFFFu, b2 ? p[j] : p[j + 4], 16);
-      p[j] = __vmaxu2(b2 ? p[j + 4] : p[j], t);
+      const float x = amax3(amax3(v[0][j].x, v[1][j].x, v[2][j].x), amax3(v[3][j].x, v[4][j].x, v[5][j].x),
+                            amax3(v[6][j].x, v[7][j].x, 0.0f));
+      const float y = amax3(amax3(v[0][j].y, v[1][j].y, v[2][j].y), amax3(v[3][j].y, v[4][j].y, v[5][j].y),
+                            amax3(v[6][j].y, v[7][j].y, 0.0f));
+      p[j] = high_halves(x, y);
     }
+    const bool a = (g & 1) != 0, b = (g & 2) != 0;
+    const uint32_t amax = unit_fold(p, a, b, 8, 16);  // columns 8 q + 2 g and + 1
+    uint32_t codes = unit_codes(amax);
+    uint32_t inv[4];
+    unit_gather((0x00FE00FEu - codes) << 7, a, b, 8, 16, inv);
+    uint32_t bad = unit_bad(amax), bads[4] = {0u, 0u, 0u, 0u};
+    const bool any_bad = __any_sync(0xFFFFFFFFu, bad != 0u);
+    if (any_bad) {
+      codes |= bad & 0x00FF00FFu;
+      unit_gather(bad, a, b, 8, 16, bads);
+    }
+    uint8_t* dst = o.col_data + c * o.col_pitch + kpos + 8 * g;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t t = __shfl_xor_sync(0xFFFFFFFFu, b1 ? p[j] : p[j + 2], 8);
-      p[j] = __vmaxu2(b1 ? p[j + 2] : p[j], t);
-    }
-    {
-      const uint32_t t = __shfl_xor_sync(0xFFFFFFFFu, b0 ? p[0] : p[1], 4);
-      p[0] = __vmaxu2(b0 ? p[1] : p[0], t);
-    }
-    const uint32_t mine = scale_code(p[0] & 0xFFFFu) | (scale_code(p[0] >> 16) << 8);
-    // The sixteen codes of the lane's columns, four to a word, from the eight lanes.
-    uint32_t k0, k1, k2, k3;
-    {
-      const uint32_t t = __shfl_xor_sync(0xFFFFFFFFu, mine, 4);
-      const uint32_t four = b0 ? __byte_perm(t, mine, 0x5410) : __byte_perm(mine, t, 0x5410);
-      const uint32_t f2 = __shfl_xor_sync(0xFFFFFFFFu, four, 8);
-      const uint32_t e0 = b1 ? f2 : four, e1 = b1 ? four : f2;
-      const uint32_t s0 = __shfl_xor_sync(0xFFFFFFFFu, e0, 16), s1 = __shfl_xor_sync(0xFFFFFFFFu, e1, 16);
-      k0 = b2 ? s0 : e0;
-      k1 = b2 ? s1 : e1;
-      k2 = b2 ? e0 : s0;
-      k3 = b2 ? e1 : s1;
-    }
-    const bool any_nan = __any_sync(0xFFFFFFFFu, __vcmpeq4(k0, ~0u) | __vcmpeq4(k1, ~0u) | __vcmpeq4(k2, ~0u) |
-                                                     __vcmpeq4(k3, ~0u));
-    uint8_t* dst = o.col_data + c * o.col_pitch + kpos + 4 * g;
+    for (int j = 0; j < 4; ++j) {
+      const float2 s = make_float2(lo_f(inv[j]), hi_f(inv[j]));
+      uint32_t w0[2], w1[2];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint32_t k = j < 2 ? k0 : j < 4 ? k1 : j < 6 ? k2 : k3;
-      const uint32_t minus = minus_codes(k);
-      const float2 s = make_float2(unit_inv(minus, (2 * j) & 3), unit_inv(minus, (2 * j + 1) & 3));
-      const float2 a = __fmul2_rn(v[0][j], s), b = __fmul2_rn(v[1][j], s), d = __fmul2_rn(v[2][j], s),
-                   e = __fmul2_rn(v[3][j], s);
-      uint32_t w0 = cvt_pair(a.x, b.x) | (cvt_pair(d.x, e.x) << 16);
-      uint32_t w1 = cvt_pair(a.y, b.y) | (cvt_pair(d.y, e.y) << 16);
-      if (any_nan) {
-        if (((k >> (8 * ((2 * j) & 3))) & 0xFFu) == 0xFFu)
-          w0 = nan_code(v[0][j].x) | (nan_code(v[1][j].x) << 8) | (nan_code(v[2][j].x) << 16) | (nan_code(v[3][j].x) << 24);
-        if (((k >> (8 * ((2 * j + 1) & 3))) & 0xFFu) == 0xFFu)
-          w1 = nan_code(v[0][j].y) | (nan_code(v[1][j].y) << 8) | (nan_code(v[2][j].y) << 16) | (nan_code(v[3][j].y) << 24);
+      for (int k = 0; k < 2; ++k) {
+        const float2 x0 = __fmul2_rn(v[4 * k][j], s), x1 = __fmul2_rn(v[4 * k + 1][j], s),
+                     x2 = __fmul2_rn(v[4 * k + 2][j], s), x3 = __fmul2_rn(v[4 * k + 3][j], s);
+        w0[k] = cvt_pair(x0.x, x1.x) | (cvt_pair(x2.x, x3.x) << 16);
+        w1[k] = cvt_pair(x0.y, x1.y) | (cvt_pair(x2.y, x3.y) << 16);
+      }
+      if (any_bad) {
+        const uint32_t f0 = (bads[j] & 0xFFFFu) ? 0x7F7F7F7Fu : 0u, f1 = (bads[j] >> 16) ? 0x7F7F7F7Fu : 0u;
+        w0[0] |= f0;
+        w0[1] |= f0;
+        w1[0] |= f1;
+        w1[1] |= f1;
       }
       if (in) {
-        *reinterpret_cast<uint32_t*>(dst) = w0;
-        *reinterpret_cast<uint32_t*>(dst + o.col_pitch) = w1;
+        *reinterpret_cast<uint2*>(dst) = make_uint2(w0[0], w0[1]);
+        *reinterpret_cast<uint2*>(dst + o.col_pitch) = make_uint2(w1[0], w1[1]);
       }
       dst += 2 * o.col_pitch;
     }
     if (in) {
-      o.col_scale[scale_offset(c + 2 * g, kpos >> 5, o.col_ka)] = static_cast<uint8_t>(mine);
-      o.col_scale[scale_offset(c + 2 * g + 1, kpos >> 5, o.col_ka)] = static_cast<uint8_t>(mine >> 8);
+      o.col_scale[scale_offset(c + 2 * g, kpos >> 5, o.col_ka)] = static_cast<uint8_t>(codes);
+      o.col_scale[scale_offset(c + 2 * g + 1, kpos >> 5, o.col_ka)] = static_cast<uint8_t>(codes >> 16);
     }
   }
 }
@@ -210,88 +222,86 @@ __device__ __forceinline__ void zero_scale_padding(uint8_t* scale, int64_t rows,
     *reinterpret_cast<uint32_t*>(scale + scale_offset(rows + i / atoms, 4 * (i % atoms), ka)) = 0u;
 }
 
-// A lane's 16 columns of row r (of 32) of a unit in shared memory: a [32][64] BF16
+// A lane's 8 columns of row r (of 32) of a unit in shared memory: a [32][64] BF16
 // box or two [32][32] FP32 boxes, 128-byte rows, 16-byte chunk n of row r at
-// n ^ (r % 8).
-__device__ __forceinline__ void unit_row_bf16(const uint8_t* box, int r, int q, float2 (&out)[8]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint4 w = ld_shared_v4(box + r * 128 + (((2 * q + h) ^ (r & 7)) << 4));
-    out[4 * h + 0] = make_float2(lo_f(w.x), hi_f(w.x));
-    out[4 * h + 1] = make_float2(lo_f(w.y), hi_f(w.y));
-    out[4 * h + 2] = make_float2(lo_f(w.z), hi_f(w.z));
-    out[4 * h + 3] = make_float2(lo_f(w.w), hi_f(w.w));
-  }
+// n ^ (r % 8). The second FP32 box starts a row further on (kF32Box): its chunks
+// are swizzled by r + 1, so that the eight lanes of a row, four in each box, meet
+// different banks.
+constexpr int kF32Box = 4096 + 128;
+__host__ __device__ constexpr uint32_t unit_box_bytes(bool f32) { return f32 ? 9216 : 4096; }  // with the row between the boxes, to 1024
+
+__device__ __forceinline__ void unit_row_bf16(const uint8_t* box, int r, int q, float2 (&out)[4]) {
+  const uint4 w = ld_shared_v4(box + r * 128 + ((q ^ (r & 7)) << 4));
+  out[0] = make_float2(lo_f(w.x), hi_f(w.x));
+  out[1] = make_float2(lo_f(w.y), hi_f(w.y));
+  out[2] = make_float2(lo_f(w.z), hi_f(w.z));
+  out[3] = make_float2(lo_f(w.w), hi_f(w.w));
 }
 
-__device__ __forceinline__ void unit_row_f32(const uint8_t* boxes, int r, int q, float2 (&out)[8]) {
-  const uint8_t* box = boxes + (q >> 1) * 4096;
+__device__ __forceinline__ void unit_row_f32(const uint8_t* boxes, int r, int q, float2 (&out)[4]) {
+  const int second = q >> 2;
+  const uint8_t* box = boxes + second * kF32Box;
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    const uint4 w = ld_shared_v4(box + r * 128 + (((4 * (q & 1) + h) ^ (r & 7)) << 4));
+  for (int h = 0; h < 2; ++h) {
+    const uint4 w = ld_shared_v4(box + r * 128 + (((2 * (q & 3) + h) ^ ((r + second) & 7)) << 4));
     out[2 * h] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
     out[2 * h + 1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
   }
 }
 
 template <bool kF32>
-__device__ __forceinline__ void unit_row(const uint8_t* box, int r, int q, float2 (&out)[8]) {
+__device__ __forceinline__ void unit_row(const uint8_t* box, int r, int q, float2 (&out)[4]) {
   if constexpr (kF32) unit_row_f32(box, r, q, out);
   else unit_row_bf16(box, r, q, out);
 }
 
-// A lane's 16 columns of a row to memory, rounded to the element type.
+// A lane's 8 columns of a row to memory, rounded to the element type.
 template <bool kF32>
-__device__ __forceinline__ void store_row(void* base, int64_t at, const float2 (&v)[8]) {
+__device__ __forceinline__ void store_row(void* base, int64_t at, const float2 (&v)[4]) {
   if constexpr (kF32) {
     float4* d = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
 #pragma unroll
-    for (int h = 0; h < 4; ++h) d[h] = make_float4(v[2 * h].x, v[2 * h].y, v[2 * h + 1].x, v[2 * h + 1].y);
+    for (int h = 0; h < 2; ++h) d[h] = make_float4(v[2 * h].x, v[2 * h].y, v[2 * h + 1].x, v[2 * h + 1].y);
   } else {
-    uint4* d = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + at);
+    uint32_t w[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[4 * h + j].x, v[4 * h + j].y);
-        w[j] = *reinterpret_cast<const uint32_t*>(&b);
-      }
-      d[h] = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[j].x, v[j].y);
+      w[j] = *reinterpret_cast<const uint32_t*>(&b);
     }
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + at) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
-// A lane's 16 columns of a row from memory.
+// A lane's 8 columns of a row from memory.
 template <bool kF32>
-__device__ __forceinline__ void load_row(const void* base, int64_t at, float2 (&v)[8]) {
+__device__ __forceinline__ void load_row(const void* base, int64_t at, float2 (&v)[4]) {
   if constexpr (kF32) {
     const float4* d = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
 #pragma unroll
-    for (int h = 0; h < 4; ++h) {
+    for (int h = 0; h < 2; ++h) {
       const float4 t = d[h];
       v[2 * h] = make_float2(t.x, t.y);
       v[2 * h + 1] = make_float2(t.z, t.w);
     }
   } else {
-    const uint4* d = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint4 t = d[h];
-      v[4 * h] = make_float2(lo_f(t.x), hi_f(t.x));
-      v[4 * h + 1] = make_float2(lo_f(t.y), hi_f(t.y));
-      v[4 * h + 2] = make_float2(lo_f(t.z), hi_f(t.z));
-      v[4 * h + 3] = make_float2(lo_f(t.w), hi_f(t.w));
-    }
+    const uint4 t = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + at);
+    v[0] = make_float2(lo_f(t.x), hi_f(t.x));
+    v[1] = make_float2(lo_f(t.y), hi_f(t.y));
+    v[2] = make_float2(lo_f(t.z), hi_f(t.z));
+    v[3] = make_float2(lo_f(t.w), hi_f(t.w));
   }
 }
 
-// Sum over a unit's columns of four row sums a lane: lane l gets row l's.
-__device__ __forceinline__ float fold_rows(const float (&s)[4], int lane) {
-  const bool a = (lane & 1) != 0, b = (lane & 2) != 0;
-  const float x = (a ? s[1] : s[0]) + __shfl_xor_sync(0xFFFFFFFFu, a ? s[0] : s[1], 1);
-  const float y = (a ? s[3] : s[2]) + __shfl_xor_sync(0xFFFFFFFFu, a ? s[2] : s[3], 1);
-  return (b ? y : x) + __shfl_xor_sync(0xFFFFFFFFu, b ? x : y, 2);
+// Sum over a unit's columns of eight row sums a lane: lane l gets row l's.
+__device__ __forceinline__ float fold_rows(const float (&s)[8], int lane) {
+  const bool a = (lane & 1) != 0, b = (lane & 2) != 0, d = (lane & 4) != 0;
+  float t[4], u[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t[i] = (d ? s[i + 4] : s[i]) + __shfl_xor_sync(0xFFFFFFFFu, d ? s[i] : s[i + 4], 4);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) u[i] = (b ? t[i + 2] : t[i]) + __shfl_xor_sync(0xFFFFFFFFu, b ? t[i] : t[i + 2], 2);
+  return (a ? u[1] : u[0]) + __shfl_xor_sync(0xFFFFFFFFu, a ? u[0] : u[1], 1);
 }
 
 }  // namespace mx

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(32 * kWarps) gated_kernel(const __grid_constan
   __shared__ uint64_t s_bar[kWarps];
   __shared__ int32_t s_off[MX_MAX_GROUPS + 1], s_tile[MX_MAX_GROUPS + 1], s_flag;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 3, g = lane >> 2;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 7, g = lane >> 3;
   uint8_t* stage = smem + warp * kStage;
   uint64_t* bar = &s_bar[warp];
   if (lane == 0) {
@@ -179,19 +179,19 @@ __global__ void __launch_bounds__(32 * kWarps) gated_kernel(const __grid_constan
         __syncwarp();
       }
     }
-    float2 a[4][8];                   // h, or dgate
-    [[maybe_unused]] float2 b[4][8];  // dup
+    float2 a[8][4];                   // h, or dgate
+    [[maybe_unused]] float2 b[8][4];  // dup
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 4 * g + i;
-      float2 gate[8], up[8];
+    for (int i = 0; i < 8; ++i) {
+      const int r = 8 * g + i;
+      float2 gate[4], up[4];
       unit_row_bf16(stage, r, q, gate);
       unit_row_bf16(stage + 4096, r, q, up);
       if constexpr (kBackward) {
-        float2 dh[8];
+        float2 dh[4];
         unit_row_bf16(stage + 8192, r, q, dh);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           float2 value, slope;
           act_both<kAct>(gate[j], value, slope);
           a[i][j] = __fmul2_rn(__fmul2_rn(dh[j], up[j]), slope);
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(32 * kWarps) gated_kernel(const __grid_constan
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) a[i][j] = __fmul2_rn(act_value<kAct>(gate[j]), up[j]);
+        for (int j = 0; j < 4; ++j) a[i][j] = __fmul2_rn(act_value<kAct>(gate[j]), up[j]);
       }
     }
     __syncwarp();
@@ -211,11 +211,11 @@ __global__ void __launch_bounds__(32 * kWarps) gated_kernel(const __grid_constan
     __syncwarp();
     if (!ok || now.rows < kUnitRows) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bool there = 4 * g + i < now.rows;
+      for (int i = 0; i < 8; ++i) {
+        const bool there = 8 * g + i < now.rows;
         const float fill = !ok && there ? __int_as_float(0x7FFFFFFF) : 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < 4; ++j) {
           if (!there || !ok) a[i][j] = make_float2(fill, fill);
           if constexpr (kBackward)
             if (!there || !ok) b[i][j] = make_float2(fill, fill);
