@@ -26,6 +26,7 @@
 #include <algorithm>
 #include <cstdint>
 #include <mutex>
+#include <vector>
 
 #include "mx_block.cuh"
 #include "mx_internal.h"
@@ -37,6 +38,7 @@ namespace {
 constexpr int kMaxCluster = 16;   // CTAs (above 8: opt-in)
 constexpr int kMaxWarps = 16;     // of a CTA
 constexpr int kMaxParts = 608;    // clusters of a launch (partial rows of dweight)
+constexpr int kMaxSmem = 226 * 1024;
 
 struct AddNormArgs {
   CUtensorMap a, b, c;  // forward: x, residual, -; backward: dy, sum, dsum
@@ -52,6 +54,7 @@ struct AddNormArgs {
   int64_t rows, cols;
   float eps;
   int32_t weight_f32;
+  int32_t weight_vec;   // 1: the weights start on a 16-byte boundary
   int32_t has_second;   // forward: a residual; backward: dsum (2: read by the lanes themselves)
   const void* direct;   // that dsum
   int64_t ld_direct;
@@ -80,15 +83,28 @@ __device__ __forceinline__ uint32_t cluster_size() {
 // have read those of the panel before, and overwrites words two panels later, when
 // it has received the sums of the panel in between from every CTA.
 struct RowSums {
-  float (*part)[32];            // [warps][32]
-  volatile uint64_t (*all)[32]; // [2 * CTAs][32]
+  uint32_t all;   // shared memory, [2 * CTAs][32] words of 8 bytes
+  uint32_t part;  // [warps][32] floats, each warp's
 };
 
 // Both in dynamic shared memory, behind the stages.
-constexpr size_t sums_bytes(int csize, int warps) { return static_cast<size_t>(csize) * 2 * 32 * 8 + static_cast<size_t>(warps) * 32 * 4; }
+__host__ __device__ constexpr uint32_t sums_bytes(uint32_t csize, uint32_t warps) { return csize * 2 * 32 * 8 + warps * 32 * 4; }
 
 __device__ __forceinline__ RowSums sums_at(uint8_t* at, uint32_t csize) {
-  return RowSums{reinterpret_cast<float(*)[32]>(at + csize * 2 * 32 * 8), reinterpret_cast<volatile uint64_t(*)[32]>(at)};
+  const uint32_t a = smem_u32(at);
+  return RowSums{a, a + csize * 2 * 32 * 8};
+}
+
+__device__ __forceinline__ void st_shared_f32(uint32_t at, float v) { asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory"); }
+__device__ __forceinline__ float ld_shared_f32(uint32_t at) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint64_t ld_shared_u64(uint32_t at) {
+  uint64_t v;
+  asm volatile("ld.volatile.shared.u64 %0, [%1];" : "=l"(v) : "r"(at) : "memory");
+  return v;
 }
 
 // `dead`: a wait of this warp has run out. Once one of the CTA's has, the CTA sends
@@ -96,13 +112,19 @@ __device__ __forceinline__ RowSums sums_at(uint8_t* at, uint32_t csize) {
 // returns true then.
 __device__ __forceinline__ bool sums_send(const RowSums& s, float mine, bool dead, int warp, int lane, int warps, uint32_t crank,
                                           uint32_t csize, int k) {
-  s.part[warp][lane] = mine;
+  st_shared_f32(s.part + (warp * 32 + lane) * 4, mine);
   if (__syncthreads_or(dead)) return true;
   if (warp == 0) {
     float t = 0.0f;
-    for (int w = 0; w < warps; ++w) t += s.part[w][lane];
+    for (int w0 = 0; w0 < warps; w0 += 8) {
+      float v[8];
+#pragma unroll
+      for (int w = 0; w < 8; ++w) v[w] = w0 + w < warps ? ld_shared_f32(s.part + ((w0 + w) * 32 + lane) * 4) : 0.0f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) t += v[w];
+    }
     const uint64_t word = (static_cast<uint64_t>(static_cast<uint32_t>(k) + 1u) << 32) | __float_as_uint(t);
-    const uint32_t at = smem_u32(const_cast<uint64_t*>(&s.all[(k & 1) * csize + crank][lane]));
+    const uint32_t at = s.all + (((k & 1) * csize + crank) * 32 + lane) * 8;
     for (uint32_t r = 0; r < csize; ++r) st_cluster_u64(mapa_shared(at, r), word);
   }
   return false;
@@ -112,32 +134,45 @@ __device__ __forceinline__ bool sums_send(const RowSums& s, float mine, bool dea
 __device__ __forceinline__ float sums_receive(const RowSums& s, bool& dead, int lane, uint32_t csize, int k,
                                               const AddNormArgs& p) {
   if (dead) return __int_as_float(0x7FFFFFFF);
-  const uint32_t number = static_cast<uint32_t>(k) + 1u;
+  const uint32_t number = static_cast<uint32_t>(k) + 1u, at = s.all + ((k & 1) * csize * 32 + lane) * 8;
+  const auto is_there = [&](uint64_t word) { return static_cast<uint32_t>(word >> 32) == number; };
   float t = 0.0f;
   bool there = true;
-  for (uint32_t r = 0; r < csize; ++r) {
-    volatile uint64_t* at = &s.all[(k & 1) * csize + r][lane];
-    uint64_t word = *at;
-    if (static_cast<uint32_t>(word >> 32) != number) {
-      const uint64_t t0 = global_timer_ns();
-      do {
-#pragma unroll 1
-        for (int i = 0; i < 64 && static_cast<uint32_t>(word >> 32) != number; ++i) word = *at;
-        there = static_cast<uint32_t>(word >> 32) == number;
-      } while (!there && global_timer_ns() - t0 <= p.timeout_ns);
-      if (!there) break;
-    }
-    t += __uint_as_float(static_cast<uint32_t>(word));
+  for (uint32_t r0 = 0; r0 < csize && there; r0 += 4) {
+    uint64_t word[4];
+    uint64_t t0 = 0;
+    do {
+      there = true;
+#pragma unroll
+      for (uint32_t r = 0; r < 4; ++r) {
+        word[r] = r0 + r < csize ? ld_shared_u64(at + (r0 + r) * 256) : static_cast<uint64_t>(number) << 32;
+        there = there && is_there(word[r]);
+      }
+      if (!there) {
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > p.timeout_ns) break;
+      }
+    } while (!there);
+#pragma unroll
+    for (uint32_t r = 0; r < 4; ++r) t += __uint_as_float(static_cast<uint32_t>(word[r]));
   }
   if (!there && p.dev_status) atomicExch(p.dev_status, static_cast<int>(MX_ERR_TIMEOUT));
   dead = !__all_sync(0xFFFFFFFFu, there);
   return dead ? __int_as_float(0x7FFFFFFF) : t;
 }
 
+// A lane's 8 weights (1 without any, 0 past the last column).
 __device__ __forceinline__ void lane_weights(const AddNormArgs& p, int64_t c, float2 (&w)[4]) {
+  const float fill = c < p.cols ? 1.0f : 0.0f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) w[j] = make_float2(c < p.cols ? 1.0f : 0.0f, c < p.cols ? 1.0f : 0.0f);
+  for (int j = 0; j < 4; ++j) w[j] = make_float2(fill, fill);
   if (!p.weight || c >= p.cols) return;
+  if (p.weight_vec) {
+    if (p.weight_f32) load_row<true>(p.weight, c, w);
+    else load_row<false>(p.weight, c, w);
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     if (p.weight_f32) {
@@ -152,9 +187,9 @@ __device__ __forceinline__ void lane_weights(const AddNormArgs& p, int64_t c, fl
 
 // One warp's load of a panel: [32 rows x 64 columns] of a tensor.
 template <bool kF32>
-__device__ __forceinline__ void load_box(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int64_t c0, int64_t row0) {
-  tma_load_2d(dst, map, bar, static_cast<int32_t>(c0), static_cast<int32_t>(row0));
-  if constexpr (kF32) tma_load_2d(dst + kF32Box, map, bar, static_cast<int32_t>(c0 + 32), static_cast<int32_t>(row0));
+__device__ __forceinline__ void load_box(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int c0, int row0) {
+  tma_load_2d(dst, map, bar, c0, row0);
+  if constexpr (kF32) tma_load_2d(dst + kF32Box, map, bar, c0 + 32, row0);
 }
 
 // Waits for a stage; false (and a status) once the limit has passed.
@@ -170,8 +205,8 @@ __device__ __forceinline__ void fill_nan(float2 (&v)[4]) {
 }
 
 // kF32: the residual stream (residual and sum; backward: sum, dsum and dx) is FP32.
-template <bool kF32, bool kRow, bool kCol, int kThreads>
-__global__ void __launch_bounds__(kThreads, 512 / kThreads) add_norm_kernel(const __grid_constant__ AddNormArgs p) {
+template <bool kF32, bool kRow, bool kCol>
+__global__ void __launch_bounds__(32 * kMaxWarps) add_norm_kernel(const __grid_constant__ AddNormArgs p) {
   constexpr uint32_t kStage = 4096 + unit_box_bytes(kF32);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -179,10 +214,10 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) add_norm_kernel(cons
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 7, g = lane >> 3;
   const uint32_t crank = cluster_ctarank(), csize = cluster_size();
-  const int64_t cluster = blockIdx.x / csize, clusters = gridDim.x / csize;
-  const int64_t panels = (p.rows + 31) >> 5;
-  const int64_t c0 = (static_cast<int64_t>(crank) * p.warps + warp) * kUnitCols;
-  const int64_t c = c0 + 8 * q;
+  const int cluster = static_cast<int>(blockIdx.x / csize), clusters = static_cast<int>(gridDim.x / csize);
+  const int panels = static_cast<int>((p.rows + 31) >> 5);  // rows < 2^31
+  const int c0 = (static_cast<int>(crank) * p.warps + warp) * kUnitCols;
+  const int c = c0 + 8 * q;
   const bool active = c0 < p.cols;
   uint8_t* stage = smem + warp * kStage;
   uint64_t* bar = &s_bar[warp];
@@ -194,12 +229,13 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) add_norm_kernel(cons
     fence_mbar_init();
   }
   __syncwarp();
-  for (uint32_t i = warp; i < 2 * csize; i += p.warps) sums.all[i][lane] = 0;
+  for (uint32_t i = warp; i < 2 * csize; i += p.warps)
+    asm volatile("st.shared.u64 [%0], %1;" ::"r"(sums.all + (i * 32 + lane) * 8), "l"(uint64_t{0}) : "memory");
   pdl_launch_dependents();
   cluster_sync();  // every CTA of the cluster runs before one writes to it
   pdl_wait();
 
-  auto load = [&](int64_t panel) {
+  auto load = [&](int panel) {
     mbar_arrive_expect_tx(bar, bytes);
     load_box<false>(stage, &p.a, bar, c0, panel * 32);
     if (p.has_second) load_box<kF32>(stage + 4096, &p.b, bar, c0, panel * 32);
@@ -215,8 +251,8 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) add_norm_kernel(cons
 
   bool ok = true, dead = false;
   int k = 0, failed = 0;
-  for (int64_t panel = cluster; panel < panels; panel += clusters, ++k) {
-    const int64_t row0 = panel * 32;
+  for (int panel = cluster; panel < panels; panel += clusters, ++k) {
+    const int row0 = panel * 32;
     const int rows = static_cast<int>(min64(32, p.rows - row0));
     float2 v[8][4];
     if (active) {
@@ -258,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) add_norm_kernel(cons
     if (active && p.out && c < p.cols) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (8 * g + i < rows) store_row<kF32>(p.out, (row0 + 8 * g + i) * p.ld_out + c, v[i]);
+        if (8 * g + i < rows) store_row<kF32>(p.out, static_cast<int64_t>(row0 + 8 * g + i) * p.ld_out + c, v[i]);
     }
     const float total = sums_receive(sums, dead, lane, csize, k, p);
     const float rstd = 1.0f / sqrtf(total / static_cast<float>(p.cols) + p.eps);
@@ -274,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 512 / kThreads) add_norm_kernel(cons
     if (p.y && c < p.cols) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (8 * g + i < rows) store_row<false>(p.y, (row0 + 8 * g + i) * p.ldy + c, v[i]);
+        if (8 * g + i < rows) store_row<false>(p.y, static_cast<int64_t>(row0 + 8 * g + i) * p.ldy + c, v[i]);
     }
     store_unit<kRow, kCol>(v, p.q, lane, row0, rows, c0, p.cols, row0);
   }
@@ -294,10 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1) add_norm_backward_kernel(const __
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane & 7, g = lane >> 3;
   const uint32_t crank = cluster_ctarank(), csize = cluster_size();
-  const int64_t cluster = blockIdx.x / csize, clusters = gridDim.x / csize;
-  const int64_t panels = (p.rows + 31) >> 5;
-  const int64_t c0 = (static_cast<int64_t>(crank) * p.warps + warp) * kUnitCols;
-  const int64_t c = c0 + 8 * q;
+  const int cluster = static_cast<int>(blockIdx.x / csize), clusters = static_cast<int>(gridDim.x / csize);
+  const int panels = static_cast<int>((p.rows + 31) >> 5);  // rows < 2^31
+  const int c0 = (static_cast<int>(crank) * p.warps + warp) * kUnitCols;
+  const int c = c0 + 8 * q;
   const bool active = c0 < p.cols;
   uint8_t* stage = smem + warp * stage_bytes;
   uint64_t* bar = &s_bar[warp];
@@ -308,22 +344,28 @@ __global__ void __launch_bounds__(kThreads, 1) add_norm_backward_kernel(const __
     fence_mbar_init();
   }
   __syncwarp();
-  for (uint32_t i = warp; i < 2 * csize; i += p.warps) sums.all[i][lane] = 0;
+  for (uint32_t i = warp; i < 2 * csize; i += p.warps)
+    asm volatile("st.shared.u64 [%0], %1;" ::"r"(sums.all + (i * 32 + lane) * 8), "l"(uint64_t{0}) : "memory");
   pdl_launch_dependents();
   cluster_sync();  // every CTA of the cluster runs before one writes to it
   pdl_wait();
 
-  auto load = [&](int64_t panel) {
+  auto load = [&](int panel) {
     mbar_arrive_expect_tx(bar, 4096 + streams * (kF32 ? 8192 : 4096));
     load_box<false>(stage, &p.a, bar, c0, panel * 32);
-    load_box<kF32>(stage + 4096, &p.b, bar, c0, panel * 32);
     if (p.has_second == 1) load_box<kF32>(stage + 4096 + kStream, &p.c, bar, c0, panel * 32);
   };
-  if (active && lane == 0 && cluster < panels) load(cluster);
-  float2 w[4], dw[4];
-  lane_weights(p, c, w);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) dw[j] = make_float2(0.0f, 0.0f);
+  // The sum's box is read again once the rows' sums are there (in registers it would
+  // cost half the warps), so its next load, of the same phase, follows later.
+  auto load_sum = [&](int panel) { load_box<kF32>(stage + 4096, &p.b, bar, c0, panel * 32); };
+  if (active && lane == 0 && cluster < panels) {
+    load(cluster);
+    load_sum(cluster);
+  }
+  // The next panel's statistic, a panel ahead (lane = row).
+  auto load_rstd = [&](int panel) { return panel < panels && panel * 32 + lane < p.rows ? p.rstd_in[panel * 32 + lane] : 0.0f; };
+  float rstd_next = load_rstd(cluster);
+  float2 dweight = make_float2(0.0f, 0.0f);  // of columns 8 q + 2 g and + 1, over the panels
   {
     const int64_t id = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x, n = static_cast<int64_t>(gridDim.x) * blockDim.x;
     if (kRow) zero_scale_padding(p.q.row_scale, p.rows, p.cols >> 5, p.q.row_ka, id, n);
@@ -332,144 +374,227 @@ __global__ void __launch_bounds__(kThreads, 1) add_norm_backward_kernel(const __
 
   bool ok = true, dead = false;
   int k = 0, failed = 0;
-  for (int64_t panel = cluster; panel < panels; panel += clusters, ++k) {
-    const int64_t row0 = panel * 32;
+  for (int panel = cluster; panel < panels; panel += clusters, ++k) {
+    const int row0 = panel * 32;
     const int rows = static_cast<int>(min64(32, p.rows - row0));
-    const float rstd = lane < rows ? p.rstd_in[row0 + lane] : 0.0f;
-    float2 v[8][4], h[8][4];  // dsum + rstd g; h
+    float rstd = rstd_next;
+    float2 v[8][4];  // dsum + rstd g
     float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (active) {
       if (ok) {
         ok = __all_sync(0xFFFFFFFFu, stage_wait(bar, k & 1, p));
         failed = k;
       }
+      // Rows that are not there come as zeros; a stage that has not come makes rstd,
+      // and so everything, NaN.
+      if (!ok) rstd = __int_as_float(0x7FFFFFFF);
+      {
+        float2 w[4], dw[4];
+        lane_weights(p, c, w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float r = __shfl_sync(0xFFFFFFFFu, rstd, 8 * g + i);
-        const float2 r2 = make_float2(r, r);
-        float2 dy[4], t = make_float2(0.0f, 0.0f);
-        if (ok) {
-          unit_row_bf16(stage, 8 * g + i, q, dy);
-          unit_row<kF32>(stage + 4096, 8 * g + i, q, h[i]);
+        for (int j = 0; j < 4; ++j) dw[j] = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float r = __shfl_sync(0xFFFFFFFFu, rstd, 8 * g + i);
+          const float2 r2 = make_float2(r, r);
+          float2 h[4], t = make_float2(0.0f, 0.0f);
+          unit_row_bf16(stage, 8 * g + i, q, v[i]);
+          unit_row<kF32>(stage + 4096, 8 * g + i, q, h);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v[i][j] = __fmul2_rn(v[i][j], r2);
+            dw[j] = __ffma2_rn(v[i][j], h[j], dw[j]);
+            v[i][j] = __fmul2_rn(v[i][j], w[j]);
+            t = __ffma2_rn(v[i][j], h[j], t);
+          }
+          s[i] = t.x + t.y;
+        }
+        // The four lanes of a column add up.
+#pragma unroll
+        for (int half = 2; half >= 1; half >>= 1) {
+          const bool up = (g & half) != 0;
+#pragma unroll
+          for (int j = 0; j < half; ++j) {
+            const float2 send = up ? dw[j] : dw[j + half], keep = up ? dw[j + half] : dw[j];
+            dw[j] = make_float2(keep.x + __shfl_xor_sync(0xFFFFFFFFu, send.x, 8 * half),
+                                keep.y + __shfl_xor_sync(0xFFFFFFFFu, send.y, 8 * half));
+          }
+        }
+        dweight = __fadd2_rn(dweight, dw[0]);
+      }
+      if (p.has_second) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float2 d[4];
           if (p.has_second == 1) {
-            unit_row<kF32>(stage + 4096 + kStream, 8 * g + i, q, v[i]);
-          } else if (p.has_second == 2 && 8 * g + i < rows && c < p.cols) {
-            load_row<kF32>(p.direct, (row0 + 8 * g + i) * p.ld_direct + c, v[i]);
+            unit_row<kF32>(stage + 4096 + kStream, 8 * g + i, q, d);
+          } else if (8 * g + i < rows && c < p.cols) {
+            load_row<kF32>(p.direct, static_cast<int64_t>(row0 + 8 * g + i) * p.ld_direct + c, d);
           } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[i][j] = make_float2(0.0f, 0.0f);
+            for (int j = 0; j < 4; ++j) d[j] = make_float2(0.0f, 0.0f);
           }
-        } else {
-          fill_nan(dy);
-          fill_nan(h[i]);
-          fill_nan(v[i]);
-        }
-        if (8 * g + i >= rows) {  // zeros from the load; rstd 0
 #pragma unroll
-          for (int j = 0; j < 4; ++j) dy[j] = h[i][j] = v[i][j] = make_float2(0.0f, 0.0f);
+          for (int j = 0; j < 4; ++j) v[i][j] = __fadd2_rn(v[i][j], d[j]);
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          h[i][j] = __fmul2_rn(h[i][j], r2);
-          dw[j] = __ffma2_rn(dy[j], h[i][j], dw[j]);
-          dy[j] = __fmul2_rn(dy[j], w[j]);
-          t = __ffma2_rn(dy[j], h[i][j], t);
-          v[i][j] = __ffma2_rn(dy[j], r2, v[i][j]);
-        }
-        s[i] = t.x + t.y;
       }
       __syncwarp();
       if (ok && lane == 0 && panel + clusters < panels) load(panel + clusters);
       __syncwarp();
     }
+    rstd_next = load_rstd(panel + clusters);
     dead = sums_send(sums, fold_rows(s, lane), dead, warp, lane, p.warps, crank, csize, k);
     const float total = sums_receive(sums, dead, lane, csize, k, p);
     const float mean = -rstd * (total / static_cast<float>(p.cols));
     if (!active) continue;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float m = __shfl_sync(0xFFFFFFFFu, mean, 8 * g + i);
+      const float m = __shfl_sync(0xFFFFFFFFu, rstd * mean, 8 * g + i);
       const float2 m2 = make_float2(m, m);
+      float2 h[4];
+      unit_row<kF32>(stage + 4096, 8 * g + i, q, h);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[i][j] = __ffma2_rn(h[i][j], m2, v[i][j]);
-      if (p.out && c < p.cols && 8 * g + i < rows) store_row<kF32>(p.out, (row0 + 8 * g + i) * p.ld_out + c, v[i]);
+      for (int j = 0; j < 4; ++j) v[i][j] = __ffma2_rn(h[j], m2, v[i][j]);
+    }
+    __syncwarp();
+    if (ok && lane == 0 && panel + clusters < panels) load_sum(panel + clusters);
+    __syncwarp();
+    if (p.out && c < p.cols) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (8 * g + i < rows) store_row<kF32>(p.out, static_cast<int64_t>(row0 + 8 * g + i) * p.ld_out + c, v[i]);
     }
     if constexpr (kRow || kCol) store_unit<kRow, kCol>(v, p.q, lane, row0, rows, c0, p.cols, row0);
   }
-  if (active && p.partial) {
-    // The four lanes of a column add up: lane 8 g + q ends with columns 8 q + 2 g and + 1.
-#pragma unroll
-    for (int half = 2; half >= 1; half >>= 1) {
-      const bool up = (g & half) != 0;
-#pragma unroll
-      for (int j = 0; j < half; ++j) {
-        const float2 send = up ? dw[j] : dw[j + half], keep = up ? dw[j + half] : dw[j];
-        dw[j] = make_float2(keep.x + __shfl_xor_sync(0xFFFFFFFFu, send.x, 8 * half),
-                            keep.y + __shfl_xor_sync(0xFFFFFFFFu, send.y, 8 * half));
-      }
-    }
-    if (c < p.cols) *reinterpret_cast<float2*>(p.partial + cluster * p.cols + c + 2 * g) = dw[0];
-  }
+  if (active && p.partial && c < p.cols) *reinterpret_cast<float2*>(p.partial + static_cast<int64_t>(cluster) * p.cols + c + 2 * g) = dweight;
   if (active && !ok && lane == 0) mbar_wait(bar, static_cast<uint32_t>(failed & 1), p.timeout_ns);
   __syncwarp();
   cluster_sync();  // no CTA leaves while another may still write to it
 }
 
-// How a width is split: CTAs of a cluster and warps of a CTA.
-struct Split {
-  int csize, warps;
-};
-
-Split split_of(int64_t cols, int max_warps) {
-  const int64_t units = (cols + kUnitCols - 1) / kUnitCols;
-  Split s{1, 1};
-  while (s.csize < kMaxCluster && static_cast<int64_t>(s.csize) * max_warps < units) s.csize *= 2;
-  s.warps = static_cast<int>((units + s.csize - 1) / s.csize);
-  return s;
-}
-
 using Kernel = void (*)(const AddNormArgs);
 
-template <int kThreads, bool kBackward, bool kF32>
-Kernel kernel_of(bool row, bool col) {
-  if constexpr (kBackward) {
-    if (row && col) return add_norm_backward_kernel<kF32, true, true, kThreads>;
-    if (row) return add_norm_backward_kernel<kF32, true, false, kThreads>;
-    if (col) return add_norm_backward_kernel<kF32, false, true, kThreads>;
-    return add_norm_backward_kernel<kF32, false, false, kThreads>;
-  } else {
-    if (row && col) return add_norm_kernel<kF32, true, true, kThreads>;
-    if (row) return add_norm_kernel<kF32, true, false, kThreads>;
-    if (col) return add_norm_kernel<kF32, false, true, kThreads>;
-    return add_norm_kernel<kF32, false, false, kThreads>;
-  }
+template <bool kF32>
+Kernel forward_kernel(bool row, bool col) {
+  if (row && col) return add_norm_kernel<kF32, true, true>;
+  if (row) return add_norm_kernel<kF32, true, false>;
+  if (col) return add_norm_kernel<kF32, false, true>;
+  return add_norm_kernel<kF32, false, false>;
 }
 
-mx_status launch(Kernel kern, AddNormArgs& a, const Split& sp, size_t smem, cudaStream_t s, int* clusters_out) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e == cudaSuccess && sp.csize > 8) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(add_norm)");
-  // As many clusters as the GPU holds at once (each then walks its panels).
+template <bool kF32, int kThreads>
+Kernel backward_kernel(bool row, bool col) {
+  if (row && col) return add_norm_backward_kernel<kF32, true, true, kThreads>;
+  if (row) return add_norm_backward_kernel<kF32, true, false, kThreads>;
+  if (col) return add_norm_backward_kernel<kF32, false, true, kThreads>;
+  return add_norm_backward_kernel<kF32, false, false, kThreads>;
+}
+
+// The backward kernel wants 200 registers a thread and gets what its warps leave:
+// 255 up to 8 of them, 168 up to 12 (a few spilled), then 128 (many).
+template <bool kF32>
+Kernel backward_kernel(bool row, bool col, int warps) {
+  return warps <= 8    ? backward_kernel<kF32, 256>(row, col)
+         : warps <= 12 ? backward_kernel<kF32, 384>(row, col)
+                       : backward_kernel<kF32, 512>(row, col);
+}
+
+// How a width is split: CTAs of a cluster, warps of a CTA; how many such clusters
+// the GPU holds at once and CTAs an SM.
+struct Split {
+  int csize, warps, held, per_sm;
+  bool direct;  // backward: dsum not through shared memory
+  size_t smem;
+  Kernel kern;
+};
+
+// Asks the runtime once for each kernel and shape on a device. held = 0: it does not fit.
+cudaError_t occupancy(Split& s) {
+  struct Entry {
+    Kernel kern;
+    int dev, csize, warps, held, per_sm;
+    size_t smem;
+  };
+  static std::mutex mu;
+  static std::vector<Entry> seen;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  for (const Entry& x : seen) {
+    if (x.kern == s.kern && x.dev == dev && x.csize == s.csize && x.warps == s.warps && x.smem == s.smem) {
+      s.held = x.held;
+      s.per_sm = x.per_sm;
+      return cudaSuccess;
+    }
+  }
+  // A kernel's limit is the largest that one of its shapes can need.
+  e = cudaFuncSetAttribute(s.kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(s.kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(sp.csize));
-  cfg.blockDim = dim3(static_cast<unsigned>(32 * sp.warps));
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3(static_cast<unsigned>(s.csize));
+  cfg.blockDim = dim3(static_cast<unsigned>(32 * s.warps));
+  cfg.dynamicSmemBytes = s.smem;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim = {static_cast<unsigned>(sp.csize), 1, 1};
+  attr.val.clusterDim = {static_cast<unsigned>(s.csize), 1, 1};
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  int held = 0;
-  e = cudaOccupancyMaxActiveClusters(&held, kern, &cfg);
-  if (e != cudaSuccess || held < 1) return cuda_status(e == cudaSuccess ? cudaErrorInvalidConfiguration : e, "add_norm clusters");
-  const int64_t panels = (a.rows + 31) / 32;
-  const int clusters = static_cast<int>(std::min<int64_t>({panels, held, kMaxParts}));
-  a.warps = sp.warps;
-  a.timeout_ns = wait_timeout_ns();
-  *clusters_out = clusters;
-  return cuda_status(launch_kernel(kern, static_cast<unsigned>(clusters * sp.csize), static_cast<unsigned>(32 * sp.warps), smem,
-                                   s, static_cast<unsigned>(sp.csize), a),
-                     "add_norm launch");
+  s.held = s.per_sm = 0;
+  if (cudaOccupancyMaxActiveClusters(&s.held, s.kern, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    s.held = 0;
+  }
+  if (s.held > 0) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&s.per_sm, s.kern, 32 * s.warps, s.smem);
+  if (e == cudaSuccess) seen.push_back(Entry{s.kern, dev, s.csize, s.warps, s.held, s.per_sm, s.smem});
+  return e;
+}
+
+// The split with the least estimated time. A cluster takes one panel a round; a round
+// takes a fixed time (the exchange; less where a second CTA of the SM works meanwhile)
+// and one in proportion to the SM's warps. Measured on GB300, us: forward 1.2 (0.7) +
+// 0.37 a warp, backward 1.9 + 0.38. What that decides (BF16 stream, both copies):
+// forward 8192 x 5120 clusters of 5 CTAs x 16 warps 65.7 us, of 8 x 10 82, 16 x 5 72;
+// 8192 x 7168 8 x 14 100, 7 x 16 107, 16 x 7 104 (FP32 stream: 154, 170, 146); backward
+// 32768 x 1408 2 x 11 85.6, 3 x 8 97, 4 x 6 110; 16384 x 2048 4 x 8 70.8, 3 x 11 72.1, 2 x
+// 16 (spilled) 112, and 8 x 4, two CTAs an SM, 69 or 81 from run to run.
+mx_status choose(const AddNormLaunch& L, Split* out) {
+  const int64_t units = (L.cols + kUnitCols - 1) / kUnitCols, panels = (L.rows + 31) / 32;
+  const bool row = L.row_data != nullptr, col = L.col_data != nullptr, f32 = L.stream_f32;
+  double best = 0.0;
+  out->held = 0;
+  for (int csize : {1, 2, 3, 4, 5, 6, 7, 8, kMaxCluster}) {
+    Split s = {};
+    s.csize = csize;
+    s.warps = static_cast<int>((units + csize - 1) / csize);
+    if (s.warps > kMaxWarps || (s.warps < 4 && out->held > 0)) continue;
+    uint32_t stage = 4096 + unit_box_bytes(f32);
+    if (L.backward && L.third) {
+      // With an FP32 stream a whole stage is 22 KB a warp, more than 8 warps' room.
+      s.direct = f32 && s.warps > 8;
+      if (!s.direct) stage += unit_box_bytes(f32);
+    }
+    s.smem = 1024 + static_cast<size_t>(s.warps) * stage + sums_bytes(csize, s.warps);
+    s.kern = !L.backward ? (f32 ? forward_kernel<true>(row, col) : forward_kernel<false>(row, col))
+                         : (f32 ? backward_kernel<true>(row, col, s.warps) : backward_kernel<false>(row, col, s.warps));
+    const cudaError_t e = occupancy(s);
+    if (e != cudaSuccess) return cuda_status(e, "add_norm occupancy");
+    if (s.held < 1) continue;
+    const int64_t held = std::min<int64_t>(s.held, kMaxParts);
+    const double fixed = L.backward ? 1.9 : (s.per_sm > 1 ? 0.7 : 1.2);
+    // fewer panels than clusters: an SM has one CTA
+    const int per_sm = panels * csize <= sm_count() ? 1 : std::max(1, s.per_sm);
+    double t = static_cast<double>((panels + held - 1) / held) * (fixed + (L.backward ? 0.38 : 0.37) * s.warps * per_sm);
+    if (s.direct) t *= 2.0;  // 8192 x 7168: 394 us with dsum read by the lanes, 197 through shared memory
+    if (L.backward && s.warps > 12) t *= 1.5;
+    if (out->held == 0 || t < best) {
+      best = t;
+      *out = s;
+    }
+  }
+  if (out->held > 0) return MX_OK;
+  return cuda_status(cudaErrorInvalidConfiguration, "add_norm clusters");
 }
 
 }  // namespace
@@ -510,13 +635,19 @@ size_t add_norm_backward_workspace(int64_t rows, int64_t cols) {
 }
 
 mx_status launch_add_norm(const AddNormLaunch& L, cudaStream_t s) {
+  Split sp;
+  mx_status st = choose(L, &sp);
+  if (st != MX_OK) return st;
   AddNormArgs a = {};
   a.weight = L.weight;
   a.weight_f32 = L.param_dtype == MX_F32;
+  a.weight_vec = (reinterpret_cast<uintptr_t>(L.weight) & 15u) == 0;
   a.rows = L.rows;
   a.cols = L.cols;
   a.eps = L.eps;
+  a.warps = sp.warps;
   a.dev_status = L.dev_status;
+  a.timeout_ns = wait_timeout_ns();
   a.out = L.out;
   a.ld_out = L.ld_out;
   a.y = static_cast<__nv_bfloat16*>(L.y);
@@ -525,37 +656,22 @@ mx_status launch_add_norm(const AddNormLaunch& L, cudaStream_t s) {
   a.rstd_in = L.rstd;
   a.q = CopyOut{static_cast<uint8_t*>(L.row_data), static_cast<uint8_t*>(L.row_scale), static_cast<uint8_t*>(L.col_data),
                 static_cast<uint8_t*>(L.col_scale), L.cols, (L.cols + 127) / 128, L.rows, (L.rows + 127) / 128};
-  const bool f32 = L.stream_f32, row = L.row_data != nullptr, col = L.col_data != nullptr;
-  mx_status st = make_unit_map(&a.a, false, L.first, L.cols, L.rows, L.ld_first);
+  st = make_unit_map(&a.a, false, L.first, L.cols, L.rows, L.ld_first);
+  if (st == MX_OK && L.second) st = make_unit_map(&a.b, L.stream_f32, L.second, L.cols, L.rows, L.ld_second);
+  if (st == MX_OK && L.third && !sp.direct) st = make_unit_map(&a.c, L.stream_f32, L.third, L.cols, L.rows, L.ld_third);
   if (st != MX_OK) return st;
-  int clusters = 0;
-  const Split sp = split_of(L.cols, L.cols > 8192 ? 16 : 8);
-  if (!L.backward) {
-    a.has_second = L.second != nullptr;
-    if (L.second) st = make_unit_map(&a.b, f32, L.second, L.cols, L.rows, L.ld_second);
-    if (st != MX_OK) return st;
-    const size_t smem = 1024 + static_cast<size_t>(sp.warps) * (4096 + unit_box_bytes(f32)) + sums_bytes(sp.csize, sp.warps);
-    const Kernel kern = sp.warps > 8 ? (f32 ? kernel_of<512, false, true>(row, col) : kernel_of<512, false, false>(row, col))
-                                     : (f32 ? kernel_of<256, false, true>(row, col) : kernel_of<256, false, false>(row, col));
-    return launch(kern, a, sp, smem, s, &clusters);
-  }
-  a.has_second = L.third != nullptr;
-  st = make_unit_map(&a.b, f32, L.second, L.cols, L.rows, L.ld_second);
-  if (st == MX_OK && L.third) st = make_unit_map(&a.c, f32, L.third, L.cols, L.rows, L.ld_third);
-  if (st != MX_OK) return st;
-  a.partial = L.dweight ? static_cast<float*>(L.ws) : nullptr;
-  // With an FP32 stream a whole stage is 22 KB a warp; where a CTA's warps do not
-  // find room for that (above 9216 columns), dsum does not come through it.
-  if (a.has_second && f32 && sp.warps > 9) {
-    a.has_second = 2;
+  if (L.backward) {
+    a.has_second = L.third ? (sp.direct ? 2 : 1) : 0;
     a.direct = L.third;
     a.ld_direct = L.ld_third;
+    a.partial = L.dweight ? static_cast<float*>(L.ws) : nullptr;
+  } else {
+    a.has_second = L.second != nullptr;
   }
-  const size_t smem = 1024 + static_cast<size_t>(sp.warps) * (4096 + (a.has_second == 1 ? 2 : 1) * unit_box_bytes(f32)) +
-                      sums_bytes(sp.csize, sp.warps);
-  const Kernel kern = sp.warps > 8 ? (f32 ? kernel_of<512, true, true>(row, col) : kernel_of<512, true, false>(row, col))
-                                   : (f32 ? kernel_of<256, true, true>(row, col) : kernel_of<256, true, false>(row, col));
-  st = launch(kern, a, sp, smem, s, &clusters);
+  const int clusters = static_cast<int>(std::min<int64_t>({(L.rows + 31) / 32, sp.held, kMaxParts}));
+  st = cuda_status(launch_kernel(sp.kern, static_cast<unsigned>(clusters * sp.csize), static_cast<unsigned>(32 * sp.warps),
+                                 sp.smem, s, static_cast<unsigned>(sp.csize), a),
+                   L.backward ? "mx_add_norm_backward launch" : "mx_add_norm_quantize launch");
   if (st != MX_OK || !L.dweight) return st;
   return launch_column_reduce(a.partial, clusters, L.cols, 0, L.dweight, nullptr, s);
 }

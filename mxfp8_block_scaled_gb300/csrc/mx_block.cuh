@@ -51,6 +51,18 @@ __device__ __forceinline__ uint32_t high_halves(float lo, float hi) {
   return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
 }
 
+// Four values -> four E4M3 codes, the first in the lowest byte.
+__device__ __forceinline__ uint32_t unit_cvt(float a, float b, float c, float d) {
+  uint32_t w;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(w)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return w;
+}
+
 // The E8M0 codes (two 16-bit fields) of two amaxes' high halves: floor(log2) - 8 +
 // 127, at least 0; 247 for Inf and NaN, which the caller replaces.
 __device__ __forceinline__ uint32_t unit_codes(uint32_t amax2) {
@@ -77,9 +89,19 @@ __device__ __forceinline__ void unit_gather(uint32_t mine, bool a, bool b, int x
   out[3] = b ? e1 : f1;
 }
 
+// scale_offset for rows and blocks below 2^31.
+__device__ __forceinline__ int64_t unit_scale_offset(uint32_t r, uint32_t kb, int64_t ka) {
+  return ((static_cast<int64_t>(r >> 7) * ka + (kb >> 2)) << 9) + (((r & 31) << 4) + (((r >> 5) & 3) << 2) + (kb & 3));
+}
+
 // Two fields of 16 bits, each all ones where the amax there is Inf or NaN.
 __device__ __forceinline__ uint32_t unit_bad(uint32_t amax2) {
   return ((amax2 & 0x7F80u) == 0x7F80u ? 0xFFFFu : 0u) | ((amax2 & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+}
+
+// Whether some lane of the warp has one (code 247).
+__device__ __forceinline__ bool unit_any_bad(uint32_t codes) {
+  return __any_sync(0xFFFFFFFFu, ((codes + 0x00090009u) & 0x01000100u) != 0u);
 }
 
 // One unit to its copies. v[i][j]: row 8 g + i, columns 8 q + 2 j and + 1.
@@ -113,9 +135,10 @@ __device__ __forceinline__ void store_unit(const float2 (&v)[8][4], const CopyOu
     uint32_t codes = unit_codes(amax);
     uint32_t inv[4];  // 2^-X of the eight rows, as BF16
     unit_gather((0x00FE00FEu - codes) << 7, a, b, 1, 2, inv);
-    uint32_t bad = unit_bad(amax), bads[4] = {0u, 0u, 0u, 0u};
-    const bool any_bad = __any_sync(0xFFFFFFFFu, bad != 0u);
+    uint32_t bads[4] = {0u, 0u, 0u, 0u};
+    const bool any_bad = unit_any_bad(codes);
     if (any_bad) {
+      const uint32_t bad = unit_bad(amax);
       codes |= bad & 0x00FF00FFu;
       unit_gather(bad, a, b, 1, 2, bads);
     }
@@ -128,7 +151,7 @@ __device__ __forceinline__ void store_unit(const float2 (&v)[8][4], const CopyOu
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const float2 x = __fmul2_rn(v[i][2 * j], s), y = __fmul2_rn(v[i][2 * j + 1], s);
-        w[j] = cvt_pair(x.x, x.y) | (cvt_pair(y.x, y.y) << 16);
+        w[j] = unit_cvt(x.x, x.y, y.x, y.y);
       }
       if (any_bad) {
         const uint32_t fill = ((i & 1) ? bads[i >> 1] >> 16 : bads[i >> 1] & 0xFFFFu) ? 0x7F7F7F7Fu : 0u;
@@ -145,13 +168,14 @@ __device__ __forceinline__ void store_unit(const float2 (&v)[8][4], const CopyOu
     const uint32_t lo = second ? other >> 16 : codes, hi = second ? codes >> 16 : other;
     const int r = 8 * g + 2 * (q & 3) + (second ? 1 : 0);
     if (r < rows) {
-      const int64_t kb = c0 >> 5;
+      const uint32_t kb = static_cast<uint32_t>(c0) >> 5;
+      uint8_t* at = o.row_scale + unit_scale_offset(static_cast<uint32_t>(row0) + r, kb, o.row_ka);
       if (c0 + 32 < c_end && (kb & 1) == 0) {
-        *reinterpret_cast<uint16_t*>(o.row_scale + scale_offset(row0 + r, kb, o.row_ka)) =
-            static_cast<uint16_t>((lo & 0xFFu) | ((hi & 0xFFu) << 8));
+        *reinterpret_cast<uint16_t*>(at) = static_cast<uint16_t>((lo & 0xFFu) | ((hi & 0xFFu) << 8));
       } else {
-        o.row_scale[scale_offset(row0 + r, kb, o.row_ka)] = static_cast<uint8_t>(lo);
-        if (c0 + 32 < c_end) o.row_scale[scale_offset(row0 + r, kb + 1, o.row_ka)] = static_cast<uint8_t>(hi);
+        *at = static_cast<uint8_t>(lo);
+        if (c0 + 32 < c_end)
+          o.row_scale[unit_scale_offset(static_cast<uint32_t>(row0) + r, kb + 1, o.row_ka)] = static_cast<uint8_t>(hi);
       }
     }
   }
@@ -170,9 +194,10 @@ __device__ __forceinline__ void store_unit(const float2 (&v)[8][4], const CopyOu
     uint32_t codes = unit_codes(amax);
     uint32_t inv[4];
     unit_gather((0x00FE00FEu - codes) << 7, a, b, 8, 16, inv);
-    uint32_t bad = unit_bad(amax), bads[4] = {0u, 0u, 0u, 0u};
-    const bool any_bad = __any_sync(0xFFFFFFFFu, bad != 0u);
+    uint32_t bads[4] = {0u, 0u, 0u, 0u};
+    const bool any_bad = unit_any_bad(codes);
     if (any_bad) {
+      const uint32_t bad = unit_bad(amax);
       codes |= bad & 0x00FF00FFu;
       unit_gather(bad, a, b, 8, 16, bads);
     }
@@ -185,8 +210,8 @@ __device__ __forceinline__ void store_unit(const float2 (&v)[8][4], const CopyOu
       for (int k = 0; k < 2; ++k) {
         const float2 x0 = __fmul2_rn(v[4 * k][j], s), x1 = __fmul2_rn(v[4 * k + 1][j], s),
                      x2 = __fmul2_rn(v[4 * k + 2][j], s), x3 = __fmul2_rn(v[4 * k + 3][j], s);
-        w0[k] = cvt_pair(x0.x, x1.x) | (cvt_pair(x2.x, x3.x) << 16);
-        w1[k] = cvt_pair(x0.y, x1.y) | (cvt_pair(x2.y, x3.y) << 16);
+        w0[k] = unit_cvt(x0.x, x1.x, x2.x, x3.x);
+        w1[k] = unit_cvt(x0.y, x1.y, x2.y, x3.y);
       }
       if (any_bad) {
         const uint32_t f0 = (bads[j] & 0xFFFFu) ? 0x7F7F7F7Fu : 0u, f1 = (bads[j] >> 16) ? 0x7F7F7F7Fu : 0u;
@@ -202,8 +227,10 @@ __device__ __forceinline__ void store_unit(const float2 (&v)[8][4], const CopyOu
       dst += 2 * o.col_pitch;
     }
     if (in) {
-      o.col_scale[scale_offset(c + 2 * g, kpos >> 5, o.col_ka)] = static_cast<uint8_t>(codes);
-      o.col_scale[scale_offset(c + 2 * g + 1, kpos >> 5, o.col_ka)] = static_cast<uint8_t>(codes >> 16);
+      // An even column and the one behind it: 16 bytes further on.
+      uint8_t* at = o.col_scale + unit_scale_offset(static_cast<uint32_t>(c) + 2 * g, static_cast<uint32_t>(kpos) >> 5, o.col_ka);
+      at[0] = static_cast<uint8_t>(codes);
+      at[16] = static_cast<uint8_t>(codes >> 16);
     }
   }
 }
