@@ -73,6 +73,13 @@ __device__ __forceinline__ float2 act_slope(float2 z) {
   return make_float2(1.0f, 1.0f);
 }
 
+// v within kSlopeMax, in one instruction (|v| against it, v's sign).
+__device__ __forceinline__ float slope_held(float v) {
+  float r;
+  asm("min.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(kSlopeMax));
+  return r;
+}
+
 // act and d act / dz from one logistic function.
 template <int kAct>
 __device__ __forceinline__ void act_both(float2 z, float2& value, float2& slope) {
@@ -87,7 +94,7 @@ __device__ __forceinline__ void act_both(float2 z, float2& value, float2& slope)
       zu = z;
     }
     const float2 rest = __fmul2_rn(q, __ffma2_rn(q, act_pair(-1.0f), act_pair(1.0f)));
-    slope = __ffma2_rn(slope_bounded(zu), rest, q);
+    slope = __ffma2_rn(make_float2(slope_held(zu.x), slope_held(zu.y)), rest, q);
     value = __fmul2_rn(z, q);
   } else {
     slope = act_slope<kAct>(z);

@@ -28,6 +28,13 @@ namespace mx {
 constexpr int kUnitRows = 32;
 constexpr int kUnitCols = 64;
 
+__device__ __forceinline__ void st_shared_v2(void* p, uint32_t a, uint32_t b) {
+  asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(smem_u32(p)), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ void st_shared_u8(void* p, uint32_t v) {
+  asm volatile("st.shared.u8 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
+}
+
 // Where a matrix's MX copies go.
 struct CopyOut {
   uint8_t* row_data;
@@ -110,11 +117,14 @@ __device__ __forceinline__ bool unit_any_bad(uint32_t codes) {
 //   rows      how many of its rows exist: others have no row copy. The column
 //             copy takes all 32 (the caller has zeroed what does not exist).
 //   kpos      position of its first row along the column copy's contraction.
+//   staged    not null: the column copy's codes and scales of panel `panel` (of four)
+//             go to this tile in shared memory instead, for store_columns.
 // A block with Inf or NaN takes scale 0xFF and codes 0x7F with the sign that the
 // element's conversion has.
-template <bool kRow, bool kCol>
+template <bool kRow, bool kCol, bool kStaged = false>
 __device__ __forceinline__ void store_unit(const float2 (&v)[8][4], const CopyOut& o, int lane, int64_t row0, int rows,
-                                           int64_t c0, int64_t c_end, int64_t kpos) {
+                                           int64_t c0, int64_t c_end, int64_t kpos, uint8_t* staged = nullptr,
+                                           int panel = 0) {
   const int q = lane & 7, g = lane >> 3;
   const int64_t c = c0 + 8 * q;
   const bool in = c < c_end;  // blocks are whole: so are a lane's columns
@@ -201,7 +211,8 @@ __device__ __forceinline__ void store_unit(const float2 (&v)[8][4], const CopyOu
       codes |= bad & 0x00FF00FFu;
       unit_gather(bad, a, b, 8, 16, bads);
     }
-    uint8_t* dst = o.col_data + c * o.col_pitch + kpos + 8 * g;
+    uint8_t* dst = kStaged ? staged + q * 1024 + (((panel * 2 + (g >> 1)) ^ q) << 4) + (g & 1) * 8
+                           : o.col_data + c * o.col_pitch + kpos + 8 * g;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const float2 s = make_float2(lo_f(inv[j]), hi_f(inv[j]));
@@ -220,19 +231,56 @@ __device__ __forceinline__ void store_unit(const float2 (&v)[8][4], const CopyOu
         w1[0] |= f1;
         w1[1] |= f1;
       }
-      if (in) {
-        *reinterpret_cast<uint2*>(dst) = make_uint2(w0[0], w0[1]);
-        *reinterpret_cast<uint2*>(dst + o.col_pitch) = make_uint2(w1[0], w1[1]);
+      if constexpr (kStaged) {
+        st_shared_v2(dst + 256 * j, w0[0], w0[1]);
+        st_shared_v2(dst + 256 * j + 128, w1[0], w1[1]);
+      } else {
+        if (in) {
+          *reinterpret_cast<uint2*>(dst) = make_uint2(w0[0], w0[1]);
+          *reinterpret_cast<uint2*>(dst + o.col_pitch) = make_uint2(w1[0], w1[1]);
+        }
+        dst += 2 * o.col_pitch;
       }
-      dst += 2 * o.col_pitch;
     }
-    if (in) {
+    if constexpr (kStaged) {
+      uint8_t* at = staged + kUnitCols * 128 + (8 * q + 2 * g) * 4 + panel;
+      st_shared_u8(at, codes);
+      st_shared_u8(at + 4, codes >> 16);
+    } else if (in) {
       // An even column and the one behind it: 16 bytes further on.
       uint8_t* at = o.col_scale + unit_scale_offset(static_cast<uint32_t>(c) + 2 * g, static_cast<uint32_t>(kpos) >> 5, o.col_ka);
       at[0] = static_cast<uint8_t>(codes);
       at[16] = static_cast<uint8_t>(codes >> 16);
     }
   }
+}
+
+// A tile of four panels' column copies that store_unit staged: 64 columns of 128
+// codes (16-byte chunk n of column c at n ^ (c / 8)), then their four scales each.
+// Written whole: 128 bytes a column where 32 at a time, from warps that are not at
+// the same place, left the lines to L2's fortune (dense backward, 8192 x 10944: 147
+// to 190 us with the order of the tiles). Warp w of four writes columns 16 w .. 16 w +
+// 15; k_end: the copy's contraction length where the last tile may pass it.
+constexpr int kStagedBytes = kUnitCols * 128 + kUnitCols * 4;
+
+__device__ __forceinline__ void store_columns(const uint8_t* staged, const CopyOut& o, int warp, int lane, int64_t c0,
+                                              int64_t c_end, int64_t kpos, int64_t k_end) {
+  const int chunk = lane & 7;
+  const int col0 = 16 * warp + (lane >> 3);
+  uint8_t* dst = o.col_data + (c0 + col0) * o.col_pitch + kpos + chunk * 16;
+  const bool in = kpos + chunk * 16 < k_end;
+#pragma unroll
+  for (int it = 0; it < 4; ++it) {
+    const int col = col0 + 4 * it;
+    const uint4 w = ld_shared_v4(staged + col * 128 + ((chunk ^ (col >> 3)) << 4));
+    if (in && c0 + col < c_end) *reinterpret_cast<uint4*>(dst) = w;
+    dst += 4 * o.col_pitch;
+  }
+  const int c = 16 * warp + lane;
+  if (lane < 16 && c0 + c < c_end)
+    *reinterpret_cast<uint32_t*>(o.col_scale + unit_scale_offset(static_cast<uint32_t>(c0) + c, static_cast<uint32_t>(kpos) >> 5,
+                                                                 o.col_ka)) =
+        *reinterpret_cast<const uint32_t*>(staged + kUnitCols * 128 + c * 4);
 }
 
 // Zeros in the scale buffer of a copy (rows x kb blocks, ka atoms wide) that belong
