@@ -2771,6 +2771,10 @@ mx_status launch_pair_multi(const GemmLaunch* Ls_in, int n, cudaStream_t s) {
 
 }  // namespace
 
+mx_status make_operand_map(CUtensorMap* map, const void* base, int64_t rows, int64_t k, int64_t ld, int box_rows) {
+  return make_map(map, base, rows, k, ld, box_rows);
+}
+
 mx_status launch_gemm(const GemmLaunch& L, cudaStream_t s) {
   if (L.M == 0 || L.N == 0) return MX_OK;
   if (L.kind != GEMM_DENSE && L.n_groups > kMaxGroups) {
@@ -2791,6 +2795,7 @@ mx_status launch_gemm(const GemmLaunch& L, cudaStream_t s) {
   int bn;
   const int epi = epi_kind(L);
   if (gated_epi(epi)) {
+    if (gated_few_applies(L)) return launch_gated_few(L, s);
     const int64_t tiles = (L.M + kBM - 1) / kBM * ((L.N + 255) / 256);
     if (dense_cfg_time_us(L, CFG_PAIR) <= dense_cfg_time_us(L, CFG_BN256))
       return epi == 3 ? launch_pair<GEMM_DENSE, 0, 256, false, 3>(L, p, s) : launch_pair<GEMM_DENSE, 0, 256, false, 4>(L, p, s);

@@ -161,6 +161,11 @@ struct GemmLaunch {
   int64_t up_ld = 0;
 };
 mx_status launch_gemm(const GemmLaunch& g, cudaStream_t s);
+// The gated product of few tiles (up_data set): whether it takes this launch, and it.
+bool gated_few_applies(const GemmLaunch& g);
+mx_status launch_gated_few(const GemmLaunch& g, cudaStream_t s);
+// An operand's map: box 128 K x box_rows, 128-byte swizzle, zeros outside.
+mx_status make_operand_map(CUtensorMap* map, const void* base, int64_t rows, int64_t k, int64_t ld, int box_rows);
 // Bytes of workspace the dense GEMM L would use for its split tail (0: none).
 size_t gemm_workspace_bytes(const GemmLaunch& L);
 // Device address and size of the library's static scratch array on the

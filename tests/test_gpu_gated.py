@@ -77,6 +77,61 @@ def test_product(M, F, K, act):
     assert none is None and torch.equal(alone, out)
 
 
+# few tokens: every width of the token tile, contractions cut into one to eight, tails of each
+@pytest.mark.parametrize("M,F,K,act", [
+    (1, 128, 32, "silu"), (16, 1408, 2048, "silu"), (17, 1376, 992, "gelu"), (32, 264, 2048, "relu"), (31, 10944, 128, "silu"),
+    (2, 18432, 416, "silu"), (3, 60000, 64, "none"), (9, 333, 7168, "silu"), (33, 520, 2048, "silu"), (64, 1408, 1952, "gelu"),
+    (63, 37, 2080, "silu"), (65, 1001, 2048, "silu"), (128, 640, 7168, "relu"), (333, 1408, 2048, "silu"), (385, 130, 4096, "gelu")])
+def test_product_of_few_tokens(M, F, K, act):
+    test_product(M, F, K, act)
+
+
+@pytest.mark.parametrize("M", [3, 20, 50, 140])
+def test_product_of_few_tokens_pitches(M):
+    F, K = 204, 2048
+    a, gate, up = quantised(M, K, 7, 1.0), quantised(F, K, 8, 0.1), quantised(F, K, 9, 0.1)
+    want, wpre = mx.gemm_gated(a, gate, up, keep_preact=True)
+    check_product(want, wpre, a, gate, up, "silu")
+    for ldc, ldp, shift in ((208, 416, 0), (203 + 4, 411, 0), (208, 412, 1), (208, 412, 2)):
+        c = torch.full((M * ldc + 64,), 7.0, dtype=BF16, device="cuda")
+        z = torch.full((M * ldp + 64,), 7.0, dtype=BF16, device="cuda")
+        mx.mx_gemm_gated(a.c_operand(), gate.c_operand(), up.c_operand(), mx.MX_ACT_SILU, c.data_ptr() + 2 * shift, ldc,
+                         z.data_ptr() + 2 * shift, ldp, None, torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        for t, ld, n, ref in ((c, ldc, F, want), (z, ldp, 2 * F, wpre)):
+            m = t[shift:shift + M * ld].view(M, ld)
+            assert torch.equal(m[:, :n], ref)
+            assert (m[:, n:] == 7).all() and (t[:shift] == 7).all() and (t[shift + M * ld:] == 7).all()
+
+
+def test_product_of_few_tokens_repeats_and_replays():
+    """The same bits from every call and from a graph's replays, two of them on two streams at once."""
+    F, K = 1408, 2048
+    gate, up = quantised(F, K, 8, 0.1), quantised(F, K, 9, 0.1)
+    graphs, outs, wants = [], [], []
+    tokens = [quantised(M, K, M, 1.0) for M in (1, 48)]  # kept for the graphs' replays
+    st = mx.new_status()
+    for a in tokens:
+        wants.append(mx.gemm_gated(a, gate, up)[0])
+        assert torch.equal(mx.gemm_gated(a, gate, up)[0], wants[-1])
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(4):
+                out, _ = mx.gemm_gated(a, gate, up, status=st)
+        graphs.append(g)
+        outs.append(out)
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert mx.read_status(st) == 0
+    for got, want in zip(outs, wants):
+        assert torch.equal(got, want)
+
+
 def test_product_of_stacked_weights():
     """The two matrices of one batched quantisation of a weight kept as [2F, K]; F = 1376 is no whole atom."""
     F, K, M = 1376, 320, 512
