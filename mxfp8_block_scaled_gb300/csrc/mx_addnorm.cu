@@ -320,8 +320,13 @@ __global__ void __launch_bounds__(32 * kMaxWarps) add_norm_kernel(const __grid_c
   cluster_sync();  // no CTA leaves while another may still write to it
 }
 
+// Up to 12 warps (kThreads 256, 384) dsum + rstd g stays in registers over the
+// exchange, so that dy's and dsum's next loads are on their way during it. For more
+// warps on an SM there are no registers for that (kThreads 512: 16 warps of 128): the
+// values are then read once more from the stage, which is free for the next load later.
 template <bool kF32, bool kRow, bool kCol, int kThreads>
 __global__ void __launch_bounds__(kThreads, 1) add_norm_backward_kernel(const __grid_constant__ AddNormArgs p) {
+  constexpr bool kHeld = kThreads < 512;
   constexpr uint32_t kStream = unit_box_bytes(kF32);
   const uint32_t streams = p.has_second == 1 ? 2 : 1, stage_bytes = 4096 + streams * kStream;
   extern __shared__ uint8_t smem_raw[];
@@ -356,7 +361,8 @@ __global__ void __launch_bounds__(kThreads, 1) add_norm_backward_kernel(const __
     if (p.has_second == 1) load_box<kF32>(stage + 4096 + kStream, &p.c, bar, c0, panel * 32);
   };
   // The sum's box is read again once the rows' sums are there (in registers it would
-  // cost half the warps), so its next load, of the same phase, follows later.
+  // cost half the warps), so its next load, of the same phase, follows later; without
+  // kHeld all of a stage's do.
   auto load_sum = [&](int panel) { load_box<kF32>(stage + 4096, &p.b, bar, c0, panel * 32); };
   if (active && lane == 0 && cluster < panels) {
     load(cluster);
@@ -378,7 +384,20 @@ __global__ void __launch_bounds__(kThreads, 1) add_norm_backward_kernel(const __
     const int row0 = panel * 32;
     const int rows = static_cast<int>(min64(32, p.rows - row0));
     float rstd = rstd_next;
-    float2 v[8][4];  // dsum + rstd g
+    float2 v[8][4];  // dsum + rstd g, then dx
+    const auto add_dsum = [&](int i, float2 (&to)[4]) {
+      float2 d[4];
+      if (p.has_second == 1) {
+        unit_row<kF32>(stage + 4096 + kStream, 8 * g + i, q, d);
+      } else if (8 * g + i < rows && c < p.cols) {
+        load_row<kF32>(p.direct, static_cast<int64_t>(row0 + 8 * g + i) * p.ld_direct + c, d);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) d[j] = make_float2(0.0f, 0.0f);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) to[j] = __fadd2_rn(to[j], d[j]);
+    };
     float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (active) {
       if (ok) {
@@ -397,15 +416,16 @@ __global__ void __launch_bounds__(kThreads, 1) add_norm_backward_kernel(const __
         for (int i = 0; i < 8; ++i) {
           const float r = __shfl_sync(0xFFFFFFFFu, rstd, 8 * g + i);
           const float2 r2 = make_float2(r, r);
-          float2 h[4], t = make_float2(0.0f, 0.0f);
-          unit_row_bf16(stage, 8 * g + i, q, v[i]);
+          float2 g2[4], h[4], t = make_float2(0.0f, 0.0f);
+          unit_row_bf16(stage, 8 * g + i, q, g2);
           unit_row<kF32>(stage + 4096, 8 * g + i, q, h);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            v[i][j] = __fmul2_rn(v[i][j], r2);
-            dw[j] = __ffma2_rn(v[i][j], h[j], dw[j]);
-            v[i][j] = __fmul2_rn(v[i][j], w[j]);
-            t = __ffma2_rn(v[i][j], h[j], t);
+            g2[j] = __fmul2_rn(g2[j], r2);
+            dw[j] = __ffma2_rn(g2[j], h[j], dw[j]);
+            g2[j] = __fmul2_rn(g2[j], w[j]);
+            t = __ffma2_rn(g2[j], h[j], t);
+            if constexpr (kHeld) v[i][j] = g2[j];
           }
           s[i] = t.x + t.y;
         }
@@ -422,42 +442,45 @@ __global__ void __launch_bounds__(kThreads, 1) add_norm_backward_kernel(const __
         }
         dweight = __fadd2_rn(dweight, dw[0]);
       }
-      if (p.has_second) {
+      if constexpr (kHeld) {
+        if (p.has_second) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float2 d[4];
-          if (p.has_second == 1) {
-            unit_row<kF32>(stage + 4096 + kStream, 8 * g + i, q, d);
-          } else if (8 * g + i < rows && c < p.cols) {
-            load_row<kF32>(p.direct, static_cast<int64_t>(row0 + 8 * g + i) * p.ld_direct + c, d);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) d[j] = make_float2(0.0f, 0.0f);
-          }
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[i][j] = __fadd2_rn(v[i][j], d[j]);
+          for (int i = 0; i < 8; ++i) add_dsum(i, v[i]);
         }
+        __syncwarp();
+        if (ok && lane == 0 && panel + clusters < panels) load(panel + clusters);
+        __syncwarp();
       }
-      __syncwarp();
-      if (ok && lane == 0 && panel + clusters < panels) load(panel + clusters);
-      __syncwarp();
     }
     rstd_next = load_rstd(panel + clusters);
     dead = sums_send(sums, fold_rows(s, lane), dead, warp, lane, p.warps, crank, csize, k);
     const float total = sums_receive(sums, dead, lane, csize, k, p);
     const float mean = -rstd * (total / static_cast<float>(p.cols));
     if (!active) continue;
+    [[maybe_unused]] float2 w[4];
+    if constexpr (!kHeld) lane_weights(p, c, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float m = __shfl_sync(0xFFFFFFFFu, rstd * mean, 8 * g + i);
       const float2 m2 = make_float2(m, m);
+      if constexpr (!kHeld) {
+        const float r = __shfl_sync(0xFFFFFFFFu, rstd, 8 * g + i);
+        const float2 r2 = make_float2(r, r);
+        unit_row_bf16(stage, 8 * g + i, q, v[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[i][j] = __fmul2_rn(__fmul2_rn(v[i][j], r2), w[j]);
+        if (p.has_second) add_dsum(i, v[i]);
+      }
       float2 h[4];
       unit_row<kF32>(stage + 4096, 8 * g + i, q, h);
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[i][j] = __ffma2_rn(h[j], m2, v[i][j]);
     }
     __syncwarp();
-    if (ok && lane == 0 && panel + clusters < panels) load_sum(panel + clusters);
+    if (ok && lane == 0 && panel + clusters < panels) {
+      if constexpr (!kHeld) load(panel + clusters);
+      load_sum(panel + clusters);
+    }
     __syncwarp();
     if (p.out && c < p.cols) {
 #pragma unroll
@@ -490,13 +513,13 @@ Kernel backward_kernel(bool row, bool col) {
   return add_norm_backward_kernel<kF32, false, false, kThreads>;
 }
 
-// The backward kernel wants 200 registers a thread and gets what its warps leave:
-// 255 up to 8 of them, 168 up to 12 (a few spilled), then 128 (many).
+// The backward kernel that holds its values gets 255 registers a thread up to 8 warps,
+// 168 up to 12 (a few spilled); the other one 128.
 template <bool kF32>
-Kernel backward_kernel(bool row, bool col, int warps) {
-  return warps <= 8    ? backward_kernel<kF32, 256>(row, col)
-         : warps <= 12 ? backward_kernel<kF32, 384>(row, col)
-                       : backward_kernel<kF32, 512>(row, col);
+Kernel backward_kernel(bool row, bool col, bool held, int warps) {
+  return !held        ? backward_kernel<kF32, 512>(row, col)
+         : warps <= 8 ? backward_kernel<kF32, 256>(row, col)
+                      : backward_kernel<kF32, 384>(row, col);
 }
 
 // How a width is split: CTAs of a cluster, warps of a CTA; how many such clusters
@@ -551,46 +574,62 @@ cudaError_t occupancy(Split& s) {
   return e;
 }
 
+// One way to split the width; false where it cannot be.
+bool split_of(const AddNormLaunch& L, int csize, bool held, Split* s) {
+  const int64_t units = (L.cols + kUnitCols - 1) / kUnitCols;
+  const bool row = L.row_data != nullptr, col = L.col_data != nullptr, f32 = L.stream_f32;
+  *s = {};
+  s->csize = csize;
+  s->warps = static_cast<int>((units + csize - 1) / csize);
+  if (s->warps > kMaxWarps || (held && s->warps > 12)) return false;
+  uint32_t stage = 4096 + unit_box_bytes(f32);
+  if (L.backward && L.third) {
+    // With an FP32 stream a whole stage is 22 KB a warp, more than 8 warps' room.
+    s->direct = f32 && s->warps > 8;
+    if (!s->direct) stage += unit_box_bytes(f32);
+  }
+  s->smem = 1024 + static_cast<size_t>(s->warps) * stage + sums_bytes(csize, s->warps);
+  s->kern = !L.backward ? (f32 ? forward_kernel<true>(row, col) : forward_kernel<false>(row, col))
+                        : (f32 ? backward_kernel<true>(row, col, held, s->warps) : backward_kernel<false>(row, col, held, s->warps));
+  return true;
+}
+
 // The split with the least estimated time. A cluster takes one panel a round; a round
 // takes a fixed time (the exchange; less where a second CTA of the SM works meanwhile)
 // and one in proportion to the SM's warps. Measured on GB300, us: forward 1.2 (0.7) +
-// 0.37 a warp, backward 1.9 + 0.38. What that decides (BF16 stream, both copies):
-// forward 8192 x 5120 clusters of 5 CTAs x 16 warps 65.7 us, of 8 x 10 82, 16 x 5 72;
-// 8192 x 7168 8 x 14 100, 7 x 16 107, 16 x 7 104 (FP32 stream: 154, 170, 146); backward
-// 32768 x 1408 2 x 11 85.6, 3 x 8 97, 4 x 6 110; 16384 x 2048 4 x 8 70.8, 3 x 11 72.1, 2 x
-// 16 (spilled) 112, and 8 x 4, two CTAs an SM, 69 or 81 from run to run.
+// 0.37 a warp, backward 1.0 + 0.40 with its values held over the exchange, else 2.0 (0.3)
+// + 0.48. What that decides (BF16 stream, both copies): forward 8192 x 5120 clusters of 5
+// CTAs x 16 warps 65.7 us, of 8 x 10 82, 16 x 5 72; 8192 x 7168 8 x 14 100, 7 x 16 107,
+// 16 x 7 104 (FP32 stream: 154, 170, 146); backward, held and not: 16384 x 2048 4 x 8 70.1
+// and 67.4, 2 x 16 - and 72.7; 8192 x 4096 6 x 11 74.3 and 94.1, 8 x 8 79.5 and 69.8; 8192 x
+// 7168 16 x 7 154.7 and 133.9; 32768 x 1408 2 x 11 85.8 and 104.8, 6 x 4 96.3 and 86.7; 4096 x
+// 12288 16 x 12 119 and 146. With an FP32 stream the values are held wherever they can
+// be (8192 x 7168: 197 us, and 308): its stages leave room for 9 warps of an SM.
 mx_status choose(const AddNormLaunch& L, Split* out) {
-  const int64_t units = (L.cols + kUnitCols - 1) / kUnitCols, panels = (L.rows + 31) / 32;
-  const bool row = L.row_data != nullptr, col = L.col_data != nullptr, f32 = L.stream_f32;
+  const int64_t panels = (L.rows + 31) / 32;
   double best = 0.0;
   out->held = 0;
   for (int csize : {1, 2, 3, 4, 5, 6, 7, 8, kMaxCluster}) {
-    Split s = {};
-    s.csize = csize;
-    s.warps = static_cast<int>((units + csize - 1) / csize);
-    if (s.warps > kMaxWarps || (s.warps < 4 && out->held > 0)) continue;
-    uint32_t stage = 4096 + unit_box_bytes(f32);
-    if (L.backward && L.third) {
-      // With an FP32 stream a whole stage is 22 KB a warp, more than 8 warps' room.
-      s.direct = f32 && s.warps > 8;
-      if (!s.direct) stage += unit_box_bytes(f32);
-    }
-    s.smem = 1024 + static_cast<size_t>(s.warps) * stage + sums_bytes(csize, s.warps);
-    s.kern = !L.backward ? (f32 ? forward_kernel<true>(row, col) : forward_kernel<false>(row, col))
-                         : (f32 ? backward_kernel<true>(row, col, s.warps) : backward_kernel<false>(row, col, s.warps));
-    const cudaError_t e = occupancy(s);
-    if (e != cudaSuccess) return cuda_status(e, "add_norm occupancy");
-    if (s.held < 1) continue;
-    const int64_t held = std::min<int64_t>(s.held, kMaxParts);
-    const double fixed = L.backward ? 1.9 : (s.per_sm > 1 ? 0.7 : 1.2);
-    // fewer panels than clusters: an SM has one CTA
-    const int per_sm = panels * csize <= sm_count() ? 1 : std::max(1, s.per_sm);
-    double t = static_cast<double>((panels + held - 1) / held) * (fixed + (L.backward ? 0.38 : 0.37) * s.warps * per_sm);
-    if (s.direct) t *= 2.0;  // 8192 x 7168: 394 us with dsum read by the lanes, 197 through shared memory
-    if (L.backward && s.warps > 12) t *= 1.5;
-    if (out->held == 0 || t < best) {
-      best = t;
-      *out = s;
+    for (const bool held : {true, false}) {
+      Split s;
+      if (held && !L.backward) continue;
+      if (!split_of(L, csize, held, &s) || (s.warps < 4 && out->held > 0)) continue;
+      if (L.backward && !held && L.stream_f32 && s.warps <= 12) continue;
+      const cudaError_t e = occupancy(s);
+      if (e != cudaSuccess) return cuda_status(e, "add_norm occupancy");
+      if (s.held < 1) continue;
+      const int64_t clusters = std::min<int64_t>(s.held, kMaxParts);
+      const bool two = s.per_sm > 1;
+      const double fixed = !L.backward ? (two ? 0.7 : 1.2) : held ? 1.0 : (two ? 0.3 : 2.0);
+      // fewer panels than clusters: an SM has one CTA
+      const int per_sm = panels * csize <= sm_count() ? 1 : std::max(1, s.per_sm);
+      double t = static_cast<double>((panels + clusters - 1) / clusters) *
+                 (fixed + (!L.backward ? 0.37 : held ? 0.40 : 0.48) * s.warps * per_sm);
+      if (s.direct) t *= 2.0;  // 8192 x 7168: 394 us with dsum read by the lanes, 197 through shared memory
+      if (out->held == 0 || t < best) {
+        best = t;
+        *out = s;
+      }
     }
   }
   if (out->held > 0) return MX_OK;

@@ -110,6 +110,17 @@ def test_backward_widths(cols, dtype):
     check_backward(b, dy, s, w, rstd, ds)
 
 
+# panels enough for several rounds of every cluster, two CTAs an SM
+@pytest.mark.parametrize("rows,cols,dtype", [(5152, 2048, BF16), (2080, 7168, BF16), (2592, 4096, BF16), (4224, 1024, F32), (1056, 7168, F32)])
+def test_rounds(rows, cols, dtype):
+    x, res, w = matrix(rows, cols, 1, BF16, std=0.5), matrix(rows, cols, 2, dtype, std=2.0), weight_of(cols, 3)
+    n = mx.add_norm_quantize(x, res, w, eps=EPS, axis=mx.MX_BOTH, keep_output=True)
+    check_forward(n, x, res, w)
+    dy, ds = matrix(rows, cols, 5, BF16, std=0.1), matrix(rows, cols, 6, dtype, std=0.3)
+    for axis, dsum in ((mx.MX_BOTH, ds), (mx.MX_ROWWISE, None), (0, ds)):
+        check_backward(mx.add_norm_backward(dy, n.sum, w, n.rstd, dsum=dsum, axis=axis), dy, n.sum, w, n.rstd, dsum)
+
+
 @pytest.mark.parametrize("rows", [1, 2, 31, 32, 33, 127, 129, 1000])
 @pytest.mark.parametrize("cols,pad,dtype", [(96, 8, BF16), (2048, 64, BF16), (1408, 4, F32)])
 def test_row_counts(rows, cols, pad, dtype):
