@@ -1181,10 +1181,15 @@ _GATED_BLOCK = ("AddNorm", "AddNormGrads", "add_norm_quantize", "add_norm_backwa
                 "gated_backward_quantize")
 
 
+_gated_block = None
+
+
 def __getattr__(name):
+    global _gated_block
     if name in _GATED_BLOCK:
-        from . import gated_block
-        return getattr(gated_block, name)
+        if _gated_block is None:
+            from . import gated_block as _gated_block
+        return getattr(_gated_block, name)
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 

@@ -52,6 +52,12 @@
 // to 148. Those are short runs at 2070 MHz; call after call the power cap holds
 // the SM clock at 1.6 to 1.7 GHz, and they take 146, 138 and 156 to 160 us.
 //
+// mx_gemm_gated's epilogue (kEpi 3, 4) takes both of a tile's products: the pair's
+// even CTA loads gate rows, its odd one up rows of the second operand, so an
+// accumulator's halves are 128 gate and the same 128 up columns. M = 8192, F = 10944,
+// K = 2048: 225 us (3.26 PFLOP/s), 256 with both products kept (358 MB). Few tiles
+// take mx_gemm_few.cu's kernel.
+//
 // Every mbarrier wait is bounded in wall time; on expiry the CTA records
 // MX_ERR_TIMEOUT in dev_status, drains its own copies and MMAs, frees its
 // tensor memory and returns.

@@ -5,16 +5,33 @@ marshalling only, as in the package."""
 
 from __future__ import annotations
 
+import functools
 from dataclasses import dataclass
 from typing import Optional
 
+import torch
+
 import mxfp8_block_scaled_gb300 as mx
+
+# A small call costs what its wrapper does on the host, so the wrappers look little up:
+# sizes of scale buffers are asked for once, a matrix's checks are one call.
+_BF16, _F32, _U8 = torch.bfloat16, torch.float32, torch.uint8
+_DTYPE = {_BF16: mx.MX_BF16, _F32: mx.MX_F32}
+_scale_bytes = functools.lru_cache(maxsize=1024)(mx.mx_scale_bytes)
+_norm_workspace = functools.lru_cache(maxsize=1024)(mx.mx_add_norm_backward_workspace_bytes)
+
+
+def _matrix(t, rows, cols, dtype, what) -> int:
+    """Pitch of a [rows, cols] matrix of contiguous rows."""
+    assert t.dtype is dtype and t.shape == (rows, cols), what
+    p, q = t.stride()
+    assert t.is_cuda and (q == 1 or cols <= 1), "needs 2-D CUDA tensors with contiguous rows"
+    return p if rows > 1 else cols
 
 
 def _copy(rows, k, orient, dev) -> mx.MXTensor:
-    torch = mx._torch()
-    return mx.MXTensor(torch.empty((rows, k), dtype=torch.uint8, device=dev),
-                       torch.empty(mx.mx_scale_bytes(rows, k), dtype=torch.uint8, device=dev), rows, k, orient)
+    empty = torch.empty
+    return mx.MXTensor(empty((rows, k), dtype=_U8, device=dev), empty(_scale_bytes(rows, k), dtype=_U8, device=dev), rows, k, orient)
 
 
 def _copies(axis, rows, cols, dev, group_offsets=None, col_capacity=None):
@@ -22,18 +39,20 @@ def _copies(axis, rows, cols, dev, group_offsets=None, col_capacity=None):
     lays them out, and the raw call's arguments for them: (row, col, pointers,
     n_groups, capacity)."""
     assert 0 <= axis <= mx.MX_BOTH, "axis: MX_ROWWISE, MX_COLWISE, MX_BOTH"
-    row = _copy(rows, cols, mx.MX_ROWWISE, dev) if axis & mx.MX_ROWWISE else None
-    col, n_groups, cap = None, 0, 0
+    n_groups, cap, width = 0, 0, rows
     if group_offsets is not None:
-        torch = mx._torch()
         assert group_offsets.is_cuda and group_offsets.dtype == torch.int64 and group_offsets.is_contiguous(), \
             "group_offsets: int64 CUDA tensor"
         n_groups = group_offsets.numel() - 1
-        cap = int(col_capacity) if col_capacity is not None else ((rows + 127 * n_groups + 127) // 128) * 128
+        cap = width = int(col_capacity) if col_capacity is not None else ((rows + 127 * n_groups + 127) // 128) * 128
+    row = col = rd = rs = cd = cs = None
+    if axis & mx.MX_ROWWISE:
+        row = _copy(rows, cols, mx.MX_ROWWISE, dev)
+        rd, rs = row.data.data_ptr(), row.scale.data_ptr()
     if axis & mx.MX_COLWISE:
-        col = _copy(cols, cap if group_offsets is not None else rows, mx.MX_COLWISE, dev)
-    pointers = [p for c in (row, col) for p in ((None, None) if c is None else (c.data.data_ptr(), c.scale.data_ptr()))]
-    return row, col, pointers, n_groups, cap
+        col = _copy(cols, width, mx.MX_COLWISE, dev)
+        cd, cs = col.data.data_ptr(), col.scale.data_ptr()
+    return row, col, (rd, rs, cd, cs), n_groups, cap
 
 
 @dataclass
@@ -67,25 +86,23 @@ def add_norm_quantize(x, residual=None, weight=None, eps: float = 1e-5, axis: in
     Any row pitch of whole 16-byte pieces."""
     if stream is not None:
         return mx._under(stream, add_norm_quantize, locals())
-    torch = mx._torch()
     R, C = x.shape
-    dev = x.device
-    assert x.dtype == torch.bfloat16, "x: BF16"
-    ldx = mx._rows(x)
-    sd, ldr = (mx.MX_BF16, 0) if residual is None else (mx._dtype(residual), mx._rows(residual))
-    assert residual is None or residual.shape == x.shape, "the residual has x's shape"
-    if out is None and residual is not None:
-        out = torch.empty((R, C), dtype=residual.dtype, device=dev)
-    lds = 0
-    if out is not None:
-        assert out.shape == x.shape and out.dtype == (torch.bfloat16 if residual is None else residual.dtype), \
-            "out: x's shape, the residual's dtype"
-        lds = mx._rows(out)
+    dev, empty = x.device, torch.empty
+    ldx = _matrix(x, R, C, _BF16, "x: BF16")
+    st, dt, ldr, lds = _BF16, mx.MX_BF16, 0, 0
+    if residual is not None:
+        st = residual.dtype
+        dt, ldr = _DTYPE.get(st), _matrix(residual, R, C, st, "the residual has x's shape")
+        assert dt is not None, f"residual: BF16 or FP32, got {st}"
+        if out is None:
+            out, lds = empty((R, C), dtype=st, device=dev), C
+    if lds == 0 and out is not None:
+        lds = _matrix(out, R, C, st, "out: x's shape, the residual's dtype")
     row, col, pointers, _, _ = _copies(axis, R, C, dev)
-    y = torch.empty((R, C), dtype=torch.bfloat16, device=dev) if keep_output else None
-    rstd = torch.empty(R, dtype=torch.float32, device=dev) if stats else None
-    mx.mx_add_norm_quantize(x.data_ptr(), ldx, mx._ptr(residual), ldr, sd, mx._ptr(weight), mx._params(weight, None, C), R, C, eps, axis,
-                         mx._ptr(out), lds, mx._ptr(y), C, mx._ptr(rstd), *pointers, mx._ptr(status), mx._stream(stream))
+    y = empty((R, C), dtype=_BF16, device=dev) if keep_output else None
+    rstd = empty(R, dtype=_F32, device=dev) if stats else None
+    mx.mx_add_norm_quantize(x.data_ptr(), ldx, mx._ptr(residual), ldr, dt, mx._ptr(weight), mx._params(weight, None, C), R, C, eps, axis,
+                            mx._ptr(out), lds, mx._ptr(y), C, mx._ptr(rstd), *pointers, mx._ptr(status), mx._stream(None))
     return AddNorm(x if out is None else out, rstd, row, col, y)
 
 
@@ -97,27 +114,26 @@ def add_norm_backward(dy, sum, weight, rstd, dsum=None, axis: int = 0, weight_gr
     wrote x). ``out``: where dx goes (may be dsum itself)."""
     if stream is not None:
         return mx._under(stream, add_norm_backward, locals())
-    torch = mx._torch()
     R, C = sum.shape
-    dev = sum.device
-    assert dy.dtype == torch.bfloat16 and dy.shape == sum.shape, "dy: BF16, of sum's shape"
-    assert rstd.is_cuda and rstd.dtype == torch.float32 and rstd.is_contiguous() and rstd.numel() == R, "rstd: FP32, one per row"
-    sd, ldd = mx._dtype(sum), 0
-    if dsum is not None:
-        assert dsum.dtype == sum.dtype and dsum.shape == sum.shape, "dsum: sum's dtype and shape"
-        ldd = mx._rows(dsum)
+    dev, st, empty = sum.device, sum.dtype, torch.empty
+    dt = _DTYPE.get(st)
+    assert dt is not None, f"sum: BF16 or FP32, got {st}"
+    lds, lddy = _matrix(sum, R, C, st, "sum"), _matrix(dy, R, C, _BF16, "dy: BF16, of sum's shape")
+    assert rstd.is_cuda and rstd.dtype is _F32 and rstd.is_contiguous() and rstd.numel() == R, "rstd: FP32, one per row"
+    ldd = 0 if dsum is None else _matrix(dsum, R, C, st, "dsum: sum's dtype and shape")
     if out is None:
-        out = torch.empty((R, C), dtype=sum.dtype, device=dev)
-    assert out.dtype == sum.dtype and out.shape == sum.shape, "out: sum's dtype and shape"
+        out, ldo = empty((R, C), dtype=st, device=dev), C
+    else:
+        ldo = _matrix(out, R, C, st, "out: sum's dtype and shape")
     row, col, pointers, _, _ = _copies(axis, R, C, dev)
     dweight, ws, nbytes = None, None, 0
     if weight_grad:
-        dweight = torch.empty(C, dtype=torch.float32, device=dev)
-        nbytes = mx.mx_add_norm_backward_workspace_bytes(R, C)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    mx.mx_add_norm_backward(dy.data_ptr(), mx._rows(dy), sum.data_ptr(), mx._rows(sum), mx._ptr(dsum), ldd, sd, mx._ptr(weight),
-                         mx._params(weight, None, C), rstd.data_ptr(), R, C, axis, out.data_ptr(), mx._rows(out), mx._ptr(dweight),
-                         *pointers, mx._ptr(ws) if nbytes else None, nbytes, mx._ptr(status), mx._stream(stream))
+        dweight = empty(C, dtype=_F32, device=dev)
+        nbytes = _norm_workspace(R, C)
+        ws = empty(nbytes, dtype=_U8, device=dev)
+    mx.mx_add_norm_backward(dy.data_ptr(), lddy, sum.data_ptr(), lds, mx._ptr(dsum), ldd, dt, mx._ptr(weight),
+                            mx._params(weight, None, C), rstd.data_ptr(), R, C, axis, out.data_ptr(), ldo, mx._ptr(dweight),
+                            *pointers, mx._ptr(ws) if nbytes else None, nbytes, mx._ptr(status), mx._stream(None))
     return AddNormGrads(out, dweight, row, col)
 
 
@@ -128,15 +144,16 @@ def gemm_gated(a: mx.MXTensor, gate: mx.MXTensor, up: mx.MXTensor, act: str = "s
     products side by side, BF16 [M, 2F], for gated_backward_quantize, else None."""
     if stream is not None:
         return mx._under(stream, gemm_gated, locals())
-    torch = mx._torch()
-    M, F = a.rows, gate.rows
-    dev = a.data.device
+    M, F, act = a.rows, gate.rows, mx.ACTIVATIONS[act]
+    dev, empty = a.data.device, torch.empty
     if out is None:
-        out = torch.empty((M, F), dtype=torch.bfloat16, device=dev)
-    assert out.dtype == torch.bfloat16 and out.shape == (M, F), "out: BF16 [M, F]"
-    pre = torch.empty((M, 2 * F), dtype=torch.bfloat16, device=dev) if keep_preact else None
-    mx.mx_gemm_gated(a.c_operand(), gate.c_operand(), up.c_operand(), mx.ACTIVATIONS[act], out.data_ptr(), mx._rows(out), mx._ptr(pre),
-                  2 * F, mx._ptr(status), mx._stream(stream))
+        out, ldc = empty((M, F), dtype=_BF16, device=dev), F
+        assert out.is_cuda, "needs CUDA tensors"
+    else:
+        ldc = _matrix(out, M, F, _BF16, "out: BF16 [M, F]")
+    pre = empty((M, 2 * F), dtype=_BF16, device=dev) if keep_preact else None
+    mx.mx_gemm_gated(a.c_operand(), gate.c_operand(), up.c_operand(), act, out.data_ptr(), ldc, mx._ptr(pre), 2 * F,
+                     mx._ptr(status), mx._stream(None))
     return out, pre
 
 
@@ -147,12 +164,13 @@ def gated_quantize(gate_up, act: str = "silu", axis: int = mx.MX_BOTH, group_off
     the column copy in the experts' segments, as quantize's."""
     if stream is not None:
         return mx._under(stream, gated_quantize, locals())
-    R, F = gate_up.shape[0], gate_up.shape[1] // 2
-    assert gate_up.dtype == mx._torch().bfloat16 and gate_up.shape[1] % 2 == 0, "gate_up: BF16 [rows, 2F]"
-    ld = mx._rows(gate_up)
+    R, F = gate_up.shape
+    ld = _matrix(gate_up, R, F, _BF16, "gate_up: BF16 [rows, 2F]")
+    assert F % 2 == 0, "gate_up: BF16 [rows, 2F]"
+    F //= 2
     row, col, pointers, n_groups, cap = _copies(axis, R, F, gate_up.device, group_offsets, col_capacity)
     mx.mx_gated_quantize(gate_up.data_ptr(), ld, R, F, mx.ACTIVATIONS[act], axis, *pointers, mx._ptr(group_offsets), n_groups, cap,
-                      mx._ptr(status), mx._stream(stream))
+                         mx._ptr(status), mx._stream(None))
     return row, col
 
 
@@ -164,10 +182,9 @@ def gated_backward_quantize(dh, gate_up, act: str = "silu", axis: int = mx.MX_BO
     if stream is not None:
         return mx._under(stream, gated_backward_quantize, locals())
     R, F = dh.shape
-    bf16 = mx._torch().bfloat16
-    assert dh.dtype == bf16 and gate_up.dtype == bf16 and tuple(gate_up.shape) == (R, 2 * F), "dh BF16 [rows, F], gate_up [rows, 2F]"
-    lddh, ld = mx._rows(dh), mx._rows(gate_up)
+    lddh = _matrix(dh, R, F, _BF16, "dh: BF16 [rows, F]")
+    ld = _matrix(gate_up, R, 2 * F, _BF16, "gate_up: BF16 [rows, 2F]")
     row, col, pointers, n_groups, cap = _copies(axis, R, 2 * F, dh.device, group_offsets, col_capacity)
     mx.mx_gated_backward_quantize(dh.data_ptr(), lddh, gate_up.data_ptr(), ld, R, F, mx.ACTIVATIONS[act], axis, *pointers,
-                               mx._ptr(group_offsets), n_groups, cap, mx._ptr(status), mx._stream(stream))
+                                  mx._ptr(group_offsets), n_groups, cap, mx._ptr(status), mx._stream(None))
     return row, col
