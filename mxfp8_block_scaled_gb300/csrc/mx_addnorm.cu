@@ -18,7 +18,7 @@
 //
 // Measured, both copies (of 6787 GB/s copied): forward 16384 x 2048 50 us (79%), 8192 x
 // 7168 103 us (67%), with an FP32 stream and the output in BF16 too 163 us (75%);
-// backward 16384 x 2048 68 us (73%, 4 of them the sum of the partial rows of dweight),
+// backward 16384 x 2048 67 us (74%, 3 of them the sum of the partial rows of dweight),
 // 8192 x 7168 134 us (65%). The rest is the exchange, and clusters that leave SMs over:
 // wide rows take 8 or 16 CTAs of a GPC's 18 to 20 SMs.
 //
@@ -735,7 +735,10 @@ mx_status launch_add_norm(const AddNormLaunch& L, cudaStream_t s) {
                                  sp.smem, s, static_cast<unsigned>(sp.csize), a),
                    L.backward ? "mx_add_norm_backward launch" : "mx_add_norm_quantize launch");
   if (st != MX_OK || !L.dweight) return st;
-  return launch_column_reduce(a.partial, clusters, L.cols, 0, L.dweight, nullptr, s);
+  // A next kernel that is placed while the sums' CTAs hold some SMs' registers comes out
+  // lopsided, for all of its time if it is one of clusters such as this: 16384 x 2048, call
+  // after call, 68 to 88 us, and 66 behind the sums.
+  return launch_column_reduce(a.partial, clusters, L.cols, 0, L.dweight, nullptr, s, true);
 }
 
 }  // namespace mx

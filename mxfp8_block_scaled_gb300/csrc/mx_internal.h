@@ -303,8 +303,9 @@ struct GatedLaunch {
 mx_status launch_gated(const GatedLaunch& L, cudaStream_t s);
 
 // Sums over p < parts of partial[p][c], added in a fixed order: columns [0, n0)
-// to out0, [n0, n0 + n1) to out1 (null: not wanted).
+// to out0, [n0, n0 + n1) to out1 (null: not wanted). hold_next: the next kernel on the
+// stream starts behind it, not beside it.
 mx_status launch_column_reduce(const float* partial, int parts, int64_t n0, int64_t n1, float* out0, float* out1,
-                               cudaStream_t s);
+                               cudaStream_t s, bool hold_next = false);
 
 }  // namespace mx

@@ -1378,12 +1378,13 @@ namespace {
 // out[c] = sum over p of partial[p][c], c over the n0 + n1 columns of a partial
 // row (the first n0 go to out0, the others to out1; null: not wanted). A CTA
 // takes 8 * V columns; thread row y adds the partial rows y, y + 32, ... and a
-// column's 32 sums are then added pairwise: a fixed order whatever the grid.
+// column's 32 sums are then added pairwise: a fixed order whatever the grid. hold_next:
+// the next kernel's CTAs are not placed beside this one's.
 template <int V>
 __global__ void __launch_bounds__(256) column_reduce_kernel(const float* partial, int parts, int64_t n0, int64_t n1,
-                                                            float* out0, float* out1) {
+                                                            float* out0, float* out1, bool hold_next) {
   __shared__ float s[32][8 * V + 1];
-  pdl_launch_dependents();
+  if (!hold_next) pdl_launch_dependents();
   const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3;
   const int64_t n = n0 + n1, c = (static_cast<int64_t>(blockIdx.x) * 8 + tx) * V;
   float v[V];
@@ -1418,13 +1419,13 @@ __global__ void __launch_bounds__(256) column_reduce_kernel(const float* partial
 }  // namespace
 
 mx_status launch_column_reduce(const float* partial, int parts, int64_t n0, int64_t n1, float* out0, float* out1,
-                               cudaStream_t s) {
+                               cudaStream_t s, bool hold_next) {
   const int64_t n = n0 + n1;
   const bool vec = n % 4 == 0 && (reinterpret_cast<uintptr_t>(partial) & 15) == 0;
   const int width = vec ? 32 : 8;
   return cuda_status(launch_kernel(vec ? column_reduce_kernel<4> : column_reduce_kernel<1>,
                                    static_cast<unsigned>((n + width - 1) / width), 256, 0, s, 1, partial, parts, n0, n1,
-                                   out0, out1),
+                                   out0, out1, hold_next),
                      "partial sums launch");
 }
 
