@@ -17,7 +17,7 @@
 // for both copies and both gradients.
 //
 // Measured, both copies, SiLU (of 6787 GB/s copied): forward 49152 x 1408, 64 experts
-// 75.6 us (82%), 8192 x 10944 88 us (91%); backward 123.5 us (84%) and 144 us (93%).
+// 71 us (87%), 8192 x 10944 89 us (90%); backward 117 us (88%) and 144 us (93%).
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -35,13 +35,17 @@ namespace {
 
 constexpr int kTile = 128;  // rows of a CTA's tile
 
-// Units side by side in a CTA's tile, four warps each, and CTAs of an SM: as many warps
-// as the registers of a unit allow (168 a thread forward, 219 backward). Wider tiles keep
-// neighbours in memory together, narrower ones keep warps from waiting; us with 1 x 3 and
-// 2 x 2 forward: 88 and 98 (8192 x 10944), 75.6 and 71 (49152 x 1408, 64 experts), 3.7 and
-// 4.4 (512 x 1408); with 1 x 2 and 2 x 1 backward: 157 and 144, 117 and 123.5.
-__host__ __device__ constexpr int units_across(bool backward) { return backward ? 2 : 1; }
-__host__ __device__ constexpr int ctas_per_sm(bool backward) { return backward ? 1 : 3; }
+// Units side by side in a CTA's tile, four warps each, and CTAs of an SM. Three shapes:
+// forward 1 x 3 (12 warps of 168 registers) or 2 x 2 (16 of 128), backward 2 x 1 or 1 x 2 (8
+// of 219). Dense matrices and row copies alone take the first of each, column copies of
+// groups the second; us of first and second:
+//   dense    forward   8192 x 10944: 88.7, 96.4   49152 x 1408: 69.8, 69.9   512 x 1408: 3.9, 4.3
+//            backward  8192 x 10944: 144, 156     49152 x 1408: 113, 111
+//   groups   forward   49152 x 1408, 64: 76.0, 70.6  256: 91.2, 84.4   16384 x 4096, 8: 71.2, 69.2
+//            backward  49152 x 1408, 64: 123, 117    256: 151, 143     16384 x 4096, 8: 116, 111
+//                      8192 x 10944, 4: 151, 145 (forward 92.5, 101)
+__host__ __device__ constexpr int units_across(bool backward, bool second) { return backward != second ? 2 : 1; }
+__host__ __device__ constexpr int ctas_per_sm(bool backward, bool second) { return backward ? (second ? 2 : 1) : (second ? 2 : 3); }
 
 struct GatedArgs {
   CUtensorMap dh, gate, up;
@@ -136,10 +140,10 @@ __device__ int32_t setup_groups(const GatedArgs& p, bool col, int32_t* off, int3
 // The four warps of a unit's column.
 __device__ __forceinline__ void column_sync(int column) { asm volatile("bar.sync %0, 128;" ::"r"(column + 1) : "memory"); }
 
-template <int kAct, bool kBackward, bool kRow, bool kCol>
-__global__ void __launch_bounds__(128 * units_across(kBackward), ctas_per_sm(kBackward))
+template <int kAct, bool kBackward, bool kRow, bool kCol, bool kSecond>
+__global__ void __launch_bounds__(128 * units_across(kBackward, kSecond), ctas_per_sm(kBackward, kSecond))
     gated_kernel(const __grid_constant__ GatedArgs p) {
-  constexpr int kAcross = units_across(kBackward), kWarps = 4 * kAcross;
+  constexpr int kAcross = units_across(kBackward, kSecond), kWarps = 4 * kAcross;
   constexpr uint32_t kStage = kBackward ? 3 * 4096 : 2 * 4096;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -280,20 +284,22 @@ __global__ void __launch_bounds__(128 * units_across(kBackward), ctas_per_sm(kBa
   }
 }
 
+using Kernel = void (*)(const GatedArgs);
+
 template <int kAct, bool kBackward>
-auto kernel_of(bool row, bool col) -> void (*)(const GatedArgs) {
-  if (row && col) return gated_kernel<kAct, kBackward, true, true>;
-  if (row) return gated_kernel<kAct, kBackward, true, false>;
-  return gated_kernel<kAct, kBackward, false, true>;
+Kernel kernel_of(bool row, bool col, bool second) {
+  if (row && col) return second ? gated_kernel<kAct, kBackward, true, true, true> : gated_kernel<kAct, kBackward, true, true, false>;
+  if (row) return gated_kernel<kAct, kBackward, true, false, false>;
+  return second ? gated_kernel<kAct, kBackward, false, true, true> : gated_kernel<kAct, kBackward, false, true, false>;
 }
 
 template <bool kBackward>
-auto kernel_of(int act, bool row, bool col) -> void (*)(const GatedArgs) {
+Kernel kernel_of(int act, bool row, bool col, bool second) {
   switch (act) {
-    case MX_ACT_RELU: return kernel_of<MX_ACT_RELU, kBackward>(row, col);
-    case MX_ACT_GELU: return kernel_of<MX_ACT_GELU, kBackward>(row, col);
-    case MX_ACT_SILU: return kernel_of<MX_ACT_SILU, kBackward>(row, col);
-    default: return kernel_of<MX_ACT_NONE, kBackward>(row, col);
+    case MX_ACT_RELU: return kernel_of<MX_ACT_RELU, kBackward>(row, col, second);
+    case MX_ACT_GELU: return kernel_of<MX_ACT_GELU, kBackward>(row, col, second);
+    case MX_ACT_SILU: return kernel_of<MX_ACT_SILU, kBackward>(row, col, second);
+    default: return kernel_of<MX_ACT_NONE, kBackward>(row, col, second);
   }
 }
 
@@ -311,7 +317,8 @@ mx_status launch_gated(const GatedLaunch& L, cudaStream_t s) {
                 static_cast<uint8_t*>(L.col_scale), width, (width + 127) / 128, L.col_pitch, (L.col_pitch + 127) / 128};
   a.rows = L.rows;
   a.f = L.f;
-  const int across = units_across(back);
+  const bool second = L.offsets != nullptr && col;
+  const int across = units_across(back, second), per_sm = ctas_per_sm(back, second);
   a.tiles_c = (L.f + across * kUnitCols - 1) / (across * kUnitCols);
   a.tiles_r = (L.rows + kTile - 1) / kTile;
   a.offsets = L.offsets;
@@ -319,12 +326,12 @@ mx_status launch_gated(const GatedLaunch& L, cudaStream_t s) {
   a.capacity = L.col_pitch;
   a.dev_status = L.dev_status;
   a.timeout_ns = wait_timeout_ns();
-  const auto kern = back ? kernel_of<true>(L.act, row, col) : kernel_of<false>(L.act, row, col);
+  const auto kern = back ? kernel_of<true>(L.act, row, col, second) : kernel_of<false>(L.act, row, col, second);
   const size_t smem = 1024 + across * (4 * (back ? 3 : 2) * 4096 + (col ? 2 * kStagedBytes : 0));
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(gated)");
   const int64_t upper = (a.tiles_r + (L.offsets ? L.n_groups : 0)) * a.tiles_c;
-  const unsigned grid = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(upper, ctas_per_sm(back) * sm_count())));
+  const unsigned grid = static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(upper, static_cast<int64_t>(per_sm) * sm_count())));
   return cuda_status(launch_kernel(kern, grid, 128 * across, smem, s, 1, a),
                      back ? "mx_gated_backward_quantize launch" : "mx_gated_quantize launch");
 }
