@@ -17,10 +17,10 @@
 // present one is no longer needed there.
 //
 // Measured, both copies (of 6787 GB/s copied): forward 16384 x 2048 50 us (79%), 8192 x
-// 7168 103 us (67%), with an FP32 stream and the output in BF16 too 163 us (75%);
-// backward 16384 x 2048 67 us (74%, 3 of them the sum of the partial rows of dweight),
-// 8192 x 7168 134 us (65%). The rest is the exchange, and clusters that leave SMs over:
-// wide rows take 8 or 16 CTAs of a GPC's 18 to 20 SMs.
+// 5120 60 us (83%), 8192 x 7168 102 us (68%), with an FP32 stream and the output in BF16
+// too 163 us (75%); backward 16384 x 2048 67 us (74%, 3 of them the sum of the partial rows
+// of dweight), 8192 x 7168 125 us (70%). The rest is the exchange, and clusters that leave
+// SMs over: wide rows take 8 to 16 CTAs of a GPC's SMs.
 //
 // A wait that runs out leaves MX_ERR_TIMEOUT, and NaN in the values it was for; the
 // warp loads nothing more, but takes part in every barrier.
@@ -610,12 +610,17 @@ bool split_of(const AddNormLaunch& L, int csize, bool held, Split* s) {
 // and 67.4, 2 x 16 - and 72.7; 8192 x 4096 6 x 11 74.3 and 94.1, 8 x 8 79.5 and 69.8; 8192 x
 // 7168 16 x 7 154.7 and 133.9; 32768 x 1408 2 x 11 85.8 and 104.8, 6 x 4 96.3 and 86.7; 4096 x
 // 12288 16 x 12 119 and 146. With an FP32 stream the values are held wherever they can
-// be (8192 x 7168: 197 us, and 308): its stages leave room for 9 warps of an SM.
+// be (8192 x 7168: 197 us, and 308): its stages leave room for 9 warps of an SM. Clusters of
+// ten and twelve leave fewer of a GPC's SMs over than those of eight at some widths:
+// forward 8192 x 5120 10 x 8 60.3 us, 8192 x 6144 with an FP32 stream 12 x 8 113.8 (16 x 6
+// 129.4); backward 8192 x 5120 10 x 8 84.7 (5 x 16 98.3), FP32 stream 124 (16 x 5 174), 8192 x
+// 7168 10 x 12 125. Of nine, eleven and thirteen to fifteen none was the fastest anywhere
+// (8192 x 8192 with nine: 105.9, eight 108.0).
 mx_status choose(const AddNormLaunch& L, Split* out) {
   const int64_t panels = (L.rows + 31) / 32;
   double best = 0.0;
   out->held = 0;
-  for (int csize : {1, 2, 3, 4, 5, 6, 7, 8, kMaxCluster}) {
+  for (int csize : {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, kMaxCluster}) {
     for (const bool held : {true, false}) {
       Split s;
       if (held && !L.backward) continue;

@@ -111,7 +111,8 @@ def test_backward_widths(cols, dtype):
 
 
 # panels enough for several rounds of every cluster, two CTAs an SM
-@pytest.mark.parametrize("rows,cols,dtype", [(5152, 2048, BF16), (2080, 7168, BF16), (2592, 4096, BF16), (4224, 1024, F32), (1056, 7168, F32)])
+@pytest.mark.parametrize("rows,cols,dtype", [(5152, 2048, BF16), (2080, 7168, BF16), (2592, 4096, BF16), (4224, 1024, F32), (1056, 7168, F32),
+                                             (1312, 5120, BF16), (1312, 5120, F32), (992, 6144, F32)])
 def test_rounds(rows, cols, dtype):
     x, res, w = matrix(rows, cols, 1, BF16, std=0.5), matrix(rows, cols, 2, dtype, std=2.0), weight_of(cols, 3)
     n = mx.add_norm_quantize(x, res, w, eps=EPS, axis=mx.MX_BOTH, keep_output=True)
