@@ -508,6 +508,7 @@ class MXTensor:
     orient: int         # MX_ROWWISE or MX_COLWISE
 
     def c_operand(self) -> MXOperandC:
+        assert self.data.is_cuda and self.scale.is_cuda, "a product's operands: CUDA tensors"
         return MXOperandC(self.data.data_ptr(), self.scale.data_ptr(), self.rows, self.k,
                           int(self.data.stride(0)), self.orient, 0)
 
@@ -645,6 +646,7 @@ class MXStacked:
     orient: int
 
     def c_operand(self) -> MXOperandC:
+        assert self.data.is_cuda and self.scale.is_cuda, "a product's operands: CUDA tensors"
         return MXOperandC(self.data.data_ptr(), self.scale.data_ptr(), self.rows, self.k,
                           int(self.data.stride(1)), self.orient, 0)
 
