@@ -486,6 +486,12 @@ def _stream(stream) -> Optional[int]:
     return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
+def _output(t):
+    """A given output's address; a CPU tensor's must not reach a kernel."""
+    assert t.is_cuda, "out: a CUDA tensor"
+    return t.data_ptr()
+
+
 def _under(stream, wrapper, arguments):
     """Calls a wrapper again under the stream it was given, so that what it
     allocates (outputs, and scratch that is dropped on return while the kernels
@@ -599,12 +605,13 @@ def gemm(mode: int, a: MXTensor, b: MXTensor, out=None, status=None, stream=None
     if stream is not None:
         return _under(stream, gemm, locals())
     torch = _torch()
+    assert workspace is None or workspace.is_cuda, "workspace: a CUDA tensor"
     if out is None:
         out = torch.empty((a.rows, b.rows), dtype=torch.bfloat16, device=a.data.device)
     if workspace is None:
-        mx_gemm(mode, a.c_operand(), b.c_operand(), out.data_ptr(), out.stride(0), _ptr(status), _stream(stream))
+        mx_gemm(mode, a.c_operand(), b.c_operand(), _output(out), out.stride(0), _ptr(status), _stream(stream))
     else:
-        mx_gemm_with_workspace(mode, a.c_operand(), b.c_operand(), out.data_ptr(), out.stride(0),
+        mx_gemm_with_workspace(mode, a.c_operand(), b.c_operand(), _output(out), out.stride(0),
                                workspace.data_ptr() if workspace.numel() else None, workspace.numel(),
                                _ptr(status), _stream(stream))
     return out
@@ -630,7 +637,7 @@ def gemm_multi(problems, status=None, stream=None):
         out = pr[3] if len(pr) > 3 and pr[3] is not None else \
             torch.empty((a.rows, b.rows), dtype=torch.bfloat16, device=a.data.device)
         outs.append(out)
-        descs.append(MXGemmProblemC(a.c_operand(), b.c_operand(), out.data_ptr(), out.stride(0), mode, 0))
+        descs.append(MXGemmProblemC(a.c_operand(), b.c_operand(), _output(out), out.stride(0), mode, 0))
     mx_gemm_multi(descs, _ptr(status), _stream(stream))
     return outs
 
@@ -683,6 +690,7 @@ def grouped_gemm(mode: int, a, b, group_offsets, out=None, status=None, stream=N
     if stream is not None:
         return _under(stream, grouped_gemm, locals())
     torch = _torch()
+    assert group_offsets.is_cuda, "group_offsets: a CUDA tensor"
     E = group_offsets.numel() - 1
     if out is None:
         if mode == MX_WGRAD:
@@ -690,7 +698,7 @@ def grouped_gemm(mode: int, a, b, group_offsets, out=None, status=None, stream=N
         else:
             out = torch.empty((a.rows, b.rows), dtype=torch.bfloat16, device=a.data.device)
     ldc = out.stride(-2)
-    mx_grouped_gemm(mode, a.c_operand(), b.c_operand(), group_offsets.data_ptr(), E, out.data_ptr(), ldc,
+    mx_grouped_gemm(mode, a.c_operand(), b.c_operand(), group_offsets.data_ptr(), E, _output(out), ldc,
                     _ptr(status), _stream(stream))
     return out
 
@@ -702,10 +710,11 @@ def grouped_gemm_swiglu(a, b, group_offsets, out=None, status=None, stream=None)
     if stream is not None:
         return _under(stream, grouped_gemm_swiglu, locals())
     torch = _torch()
+    assert group_offsets.is_cuda, "group_offsets: a CUDA tensor"
     E = group_offsets.numel() - 1
     if out is None:
         out = torch.empty((a.rows, b.rows // 2), dtype=torch.bfloat16, device=a.data.device)
-    mx_grouped_gemm_swiglu(a.c_operand(), b.c_operand(), group_offsets.data_ptr(), E, out.data_ptr(), out.stride(0),
+    mx_grouped_gemm_swiglu(a.c_operand(), b.c_operand(), group_offsets.data_ptr(), E, _output(out), out.stride(0),
                            _ptr(status), _stream(stream))
     return out
 
@@ -718,6 +727,7 @@ def grouped_gemm_swiglu_quantize(a, b, group_offsets, col_capacity: int, out=Non
     if stream is not None:
         return _under(stream, grouped_gemm_swiglu_quantize, locals())
     torch = _torch()
+    assert group_offsets.is_cuda, "group_offsets: a CUDA tensor"
     E = group_offsets.numel() - 1
     R, F = a.rows, b.rows // 2
     dev = a.data.device
@@ -729,6 +739,7 @@ def grouped_gemm_swiglu_quantize(a, b, group_offsets, col_capacity: int, out=Non
                        MX_COLWISE)
     else:
         row, col = out
+        assert all(t.is_cuda for c in out for t in (c.data, c.scale)), "out: copies of CUDA tensors"
     mx_grouped_gemm_swiglu_quantize(a.c_operand(), b.c_operand(), group_offsets.data_ptr(), E, _ptr(row.data),
                                     _ptr(row.scale), _ptr(col.data), _ptr(col.scale), col_capacity, _ptr(status),
                                     _stream(stream))
@@ -767,10 +778,11 @@ def gemm_fp8_blockwise(a: FP8Blockwise, b: FP8Blockwise, out=None, status=None, 
         return _under(stream, gemm_fp8_blockwise, locals())
     torch = _torch()
     assert a.block == 1 and b.block == 128 and a.k == b.k
+    assert all(t.is_cuda for t in (a.data, a.scale, b.data, b.scale)), "a product's operands: CUDA tensors"
     if out is None:
         out = torch.empty((a.rows, b.rows), dtype=torch.bfloat16, device=a.data.device)
     mx_gemm_fp8_blockwise(a.data.data_ptr(), a.scale.data_ptr(), a.rows, b.data.data_ptr(), b.scale.data_ptr(),
-                          b.rows, a.k, out.data_ptr(), out.stride(0), _ptr(status), _stream(stream))
+                          b.rows, a.k, _output(out), out.stride(0), _ptr(status), _stream(stream))
     return out
 
 
@@ -838,7 +850,7 @@ def gemm_current(mode: int, a, b, out=None, status=None, stream=None):
     torch = _torch()
     if out is None:
         out = torch.empty((a.rows, b.rows), dtype=torch.bfloat16, device=a.data.device)
-    mx_gemm_current(mode, a.c_operand(), b.c_operand(), out.data_ptr(), out.stride(0), _ptr(status), _stream(stream))
+    mx_gemm_current(mode, a.c_operand(), b.c_operand(), _output(out), out.stride(0), _ptr(status), _stream(stream))
     return out
 
 
@@ -855,7 +867,7 @@ def gemm_current_multi(problems, status=None, stream=None):
         out = pr[3] if len(pr) > 3 and pr[3] is not None else \
             torch.empty((a.rows, b.rows), dtype=torch.bfloat16, device=a.data.device)
         outs.append(out)
-        descs.append(MXGemmProblemC(a.c_operand(), b.c_operand(), out.data_ptr(), out.stride(0), mode, 0))
+        descs.append(MXGemmProblemC(a.c_operand(), b.c_operand(), _output(out), out.stride(0), mode, 0))
     mx_gemm_current_multi(descs, _ptr(status), _stream(stream))
     return outs
 
@@ -866,11 +878,12 @@ def grouped_gemm_current(mode: int, a, b, group_offsets, out=None, status=None, 
     if stream is not None:
         return _under(stream, grouped_gemm_current, locals())
     torch = _torch()
+    assert group_offsets.is_cuda, "group_offsets: a CUDA tensor"
     E = group_offsets.numel() - 1
     if out is None:
         shape = (E, a.rows, b.rows) if mode == MX_WGRAD else (a.rows, b.rows)
         out = torch.empty(shape, dtype=torch.bfloat16, device=a.data.device)
-    mx_grouped_gemm_current(mode, a.c_operand(), b.c_operand(), group_offsets.data_ptr(), E, out.data_ptr(),
+    mx_grouped_gemm_current(mode, a.c_operand(), b.c_operand(), group_offsets.data_ptr(), E, _output(out),
                             out.stride(-2), _ptr(status), _stream(stream))
     return out
 

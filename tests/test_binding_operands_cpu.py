@@ -1,6 +1,6 @@
 """The products' wrappers take operands of CUDA tensors only: a CPU tensor's address must
-not reach a kernel, whichever of an operand's two tensors it is. No GPU: the library's
-calls are stand-ins."""
+not reach a kernel, whichever of an operand's two tensors it is; and outputs, workspaces
+and group offsets on the GPU. No GPU: the library's calls are stand-ins."""
 import pytest
 import torch
 
@@ -47,3 +47,44 @@ def test_an_operand_on_the_cpu_is_refused(name, which, part, launches):  # noqa:
     with pytest.raises(AssertionError):
         call(*[make(*tensors) if i == which else make() for i, make in enumerate(makers)])
     assert not launches
+
+
+def blockwise(block, make_data=gpu, make_scale=gpu):
+    return mx.FP8Blockwise(make_data(128, 128, dtype=U8), make_scale(1, 128), 128, 128, block)
+
+
+def copies(make):
+    row = mx.MXTensor(make(64, 32, dtype=U8), make(512, dtype=U8), 64, 32, mx.MX_ROWWISE)
+    return row, mx.MXTensor(make(32, 128, dtype=U8), make(512, dtype=U8), 32, 128, mx.MX_COLWISE)
+
+
+a, b, s = operand(), operand(), stacked()
+OTHERS = {   # every other tensor of a product's call, made here by `make`
+    "gemm out": lambda make: mx.gemm(mx.MX_FPROP, a, b, out=make(*OUT, dtype=BF16)),
+    "gemm_with_workspace out": lambda make: mx.gemm(mx.MX_FPROP, a, b, out=make(*OUT, dtype=BF16), workspace=gpu(512, dtype=U8)),
+    "gemm_with_workspace workspace": lambda make: mx.gemm(mx.MX_FPROP, a, b, out=gpu(*OUT, dtype=BF16), workspace=make(512, dtype=U8)),
+    "gemm_multi out": lambda make: mx.gemm_multi([(mx.MX_FPROP, a, b, make(*OUT, dtype=BF16))]),
+    "gemm_gated out": lambda make: mx.gemm_gated(a, b, b, out=make(*OUT, dtype=BF16)),
+    "gemm_current out": lambda make: mx.gemm_current(mx.MX_FPROP, a, b, out=make(*OUT, dtype=BF16)),
+    "gemm_current_multi out": lambda make: mx.gemm_current_multi([(mx.MX_FPROP, a, b, make(*OUT, dtype=BF16))]),
+    "grouped_gemm out": lambda make: mx.grouped_gemm(mx.MX_FPROP, a, s, gpu(3, dtype=I64), out=make(*OUT, dtype=BF16)),
+    "grouped_gemm offsets": lambda make: mx.grouped_gemm(mx.MX_FPROP, a, s, make(3, dtype=I64), out=gpu(*OUT, dtype=BF16)),
+    "grouped_gemm_current out": lambda make: mx.grouped_gemm_current(mx.MX_FPROP, a, s, gpu(3, dtype=I64), out=make(*OUT, dtype=BF16)),
+    "grouped_gemm_current offsets": lambda make: mx.grouped_gemm_current(mx.MX_FPROP, a, s, make(3, dtype=I64), out=gpu(*OUT, dtype=BF16)),
+    "grouped_gemm_swiglu out": lambda make: mx.grouped_gemm_swiglu(a, s, gpu(3, dtype=I64), out=make(64, 32, dtype=BF16)),
+    "grouped_gemm_swiglu offsets": lambda make: mx.grouped_gemm_swiglu(a, s, make(3, dtype=I64), out=gpu(64, 32, dtype=BF16)),
+    "grouped_gemm_swiglu_quantize out": lambda make: mx.grouped_gemm_swiglu_quantize(a, s, gpu(3, dtype=I64), 128, out=copies(make)),
+    "grouped_gemm_swiglu_quantize offsets": lambda make: mx.grouped_gemm_swiglu_quantize(a, s, make(3, dtype=I64), 128, out=copies(gpu)),
+    "gemm_fp8_blockwise out": lambda make: mx.gemm_fp8_blockwise(blockwise(1), blockwise(128), out=make(128, 128, dtype=BF16)),
+    "gemm_fp8_blockwise a": lambda make: mx.gemm_fp8_blockwise(blockwise(1, make), blockwise(128), out=gpu(128, 128, dtype=BF16)),
+    "gemm_fp8_blockwise b": lambda make: mx.gemm_fp8_blockwise(blockwise(1), blockwise(128, gpu, make), out=gpu(128, 128, dtype=BF16)),
+}
+
+
+@pytest.mark.parametrize("name", OTHERS)
+def test_other_tensors_on_the_cpu_are_refused(name, launches):  # noqa: F811
+    OTHERS[name](gpu)
+    assert launches == ["mx_" + name.split()[0]]
+    with pytest.raises(AssertionError):
+        OTHERS[name](cpu)
+    assert len(launches) == 1
