@@ -814,7 +814,9 @@ mx_status mx_gemm_gated(const mx_operand* a, const mx_operand* gate, const mx_op
  *
  *   axis         MX_ROWWISE, MX_COLWISE or MX_BOTH; row_data .. col_capacity, groups
  *                and their errors as mx_quantize's of the [rows, F] (backward: [rows,
- *                2F]) matrix. Dense column copies need rows % 32 == 0.
+ *                2F]) matrix, but that a col_capacity that is negative or no multiple
+ *                of 128 is MX_ERR_INVALID_ARG (0 with rows MX_ERR_UNSUPPORTED_SHAPE as
+ *                there). Dense column copies need rows % 32 == 0.
  *   F a multiple of 32. gate_up and dh 16-byte aligned, pitches multiples of 8.
  *   dev_status: also MX_ERR_TIMEOUT where a wait inside the kernel ran out; the values
  *   it was for are NaN.

@@ -192,6 +192,10 @@ mx_status gated(const char* fn, bool backward, const void* dh, int64_t lddh, con
     MX_CHECK(check_aligned(fn, "group_offsets", group_offsets, 8));
   }
   if (rows == 0 || f == 0) return MX_OK;
+  if (grouped && col && col_capacity == 0) {  // the kernel would refuse it, unseen without a dev_status
+    set_error("%s: col_capacity is 0 but rows > 0", fn);
+    return MX_ERR_UNSUPPORTED_SHAPE;
+  }
   if (backward) MX_CHECK(check_wide_matrix(fn, "dh", dh, lddh, f, 2));
   MX_CHECK(check_wide_matrix(fn, "gate_up", gate_up, ld, 2 * f, 2));
   MX_CHECK(check_device());
