@@ -816,7 +816,9 @@ mx_status mx_gemm_gated(const mx_operand* a, const mx_operand* gate, const mx_op
  *                and their errors as mx_quantize's of the [rows, F] (backward: [rows,
  *                2F]) matrix, but that a col_capacity that is negative or no multiple
  *                of 128 is MX_ERR_INVALID_ARG (0 with rows MX_ERR_UNSUPPORTED_SHAPE as
- *                there). Dense column copies need rows % 32 == 0.
+ *                there), and that groups may be given with MX_ROWWISE: a row copy does
+ *                not depend on them, and the offsets are not read. Dense column copies
+ *                need rows % 32 == 0.
  *   F a multiple of 32. gate_up and dh 16-byte aligned, pitches multiples of 8.
  *   dev_status: also MX_ERR_TIMEOUT where a wait inside the kernel ran out; the values
  *   it was for are NaN.

@@ -215,8 +215,10 @@ mx_status gated(const char* fn, bool backward, const void* dh, int64_t lddh, con
     L.col_data = col_data;
     L.col_scale = col_scale;
   }
-  L.offsets = group_offsets;
-  L.n_groups = n_groups;
+  if (grouped && col) {  // a row copy has no segments
+    L.offsets = group_offsets;
+    L.n_groups = n_groups;
+  }
   L.col_pitch = grouped ? col_capacity : rows;
   L.dev_status = dev_status;
   return launch_gated(L, static_cast<cudaStream_t>(stream));

@@ -161,7 +161,8 @@ def gated_quantize(gate_up, act: str = "silu", axis: int = mx.MX_BOTH, group_off
                    status=None, stream=None):
     """MX copies (row, col) of h = act(gate) * up from gate_up = [gate | up], BF16
     [rows, 2F]: what the down projection reads. ``group_offsets``, ``col_capacity``:
-    the column copy in the experts' segments, as quantize's."""
+    the column copy in the experts' segments, as quantize's (the row copy does not
+    depend on them)."""
     if stream is not None:
         return mx._under(stream, gated_quantize, locals())
     R, F = gate_up.shape
