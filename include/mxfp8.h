@@ -799,6 +799,8 @@ mx_status mx_add_norm_backward(const void* dy, int64_t lddy, const void* sum, in
  *   preact       BF16 [M, 2F], pitch ld_preact: receives [A . gate^T | A . up^T] for
  *                mx_gated_backward_quantize; NULL: not kept.
  *   Alignment, K = 0 and errors as mx_gemm. No output overlaps another or an input.
+ *   dev_status: with MX_ERR_TIMEOUT the outputs of tiles whose wait ran out are NaN
+ *   where the kernel for few tokens was taken, and unwritten elsewhere (as mx_gemm's).
  */
 mx_status mx_gemm_gated(const mx_operand* a, const mx_operand* gate, const mx_operand* up, int act, void* c, int64_t ldc,
                         void* preact, int64_t ld_preact, int* dev_status, void* stream);
@@ -867,6 +869,23 @@ mx_status mx_selftest_wait_timeout(uint64_t timeout_ns, int* dev_status, void* s
 mx_status mx_selftest_norm_timeout(uint64_t timeout_ns, const void* dy, const void* x, int64_t rows, int64_t cols,
                                    void* out, float* rstd, float* dweight, float* dbias, void* workspace,
                                    size_t workspace_bytes, int* dev_status, void* stream);
+
+/*
+ * mx_selftest_block_timeout - the same for the gated feed-forward block: the calling
+ * thread's next launch of mx_add_norm_quantize, mx_add_norm_backward,
+ * mx_gated_quantize, mx_gated_backward_quantize or mx_gemm_gated's kernel for few
+ * tokens has a wait that runs out after timeout_ns (1 ms to 10 s), and no launch after
+ * it. Host only; it launches nothing.
+ *   what  1: every stage waits for bytes that nothing sends: all that the call writes
+ *            is NaN (in copies scale 0xFF and codes 0x7F), but for padding.
+ *         2: the norms with both copies: the last CTA of each cluster is not sent the
+ *            sums of the rows of its first panel (32 rows), and sends none from the
+ *            second on. NaN are its columns of the first panel, and all of the
+ *            cluster's other rows; sum and dweight, which do not need a row's sum, are
+ *            right. Other calls run as ever.
+ *         0: takes back what was asked.
+ */
+mx_status mx_selftest_block_timeout(int what, uint64_t timeout_ns);
 
 #ifdef __cplusplus
 }

@@ -51,7 +51,7 @@ EXPORTED = ("mx_scale_bytes", "mx_grouped_padded_rows", "mx_quantize", "mx_quant
             "mx_gemm_epilogue", "mx_epilogue_backward_workspace_bytes", "mx_epilogue_backward",
             "mx_router_workspace_bytes", "mx_router_forward", "mx_router_backward", "mx_selftest_norm_timeout",
             "mx_add_norm_quantize", "mx_add_norm_backward_workspace_bytes", "mx_add_norm_backward", "mx_gemm_gated",
-            "mx_gated_quantize", "mx_gated_backward_quantize")
+            "mx_gated_quantize", "mx_gated_backward_quantize", "mx_selftest_block_timeout")
 MX_STATIC_WORKSPACE_BYTES = 40 * 1024 * 1024
 
 
@@ -201,6 +201,8 @@ def lib() -> ctypes.CDLL:
     L.mx_selftest_wait_timeout.restype = i32
     L.mx_selftest_norm_timeout.argtypes = [ctypes.c_uint64, vp, vp, i64, i64, vp, vp, vp, vp, vp, ctypes.c_size_t, vp, vp]
     L.mx_selftest_norm_timeout.restype = i32
+    L.mx_selftest_block_timeout.argtypes = [i32, ctypes.c_uint64]
+    L.mx_selftest_block_timeout.restype = i32
     L.mx_status_string.argtypes = [i32]
     L.mx_status_string.restype = ctypes.c_char_p
     L.mx_last_error.argtypes = []
@@ -284,6 +286,10 @@ def mx_selftest_norm_timeout(timeout_ns, dy, x, rows, cols, out, rstd, dweight, 
                              stream) -> None:
     _check(lib().mx_selftest_norm_timeout(timeout_ns, dy, x, rows, cols, out, rstd, dweight, dbias, workspace,
                                           workspace_bytes, dev_status, stream), "mx_selftest_norm_timeout")
+
+
+def mx_selftest_block_timeout(what, timeout_ns) -> None:
+    _check(lib().mx_selftest_block_timeout(what, timeout_ns), "mx_selftest_block_timeout")
 
 
 def _ref(op):

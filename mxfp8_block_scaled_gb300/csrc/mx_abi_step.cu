@@ -224,7 +224,15 @@ mx_status gated(const char* fn, bool backward, const void* dh, int64_t lddh, con
   return launch_gated(L, static_cast<cudaStream_t>(stream));
 }
 
+thread_local WaitTest g_wait_test = {};
+
 }  // namespace
+
+mx::WaitTest mx::take_wait_test() {
+  const WaitTest t = g_wait_test;
+  g_wait_test = WaitTest{};
+  return t;
+}
 
 extern "C" {
 
@@ -388,6 +396,15 @@ mx_status mx_selftest_norm_timeout(uint64_t timeout_ns, const void* dy, const vo
   L.withheld = 16;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   return dy ? launch_norm_backward(L, s) : launch_norm_forward(L, s);
+}
+
+mx_status mx_selftest_block_timeout(int what, uint64_t timeout_ns) {
+  if (what < 0 || what > 2 || (what != 0 && (timeout_ns < 1000000ull || timeout_ns > 10000000000ull))) {
+    set_error("mx_selftest_block_timeout: needs what 0, 1 or 2, 1 ms <= timeout_ns <= 10 s");
+    return MX_ERR_INVALID_ARG;
+  }
+  g_wait_test = WaitTest{what, timeout_ns};
+  return MX_OK;
 }
 
 size_t mx_epilogue_backward_workspace_bytes(int64_t rows, int64_t cols) {

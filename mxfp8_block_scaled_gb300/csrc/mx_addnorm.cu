@@ -115,7 +115,8 @@ __device__ __forceinline__ uint64_t ld_shared_u64(uint32_t at) {
 
 // `dead`: a wait of this warp has run out. Once one of the CTA's has, the CTA sends
 // nothing more (its panels come out as NaN, and the others' waits run out too):
-// returns true then.
+// returns true then. kWithheld (the self test): the last CTA is sent nothing.
+template <bool kWithheld>
 __device__ __forceinline__ bool sums_send(const RowSums& s, float mine, bool dead, int warp, int lane, int warps, uint32_t crank,
                                           uint32_t csize, int k) {
   st_shared_f32(s.part + (warp * 32 + lane) * 4, mine);
@@ -131,7 +132,7 @@ __device__ __forceinline__ bool sums_send(const RowSums& s, float mine, bool dea
     }
     const uint64_t word = (static_cast<uint64_t>(static_cast<uint32_t>(k) + 1u) << 32) | __float_as_uint(t);
     const uint32_t at = s.all + (((k & 1) * csize + crank) * 32 + lane) * 8;
-    for (uint32_t r = 0; r < csize; ++r) st_cluster_u64(mapa_shared(at, r), word);
+    for (uint32_t r = 0; r < csize - (kWithheld ? 1 : 0); ++r) st_cluster_u64(mapa_shared(at, r), word);
   }
   return false;
 }
@@ -211,7 +212,7 @@ __device__ __forceinline__ void fill_nan(float2 (&v)[4]) {
 }
 
 // kF32: the residual stream (residual and sum; backward: sum, dsum and dx) is FP32.
-template <bool kF32, bool kRow, bool kCol>
+template <bool kF32, bool kRow, bool kCol, bool kWithheld = false>
 __global__ void __launch_bounds__(32 * kMaxWarps) add_norm_kernel(const __grid_constant__ AddNormArgs p) {
   constexpr uint32_t kStage = 4096 + unit_box_bytes(kF32);
   extern __shared__ uint8_t smem_raw[];
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) add_norm_kernel(const __grid_c
         s[i] = t.x + t.y;
       }
     }
-    dead = sums_send(sums, fold_rows(s, lane), dead, warp, lane, p.warps, crank, csize, k);
+    dead = sums_send<kWithheld>(sums, fold_rows(s, lane), dead, warp, lane, p.warps, crank, csize, k);
     if (active && p.out && c < p.cols) {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -330,7 +331,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) add_norm_kernel(const __grid_c
 // exchange, so that dy's and dsum's next loads are on their way during it. For more
 // warps on an SM there are no registers for that (kThreads 512: 16 warps of 128): the
 // values are then read once more from the stage, which is free for the next load later.
-template <bool kF32, bool kRow, bool kCol, int kThreads>
+template <bool kF32, bool kRow, bool kCol, int kThreads, bool kWithheld = false>
 __global__ void __launch_bounds__(kThreads, 1) add_norm_backward_kernel(const __grid_constant__ AddNormArgs p) {
   constexpr bool kHeld = kThreads < 512;
   constexpr uint32_t kStream = unit_box_bytes(kF32);
@@ -459,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1) add_norm_backward_kernel(const __
       }
     }
     rstd_next = load_rstd(panel + clusters);
-    dead = sums_send(sums, fold_rows(s, lane), dead, warp, lane, p.warps, crank, csize, k);
+    dead = sums_send<kWithheld>(sums, fold_rows(s, lane), dead, warp, lane, p.warps, crank, csize, k);
     const float total = sums_receive(sums, dead, lane, csize, k, p);
     const float mean = -rstd * (total / static_cast<float>(p.cols));
     if (!active) continue;
@@ -528,10 +529,20 @@ Kernel backward_kernel(bool row, bool col, bool held, int warps) {
                       : backward_kernel<kF32, 384>(row, col);
 }
 
+// Their variants for the self test, both copies.
+template <bool kF32>
+Kernel withheld_kernel(bool backward, bool held, int warps) {
+  return !backward    ? add_norm_kernel<kF32, true, true, true>
+         : !held      ? add_norm_backward_kernel<kF32, true, true, 512, true>
+         : warps <= 8 ? add_norm_backward_kernel<kF32, true, true, 256, true>
+                      : add_norm_backward_kernel<kF32, true, true, 384, true>;
+}
+
 // How a width is split: CTAs of a cluster, warps of a CTA; how many such clusters
 // the GPU holds at once and CTAs an SM.
 struct Split {
   int csize, warps, held, per_sm;
+  bool holds;   // backward: the values stay in registers over the exchange
   bool direct;  // backward: dsum not through shared memory
   size_t smem;
   Kernel kern;
@@ -586,6 +597,7 @@ bool split_of(const AddNormLaunch& L, int csize, bool held, Split* s) {
   const bool row = L.row_data != nullptr, col = L.col_data != nullptr, f32 = L.stream_f32;
   *s = {};
   s->csize = csize;
+  s->holds = held;
   s->warps = static_cast<int>((units + csize - 1) / csize);
   if (s->warps > kMaxWarps || (held && s->warps > 12)) return false;
   uint32_t stage = 4096 + unit_box_bytes(f32);
@@ -649,7 +661,7 @@ mx_status choose(const AddNormLaunch& L, Split* out) {
 
 }  // namespace
 
-mx_status make_unit_map(CUtensorMap* map, bool f32, const void* base, int64_t cols, int64_t rows, int64_t ld) {
+mx_status make_unit_map(CUtensorMap* map, bool f32, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
   using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                      const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                      CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -668,7 +680,7 @@ mx_status make_unit_map(CUtensorMap* map, bool f32, const void* base, int64_t co
   }
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * (f32 ? 4 : 2)};
-  const cuuint32_t box[2] = {f32 ? 32u : 64u, static_cast<cuuint32_t>(kUnitRows)};
+  const cuuint32_t box[2] = {f32 ? 32u : 64u, static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t step[2] = {1, 1};
   const CUresult r = enc(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
                          const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -704,7 +716,13 @@ mx_status launch_add_norm(const AddNormLaunch& L, cudaStream_t s) {
     if (st != MX_OK) return st;
     ch = Chosen{L.rows, L.cols, dev, flags, found};
   }
-  const Split sp = ch.split;
+  Split sp = ch.split;
+  const WaitTest test = take_wait_test();
+  if (test.sums() && L.row_data && L.col_data) {
+    sp.kern = L.stream_f32 ? withheld_kernel<true>(L.backward, sp.holds, sp.warps) : withheld_kernel<false>(L.backward, sp.holds, sp.warps);
+    if (const cudaError_t e = occupancy(sp); e != cudaSuccess || sp.held < 1)
+      return cuda_status(e != cudaSuccess ? e : cudaErrorInvalidConfiguration, "add_norm self test");
+  }
   AddNormArgs a = {};
   a.weight = L.weight;
   a.weight_f32 = L.param_dtype == MX_F32;
@@ -714,7 +732,7 @@ mx_status launch_add_norm(const AddNormLaunch& L, cudaStream_t s) {
   a.eps = L.eps;
   a.warps = sp.warps;
   a.dev_status = L.dev_status;
-  a.timeout_ns = wait_timeout_ns();
+  a.timeout_ns = test.limit();
   a.out = L.out;
   a.ld_out = L.ld_out;
   a.y = static_cast<__nv_bfloat16*>(L.y);
@@ -723,7 +741,7 @@ mx_status launch_add_norm(const AddNormLaunch& L, cudaStream_t s) {
   a.rstd_in = L.rstd;
   a.q = CopyOut{static_cast<uint8_t*>(L.row_data), static_cast<uint8_t*>(L.row_scale), static_cast<uint8_t*>(L.col_data),
                 static_cast<uint8_t*>(L.col_scale), L.cols, (L.cols + 127) / 128, L.rows, (L.rows + 127) / 128};
-  st = make_unit_map(&a.a, false, L.first, L.cols, L.rows, L.ld_first);
+  st = make_unit_map(&a.a, false, L.first, L.cols, L.rows, L.ld_first, test.stages() ? kUnitRows / 2 : kUnitRows);
   if (st == MX_OK && L.second) st = make_unit_map(&a.b, L.stream_f32, L.second, L.cols, L.rows, L.ld_second);
   if (st == MX_OK && L.third && !sp.direct) st = make_unit_map(&a.c, L.stream_f32, L.third, L.cols, L.rows, L.ld_third);
   if (st != MX_OK) return st;

@@ -309,7 +309,8 @@ mx_status launch_gated(const GatedLaunch& L, cudaStream_t s) {
   GatedArgs a = {};
   const bool back = L.dh != nullptr, row = L.row_data != nullptr, col = L.col_data != nullptr;
   const int64_t width = back ? 2 * L.f : L.f;
-  mx_status st = make_unit_map(&a.gate, false, L.gate_up, L.f, L.rows, L.ld);
+  const WaitTest test = take_wait_test();
+  mx_status st = make_unit_map(&a.gate, false, L.gate_up, L.f, L.rows, L.ld, test.stages() ? kUnitRows / 2 : kUnitRows);
   if (st == MX_OK) st = make_unit_map(&a.up, false, static_cast<const uint16_t*>(L.gate_up) + L.f, L.f, L.rows, L.ld);
   if (st == MX_OK && back) st = make_unit_map(&a.dh, false, L.dh, L.f, L.rows, L.lddh);
   if (st != MX_OK) return st;
@@ -325,7 +326,7 @@ mx_status launch_gated(const GatedLaunch& L, cudaStream_t s) {
   a.n_groups = L.n_groups;
   a.capacity = L.col_pitch;
   a.dev_status = L.dev_status;
-  a.timeout_ns = wait_timeout_ns();
+  a.timeout_ns = test.limit();
   const auto kern = back ? kernel_of<true>(L.act, row, col, second) : kernel_of<false>(L.act, row, col, second);
   const size_t smem = 1024 + across * (4 * (back ? 3 : 2) * 4096 + (col ? 2 * kStagedBytes : 0));
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));

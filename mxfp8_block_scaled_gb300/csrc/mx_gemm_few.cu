@@ -313,7 +313,8 @@ mx_status launch_few(const GemmLaunch& L, int min_blocks, cudaStream_t s) {
   FewArgs a = {};
   mx_status st = make_operand_map(&a.gate, L.b_data, L.N / 2, L.K, L.b_ld, kRows);
   if (st == MX_OK) st = make_operand_map(&a.up, L.up_data, L.N / 2, L.K, L.up_ld, kRows);
-  if (st == MX_OK) st = make_operand_map(&a.tokens, L.a_data, L.M, L.K, L.a_ld, kN);
+  const WaitTest test = take_wait_test();
+  if (st == MX_OK) st = make_operand_map(&a.tokens, L.a_data, L.M, L.K, L.a_ld, test.stages() ? kN / 2 : kN);
   if (st != MX_OK) return st;
   a.gate_scale = static_cast<const uint8_t*>(L.b_scale);
   a.up_scale = static_cast<const uint8_t*>(L.up_scale);
@@ -330,7 +331,7 @@ mx_status launch_few(const GemmLaunch& L, int min_blocks, cudaStream_t s) {
   const auto aligned = [](const void* q, int64_t ld) { return (reinterpret_cast<uintptr_t>(q) & 7u) == 0 && ld % 4 == 0; };
   a.vec = aligned(L.c, L.ldc) && (!L.epi.preact || (aligned(L.epi.preact, L.epi.ld_preact) && a.F % 4 == 0));
   a.dev_status = L.dev_status;
-  a.timeout_ns = wait_timeout_ns();
+  a.timeout_ns = test.limit();
   const auto kern = gated_few_kernel<kN>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
   if (e != cudaSuccess) return cuda_status(e, "cudaFuncSetAttribute(gated few)");

@@ -26,6 +26,17 @@ mx_status check_device();
 // from the MXFP8_WAIT_TIMEOUT_NS environment variable (default 2 s).
 uint64_t wait_timeout_ns();
 
+// What mx_selftest_block_timeout asked of the calling thread's next launch of the
+// gated block's kernels, handed out once: which wait runs out (0: none), after how long.
+struct WaitTest {
+  int what;
+  uint64_t timeout_ns;
+  bool stages() const { return what == 1; }
+  bool sums() const { return what == 2; }
+  uint64_t limit() const { return what ? timeout_ns : wait_timeout_ns(); }
+};
+WaitTest take_wait_test();
+
 // Number of SMs of the current device (cached per device).
 int sm_count();
 
@@ -252,8 +263,10 @@ mx_status launch_norm_forward(const NormLaunch& L, cudaStream_t s);
 mx_status launch_norm_backward(const NormLaunch& L, cudaStream_t s);
 size_t norm_backward_workspace(int64_t rows, int64_t cols);
 // Tensor map over a [rows, cols] matrix (pitch ld elements) in boxes of 32 rows of
-// 128 bytes, 128-byte swizzle: BF16 boxes of 64 columns, FP32 ones of 32.
-mx_status make_unit_map(CUtensorMap* map, bool f32, const void* base, int64_t cols, int64_t rows, int64_t ld);
+// 128 bytes, 128-byte swizzle: BF16 boxes of 64 columns, FP32 ones of 32. box_rows:
+// fewer in the self test, whose stages wait for the rest in vain.
+mx_status make_unit_map(CUtensorMap* map, bool f32, const void* base, int64_t cols, int64_t rows, int64_t ld,
+                        int box_rows = 32);
 
 struct AddNormLaunch {
   bool backward;
