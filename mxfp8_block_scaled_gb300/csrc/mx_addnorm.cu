@@ -602,7 +602,9 @@ bool split_of(const AddNormLaunch& L, int csize, bool held, Split* s) {
   if (s->warps > kMaxWarps || (held && s->warps > 12)) return false;
   uint32_t stage = 4096 + unit_box_bytes(f32);
   if (L.backward && L.third) {
-    // With an FP32 stream a whole stage is 22 KB a warp, more than 8 warps' room.
+    // With an FP32 stream a whole stage is 22 KB a warp. Eight warps have one; nine (8193 to
+    // 9216 columns) would find room but read dsum themselves as more do: 4096 x 9216 takes
+    // 253 us, 36% of the copy rate, where 8192 x 8192 has 76%.
     s->direct = f32 && s->warps > 8;
     if (!s->direct) stage += unit_box_bytes(f32);
   }
@@ -626,8 +628,8 @@ bool split_of(const AddNormLaunch& L, int csize, bool held, Split* s) {
 // ten and twelve leave fewer of a GPC's SMs over than those of eight at some widths:
 // forward 8192 x 5120 10 x 8 60.3 us, 8192 x 6144 with an FP32 stream 12 x 8 113.8 (16 x 6
 // 129.4); backward 8192 x 5120 10 x 8 84.7 (5 x 16 98.3), FP32 stream 124 (16 x 5 174), 8192 x
-// 7168 10 x 12 125. Of nine, eleven and thirteen to fifteen none was the fastest anywhere
-// (8192 x 8192 with nine: 105.9, eight 108.0).
+// 7168 10 x 12 125. Of nine, eleven and thirteen to fifteen one alone was the fastest at one
+// width, nine (forward 8192 x 8192: 105.9, eight 108.0); they are left out.
 mx_status choose(const AddNormLaunch& L, Split* out) {
   const int64_t panels = (L.rows + 31) / 32;
   double best = 0.0;

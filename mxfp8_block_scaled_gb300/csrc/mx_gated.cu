@@ -43,7 +43,7 @@ constexpr int kTile = 128;  // rows of a CTA's tile
 //            backward  8192 x 10944: 144, 156     49152 x 1408: 113, 111
 //   groups   forward   49152 x 1408, 64: 76.0, 70.6  256: 91.2, 84.4   16384 x 4096, 8: 71.2, 69.2
 //            backward  49152 x 1408, 64: 123, 117    256: 151, 143     16384 x 4096, 8: 116, 111
-//                      8192 x 10944, 4: 151, 145 (forward 92.5, 101)
+//                      8192 x 10944, 4: 151, 145 (forward 92.5, 101: there the rule costs 9%)
 __host__ __device__ constexpr int units_across(bool backward, bool second) { return backward != second ? 2 : 1; }
 __host__ __device__ constexpr int ctas_per_sm(bool backward, bool second) { return backward ? (second ? 2 : 1) : (second ? 2 : 3); }
 

@@ -346,13 +346,16 @@ mx_status launch_few(const GemmLaunch& L, int min_blocks, cudaStream_t s) {
 }  // namespace
 
 // Taken for up to 32 tokens, and for more where a tile of 128 x 128 can have four CTAs
-// with four K blocks each and they all run at once. us of this kernel and of the one for
-// whole tiles (mx_gemm.cu), weights from HBM:
+// with four K blocks each and they are no more than the SMs. (All run at once up to 36
+// tiles; with 37 or 38 of more than 64 tokens launch_few cuts in three: F 4736, K 2048, 100
+// tokens 12.0 us.) us of this kernel and of the one for whole tiles (mx_gemm.cu), weights
+// from HBM:
 //   F 10944, K 2048:   1 token 11.3, 17.4   32: 13.5, 16.8   64: 15.6, 13.7
 //   F 18432, K 7168:   1 token 43.9, 55.9   32: 46.4, 46.5   64: 48.2, 46.8
 //   F  1408, K 2048:   1 token  5.6, 10.8   64:  8.5, 10.9  333: 10.5, 10.9
 //   F  2816, K 7168:   1 token 12.1, 25.4   64: 17.7, 23.8  128: 16.3, 23.9
 //   F   512, K  512:   1 token  3.5,  6.5  128:  7.2,  6.6
+// With weights in L2 333 tokens take 9.7 at F 1408, K 2048.
 bool gated_few_applies(const GemmLaunch& L) {
   const int64_t tiles = (L.N / 2 + kRows - 1) / kRows * ((L.M + 127) / 128);
   if (L.M <= 32) return tiles * kMaxSplit <= INT32_MAX;

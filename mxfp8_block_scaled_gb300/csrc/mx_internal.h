@@ -47,7 +47,8 @@ bool pdl_enabled();
 // may be scheduled while the kernel before it on the stream is finishing; each
 // kernel of this library runs griddepcontrol.wait before its first global
 // memory access, which returns once that previous grid has completed and its
-// writes are visible, and griddepcontrol.launch_dependents at its start.
+// writes are visible, and griddepcontrol.launch_dependents at its start (but for
+// a sum of partial rows that holds the next kernel back, launch_column_reduce).
 // cluster_x > 1 also sets the cluster shape.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_kernel(void (*kern)(KArgs...), unsigned grid, unsigned block, size_t smem, cudaStream_t s,
