@@ -483,6 +483,14 @@ def _ptr(t) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
+def _given(t) -> Optional[int]:
+    """The address of a tensor that a caller may give; a CPU tensor's must not reach a kernel."""
+    if t is None:
+        return None
+    assert t.is_cuda, "status and group_offsets: CUDA tensors"
+    return t.data_ptr()
+
+
 def _stream(stream) -> Optional[int]:
     if stream is not None:
         return stream.cuda_stream
@@ -493,7 +501,7 @@ def _stream(stream) -> Optional[int]:
 
 
 def _output(t):
-    """A given output's address; a CPU tensor's must not reach a kernel."""
+    """A given output's address, likewise."""
     assert t.is_cuda, "out: a CUDA tensor"
     return t.data_ptr()
 
@@ -567,12 +575,12 @@ def quantize(x, axis: int = MX_BOTH, group_offsets=None, col_capacity: Optional[
         mx_quantize_f32(x.data_ptr(), 1, R, C, x.stride(0), 0, axis,
                         _ptr(row.data) if row else None, _ptr(row.scale) if row else None,
                         _ptr(col.data) if col else None, _ptr(col.scale) if col else None,
-                        _ptr(status), _stream(stream))
+                        _given(status), _stream(stream))
         return row, col
     mx_quantize(x.data_ptr(), R, C, x.stride(0), axis,
                 _ptr(row.data) if row else None, _ptr(row.scale) if row else None,
                 _ptr(col.data) if col else None, _ptr(col.scale) if col else None,
-                _ptr(group_offsets), n_groups, cap, _ptr(status), _stream(stream))
+                _given(group_offsets), n_groups, cap, _given(status), _stream(stream))
     return row, col
 
 
@@ -601,7 +609,7 @@ def quantize_multi(xs, axis: int = MX_BOTH, status=None, stream=None):
         descs.append(MXQuantTensorC(x.data_ptr(), R, C, ldx,
                                     _ptr(row.data) if row else None, _ptr(row.scale) if row else None,
                                     _ptr(col.data) if col else None, _ptr(col.scale) if col else None))
-    mx_quantize_multi(descs, axis, _ptr(status), _stream(stream))
+    mx_quantize_multi(descs, axis, _given(status), _stream(stream))
     return outs
 
 
@@ -615,11 +623,11 @@ def gemm(mode: int, a: MXTensor, b: MXTensor, out=None, status=None, stream=None
     if out is None:
         out = torch.empty((a.rows, b.rows), dtype=torch.bfloat16, device=a.data.device)
     if workspace is None:
-        mx_gemm(mode, a.c_operand(), b.c_operand(), _output(out), out.stride(0), _ptr(status), _stream(stream))
+        mx_gemm(mode, a.c_operand(), b.c_operand(), _output(out), out.stride(0), _given(status), _stream(stream))
     else:
         mx_gemm_with_workspace(mode, a.c_operand(), b.c_operand(), _output(out), out.stride(0),
                                workspace.data_ptr() if workspace.numel() else None, workspace.numel(),
-                               _ptr(status), _stream(stream))
+                               _given(status), _stream(stream))
     return out
 
 
@@ -644,7 +652,7 @@ def gemm_multi(problems, status=None, stream=None):
             torch.empty((a.rows, b.rows), dtype=torch.bfloat16, device=a.data.device)
         outs.append(out)
         descs.append(MXGemmProblemC(a.c_operand(), b.c_operand(), _output(out), out.stride(0), mode, 0))
-    mx_gemm_multi(descs, _ptr(status), _stream(stream))
+    mx_gemm_multi(descs, _given(status), _stream(stream))
     return outs
 
 
@@ -680,12 +688,12 @@ def quantize_stacked(w, axis: int, status=None, stream=None):
     if axis & MX_COLWISE:
         col = MXStacked(torch.empty((E, K, N), dtype=torch.uint8, device=dev),
                         torch.empty((E, mx_scale_bytes(K, N)), dtype=torch.uint8, device=dev), K, N, MX_COLWISE)
-    assert w.stride(2) == 1 and w.dtype in (torch.bfloat16, torch.float32)
+    assert w.is_cuda and w.stride(2) == 1 and w.dtype in (torch.bfloat16, torch.float32)
     fn = mx_quantize_f32 if w.dtype == torch.float32 else mx_quantize_batched
     fn(w.data_ptr(), E, N, K, w.stride(1), w.stride(0), axis,
        _ptr(row.data) if row else None, _ptr(row.scale) if row else None,
        _ptr(col.data) if col else None, _ptr(col.scale) if col else None,
-       _ptr(status), _stream(stream))
+       _given(status), _stream(stream))
     return row, col
 
 
@@ -705,7 +713,7 @@ def grouped_gemm(mode: int, a, b, group_offsets, out=None, status=None, stream=N
             out = torch.empty((a.rows, b.rows), dtype=torch.bfloat16, device=a.data.device)
     ldc = out.stride(-2)
     mx_grouped_gemm(mode, a.c_operand(), b.c_operand(), group_offsets.data_ptr(), E, _output(out), ldc,
-                    _ptr(status), _stream(stream))
+                    _given(status), _stream(stream))
     return out
 
 
@@ -721,7 +729,7 @@ def grouped_gemm_swiglu(a, b, group_offsets, out=None, status=None, stream=None)
     if out is None:
         out = torch.empty((a.rows, b.rows // 2), dtype=torch.bfloat16, device=a.data.device)
     mx_grouped_gemm_swiglu(a.c_operand(), b.c_operand(), group_offsets.data_ptr(), E, _output(out), out.stride(0),
-                           _ptr(status), _stream(stream))
+                           _given(status), _stream(stream))
     return out
 
 
@@ -747,7 +755,7 @@ def grouped_gemm_swiglu_quantize(a, b, group_offsets, col_capacity: int, out=Non
         row, col = out
         assert all(t.is_cuda for c in out for t in (c.data, c.scale)), "out: copies of CUDA tensors"
     mx_grouped_gemm_swiglu_quantize(a.c_operand(), b.c_operand(), group_offsets.data_ptr(), E, _ptr(row.data),
-                                    _ptr(row.scale), _ptr(col.data), _ptr(col.scale), col_capacity, _ptr(status),
+                                    _ptr(row.scale), _ptr(col.data), _ptr(col.scale), col_capacity, _given(status),
                                     _stream(stream))
     return row, col
 
@@ -774,7 +782,7 @@ def quantize_fp8_blockwise(x, block: int, status=None, stream=None) -> FP8Blockw
     shape = (C // 128, R) if block == 1 else ((R + 127) // 128, C // 128)
     scale = torch.empty(shape, dtype=torch.float32, device=x.device)
     mx_quantize_fp8_blockwise(x.data_ptr(), R, C, x.stride(0), block, data.data_ptr(), scale.data_ptr(),
-                              _ptr(status), _stream(stream))
+                              _given(status), _stream(stream))
     return FP8Blockwise(data, scale, R, C, block)
 
 
@@ -788,7 +796,7 @@ def gemm_fp8_blockwise(a: FP8Blockwise, b: FP8Blockwise, out=None, status=None, 
     if out is None:
         out = torch.empty((a.rows, b.rows), dtype=torch.bfloat16, device=a.data.device)
     mx_gemm_fp8_blockwise(a.data.data_ptr(), a.scale.data_ptr(), a.rows, b.data.data_ptr(), b.scale.data_ptr(),
-                          b.rows, a.k, _output(out), out.stride(0), _ptr(status), _stream(stream))
+                          b.rows, a.k, _output(out), out.stride(0), _given(status), _stream(stream))
     return out
 
 
@@ -808,7 +816,7 @@ def current_amax(x, status=None, stream=None):
     assert xs.dtype == torch.bfloat16 and xs.is_cuda and xs.stride(2) == 1
     E, R, C = xs.shape
     amax = torch.empty(E, dtype=torch.float32, device=x.device)
-    mx_current_amax(xs.data_ptr(), E, R, C, xs.stride(1), xs.stride(0), amax.data_ptr(), _ptr(status), _stream(stream))
+    mx_current_amax(xs.data_ptr(), E, R, C, xs.stride(1), xs.stride(0), amax.data_ptr(), _given(status), _stream(stream))
     return amax
 
 
@@ -823,6 +831,7 @@ def quantize_current(x, axis: int = MX_BOTH, amax=None, format_max: float = CURR
     torch = _torch()
     stacked = x.dim() == 3
     xs = x if stacked else x.unsqueeze(0)
+    assert x.is_cuda and (amax is None or amax.is_cuda), "needs CUDA tensors"
     E, R, C = xs.shape
     dev = x.device
     if amax is None:
@@ -845,7 +854,7 @@ def quantize_current(x, axis: int = MX_BOTH, amax=None, format_max: float = CURR
             col = (MXStacked(d, scale, C, R, MX_COLWISE) if stacked else MXTensor(d[0], scale, C, R, MX_COLWISE))
     mx_quantize_current(xs.data_ptr(), E, R, C, xs.stride(1), xs.stride(0), axis, amax.data_ptr(), float(format_max),
                         _ptr(row.data) if row else None, _ptr(col.data) if col else None, scale.data_ptr(),
-                        _ptr(group_offsets), n_groups, cap, _ptr(status), _stream(stream))
+                        _given(group_offsets), n_groups, cap, _given(status), _stream(stream))
     return row, col
 
 
@@ -856,7 +865,7 @@ def gemm_current(mode: int, a, b, out=None, status=None, stream=None):
     torch = _torch()
     if out is None:
         out = torch.empty((a.rows, b.rows), dtype=torch.bfloat16, device=a.data.device)
-    mx_gemm_current(mode, a.c_operand(), b.c_operand(), _output(out), out.stride(0), _ptr(status), _stream(stream))
+    mx_gemm_current(mode, a.c_operand(), b.c_operand(), _output(out), out.stride(0), _given(status), _stream(stream))
     return out
 
 
@@ -874,7 +883,7 @@ def gemm_current_multi(problems, status=None, stream=None):
             torch.empty((a.rows, b.rows), dtype=torch.bfloat16, device=a.data.device)
         outs.append(out)
         descs.append(MXGemmProblemC(a.c_operand(), b.c_operand(), _output(out), out.stride(0), mode, 0))
-    mx_gemm_current_multi(descs, _ptr(status), _stream(stream))
+    mx_gemm_current_multi(descs, _given(status), _stream(stream))
     return outs
 
 
@@ -890,7 +899,7 @@ def grouped_gemm_current(mode: int, a, b, group_offsets, out=None, status=None, 
         shape = (E, a.rows, b.rows) if mode == MX_WGRAD else (a.rows, b.rows)
         out = torch.empty(shape, dtype=torch.bfloat16, device=a.data.device)
     mx_grouped_gemm_current(mode, a.c_operand(), b.c_operand(), group_offsets.data_ptr(), E, _output(out),
-                            out.stride(-2), _ptr(status), _stream(stream))
+                            out.stride(-2), _given(status), _stream(stream))
     return out
 
 
@@ -983,7 +992,7 @@ def adamw_step(params, grads, states, lr: float, betas=(0.9, 0.999), eps: float 
     rows = zip(*[ptr[k * n:(k + 1) * n] for k in range(6)], size, decay, g32, [0] * n)
     hyper = MXAdamWHyperC(lr, betas[0], betas[1], eps, step, (step if seed is None else seed) & 0xFFFFFFFF, 0)
     mx_adamw_step(struct.pack(_ADAMW_TENSOR * n, *itertools.chain.from_iterable(rows)), n, bits, hyper, _ptr(grad_scale),
-                  _ptr(status), _stream(stream))
+                  _given(status), _stream(stream))
 
 
 def _rows(t) -> int:
@@ -1025,7 +1034,7 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, center: bool = True
     mean = torch.empty(R, dtype=torch.float32, device=dev) if stats and center else None
     rstd = torch.empty(R, dtype=torch.float32, device=dev) if stats else None
     mx_layer_norm(x.data_ptr(), ldx, _ptr(weight), _ptr(bias), pd, R, C, eps, int(center), dtype, out.data_ptr(), ldy,
-                  _ptr(mean), _ptr(rstd), _ptr(status), _stream(stream))
+                  _ptr(mean), _ptr(rstd), _given(status), _stream(stream))
     return out, mean, rstd
 
 
@@ -1053,7 +1062,7 @@ def layer_norm_backward(dy, x, weight, mean, rstd, center: bool = True, param_gr
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
     mx_layer_norm_backward(dy.data_ptr(), _rows(dy), x.data_ptr(), _rows(x), _ptr(weight), pd,
                            _ptr(mean) if center else None, rstd.data_ptr(), R, C, int(center), _dtype(x), dx.data_ptr(),
-                           C, _ptr(dw), _ptr(db), _ptr(ws), need, _ptr(status), _stream(stream))
+                           C, _ptr(dw), _ptr(db), _ptr(ws), need, _given(status), _stream(stream))
     return dx, dw, db
 
 
@@ -1088,7 +1097,7 @@ def gemm_epilogue(mode: int, a: MXTensor, b: MXTensor, bias=None, act: str = "no
         assert bias.is_cuda and bias.is_contiguous() and bias.numel() == N, "bias: contiguous, one entry per column"
         bd = _dtype(bias)
     e = MXEpilogueC(_ptr(bias), _ptr(residual), _ptr(preact), ldr, ldz, bd, ACTIVATIONS[act])
-    mx_gemm_epilogue(mode, a.c_operand(), b.c_operand(), e, out.data_ptr(), ldc, _ptr(status), _stream(stream))
+    mx_gemm_epilogue(mode, a.c_operand(), b.c_operand(), e, out.data_ptr(), ldc, _given(status), _stream(stream))
     return out, preact
 
 
@@ -1115,7 +1124,7 @@ def epilogue_backward(dy, preact, act: str = "none", bias_grad: bool = True, dz=
         need = mx_epilogue_backward_workspace_bytes(M, N)
         ws = torch.empty(need, dtype=torch.uint8, device=dy.device) if need else None
     mx_epilogue_backward(dy.data_ptr(), _rows(dy), _ptr(preact), 0 if preact is None else _rows(preact), M, N, a,
-                         dz.data_ptr(), lddz, _ptr(dbias), _ptr(ws), need, _ptr(status), _stream(stream))
+                         dz.data_ptr(), lddz, _ptr(dbias), _ptr(ws), need, _given(status), _stream(stream))
     return dz, dbias
 
 
@@ -1156,7 +1165,7 @@ def router_forward(logits, top_k: int, tokens_per_seq: Optional[int] = None, tok
     ws = empty(need, dtype=torch.uint8, device=dev)
     mx_router_forward(logits.data_ptr(), _rows(logits), _dtype(logits), mask, T, seq, E, top_k, int(normalize), coef,
                       indices.data_ptr(), weights.data_ptr(), counts.data_ptr(), offsets.data_ptr(), load.data_ptr(),
-                      loss.data_ptr(), ws.data_ptr(), need, _ptr(status), _stream(stream))
+                      loss.data_ptr(), ws.data_ptr(), need, _given(status), _stream(stream))
     return Routing(indices, weights, counts, offsets, load, loss)
 
 
@@ -1189,7 +1198,7 @@ def router_backward(logits, indices, load, dweights=None, dloss=None, tokens_per
     dx = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
     mx_router_backward(logits.data_ptr(), _rows(logits), _dtype(logits), _mask(token_mask, T), T, seq, E, top_k,
                        int(normalize), indices.data_ptr(), load.data_ptr(), _ptr(dweights), _ptr(dloss), dx.data_ptr(),
-                       E, _ptr(status), _stream(stream))
+                       E, _given(status), _stream(stream))
     return dx
 
 

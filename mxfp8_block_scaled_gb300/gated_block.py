@@ -102,7 +102,7 @@ def add_norm_quantize(x, residual=None, weight=None, eps: float = 1e-5, axis: in
     y = empty((R, C), dtype=_BF16, device=dev) if keep_output else None
     rstd = empty(R, dtype=_F32, device=dev) if stats else None
     mx.mx_add_norm_quantize(x.data_ptr(), ldx, mx._ptr(residual), ldr, dt, mx._ptr(weight), mx._params(weight, None, C), R, C, eps, axis,
-                            mx._ptr(out), lds, mx._ptr(y), C, mx._ptr(rstd), *pointers, mx._ptr(status), mx._stream(None))
+                            mx._ptr(out), lds, mx._ptr(y), C, mx._ptr(rstd), *pointers, mx._given(status), mx._stream(None))
     return AddNorm(x if out is None else out, rstd, row, col, y)
 
 
@@ -133,7 +133,7 @@ def add_norm_backward(dy, sum, weight, rstd, dsum=None, axis: int = 0, weight_gr
         ws = empty(nbytes, dtype=_U8, device=dev)
     mx.mx_add_norm_backward(dy.data_ptr(), lddy, sum.data_ptr(), lds, mx._ptr(dsum), ldd, dt, mx._ptr(weight),
                             mx._params(weight, None, C), rstd.data_ptr(), R, C, axis, out.data_ptr(), ldo, mx._ptr(dweight),
-                            *pointers, mx._ptr(ws) if nbytes else None, nbytes, mx._ptr(status), mx._stream(None))
+                            *pointers, mx._ptr(ws) if nbytes else None, nbytes, mx._given(status), mx._stream(None))
     return AddNormGrads(out, dweight, row, col)
 
 
@@ -153,7 +153,7 @@ def gemm_gated(a: mx.MXTensor, gate: mx.MXTensor, up: mx.MXTensor, act: str = "s
         ldc = _matrix(out, M, F, _BF16, "out: BF16 [M, F]")
     pre = empty((M, 2 * F), dtype=_BF16, device=dev) if keep_preact else None
     mx.mx_gemm_gated(a.c_operand(), gate.c_operand(), up.c_operand(), act, out.data_ptr(), ldc, mx._ptr(pre), 2 * F,
-                     mx._ptr(status), mx._stream(None))
+                     mx._given(status), mx._stream(None))
     return out, pre
 
 
@@ -170,8 +170,8 @@ def gated_quantize(gate_up, act: str = "silu", axis: int = mx.MX_BOTH, group_off
     assert F % 2 == 0, "gate_up: BF16 [rows, 2F]"
     F //= 2
     row, col, pointers, n_groups, cap = _copies(axis, R, F, gate_up.device, group_offsets, col_capacity)
-    mx.mx_gated_quantize(gate_up.data_ptr(), ld, R, F, mx.ACTIVATIONS[act], axis, *pointers, mx._ptr(group_offsets), n_groups, cap,
-                         mx._ptr(status), mx._stream(None))
+    mx.mx_gated_quantize(gate_up.data_ptr(), ld, R, F, mx.ACTIVATIONS[act], axis, *pointers, mx._given(group_offsets), n_groups, cap,
+                         mx._given(status), mx._stream(None))
     return row, col
 
 
@@ -187,5 +187,5 @@ def gated_backward_quantize(dh, gate_up, act: str = "silu", axis: int = mx.MX_BO
     ld = _matrix(gate_up, R, 2 * F, _BF16, "gate_up: BF16 [rows, 2F]")
     row, col, pointers, n_groups, cap = _copies(axis, R, 2 * F, dh.device, group_offsets, col_capacity)
     mx.mx_gated_backward_quantize(dh.data_ptr(), lddh, gate_up.data_ptr(), ld, R, F, mx.ACTIVATIONS[act], axis, *pointers,
-                                  mx._ptr(group_offsets), n_groups, cap, mx._ptr(status), mx._stream(None))
+                                  mx._given(group_offsets), n_groups, cap, mx._given(status), mx._stream(None))
     return row, col

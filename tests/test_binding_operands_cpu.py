@@ -1,6 +1,7 @@
 """The products' wrappers take operands of CUDA tensors only: a CPU tensor's address must
 not reach a kernel, whichever of an operand's two tensors it is; and outputs, workspaces
-and group offsets on the GPU. No GPU: the library's calls are stand-ins."""
+and group offsets on the GPU, as the quantisers take theirs, and every call its status
+word. No GPU: the library's calls are stand-ins."""
 import pytest
 import torch
 
@@ -79,6 +80,20 @@ OTHERS = {   # every other tensor of a product's call, made here by `make`
     "gemm_fp8_blockwise a": lambda make: mx.gemm_fp8_blockwise(blockwise(1, make), blockwise(128), out=gpu(128, 128, dtype=BF16)),
     "gemm_fp8_blockwise b": lambda make: mx.gemm_fp8_blockwise(blockwise(1), blockwise(128, gpu, make), out=gpu(128, 128, dtype=BF16)),
 }
+X = (64, 32)
+OTHERS.update({   # the quantisers'
+    "quantize offsets": lambda make: mx.quantize(gpu(*X, dtype=BF16), mx.MX_BOTH, group_offsets=make(3, dtype=I64)),
+    "quantize status": lambda make: mx.quantize(gpu(*X, dtype=BF16), status=make(1, dtype=torch.int32)),
+    "quantize_batched w": lambda make: mx.quantize_stacked(make(2, *X, dtype=BF16), mx.MX_BOTH),
+    "quantize_f32 w": lambda make: mx.quantize_stacked(make(2, *X), mx.MX_BOTH),
+    "quantize_current x": lambda make: mx.quantize_current(make(*X, dtype=BF16), amax=gpu(1)),
+    "quantize_current amax": lambda make: mx.quantize_current(gpu(*X, dtype=BF16), amax=make(1)),
+    "quantize_current offsets": lambda make: mx.quantize_current(gpu(*X, dtype=BF16), amax=gpu(1), group_offsets=make(3, dtype=I64)),
+    "gated_quantize offsets": lambda make: mx.gated_quantize(gpu(64, 64, dtype=BF16), group_offsets=make(3, dtype=I64)),
+    "gated_quantize status": lambda make: mx.gated_quantize(gpu(64, 64, dtype=BF16), status=make(1, dtype=torch.int32)),
+    "add_norm_quantize status": lambda make: mx.add_norm_quantize(gpu(*X, dtype=BF16), status=make(1, dtype=torch.int32)),
+    "gemm status": lambda make: mx.gemm(mx.MX_FPROP, a, b, out=gpu(*OUT, dtype=BF16), status=make(1, dtype=torch.int32)),
+})
 
 
 @pytest.mark.parametrize("name", OTHERS)
